@@ -30,7 +30,7 @@ __all__ = [
     "linear_sigmoid", "linear_sigmoid_bwd", "quantize_fp8_rows", "linear_fp8", "linear_swiglu_fp8", "quantize_nvfp4_rows", "rmsnorm_scale_nvfp4", "linear_nvfp4",
     "linear_swiglu_nvfp4", "quantize_fp8_cols", "linear_qknorm_rope_fp8", "linear_cross_entropy_fp8",
     "linear_cross_entropy_bwd_fp8", "linear_dswiglu_fp8", "rmsnorm_linear_dx_fp8",
-    "linear_qknorm_rope_bwd_fp8", "launch_count",
+    "linear_qknorm_rope_bwd_fp8", "launch_count", "attention",
     "MAP_NONE", "MAP_SWIGLU", "MAP_DSWIGLU", "MAP_QKNORM_ROPE", "MAP_CE_LSE",
     "MAP_CE_DLOGITS", "MAP_COLDOT", "MAP_SIGMOID", "MAP_DSIGMOID", "K_MAJOR", "MN_MAJOR",
 ]
@@ -119,6 +119,9 @@ _SIGS = {
     "coda_rmsnorm_linear_cross_entropy_bwd_workspace_size": ([_I64, _I64, _I64], _SZ),
     "coda_rmsnorm_linear_cross_entropy_bwd": ([_P, _P, _P, _P, _P, _P, _I32, _P, _P, _F, _P, _P, _P, _P,
                                                _I64, _I64, _I64, _P, _SZ, _P], ctypes.c_int),
+    "coda_attention_workspace_size": ([_I64, _I64, _I64, _I32, _I32, _I32], _SZ),
+    "coda_attention": ([_P, _I64] * 3 + [_P, _P, _I64, _I32, _I32, _I32, _F, _P, _P, _I64, _I64, _P, _SZ, _P],
+                       ctypes.c_int),
     "coda_noalloc_scratch_bytes": ([], _SZ),
     "coda_linear_cross_entropy_noalloc": ([_P, _P, _P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P], ctypes.c_int),
     "coda_linear_cross_entropy_bwd_workspace_size": ([_I64, _I64, _I64], _SZ),
@@ -885,4 +888,96 @@ def linear_cross_entropy_bwd(X, W, labels, lse, n_valid, dloss=1.0, ignore_index
         _i32(n_valid, "n_valid"), float(dloss), _bf(out["dX"], "dX"), _bf(out["dW"], "dW"), M, V, K,
         _ptr(ws), ws.numel(), _stream(stream)))
     out["ws"] = ws
+    return out
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+def _strided(t, width, name):
+    """Pointer, row stride and rows of a bf16 [rows, width] operand whose rows
+    may lie apart (columns of a wider projection output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name}: expected [rows, {width}], got {tuple(t.shape)}")
+    if t.shape[0] > 1 and t.stride(0) < width or t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return t.data_ptr(), max(t.stride(0), width) if t.shape[0] > 1 else width, t.shape[0]
+
+
+def _same_device(*tensors):
+    """The calls launch on the current device: every tensor must live there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _expect(t, shape, name):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+class _on:
+    """Allocates inside on `stream` when one is given, so that the allocator
+    and the workspace's clearing follow the stream that uses them."""
+
+    def __init__(self, stream):
+        self._ctx = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        return self._ctx.__enter__() if self._ctx else None
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc) if self._ctx else None
+
+
+def _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim):
+    q, ldq, Tq = _strided(Q, n_q * head_dim, "Q")
+    k, ldk, Tk = _strided(K, n_kv * head_dim, "K")
+    v, ldv, Tv = _strided(V, n_kv * head_dim, "V")
+    if Tv != Tk:
+        raise ValueError(f"K has {Tk} rows, V {Tv}")
+    cu = _i32(cu_seqlens, "cu_seqlens")
+    cuk = _i32(cu_seqlens_k, "cu_seqlens_k")
+    n_seq = cu_seqlens.numel() - 1
+    if n_seq < 0:
+        raise ValueError("cu_seqlens: expected n_seq + 1 offsets")
+    if cuk is None and Tk != Tq:
+        raise ValueError(f"Q has {Tq} rows, K {Tk}: give cu_seqlens_k")
+    if cuk is not None and cu_seqlens_k.numel() != n_seq + 1:
+        raise ValueError("cu_seqlens_k: expected as many offsets as cu_seqlens")
+    _same_device(Q, K, V, cu_seqlens, cu_seqlens_k)
+    return (q, ldq, k, ldk, v, ldv, cu, cuk, n_seq, n_q, n_kv, head_dim,
+            float(head_dim ** -0.5 if scale is None else scale)), Tq, Tk, n_seq
+
+
+def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, head_dim=128, out=None, ws=None,
+              stream=None):
+    """Causal attention over packed sequences (coda_attention): Q
+    [Tq, n_q*128], K, V [Tk, n_kv*128], whose rows may be columns of a wider
+    tensor; cu_seqlens [n_seq + 1] int32 offsets of the sequences' queries,
+    cu_seqlens_k those of their keys when they are longer (a prompt continued
+    from a cached prefix).  scale defaults to 1/sqrt(head_dim).  Returns O
+    [Tq, n_q*128] and lse [n_q, Tq]; rows outside every sequence stay as they
+    are (undefined in tensors allocated here)."""
+    lib = load()
+    args, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim)
+    dev = Q.device
+    with _on(stream):
+        if out is None:
+            out = {"O": torch.empty(Tq, n_q * head_dim, dtype=torch.bfloat16, device=dev),
+                   "lse": torch.empty(n_q, Tq, dtype=torch.float32, device=dev)}
+        ws = _ws(ws, lib.coda_attention_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev)
+    O, lse = _expect(out["O"], (Tq, n_q * head_dim), "O"), _expect(out["lse"], (n_q, Tq), "lse")
+    _same_device(O, lse, ws)
+    _check("coda_attention", lib.coda_attention(*args, _bf(O, "O"), _f32(lse, "lse"), Tq, Tk, _ptr(ws), ws.numel(),
+                                                _stream(stream)))
     return out

@@ -101,6 +101,28 @@ bool encode_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace coda {
+int device_sms() { return num_sms(); }
+bool tensor_map_encoder() { return get_encoder(); }
+bool encode_bf16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+  cuuint64_t d[3] = {1, 1, 1}, st[2] = {0, 0};
+  cuuint32_t bx[3] = {1, 1, 1}, es[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), d, st, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace coda
+
+namespace {
+
 // A 2-D byte tensor map without swizzling (rows of `cols` bytes), for data
 // that is not a matrix operand (the NVFP4 block scales).
 bool encode_map_plain(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, uint32_t box_cols,
@@ -576,6 +598,8 @@ const char* coda_status_string(int st) {
     case CODA_ERR_TIMEOUT: return "CODA_ERR_TIMEOUT";
     case CODA_ERR_LABEL_RANGE: return "CODA_ERR_LABEL_RANGE";
     case CODA_ERR_POSITION_RANGE: return "CODA_ERR_POSITION_RANGE";
+    case CODA_ERR_SEQLEN_RANGE: return "CODA_ERR_SEQLEN_RANGE";
+    case CODA_ERR_PAGE_RANGE: return "CODA_ERR_PAGE_RANGE";
     default: return "CODA_ERR_UNKNOWN";
   }
 }
@@ -588,6 +612,8 @@ int coda_get_status(const void* ws, coda_stream stream) {
   if (word & CODA_DEV_TIMEOUT) return CODA_ERR_TIMEOUT;
   if (word & CODA_DEV_LABEL_RANGE) return CODA_ERR_LABEL_RANGE;
   if (word & CODA_DEV_POSITION_RANGE) return CODA_ERR_POSITION_RANGE;
+  if (word & CODA_DEV_SEQLEN_RANGE) return CODA_ERR_SEQLEN_RANGE;
+  if (word & CODA_DEV_PAGE_RANGE) return CODA_ERR_PAGE_RANGE;
   return CODA_OK;
 }
 

@@ -1,0 +1,417 @@
+// Causal attention over packed sequences, forward.
+//
+//   s_ij = scale q_i . k_j  (j <= i + lk - lq),  lse_i = log sum_j exp s_ij,
+//   o_i  = sum_j exp(s_ij - lse_i) v_j
+//
+// in one pass over the keys with the running maximum m and sum l of each row
+// (the attention core between the QKV projection and the output projection
+// of the block).  Tensor bound: 4 * 128 multiply-adds per visible pair and
+// head against 512 bytes of K and V per key, shared by a 256-row item.
+//
+// One persistent CTA per SM walks the work list.  An item is two 128-row
+// query tiles of one key/value head -- two sets of query heads on the same
+// tokens when the group is even, else consecutive tokens -- so every K and V
+// block in shared memory feeds two tiles:
+//
+//   warps 0-3    softmax of tile 0: thread = row.  128 scores come from TMEM
+//   warps 4-7    softmax of tile 1  into registers, the weights go back as
+//                                   bf16 over the scores, and are the A
+//                                   operand of the P V product from there.
+//   warp 8       UMMA issuer: S0 S1 | P0V S0' | P1V S1' ...  While one tile's
+//                softmax runs, the tensor core works for the other tile.
+//   warp 9       TMA producer: Q tiles, and a ring of K and V blocks.
+//   warp 10      zeroes the rows of a V block that lie behind the sequence.
+//
+// TMEM: S0 S1 (128 fp32 columns each, P in the lower 64) and O0 O1.  The
+// accumulator O is rescaled only when a row's maximum has risen by more than
+// 2^8 over the one its weights refer to (weights stay below 256, which bf16
+// and the fp32 sums hold without loss); the tile's P V product of the
+// previous block is complete by then, since S of this block was issued
+// behind it.
+//
+// Roundings: P to bf16 before the second product (the sum l adds the fp32
+// weights), O to bf16 once at the end.
+#include <algorithm>
+
+#include "coda_attn.cuh"
+#include "coda_internal.h"
+#include "coda_status.h"
+
+namespace coda {
+namespace {
+
+constexpr int FWD_THREADS = 384;
+constexpr int FWD_STAGES = 5;
+constexpr uint32_t TILE_BYTES = ATTN_BLK * ATTN_D * 2;  // 32 KB
+constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;         // 64 columns
+constexpr uint32_t FWD_SMEM = 1024 + (2 + FWD_STAGES) * TILE_BYTES + 512;
+static_assert(FWD_SMEM <= 232448, "shared memory per CTA");
+
+struct FwdItem {
+  AttnTile t;
+  int head[2], row[2], n[2];  // per tile: first head, first row of the sequence, key blocks (0: none)
+  int kv;
+};
+
+__device__ __forceinline__ FwdItem fwd_item(const AttnFwdArgs& a, int w) {
+  FwdItem it;
+  const int hp = 1 << a.head_shift;
+  const int per = a.n_q >> (a.head_shift + a.pair_heads);
+  const int ti = w / per, hi = w - ti * per;
+  it.t = load_tile(a.tiles + ti);
+  const int span = ATTN_BLK >> a.head_shift;  // tokens of a tile
+  it.head[0] = hi << (a.head_shift + a.pair_heads);
+  it.head[1] = a.pair_heads ? it.head[0] + hp : it.head[0];
+  it.row[0] = it.t.t0;
+  it.row[1] = a.pair_heads ? it.t.t0 : it.t.t0 + span;
+  it.kv = it.head[0] / a.group;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    it.n[x] = it.row[x] < it.t.lq ? key_blocks(it.t, min(it.row[x] + span, it.t.lq) - 1) : 0;
+  return it;
+}
+
+__global__ void __launch_bounds__(FWD_THREADS, 1)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                    const __grid_constant__ CUtensorMap mV, const AttnFwdArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * TILE_BYTES;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + FWD_STAGES * TILE_BYTES);
+  uint64_t* kv_empty = kv_full + FWD_STAGES;
+  uint64_t* kv_raw = kv_empty + FWD_STAGES;  // a V block that still has to be cleared behind the sequence
+  uint64_t* q_full = kv_raw + FWD_STAGES;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* drain = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((3 * FWD_STAGES + 11) * 8 + 8 <= 512, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < FWD_STAGES; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_raw[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&mQ);
+    tma_prefetch_desc(&mK);
+    tma_prefetch_desc(&mV);
+  }
+  if (warp == 8) {
+    tmem_alloc<false>(tmem_slot, 512);
+    tmem_relinquish<false>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int items = *reinterpret_cast<const volatile int*>(a.counts) * (a.n_q >> (a.head_shift + a.pair_heads));
+  const int step = static_cast<int>(gridDim.x);
+  bool ok = true;
+
+  // Registers: 384 threads x 168 at launch = 256 x 216 + 128 x 72.  Each
+  // branch below begins with its own share, so the compiler sees it.
+  if (warp >= 8) {
+  reg_dec<72>();
+  if (warp == 9) {
+    // ------------------------------------------------------------ producer
+    const uint32_t el = elect_one();
+    uint32_t pos = 0, qn[2] = {0, 0};
+    auto put = [&](const CUtensorMap& m, int col, int row, bool ragged) {
+      const uint32_t s = pos % FWD_STAGES, ph = (pos / FWD_STAGES) & 1;
+      if (!mbar_wait_bounded(&kv_empty[s], ph ^ 1, abort_flag, a.status, a.timeout_ns)) return false;
+      uint64_t* bar = ragged ? &kv_raw[s] : &kv_full[s];
+      mbar_arrive_expect_tx(bar, TILE_BYTES, el);
+      tma_load_2d(sKV + s * TILE_BYTES, &m, bar, col, row, el);
+      tma_load_2d(sKV + s * TILE_BYTES + HALF_BYTES, &m, bar, col + 64, row, el);
+      ++pos;
+      return true;
+    };
+    for (int w = blockIdx.x; w < items && ok; w += step) {
+      const FwdItem it = fwd_item(a, w);
+      const int n = max(it.n[0], it.n[1]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (!ok) break;
+        if (it.n[x] > 0) {
+          ok = mbar_wait_bounded(&q_empty[x], (qn[x] & 1) ^ 1, abort_flag, a.status, a.timeout_ns);
+          if (!ok) break;
+          ++qn[x];
+          uint8_t* q = sQ + x * TILE_BYTES;
+          mbar_arrive_expect_tx(&q_full[x], TILE_BYTES, el);
+          tma_load_3d(q, &mQ, &q_full[x], 0, it.head[x], it.t.q0 + it.row[x], el);
+          tma_load_3d(q + HALF_BYTES, &mQ, &q_full[x], 64, it.head[x], it.t.q0 + it.row[x], el);
+        }
+        if (x == 0 && n > 0) ok = put(mK, it.kv * ATTN_D, it.t.k0, false);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int row = j * ATTN_BLK;
+        ok = put(mV, it.kv * ATTN_D, it.t.k0 + row, row + ATTN_BLK > it.t.lk);
+        if (ok && j + 1 < n) ok = put(mK, it.kv * ATTN_D, it.t.k0 + row + ATTN_BLK, false);
+      }
+    }
+    if (!ok) {
+      // let every copy already issued land before the CTA's memory is reused
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ rows behind the sequence
+    uint32_t pos = 0, seen = 0;  // seen: bit s = parity of kv_raw[s]'s next phase
+    for (int w = blockIdx.x; w < items && ok; w += step) {
+      const FwdItem it = fwd_item(a, w);
+      const int n = max(it.n[0], it.n[1]);
+      if (n > 0 && n * ATTN_BLK > it.t.lk) {
+        const uint32_t s = (pos + 2 * n - 1) % FWD_STAGES;  // the item's last V block
+        ok = mbar_wait_bounded(&kv_raw[s], (seen >> s) & 1, abort_flag, a.status, a.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        seen ^= 1u << s;
+        zero_tile_rows(sKV + s * TILE_BYTES, it.t.lk - (n - 1) * ATTN_BLK);
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+      }
+      pos += 2 * n;
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ UMMA issuer
+    const uint32_t el = elect_one();
+    constexpr uint32_t ID_S = idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t ID_O = idesc_bf16(128, 128, 0, 1);
+    uint32_t pos = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+    bool issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = mbar_wait_bounded(bar, parity, abort_flag, a.status, a.timeout_ns);
+      tc_fence_after();
+      return ok;
+    };
+    auto score = [&](int x, uint32_t kpos) {  // S_x = Q_x K^T
+      const uint32_t q = smem_u32(sQ + x * TILE_BYTES), k = smem_u32(sKV + (kpos % FWD_STAGES) * TILE_BYTES);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t o = (i >> 2) * HALF_BYTES + (i & 3) * 32;
+        umma_bf16(tmem + x * 128, sdesc_sw128(q + o, 16, 1024), sdesc_sw128(k + o, 16, 1024), ID_S, i > 0, el);
+      }
+      umma_commit(&s_full[x], el);
+      issued = true;
+    };
+    for (int w = blockIdx.x; w < items && ok; w += step) {
+      const FwdItem it = fwd_item(a, w);
+      const int n = max(it.n[0], it.n[1]);
+      if (n == 0) continue;
+      if (!wait(&kv_full[pos % FWD_STAGES], (pos / FWD_STAGES) & 1)) break;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (!ok || it.n[x] == 0) continue;
+        if (!wait(&q_full[x], qn[x] & 1)) break;
+        ++qn[x];
+        score(x, pos);
+        if (it.n[x] == 1) umma_commit(&q_empty[x], el);
+      }
+      if (!ok) break;
+      umma_commit(&kv_empty[pos % FWD_STAGES], el);
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t vpos = pos + 2 * j + 1, kpos = vpos + 1, vs = vpos % FWD_STAGES;
+        if (!wait(&kv_full[vs], (vpos / FWD_STAGES) & 1)) break;
+        const uint32_t v = smem_u32(sKV + vs * TILE_BYTES);
+        bool k_here = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (j < it.n[x]) {
+            if (!wait(&p_full[x], pn[x] & 1)) break;
+            ++pn[x];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // O_x += P_x V, 16 keys a step
+              umma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, sdesc_sw128(v + i * 2048, HALF_BYTES, 1024),
+                           ID_O, (j | i) > 0, el);
+            if (j + 1 == it.n[x]) umma_commit(&o_full[x], el);
+          }
+          if (x == 1) umma_commit(&kv_empty[vs], el);
+          if (j + 1 < it.n[x]) {
+            if (!k_here && !wait(&kv_full[kpos % FWD_STAGES], (kpos / FWD_STAGES) & 1)) break;
+            k_here = true;
+            score(x, kpos);
+            if (j + 2 == it.n[x]) umma_commit(&q_empty[x], el);
+          }
+        }
+        if (ok && j + 1 < n) umma_commit(&kv_empty[kpos % FWD_STAGES], el);
+      }
+      pos += 2 * n;
+    }
+    if (!ok && issued) {
+      umma_commit(drain, el);
+      mbar_wait_drain(drain, 0, 200000000ull);
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ softmax
+    reg_inc<216>();
+    const int x = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + x * 128, tO = tmem + lanes + 256 + x * 128;
+    const int tok = r >> a.head_shift, hd = r & ((1 << a.head_shift) - 1);
+    const float c = a.scale_log2;
+    uint32_t sn = 0, on = 0;
+    for (int w = blockIdx.x; w < items && ok; w += step) {
+      const FwdItem it = fwd_item(a, w);
+      const int n = x ? it.n[1] : it.n[0];
+      const int row0 = x ? it.row[1] : it.row[0];
+      const int row = row0 + tok;
+      const int vis = max(0, min(it.t.lk, row + 1 + it.t.lk - it.t.lq));  // keys this row sees
+      const int all = row0 + 1 + it.t.lk - it.t.lq;                  // keys every row of the tile sees
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        ok = mbar_wait_bounded(&s_full[x], sn & 1, abort_flag, a.status, a.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++sn;
+        tc_fence_after();
+        uint32_t s[128];
+        tmem_ld128(tS, s);
+        if ((j + 1) * ATTN_BLK > all) {
+          const int lim = vis - j * ATTN_BLK;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = i < lim ? s[i] : 0xFF800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmaxf(mx[k], fmaxf(__uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1])));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool raise = j == 0 || (top - m) * c > 8.f;
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? exp2_sfu((m - top) * c) : 1.f;
+          if (raise) m = top;
+          l *= f;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float o[32];
+            tmem_ld32(tO + q * 32, o);
+            uint32_t u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+            tmem_st32(tO + q * 32, u);
+          }
+          tmem_st_wait();
+        }
+        // a row without any key keeps m = -inf: its weights are 2^-inf = 0
+        const float mc = m == -INFINITY ? 0.f : m * c;
+        const uint64_t c2 = f2_pack(c, c), mc2 = f2_pack(-mc, -mc);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = h * 64 + 2 * i;
+            uint64_t z = f2_fma(f2_pack(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, mc2);
+            float z0, z1;
+            f2_unpack(z, z0, z1);
+            z0 = exp2_sfu(z0);
+            z1 = exp2_sfu(z1);
+            sum[i & 1] = f2_add(sum[i & 1], f2_pack(z0, z1));
+            p[i] = pack_bf16x2(z0, z1);
+          }
+          tmem_st32(tS + h * 32, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+        float s0, s1;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+      }
+      if (!ok) break;
+      const bool valid = row < it.t.lq;
+      const int head = (x ? it.head[1] : it.head[0]) + hd;
+      const int64_t grow = static_cast<int64_t>(it.t.q0) + row;
+      __nv_bfloat16* dst = a.O + grow * a.n_q * ATTN_D + head * ATTN_D;
+      if (n > 0) {
+        ok = mbar_wait_bounded(&o_full[x], on & 1, abort_flag, a.status, a.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++on;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+      if (n > 0) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float o[32];
+          __syncwarp();
+          tmem_ld32(tO + q * 32, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= inv;
+          if (valid && vis > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store_bf16x8(dst + q * 32 + i * 8, o + i * 8);
+          }
+        }
+        tc_fence_before();
+      }
+      if (valid) {
+        if (vis == 0) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
+        }
+        a.lse[static_cast<int64_t>(head) * a.Tq + grow] = vis == 0 ? -INFINITY : m * a.scale + logf(l);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) {
+    __syncwarp();
+    tmem_dealloc<false>(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd(const AttnFwdArgs& a, const CUtensorMap* maps, int64_t max_items, int sms,
+                            cudaStream_t s) {
+  cudaError_t e = attn_smem_attribute(reinterpret_cast<const void*>(attn_fwd_kernel), 0, FWD_SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, max_items))));
+  cfg.blockDim = dim3(FWD_THREADS);
+  cfg.dynamicSmemBytes = FWD_SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = attn_programmatic_launch() ? 1 : 0;
+  note_launch();
+  e = cudaLaunchKernelEx(&cfg, attn_fwd_kernel, maps[0], maps[1], maps[2], a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace coda

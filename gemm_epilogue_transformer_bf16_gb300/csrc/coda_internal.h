@@ -16,6 +16,15 @@ enum class EpiKind : int { Plain = 0, Swiglu, DSwiglu, QkRope, CeLse, CeDlogits,
 // just before its launch); coda_launch_count returns the process-wide total.
 void note_launch();
 
+// SMs of the current device (0 on error), cached per device.
+int device_sms();
+// Resolves the tensor-map encoder (false: no driver).
+bool tensor_map_encoder();
+// bf16 tensor map of `rank` (2 or 3) dimensions, innermost first; strides in
+// bytes of dimensions 1 .. rank - 1; 128-byte swizzle, zero fill.
+bool encode_bf16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box);
+
 // Tensor maps in the order A0, B0, A1, B1.  `cg` is the cluster size: 1
 // (single CTAs), 2 (a cta_group::2 pair) or 4 (two pairs sharing B by TMA
 // multicast); the launcher sizes the persistent grid.

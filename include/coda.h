@@ -68,7 +68,9 @@ typedef enum coda_status {
   CODA_ERR_CUDA = 5,           /* a CUDA runtime call or launch failed */
   CODA_ERR_TIMEOUT = 6,        /* device: a bounded pipeline wait ran out */
   CODA_ERR_LABEL_RANGE = 7,    /* device: label outside [0,V) and != ignore_index */
-  CODA_ERR_POSITION_RANGE = 8  /* device: RoPE position outside [0, max_pos) */
+  CODA_ERR_POSITION_RANGE = 8, /* device: RoPE position outside [0, max_pos) */
+  CODA_ERR_SEQLEN_RANGE = 9,   /* device: sequence offsets that fall or leave the tensor, a length beyond its page table */
+  CODA_ERR_PAGE_RANGE = 10     /* device: cache slot or page index outside the cache */
 } coda_status;
 
 /* Operand storage order of a GEMM operand. */
@@ -713,6 +715,37 @@ int coda_linear_cross_entropy_bwd(const coda_bf16* X, const coda_bf16* W, const 
                                   float dloss, coda_bf16* dX, coda_bf16* dW,
                                   int64_t M, int64_t V, int64_t K, void* ws, size_t ws_bytes,
                                   coda_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Causal attention over packed sequences (the core between
+ * coda_linear_qknorm_rope and coda_linear_residual; the pages leave it out of
+ * the block and take its output A and the gradients dQ, dK, dV as given).
+ *
+ * Sequence b owns the query rows [cu_q[b], cu_q[b+1]) and the key/value rows
+ * [cu_k[b], cu_k[b+1]); with lq and lk of them, query i sees the keys
+ * j <= i + lk - lq (the queries are the sequence's last lq tokens; a query
+ * with no key gets O = 0, lse = -inf).  Head h of n_q reads key/value head
+ * h / (n_q / n_kv).
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),
+ *   O_i = sum_j exp(s_ij - lse_i) v_j
+ * Q [Tq, n_q*128] (row stride ldq), K, V [Tk, n_kv*128] (row strides ldk,
+ * ldv) bf16: columns of one projection output or separate tensors; cu_q,
+ * cu_k [n_seq + 1] int32 device arrays, rising (equal neighbours: an empty
+ * sequence); cu_k NULL: cu_q (then Tk == Tq).  O [Tq, n_q*128] bf16, lse
+ * [n_q, Tq] fp32.  Rows outside every sequence are neither read nor written.
+ * Offsets that fall or leave [0, T] set CODA_ERR_SEQLEN_RANGE in the status
+ * word and nothing is computed.  scale > 0 and finite.  P is rounded to bf16
+ * before the P V product; sums, maxima and O are fp32 until O's rounding.  An
+ * infinity or NaN reaches tokens of its own sequence only (and there also
+ * earlier ones: a zero weight times an infinite value is NaN).
+ * head_dim 128; n_q a multiple of n_kv; Tq, Tk below 2^30.
+ * ---------------------------------------------------------------------- */
+size_t coda_attention_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, int32_t n_q, int32_t n_kv,
+                                     int32_t head_dim);
+int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t ldk, const coda_bf16* V, int64_t ldv,
+                   const int32_t* cu_q, const int32_t* cu_k, int64_t n_seq, int32_t n_q, int32_t n_kv,
+                   int32_t head_dim, float scale, coda_bf16* O, float* lse, int64_t Tq, int64_t Tk,
+                   void* ws, size_t ws_bytes, coda_stream stream);
 
 #ifdef __cplusplus
 }

@@ -58,6 +58,7 @@ __all__ = [
     "E2M1_MAX", "E2M1_GRID", "NVFP4_BLOCK", "e2m1_round", "e2m1_value", "quantize_nvfp4_rows",
     "rmsnorm_scale_nvfp4",
     "linear_nvfp4_fwd", "swiglu_nvfp4_fwd",
+    "attention_fwd",
 ]
 
 
@@ -751,3 +752,43 @@ def ce_flops(tokens, hidden, vocab, backward=True):
 def block_flops(tokens, hidden, qkv_out, attn_in, inter, backward=True):
     fwd = 2 * tokens * hidden * (qkv_out + 3 * inter) + 2 * tokens * attn_in * hidden
     return fwd + (2 * fwd if backward else 0)
+
+
+# ---------------------------------------------------------------------------
+# causal attention over packed sequences (the core the block takes as given)
+# ---------------------------------------------------------------------------
+
+def _attention_spans(cu_q, cu_k):
+    for b in range(len(cu_q) - 1):
+        yield int(cu_q[b]), int(cu_q[b + 1]), int(cu_k[b]), int(cu_k[b + 1])
+
+
+def _attention_weights(q, k, scale):
+    """Weights and log-sum-exp of one head: query i sees keys j <= i + lk - lq;
+    a query without keys has zero weights and lse = -inf."""
+    lq, lk = q.shape[0], k.shape[0]
+    s = scale * (q @ k.T)
+    seen = np.arange(lk)[None, :] <= np.arange(lq)[:, None] + (lk - lq)
+    s = np.where(seen, s, -np.inf)
+    m = s.max(axis=1, initial=-np.inf)
+    m0 = np.where(np.isneginf(m), 0.0, m)
+    e = np.exp(s - m0[:, None])
+    tot = e.sum(axis=1)
+    with np.errstate(divide="ignore"):
+        lse = m0 + np.log(tot)
+    return e / np.where(tot == 0, 1.0, tot)[:, None], lse
+
+
+def attention_fwd(Q, K, V, cu_q, cu_k, n_q, n_kv, scale):
+    """O [Tq, n_q*d], lse [n_q, Tq] and A = sum_j p_ij |v_j| (the scale of the
+    rounding errors of O); rows outside every sequence are zero."""
+    d = Q.shape[1] // n_q
+    O, A = np.zeros(Q.shape), np.zeros(Q.shape)
+    lse = np.zeros((n_q, Q.shape[0]))
+    for q0, q1, k0, k1 in _attention_spans(cu_q, cu_k):
+        for h in range(n_q):
+            c, kc = slice(h * d, (h + 1) * d), slice((h // (n_q // n_kv)) * d, (h // (n_q // n_kv) + 1) * d)
+            p, lse[h, q0:q1] = _attention_weights(Q[q0:q1, c], K[k0:k1, kc], scale)
+            O[q0:q1, c] = p @ V[k0:k1, kc]
+            A[q0:q1, c] = p @ np.abs(V[k0:k1, kc])
+    return {"O": O, "lse": lse, "A": A}

@@ -1,0 +1,78 @@
+"""CPU checks of the attention operators: arguments refused on the host
+before anything is enqueued, empty problems, workspace sizes, and the oracle's
+own pins (against a direct evaluation and finite differences)."""
+import numpy as np
+import pytest
+import torch
+
+import gemm_epilogue_transformer_bf16_gb300 as coda
+from oracle import coda_oracle as O
+
+FAKE = 1 << 20          # a 16-byte aligned non-null address (never dereferenced)
+WS = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gemm_epilogue_transformer_bf16_gb300 import _build
+    _build.build()
+    return coda.load()
+
+
+def fwd(lib, Q=FAKE, ldq=512, K=FAKE, ldk=256, V=FAKE, ldv=256, cu_q=FAKE, cu_k=None, n_seq=2, n_q=4, n_kv=2, d=128,
+        scale=0.1, O=FAKE, lse=FAKE, Tq=64, Tk=64, ws=FAKE, ws_bytes=WS):
+    return lib.coda_attention(Q, ldq, K, ldk, V, ldv, cu_q, cu_k, n_seq, n_q, n_kv, d, scale, O, lse, Tq, Tk, ws,
+                              ws_bytes, None)
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(Q=None), 1), (dict(K=None), 1), (dict(V=None), 1), (dict(O=None), 1), (dict(lse=None), 1),
+    (dict(cu_q=None), 1), (dict(Tq=-1), 1), (dict(Tk=-1), 1), (dict(n_seq=-1), 1), (dict(n_q=0), 1), (dict(n_kv=0), 1),
+    (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(Tk=65), 1),                                   # other key rows need their own offsets
+    (dict(ldq=504), 1), (dict(ldk=128), 1), (dict(ldv=248), 1),
+    (dict(d=64), 3), (dict(n_q=5), 3), (dict(Tq=1 << 30, Tk=1 << 30), 3),
+    (dict(Q=FAKE + 2), 2), (dict(O=FAKE + 8), 2), (dict(cu_q=FAKE + 2), 2), (dict(ldq=516), 2), (dict(ws=FAKE + 4), 2),
+    (dict(ws=None), 4), (dict(ws_bytes=255), 4),
+    (dict(Tq=0, Tk=0), 0), (dict(n_seq=0), 0),          # nothing to do
+])
+def test_forward_refusals(lib, change, code):
+    assert fwd(lib, **change) == code
+
+
+def test_workspace_grows_with_rows_and_sequences(lib):
+    w = lib.coda_attention_workspace_size
+    assert w(8192, 8192, 4, 64, 8, 128) < 65536
+    assert w(8192, 8192, 4096, 64, 8, 128) > w(8192, 8192, 4, 64, 8, 128)
+
+
+def test_binding_refuses_host_tensors_and_shapes():
+    q = torch.zeros(4, 256, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        coda.attention(q, q, q, cu, 2, 2)
+
+
+def test_oracle_forward_pins():
+    rng = np.random.default_rng(0)
+    n_q, n_kv, d = 4, 2, 8
+    cq, ck = [0, 3, 3, 7], [0, 5, 6, 8]
+    Q, K, V = rng.normal(size=(7, n_q * d)), rng.normal(size=(8, n_kv * d)), rng.normal(size=(8, n_kv * d))
+    r = O.attention_fwd(Q, K, V, cq, ck, n_q, n_kv, 0.3)
+    for h in range(n_q):
+        kv = h // 2
+        for b in range(3):
+            lq, lk = cq[b + 1] - cq[b], ck[b + 1] - ck[b]
+            for i in range(lq):
+                seen = range(max(0, min(lk, i + lk - lq + 1)))
+                w = [np.exp(0.3 * Q[cq[b] + i, h * d:(h + 1) * d] @ K[ck[b] + j, kv * d:(kv + 1) * d]) for j in seen]
+                got = r["O"][cq[b] + i, h * d:(h + 1) * d]
+                if not w:
+                    assert np.all(got == 0) and np.isneginf(r["lse"][h, cq[b] + i])
+                    continue
+                want = sum(x * V[ck[b] + j, kv * d:(kv + 1) * d] for x, j in zip(w, seen)) / sum(w)
+                assert np.allclose(got, want, rtol=1e-12, atol=1e-14)
+                assert np.isclose(r["lse"][h, cq[b] + i], np.log(sum(w)), rtol=1e-12)
+    # one key: its value, whatever the score
+    one = O.attention_fwd(Q[:1], K[:1], V[:1], [0, 1], [0, 1], n_q, n_kv, 5.0)
+    assert np.allclose(one["O"].reshape(n_q, d), np.repeat(V[:1].reshape(n_kv, d), 2, axis=0))
