@@ -31,6 +31,7 @@ __all__ = [
     "linear_swiglu_nvfp4", "quantize_fp8_cols", "linear_qknorm_rope_fp8", "linear_cross_entropy_fp8",
     "linear_cross_entropy_bwd_fp8", "linear_dswiglu_fp8", "rmsnorm_linear_dx_fp8",
     "linear_qknorm_rope_bwd_fp8", "launch_count", "attention",
+    "kv_cache_nvfp4", "kv_append_nvfp4", "kv_read_nvfp4", "attention_decode_nvfp4",
     "MAP_NONE", "MAP_SWIGLU", "MAP_DSWIGLU", "MAP_QKNORM_ROPE", "MAP_CE_LSE",
     "MAP_CE_DLOGITS", "MAP_COLDOT", "MAP_SIGMOID", "MAP_DSIGMOID", "K_MAJOR", "MN_MAJOR",
 ]
@@ -122,6 +123,13 @@ _SIGS = {
     "coda_attention_workspace_size": ([_I64, _I64, _I64, _I32, _I32, _I32], _SZ),
     "coda_attention": ([_P, _I64] * 3 + [_P, _P, _I64, _I32, _I32, _I32, _F, _P, _P, _I64, _I64, _P, _SZ, _P],
                        ctypes.c_int),
+    "coda_kv_append_nvfp4": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _SZ, _P],
+                             ctypes.c_int),
+    "coda_kv_read_nvfp4": ([_P, _P, _P, _I64, _I32, _P, _I64, _I32, _I32, _P, _P, ctypes.c_int, _P, _SZ, _P],
+                           ctypes.c_int),
+    "coda_attention_decode_nvfp4_workspace_size": ([_I64, _I32, _I32, _I32], _SZ),
+    "coda_attention_decode_nvfp4": ([_P, _I64, _P, _P, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, _I32, _I32, _F, _P,
+                                     _P, _P, _SZ, _P], ctypes.c_int),
     "coda_noalloc_scratch_bytes": ([], _SZ),
     "coda_linear_cross_entropy_noalloc": ([_P, _P, _P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P], ctypes.c_int),
     "coda_linear_cross_entropy_bwd_workspace_size": ([_I64, _I64, _I64], _SZ),
@@ -980,4 +988,90 @@ def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, hea
     _same_device(O, lse, ws)
     _check("coda_attention", lib.coda_attention(*args, _bf(O, "O"), _f32(lse, "lse"), Tq, Tk, _ptr(ws), ws.numel(),
                                                 _stream(stream)))
+    return out
+
+
+def kv_cache_nvfp4(num_pages, page_size, n_kv, head_dim=128, device="cuda"):
+    """An empty paged key/value cache in 4 bits: the three arrays that
+    coda_kv_append_nvfp4 describes, zeroed (rows of zeros)."""
+    z = torch.zeros
+    return {"codes": z(num_pages, 2, n_kv, page_size, head_dim // 2, dtype=torch.uint8, device=device),
+            "sf": z(num_pages, 2, n_kv, page_size, head_dim // 16, dtype=torch.uint8, device=device),
+            "scale": z(num_pages, 2, n_kv, page_size, dtype=torch.float32, device=device)}
+
+
+def _cache_args(cache):
+    codes, sf, scale = cache["codes"], cache["sf"], cache["scale"]
+    if scale.dim() != 4 or scale.shape[1] != 2:
+        raise ValueError("cache: expected scale [num_pages, 2, n_kv, page_size]")
+    pages, _, n_kv, page = scale.shape
+    d = 2 * codes.shape[-1]
+    _expect(codes, (pages, 2, n_kv, page, d // 2), "cache codes")
+    _expect(sf, (pages, 2, n_kv, page, d // 16), "cache sf")
+    return (_u8(codes, "cache codes"), _u8(sf, "cache sf"), _f32(scale, "cache scale"), pages, page), n_kv, d
+
+
+def kv_append_nvfp4(K, V, slots, cache, ws=None, stream=None):
+    """Quantise the rows of K, V [T, n_kv*128] (rows may be columns of a wider
+    tensor) into their cache slots [T] int32 (coda_kv_append_nvfp4; a negative
+    slot skips its token, the slots of one call must differ)."""
+    c, n_kv, d = _cache_args(cache)
+    k, ldk, T = _strided(K, n_kv * d, "K")
+    v, ldv, Tv = _strided(V, n_kv * d, "V")
+    if Tv != T:
+        raise ValueError(f"K has {T} rows, V {Tv}")
+    _expect(slots, (T,), "slots")
+    _same_device(K, V, slots, cache["codes"], cache["sf"], cache["scale"], ws)
+    with _on(stream):
+        ws = _ws(ws, 256, K.device)
+    _check("coda_kv_append_nvfp4", load().coda_kv_append_nvfp4(
+        k, ldk, v, ldv, _i32(slots, "slots"), T, *c, n_kv, d, _ptr(ws), ws.numel(), _stream(stream)))
+    return cache
+
+
+def kv_read_nvfp4(cache, slots, dtype=torch.bfloat16, out=None, ws=None, stream=None):
+    """The rows of cache slots [T] int32 back as {"K", "V"} [T, n_kv*128] in
+    torch.bfloat16 or torch.float32 (coda_kv_read_nvfp4; a negative slot gives
+    zeros)."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"kv_read_nvfp4: dtype must be torch.bfloat16 or torch.float32, not {dtype}")
+    c, n_kv, d = _cache_args(cache)
+    T = slots.numel()
+    dev = cache["scale"].device
+    with _on(stream):
+        if out is None:
+            out = {k: torch.empty(T, n_kv * d, dtype=dtype, device=dev) for k in ("K", "V")}
+        ws = _ws(ws, 256, dev)
+    K, V = (_expect(out[k], (T, n_kv * d), k) for k in ("K", "V"))
+    _expect(slots, (T,), "slots")
+    _same_device(slots, cache["codes"], cache["sf"], cache["scale"], K, V, ws)
+    _check("coda_kv_read_nvfp4", load().coda_kv_read_nvfp4(
+        *c, _i32(slots, "slots"), T, n_kv, d, _ptr(K, dtype, "K"), _ptr(V, dtype, "V"),
+        F32 if dtype == torch.float32 else BF16, _ptr(ws), ws.numel(), _stream(stream)))
+    return out
+
+
+def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out=None, ws=None, stream=None):
+    """One query token per sequence, Q [batch, n_q*128], over the first
+    seq_lens [batch] int32 cached tokens of the pages block_table
+    [batch, max_pages] int32 names (coda_attention_decode_nvfp4).  Returns O
+    [batch, n_q*128] and lse [batch, n_q]."""
+    lib = load()
+    c, n_kv, d = _cache_args(cache)
+    q, ldq, batch = _strided(Q, n_q * d, "Q")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table: expected [{batch}, max_pages], got {tuple(block_table.shape)}")
+    _expect(seq_lens, (batch,), "seq_lens")
+    dev = Q.device
+    with _on(stream):
+        if out is None:
+            out = {"O": torch.empty(batch, n_q * d, dtype=torch.bfloat16, device=dev),
+                   "lse": torch.empty(batch, n_q, dtype=torch.float32, device=dev)}
+        ws = _ws(ws, lib.coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, d), dev)
+    O, lse = _expect(out["O"], (batch, n_q * d), "O"), _expect(out["lse"], (batch, n_q), "lse")
+    _same_device(Q, block_table, seq_lens, cache["codes"], cache["sf"], cache["scale"], O, lse, ws)
+    _check("coda_attention_decode_nvfp4", lib.coda_attention_decode_nvfp4(
+        q, ldq, *c, _i32(block_table, "block_table"), block_table.shape[1], _i32(seq_lens, "seq_lens"), batch, n_q,
+        n_kv, d, float(d ** -0.5 if scale is None else scale), _bf(O, "O"), _f32(lse, "lse"), _ptr(ws), ws.numel(),
+        _stream(stream)))
     return out

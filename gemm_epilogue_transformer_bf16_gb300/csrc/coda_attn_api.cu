@@ -10,6 +10,7 @@
 #include "coda.h"
 #include "coda_attn.cuh"
 #include "coda_internal.h"
+#include "coda_kvcache.cuh"
 #include "coda_status.h"
 
 namespace coda {
@@ -114,6 +115,42 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
 #define CU(x) \
   do { if ((x) != cudaSuccess) return CODA_ERR_CUDA; } while (0)
 
+// The cache's shape; CODA_OK or the error to return.
+int check_cache(coda::KvCache& c, const uint8_t* codes, const uint8_t* sf, const float* scale, int64_t num_pages,
+                int32_t page_size, int32_t n_kv, int32_t head_dim) {
+  if (num_pages < 0 || page_size <= 0 || n_kv <= 0) return CODA_ERR_INVALID_ARG;
+  if (head_dim != coda::ATTN_D || page_size < 16 || (page_size & (page_size - 1)) || n_kv >= 65536)
+    return CODA_ERR_UNSUPPORTED;
+  if (num_pages * page_size >= (int64_t(1) << 31)) return CODA_ERR_UNSUPPORTED;  // slots are 32-bit
+  if (num_pages > 0 && (!codes || !sf || !scale)) return CODA_ERR_INVALID_ARG;
+  if (!al16(codes) || !al16(sf) || !al16(scale)) return CODA_ERR_ALIGNMENT;
+  c.codes = const_cast<uint8_t*>(codes);
+  c.sf = const_cast<uint8_t*>(sf);
+  c.scale = const_cast<float*>(scale);
+  c.num_pages = static_cast<int>(num_pages);
+  c.page_shift = 0;
+  while ((1 << c.page_shift) < page_size) ++c.page_shift;
+  c.n_kv = n_kv;
+  return CODA_OK;
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return CODA_ERR_WORKSPACE;
+  return al16(ws) ? CODA_OK : CODA_ERR_ALIGNMENT;
+}
+
+struct DecodeLayout {
+  int* units;
+  float* part;
+  float* part_lse;
+};
+void lay_decode(Cursor& c, DecodeLayout& l, int64_t batch, int group) {
+  const int heads = std::min(group, coda::DEC_HEADS);
+  l.units = c.take<int>(batch + 2);
+  l.part = c.take<float>(int64_t(2) * coda::DEC_MAX_CTAS * heads * coda::ATTN_D);
+  l.part_lse = c.take<float>(int64_t(2) * coda::DEC_MAX_CTAS * heads);
+}
+
 const __nv_bfloat16* B(const coda_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
 __nv_bfloat16* B(coda_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
 
@@ -189,6 +226,94 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
   a.timeout_ns = WAIT_LIMIT_NS;
   CU(coda::launch_attn_plan(l.a, s));
   CU(coda::launch_attn_fwd(a, maps, l.max_q_tiles * (n_q >> (hs + pair_heads)), sms, s));
+  return CODA_OK;
+}
+
+int coda_kv_append_nvfp4(const coda_bf16* K, int64_t ldk, const coda_bf16* V, int64_t ldv, const int32_t* slots,
+                         int64_t T, uint8_t* codes, uint8_t* sf, float* scale, int64_t num_pages, int32_t page_size,
+                         int32_t n_kv, int32_t head_dim, void* ws, size_t ws_bytes, coda_stream stream) {
+  if (T < 0) return CODA_ERR_INVALID_ARG;
+  coda::KvCache c{};
+  CK(check_cache(c, codes, sf, scale, num_pages, page_size, n_kv, head_dim));
+  if (T == 0) return CODA_OK;
+  if (!K || !V || !slots || ldk < int64_t(n_kv) * head_dim || ldv < int64_t(n_kv) * head_dim)
+    return CODA_ERR_INVALID_ARG;
+  if (!al16(K) || !al16(V) || !al4(slots) || ldk % 8 || ldv % 8) return CODA_ERR_ALIGNMENT;
+  CK(check_ws(ws, ws_bytes, HEADER));
+  const int sms = coda::device_sms();
+  if (sms <= 0) return CODA_ERR_CUDA;
+  CU(coda::launch_kv_append(c, B(K), ldk, B(V), ldv, slots, T, static_cast<int*>(ws), sms,
+                            static_cast<cudaStream_t>(stream)));
+  return CODA_OK;
+}
+
+int coda_kv_read_nvfp4(const uint8_t* codes, const uint8_t* sf, const float* scale, int64_t num_pages,
+                       int32_t page_size, const int32_t* slots, int64_t T, int32_t n_kv, int32_t head_dim, void* K,
+                       void* V, int dtype, void* ws, size_t ws_bytes, coda_stream stream) {
+  if (T < 0 || (dtype != CODA_BF16 && dtype != CODA_F32)) return CODA_ERR_INVALID_ARG;
+  coda::KvCache c{};
+  CK(check_cache(c, codes, sf, scale, num_pages, page_size, n_kv, head_dim));
+  if (T == 0) return CODA_OK;
+  if (!K || !V || !slots) return CODA_ERR_INVALID_ARG;
+  if (!al16(K) || !al16(V) || !al4(slots)) return CODA_ERR_ALIGNMENT;
+  CK(check_ws(ws, ws_bytes, HEADER));
+  const int sms = coda::device_sms();
+  if (sms <= 0) return CODA_ERR_CUDA;
+  CU(coda::launch_kv_read(c, slots, T, K, V, dtype == CODA_F32, static_cast<int*>(ws), sms,
+                          static_cast<cudaStream_t>(stream)));
+  return CODA_OK;
+}
+
+size_t coda_attention_decode_nvfp4_workspace_size(int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim) {
+  if (check_shape(batch, batch, batch, n_q, n_kv, head_dim, 1.f) != CODA_OK) return HEADER;
+  Cursor c{nullptr};
+  DecodeLayout l{};
+  lay_decode(c, l, batch, n_q / n_kv);
+  return c.off;
+}
+
+int coda_attention_decode_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
+                                const float* scale, int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                                int64_t max_pages, const int32_t* seq_lens, int64_t batch, int32_t n_q, int32_t n_kv,
+                                int32_t head_dim, float softmax_scale, coda_bf16* O, float* lse, void* ws,
+                                size_t ws_bytes, coda_stream stream) {
+  CK(check_shape(batch, batch, batch, n_q, n_kv, head_dim, softmax_scale));
+  if (max_pages < 0) return CODA_ERR_INVALID_ARG;
+  coda::DecodeArgs a{};
+  CK(check_cache(a.c, codes, sf, scale, num_pages, page_size, n_kv, head_dim));
+  if (batch == 0) return CODA_OK;
+  if (!Q || !seq_lens || !O || !lse || (max_pages > 0 && !block_table) || ldq < int64_t(n_q) * head_dim)
+    return CODA_ERR_INVALID_ARG;
+  if (!al16(Q) || !al16(O) || !al4(lse) || !al4(block_table) || !al4(seq_lens) || ldq % 8) return CODA_ERR_ALIGNMENT;
+  a.group = n_q / n_kv;
+  a.splits = (a.group + coda::DEC_HEADS - 1) / coda::DEC_HEADS;
+  // key positions and work units are 32-bit on the device
+  const int64_t longest = max_pages * page_size;
+  if (max_pages >= (int64_t(1) << 31) || longest >= (int64_t(1) << 31) - 256 ||
+      batch * ((longest + 127) / 128) * n_kv * a.splits >= (int64_t(1) << 31) - 65536)
+    return CODA_ERR_UNSUPPORTED;
+  CK(check_ws(ws, ws_bytes, coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, head_dim)));
+  const int sms = coda::device_sms();
+  if (sms <= 0) return CODA_ERR_CUDA;
+  Cursor cur{static_cast<uint8_t*>(ws)};
+  DecodeLayout l{};
+  lay_decode(cur, l, batch, a.group);
+  a.Q = B(Q);
+  a.ldq = ldq;
+  a.table = block_table;
+  a.max_pages = static_cast<int>(max_pages);
+  a.seq_lens = seq_lens;
+  a.B = static_cast<int>(batch);
+  a.n_q = n_q;
+  a.scale_log2 = static_cast<float>(softmax_scale * LOG2E);
+  a.O = B(O);
+  a.lse = lse;
+  a.units = l.units;
+  a.part = l.part;
+  a.part_lse = l.part_lse;
+  a.part_heads = std::min(a.group, coda::DEC_HEADS);
+  a.status = static_cast<int*>(ws);
+  CU(coda::launch_attn_decode(a, sms, static_cast<cudaStream_t>(stream)));
   return CODA_OK;
 }
 

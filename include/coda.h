@@ -747,6 +747,57 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
                    int32_t head_dim, float scale, coda_bf16* O, float* lse, int64_t Tq, int64_t Tk,
                    void* ws, size_t ws_bytes, coda_stream stream);
 
+/* ------------------------------------------------------------------------
+ * A paged key/value cache held in 4 bits, and attention of single new tokens
+ * over it (serving form of coda_attention).
+ *
+ * A row (one token's key or value of one head, 128 elements) is held as
+ * coda_quantize_nvfp4_rows defines it: 64 bytes of e2m1 codes (element 2j in
+ * the low nibble of byte j), an e4m3 scale per 16 elements, an fp32 scale:
+ * 76 bytes instead of 256.  The cache is three arrays, 16-byte aligned:
+ *   codes  [num_pages, 2, n_kv, page_size, 64] bytes
+ *   sf     [num_pages, 2, n_kv, page_size, 8]  bytes (e4m3)
+ *   scale  [num_pages, 2, n_kv, page_size]     fp32
+ * with plane 0 the keys and 1 the values.  page_size is a power of two >= 16;
+ * a token's slot is page * page_size + offset, num_pages * page_size < 2^31.
+ * ---------------------------------------------------------------------- */
+
+/* Quantises the rows of T tokens into their slots: K, V [T, n_kv*128] bf16
+ * (row strides ldk, ldv), slots [T] int32.  A negative slot skips its token;
+ * one behind the cache sets CODA_ERR_PAGE_RANGE and skips it.  Slots of one
+ * call must differ: what a slot named twice holds is unspecified (rows may mix
+ * the two tokens).  ws: 256 bytes (the status word). */
+int coda_kv_append_nvfp4(const coda_bf16* K, int64_t ldk, const coda_bf16* V, int64_t ldv, const int32_t* slots,
+                         int64_t T, uint8_t* codes, uint8_t* sf, float* scale, int64_t num_pages, int32_t page_size,
+                         int32_t n_kv, int32_t head_dim, void* ws, size_t ws_bytes, coda_stream stream);
+
+/* The rows of T slots back as K, V [T, n_kv*128] in dtype CODA_BF16 or
+ * CODA_F32 (e2m1 * e4m3 * scale: one fp32 rounding, then bf16's): a cached
+ * prefix in front of new tokens for coda_attention.  A negative slot gives
+ * zeros; one behind the cache too, and sets CODA_ERR_PAGE_RANGE. */
+int coda_kv_read_nvfp4(const uint8_t* codes, const uint8_t* sf, const float* scale, int64_t num_pages,
+                       int32_t page_size, const int32_t* slots, int64_t T, int32_t n_kv, int32_t head_dim, void* K,
+                       void* V, int dtype, void* ws, size_t ws_bytes, coda_stream stream);
+
+/* One query token per sequence over its first seq_lens[b] cached tokens (its
+ * own, appended before, among them):
+ *   s_j = softmax_scale q . k_j,  O = sum_j exp(s_j - lse) v_j
+ * Q [batch, n_q*128] bf16 (row stride ldq); block_table [batch, max_pages]
+ * int32: the pages of sequence b in order (entries behind its last page are
+ * not read); seq_lens [batch] int32; O [batch, n_q*128] bf16, lse
+ * [batch, n_q] fp32.  A length of 0 gives O = 0, lse = -inf.  A negative
+ * length, or one beyond max_pages * page_size, sets CODA_ERR_SEQLEN_RANGE and
+ * counts as 0; a page outside the cache sets CODA_ERR_PAGE_RANGE and its keys
+ * are left out.  The weights are rounded to f16 before the second product,
+ * Q is scaled per head by a power of two and held in f16; everything else is
+ * fp32 until O's rounding.  softmax_scale > 0 and finite. */
+size_t coda_attention_decode_nvfp4_workspace_size(int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
+int coda_attention_decode_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
+                                const float* scale, int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                                int64_t max_pages, const int32_t* seq_lens, int64_t batch, int32_t n_q, int32_t n_kv,
+                                int32_t head_dim, float softmax_scale, coda_bf16* O, float* lse, void* ws,
+                                size_t ws_bytes, coda_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

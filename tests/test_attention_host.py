@@ -76,3 +76,51 @@ def test_oracle_forward_pins():
     # one key: its value, whatever the score
     one = O.attention_fwd(Q[:1], K[:1], V[:1], [0, 1], [0, 1], n_q, n_kv, 5.0)
     assert np.allclose(one["O"].reshape(n_q, d), np.repeat(V[:1].reshape(n_kv, d), 2, axis=0))
+
+
+# --------------------------------------------------------------------------- the 4-bit cache
+
+def append(lib, K=FAKE, ldk=256, V=FAKE, ldv=256, slots=FAKE, T=5, codes=FAKE, sf=FAKE, scale=FAKE, pages=4, page=16,
+           n_kv=2, d=128, ws=FAKE, ws_bytes=256):
+    return lib.coda_kv_append_nvfp4(K, ldk, V, ldv, slots, T, codes, sf, scale, pages, page, n_kv, d, ws, ws_bytes, None)
+
+
+def read(lib, codes=FAKE, sf=FAKE, scale=FAKE, pages=4, page=16, slots=FAKE, T=5, n_kv=2, d=128, K=FAKE, V=FAKE,
+         dtype=0, ws=FAKE, ws_bytes=256):
+    return lib.coda_kv_read_nvfp4(codes, sf, scale, pages, page, slots, T, n_kv, d, K, V, dtype, ws, ws_bytes, None)
+
+
+def decode(lib, Q=FAKE, ldq=512, codes=FAKE, sf=FAKE, scale=FAKE, pages=4, page=16, table=FAKE, max_pages=4, lens=FAKE,
+           batch=3, n_q=4, n_kv=2, d=128, sm=0.1, O=FAKE, lse=FAKE, ws=FAKE, ws_bytes=WS):
+    return lib.coda_attention_decode_nvfp4(Q, ldq, codes, sf, scale, pages, page, table, max_pages, lens, batch, n_q,
+                                           n_kv, d, sm, O, lse, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("call, change, code", [
+    (append, dict(K=None), 1), (append, dict(slots=None), 1), (append, dict(codes=None), 1), (append, dict(T=-1), 1),
+    (append, dict(ldk=128), 1), (append, dict(page=0), 1), (append, dict(page=24), 3), (append, dict(page=8), 3),
+    (append, dict(pages=1 << 27), 3), (append, dict(d=64), 3), (append, dict(V=FAKE + 2), 2), (append, dict(ldv=260), 2),
+    (append, dict(sf=FAKE + 8), 2), (append, dict(ws=None), 4), (append, dict(ws_bytes=128), 4), (append, dict(T=0), 0),
+    (read, dict(K=None), 1), (read, dict(dtype=2), 1), (read, dict(slots=None), 1), (read, dict(page=48), 3),
+    (read, dict(V=FAKE + 4), 2), (read, dict(ws=None), 4), (read, dict(T=0), 0),
+    (decode, dict(Q=None), 1), (decode, dict(table=None), 1), (decode, dict(lens=None), 1), (decode, dict(O=None), 1),
+    (decode, dict(batch=-1), 1), (decode, dict(max_pages=-1), 1), (decode, dict(sm=0.0), 1), (decode, dict(ldq=256), 1),
+    (decode, dict(n_q=3), 3), (decode, dict(d=96), 3), (decode, dict(page=100), 3), (decode, dict(max_pages=1 << 28), 3),
+    (decode, dict(Q=FAKE + 2), 2), (decode, dict(ldq=516), 2), (decode, dict(lens=FAKE + 1), 2),
+    (decode, dict(ws=None), 4), (decode, dict(ws_bytes=4096), 4), (decode, dict(batch=0), 0),
+])
+def test_cache_refusals(lib, call, change, code):
+    assert call(lib, **change) == code
+
+
+def test_binding_refuses_cache_shapes():
+    cache = coda.kv_cache_nvfp4(2, 16, 2, device="cpu")
+    assert cache["codes"].shape == (2, 2, 2, 16, 64) and cache["sf"].shape == (2, 2, 2, 16, 8)
+    x = torch.zeros(3, 256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        coda.kv_append_nvfp4(x, x, torch.zeros(3, dtype=torch.int32), cache)
+    with pytest.raises(TypeError):
+        coda.kv_read_nvfp4(cache, torch.zeros(3, dtype=torch.int32), dtype=torch.float16)
+    bad = dict(cache, sf=cache["sf"][:1])
+    with pytest.raises(ValueError, match="cache sf"):
+        coda.kv_read_nvfp4(bad, torch.zeros(3, dtype=torch.int32))

@@ -1,0 +1,252 @@
+"""The 4-bit key/value cache against the fp64 oracle: append (codes and scales
+bit for bit), read back, and single-token attention over it.
+
+Tolerances of the attention, from the kernel's roundings:
+
+  scores  K' = e2m1 * e4m3 and Q (scaled by a power of two) are exact in f16
+          up to f16's smallest step for Q elements far below the head's
+          largest (2^-25 of it); 128 products summed in fp32 are off by at
+          most 128 * 2^-24 of their absolute sum, three fp32 factors by
+          2^-24 of the score each:
+            e = scale (128 2^-24 sum|q k| + 128 2^-25 max|q| max|k|) + 2^-22 |s|
+  O       weights times row scales are rounded to f16: half a step is 2^-11
+          relative, or 2^-25 of at least the largest weighted row scale
+          (the kernel keeps that between 1 and 2^8 units), times values of at
+          most 2688; O is rounded to bf16 once (2^-8); a weight moves by
+          exp(+-2e); the sums over n keys add n 2^-24 each.
+  lse     off by e, n 2^-24, and 2^-22 (|lse| + 16) for the fp32 logarithms
+          and products.
+"""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import coda_oracle as O
+from parity import to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+D = 128
+
+
+@pytest.fixture(scope="module")
+def coda():
+    import gemm_epilogue_transformer_bf16_gb300 as c
+    from gemm_epilogue_transformer_bf16_gb300 import _build
+    _build.build()
+    c.load()
+    return c
+
+
+def rows(T, n_kv, seed, spread=True):
+    """bf16 rows of very different sizes, a zero row and a row of one element
+    among them."""
+    x = synth.randn_bf16((T, n_kv * D), 1.0, seed).float()
+    if spread:
+        g = torch.Generator().manual_seed(seed + 50)
+        x *= torch.exp2(torch.randint(-12, 12, (T, 1), generator=g).float())
+    x = x.to(torch.bfloat16)
+    if T > 3:
+        x[1] = 0
+        x[2] = 0
+        x[2, 5] = 3.0
+    return x
+
+
+def oracle_rows(x, n_kv):
+    """codes [T, n_kv, 64], sf [T, n_kv, 8], scale [T, n_kv], values [T, n_kv*128]."""
+    T = x.shape[0]
+    codes, sf, s, vals = O.quantize_nvfp4_rows(to_np(x).reshape(T * n_kv, D))
+    packed = (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+    return (packed.reshape(T, n_kv, 64), sf.reshape(T, n_kv, 8), s.reshape(T, n_kv),
+            (vals * s.astype(np.float64)[:, None]).reshape(T, n_kv * D))
+
+
+@pytest.mark.parametrize("T, page, pages, n_kv", [(1, 16, 2, 1), (7, 16, 3, 3), (130, 64, 5, 2), (65, 256, 1, 8)])
+def test_append_and_read(coda, T, page, pages, n_kv):
+    K, V = rows(T, n_kv, 1), rows(T, n_kv, 2)
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(3))[:T].to(torch.int32)
+    if T > 4:
+        slots[4] = -1                                   # skipped
+    cache = coda.kv_cache_nvfp4(pages, page, n_kv)
+    for t in cache.values():
+        t.fill_(77)                                     # what no token names must stay
+    ws = coda.workspace(256)
+    # rows as columns of one wider tensor
+    kv = torch.cat([K, V], dim=1).to(DEV)
+    k, v = kv.split([n_kv * D, n_kv * D], dim=1)
+    coda.kv_append_nvfp4(k, v, slots.to(DEV), cache, ws=ws)
+    assert coda.get_status(ws) == 0
+    live = (slots >= 0).numpy()
+    want = {n: t.clone().fill_(77).cpu().numpy() for n, t in cache.items()}
+    at = slots.numpy()[live]
+    for plane, x in enumerate((K, V)):
+        for name, part in zip(("codes", "sf", "scale"), oracle_rows(x, n_kv)):
+            want[name][at // page, plane, :, at % page] = part[live]
+    for name in want:
+        assert np.array_equal(cache[name].cpu().numpy(), want[name]), name
+    back = coda.kv_read_nvfp4(cache, slots.to(DEV), dtype=torch.float32, ws=ws)
+    half = coda.kv_read_nvfp4(cache, slots.to(DEV), ws=ws)
+    assert coda.get_status(ws) == 0
+    for n, x in (("K", K), ("V", V)):
+        val = oracle_rows(x, n_kv)[3]
+        val[~live] = 0
+        f32 = torch.from_numpy(val).float()             # the exact product, rounded once
+        assert torch.equal(back[n].cpu(), f32), n
+        assert torch.equal(half[n].cpu(), f32.to(torch.bfloat16)), n
+
+
+def test_slots_outside_the_cache_set_status(coda):
+    n_kv, page, pages = 2, 16, 2
+    K, V = rows(5, n_kv, 1).to(DEV), rows(5, n_kv, 2).to(DEV)
+    cache = coda.kv_cache_nvfp4(pages, page, n_kv)
+    ws = coda.workspace(256)
+    slots = torch.tensor([0, 32, 5, -3, 31], dtype=torch.int32, device=DEV)
+    coda.kv_append_nvfp4(K, V, slots, cache, ws=ws)
+    assert coda.get_status(ws) == 10                     # CODA_ERR_PAGE_RANGE
+    coda.reset_status(ws)
+    good = torch.tensor([0, 5, 31], dtype=torch.int32, device=DEV)
+    got = coda.kv_read_nvfp4(cache, good, dtype=torch.float32, ws=ws)["K"].cpu()
+    assert torch.equal(got, torch.from_numpy(oracle_rows(K.cpu(), n_kv)[3][[0, 2, 4]]).float())
+    assert coda.get_status(ws) == 0
+    z = coda.kv_read_nvfp4(cache, slots, ws=ws)
+    assert coda.get_status(ws) == 10 and torch.all(z["V"][[1, 3]] == 0)
+
+
+def fill(coda, lens, page, n_kv, spread, seed=7):
+    """A cache with the sequences' rows on shuffled pages, its table, and what
+    the rows stand for (per sequence, [len, n_kv*128])."""
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 2
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+    table = torch.full((len(lens), max(need + [0]) + 1), 1 << 28, dtype=torch.int32)   # entries that must not be read
+    cache = coda.kv_cache_nvfp4(pages, page, n_kv)
+    cache["sf"].fill_(0x7F)                              # unwritten rows hold NaN scales
+    cache["scale"].fill_(float("nan"))
+    ks, vs, slots, at = [], [], [], 0
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = order[at:at + need[b]]
+        j = torch.arange(n)
+        slots.append(table[b][(j // page)] * page + (j % page).to(torch.int32))
+        ks.append(rows(n, n_kv, seed + 10 * b, False))
+        vs.append(rows(n, n_kv, seed + 10 * b + 1, spread))
+        at += need[b]
+    if sum(lens):
+        coda.kv_append_nvfp4(torch.cat(ks).to(DEV), torch.cat(vs).to(DEV), torch.cat(slots).to(torch.int32).to(DEV), cache)
+    val = [[oracle_rows(x, n_kv)[3] if x.shape[0] else np.zeros((0, n_kv * D)) for x in part] for part in (ks, vs)]
+    scl = [oracle_rows(x, n_kv)[2] if x.shape[0] else np.zeros((0, n_kv)) for x in vs]
+    return cache, table, val[0], val[1], scl
+
+
+def check_decode(out, Q, lens, kval, vval, vscale, n_q, n_kv, scale):
+    cq = np.arange(len(lens) + 1)
+    ck = np.concatenate([[0], np.cumsum(lens)]).astype(int)
+    K, V = np.concatenate(kval), np.concatenate(vval)
+    ref = O.attention_fwd(Q, K, V, cq, ck, n_q, n_kv, scale)
+    got, lse = to_np(out["O"]), to_np(out["lse"])
+    for b, n in enumerate(lens):
+        for h in range(n_q):
+            kv = h // (n_q // n_kv)
+            c = slice(h * D, (h + 1) * D)
+            if n == 0:
+                assert np.all(got[b, c] == 0) and np.isneginf(lse[b, h])
+                continue
+            q, k = Q[b, c], K[ck[b]:ck[b + 1], kv * D:(kv + 1) * D]
+            s = scale * (k @ q)
+            e = (scale * (D * 2.0 ** -24 * np.abs(k) @ np.abs(q) + D * 2.0 ** -25 * np.abs(q).max() * np.abs(k).max())
+                 + 2.0 ** -22 * np.abs(s)).max()
+            p = np.exp(s - ref["lse"][h, b])
+            rel = np.expm1(2 * e) + 4 * n * 2.0 ** -24 + 2.0 ** -20
+            small = n * 2.0 ** -25 * (p * vscale[b][:, kv]).max() * 2688
+            bound = (2.0 ** -11 + rel) * ref["A"][b, c] * (1 + 2.0 ** -8) + small + 2.0 ** -8 * np.abs(ref["O"][b, c])
+            err = np.abs(got[b, c] - ref["O"][b, c])
+            assert np.all(err <= bound), (b, h, float((err - bound).max()), float(err.max()))
+            assert abs(lse[b, h] - ref["lse"][h, b]) <= e + n * 2.0 ** -24 + 2.0 ** -22 * (abs(ref["lse"][h, b]) + 16)
+
+
+CASES = {
+    # lens, page, n_q, n_kv, values of very different sizes, std of Q
+    "one_token": ([1], 16, 2, 2, False, 1.0),
+    "page_ends": ([16, 17, 31, 32, 33], 16, 4, 2, False, 1.0),
+    "unit_ends": ([127, 128, 129, 255, 257], 64, 8, 1, True, 1.0),
+    "empty_among": ([0, 5, 0, 300, 0], 32, 6, 2, True, 1.0),
+    "all_empty": ([0, 0], 16, 4, 4, False, 1.0),
+    "group_of_16": ([77, 400], 64, 32, 2, True, 1.0),
+    "group_of_40": ([50, 290], 64, 40, 1, True, 1.0),
+    "odd_group": ([513], 128, 7, 1, True, 1.0),
+    "split_over_ctas": ([9000], 256, 8, 1, True, 1.0),
+    "peaked": ([700, 90], 64, 8, 2, True, 60.0),
+    "flat": ([700, 90], 64, 8, 2, True, 0.0),
+    "tiny_q": ([300], 64, 4, 1, False, 2.0 ** -40),
+    "many": (list(range(1, 60)), 16, 8, 8, False, 1.0),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_decode(coda, name):
+    lens, page, n_q, n_kv, spread, std = CASES[name]
+    cache, table, kval, vval, vs = fill(coda, lens, page, n_kv, spread)
+    Q = synth.randn_bf16((len(lens), n_q * D), std, 99)
+    ws = coda.workspace(coda.load().coda_attention_decode_nvfp4_workspace_size(len(lens), n_q, n_kv, D))
+    out = coda.attention_decode_nvfp4(Q.to(DEV), cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                      n_q, ws=ws)
+    assert coda.get_status(ws) == 0
+    check_decode(out, to_np(Q), lens, kval, vval, vs, n_q, n_kv, D ** -0.5)
+
+
+def test_decode_bad_lengths_and_pages_set_status(coda):
+    n_q, n_kv, page, lens = 4, 2, 16, [40, 20, 33]
+    cache, table, kval, vval, vs = fill(coda, lens, page, n_kv, False)
+    Q = synth.randn_bf16((3, n_q * D), 1.0, 5)
+    ws = coda.workspace(coda.load().coda_attention_decode_nvfp4_workspace_size(3, n_q, n_kv, D))
+
+    def run(tab, n):
+        return coda.attention_decode_nvfp4(Q.to(DEV), cache, tab.to(DEV), torch.tensor(n, dtype=torch.int32, device=DEV),
+                                           n_q, ws=ws)
+    for bad in (-1, table.shape[1] * page + 1):
+        out = run(table, [40, bad, 33])
+        assert coda.get_status(ws) == 9                  # CODA_ERR_SEQLEN_RANGE
+        coda.reset_status(ws)
+        check_decode(out, to_np(Q), [40, 0, 33], [kval[0], kval[1][:0], kval[2]], [vval[0], vval[1][:0], vval[2]],
+                     [vs[0], vs[1][:0], vs[2]], n_q, n_kv, D ** -0.5)
+    for bad in (-1, cache["scale"].shape[0]):
+        tab = table.clone()
+        tab[0, 1] = bad                                  # keys 16 .. 31 of sequence 0 are left out
+        out = run(tab, lens)
+        assert coda.get_status(ws) == 10                 # CODA_ERR_PAGE_RANGE
+        coda.reset_status(ws)
+        keep = np.r_[0:16, 32:40]
+        check_decode(out, to_np(Q), [24, 20, 33], [kval[0][keep], kval[1], kval[2]],
+                     [vval[0][keep], vval[1], vval[2]], [vs[0][keep], vs[1], vs[2]], n_q, n_kv, D ** -0.5)
+
+
+def test_decode_offsets_beyond_32_bits(coda):
+    """Rows whose byte offsets pass 2^32: pages at the end of a large cache."""
+    n_q, n_kv, page = 8, 8, 256
+    pages = (1 << 32) // (2 * n_kv * page * 64) + 40     # codes alone pass 4 GiB
+    cache = {"codes": torch.zeros(pages, 2, n_kv, page, 64, dtype=torch.uint8, device=DEV),
+             "sf": torch.zeros(pages, 2, n_kv, page, 8, dtype=torch.uint8, device=DEV),
+             "scale": torch.zeros(pages, 2, n_kv, page, device=DEV)}
+    lens = [300]
+    table = torch.tensor([[pages - 1, pages - 3]], dtype=torch.int32)
+    j = torch.arange(300)
+    slots = (table[0][j // page].long() * page + j % page).to(torch.int32)
+    K, V = rows(300, n_kv, 1, False), rows(300, n_kv, 2)
+    coda.kv_append_nvfp4(K.to(DEV), V.to(DEV), slots.to(DEV), cache)
+    Q = synth.randn_bf16((1, n_q * D), 1.0, 5)
+    out = coda.attention_decode_nvfp4(Q.to(DEV), cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), n_q)
+    back = coda.kv_read_nvfp4(cache, slots.to(DEV), dtype=torch.float32)
+    (_, _, _, kv), (_, _, sc, vv) = oracle_rows(K, n_kv), oracle_rows(V, n_kv)
+    assert torch.equal(back["K"].cpu(), torch.from_numpy(kv).float())
+    check_decode(out, to_np(Q), lens, [kv], [vv], [sc], n_q, n_kv, D ** -0.5)
+
+
+def test_decode_twice_gives_the_same_bits(coda):
+    lens = [5000, 3, 700]
+    cache, table, *_ = fill(coda, lens, 64, 2, True)
+    Q = synth.randn_bf16((3, 8 * D), 1.0, 5).to(DEV)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    a = coda.attention_decode_nvfp4(Q, cache, table.to(DEV), n, 8)
+    b = coda.attention_decode_nvfp4(Q, cache, table.to(DEV), n, 8)
+    assert torch.equal(a["O"], b["O"]) and torch.equal(a["lse"], b["lse"])
