@@ -30,7 +30,7 @@ __all__ = [
     "linear_sigmoid", "linear_sigmoid_bwd", "quantize_fp8_rows", "linear_fp8", "linear_swiglu_fp8", "quantize_nvfp4_rows", "rmsnorm_scale_nvfp4", "linear_nvfp4",
     "linear_swiglu_nvfp4", "quantize_fp8_cols", "linear_qknorm_rope_fp8", "linear_cross_entropy_fp8",
     "linear_cross_entropy_bwd_fp8", "linear_dswiglu_fp8", "rmsnorm_linear_dx_fp8",
-    "linear_qknorm_rope_bwd_fp8", "launch_count", "attention",
+    "linear_qknorm_rope_bwd_fp8", "launch_count", "attention", "attention_bwd",
     "kv_cache_nvfp4", "kv_append_nvfp4", "kv_read_nvfp4", "attention_decode_nvfp4",
     "MAP_NONE", "MAP_SWIGLU", "MAP_DSWIGLU", "MAP_QKNORM_ROPE", "MAP_CE_LSE",
     "MAP_CE_DLOGITS", "MAP_COLDOT", "MAP_SIGMOID", "MAP_DSIGMOID", "K_MAJOR", "MN_MAJOR",
@@ -123,6 +123,9 @@ _SIGS = {
     "coda_attention_workspace_size": ([_I64, _I64, _I64, _I32, _I32, _I32], _SZ),
     "coda_attention": ([_P, _I64] * 3 + [_P, _P, _I64, _I32, _I32, _I32, _F, _P, _P, _I64, _I64, _P, _SZ, _P],
                        ctypes.c_int),
+    "coda_attention_bwd_workspace_size": ([_I64, _I64, _I64, _I32, _I32, _I32], _SZ),
+    "coda_attention_bwd": ([_P] + [_P, _I64] * 3 + [_P] * 4 + [_I64, _I32, _I32, _I32, _F, _P, _P, _P, _I64, _I64, _P,
+                                                            _SZ, _P], ctypes.c_int),
     "coda_kv_append_nvfp4": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _SZ, _P],
                              ctypes.c_int),
     "coda_kv_read_nvfp4": ([_P, _P, _P, _I64, _I32, _P, _I64, _I32, _I32, _P, _P, ctypes.c_int, _P, _SZ, _P],
@@ -988,6 +991,32 @@ def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, hea
     _same_device(O, lse, ws)
     _check("coda_attention", lib.coda_attention(*args, _bf(O, "O"), _f32(lse, "lse"), Tq, Tk, _ptr(ws), ws.numel(),
                                                 _stream(stream)))
+    return out
+
+
+def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, head_dim=128, out=None,
+                  ws=None, stream=None):
+    """Gradients dQ [Tq, n_q*128], dK, dV [Tk, n_kv*128] of attention for the
+    upstream gradient dO (coda_attention_bwd); O and lse as the forward wrote
+    them.  Rows outside every sequence stay as they are (undefined in tensors
+    allocated here)."""
+    lib = load()
+    args, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim)
+    wq, wk = n_q * head_dim, n_kv * head_dim
+    dev = Q.device
+    with _on(stream):
+        if out is None:
+            out = {"dQ": torch.empty(Tq, wq, dtype=torch.bfloat16, device=dev),
+                   "dK": torch.empty(Tk, wk, dtype=torch.bfloat16, device=dev),
+                   "dV": torch.empty(Tk, wk, dtype=torch.bfloat16, device=dev)}
+        ws = _ws(ws, lib.coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev)
+    for t, shape, name in ((dO, (Tq, wq), "dO"), (O, (Tq, wq), "O"), (lse, (n_q, Tq), "lse"),
+                           (out["dQ"], (Tq, wq), "dQ"), (out["dK"], (Tk, wk), "dK"), (out["dV"], (Tk, wk), "dV")):
+        _expect(t, shape, name)
+    _same_device(dO, O, lse, out["dQ"], out["dK"], out["dV"], ws)
+    _check("coda_attention_bwd", lib.coda_attention_bwd(
+        _bf(dO, "dO"), *args[:6], _bf(O, "O"), _f32(lse, "lse"), *args[6:], _bf(out["dQ"], "dQ"), _bf(out["dK"], "dK"),
+        _bf(out["dV"], "dV"), Tq, Tk, _ptr(ws), ws.numel(), _stream(stream)))
     return out
 
 

@@ -20,7 +20,7 @@ constexpr int ATTN_BLK = 128;  // keys per block, rows per tile
 // tensors; t0 is the run's first row within the sequence.
 struct AttnTile {
   int q0, lq, k0, lk;
-  int t0, pad0, pad1, pad2;
+  int t0, seq, pad1, pad2;
 };
 static_assert(sizeof(AttnTile) == 32, "two 16-byte loads");
 
@@ -68,13 +68,20 @@ struct AttnFwdArgs {
 cudaError_t launch_attn_fwd(const AttnFwdArgs& a, const CUtensorMap* maps, int64_t max_items, int sms,
                             cudaStream_t s);
 
+// Per-row values of the backward live in padded rows: sequence b's queries
+// start at row (q0 / 128 + b) * 128, so every 128-row tile is aligned and its
+// rows behind the sequence exist.
 struct AttnBwdArgs {
   const int* counts;
   const AttnTile* q_tiles;
   const AttnTile* k_tiles;
-  const float* lse;        // [n_q, Tq]
-  float* lse2;             // [n_q, Tp]: lse * log2(e), +inf where the row must vanish
-  float* delta;            // [n_q, Tp]: rowsum(dO * O)
+  const __nv_bfloat16* Q;   // [Tq, n_q * 128], row stride ldq
+  int64_t ldq;
+  const __nv_bfloat16* O;   // [Tq, n_q * 128]
+  const __nv_bfloat16* dO;
+  const float* lse;         // [n_q, Tq]
+  float* nlse2;             // [n_q, Tp]: -lse * log2(e); -inf where the row has no weight
+  float* ndelta;            // [n_q, Tp]: -rowsum(dO * O)
   __nv_bfloat16* dQ;       // [Tq, n_q * 128]
   __nv_bfloat16* dK;       // [Tk, n_kv * 128]
   __nv_bfloat16* dV;
@@ -84,6 +91,9 @@ struct AttnBwdArgs {
   int* status;
   uint64_t timeout_ns;
 };
+// maps: Q, K, V, dO (boxes of 64 columns x 128 rows)
+cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64_t max_q_tiles, int64_t max_k_tiles,
+                            int sms, cudaStream_t s);
 
 // --------------------------------------------------------------------- PTX
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z,
@@ -220,9 +230,13 @@ __device__ __forceinline__ AttnTile load_tile(const AttnTile* p) {
   const int4 b = __ldcg(reinterpret_cast<const int4*>(p) + 1);
   AttnTile t;
   t.q0 = a.x; t.lq = a.y; t.k0 = a.z; t.lk = a.w;
-  t.t0 = b.x; t.pad0 = t.pad1 = t.pad2 = 0;
+  t.t0 = b.x; t.seq = b.y; t.pad1 = t.pad2 = 0;
   return t;
 }
+
+// Item that CTA `c` of `n` takes in round `k`: odd rounds run backwards, so
+// with items sorted longest first every CTA gets about the same total.
+__device__ __forceinline__ int snake_item(int c, int n, int k) { return k * n + ((k & 1) ? n - 1 - c : c); }
 
 // Blocks of 128 keys that queries up to `last` (within the sequence) see.
 __device__ __forceinline__ int key_blocks(const AttnTile& t, int last) {

@@ -100,6 +100,9 @@ void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, i
   l.a.q_span = q_span;
 }
 
+// Padded rows of the backward's per-row values (see AttnBwdArgs).
+int64_t padded_rows(int64_t Tq, int64_t n_seq) { return (Tq / coda::ATTN_BLK + n_seq + 1) * coda::ATTN_BLK; }
+
 bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
   const uint64_t st[1] = {static_cast<uint64_t>(ld) * 2};
@@ -226,6 +229,80 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
   a.timeout_ns = WAIT_LIMIT_NS;
   CU(coda::launch_attn_plan(l.a, s));
   CU(coda::launch_attn_fwd(a, maps, l.max_q_tiles * (n_q >> (hs + pair_heads)), sms, s));
+  return CODA_OK;
+}
+
+size_t coda_attention_bwd_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, int32_t n_q, int32_t n_kv,
+                                         int32_t head_dim) {
+  if (check_shape(Tq, Tk, n_seq, n_q, n_kv, head_dim, 1.f) != CODA_OK) return HEADER;
+  Cursor c{nullptr};
+  PlanLayout l{};
+  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true);
+  c.take<float>(2 * n_q * padded_rows(Tq, n_seq));
+  return c.off;
+}
+
+int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t ldk,
+                       const coda_bf16* V, int64_t ldv, const coda_bf16* O, const float* lse, const int32_t* cu_q,
+                       const int32_t* cu_k, int64_t n_seq, int32_t n_q, int32_t n_kv, int32_t head_dim, float scale,
+                       coda_bf16* dQ, coda_bf16* dK, coda_bf16* dV, int64_t Tq, int64_t Tk, void* ws, size_t ws_bytes,
+                       coda_stream stream) {
+  CK(check_shape(Tq, Tk, n_seq, n_q, n_kv, head_dim, scale));
+  if ((Tq == 0 && Tk == 0) || n_seq == 0) return CODA_OK;
+  if (!cu_q || (Tq > 0 && (!Q || !dO || !O || !lse || !dQ)) || (Tk > 0 && (!K || !V || !dK || !dV)))
+    return CODA_ERR_INVALID_ARG;
+  if (!cu_k) cu_k = cu_q;
+  if (cu_k == cu_q && Tk != Tq) return CODA_ERR_INVALID_ARG;
+  const int64_t wq = int64_t(n_q) * head_dim, wk = int64_t(n_kv) * head_dim;
+  if (ldq < wq || ldk < wk || ldv < wk) return CODA_ERR_INVALID_ARG;
+  if (!al16(Q) || !al16(K) || !al16(V) || !al16(O) || !al16(dO) || !al16(dQ) || !al16(dK) || !al16(dV) || !al4(lse) ||
+      !al4(cu_q) || !al4(cu_k) || ldq % 8 || ldk % 8 || ldv % 8)
+    return CODA_ERR_ALIGNMENT;
+  CK(check_ws(ws, ws_bytes, coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim)));
+  const int sms = coda::device_sms();
+  if (sms <= 0 || !coda::tensor_map_encoder()) return CODA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Cursor c{static_cast<uint8_t*>(ws)};
+  PlanLayout l{};
+  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true);
+  l.a.cu_q = cu_q;
+  l.a.cu_k = cu_k;
+  l.a.n_seq = static_cast<int>(n_seq);
+  l.a.Tq = Tq;
+  l.a.Tk = Tk;
+  l.a.status = static_cast<int*>(ws);
+  coda::AttnBwdArgs a{};
+  a.Tp = padded_rows(Tq, n_seq);
+  a.nlse2 = c.take<float>(2 * n_q * a.Tp);
+  a.ndelta = a.nlse2 + n_q * a.Tp;
+  a.counts = l.a.plan.counts;
+  a.q_tiles = l.a.plan.q_tiles;
+  a.k_tiles = l.a.plan.k_tiles;
+  a.Q = B(Q);
+  a.ldq = ldq;
+  a.O = B(O);
+  a.dO = B(dO);
+  a.lse = lse;
+  a.dQ = B(dQ);
+  a.dK = B(dK);
+  a.dV = B(dV);
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.n_q = n_q;
+  a.n_kv = n_kv;
+  a.group = n_q / n_kv;
+  a.scale = scale;
+  a.scale_log2 = static_cast<float>(scale * LOG2E);
+  a.status = static_cast<int*>(ws);
+  a.timeout_ns = WAIT_LIMIT_NS;
+  CUtensorMap maps[4];
+  if (Tq > 0 && (!map_rows(&maps[0], Q, Tq, wq, ldq) || !map_rows(&maps[3], dO, Tq, wq, wq))) return CODA_ERR_CUDA;
+  if (Tk > 0 && (!map_rows(&maps[1], K, Tk, wk, ldk) || !map_rows(&maps[2], V, Tk, wk, ldv))) return CODA_ERR_CUDA;
+  // without queries (keys) no tile of them is ever loaded
+  if (Tq == 0) maps[0] = maps[3] = maps[1];
+  if (Tk == 0) maps[1] = maps[2] = maps[0];
+  CU(coda::launch_attn_plan(l.a, s));
+  CU(coda::launch_attn_bwd(a, maps, Tq > 0 ? l.max_q_tiles : 0, Tk > 0 ? l.max_k_tiles : 0, sms, s));
   return CODA_OK;
 }
 

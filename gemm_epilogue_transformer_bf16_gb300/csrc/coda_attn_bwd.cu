@@ -1,0 +1,816 @@
+// Causal attention over packed sequences, backward.
+//
+//   p_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i,  ds_ij = p_ij (dO_i . v_j - D_i)
+//   dv_j = sum_i p_ij dO_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+//
+// Two persistent kernels, each owning its outputs, so nothing is summed
+// through memory and the gradients do not depend on the order of anything:
+// one walks key tiles (dK, dV in TMEM, four products per block pair), one
+// walks query tiles (dQ, three products).  S and dO V^T are formed twice: 7
+// products where a single pass has 5, against fp32 sums of dQ over the key
+// tiles in global memory (64 KB per block pair and head, in an order that
+// changes from run to run).  Tensor bound.
+//
+// A small kernel first writes -lse * log2(e) and -D per row and head.
+//
+// Roundings: P and dS to bf16 before their products; dQ, dK, dV to bf16 once.
+#include <algorithm>
+
+#include "coda_attn.cuh"
+#include "coda_internal.h"
+#include "coda_status.h"
+
+namespace coda {
+namespace {
+
+constexpr int BWD_THREADS = 384;
+constexpr uint32_t TILE_BYTES = ATTN_BLK * ATTN_D * 2;  // 32 KB
+constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
+constexpr int KV_STAGES = 5;  // key-tile kernel: ring of Q and dO tiles beside K and V
+constexpr int Q_STAGES = 6;   // query-tile kernel: ring of K and V tiles
+constexpr uint32_t ROW_BYTES = 2 * ATTN_BLK * 4;  // -lse2 and -D of a tile
+constexpr uint32_t KV_SMEM = (2 + KV_STAGES) * TILE_BYTES + 2 * ROW_BYTES + 512;
+constexpr uint32_t Q_SMEM = Q_STAGES * TILE_BYTES + 512;
+static_assert(KV_SMEM <= 232448 && Q_SMEM <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ int64_t padded_row(const AttnTile& t) {
+  return (static_cast<int64_t>(t.q0 / ATTN_BLK) + t.seq) * ATTN_BLK;
+}
+
+// ------------------------------------------------------------------ row values
+// Sixteen lanes per row and head; HBM-bound (O and dO once).
+__global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const AttnBwdArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tiles = *reinterpret_cast<const volatile int*>(a.counts);
+  const int sub = threadIdx.x & 15;
+  const int per = ATTN_BLK * a.n_q;  // (row, head) pairs of a tile
+  const int chunks = (per + 127) / 128;
+  // a block takes 128 pairs at a time, sixteen per step
+  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(tiles) * chunks; w += gridDim.x) {
+    const int ti = static_cast<int>(w / chunks), ch = static_cast<int>(w - static_cast<int64_t>(ti) * chunks);
+    const AttnTile t = load_tile(a.q_tiles + ti);
+    const int64_t pad = padded_row(t) + t.t0;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int pair = ch * 128 + i * 16 + (threadIdx.x >> 4);
+      const int r = pair / a.n_q, h = pair - r * a.n_q;
+      const int row = t.t0 + r;
+      float d = 0.f;
+      const bool in = pair < per && row < t.lq;
+      if (in) {
+        const int64_t at = (static_cast<int64_t>(t.q0) + row) * a.n_q * ATTN_D + h * ATTN_D + sub * 8;
+        float x[8], y[8];
+        load_bf16x8(a.O + at, x);
+        load_bf16x8(a.dO + at, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d = fmaf(x[k], y[k], d);
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (sub == 0 && pair < per) {
+        const bool seen = in && row + 1 + t.lk - t.lq > 0;  // the row has a key
+        const float l = seen ? a.lse[static_cast<int64_t>(h) * a.Tq + t.q0 + row] : 0.f;
+        const int64_t o = static_cast<int64_t>(h) * a.Tp + pad + r;
+        a.nlse2[o] = seen ? -l * 1.4426950408889634f : -INFINITY;
+        a.ndelta[o] = seen ? -d : 0.f;
+      }
+    }
+  }
+}
+
+// Barrier waits of one role; `ok` latches the first failure.
+struct Waiter {
+  volatile int* abort_flag;
+  int* status;
+  uint64_t limit;
+  bool ok = true;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) {
+    if (ok) ok = mbar_wait_bounded(bar, parity, abort_flag, status, limit);
+    return ok;
+  }
+  // the same for a whole warp that stays converged
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, status, limit)) && ok;
+    return ok;
+  }
+};
+
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 2000000ull) {
+  }
+}
+
+// C (+)= A B^T, 128 x 128 x 128: A, B in shared memory, K-major.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t sa, uint32_t sb, bool acc, uint32_t el) {
+  constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t o = (i >> 2) * HALF_BYTES + (i & 3) * 32;
+    umma_bf16(d, sdesc_sw128(sa + o, 16, 1024), sdesc_sw128(sb + o, 16, 1024), ID, acc || i > 0, el);
+  }
+}
+// A in TMEM (64 columns, contiguous), B in shared memory, K-major.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint32_t sb, bool acc, uint32_t el) {
+  constexpr uint32_t ID = idesc_bf16(128, 128, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t o = (i >> 2) * HALF_BYTES + (i & 3) * 32;
+    umma_bf16_ts(d, ta + i * 8, sdesc_sw128(sb + o, 16, 1024), ID, acc || i > 0, el);
+  }
+}
+// C (+)= A B: A in TMEM, 64 of the contraction's columns in each half of a
+// 128-column region; B [contraction, 128] in shared memory (MN-major).
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t ta, uint32_t sb, bool acc, uint32_t el) {
+  constexpr uint32_t ID = idesc_bf16(128, 128, 0, 1);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    umma_bf16_ts(d, ta + (i >> 2) * 64 + (i & 3) * 8, sdesc_sw128(sb + i * 2048, HALF_BYTES, 1024), ID, acc || i > 0,
+                 el);
+}
+
+__device__ __forceinline__ void load_pair(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int col, int row,
+                                          uint32_t el) {
+  tma_load_2d(dst, m, bar, col, row, el);
+  tma_load_2d(dst + HALF_BYTES, m, bar, col + 64, row, el);
+}
+
+// 64 bf16 (as fp32 pairs) of a row, scaled, from 64 TMEM columns.
+__device__ __forceinline__ void store_row64(uint32_t taddr, __nv_bfloat16* dst, float scale, bool write) {
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    float v[32];
+    __syncwarp();
+    tmem_ld32(taddr + q * 32, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= scale;
+    if (write) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_bf16x8(dst + q * 32 + i * 8, v + i * 8);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+// Item: a tile of 128 keys of one key/value head; it meets the query tiles
+// that see it, for every query head of the group (iterations).
+//
+//   warps 0-7   thread = key row, warpgroup = half of the 128 queries:
+//               P^T = exp2(S^T c - lse2) and dS^T = P^T (dP^T - D), bf16,
+//               back into TMEM over their sources (each half its own).
+//   warp 8      UMMA: dV += P^T dO | S^T = K Q'^T | dK += dS^T Q | dP^T = V dO'^T
+//               (primes: the next iteration), so the exponentials run beside
+//               dK and dP^T, and dS^T beside dV and S^T.
+//   warp 9      TMA: K and V, a ring of Q and dO tiles, the rows' -lse2 and -D.
+//   warp 10     zeroes Q and dO rows behind the sequence.
+struct KvItem {
+  AttnTile t;
+  int kv, first, n;  // first query tile, query tiles
+};
+__device__ __forceinline__ KvItem kv_item(const AttnBwdArgs& a, int w) {
+  KvItem it;
+  const int ti = w / a.n_kv;
+  it.kv = w - ti * a.n_kv;
+  it.t = load_tile(a.k_tiles + ti);
+  it.first = max(0, it.t.t0 - (it.t.lk - it.t.lq)) / ATTN_BLK;
+  it.n = max(0, (it.t.lq + ATTN_BLK - 1) / ATTN_BLK - it.first);
+  return it;
+}
+
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+    attn_bwd_kv_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                       const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG,
+                       const AttnBwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t bwd_smem[];
+  uint8_t* sK = bwd_smem;
+  uint8_t* sV = sK + TILE_BYTES;
+  uint8_t* ring = sV + TILE_BYTES;
+  float* rows = reinterpret_cast<float*>(ring + KV_STAGES * TILE_BYTES);  // two buffers of -lse2 | -D
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(rows) + 2 * ROW_BYTES);
+  uint64_t* empty = full + KV_STAGES;
+  uint64_t* raw = empty + KV_STAGES;
+  uint64_t* row_full = raw + KV_STAGES;
+  uint64_t* row_empty = row_full + 2;
+  uint64_t* kv_full = row_empty + 2;
+  uint64_t* kv_empty = kv_full + 1;
+  uint64_t* s_full = kv_empty + 1;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_ready = dp_full + 1;
+  uint64_t* ds_ready = p_ready + 1;
+  uint64_t* acc_full = ds_ready + 1;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((3 * KV_STAGES + 12) * 8 + 8 <= 512, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KV_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&raw[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&row_full[b], 1);
+      mbar_init(&row_empty[b], 8);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, 8);
+    mbar_init(ds_ready, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&mQ);
+    tma_prefetch_desc(&mK);
+    tma_prefetch_desc(&mV);
+    tma_prefetch_desc(&mG);
+  }
+  if (warp == 8) {
+    tmem_alloc<false>(tmem_slot, 512);
+    tmem_relinquish<false>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv;
+  const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+  Waiter wait{abort_flag, a.status, a.timeout_ns};
+
+  // Registers: 384 threads x 168 at launch = 256 x 216 + 128 x 72
+  if (warp >= 8) {
+    reg_dec<72>();
+    if (warp == 9) {
+      // ---------------------------------------------------------- producer
+      const uint32_t el = elect_one();
+      uint32_t pos = 0, iter = 0, kvn = 0;
+      auto put = [&](const CUtensorMap& m, int col, int row, bool ragged) {
+        const uint32_t s = pos % KV_STAGES;
+        if (!wait(&empty[s], ((pos / KV_STAGES) & 1) ^ 1)) return;
+        uint64_t* bar = ragged ? &raw[s] : &full[s];
+        mbar_arrive_expect_tx(bar, TILE_BYTES, el);
+        load_pair(ring + s * TILE_BYTES, &m, bar, col, row, el);
+        ++pos;
+      };
+      for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+        const KvItem it = kv_item(a, w);
+        if (it.n == 0) continue;
+        if (!wait(kv_empty, (kvn & 1) ^ 1)) break;
+        ++kvn;
+        mbar_arrive_expect_tx(kv_full, 2 * TILE_BYTES, el);
+        load_pair(sK, &mK, kv_full, it.kv * ATTN_D, it.t.k0 + it.t.t0, el);
+        load_pair(sV, &mV, kv_full, it.kv * ATTN_D, it.t.k0 + it.t.t0, el);
+        const int64_t pad = padded_row(it.t);
+        for (int h = it.kv * a.group; h < (it.kv + 1) * a.group && wait.ok; ++h) {
+          for (int j = 0; j < it.n && wait.ok; ++j, ++iter) {
+            const int row = (it.first + j) * ATTN_BLK;
+            const bool ragged = row + ATTN_BLK > it.t.lq;
+            put(mQ, h * ATTN_D, it.t.q0 + row, ragged);
+            const uint32_t b = iter & 1;
+            if (!wait(&row_empty[b], ((iter >> 1) & 1) ^ 1)) break;
+            float* dst = rows + b * 2 * ATTN_BLK;
+            mbar_arrive_expect_tx(&row_full[b], ROW_BYTES, el);
+            bulk_load(dst, a.nlse2 + h * a.Tp + pad + row, ATTN_BLK * 4, &row_full[b], el);
+            bulk_load(dst + ATTN_BLK, a.ndelta + h * a.Tp + pad + row, ATTN_BLK * 4, &row_full[b], el);
+            put(mG, h * ATTN_D, it.t.q0 + row, ragged);
+          }
+        }
+      }
+      if (!wait.ok) let_copies_land();
+    } else if (warp == 10) {
+      // ---------------------------------------------------------- rows behind the sequence
+      uint32_t pos = 0, seen = 0;
+      for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+        const KvItem it = kv_item(a, w);
+        const int last = (it.first + it.n - 1) * ATTN_BLK;
+        for (int h = 0; h < a.group && it.n > 0 && wait.ok; ++h) {
+          pos += 2 * it.n;
+          if (last + ATTN_BLK <= it.t.lq) continue;
+          for (int x = 2; x >= 1; --x) {  // the head's last Q tile, then its dO tile
+            const uint32_t s = (pos - x) % KV_STAGES;
+            if (!wait.warp(&raw[s], (seen >> s) & 1)) break;
+            seen ^= 1u << s;
+            zero_tile_rows(ring + s * TILE_BYTES, it.t.lq - last);
+            if (lane == 0) mbar_arrive(&full[s]);
+          }
+        }
+      }
+    } else if (warp == 8) {
+      // ---------------------------------------------------------- UMMA issuer
+      const uint32_t el = elect_one();
+      uint32_t pos = 0, iter = 0, kvn = 0;
+      bool issued = false;
+      const uint32_t k_s = smem_u32(sK), v_s = smem_u32(sV), r_s = smem_u32(ring);
+      auto stage = [&](uint32_t p) { return r_s + (p % KV_STAGES) * TILE_BYTES; };
+      auto ready = [&](uint32_t p) {
+        const bool ok = wait(&full[p % KV_STAGES], (p / KV_STAGES) & 1);
+        tc_fence_after();
+        return ok;
+      };
+      for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+        const KvItem it = kv_item(a, w);
+        if (it.n == 0) continue;
+        const int n = it.n * a.group;
+        if (!wait(kv_full, kvn & 1)) break;
+        ++kvn;
+        if (!ready(pos)) break;
+        mma_ss(tS, k_s, stage(pos), false, el);
+        issued = true;
+        umma_commit(s_full, el);
+        if (!ready(pos + 1)) break;
+        mma_ss(tP, v_s, stage(pos + 1), false, el);
+        umma_commit(dp_full, el);
+        for (int i = 0; i < n; ++i, ++iter, pos += 2) {
+          if (!wait(p_ready, iter & 1)) break;
+          tc_fence_after();
+          mma_tn(tDV, tS, stage(pos + 1), i > 0, el);
+          umma_commit(&empty[(pos + 1) % KV_STAGES], el);
+          if (i + 1 < n) {
+            if (!ready(pos + 2)) break;
+            mma_ss(tS, k_s, stage(pos + 2), false, el);
+            umma_commit(s_full, el);
+          }
+          if (!wait(ds_ready, iter & 1)) break;
+          tc_fence_after();
+          mma_tn(tDK, tP, stage(pos), i > 0, el);
+          umma_commit(&empty[pos % KV_STAGES], el);
+          if (i + 1 < n) {
+            if (!ready(pos + 3)) break;
+            mma_ss(tP, v_s, stage(pos + 3), false, el);
+            umma_commit(dp_full, el);
+          }
+          if (i + 1 == n) umma_commit(acc_full, el);
+          if (i + 2 == n || n == 1) umma_commit(kv_empty, el);  // K and V have been read for the last time
+        }
+      }
+      if (!wait.ok && issued) {
+        umma_commit(drain, el);
+        mbar_wait_drain(drain, 0, 200000000ull);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ P^T, dS^T
+    reg_inc<216>();
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t mS = tS + lanes + half * 64, mP = tP + lanes + half * 64;
+    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    uint32_t iter = 0, done = 0;
+    for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+      const KvItem it = kv_item(a, w);
+      const int off = it.t.lk - it.t.lq;
+      for (int h = 0; h < a.group && wait.ok; ++h) {
+        for (int j = 0; j < it.n; ++j, ++iter) {
+          const int q0 = (it.first + j) * ATTN_BLK;
+          const bool diag = it.t.t0 + ATTN_BLK - 1 > q0 + off;          // some key is later than some query
+          const int from = it.t.t0 + r - off - q0 - half * 64;          // first query column that sees this key
+          const float* nl = rows + (iter & 1) * 2 * ATTN_BLK + half * 64;
+          const float* nd = nl + ATTN_BLK;
+          if (!wait.warp(&row_full[iter & 1], (iter >> 1) & 1)) break;
+          if (!wait.warp(s_full, iter & 1)) break;
+          tc_fence_after();
+          float p[64];
+          {
+            uint32_t s[64];
+            tmem_ld64(mS, s);
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(nl + i);
+              float z0, z1, z2, z3;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, f2_pack(l4.x, l4.y)), z0, z1);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2, f2_pack(l4.z, l4.w)), z2,
+                        z3);
+              p[i] = exp2_sfu(z0);
+              p[i + 1] = exp2_sfu(z1);
+              p[i + 2] = exp2_sfu(z2);
+              p[i + 3] = exp2_sfu(z3);
+            }
+          }
+          if (diag) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) p[i] = i >= from ? p[i] : 0.f;
+          }
+          {
+            uint32_t u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = pack_bf16x2(p[2 * i], p[2 * i + 1]);
+            tmem_st32(mS, u);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready);
+          if (!wait.warp(dp_full, iter & 1)) break;
+          tc_fence_after();
+          {
+            uint32_t d[64], u[32];
+            tmem_ld64(mP, d);
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              const float4 d4 = *reinterpret_cast<const float4*>(nd + i);
+              const uint64_t x0 = f2_mul(f2_pack(p[i], p[i + 1]),
+                                         f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])),
+                                                f2_pack(d4.x, d4.y)));
+              const uint64_t x1 = f2_mul(f2_pack(p[i + 2], p[i + 3]),
+                                         f2_add(f2_pack(__uint_as_float(d[i + 2]), __uint_as_float(d[i + 3])),
+                                                f2_pack(d4.z, d4.w)));
+              float e0, e1, e2, e3;
+              f2_unpack(x0, e0, e1);
+              f2_unpack(x1, e2, e3);
+              u[i / 2] = pack_bf16x2(e0, e1);
+              u[i / 2 + 1] = pack_bf16x2(e2, e3);
+            }
+            tmem_st32(mP, u);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(ds_ready);
+            mbar_arrive(&row_empty[iter & 1]);
+          }
+        }
+      }
+      if (!wait.ok) break;
+      // warpgroup 0 writes dV, warpgroup 1 dK
+      const int key = it.t.t0 + r;
+      const bool valid = key < it.t.lk;
+      __nv_bfloat16* dst = (half ? a.dK : a.dV) +
+                           ((static_cast<int64_t>(it.t.k0) + key) * a.n_kv + it.kv) * ATTN_D;
+      if (it.n > 0) {
+        if (!wait.warp(acc_full, done & 1)) break;
+        ++done;
+        tc_fence_after();
+        const uint32_t src = (half ? tDK : tDV) + lanes;
+        const float f = half ? a.scale : 1.f;
+        store_row64(src, dst, f, valid);
+        store_row64(src + 64, dst + 64, f, valid);
+        tc_fence_before();
+      } else if (valid) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) {
+    __syncwarp();
+    tmem_dealloc<false>(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+// Item: a tile of 128 queries of one head; it meets the key blocks it sees.
+// Q and dO go to TMEM (the A operands of S and dP), so each product reads
+// only its K or V block from shared memory:
+//   TMEM  S 128 | dP (dS over it) 128 | dQ 128 | Q 64 | dO 64
+//   UMMA  S' = Q K'^T | dQ += dS K | dP' = dO V'^T   (primes: the next block)
+struct QItem {
+  AttnTile t;
+  int head, n;
+};
+__device__ __forceinline__ QItem q_item(const AttnBwdArgs& a, int w) {
+  QItem it;
+  const int ti = w / a.n_q;
+  it.head = w - ti * a.n_q;
+  it.t = load_tile(a.q_tiles + ti);
+  it.n = key_blocks(it.t, min(it.t.t0 + ATTN_BLK, it.t.lq) - 1);
+  return it;
+}
+
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+    attn_bwd_q_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                      const AttnBwdArgs a) {
+  extern __shared__ __align__(1024) uint8_t bwd_smem[];
+  uint8_t* ring = bwd_smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + Q_STAGES * TILE_BYTES);
+  uint64_t* empty = full + Q_STAGES;
+  uint64_t* raw = empty + Q_STAGES;
+  uint64_t* qg_ready = raw + Q_STAGES;
+  uint64_t* s_full = qg_ready + 1;
+  uint64_t* s_read = s_full + 1;
+  uint64_t* dp_full = s_read + 1;
+  uint64_t* ds_ready = dp_full + 1;
+  uint64_t* acc_full = ds_ready + 1;
+  uint64_t* drain = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert((3 * Q_STAGES + 7) * 8 + 8 <= 512, "barrier area");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Q_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&raw[s], 1);
+    }
+    mbar_init(qg_ready, 8);
+    mbar_init(s_full, 1);
+    mbar_init(s_read, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&mK);
+    tma_prefetch_desc(&mV);
+  }
+  if (warp == 8) {
+    tmem_alloc<false>(tmem_slot, 512);
+    tmem_relinquish<false>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tP = tmem + 128, tDQ = tmem + 256, tQ = tmem + 384, tG = tmem + 448;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int items = *reinterpret_cast<const volatile int*>(a.counts) * a.n_q;
+  const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+  Waiter wait{abort_flag, a.status, a.timeout_ns};
+
+  if (warp >= 8) {
+    reg_dec<72>();
+    if (warp == 9) {
+      // ---------------------------------------------------------- producer
+      const uint32_t el = elect_one();
+      uint32_t pos = 0;
+      auto put = [&](const CUtensorMap& m, int col, int row, bool ragged) {
+        const uint32_t s = pos % Q_STAGES;
+        if (!wait(&empty[s], ((pos / Q_STAGES) & 1) ^ 1)) return;
+        uint64_t* bar = ragged ? &raw[s] : &full[s];
+        mbar_arrive_expect_tx(bar, TILE_BYTES, el);
+        load_pair(ring + s * TILE_BYTES, &m, bar, col, row, el);
+        ++pos;
+      };
+      for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+        const QItem it = q_item(a, w);
+        const int col = it.head / a.group * ATTN_D;
+        for (int j = 0; j < it.n && wait.ok; ++j) {
+          const int row = j * ATTN_BLK;
+          put(mK, col, it.t.k0 + row, row + ATTN_BLK > it.t.lk);
+          if (wait.ok) put(mV, col, it.t.k0 + row, false);
+        }
+      }
+      if (!wait.ok) let_copies_land();
+    } else if (warp == 10) {
+      // ---------------------------------------------------------- K rows behind the sequence
+      uint32_t pos = 0, seen = 0;
+      for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+        const QItem it = q_item(a, w);
+        pos += 2 * it.n;
+        if (it.n == 0 || it.n * ATTN_BLK <= it.t.lk) continue;
+        const uint32_t s = (pos - 2) % Q_STAGES;
+        if (!wait.warp(&raw[s], (seen >> s) & 1)) break;
+        seen ^= 1u << s;
+        zero_tile_rows(ring + s * TILE_BYTES, it.t.lk - (it.n - 1) * ATTN_BLK);
+        if (lane == 0) mbar_arrive(&full[s]);
+      }
+    } else if (warp == 8) {
+      // ---------------------------------------------------------- UMMA issuer
+      const uint32_t el = elect_one();
+      uint32_t pos = 0, iter = 0, itn = 0;
+      bool issued = false;
+      const uint32_t r_s = smem_u32(ring);
+      auto stage = [&](uint32_t p) { return r_s + (p % Q_STAGES) * TILE_BYTES; };
+      auto ready = [&](uint32_t p) {
+        const bool ok = wait(&full[p % Q_STAGES], (p / Q_STAGES) & 1);
+        tc_fence_after();
+        return ok;
+      };
+      for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+        const QItem it = q_item(a, w);
+        if (it.n == 0) continue;
+        if (!wait(qg_ready, itn & 1)) break;
+        ++itn;
+        if (!ready(pos)) break;
+        mma_ts(tS, tQ, stage(pos), false, el);
+        issued = true;
+        umma_commit(s_full, el);
+        if (!ready(pos + 1)) break;
+        mma_ts(tP, tG, stage(pos + 1), false, el);
+        umma_commit(dp_full, el);
+        umma_commit(&empty[(pos + 1) % Q_STAGES], el);
+        for (int i = 0; i < it.n; ++i, ++iter, pos += 2) {
+          if (!wait(s_read, iter & 1)) break;
+          tc_fence_after();
+          if (i + 1 < it.n) {
+            if (!ready(pos + 2)) break;
+            mma_ts(tS, tQ, stage(pos + 2), false, el);
+            umma_commit(s_full, el);
+          }
+          if (!wait(ds_ready, iter & 1)) break;
+          tc_fence_after();
+          mma_tn(tDQ, tP, stage(pos), i > 0, el);
+          umma_commit(&empty[pos % Q_STAGES], el);
+          if (i + 1 < it.n) {
+            if (!ready(pos + 3)) break;
+            mma_ts(tP, tG, stage(pos + 3), false, el);
+            umma_commit(dp_full, el);
+            umma_commit(&empty[(pos + 3) % Q_STAGES], el);
+          } else {
+            umma_commit(acc_full, el);
+          }
+        }
+      }
+      if (!wait.ok && issued) {
+        umma_commit(drain, el);
+        mbar_wait_drain(drain, 0, 200000000ull);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS, and the Q and dO operands
+    reg_inc<216>();
+    const int half = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t mS = tS + lanes + half * 64, mP = tP + lanes + half * 64;
+    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    uint32_t iter = 0, done = 0;
+    // this thread's row of the item's Q (warpgroup 0) or dO (warpgroup 1)
+    auto operand_row = [&](const QItem& it, uint32_t (&u)[64]) {
+      const int row = it.t.t0 + r;
+      if (row < it.t.lq) {
+        const int64_t grow = static_cast<int64_t>(it.t.q0) + row;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            (half ? a.dO + grow * a.n_q * ATTN_D : a.Q + grow * a.ldq) + it.head * ATTN_D);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = src[i];
+          u[4 * i] = x.x;
+          u[4 * i + 1] = x.y;
+          u[4 * i + 2] = x.z;
+          u[4 * i + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) u[i] = 0;
+      }
+    };
+    auto operand_store = [&](const uint32_t (&u)[64]) {
+      const uint32_t t = (half ? tG : tQ) + lanes;
+      tmem_st32(t, u);
+      tmem_st32(t + 32, u + 32);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qg_ready);
+    };
+    QItem it;
+    int k = 0, w = first;
+    if (w < items) {
+      it = q_item(a, w);
+      if (it.n > 0) {
+        uint32_t u[64];
+        operand_row(it, u);
+        operand_store(u);
+      }
+    }
+    while (w < items) {
+      const int row = it.t.t0 + r;
+      const int vis = min(it.t.lk, row + 1 + it.t.lk - it.t.lq);
+      const int all = it.t.t0 + 1 + it.t.lk - it.t.lq;  // keys every row sees
+      const int64_t pr = it.head * a.Tp + padded_row(it.t) + row;
+      const float nl = __ldcg(a.nlse2 + pr), nd = __ldcg(a.ndelta + pr);
+      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+      for (int j = 0; j < it.n; ++j, ++iter) {
+        const bool diag = (j + 1) * ATTN_BLK > all;
+        const int lim = vis - j * ATTN_BLK - half * 64;
+        if (!wait.warp(s_full, iter & 1)) break;
+        tc_fence_after();
+        float p[64];
+        {
+          uint32_t s[64];
+          tmem_ld64(mS, s);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            float z0, z1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nl2), z0, z1);
+            p[i] = exp2_sfu(z0);
+            p[i + 1] = exp2_sfu(z1);
+          }
+        }
+        if (!wait.warp(dp_full, iter & 1)) break;
+        tc_fence_after();
+        {
+          uint32_t d[64], u[32];
+          tmem_ld64(mP, d);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            float e0, e1;
+            f2_unpack(f2_mul(f2_pack(p[i], p[i + 1]),
+                             f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), nd2)),
+                      e0, e1);
+            if (diag) {
+              e0 = i < lim ? e0 : 0.f;
+              e1 = i + 1 < lim ? e1 : 0.f;
+            }
+            u[i / 2] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(mP, u);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_ready);
+      }
+      if (!wait.ok) break;
+      // the next item's operands are on their way while this one's last product runs
+      const int wn = snake_item(first, step, ++k);
+      QItem nx = it;
+      nx.n = 0;
+      uint32_t u[64];
+      if (wn < items) {
+        nx = q_item(a, wn);
+        if (nx.n > 0) operand_row(nx, u);
+      }
+      if (it.n > 0) {
+        if (!wait.warp(acc_full, done & 1)) break;
+        ++done;
+        tc_fence_after();
+      }
+      if (nx.n > 0) operand_store(u);
+      __nv_bfloat16* dst = a.dQ + ((static_cast<int64_t>(it.t.q0) + row) * a.n_q + it.head) * ATTN_D + half * 64;
+      const bool valid = row < it.t.lq;
+      if (it.n > 0) {
+        store_row64(tDQ + lanes + half * 64, dst, a.scale, valid);
+        tc_fence_before();
+      } else if (valid) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
+      }
+      it = nx;
+      w = wn;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) {
+    __syncwarp();
+    tmem_dealloc<false>(tmem, 512);
+  }
+}
+
+template <class... Exp, class... Act>
+cudaError_t launch(void (*kern)(Exp...), int64_t grid, unsigned threads, uint32_t smem, cudaStream_t s, Act&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, grid)));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = attn_programmatic_launch() ? 1 : 0;
+  note_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Exp>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64_t max_q_tiles, int64_t max_k_tiles,
+                            int sms, cudaStream_t s) {
+  cudaError_t e = attn_smem_attribute(reinterpret_cast<const void*>(attn_bwd_kv_kernel), 3, KV_SMEM);
+  if (e != cudaSuccess) return e;
+  e = attn_smem_attribute(reinterpret_cast<const void*>(attn_bwd_q_kernel), 4, Q_SMEM);
+  if (e != cudaSuccess) return e;
+  if (max_q_tiles > 0) {
+    e = launch(attn_bwd_rows_kernel, std::min<int64_t>(int64_t(8) * sms, max_q_tiles * a.n_q), 256, 0, s, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (max_k_tiles > 0) {
+    e = launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv), BWD_THREADS, KV_SMEM, s, maps[0],
+               maps[1], maps[2], maps[3], a);
+    if (e != cudaSuccess) return e;
+  }
+  if (max_q_tiles == 0) return cudaSuccess;
+  return launch(attn_bwd_q_kernel, std::min<int64_t>(sms, max_q_tiles * a.n_q), BWD_THREADS, Q_SMEM, s, maps[1],
+                maps[2], a);
+}
+
+}  // namespace coda

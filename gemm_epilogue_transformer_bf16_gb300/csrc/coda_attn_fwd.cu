@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   griddep_wait();
   griddep_launch_dependents();
   const int items = *reinterpret_cast<const volatile int*>(a.counts) * (a.n_q >> (a.head_shift + a.pair_heads));
-  const int step = static_cast<int>(gridDim.x);
+  const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
   bool ok = true;
 
   // Registers: 384 threads x 168 at launch = 256 x 216 + 128 x 72.  Each
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       ++pos;
       return true;
     };
-    for (int w = blockIdx.x; w < items && ok; w += step) {
+    for (int k = 0, w = first; w < items && ok; w = snake_item(first, step, ++k)) {
       const FwdItem it = fwd_item(a, w);
       const int n = max(it.n[0], it.n[1]);
 #pragma unroll
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------ rows behind the sequence
     uint32_t pos = 0, seen = 0;  // seen: bit s = parity of kv_raw[s]'s next phase
-    for (int w = blockIdx.x; w < items && ok; w += step) {
+    for (int k = 0, w = first; w < items && ok; w = snake_item(first, step, ++k)) {
       const FwdItem it = fwd_item(a, w);
       const int n = max(it.n[0], it.n[1]);
       if (n > 0 && n * ATTN_BLK > it.t.lk) {
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       umma_commit(&s_full[x], el);
       issued = true;
     };
-    for (int w = blockIdx.x; w < items && ok; w += step) {
+    for (int k = 0, w = first; w < items && ok; w = snake_item(first, step, ++k)) {
       const FwdItem it = fwd_item(a, w);
       const int n = max(it.n[0], it.n[1]);
       if (n == 0) continue;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     const int tok = r >> a.head_shift, hd = r & ((1 << a.head_shift) - 1);
     const float c = a.scale_log2;
     uint32_t sn = 0, on = 0;
-    for (int w = blockIdx.x; w < items && ok; w += step) {
+    for (int k = 0, w = first; w < items && ok; w = snake_item(first, step, ++k)) {
       const FwdItem it = fwd_item(a, w);
       const int n = x ? it.n[1] : it.n[0];
       const int row0 = x ? it.row[1] : it.row[0];

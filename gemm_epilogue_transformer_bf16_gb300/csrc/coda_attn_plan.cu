@@ -83,7 +83,8 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
       e.k0 = a.cu_k[lo];
       e.lk = a.cu_k[lo + 1] - e.k0;
       e.t0 = (t - sd.prefix[lo]) * sd.span;
-      e.pad0 = e.pad1 = e.pad2 = 0;
+      e.seq = lo;
+      e.pad1 = e.pad2 = 0;
       int w;
       if (sd.keys) {
         const int first = max(0, e.t0 - (e.lk - e.lq)) / ATTN_BLK;   // first query block that sees the run
@@ -98,7 +99,7 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
         const int at = atomicAdd(&hist[bin], 1);
         int4* o = reinterpret_cast<int4*>(sd.out + at);
         o[0] = make_int4(e.q0, e.lq, e.k0, e.lk);
-        o[1] = make_int4(e.t0, 0, 0, 0);
+        o[1] = make_int4(e.t0, e.seq, 0, 0);
       }
     }
     __syncthreads();

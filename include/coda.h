@@ -747,6 +747,23 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
                    int32_t head_dim, float scale, coda_bf16* O, float* lse, int64_t Tq, int64_t Tk,
                    void* ws, size_t ws_bytes, coda_stream stream);
 
+/* Backward of coda_attention for the upstream gradient dO [Tq, n_q*128] (O and
+ * lse as the forward wrote them; O, dO, and the gradients contiguous):
+ *   p_ij = exp(s_ij - lse_i),  D_i = dO_i . O_i,  ds_ij = p_ij (dO_i . v_j - D_i),
+ *   dQ_i = scale sum_j ds_ij k_j,  dK_j = scale sum_i ds_ij q_i,
+ *   dV_j = sum_i p_ij dO_i,
+ * dK and dV summed over the n_q / n_kv query heads of a key/value head.  dQ
+ * [Tq, n_q*128], dK, dV [Tk, n_kv*128] bf16; rows outside every sequence stay
+ * as they are.  P and dS are rounded to bf16 before their products, sums are
+ * fp32, and their order is fixed: two runs give the same bits. */
+size_t coda_attention_bwd_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, int32_t n_q, int32_t n_kv,
+                                         int32_t head_dim);
+int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t ldk,
+                       const coda_bf16* V, int64_t ldv, const coda_bf16* O, const float* lse, const int32_t* cu_q,
+                       const int32_t* cu_k, int64_t n_seq, int32_t n_q, int32_t n_kv, int32_t head_dim, float scale,
+                       coda_bf16* dQ, coda_bf16* dK, coda_bf16* dV, int64_t Tq, int64_t Tk, void* ws, size_t ws_bytes,
+                       coda_stream stream);
+
 /* ------------------------------------------------------------------------
  * A paged key/value cache held in 4 bits, and attention of single new tokens
  * over it (serving form of coda_attention).

@@ -58,7 +58,7 @@ __all__ = [
     "E2M1_MAX", "E2M1_GRID", "NVFP4_BLOCK", "e2m1_round", "e2m1_value", "quantize_nvfp4_rows",
     "rmsnorm_scale_nvfp4",
     "linear_nvfp4_fwd", "swiglu_nvfp4_fwd",
-    "attention_fwd",
+    "attention_fwd", "attention_bwd",
 ]
 
 
@@ -792,3 +792,42 @@ def attention_fwd(Q, K, V, cu_q, cu_k, n_q, n_kv, scale):
             O[q0:q1, c] = p @ V[k0:k1, kc]
             A[q0:q1, c] = p @ np.abs(V[k0:k1, kc])
     return {"O": O, "lse": lse, "A": A}
+
+
+def attention_bwd(dO, Q, K, V, cu_q, cu_k, n_q, n_kv, scale):
+    """dQ, dK, dV for the upstream gradient dO, and the sums that scale their
+    rounding errors: bQ, bK, bV (what relative errors of the weights p and of
+    ds, and absolute errors of dO.v - D, add up to; see the arguments below).
+
+    With u the relative error of a weight and t_i an absolute error of
+    dO_i.v_j - D_i:  |err ds_ij| <= u p_ij (|dP_ij| + |D_i|) + p_ij t_i, so
+      EQ = scale sum_j |ds_ij| |k_j|            (bf16 rounding of ds)
+      UQ = scale sum_j p_ij (|dP_ij| + |D_i|) |k_j|
+      TQ = scale sum_j p_ij t_i |k_j|,  t_i = sum_d |dO_id| (|O_id| + A_id)
+    and likewise for dK with |q_i|; EV = sum_i p_ij |dO_i| serves dV."""
+    d = Q.shape[1] // n_q
+    g = n_q // n_kv
+    f = attention_fwd(Q, K, V, cu_q, cu_k, n_q, n_kv, scale)
+    out = {n: np.zeros(Q.shape) for n in ("dQ", "EQ", "UQ", "TQ")}
+    out.update({n: np.zeros(K.shape) for n in ("dK", "EK", "UK", "TK", "dV", "EV")})
+    for q0, q1, k0, k1 in _attention_spans(cu_q, cu_k):
+        for h in range(n_q):
+            c, kc = slice(h * d, (h + 1) * d), slice((h // g) * d, (h // g + 1) * d)
+            q, k, v, do = Q[q0:q1, c], K[k0:k1, kc], V[k0:k1, kc], dO[q0:q1, c]
+            p, _ = _attention_weights(q, k, scale)
+            dp = do @ v.T
+            D = np.sum(do * f["O"][q0:q1, c], axis=1, keepdims=True)
+            t = np.sum(np.abs(do) * (np.abs(f["O"][q0:q1, c]) + f["A"][q0:q1, c]), axis=1, keepdims=True)
+            ds = p * (dp - D)
+            u = p * (np.abs(dp) + np.abs(D))
+            out["dQ"][q0:q1, c] = scale * ds @ k
+            out["EQ"][q0:q1, c] = scale * np.abs(ds) @ np.abs(k)
+            out["UQ"][q0:q1, c] = scale * u @ np.abs(k)
+            out["TQ"][q0:q1, c] = scale * (p * t) @ np.abs(k)
+            out["dK"][k0:k1, kc] += scale * ds.T @ q
+            out["EK"][k0:k1, kc] += scale * np.abs(ds).T @ np.abs(q)
+            out["UK"][k0:k1, kc] += scale * u.T @ np.abs(q)
+            out["TK"][k0:k1, kc] += scale * (p * t).T @ np.abs(q)
+            out["dV"][k0:k1, kc] += p.T @ do
+            out["EV"][k0:k1, kc] += p.T @ np.abs(do)
+    return out

@@ -179,3 +179,172 @@ def test_forward_bad_offsets_set_status(coda):
         coda.reset_status(ws)
     coda.attention(d["Q"], d["K"], d["V"], torch.tensor([0, 64, 128], dtype=torch.int32, device=DEV), n_q, n_kv, ws=ws)
     assert coda.get_status(ws) == 0
+
+
+# --------------------------------------------------------------------------- backward
+#
+# Gradients, from the kernel's roundings.  p is recomputed as
+# exp2(s c - lse2) from fp32 scores and the forward's lse: relative error
+# u = exp(2 e') - 1, e' = e + |lse| 2^-22 + n 2^-24 + 2^-20.  For dV it is
+# rounded to bf16 (2^-8).  dO.v is an fp32 sum of 128 products (far below the
+# next term); D uses the forward's bf16 O, off by 2^-8 (|O| + sum p |v|) per
+# element and so by 2^-8 t_i.  ds is rounded to bf16 (2^-8), the sums over
+# n rows add n 2^-24, the outputs are rounded to bf16 once (2^-8).
+
+def check_backward(got, r, t, cq, ck, n_q, n_kv, scale):
+    e = score_error(t, cq, ck, n_q, n_kv, scale).max()
+    lse = O.attention_fwd(to_np(t["Q"]), to_np(t["K"]), to_np(t["V"]), cq, ck, n_q, n_kv, scale)["lse"]
+    top = np.abs(np.where(np.isfinite(lse), lse, 0)).max()
+    n = max(int((ck[1:] - ck[:-1]).max()), int((cq[1:] - cq[:-1]).max()), 1) * (n_q // n_kv)
+    u = np.expm1(2 * (e + top * 2.0 ** -22 + n * 2.0 ** -24 + 2.0 ** -20))
+    h = 2.0 ** -8
+    more = 1 + 4 * h                                       # products of the relative errors above
+    bounds = {"dQ": more * ((h + n * 2.0 ** -24) * r["EQ"] + u * r["UQ"] + h * r["TQ"]) + h * np.abs(r["dQ"]),
+              "dK": more * ((h + n * 2.0 ** -24) * r["EK"] + u * r["UK"] + h * r["TK"]) + h * np.abs(r["dK"]),
+              "dV": more * (h + u + n * 2.0 ** -24) * r["EV"] + h * np.abs(r["dV"])}
+    for name, b in bounds.items():
+        cu = cq if name == "dQ" else ck
+        rows = slice(int(cu[0]), int(cu[-1]))
+        err = np.abs(to_np(got[name]) - r[name])[rows]
+        assert np.all(err <= b[rows]), (name, float((err - b[rows]).max()), float(err.max()))
+        ref = np.linalg.norm(r[name][rows])
+        if ref > 0:
+            assert np.linalg.norm(err) <= 1e-2 * ref, (name, float(np.linalg.norm(err) / ref))
+
+
+def run_backward(coda, t, cq, ck, n_q, n_kv, same, fill=7.0):
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu = torch.from_numpy(cq).to(DEV)
+    kw = {} if same else {"cu_seqlens_k": torch.from_numpy(ck).to(DEV)}
+    f = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, **kw)
+    out = {"dQ": torch.full_like(d["Q"], fill), "dK": torch.full_like(d["K"], fill), "dV": torch.full_like(d["V"], fill)}
+    ws = coda.workspace(coda.load().coda_attention_bwd_workspace_size(d["Q"].shape[0], d["K"].shape[0], len(cq) - 1, n_q,
+                                                                      n_kv, D))
+    coda.attention_bwd(d["dO"], d["Q"], d["K"], d["V"], f["O"], f["lse"], cu, n_q, n_kv, out=out, ws=ws, **kw)
+    assert coda.get_status(ws) == 0
+    return out
+
+
+BWD_CASES = {k: CASES[k] for k in CASES if k != "long"}
+BWD_CASES["long"] = ([1100], None, 4, 2, 0, 0)
+BWD_CASES["queries_missing"] = ([0, 40], [200, 60], 4, 2, 0, 5)
+
+
+@pytest.mark.parametrize("name", BWD_CASES)
+def test_backward(coda, name):
+    lq, lk, n_q, n_kv, front, pad = BWD_CASES[name]
+    t, cq, ck, Tq, Tk = make(lq, lk, n_q, n_kv, front, pad, seed=len(name))
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 77)
+    out = run_backward(coda, t, cq, ck, n_q, n_kv, lk is None)
+    ref = O.attention_bwd(to_np(t["dO"]), to_np(t["Q"]), to_np(t["K"]), to_np(t["V"]), cq, ck, n_q, n_kv, D ** -0.5)
+    check_backward(out, ref, t, cq, ck, n_q, n_kv, D ** -0.5)
+    for k, cu in (("dQ", cq), ("dK", ck), ("dV", ck)):     # rows outside every sequence stay as they were
+        outside = np.ones(out[k].shape[0], bool)
+        outside[cu[0]:cu[-1]] = False
+        assert torch.all(out[k].cpu()[torch.from_numpy(outside)] == 7), k
+
+
+@pytest.mark.parametrize("std", [0.0, 8.0])
+def test_backward_flat_and_peaked_scores(coda, std):
+    n_q, n_kv = 2, 1
+    t, cq, _, Tq, _ = make([400, 30], None, n_q, n_kv, seed=11, std=std)
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 78)
+    out = run_backward(coda, t, cq, cq, n_q, n_kv, True)
+    ref = O.attention_bwd(to_np(t["dO"]), to_np(t["Q"]), to_np(t["K"]), to_np(t["V"]), cq, cq, n_q, n_kv, D ** -0.5)
+    if std == 0.0:
+        # all weights equal: dK = 0 exactly in the formula when Q = 0; the kernel's sums of zeros are zeros
+        assert torch.all(out["dK"] == 0)
+        ref["dK"][:] = 0
+    check_backward(out, ref, t, cq, cq, n_q, n_kv, D ** -0.5)
+
+
+def test_backward_against_differences(coda):
+    """Directional differences of sum(O dO) in fp64 against the kernel's
+    gradients.  The difference quotient's own error is O(step^2), 1e-8 here;
+    the gradients are bf16, so their inner product with a unit direction is
+    off by at most the Frobenius rule's 1e-2 of |gradient|."""
+    n_q, n_kv = 2, 1
+    t, cq, _, Tq, _ = make([150, 20], None, n_q, n_kv, seed=4)
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 79)
+    out = run_backward(coda, t, cq, cq, n_q, n_kv, True)
+    x = {k: to_np(v) for k, v in t.items()}
+    rng = np.random.default_rng(1)
+    for k in ("Q", "K", "V"):
+        dirn = rng.normal(size=x[k].shape)
+        dirn /= np.linalg.norm(dirn)
+        f = []
+        for sgn in (1, -1):
+            y = dict(x, **{k: x[k] + sgn * 1e-4 * dirn})
+            f.append(np.sum(O.attention_fwd(y["Q"], y["K"], y["V"], cq, cq, n_q, n_kv, D ** -0.5)["O"] * x["dO"]))
+        g = to_np(out["d" + k])
+        assert abs((f[0] - f[1]) / 2e-4 - np.sum(g * dirn)) <= 1e-2 * np.linalg.norm(g), k
+
+
+@pytest.mark.parametrize("lens", [[100, 60], [130, 140], [5, 9, 3]])
+def test_backward_non_finite_rows_stay_in_their_sequence(coda, lens):
+    n_q, n_kv, pad = 4, 2, 30
+    t, cq, _, Tq, _ = make(lens, None, n_q, n_kv, 0, pad, seed=3)
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 80)
+    clean = run_backward(coda, t, cq, cq, n_q, n_kv, True)
+    for k in ("Q", "K", "V", "dO"):
+        for bad in (float("nan"), float("inf")):
+            e = {n: v.clone() for n, v in t.items()}
+            e[k][int(cq[1]):int(cq[2])] = bad
+            e[k][int(cq[-1]):] = bad
+            got = run_backward(coda, e, cq, cq, n_q, n_kv, True)
+            for lo, hi in [(int(cq[0]), int(cq[1]))] + [(int(a), int(b)) for a, b in zip(cq[2:-1], cq[3:])]:
+                for g in ("dQ", "dK", "dV"):
+                    assert torch.equal(got[g][lo:hi], clean[g][lo:hi]), (k, bad, g)
+
+
+def test_twice_gives_the_same_bits_and_so_does_a_graph(coda):
+    n_q, n_kv = 6, 2
+    t, cq, _, Tq, _ = make([500, 3, 260, 129], None, n_q, n_kv, seed=6)
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 81)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu = torch.from_numpy(cq).to(DEV)
+    lib = coda.load()
+    ws = coda.workspace(max(lib.coda_attention_workspace_size(Tq, Tq, 4, n_q, n_kv, D),
+                            lib.coda_attention_bwd_workspace_size(Tq, Tq, 4, n_q, n_kv, D)))
+
+    def step(f, b):
+        coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, out=f, ws=ws)
+        coda.attention_bwd(d["dO"], d["Q"], d["K"], d["V"], f["O"], f["lse"], cu, n_q, n_kv, out=b, ws=ws)
+
+    def buffers():
+        return ({"O": torch.zeros_like(d["Q"]), "lse": torch.zeros(n_q, Tq, device=DEV)},
+                {"dQ": torch.zeros_like(d["Q"]), "dK": torch.zeros_like(d["K"]), "dV": torch.zeros_like(d["V"])})
+    one, two, three = buffers(), buffers(), buffers()
+    step(*one)
+    step(*two)
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(cap):
+        step(*three)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=cap):
+        step(*three)
+    for part in three:
+        for v in part.values():
+            v.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert coda.get_status(ws) == 0
+    for a, b, c in zip(one, two, three):
+        for k in a:
+            assert torch.equal(a[k], b[k]) and torch.equal(a[k], c[k]), k
+
+
+def test_on_another_stream(coda):
+    """A call that names a stream allocates and runs there."""
+    n_q, n_kv = 4, 2
+    t, cq, _, Tq, _ = make([300, 41], None, n_q, n_kv, seed=8)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu = torch.from_numpy(cq).to(DEV)
+    want = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, stream=side)
+    side.synchronize()
+    assert torch.equal(got["O"], want["O"]) and torch.equal(got["lse"], want["lse"])

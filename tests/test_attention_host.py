@@ -124,3 +124,38 @@ def test_binding_refuses_cache_shapes():
     bad = dict(cache, sf=cache["sf"][:1])
     with pytest.raises(ValueError, match="cache sf"):
         coda.kv_read_nvfp4(bad, torch.zeros(3, dtype=torch.int32))
+
+
+# --------------------------------------------------------------------------- backward
+
+def bwd(lib, dO=FAKE, Q=FAKE, ldq=512, K=FAKE, ldk=256, V=FAKE, ldv=256, O=FAKE, lse=FAKE, cu_q=FAKE, cu_k=None,
+        n_seq=2, n_q=4, n_kv=2, d=128, scale=0.1, dQ=FAKE, dK=FAKE, dV=FAKE, Tq=64, Tk=64, ws=FAKE, ws_bytes=WS):
+    return lib.coda_attention_bwd(dO, Q, ldq, K, ldk, V, ldv, O, lse, cu_q, cu_k, n_seq, n_q, n_kv, d, scale, dQ, dK, dV,
+                                  Tq, Tk, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change, code", [
+    *[({n: None}, 1) for n in ("dO", "Q", "K", "V", "O", "lse", "cu_q", "dQ", "dK", "dV")],
+    (dict(Tk=65), 1), (dict(scale=0.0), 1), (dict(ldq=256), 1), (dict(d=256), 3), (dict(n_q=3), 3),
+    *[({n: FAKE + 2}, 2) for n in ("dO", "Q", "K", "V", "O", "dQ", "dK", "dV")], (dict(ldv=260), 2),
+    (dict(ws=None), 4), (dict(ws_bytes=1024), 4), (dict(Tq=0, Tk=0), 0), (dict(n_seq=0), 0),
+])
+def test_backward_refusals(lib, change, code):
+    assert bwd(lib, **change) == code
+
+
+def test_oracle_backward_against_differences():
+    rng = np.random.default_rng(2)
+    n_q, n_kv, d = 4, 2, 4
+    cq, ck = [0, 3, 5], [0, 5, 6]
+    x = {"Q": rng.normal(size=(5, n_q * d)), "K": rng.normal(size=(6, n_kv * d)), "V": rng.normal(size=(6, n_kv * d))}
+    dO = rng.normal(size=(5, n_q * d))
+    r = O.attention_bwd(dO, x["Q"], x["K"], x["V"], cq, ck, n_q, n_kv, 0.4)
+    for name in x:
+        for i in np.ndindex(x[name].shape):
+            f = []
+            for s in (1, -1):
+                y = {k: v.copy() for k, v in x.items()}
+                y[name][i] += s * 1e-6
+                f.append(np.sum(O.attention_fwd(y["Q"], y["K"], y["V"], cq, ck, n_q, n_kv, 0.4)["O"] * dO))
+            assert abs((f[0] - f[1]) / 2e-6 - r["d" + name][i]) < 1e-7
