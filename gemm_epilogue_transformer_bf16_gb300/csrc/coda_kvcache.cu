@@ -22,6 +22,19 @@ __device__ __forceinline__ uint32_t e2m1x2_f16(uint32_t byte) {
   const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
   return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
 }
+// The eight codes of a word as four f16 pairs (byte by byte, low nibble
+// first), exact: the conversion takes its byte from the register, without
+// shifts and masks.
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
   return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
@@ -436,20 +449,22 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
         const uint4 w0 = *reinterpret_cast<const uint4*>(kp), w1 = *reinterpret_cast<const uint4*>(kp + 512);
         const uint32_t f0 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(st + ST_SFK + (16 * h + pi) * 8 + 2 * c));
         const uint32_t f1 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(st + ST_SFK + (16 * h + pi + 8) * 8 + 2 * c));
+        // both halves of the scale register: block 2c for the first 16 elements, 2c + 1 for the others
+        const uint32_t g00 = __byte_perm(f0, f0, 0x1010), g01 = __byte_perm(f0, f0, 0x3232);
+        const uint32_t g10 = __byte_perm(f1, f1, 0x1010), g11 = __byte_perm(f1, f1, 0x3232);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t a_ = k < 2 ? w0.x : k < 4 ? w0.y : k < 6 ? w0.z : w0.w;
-          const uint32_t b_ = k < 2 ? w1.x : k < 4 ? w1.y : k < 6 ? w1.z : w1.w;
-          const int sh = (k & 1) * 16;
-          // both halves of the scale register: block 2c for the first 16 elements, 2c + 1 for the others
-          const uint32_t g0 = k < 4 ? __byte_perm(f0, f0, 0x1010) : __byte_perm(f0, f0, 0x3232);
-          const uint32_t g1 = k < 4 ? __byte_perm(f1, f1, 0x1010) : __byte_perm(f1, f1, 0x3232);
-          const uint32_t a0 = hmul2(e2m1x2_f16((a_ >> sh) & 0xFFu), g0);
-          const uint32_t a1 = hmul2(e2m1x2_f16((b_ >> sh) & 0xFFu), g1);
-          const uint32_t a2 = hmul2(e2m1x2_f16((a_ >> (sh + 8)) & 0xFFu), g0);
-          const uint32_t a3 = hmul2(e2m1x2_f16((b_ >> (sh + 8)) & 0xFFu), g1);
+        for (int k = 0; k < 8; k += 2) {
+          uint32_t x[4], y[4];
+          e2m1x8_f16(k == 0 ? w0.x : k == 2 ? w0.y : k == 4 ? w0.z : w0.w, x);
+          e2m1x8_f16(k == 0 ? w1.x : k == 2 ? w1.y : k == 4 ? w1.z : w1.w, y);
+          const uint32_t g0 = k < 4 ? g00 : g01, g1 = k < 4 ? g10 : g11;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(z[t][h], a0, a1, a2, a3, q[t][2 * k], q[t][2 * k + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0 = hmul2(x[2 * i], g0), a1 = hmul2(y[2 * i], g1);
+            const uint32_t a2 = hmul2(x[2 * i + 1], g0), a3 = hmul2(y[2 * i + 1], g1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma_f16(z[t][h], a0, a1, a2, a3, q[t][2 * (k + i)], q[t][2 * (k + i) + 1]);
+          }
         }
         const float* rk = reinterpret_cast<const float*>(st + ST_RSK) + 16 * h + pi;
         const float r0 = rk[0], r1 = rk[8];
@@ -568,12 +583,14 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
           const uint32_t od0 = ((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u);
           const uint32_t ev1 = (x2 & 0x0F0F0F0Fu) | ((x3 << 4) & 0xF0F0F0F0u);
           const uint32_t od1 = ((x2 >> 4) & 0x0F0F0F0Fu) | (x3 & 0xF0F0F0F0u);
+          uint32_t e0[4], o0[4], e1[4], o1[4];
+          e2m1x8_f16(ev0, e0);
+          e2m1x8_f16(od0, o0);
+          e2m1x8_f16(ev1, e1);
+          e2m1x8_f16(od1, o1);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = hmul2(e2m1x2_f16((ev0 >> (8 * j)) & 0xFFu), g0);
-            const uint32_t a1 = hmul2(e2m1x2_f16((od0 >> (8 * j)) & 0xFFu), g0);
-            const uint32_t a2 = hmul2(e2m1x2_f16((ev1 >> (8 * j)) & 0xFFu), g1);
-            const uint32_t a3 = hmul2(e2m1x2_f16((od1 >> (8 * j)) & 0xFFu), g1);
+            const uint32_t a0 = hmul2(e0[j], g0), a1 = hmul2(o0[j], g0), a2 = hmul2(e1[j], g1), a3 = hmul2(o1[j], g1);
 #pragma unroll
             for (int t = 0; t < NT; ++t) mma_f16(o[t][half * 4 + j], a0, a1, a2, a3, p[t][0], p[t][1]);
           }
