@@ -184,8 +184,10 @@ __global__ void __launch_bounds__(256)
 // whose stretch covers a whole (sequence, head) writes the output itself;
 // the others leave normalised partial outputs, merged by a second kernel.
 //
-// A warp takes tiles of 32 keys, copied to its own shared-memory ring by
-// cp.async two tiles ahead.  Products are m16n8k16 on f16:
+// A fifth warp copies units into a shared-memory ring by bulk copies (one per
+// page and array), ahead of the four that compute and across the ends of
+// stretches; each of the four takes 32 keys of a unit.  Products are m16n8k16
+// on f16:
 //   S^T [16 keys x 8 heads] = K Q^T:  e2m1 * e4m3 has at most 6 significant
 //     bits, so K' = code * sf is exact in f16; the row scale multiplies S.
 //     A lane's 16 bytes of a key row are 32 neighbouring elements, two blocks
@@ -197,26 +199,18 @@ __global__ void __launch_bounds__(256)
 // The keys of a tile are read in the order 0 4 1 5 2 6 3 7: then the lanes'
 // shared-memory reads of both K and V are contiguous, and movmatrix turns
 // the S^T fragment into the P operand.
-constexpr int DEC_WARPS = 4;
+constexpr int DEC_WARPS = 4;  // computing warps
+constexpr int DEC_THREADS = (DEC_WARPS + 1) * 32;
 constexpr int DEC_STAGES = 3;
-constexpr int DEC_TILE = 32;
 constexpr int DEC_UNIT = 128;
-constexpr int ST_K = 0, ST_V = 2048, ST_SFK = 4096, ST_SFV = 4352, ST_RSK = 4608, ST_RSV = 4736;
-constexpr int DEC_STAGE_BYTES = 4864;
-constexpr int DEC_SMEM = DEC_WARPS * DEC_STAGES * DEC_STAGE_BYTES;
-static_assert(DEC_SMEM >= DEC_WARPS * DEC_HEADS * (128 + 4) * 4, "merge buffer");
+constexpr int ST_K = 0, ST_V = 8192, ST_SFK = 16384, ST_SFV = 17408, ST_RSK = 18432, ST_RSV = 18944;
+constexpr int DEC_STAGE_BYTES = 19456;
+// ring, merge buffer (two warps' fragments), barriers and page masks
+constexpr uint32_t dec_smem_bytes(int nt) { return DEC_STAGES * DEC_STAGE_BYTES + 2 * nt * (4096 + 256) + 128; }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -224,7 +218,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -244,66 +238,55 @@ __device__ __forceinline__ int decode_len(const DecodeArgs& a, int b, bool tell)
   return n;
 }
 
-// Copies keys [key, key + 32) of the sequence, those below `len` whose pages
-// are in the cache; returns one bit per 16-key half that has such keys.
-__device__ __forceinline__ uint32_t decode_fetch(const DecodeArgs& a, const int32_t* table, int kvh, int key, int len,
-                                                 uint32_t stage) {
-  const int lane = threadIdx.x & 31;
-  const KvCache& c = a.c;
-  uint32_t halves = 0;
-  int64_t row[2];  // of the keys plane
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int k = key + 16 * h;
-    row[h] = 0;
-    if (k < len) {
-      const int page = table[k >> c.page_shift];
-      if (page >= 0 && page < c.num_pages) {
-        halves |= 1u << h;
-        row[h] = cache_row(c, page, 0, kvh, k & ((1 << c.page_shift) - 1));
-      } else if (lane == 0) {
-        atomicOr(a.status, CODA_DEV_PAGE_RANGE);
-      }
+// A CTA's way along the line of units: stretches of one (sequence, virtual
+// head).  Every warp walks it for itself.
+struct Stretch {
+  int b, before;        // sequence, units before it
+  int u;                // next unit of the line
+  // current stretch
+  int first, nu, stop;  // its first unit, its units, where this CTA stops in it
+  int vh, len;
+  __device__ __forceinline__ void next(const DecodeArgs& a, int vheads, int last) {
+    len = decode_len(a, b, false);
+    nu = (len + DEC_UNIT - 1) / DEC_UNIT;
+    while (u >= before + nu * vheads) {
+      before += nu * vheads;
+      len = decode_len(a, ++b, false);
+      nu = (len + DEC_UNIT - 1) / DEC_UNIT;
     }
+    vh = (u - before) / nu;
+    first = before + vh * nu;
+    stop = min(last, first + nu);
   }
-  const int64_t plane = static_cast<int64_t>(c.n_kv) << c.page_shift;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int h = i >> 1;
-    const uint32_t o = i * 512 + lane * 16;
-    const uint8_t* src = c.codes + row[h] * 64 + (o & 1023);
-    const bool on = (halves >> h) & 1;
-    cp_async16(stage + ST_K + o, src, on);
-    cp_async16(stage + ST_V + o, on ? src + plane * 64 : src, on);
-  }
-  {
-    const int h = (lane >> 3) & 1;  // 8 lanes cover 16 keys of one plane
-    const bool on = (halves >> h) & 1;
-    const int64_t r = row[h] + (on && lane >= 16 ? plane : 0);
-    cp_async16(stage + ST_SFK + lane * 16, c.sf + r * 8 + (lane & 7) * 16, on);
-    if (lane < 16) {
-      const int h2 = (lane >> 2) & 1;  // 4 lanes cover 16 keys
-      const bool on2 = (halves >> h2) & 1;
-      const int64_t r2 = row[h2] + (on2 && lane >= 8 ? plane : 0);
-      cp_async16(stage + ST_RSK + lane * 16, c.scale + r2 + (lane & 3) * 4, on2);
-    }
-  }
-  return halves;
-}
+};
 
 template <int NT>
-__global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kernel(const DecodeArgs a) {
   extern __shared__ __align__(128) uint8_t dec_smem[];
-  __shared__ int sh_warp[DEC_WARPS], sh_seq, sh_before;
+  __shared__ int sh_warp[DEC_WARPS + 1], sh_seq, sh_before;
+  float* merge = reinterpret_cast<float*>(dec_smem + DEC_STAGES * DEC_STAGE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(dec_smem + DEC_STAGES * DEC_STAGE_BYTES + 2 * NT * (4096 + 256));
+  uint64_t* empty = full + DEC_STAGES;
+  uint32_t* pages_in = reinterpret_cast<uint32_t*>(empty + DEC_STAGES);  // per stage: bit i = keys 16 i .. 16 i + 15 are there
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(pages_in + DEC_STAGES);
+  static_assert(2 * DEC_STAGES * 8 + DEC_STAGES * 4 + 4 <= 128, "barrier area");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int vheads = a.c.n_kv * a.splits;
+  if (tid == 0) {
+    for (int s = 0; s < DEC_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], DEC_WARPS);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
   griddep_wait();
   griddep_launch_dependents();
 
   // units before each sequence: a contiguous run of sequences per thread,
   // scanned over the block
-  const int chunk = (a.B + DEC_WARPS * 32 - 1) / (DEC_WARPS * 32);
+  const int chunk = (a.B + DEC_THREADS - 1) / DEC_THREADS;
   const int s0 = min(a.B, tid * chunk), s1 = min(a.B, s0 + chunk);
   int mine = 0;
   for (int b = s0; b < s1; ++b) mine += (decode_len(a, b, blockIdx.x == 0) + DEC_UNIT - 1) / DEC_UNIT * vheads;
@@ -317,7 +300,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int w = 0; w < DEC_WARPS; ++w) {
+  for (int w = 0; w <= DEC_WARPS; ++w) {
     if (w < warp) incl += sh_warp[w];
     total += sh_warp[w];
   }
@@ -342,27 +325,87 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
   __syncthreads();
   if (first >= last) return;
 
-  uint8_t* ring = dec_smem + warp * DEC_STAGES * DEC_STAGE_BYTES;
-  const uint32_t ring_u = smem_u32(ring);
-  int b = sh_seq, before = sh_before;
-  int u = first;
-  while (u < last) {
-    // next (sequence, virtual head) stretch
-    int len = decode_len(a, b, false);
-    int nu = (len + DEC_UNIT - 1) / DEC_UNIT;
-    while (u >= before + nu * vheads) {
-      before += nu * vheads;
-      len = decode_len(a, ++b, false);
-      nu = (len + DEC_UNIT - 1) / DEC_UNIT;
+  Stretch x;
+  x.b = sh_seq;
+  x.before = sh_before;
+  x.u = first;
+  uint32_t it = 0;  // units so far: stage it % DEC_STAGES
+  bool ok = true;
+
+  if (warp == DEC_WARPS) {
+    // ------------------------------------------------------------ copies
+    // Lane i of each group of eight takes part i of a unit (a page, or 128
+    // keys of one): group 0 the codes, 1 the block scales, 2 the row scales,
+    // keys and values each.
+    const KvCache& kc = a.c;
+    const int part = lane & 7, arr = lane >> 3;
+    const int part_shift = min(kc.page_shift, 7);
+    const uint32_t row_bytes = arr == 0 ? 64 : arr == 1 ? 8 : 4;
+    const uint32_t to_k = arr == 0 ? ST_K : arr == 1 ? ST_SFK : ST_RSK, to_v = arr == 0 ? ST_V : arr == 1 ? ST_SFV : ST_RSV;
+    const uint8_t* src = arr == 0 ? kc.codes : arr == 1 ? kc.sf : reinterpret_cast<const uint8_t*>(kc.scale);
+    const int64_t plane = static_cast<int64_t>(kc.n_kv) << kc.page_shift;
+    while (x.u < last && ok) {
+      x.next(a, vheads, last);
+      const int kvh = x.vh / a.splits;
+      const int32_t* table = a.table + static_cast<int64_t>(x.b) * a.max_pages;
+      auto page_of = [&](int u) {  // of this lane's part of unit u; -1: nothing there
+        const int k = (u - x.first) * DEC_UNIT + (part << part_shift);
+        return u < x.stop && (part << part_shift) < DEC_UNIT && k < x.len ? table[k >> kc.page_shift] : -1;
+      };
+      int page = page_of(x.u);
+      for (; x.u < x.stop; ++x.u, ++it) {
+        const int nextp = page_of(x.u + 1);
+        const int k = (x.u - x.first) * DEC_UNIT + (part << part_shift);
+        const bool named = (part << part_shift) < DEC_UNIT && k < x.len;
+        const bool in = named && page >= 0 && page < kc.num_pages;
+        if (named && !in && arr == 0) atomicOr(a.status, CODA_DEV_PAGE_RANGE);
+        // whole groups of 16 keys: rows behind the length exist within the page
+        const int n = in ? min(1 << part_shift, (x.len - k + 15) & ~15) : 0;
+        const uint32_t bytes = arr < 3 ? n * row_bytes : 0;
+        const uint32_t s = it % DEC_STAGES;
+        ok = mbar_wait_bounded(&empty[s], ((it / DEC_STAGES) & 1) ^ 1, abort_flag, a.status, 2000000000ull, 100);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, 2 * bytes);
+        const uint32_t mask = __reduce_or_sync(0xffffffffu, arr == 0 && n ? ((1u << (n / 16)) - 1) << (part << part_shift >> 4) : 0);
+        if (lane == 0) {
+          pages_in[s] = mask;
+          if (sum == 0) mbar_arrive(&full[s]);
+        }
+        mbar_arrive_expect_tx(&full[s], sum, lane == 0 && sum != 0);
+        __syncwarp();
+        if (bytes) {
+          const int64_t row = cache_row(kc, page, 0, kvh, k & ((1 << kc.page_shift) - 1));
+          uint8_t* st = dec_smem + s * DEC_STAGE_BYTES + (part << part_shift) * row_bytes;
+          bulk_load(st + to_k, src + row * row_bytes, bytes, &full[s], 1);
+          bulk_load(st + to_v, src + (row + plane) * row_bytes, bytes, &full[s], 1);
+        }
+        page = nextp;
+      }
     }
-    const int vh = (u - before) / nu;
-    const int h_first = before + vh * nu;               // the stretch's units are [h_first, h_first + nu)
-    const int stop = min(last, h_first + nu);
-    const int key0 = (u - h_first) * DEC_UNIT, key1 = min(len, (stop - h_first) * DEC_UNIT);
-    const int kvh = vh / a.splits;
-    const int head0 = kvh * a.group + (vh - kvh * a.splits) * DEC_HEADS;
+    if (!ok) {
+      // let every copy already issued land before the CTA's memory is reused
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {
+      }
+    }
+    return;
+  }
+
+  const int pi = (g >> 1) + (g & 1) * 4;  // key of fragment row g; row g + 8 is 8 keys on
+  // this lane's places in a stage, of the warp's 32 keys
+  const uint8_t* k_at = dec_smem + ST_K + (warp * 32 + pi) * 64 + c * 16;
+  const uint8_t* sfk_at = dec_smem + ST_SFK + (warp * 32 + pi) * 8 + 2 * c;
+  const uint8_t* rsk_at = dec_smem + ST_RSK + (warp * 32 + pi) * 4;
+  const uint8_t* v_at = dec_smem + ST_V + (warp * 32 + c) * 64 + g * 8;
+  const uint8_t* sfv_at = dec_smem + ST_SFV + (warp * 32 + c) * 8 + g;
+  const uint8_t* rsv_at = dec_smem + ST_RSV + (warp * 32 + pi) * 4;
+  while (x.u < last) {
+    x.next(a, vheads, last);
+    const int u0 = x.u;
+    const int kvh = x.vh / a.splits;
+    const int head0 = kvh * a.group + (x.vh - kvh * a.splits) * DEC_HEADS;
     const int heads = min(DEC_HEADS, (kvh + 1) * a.group - head0);
-    const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
 
     // Q of head g (+ 8 per n tile), elements 32c .. 32c + 31, scaled by a
     // power of two to a maximum in [1, 2) so that f16 holds it
@@ -370,26 +413,26 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
     float hf[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float x[32];
+      float y[32];
       const int h = t * 8 + g;
       if (h < heads) {
-        const __nv_bfloat16* src = a.Q + b * a.ldq + (head0 + h) * 128 + c * 32;
+        const __nv_bfloat16* src = a.Q + x.b * a.ldq + (head0 + h) * 128 + c * 32;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_bf16x8(src + 8 * i, x + 8 * i);
+        for (int i = 0; i < 4; ++i) load_bf16x8(src + 8 * i, y + 8 * i);
       } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        for (int i = 0; i < 32; ++i) y[i] = 0.f;
       }
       float mx = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
+      for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fabsf(y[i]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
       e = mx == 0.f ? 0 : max(-126, min(126, e));
       const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) q[t][i] = pack_f16(x[2 * i] * down, x[2 * i + 1] * down);
+      for (int i = 0; i < 16; ++i) q[t][i] = pack_f16(y[2 * i] * down, y[2 * i + 1] * down);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
       hf[t][0] = __shfl_sync(0xffffffffu, up, (2 * c) * 4);
       hf[t][1] = __shfl_sync(0xffffffffu, up, (2 * c + 1) * 4);
@@ -400,7 +443,7 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[t][k] = -INFINITY;
+        m[t][k] = 0.f;
         l[t][k] = 0.f;
         f[t][k] = 0.f;
       }
@@ -409,257 +452,284 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 3) attn_decode_kernel(const De
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
     }
+    bool fresh = true, unset = true;  // no key yet (m is a placeholder); a head without units of O (f = 0)
 
-    // this warp's tiles: key0 + 32 * (warp + 4 i)
-    const int tiles = (key1 - key0 + DEC_TILE - 1) / DEC_TILE;
-    const int count = tiles > warp ? (tiles - warp + DEC_WARPS - 1) / DEC_WARPS : 0;
-    uint32_t have = 0;  // two bits per stage
-    auto fetch = [&](int i) {
-      if (i < count) {
-        const uint32_t s = i % DEC_STAGES;
-        const uint32_t h = decode_fetch(a, table, kvh, key0 + DEC_TILE * (warp + DEC_WARPS * i), key1,
-                                        ring_u + s * DEC_STAGE_BYTES);
-        have = (have & ~(3u << (2 * s))) | (h << (2 * s));
+    for (; x.u < x.stop; ++x.u, ++it) {
+      const uint32_t s = it % DEC_STAGES;
+      ok = ok && mbar_wait_bounded(&full[s], (it / DEC_STAGES) & 1, abort_flag, a.status, 2000000000ull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {  // the status word tells; the warp still meets the others at the merges
+        x.u = x.stop;
+        break;
       }
-      cp_commit();
-    };
+      const uint32_t so = s * DEC_STAGE_BYTES;
+      const uint32_t on = (pages_in[s] >> (2 * warp)) & 3u;
+      const int left = x.len - (x.u - x.first) * DEC_UNIT - 32 * warp;  // of the warp's 32 keys
+      if (left > 0 && on) {
+        const bool whole = on == 3u && left >= 32;
+        // S^T: z = s * scale * log2(e); the two groups of 16 keys side by side
+        // (each a chain of eight dependent products)
+        float z[NT][2][4];
+        uint4 w0[2], w1[2];
+        uint32_t f0[2], f1[2];
 #pragma unroll
-    for (int i = 0; i < DEC_STAGES - 1; ++i) fetch(i);
-    for (int i = 0; i < count; ++i) {
-      fetch(i + DEC_STAGES - 1);
-      cp_wait<DEC_STAGES - 1>();
-      __syncwarp();
-      const int s = i % DEC_STAGES;
-      const uint8_t* st = ring + s * DEC_STAGE_BYTES;
-      const int key = key0 + DEC_TILE * (warp + DEC_WARPS * i);
-      const uint32_t on = (have >> (2 * s)) & 3u;
-      const int left = key1 - key;  // keys of the tile that exist
-      const bool whole = on == 3u && left >= DEC_TILE;
-      const int pi = (g >> 1) + (g & 1) * 4;  // key of fragment row g; row g + 8 is 8 keys on
-
-      // S^T and the weights
-      float z[NT][2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) z[t][h][k] = 0.f;
-        const uint8_t* kp = st + ST_K + (16 * h + pi) * 64 + c * 16;
-        const uint4 w0 = *reinterpret_cast<const uint4*>(kp), w1 = *reinterpret_cast<const uint4*>(kp + 512);
-        const uint32_t f0 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(st + ST_SFK + (16 * h + pi) * 8 + 2 * c));
-        const uint32_t f1 = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(st + ST_SFK + (16 * h + pi + 8) * 8 + 2 * c));
-        // both halves of the scale register: block 2c for the first 16 elements, 2c + 1 for the others
-        const uint32_t g00 = __byte_perm(f0, f0, 0x1010), g01 = __byte_perm(f0, f0, 0x3232);
-        const uint32_t g10 = __byte_perm(f1, f1, 0x1010), g11 = __byte_perm(f1, f1, 0x3232);
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          uint32_t x[4], y[4];
-          e2m1x8_f16(k == 0 ? w0.x : k == 2 ? w0.y : k == 4 ? w0.z : w0.w, x);
-          e2m1x8_f16(k == 0 ? w1.x : k == 2 ? w1.y : k == 4 ? w1.z : w1.w, y);
-          const uint32_t g0 = k < 4 ? g00 : g01, g1 = k < 4 ? g10 : g11;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a0 = hmul2(x[2 * i], g0), a1 = hmul2(y[2 * i], g1);
-            const uint32_t a2 = hmul2(x[2 * i + 1], g0), a3 = hmul2(y[2 * i + 1], g1);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(z[t][h], a0, a1, a2, a3, q[t][2 * (k + i)], q[t][2 * (k + i) + 1]);
-          }
-        }
-        const float* rk = reinterpret_cast<const float*>(st + ST_RSK) + 16 * h + pi;
-        const float r0 = rk[0], r1 = rk[8];
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) z[t][h][k] = z[t][h][k] * (k < 2 ? r0 : r1) * hf[t][k & 1];
-        if (!whole) {
-          const bool in0 = ((on >> h) & 1) && 16 * h + pi < left, in1 = ((on >> h) & 1) && 16 * h + pi + 8 < left;
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) z[t][h][k] = (k < 2 ? in0 : in1) ? z[t][h][k] : -INFINITY;
+            for (int k = 0; k < 4; ++k) z[t][h][k] = 0.f;
+          w0[h] = *reinterpret_cast<const uint4*>(k_at + so + h * 1024);
+          w1[h] = *reinterpret_cast<const uint4*>(k_at + so + h * 1024 + 512);
+          f0[h] = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(sfk_at + so + h * 128));
+          f1[h] = e4m3x2_f16(*reinterpret_cast<const uint16_t*>(sfk_at + so + h * 128 + 64));
         }
-      }
-      // raise the reference maximum when a score lies more than 2^8 above it
-      float top[NT][2];
-      bool up = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int k = 0; k < 8; k += 2) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          top[t][k] = fmaxf(fmaxf(z[t][0][k], z[t][0][k + 2]), fmaxf(z[t][1][k], z[t][1][k + 2]));
-          up |= top[t][k] > m[t][k] + 8.f;
-        }
-      if (__any_sync(0xffffffffu, up)) {
+          for (int h = 0; h < 2; ++h) {
+            uint32_t xa[4], ya[4];
+            e2m1x8_f16(k == 0 ? w0[h].x : k == 2 ? w0[h].y : k == 4 ? w0[h].z : w0[h].w, xa);
+            e2m1x8_f16(k == 0 ? w1[h].x : k == 2 ? w1[h].y : k == 4 ? w1[h].z : w1[h].w, ya);
+            // both halves of the scale register: block 2c for the first 16 elements, 2c + 1 for the others
+            const uint32_t g0 = __byte_perm(f0[h], f0[h], k < 4 ? 0x1010 : 0x3232);
+            const uint32_t g1 = __byte_perm(f1[h], f1[h], k < 4 ? 0x1010 : 0x3232);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a0 = hmul2(xa[2 * i], g0), a1 = hmul2(ya[2 * i], g1);
+              const uint32_t a2 = hmul2(xa[2 * i + 1], g0), a3 = hmul2(ya[2 * i + 1], g1);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x = top[t][k];
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            if (x > m[t][k]) {
-              const float by = x - m[t][k];
-              l[t][k] *= exp2_sfu(-by);   // m = -inf: l is 0 and stays 0
-              // O is in units of f * 2^m and keeps its value
-              f[t][k] = f[t][k] == 0.f ? 0.f : fminf(f[t][k] * exp2_sfu(by), 3e38f);
-              m[t][k] = x;
+              for (int t = 0; t < NT; ++t) mma_f16(z[t][h], a0, a1, a2, a3, q[t][2 * (k + i)], q[t][2 * (k + i) + 1]);
             }
           }
-      }
-      const float* rv = reinterpret_cast<const float*>(st + ST_RSV);
-      float big[NT][2];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) big[t][0] = big[t][1] = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float r0 = rv[16 * h + pi], r1 = rv[16 * h + pi + 8];
-        if (!whole) {
-          r0 = ((on >> h) & 1) && 16 * h + pi < left ? r0 : 0.f;
-          r1 = ((on >> h) & 1) && 16 * h + pi + 8 < left ? r1 : 0.f;
         }
+        // z = s * scale * log2(e) - m, the exponent of the weight
+        float rv[4], top[NT][2];
+        bool up = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int h = 0; h < 2; ++h) {
+          const float r0 = *reinterpret_cast<const float*>(rsk_at + so + h * 64);
+          const float r1 = *reinterpret_cast<const float*>(rsk_at + so + h * 64 + 32);
+          rv[2 * h] = *reinterpret_cast<const float*>(rsv_at + so + h * 64);
+          rv[2 * h + 1] = *reinterpret_cast<const float*>(rsv_at + so + h * 64 + 32);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float mm = m[t][k & 1];
-            const float e = exp2_sfu(z[t][h][k] - (mm == -INFINITY ? 0.f : mm));
-            l[t][k & 1] += e;
-            z[t][h][k] = e * (k < 2 ? r0 : r1);
-            big[t][k & 1] = fmaxf(big[t][k & 1], z[t][h][k]);
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[t][h][k] = fmaf(z[t][h][k] * (k < 2 ? r0 : r1), hf[t][k & 1], -m[t][k & 1]);
+          if (!whole) {
+            const bool in0 = ((on >> h) & 1) && 16 * h + pi < left, in1 = ((on >> h) & 1) && 16 * h + pi + 8 < left;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) z[t][h][k] = (k < 2 ? in0 : in1) ? z[t][h][k] : -INFINITY;
+            rv[2 * h] = in0 ? rv[2 * h] : 0.f;
+            rv[2 * h + 1] = in1 ? rv[2 * h + 1] : 0.f;
           }
-      }
-      up = false;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) up |= big[t][k] * f[t][k] > 256.f || (f[t][k] == 0.f && big[t][k] > 0.f);
-      if (__any_sync(0xffffffffu, up)) {
+        }
+        // raise m when a weight passes 2^8 of it
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float x = big[t][k];
+            top[t][k] = fmaxf(fmaxf(z[t][0][k], z[t][0][k + 2]), fmaxf(z[t][1][k], z[t][1][k + 2]));
+            up |= top[t][k] > 8.f;
+          }
+        up |= fresh;
+        if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            if (x * f[t][k] > 1.f || (f[t][k] == 0.f && x > 0.f)) {
-              const float nf = fminf(1.f / x, 3e38f);
-              const float by = f[t][k] == 0.f ? 0.f : nf / f[t][k];
-              f[t][k] = nf;
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                o[t][i][k] *= by;
-                o[t][i][k + 2] *= by;
+            for (int k = 0; k < 2; ++k) {
+              float y = top[t][k];
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+              if ((fresh && y > -INFINITY) || y > 0.f) {
+                l[t][k] = fresh ? 0.f : l[t][k] * exp2_sfu(-y);
+                // O is in units of f * 2^m and keeps its value
+                f[t][k] = f[t][k] == 0.f ? 0.f : fminf(f[t][k] * exp2_sfu(y), 3e38f);
+                m[t][k] += y;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  z[t][h][k] -= y;
+                  z[t][h][k + 2] -= y;
+                }
               }
             }
+        }
+        // the weights, times the row scales of V, in units of O
+        float pf[NT][2][4], big = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float e = exp2_sfu(z[t][h][k]);
+              l[t][k & 1] += e;
+              z[t][h][k] = e * rv[2 * h + (k >> 1)];
+              pf[t][h][k] = z[t][h][k] * f[t][k & 1];
+              big = fmaxf(big, pf[t][h][k]);
+            }
+        // new units when P' would pass 2^14, or a head has none yet
+        if (__any_sync(0xffffffffu, unset || big > 16384.f)) {
+          unset = false;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float y = fmaxf(fmaxf(z[t][0][k], z[t][0][k + 2]), fmaxf(z[t][1][k], z[t][1][k + 2]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+              if (y * f[t][k] > 1.f || (f[t][k] == 0.f && y > 0.f)) {
+                const float nf = fminf(1.f / y, 3e38f);
+                const float by = f[t][k] == 0.f ? 0.f : nf / f[t][k];
+                f[t][k] = nf;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  o[t][i][k] *= by;
+                  o[t][i][k + 2] *= by;
+                }
+              }
+              unset |= f[t][k] == 0.f;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                pf[t][h][k] = z[t][h][k] * f[t][k];
+                pf[t][h][k + 2] = z[t][h][k + 2] * f[t][k];
+              }
+            }
+        }
+        fresh = false;
+        // O^T += V'^T P'^T
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            p[t][0] = movmatrix_t(pack_f16(pf[t][h][0], pf[t][h][1]));
+            p[t][1] = movmatrix_t(pack_f16(pf[t][h][2], pf[t][h][3]));
           }
-      }
-      // O^T += V'^T P'^T
+          // keys c, c + 4, c + 8, c + 12; elements 16 g .. 16 g + 15: one block
+          uint2 w[4];
+          uint32_t sf[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[NT][2];
+          for (int y = 0; y < 4; ++y) {
+            w[y] = *reinterpret_cast<const uint2*>(v_at + so + h * 1024 + y * 256);
+            sf[y] = sfv_at[so + h * 128 + y * 32];
+          }
+          if (!whole) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          p[t][0] = movmatrix_t(pack_f16(z[t][h][0] * f[t][0], z[t][h][1] * f[t][1]));
-          p[t][1] = movmatrix_t(pack_f16(z[t][h][2] * f[t][0], z[t][h][3] * f[t][1]));
-        }
-        // keys c, c + 4, c + 8, c + 12; elements 16 g .. 16 g + 15: one block
-        uint2 w[4];
-        uint32_t sf[4];
+            for (int y = 0; y < 4; ++y)  // an unwritten row's scale may be NaN
+              if (!(((on >> h) & 1) && 16 * h + c + 4 * y < left)) sf[y] = 0;
+          }
+          const uint32_t g0 = e4m3x2_f16(sf[0] | (sf[1] << 8)), g1 = e4m3x2_f16(sf[2] | (sf[3] << 8));
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int kk = 16 * h + c + 4 * x;
-          w[x] = *reinterpret_cast<const uint2*>(st + ST_V + kk * 64 + g * 8);
-          sf[x] = st[ST_SFV + kk * 8 + g];
-          if (!whole && !(((on >> h) & 1) && kk < left)) sf[x] = 0;  // an unwritten row's scale may be NaN
-        }
-        const uint32_t g0 = e4m3x2_f16(sf[0] | (sf[1] << 8)), g1 = e4m3x2_f16(sf[2] | (sf[3] << 8));
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t x0 = half ? w[0].y : w[0].x, x1 = half ? w[1].y : w[1].x;
+            const uint32_t x2 = half ? w[2].y : w[2].x, x3 = half ? w[3].y : w[3].x;
+            // the same element of two keys in one byte: even elements, odd elements
+            uint32_t e0[4], o0[4], e1[4], o1[4];
+            e2m1x8_f16((x0 & 0x0F0F0F0Fu) | ((x1 << 4) & 0xF0F0F0F0u), e0);
+            e2m1x8_f16(((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u), o0);
+            e2m1x8_f16((x2 & 0x0F0F0F0Fu) | ((x3 << 4) & 0xF0F0F0F0u), e1);
+            e2m1x8_f16(((x2 >> 4) & 0x0F0F0F0Fu) | (x3 & 0xF0F0F0F0u), o1);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t x0 = half ? w[0].y : w[0].x, x1 = half ? w[1].y : w[1].x;
-          const uint32_t x2 = half ? w[2].y : w[2].x, x3 = half ? w[3].y : w[3].x;
-          // the same element of two keys in one byte: even elements, odd elements
-          const uint32_t ev0 = (x0 & 0x0F0F0F0Fu) | ((x1 << 4) & 0xF0F0F0F0u);
-          const uint32_t od0 = ((x0 >> 4) & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u);
-          const uint32_t ev1 = (x2 & 0x0F0F0F0Fu) | ((x3 << 4) & 0xF0F0F0F0u);
-          const uint32_t od1 = ((x2 >> 4) & 0x0F0F0F0Fu) | (x3 & 0xF0F0F0F0u);
-          uint32_t e0[4], o0[4], e1[4], o1[4];
-          e2m1x8_f16(ev0, e0);
-          e2m1x8_f16(od0, o0);
-          e2m1x8_f16(ev1, e1);
-          e2m1x8_f16(od1, o1);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a0 = hmul2(e0[j], g0), a1 = hmul2(o0[j], g0), a2 = hmul2(e1[j], g1), a3 = hmul2(o1[j], g1);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = hmul2(e0[j], g0), a1 = hmul2(o0[j], g0), a2 = hmul2(e1[j], g1), a3 = hmul2(o1[j], g1);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) mma_f16(o[t][half * 4 + j], a0, a1, a2, a3, p[t][0], p[t][1]);
+              for (int t = 0; t < NT; ++t) mma_f16(o[t][half * 4 + j], a0, a1, a2, a3, p[t][0], p[t][1]);
+            }
           }
         }
       }
-      __syncwarp();  // the stage may be refilled
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
     }
-    cp_wait<0>();
-    __syncthreads();
 
-    // merge the warps: row w * 16 + head of 132 floats (128 outputs, m, l, f)
-    float* mg = reinterpret_cast<float*>(dec_smem);
+    // merge the four warps, pairs first: the fragments lie alike, so a lane
+    // adds what the same lane of the other warp left
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float x = l[t][k];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        float* row = mg + (warp * DEC_HEADS + t * 8 + 2 * c + k) * 132;
+        for (int d = 4; d < 32; d <<= 1) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
+        if (l[t][k] == 0.f) m[t][k] = -INFINITY;  // no key
+        // O in units of 2^m
+        const float by = f[t][k] > 0.f ? 1.f / f[t][k] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<float2*>(row + 16 * g + 2 * i) = make_float2(o[t][i][k], o[t][i][k + 2]);
-        if (g == 0) {
-          row[128] = m[t][k];
-          row[129] = x;
-          row[130] = f[t][k];
+        for (int i = 0; i < 8; ++i) {
+          o[t][i][k] = f[t][k] > 0.f ? o[t][i][k] * by : o[t][i][k];
+          o[t][i][k + 2] = f[t][k] > 0.f ? o[t][i][k + 2] * by : o[t][i][k + 2];
         }
       }
-    __syncthreads();
-    const bool alone = u == h_first && stop == h_first + nu;
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (u == first ? 0 : 1);
-    for (int h = warp; h < heads; h += DEC_WARPS) {
-      float M = -INFINITY;
+#pragma unroll 1
+    for (int pair = DEC_WARPS / 2; pair >= 1; pair >>= 1) {
+      float4* box = reinterpret_cast<float4*>(merge + (warp % pair) * NT * (1024 + 64));
+      if (warp >= pair && warp < 2 * pair) {
 #pragma unroll
-      for (int w = 0; w < DEC_WARPS; ++w) M = fmaxf(M, mg[(w * DEC_HEADS + h) * 132 + 128]);
-      const float M0 = M == -INFINITY ? 0.f : M;
-      float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int w = 0; w < DEC_WARPS; ++w) {
-        const float* row = mg + (w * DEC_HEADS + h) * 132;
-        const float e = exp2_sfu(row[128] - M0);
-        L += row[129] * e;
-        const float by = row[130] > 0.f ? e / row[130] : 0.f;
-        const float4 v = *reinterpret_cast<const float4*>(row + lane * 4);
-        if (row[130] != 0.f) {
-          acc[0] += v.x * by;
-          acc[1] += v.y * by;
-          acc[2] += v.z * by;
-          acc[3] += v.w * by;
+          for (int i = 0; i < 8; ++i) box[(t * 8 + i) * 32 + lane] = make_float4(o[t][i][0], o[t][i][1], o[t][i][2], o[t][i][3]);
+          if (g == 0) box[NT * 256 + t * 4 + c] = make_float4(m[t][0], m[t][1], l[t][0], l[t][1]);
         }
       }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      asm volatile("bar.sync 1, %0;" ::"n"(DEC_WARPS * 32) : "memory");
+      if (warp < pair) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] *= inv;
-      if (alone) {
-        uint2 v;
-        v.x = pack_bf16x2(acc[0], acc[1]);
-        v.y = pack_bf16x2(acc[2], acc[3]);
-        *reinterpret_cast<uint2*>(a.O + (static_cast<int64_t>(b) * a.n_q + head0 + h) * 128 + lane * 4) = v;
-        if (lane == 0)
-          a.lse[static_cast<int64_t>(b) * a.n_q + head0 + h] = L == 0.f ? -INFINITY : M * 0.69314718056f + logf(L);
-      } else {
-        const int64_t at = static_cast<int64_t>(slot) * a.part_heads + h;
-        *reinterpret_cast<float4*>(a.part + at * 128 + lane * 4) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        if (lane == 0) a.part_lse[at] = L == 0.f ? -INFINITY : M + log2f(L);
+        for (int t = 0; t < NT; ++t) {
+          const float4 st = box[NT * 256 + t * 4 + c];
+          float by[2], of[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float om = k ? st.y : st.x, ol = k ? st.w : st.z;
+            const float M = fmaxf(m[t][k], om), M0 = fmaxf(M, -3e38f);
+            by[k] = exp2_sfu(m[t][k] - M0);
+            of[k] = exp2_sfu(om - M0);
+            l[t][k] = l[t][k] * by[k] + ol * of[k];
+            m[t][k] = M;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 v = box[(t * 8 + i) * 32 + lane];
+            o[t][i][0] = o[t][i][0] * by[0] + v.x * of[0];
+            o[t][i][1] = o[t][i][1] * by[1] + v.y * of[1];
+            o[t][i][2] = o[t][i][2] * by[0] + v.z * of[0];
+            o[t][i][3] = o[t][i][3] * by[1] + v.w * of[1];
+          }
+        }
       }
+      asm volatile("bar.sync 1, %0;" ::"n"(DEC_WARPS * 32) : "memory");
     }
-    __syncthreads();  // the merge buffer is the next stretch's ring
-    u = stop;
+    if (warp == 0) {
+      const bool alone = u0 == x.first && x.stop == x.first + x.nu;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == first ? 0 : 1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int h = t * 8 + 2 * c + k;
+          if (h >= heads) continue;
+          const float inv = l[t][k] == 0.f ? 0.f : 1.f / l[t][k];
+          float v[16];  // elements 16 g .. 16 g + 15
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[2 * i] = o[t][i][k] * inv;
+            v[2 * i + 1] = o[t][i][k + 2] * inv;
+          }
+          if (alone) {
+            const int64_t at = static_cast<int64_t>(x.b) * a.n_q + head0 + h;
+            store_bf16x8(a.O + at * 128 + 16 * g, v);
+            store_bf16x8(a.O + at * 128 + 16 * g + 8, v + 8);
+            if (g == 0) a.lse[at] = l[t][k] == 0.f ? -INFINITY : m[t][k] * 0.69314718056f + logf(l[t][k]);
+          } else {
+            const int64_t at = static_cast<int64_t>(slot) * a.part_heads + h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(a.part + at * 128 + 16 * g + 4 * i) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (g == 0) a.part_lse[at] = l[t][k] == 0.f ? -INFINITY : m[t][k] + log2f(l[t][k]);
+          }
+        }
+    }
   }
 }
 
@@ -743,14 +813,15 @@ cudaError_t launch_kv_read(const KvCache& c, const int32_t* slots, int64_t T, vo
 }
 
 cudaError_t launch_attn_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(std::min(DEC_MAX_CTAS, 3 * sms));
+  const unsigned ctas = a.part_heads <= 8 ? 3 : 2;  // per SM: registers
+  const unsigned grid = std::min<unsigned>(DEC_MAX_CTAS, ctas * static_cast<unsigned>(sms));
   cudaError_t e;
   if (a.part_heads <= 8) {
-    e = attn_smem_attribute(reinterpret_cast<const void*>(attn_decode_kernel<1>), 1, DEC_SMEM);
-    if (e == cudaSuccess) e = launch(attn_decode_kernel<1>, grid, DEC_WARPS * 32, DEC_SMEM, s, a);
+    e = attn_smem_attribute(reinterpret_cast<const void*>(attn_decode_kernel<1>), 1, dec_smem_bytes(1));
+    if (e == cudaSuccess) e = launch(attn_decode_kernel<1>, grid, DEC_THREADS, dec_smem_bytes(1), s, a);
   } else {
-    e = attn_smem_attribute(reinterpret_cast<const void*>(attn_decode_kernel<2>), 2, DEC_SMEM);
-    if (e == cudaSuccess) e = launch(attn_decode_kernel<2>, grid, DEC_WARPS * 32, DEC_SMEM, s, a);
+    e = attn_smem_attribute(reinterpret_cast<const void*>(attn_decode_kernel<2>), 2, dec_smem_bytes(2));
+    if (e == cudaSuccess) e = launch(attn_decode_kernel<2>, grid, DEC_THREADS, dec_smem_bytes(2), s, a);
   }
   if (e != cudaSuccess) return e;
   return launch(attn_decode_join_kernel, static_cast<unsigned>((static_cast<int64_t>(a.B) * a.n_q + 7) / 8), 256, 0, s,
