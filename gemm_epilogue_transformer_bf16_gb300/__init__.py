@@ -906,68 +906,114 @@ def linear_cross_entropy_bwd(X, W, labels, lse, n_valid, dloss=1.0, ignore_index
 # attention
 # ---------------------------------------------------------------------------
 
-def _strided(t, width, name):
+# These calls are short next to their checks, so each argument is looked at
+# once: _arg and _strided test type, device, dtype and layout together.
+
+def _where(t, dev, name):
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name}: must be a CUDA tensor (no CPU path)")
+    raise ValueError(f"{name}: tensor on cuda:{at}, but the current device is cuda:{dev}")
+
+
+def _device(t, name):
+    """The current device, on which the calls launch: every tensor must live
+    there.  `t` is the call's first operand (a host tensor ends here)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.get_device() < 0:
+        _where(t, -1, name)
+    return torch.cuda.current_device()
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Pointer of a contiguous operand of `dtype` and `shape` (None: any) on
+    device `dev`; None passes through."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.get_device() != dev:
+        _where(t, dev, name)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _strided(t, width, dev, name):
     """Pointer, row stride and rows of a bf16 [rows, width] operand whose rows
     may lie apart (columns of a wider projection output)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor (no CPU path)")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != dev:
+        _where(t, dev, name)
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name}: expected [rows, {width}], got {tuple(t.shape)}")
-    if t.shape[0] > 1 and t.stride(0) < width or t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name}: expected [rows, {width}], got {tuple(shape)}")
+    rows = shape[0]
+    ld, one = t.stride()
+    if rows < 2:
+        ld = width
+    if one != 1 or ld < width:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap")
-    return t.data_ptr(), max(t.stride(0), width) if t.shape[0] > 1 else width, t.shape[0]
+    return t.data_ptr(), ld, rows
 
 
-def _same_device(*tensors):
-    """The calls launch on the current device: every tensor must live there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+def _new(shape, dtype, dev, stream):
+    """An output for a call on `stream`: allocated there when it is given, so
+    that the allocator knows which stream uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _expect(t, shape, name):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+def _scratch(ws, need, dev, stream):
+    """Pointer and size of the caller's workspace, or of a zeroed one made on
+    the call's stream (returned too: it must outlive the launch)."""
+    if ws is None:
+        if stream is None:
+            ws = workspace(need, dev)
+        else:
+            with torch.cuda.stream(stream):
+                ws = workspace(need, dev)
+    elif ws.get_device() != dev:
+        _where(ws, dev, "ws")
+    n = ws.numel()
+    if n < need:
+        raise ValueError(f"workspace too small: {n} < {need}")
+    return ws.data_ptr(), n, ws
 
 
-class _on:
-    """Allocates inside on `stream` when one is given, so that the allocator
-    and the workspace's clearing follow the stream that uses them."""
-
-    def __init__(self, stream):
-        self._ctx = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        return self._ctx.__enter__() if self._ctx else None
-
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc) if self._ctx else None
+def _on_stream(stream, dev):
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim):
-    q, ldq, Tq = _strided(Q, n_q * head_dim, "Q")
-    k, ldk, Tk = _strided(K, n_kv * head_dim, "K")
-    v, ldv, Tv = _strided(V, n_kv * head_dim, "V")
+def _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim, dev):
+    q, ldq, Tq = _strided(Q, n_q * head_dim, dev, "Q")
+    k, ldk, Tk = _strided(K, n_kv * head_dim, dev, "K")
+    v, ldv, Tv = _strided(V, n_kv * head_dim, dev, "V")
     if Tv != Tk:
         raise ValueError(f"K has {Tk} rows, V {Tv}")
-    cu = _i32(cu_seqlens, "cu_seqlens")
-    cuk = _i32(cu_seqlens_k, "cu_seqlens_k")
+    cu = _arg(cu_seqlens, torch.int32, None, dev, "cu_seqlens")
     n_seq = cu_seqlens.numel() - 1
     if n_seq < 0:
         raise ValueError("cu_seqlens: expected n_seq + 1 offsets")
-    if cuk is None and Tk != Tq:
+    cuk = None
+    if cu_seqlens_k is not None:
+        cuk = _arg(cu_seqlens_k, torch.int32, None, dev, "cu_seqlens_k")
+        if cu_seqlens_k.numel() != n_seq + 1:
+            raise ValueError("cu_seqlens_k: expected as many offsets as cu_seqlens")
+    elif Tk != Tq:
         raise ValueError(f"Q has {Tq} rows, K {Tk}: give cu_seqlens_k")
-    if cuk is not None and cu_seqlens_k.numel() != n_seq + 1:
-        raise ValueError("cu_seqlens_k: expected as many offsets as cu_seqlens")
-    _same_device(Q, K, V, cu_seqlens, cu_seqlens_k)
-    return (q, ldq, k, ldk, v, ldv, cu, cuk, n_seq, n_q, n_kv, head_dim,
-            float(head_dim ** -0.5 if scale is None else scale)), Tq, Tk, n_seq
+    return (q, ldq, k, ldk, v, ldv), (cu, cuk, n_seq, n_q, n_kv, head_dim,
+                                      head_dim ** -0.5 if scale is None else float(scale)), Tq, Tk, n_seq
 
 
 def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, head_dim=128, out=None, ws=None,
@@ -980,17 +1026,15 @@ def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, hea
     [Tq, n_q*128] and lse [n_q, Tq]; rows outside every sequence stay as they
     are (undefined in tensors allocated here)."""
     lib = load()
-    args, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim)
-    dev = Q.device
-    with _on(stream):
-        if out is None:
-            out = {"O": torch.empty(Tq, n_q * head_dim, dtype=torch.bfloat16, device=dev),
-                   "lse": torch.empty(n_q, Tq, dtype=torch.float32, device=dev)}
-        ws = _ws(ws, lib.coda_attention_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev)
-    O, lse = _expect(out["O"], (Tq, n_q * head_dim), "O"), _expect(out["lse"], (n_q, Tq), "lse")
-    _same_device(O, lse, ws)
-    _check("coda_attention", lib.coda_attention(*args, _bf(O, "O"), _f32(lse, "lse"), Tq, Tk, _ptr(ws), ws.numel(),
-                                                _stream(stream)))
+    dev = _device(Q, "Q")
+    qkv, rest, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim, dev)
+    if out is None:
+        out = {"O": _new((Tq, n_q * head_dim), torch.bfloat16, dev, stream),
+               "lse": _new((n_q, Tq), torch.float32, dev, stream)}
+    O = _arg(out["O"], torch.bfloat16, (Tq, n_q * head_dim), dev, "O")
+    lse = _arg(out["lse"], torch.float32, (n_q, Tq), dev, "lse")
+    w, nw, ws = _scratch(ws, lib.coda_attention_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
+    _check("coda_attention", lib.coda_attention(*qkv, *rest, O, lse, Tq, Tk, w, nw, _on_stream(stream, dev)))
     return out
 
 
@@ -1001,22 +1045,17 @@ def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None,
     them.  Rows outside every sequence stay as they are (undefined in tensors
     allocated here)."""
     lib = load()
-    args, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim)
-    wq, wk = n_q * head_dim, n_kv * head_dim
-    dev = Q.device
-    with _on(stream):
-        if out is None:
-            out = {"dQ": torch.empty(Tq, wq, dtype=torch.bfloat16, device=dev),
-                   "dK": torch.empty(Tk, wk, dtype=torch.bfloat16, device=dev),
-                   "dV": torch.empty(Tk, wk, dtype=torch.bfloat16, device=dev)}
-        ws = _ws(ws, lib.coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev)
-    for t, shape, name in ((dO, (Tq, wq), "dO"), (O, (Tq, wq), "O"), (lse, (n_q, Tq), "lse"),
-                           (out["dQ"], (Tq, wq), "dQ"), (out["dK"], (Tk, wk), "dK"), (out["dV"], (Tk, wk), "dV")):
-        _expect(t, shape, name)
-    _same_device(dO, O, lse, out["dQ"], out["dK"], out["dV"], ws)
-    _check("coda_attention_bwd", lib.coda_attention_bwd(
-        _bf(dO, "dO"), *args[:6], _bf(O, "O"), _f32(lse, "lse"), *args[6:], _bf(out["dQ"], "dQ"), _bf(out["dK"], "dK"),
-        _bf(out["dV"], "dV"), Tq, Tk, _ptr(ws), ws.numel(), _stream(stream)))
+    dev = _device(Q, "Q")
+    qkv, rest, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim, dev)
+    sq, sk = (Tq, n_q * head_dim), (Tk, n_kv * head_dim)
+    bf = torch.bfloat16
+    if out is None:
+        out = {"dQ": _new(sq, bf, dev, stream), "dK": _new(sk, bf, dev, stream), "dV": _new(sk, bf, dev, stream)}
+    saved = (_arg(O, bf, sq, dev, "O"), _arg(lse, torch.float32, (n_q, Tq), dev, "lse"))
+    grads = (_arg(out["dQ"], bf, sq, dev, "dQ"), _arg(out["dK"], bf, sk, dev, "dK"), _arg(out["dV"], bf, sk, dev, "dV"))
+    w, nw, ws = _scratch(ws, lib.coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
+    _check("coda_attention_bwd", lib.coda_attention_bwd(_arg(dO, bf, sq, dev, "dO"), *qkv, *saved, *rest, *grads, Tq, Tk,
+                                                        w, nw, _on_stream(stream, dev)))
     return out
 
 
@@ -1029,32 +1068,32 @@ def kv_cache_nvfp4(num_pages, page_size, n_kv, head_dim=128, device="cuda"):
             "scale": z(num_pages, 2, n_kv, page_size, dtype=torch.float32, device=device)}
 
 
-def _cache_args(cache):
+def _cache_args(cache, dev):
     codes, sf, scale = cache["codes"], cache["sf"], cache["scale"]
-    if scale.dim() != 4 or scale.shape[1] != 2:
+    shape = scale.shape
+    if len(shape) != 4 or shape[1] != 2:
         raise ValueError("cache: expected scale [num_pages, 2, n_kv, page_size]")
-    pages, _, n_kv, page = scale.shape
+    pages, _, n_kv, page = shape
     d = 2 * codes.shape[-1]
-    _expect(codes, (pages, 2, n_kv, page, d // 2), "cache codes")
-    _expect(sf, (pages, 2, n_kv, page, d // 16), "cache sf")
-    return (_u8(codes, "cache codes"), _u8(sf, "cache sf"), _f32(scale, "cache scale"), pages, page), n_kv, d
+    return (_arg(codes, torch.uint8, (pages, 2, n_kv, page, d // 2), dev, "cache codes"),
+            _arg(sf, torch.uint8, (pages, 2, n_kv, page, d // 16), dev, "cache sf"),
+            _arg(scale, torch.float32, None, dev, "cache scale"), pages, page), n_kv, d
 
 
 def kv_append_nvfp4(K, V, slots, cache, ws=None, stream=None):
     """Quantise the rows of K, V [T, n_kv*128] (rows may be columns of a wider
     tensor) into their cache slots [T] int32 (coda_kv_append_nvfp4; a negative
     slot skips its token, the slots of one call must differ)."""
-    c, n_kv, d = _cache_args(cache)
-    k, ldk, T = _strided(K, n_kv * d, "K")
-    v, ldv, Tv = _strided(V, n_kv * d, "V")
+    dev = _device(K, "K")
+    c, n_kv, d = _cache_args(cache, dev)
+    k, ldk, T = _strided(K, n_kv * d, dev, "K")
+    v, ldv, Tv = _strided(V, n_kv * d, dev, "V")
     if Tv != T:
         raise ValueError(f"K has {T} rows, V {Tv}")
-    _expect(slots, (T,), "slots")
-    _same_device(K, V, slots, cache["codes"], cache["sf"], cache["scale"], ws)
-    with _on(stream):
-        ws = _ws(ws, 256, K.device)
-    _check("coda_kv_append_nvfp4", load().coda_kv_append_nvfp4(
-        k, ldk, v, ldv, _i32(slots, "slots"), T, *c, n_kv, d, _ptr(ws), ws.numel(), _stream(stream)))
+    at = _arg(slots, torch.int32, (T,), dev, "slots")
+    w, nw, ws = _scratch(ws, 256, dev, stream)
+    _check("coda_kv_append_nvfp4", load().coda_kv_append_nvfp4(k, ldk, v, ldv, at, T, *c, n_kv, d, w, nw,
+                                                               _on_stream(stream, dev)))
     return cache
 
 
@@ -1064,19 +1103,17 @@ def kv_read_nvfp4(cache, slots, dtype=torch.bfloat16, out=None, ws=None, stream=
     zeros)."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"kv_read_nvfp4: dtype must be torch.bfloat16 or torch.float32, not {dtype}")
-    c, n_kv, d = _cache_args(cache)
+    dev = _device(cache["scale"], "cache scale")
+    c, n_kv, d = _cache_args(cache, dev)
+    at = _arg(slots, torch.int32, None, dev, "slots")
     T = slots.numel()
-    dev = cache["scale"].device
-    with _on(stream):
-        if out is None:
-            out = {k: torch.empty(T, n_kv * d, dtype=dtype, device=dev) for k in ("K", "V")}
-        ws = _ws(ws, 256, dev)
-    K, V = (_expect(out[k], (T, n_kv * d), k) for k in ("K", "V"))
-    _expect(slots, (T,), "slots")
-    _same_device(slots, cache["codes"], cache["sf"], cache["scale"], K, V, ws)
+    shape = (T, n_kv * d)
+    if out is None:
+        out = {"K": _new(shape, dtype, dev, stream), "V": _new(shape, dtype, dev, stream)}
+    w, nw, ws = _scratch(ws, 256, dev, stream)
     _check("coda_kv_read_nvfp4", load().coda_kv_read_nvfp4(
-        *c, _i32(slots, "slots"), T, n_kv, d, _ptr(K, dtype, "K"), _ptr(V, dtype, "V"),
-        F32 if dtype == torch.float32 else BF16, _ptr(ws), ws.numel(), _stream(stream)))
+        *c, at, T, n_kv, d, _arg(out["K"], dtype, shape, dev, "K"), _arg(out["V"], dtype, shape, dev, "V"),
+        F32 if dtype is torch.float32 else BF16, w, nw, _on_stream(stream, dev)))
     return out
 
 
@@ -1086,21 +1123,19 @@ def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out
     [batch, max_pages] int32 names (coda_attention_decode_nvfp4).  Returns O
     [batch, n_q*128] and lse [batch, n_q]."""
     lib = load()
-    c, n_kv, d = _cache_args(cache)
-    q, ldq, batch = _strided(Q, n_q * d, "Q")
+    dev = _device(Q, "Q")
+    c, n_kv, d = _cache_args(cache, dev)
+    q, ldq, batch = _strided(Q, n_q * d, dev, "Q")
+    table = _arg(block_table, torch.int32, None, dev, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table: expected [{batch}, max_pages], got {tuple(block_table.shape)}")
-    _expect(seq_lens, (batch,), "seq_lens")
-    dev = Q.device
-    with _on(stream):
-        if out is None:
-            out = {"O": torch.empty(batch, n_q * d, dtype=torch.bfloat16, device=dev),
-                   "lse": torch.empty(batch, n_q, dtype=torch.float32, device=dev)}
-        ws = _ws(ws, lib.coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, d), dev)
-    O, lse = _expect(out["O"], (batch, n_q * d), "O"), _expect(out["lse"], (batch, n_q), "lse")
-    _same_device(Q, block_table, seq_lens, cache["codes"], cache["sf"], cache["scale"], O, lse, ws)
+    lens = _arg(seq_lens, torch.int32, (batch,), dev, "seq_lens")
+    if out is None:
+        out = {"O": _new((batch, n_q * d), torch.bfloat16, dev, stream),
+               "lse": _new((batch, n_q), torch.float32, dev, stream)}
+    w, nw, ws = _scratch(ws, lib.coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, d), dev, stream)
     _check("coda_attention_decode_nvfp4", lib.coda_attention_decode_nvfp4(
-        q, ldq, *c, _i32(block_table, "block_table"), block_table.shape[1], _i32(seq_lens, "seq_lens"), batch, n_q,
-        n_kv, d, float(d ** -0.5 if scale is None else scale), _bf(O, "O"), _f32(lse, "lse"), _ptr(ws), ws.numel(),
-        _stream(stream)))
+        q, ldq, *c, table, block_table.shape[1], lens, batch, n_q, n_kv, d, d ** -0.5 if scale is None else float(scale),
+        _arg(out["O"], torch.bfloat16, (batch, n_q * d), dev, "O"),
+        _arg(out["lse"], torch.float32, (batch, n_q), dev, "lse"), w, nw, _on_stream(stream, dev)))
     return out

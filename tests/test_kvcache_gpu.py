@@ -250,3 +250,26 @@ def test_decode_twice_gives_the_same_bits(coda):
     a = coda.attention_decode_nvfp4(Q, cache, table.to(DEV), n, 8)
     b = coda.attention_decode_nvfp4(Q, cache, table.to(DEV), n, 8)
     assert torch.equal(a["O"], b["O"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_binding_refuses_shapes(coda):
+    cache = coda.kv_cache_nvfp4(2, 16, 2)
+    slots = torch.zeros(3, dtype=torch.int32, device=DEV)
+    x = torch.zeros(3, 2 * D, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="cache sf"):
+        coda.kv_read_nvfp4(dict(cache, sf=cache["sf"][:1]), slots)
+    with pytest.raises(ValueError, match="slots"):
+        coda.kv_append_nvfp4(x, x, slots[:2], cache)
+    with pytest.raises(TypeError, match="slots"):
+        coda.kv_append_nvfp4(x, x, slots.long(), cache)
+    with pytest.raises(ValueError, match="K: expected"):
+        coda.kv_append_nvfp4(x[:, :D], x, slots, cache)
+    q = torch.zeros(3, 4 * D, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="block_table"):
+        coda.attention_decode_nvfp4(q, cache, torch.zeros(2, 2, dtype=torch.int32, device=DEV), slots, 4)
+    with pytest.raises(ValueError, match="workspace too small"):
+        coda.attention_decode_nvfp4(q, cache, torch.zeros(3, 2, dtype=torch.int32, device=DEV), slots, 4,
+                                    ws=coda.workspace(256))
+    with pytest.raises(coda.CodaError):                 # 5 query heads over 2 key/value heads
+        coda.attention_decode_nvfp4(torch.zeros(3, 5 * D, dtype=torch.bfloat16, device=DEV), cache,
+                                    torch.zeros(3, 2, dtype=torch.int32, device=DEV), slots, 5)
