@@ -53,6 +53,8 @@ struct FwdItem {
   int kv;
 };
 
+// Loading the next item's entry one item ahead was slower (prompt of 16384
+// tokens 1295 -> 1375 us): the registers it holds cost more than the latency.
 __device__ __forceinline__ FwdItem fwd_item(const AttnFwdArgs& a, int w) {
   FwdItem it;
   const int hp = 1 << a.head_shift;
@@ -124,14 +126,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
   griddep_launch_dependents();
-  const int items = *reinterpret_cast<const volatile int*>(a.counts) * (a.n_q >> (a.head_shift + a.pair_heads));
+  const int items = __ldcg(a.counts) * (a.n_q >> (a.head_shift + a.pair_heads));
   const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
   bool ok = true;
 
-  // Registers: 384 threads x 168 at launch = 256 x 216 + 128 x 72.  Each
+  // Registers: 384 threads x 168 at launch = 256 x 200 + 128 x 104.  Each
   // branch below begins with its own share, so the compiler sees it.
   if (warp >= 8) {
-  reg_dec<72>();
+  reg_dec<104>();
   if (warp == 9) {
     // ------------------------------------------------------------ producer
     const uint32_t el = elect_one();
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   }
   } else {
     // ------------------------------------------------------------ softmax
-    reg_inc<216>();
+    reg_inc<200>();
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_BINS = 2048;
+constexpr int PLAN_SMALL = 1024;  // sequences whose offsets fit in shared memory
 
 // Inclusive scan over the block (1024 threads).
 __device__ int block_scan(int v, int* warp_sums) {
@@ -39,79 +40,87 @@ __device__ int block_scan(int v, int* warp_sums) {
 }
 
 struct Side {
-  const int32_t* cu;   // lengths that are cut
+  const int32_t* cu_q;  // the offsets (shared memory when there are few sequences)
+  const int32_t* cu_k;
   int span;
-  int* prefix;
+  int* prefix;          // runs before each sequence, likewise
   AttnTile* out;
   int* count;
-  bool keys;           // the list of key runs
+  bool keys;            // the list of key runs
 };
 
+// Entry t of a list and its bin (longest first).
+__device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side& sd, int t, int shift, int& bin) {
+  int lo = 0, hi = a.n_seq;  // prefix[lo] <= t < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sd.prefix[mid] <= t) lo = mid; else hi = mid;
+  }
+  AttnTile e;
+  e.q0 = sd.cu_q[lo];
+  e.lq = sd.cu_q[lo + 1] - e.q0;
+  e.k0 = sd.cu_k[lo];
+  e.lk = sd.cu_k[lo + 1] - e.k0;
+  e.t0 = (t - sd.prefix[lo]) * sd.span;
+  e.seq = lo;
+  e.pad1 = e.pad2 = 0;
+  int w;
+  if (sd.keys) {
+    const int first = max(0, e.t0 - (e.lk - e.lq)) / ATTN_BLK;  // first query block that sees the run
+    w = max(0, (e.lq + ATTN_BLK - 1) / ATTN_BLK - first);
+  } else {
+    w = key_blocks(e, min(e.t0 + sd.span, e.lq) - 1);
+  }
+  bin = PLAN_BINS - 1 - min(w >> shift, PLAN_BINS - 1);
+  return e;
+}
+__device__ __forceinline__ void put_entry(AttnTile* out, const AttnTile& e) {
+  int4* o = reinterpret_cast<int4*>(out);
+  o[0] = make_int4(e.q0, e.lq, e.k0, e.lk);
+  o[1] = make_int4(e.t0, e.seq, 0, 0);
+}
+
 __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int* warp_sums) {
-  // runs before each sequence
-  __shared__ int carry;
-  if (threadIdx.x == 0) {
-    carry = 0;
-    sd.prefix[0] = 0;
-  }
-  __syncthreads();
-  for (int b0 = 0; b0 < a.n_seq; b0 += PLAN_THREADS) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    const int runs = b < a.n_seq ? (sd.cu[b + 1] - sd.cu[b] + sd.span - 1) / sd.span : 0;
-    const int incl = block_scan(runs, warp_sums);
-    if (b < a.n_seq) sd.prefix[b + 1] = carry + incl;
-    __syncthreads();
-    if (threadIdx.x == PLAN_THREADS - 1) carry += incl;
-    __syncthreads();
-  }
-  const int total = carry;
+  const int32_t* cu = sd.keys ? sd.cu_k : sd.cu_q;
   const int64_t other = (sd.keys ? a.Tq : a.Tk) / ATTN_BLK + 2;
   int shift = 0;  // weights beyond the bins share bins
   while ((other >> shift) >= PLAN_BINS) ++shift;
   for (int i = threadIdx.x; i < PLAN_BINS; i += PLAN_THREADS) hist[i] = 0;
-  __syncthreads();
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int t = threadIdx.x; t < total; t += PLAN_THREADS) {
-      int lo = 0, hi = a.n_seq;  // prefix[lo] <= t < prefix[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sd.prefix[mid] <= t) lo = mid; else hi = mid;
-      }
-      AttnTile e;
-      e.q0 = a.cu_q[lo];
-      e.lq = a.cu_q[lo + 1] - e.q0;
-      e.k0 = a.cu_k[lo];
-      e.lk = a.cu_k[lo + 1] - e.k0;
-      e.t0 = (t - sd.prefix[lo]) * sd.span;
-      e.seq = lo;
-      e.pad1 = e.pad2 = 0;
-      int w;
-      if (sd.keys) {
-        const int first = max(0, e.t0 - (e.lk - e.lq)) / ATTN_BLK;   // first query block that sees the run
-        w = max(0, (e.lq + ATTN_BLK - 1) / ATTN_BLK - first);
-      } else {
-        w = key_blocks(e, min(e.t0 + sd.span, e.lq) - 1);
-      }
-      const int bin = PLAN_BINS - 1 - min(w >> shift, PLAN_BINS - 1);
-      if (pass == 0) {
-        atomicAdd(&hist[bin], 1);
-      } else {
-        const int at = atomicAdd(&hist[bin], 1);
-        int4* o = reinterpret_cast<int4*>(sd.out + at);
-        o[0] = make_int4(e.q0, e.lq, e.k0, e.lk);
-        o[1] = make_int4(e.t0, e.seq, 0, 0);
-      }
-    }
+  // runs before each sequence
+  int total = 0;
+  if (threadIdx.x == 0) sd.prefix[0] = 0;
+  for (int b0 = 0; b0 < a.n_seq; b0 += PLAN_THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    const int runs = b < a.n_seq ? (cu[b + 1] - cu[b] + sd.span - 1) / sd.span : 0;
+    const int incl = block_scan(runs, warp_sums) + total;
+    if (b < a.n_seq) sd.prefix[b + 1] = incl;
+    if (threadIdx.x == PLAN_THREADS - 1) warp_sums[32] = incl;
     __syncthreads();
-    if (pass == 0) {
-      // counts -> first positions, two bins a thread
-      const int i = 2 * static_cast<int>(threadIdx.x);
-      const int c0 = hist[i], c1 = hist[i + 1];
-      const int incl = block_scan(c0 + c1, warp_sums);
-      hist[i] = incl - c0 - c1;
-      hist[i + 1] = incl - c1;
-      __syncthreads();
-    }
+    total = warp_sums[32];
+  }
+  // counts per bin -> first positions -> entries.  A thread's first entry
+  // stays in registers between the two passes.
+  const int t0 = static_cast<int>(threadIdx.x);
+  int bin0 = 0, bin;
+  AttnTile e0;
+  if (t0 < total) {
+    e0 = make_entry(a, sd, t0, shift, bin0);
+    atomicAdd(&hist[bin0], 1);
+  }
+  for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
+    make_entry(a, sd, t, shift, bin);
+    atomicAdd(&hist[bin], 1);
+  }
+  __syncthreads();
+  const int i = 2 * t0, c0 = hist[i], c1 = hist[i + 1];
+  const int incl = block_scan(c0 + c1, warp_sums);
+  hist[i] = incl - c0 - c1;
+  hist[i + 1] = incl - c1;
+  __syncthreads();
+  if (t0 < total) put_entry(sd.out + atomicAdd(&hist[bin0], 1), e0);
+  for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
+    const AttnTile e = make_entry(a, sd, t, shift, bin);
+    put_entry(sd.out + atomicAdd(&hist[bin], 1), e);
   }
   if (threadIdx.x == 0) *sd.count = total;
   __syncthreads();
@@ -119,15 +128,29 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
 
 __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanArgs a) {
   __shared__ int hist[PLAN_BINS];
-  __shared__ int warp_sums[32];
+  __shared__ int warp_sums[33];
+  __shared__ int32_t small_q[PLAN_SMALL + 1], small_k[PLAN_SMALL + 1];
+  __shared__ int small_prefix[PLAN_SMALL + 1];
   __shared__ int bad;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
   griddep_wait();
+  // the next kernel's prologue may start now: it waits for this grid's end in
+  // griddep_wait before it reads the lists
+  griddep_launch_dependents();
+  const bool small = a.n_seq <= PLAN_SMALL;
   // offsets must rise from >= 0 to at most the row counts
   for (int b = threadIdx.x; b < a.n_seq; b += PLAN_THREADS) {
     const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
     if (q0 < 0 || q1 < q0 || q1 > a.Tq || k0 < 0 || k1 < k0 || k1 > a.Tk) bad = 1;
+    if (small) {
+      small_q[b] = q0;
+      small_k[b] = k0;
+      if (b == a.n_seq - 1) {
+        small_q[b + 1] = q1;
+        small_k[b + 1] = k1;
+      }
+    }
   }
   __syncthreads();
   if (bad) {
@@ -136,15 +159,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
       a.plan.counts[0] = 0;
       a.plan.counts[1] = 0;
     }
-    __syncthreads();
-  } else {
-    build_side(a, Side{a.cu_q, a.q_span, a.prefix_q, a.plan.q_tiles, a.plan.counts, false}, hist, warp_sums);
-    if (a.plan.k_tiles)
-      build_side(a, Side{a.cu_k, ATTN_BLK, a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true}, hist, warp_sums);
+    return;
   }
-  // the lists are complete: the next kernel waits for this grid's end in
-  // griddep_wait, so its prologue may start now
-  griddep_launch_dependents();
+  const int32_t* cq = small ? small_q : a.cu_q;
+  const int32_t* ck = small ? small_k : a.cu_k;
+  build_side(a, Side{cq, ck, a.q_span, small ? small_prefix : a.prefix_q, a.plan.q_tiles, a.plan.counts, false}, hist,
+             warp_sums);
+  if (a.plan.k_tiles)
+    build_side(a, Side{cq, ck, ATTN_BLK, small ? small_prefix : a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true},
+               hist, warp_sums);
 }
 
 }  // namespace
