@@ -41,10 +41,11 @@ namespace coda {
 namespace {
 
 constexpr int FWD_THREADS = 384;
-constexpr int FWD_STAGES = 5;
+constexpr int FWD_STAGES = 4;
 constexpr uint32_t TILE_BYTES = ATTN_BLK * ATTN_D * 2;  // 32 KB
 constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;         // 64 columns
-constexpr uint32_t FWD_SMEM = 1024 + (2 + FWD_STAGES) * TILE_BYTES + 512;
+constexpr uint32_t FWD_OUT = 8 * 4096;  // 32 rows x 64 columns of O per softmax warp, on their way to memory
+constexpr uint32_t FWD_SMEM = 1024 + (2 + FWD_STAGES) * TILE_BYTES + FWD_OUT + 512;
 static_assert(FWD_SMEM <= 232448, "shared memory per CTA");
 
 struct FwdItem {
@@ -80,7 +81,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * TILE_BYTES;
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + FWD_STAGES * TILE_BYTES);
+  uint8_t* sO = sKV + FWD_STAGES * TILE_BYTES;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(sO + FWD_OUT);
   uint64_t* kv_empty = kv_full + FWD_STAGES;
   uint64_t* kv_raw = kv_empty + FWD_STAGES;  // a V block that still has to be cleared behind the sequence
   uint64_t* q_full = kv_raw + FWD_STAGES;
@@ -362,22 +364,41 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       }
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
       if (n > 0) {
+        // through shared memory, so that a warp's store covers whole 128-byte
+        // lines: rows of 64 columns, 16-byte piece p of row r at p ^ (r & 7)
+        uint8_t* box = sO + warp * 4096;
+        const int64_t rows = static_cast<int64_t>(it.t.q0) + row0;
+        const int heads0 = x ? it.head[1] : it.head[0];
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          float o[32];
-          __syncwarp();
-          tmem_ld32(tO + q * 32, o);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= inv;
-          if (valid && vis > 0) {
+          for (int q = 0; q < 2; ++q) {
+            float o[32];
+            tmem_ld32(tO + h * 64 + q * 32, o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) store_bf16x8(dst + q * 32 + i * 8, o + i * 8);
+            for (int i = 0; i < 4; ++i) {
+              float v[8];
+#pragma unroll
+              for (int k2 = 0; k2 < 8; ++k2) v[k2] = vis > 0 ? o[8 * i + k2] * inv : 0.f;
+              store_bf16x8(reinterpret_cast<__nv_bfloat16*>(box + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)), v);
+            }
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int br = 4 * i + (lane >> 3), tr = (warp & 3) * 32 + br;  // row of the box, of the tile
+            const int trow = row0 + (tr >> a.head_shift);
+            const uint4 v = *reinterpret_cast<const uint4*>(box + br * 128 + (((lane & 7) ^ (br & 7)) << 4));
+            if (trow < it.t.lq)
+              *reinterpret_cast<uint4*>(a.O + ((rows + (tr >> a.head_shift)) * a.n_q + heads0 +
+                                               (tr & ((1 << a.head_shift) - 1))) * ATTN_D + h * 64 + (lane & 7) * 8) = v;
+          }
+          __syncwarp();
         }
         tc_fence_before();
       }
       if (valid) {
-        if (vis == 0) {
+        if (n == 0) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
         }
