@@ -75,10 +75,6 @@ struct AttnBwdArgs {
   const int* counts;
   const AttnTile* q_tiles;
   const AttnTile* k_tiles;
-  const __nv_bfloat16* Q;   // [Tq, n_q * 128], row stride ldq
-  int64_t ldq;
-  const __nv_bfloat16* O;   // [Tq, n_q * 128]
-  const __nv_bfloat16* dO;
   const float* lse;         // [n_q, Tq]
   float* nlse2;             // [n_q, Tp]: -lse * log2(e); -inf where the row has no weight
   float* ndelta;            // [n_q, Tp]: -rowsum(dO * O)
@@ -87,11 +83,13 @@ struct AttnBwdArgs {
   __nv_bfloat16* dV;
   int64_t Tq, Tk, Tp;
   int n_q, n_kv, group;
+  int splits;              // parts a group's heads are cut into for dK, dV (divides group)
+  float* part;             // splits > 1: [key tile, n_kv, splits, 2, 32, 128, 4] partial dV | dK
   float scale_log2, scale;
   int* status;
   uint64_t timeout_ns;
 };
-// maps: Q, K, V, dO (boxes of 64 columns x 128 rows)
+// maps: Q, K, V, dO, O (boxes of 64 columns x 128 rows)
 cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64_t max_q_tiles, int64_t max_k_tiles,
                             int sms, cudaStream_t s);
 

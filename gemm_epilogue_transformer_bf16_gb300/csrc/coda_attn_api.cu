@@ -103,6 +103,34 @@ void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, i
 // Padded rows of the backward's per-row values (see AttnBwdArgs).
 int64_t padded_rows(int64_t Tq, int64_t n_seq) { return (Tq / coda::ATTN_BLK + n_seq + 1) * coda::ATTN_BLK; }
 
+// Parts a group's heads are cut into for dK and dV (a divisor of the group).
+// An item of the key-tile kernel meets all query tiles of its part's heads, so
+// with few key tiles the longest item (whole group, whole sequence) runs on
+// while most SMs are idle; each part costs a write and a read of 128 KB.  The
+// choice minimises that kernel's estimated time for sequences of the mean
+// length: ITER us per block pair of the longest item or of an SM's share,
+// JOIN us for the joining kernel and PART us for each part.
+int bwd_splits(int64_t Tk, int64_t n_seq, int group, int n_kv) {
+  constexpr double SMS = 152, ITER = 1.1, JOIN = 3, PART = 0.06;
+  if (Tk == 0 || n_seq == 0) return 1;
+  const double blocks = std::ceil(std::ceil(double(Tk) / n_seq) / coda::ATTN_BLK);
+  const double items = blocks * n_seq * n_kv, pairs = items * group * (blocks + 1) / 2;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= group; ++s) {
+    if (group % s) continue;
+    const double t = ITER * std::max(group / s * blocks, pairs / SMS) + (s > 1 ? JOIN + PART * items * s : 0);
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
+}
+int64_t bwd_part_floats(int64_t key_tiles, int splits, int n_kv) {
+  return splits == 1 ? 0 : key_tiles * n_kv * splits * 2 * coda::ATTN_BLK * coda::ATTN_D;
+}
+
 bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
   const uint64_t st[1] = {static_cast<uint64_t>(ld) * 2};
@@ -239,6 +267,7 @@ size_t coda_attention_bwd_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, 
   PlanLayout l{};
   lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true);
   c.take<float>(2 * n_q * padded_rows(Tq, n_seq));
+  c.take<float>(bwd_part_floats(l.max_k_tiles, bwd_splits(Tk, n_seq, n_q / n_kv, n_kv), n_kv));
   return c.off;
 }
 
@@ -275,13 +304,11 @@ int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, con
   a.Tp = padded_rows(Tq, n_seq);
   a.nlse2 = c.take<float>(2 * n_q * a.Tp);
   a.ndelta = a.nlse2 + n_q * a.Tp;
+  a.splits = bwd_splits(Tk, n_seq, n_q / n_kv, n_kv);
+  a.part = c.take<float>(bwd_part_floats(l.max_k_tiles, a.splits, n_kv));
   a.counts = l.a.plan.counts;
   a.q_tiles = l.a.plan.q_tiles;
   a.k_tiles = l.a.plan.k_tiles;
-  a.Q = B(Q);
-  a.ldq = ldq;
-  a.O = B(O);
-  a.dO = B(dO);
   a.lse = lse;
   a.dQ = B(dQ);
   a.dK = B(dK);
@@ -295,11 +322,13 @@ int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, con
   a.scale_log2 = static_cast<float>(scale * LOG2E);
   a.status = static_cast<int*>(ws);
   a.timeout_ns = WAIT_LIMIT_NS;
-  CUtensorMap maps[4];
-  if (Tq > 0 && (!map_rows(&maps[0], Q, Tq, wq, ldq) || !map_rows(&maps[3], dO, Tq, wq, wq))) return CODA_ERR_CUDA;
+  CUtensorMap maps[5];
+  if (Tq > 0 && (!map_rows(&maps[0], Q, Tq, wq, ldq) || !map_rows(&maps[3], dO, Tq, wq, wq) ||
+                 !map_rows(&maps[4], O, Tq, wq, wq)))
+    return CODA_ERR_CUDA;
   if (Tk > 0 && (!map_rows(&maps[1], K, Tk, wk, ldk) || !map_rows(&maps[2], V, Tk, wk, ldv))) return CODA_ERR_CUDA;
   // without queries (keys) no tile of them is ever loaded
-  if (Tq == 0) maps[0] = maps[3] = maps[1];
+  if (Tq == 0) maps[0] = maps[3] = maps[4] = maps[1];
   if (Tk == 0) maps[1] = maps[2] = maps[0];
   CU(coda::launch_attn_plan(l.a, s));
   CU(coda::launch_attn_bwd(a, maps, Tq > 0 ? l.max_q_tiles : 0, Tk > 0 ? l.max_k_tiles : 0, sms, s));

@@ -11,9 +11,18 @@
 // tiles in global memory (64 KB per block pair and head, in an order that
 // changes from run to run).  Tensor bound.
 //
-// A small kernel first writes -lse * log2(e) and -D per row and head.
+// The query-tile kernel runs first: it has the rows of dO at hand, forms D, and
+// leaves -lse * log2(e) and -D per row and head for the key-tile kernel.
+//
+// Few or short sequences give few key tiles, and one item of the key-tile
+// kernel holds all query heads of its group.  Then the group is cut into
+// parts (`splits`), whose fp32 partial dK and dV a third kernel adds in fixed
+// order.
 //
 // Roundings: P and dS to bf16 before their products; dQ, dK, dV to bf16 once.
+// D = dO . O inherits O's rounding to bf16, which weighs where a row sees few
+// keys (|O| is then as large as the values); rows of a tile with one key block
+// take D = sum_j p_ij dP_ij instead, which is the same number.
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -30,53 +39,12 @@ constexpr int KV_STAGES = 5;  // key-tile kernel: ring of Q and dO tiles beside 
 constexpr int Q_STAGES = 6;   // query-tile kernel: ring of K and V tiles
 constexpr uint32_t ROW_BYTES = 2 * ATTN_BLK * 4;  // -lse2 and -D of a tile
 constexpr uint32_t KV_SMEM = (2 + KV_STAGES) * TILE_BYTES + 2 * ROW_BYTES + 512;
-constexpr uint32_t Q_SMEM = Q_STAGES * TILE_BYTES + 512;
+constexpr uint32_t Q_BOX = 4096;  // 32 rows x 64 columns per softmax warp: rows on their way between memory and TMEM
+constexpr uint32_t Q_SMEM = Q_STAGES * TILE_BYTES + 8 * Q_BOX + 512 + 3 * ATTN_BLK * 4;
 static_assert(KV_SMEM <= 232448 && Q_SMEM <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ int64_t padded_row(const AttnTile& t) {
   return (static_cast<int64_t>(t.q0 / ATTN_BLK) + t.seq) * ATTN_BLK;
-}
-
-// ------------------------------------------------------------------ row values
-// Sixteen lanes per row and head; HBM-bound (O and dO once).
-__global__ void __launch_bounds__(256) attn_bwd_rows_kernel(const AttnBwdArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tiles = *reinterpret_cast<const volatile int*>(a.counts);
-  const int sub = threadIdx.x & 15;
-  const int per = ATTN_BLK * a.n_q;  // (row, head) pairs of a tile
-  const int chunks = (per + 127) / 128;
-  // a block takes 128 pairs at a time, sixteen per step
-  for (int64_t w = blockIdx.x; w < static_cast<int64_t>(tiles) * chunks; w += gridDim.x) {
-    const int ti = static_cast<int>(w / chunks), ch = static_cast<int>(w - static_cast<int64_t>(ti) * chunks);
-    const AttnTile t = load_tile(a.q_tiles + ti);
-    const int64_t pad = padded_row(t) + t.t0;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const int pair = ch * 128 + i * 16 + (threadIdx.x >> 4);
-      const int r = pair / a.n_q, h = pair - r * a.n_q;
-      const int row = t.t0 + r;
-      float d = 0.f;
-      const bool in = pair < per && row < t.lq;
-      if (in) {
-        const int64_t at = (static_cast<int64_t>(t.q0) + row) * a.n_q * ATTN_D + h * ATTN_D + sub * 8;
-        float x[8], y[8];
-        load_bf16x8(a.O + at, x);
-        load_bf16x8(a.dO + at, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d = fmaf(x[k], y[k], d);
-      }
-#pragma unroll
-      for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if (sub == 0 && pair < per) {
-        const bool seen = in && row + 1 + t.lk - t.lq > 0;  // the row has a key
-        const float l = seen ? a.lse[static_cast<int64_t>(h) * a.Tq + t.q0 + row] : 0.f;
-        const int64_t o = static_cast<int64_t>(h) * a.Tp + pad + r;
-        a.nlse2[o] = seen ? -l * 1.4426950408889634f : -INFINITY;
-        a.ndelta[o] = seen ? -d : 0.f;
-      }
-    }
-  }
 }
 
 // Barrier waits of one role; `ok` latches the first failure.
@@ -153,8 +121,8 @@ __device__ __forceinline__ void store_row64(uint32_t taddr, __nv_bfloat16* dst, 
 }
 
 // ------------------------------------------------------------------ dK, dV
-// Item: a tile of 128 keys of one key/value head; it meets the query tiles
-// that see it, for every query head of the group (iterations).
+// Item: a tile of 128 keys of one key/value head and a part of its query
+// heads; it meets the query tiles that see it, head by head (iterations).
 //
 //   warps 0-7   thread = key row, warpgroup = half of the 128 queries:
 //               P^T = exp2(S^T c - lse2) and dS^T = P^T (dP^T - D), bf16,
@@ -167,11 +135,15 @@ __device__ __forceinline__ void store_row64(uint32_t taddr, __nv_bfloat16* dst, 
 struct KvItem {
   AttnTile t;
   int kv, first, n;  // first query tile, query tiles
+  int h0, nh;        // query heads
 };
 __device__ __forceinline__ KvItem kv_item(const AttnBwdArgs& a, int w) {
   KvItem it;
-  const int ti = w / a.n_kv;
-  it.kv = w - ti * a.n_kv;
+  const int per = a.n_kv * a.splits;
+  const int ti = w / per, rest = w - ti * per;
+  it.kv = rest / a.splits;
+  it.nh = a.group / a.splits;
+  it.h0 = it.kv * a.group + (rest - it.kv * a.splits) * it.nh;
   it.t = load_tile(a.k_tiles + ti);
   it.first = max(0, it.t.t0 - (it.t.lk - it.t.lq)) / ATTN_BLK;
   it.n = max(0, (it.t.lq + ATTN_BLK - 1) / ATTN_BLK - it.first);
@@ -243,7 +215,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
   griddep_wait();
   griddep_launch_dependents();
-  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv;
+  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv * a.splits;
   const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
   Waiter wait{abort_flag, a.status, a.timeout_ns};
 
@@ -271,7 +243,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         load_pair(sK, &mK, kv_full, it.kv * ATTN_D, it.t.k0 + it.t.t0, el);
         load_pair(sV, &mV, kv_full, it.kv * ATTN_D, it.t.k0 + it.t.t0, el);
         const int64_t pad = padded_row(it.t);
-        for (int h = it.kv * a.group; h < (it.kv + 1) * a.group && wait.ok; ++h) {
+        for (int h = it.h0; h < it.h0 + it.nh && wait.ok; ++h) {
           for (int j = 0; j < it.n && wait.ok; ++j, ++iter) {
             const int row = (it.first + j) * ATTN_BLK;
             const bool ragged = row + ATTN_BLK > it.t.lq;
@@ -293,7 +265,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const KvItem it = kv_item(a, w);
         const int last = (it.first + it.n - 1) * ATTN_BLK;
-        for (int h = 0; h < a.group && it.n > 0 && wait.ok; ++h) {
+        for (int h = 0; h < it.nh && it.n > 0 && wait.ok; ++h) {
           pos += 2 * it.n;
           if (last + ATTN_BLK <= it.t.lq) continue;
           for (int x = 2; x >= 1; --x) {  // the head's last Q tile, then its dO tile
@@ -320,7 +292,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const KvItem it = kv_item(a, w);
         if (it.n == 0) continue;
-        const int n = it.n * a.group;
+        const int n = it.n * it.nh;
         if (!wait(kv_full, kvn & 1)) break;
         ++kvn;
         if (!ready(pos)) break;
@@ -370,7 +342,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
       const KvItem it = kv_item(a, w);
       const int off = it.t.lk - it.t.lq;
-      for (int h = 0; h < a.group && wait.ok; ++h) {
+      for (int h = 0; h < it.nh && wait.ok; ++h) {
         for (int j = 0; j < it.n; ++j, ++iter) {
           const int q0 = (it.first + j) * ATTN_BLK;
           const bool diag = it.t.t0 + ATTN_BLK - 1 > q0 + off;          // some key is later than some query
@@ -446,21 +418,41 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       // warpgroup 0 writes dV, warpgroup 1 dK
       const int key = it.t.t0 + r;
       const bool valid = key < it.t.lk;
-      __nv_bfloat16* dst = (half ? a.dK : a.dV) +
-                           ((static_cast<int64_t>(it.t.k0) + key) * a.n_kv + it.kv) * ATTN_D;
+      const float f = half ? a.scale : 1.f;
+      const uint32_t src = (half ? tDK : tDV) + lanes;
       if (it.n > 0) {
         if (!wait.warp(acc_full, done & 1)) break;
         ++done;
         tc_fence_after();
-        const uint32_t src = (half ? tDK : tDV) + lanes;
-        const float f = half ? a.scale : 1.f;
-        store_row64(src, dst, f, valid);
-        store_row64(src + 64, dst + 64, f, valid);
-        tc_fence_before();
-      } else if (valid) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
       }
+      if (a.splits > 1) {
+        // column by column of four, rows side by side
+        float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(w) * 2 + half) * ATTN_BLK * ATTN_D) + r;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float v[32];
+          if (it.n > 0) {
+            __syncwarp();
+            tmem_ld32(src + q * 32, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (valid) dst[(q * 8 + i) * ATTN_BLK] = make_float4(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+        }
+      } else {
+        __nv_bfloat16* dst = (half ? a.dK : a.dV) + ((static_cast<int64_t>(it.t.k0) + key) * a.n_kv + it.kv) * ATTN_D;
+        if (it.n > 0) {
+          store_row64(src, dst, f, valid);
+          store_row64(src + 64, dst + 64, f, valid);
+        } else if (valid) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc_fence_before();
     }
   }
 
@@ -473,10 +465,40 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   }
 }
 
+// Adds the parts of a key tile's dV and dK: a thread takes one row and eight
+// columns, a block 256 of the 2 * 2048 such pieces of a (key tile, head), so
+// the loads of all parts are in flight at once.
+__global__ void __launch_bounds__(256) attn_bwd_join_kernel(const AttnBwdArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tiles = reinterpret_cast<const volatile int*>(a.counts)[1];
+  const int which = (blockIdx.x >> 3) & 1;  // 0: dV
+  const int64_t at = blockIdx.x >> 4;       // key tile, head
+  const int ti = static_cast<int>(at / a.n_kv), kv = static_cast<int>(at - static_cast<int64_t>(ti) * a.n_kv);
+  if (ti >= tiles) return;
+  const AttnTile t = load_tile(a.k_tiles + ti);
+  const int u = (blockIdx.x & 7) * 256 + static_cast<int>(threadIdx.x);
+  const int row = u & (ATTN_BLK - 1), c8 = u >> 7;
+  if (t.t0 + row >= t.lk) return;
+  const float4* src = reinterpret_cast<const float4*>(a.part + (at * a.splits * 2 + which) * ATTN_BLK * ATTN_D) +
+                      2 * c8 * ATTN_BLK + row;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < a.splits; ++p) {
+    const float4* s = src + static_cast<int64_t>(p) * 2 * ATTN_BLK * ATTN_D / 4;
+    const float4 x = s[0], y = s[ATTN_BLK];
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  }
+  store_bf16x8((which ? a.dK : a.dV) + ((static_cast<int64_t>(t.k0) + t.t0 + row) * a.n_kv + kv) * ATTN_D + c8 * 8, v);
+}
+
 // ------------------------------------------------------------------ dQ
 // Item: a tile of 128 queries of one head; it meets the key blocks it sees.
 // Q and dO go to TMEM (the A operands of S and dP), so each product reads
-// only its K or V block from shared memory:
+// only its K or V block from shared memory.  They and O (for D) come through
+// the ring in front of the item's K and V blocks, so they are at hand when the
+// previous item ends:
 //   TMEM  S 128 | dP (dS over it) 128 | dQ 128 | Q 64 | dO 64
 //   UMMA  S' = Q K'^T | dQ += dS K | dP' = dO V'^T   (primes: the next block)
 struct QItem {
@@ -493,11 +515,13 @@ __device__ __forceinline__ QItem q_item(const AttnBwdArgs& a, int w) {
 }
 
 __global__ void __launch_bounds__(BWD_THREADS, 1)
-    attn_bwd_q_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
-                      const AttnBwdArgs a) {
+    attn_bwd_q_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
+                      const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG,
+                      const __grid_constant__ CUtensorMap mO, const AttnBwdArgs a) {
   extern __shared__ __align__(1024) uint8_t bwd_smem[];
   uint8_t* ring = bwd_smem;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + Q_STAGES * TILE_BYTES);
+  uint8_t* boxes = ring + Q_STAGES * TILE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 8 * Q_BOX);
   uint64_t* empty = full + Q_STAGES;
   uint64_t* raw = empty + Q_STAGES;
   uint64_t* qg_ready = raw + Q_STAGES;
@@ -506,10 +530,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   uint64_t* dp_full = s_read + 1;
   uint64_t* ds_ready = dp_full + 1;
   uint64_t* acc_full = ds_ready + 1;
-  uint64_t* drain = acc_full + 1;
+  uint64_t* d_ready = acc_full + 1;
+  uint64_t* x_ready = d_ready + 1;
+  uint64_t* drain = x_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((3 * Q_STAGES + 7) * 8 + 8 <= 512, "barrier area");
+  static_assert((3 * Q_STAGES + 9) * 8 + 8 <= 512, "barrier area");
+  float* row_d = reinterpret_cast<float*>(boxes + 8 * Q_BOX + 512);  // D of the item's rows
+  float* row_x = row_d + ATTN_BLK;                                              // two half sums of p dP
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -524,13 +552,18 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     mbar_init(dp_full, 1);
     mbar_init(ds_ready, 8);
     mbar_init(acc_full, 1);
+    mbar_init(d_ready, 4);
+    mbar_init(x_ready, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 9 && lane == 0) {
+    tma_prefetch_desc(&mQ);
     tma_prefetch_desc(&mK);
     tma_prefetch_desc(&mV);
+    tma_prefetch_desc(&mG);
+    tma_prefetch_desc(&mO);
   }
   if (warp == 8) {
     tmem_alloc<false>(tmem_slot, 512);
@@ -564,6 +597,10 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const QItem it = q_item(a, w);
         const int col = it.head / a.group * ATTN_D;
+        if (it.n == 0) continue;
+        put(mQ, it.head * ATTN_D, it.t.q0 + it.t.t0, false);
+        if (wait.ok) put(mG, it.head * ATTN_D, it.t.q0 + it.t.t0, false);
+        if (wait.ok) put(mO, it.head * ATTN_D, it.t.q0 + it.t.t0, false);
         for (int j = 0; j < it.n && wait.ok; ++j) {
           const int row = j * ATTN_BLK;
           put(mK, col, it.t.k0 + row, row + ATTN_BLK > it.t.lk);
@@ -576,8 +613,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       uint32_t pos = 0, seen = 0;
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const QItem it = q_item(a, w);
-        pos += 2 * it.n;
-        if (it.n == 0 || it.n * ATTN_BLK <= it.t.lk) continue;
+        if (it.n == 0) continue;
+        pos += 3 + 2 * it.n;
+        if (it.n * ATTN_BLK <= it.t.lk) continue;
         const uint32_t s = (pos - 2) % Q_STAGES;
         if (!wait.warp(&raw[s], (seen >> s) & 1)) break;
         seen ^= 1u << s;
@@ -600,7 +638,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const QItem it = q_item(a, w);
         if (it.n == 0) continue;
         if (!wait(qg_ready, itn & 1)) break;
+        tc_fence_after();
         ++itn;
+        if (el) {  // Q, dO and O have left the ring
+#pragma unroll
+          for (int i = 0; i < 3; ++i) mbar_arrive(&empty[(pos + i) % Q_STAGES]);
+        }
+        __syncwarp();
+        pos += 3;
         if (!ready(pos)) break;
         mma_ts(tS, tQ, stage(pos), false, el);
         issued = true;
@@ -644,53 +689,96 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t mS = tS + lanes + half * 64, mP = tP + lanes + half * 64;
     const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
-    uint32_t iter = 0, done = 0;
-    // this thread's row of the item's Q (warpgroup 0) or dO (warpgroup 1)
-    auto operand_row = [&](const QItem& it, uint32_t (&u)[64]) {
-      const int row = it.t.t0 + r;
-      if (row < it.t.lq) {
-        const int64_t grow = static_cast<int64_t>(it.t.q0) + row;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            (half ? a.dO + grow * a.n_q * ATTN_D : a.Q + grow * a.ldq) + it.head * ATTN_D);
+    uint32_t iter = 0, done = 0, dn = 0, xn = 0;
+    uint8_t* box = boxes + warp * Q_BOX;
+    const int q_row = (warp & 3) * 32;  // first row of the warp
+    // this thread's row of the item's Q (warpgroup 0) or dO (warpgroup 1) from
+    // ring position `at` on; D = dO . O of the row, for both warpgroups
+    auto operand_read = [&](uint32_t at, uint4 (&u)[16]) {
+      auto piece = [&](uint32_t p, int i) {
+        return *reinterpret_cast<const uint4*>(ring + (p % Q_STAGES) * TILE_BYTES + (i >> 3) * HALF_BYTES + r * 128 +
+                                               (((i & 7) ^ (r & 7)) << 4));
+      };
+      const uint32_t mine = at + half;
+      if (!wait.warp(&full[mine % Q_STAGES], (mine / Q_STAGES) & 1)) return;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 x = src[i];
-          u[4 * i] = x.x;
-          u[4 * i + 1] = x.y;
-          u[4 * i + 2] = x.z;
-          u[4 * i + 3] = x.w;
-        }
-      } else {
+      for (int i = 0; i < 16; ++i) u[i] = piece(mine, i);
+      if (half == 0) return;
+      if (!wait.warp(&full[(at + 2) % Q_STAGES], ((at + 2) / Q_STAGES) & 1)) return;
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 64; ++i) u[i] = 0;
+      for (int i = 0; i < 16; ++i) {
+        float x[8], y[8];
+        bf16x8_to_f32(piece(at + 2, i), x);
+        bf16x8_to_f32(u[i], y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k & 3] = fmaf(x[k], y[k], d[k & 3]);
       }
+      row_d[r] = (d[0] + d[1]) + (d[2] + d[3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(d_ready);
     };
-    auto operand_store = [&](const uint32_t (&u)[64]) {
+    auto operand_store = [&](const uint4 (&u)[16]) {
       const uint32_t t = (half ? tG : tQ) + lanes;
-      tmem_st32(t, u);
-      tmem_st32(t + 32, u + 32);
+      uint32_t v[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[4 * i] = u[8 * h + i].x;
+          v[4 * i + 1] = u[8 * h + i].y;
+          v[4 * i + 2] = u[8 * h + i].z;
+          v[4 * i + 3] = u[8 * h + i].w;
+        }
+        tmem_st32(t + 32 * h, v);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(qg_ready);
     };
+    auto row_lse = [&](const QItem& y) {  // lse of this thread's row, 0 where it has none
+      const int row = y.t.t0 + r;
+      return row < y.t.lq && row + 1 + y.t.lk - y.t.lq > 0
+                 ? __ldcg(a.lse + static_cast<int64_t>(y.head) * a.Tq + y.t.q0 + row) : 0.f;
+    };
+    uint32_t pos = 0;  // ring position behind the last item whose operands have been read
     QItem it;
+    float lse = 0.f;
     int k = 0, w = first;
     if (w < items) {
       it = q_item(a, w);
       if (it.n > 0) {
-        uint32_t u[64];
-        operand_row(it, u);
-        operand_store(u);
+        uint4 u[16];
+        lse = row_lse(it);
+        operand_read(pos, u);
+        pos += 3 + 2 * it.n;
+        if (wait.ok) operand_store(u);
       }
     }
-    while (w < items) {
+    while (w < items && wait.ok) {
       const int row = it.t.t0 + r;
       const int vis = min(it.t.lk, row + 1 + it.t.lk - it.t.lq);
       const int all = it.t.t0 + 1 + it.t.lk - it.t.lq;  // keys every row sees
+      // the row's -lse2 and -D (0 weight: behind the sequence, or no key)
       const int64_t pr = it.head * a.Tp + padded_row(it.t) + row;
-      const float nl = __ldcg(a.nlse2 + pr), nd = __ldcg(a.ndelta + pr);
-      const uint64_t nl2 = f2_pack(nl, nl), nd2 = f2_pack(nd, nd);
+      const bool seen = row < it.t.lq && vis > 0;
+      const float nl = seen ? -lse * 1.4426950408889634f : -INFINITY;
+      float nd = 0.f;
+      if (it.n > 0) {
+        if (!wait.warp(d_ready, dn & 1)) break;
+        ++dn;
+        nd = seen ? -row_d[r] : 0.f;
+      }
+      if (half == 0) {
+        a.nlse2[pr] = nl;
+        if (it.n != 1) a.ndelta[pr] = nd;
+      }
+      const uint64_t nl2 = f2_pack(nl, nl);
+      const int wn = snake_item(first, step, ++k);
+      QItem nx = it;
+      nx.n = 0;
+      if (wn < items) nx = q_item(a, wn);
       for (int j = 0; j < it.n; ++j, ++iter) {
         const bool diag = (j + 1) * ATTN_BLK > all;
         const int lim = vis - j * ATTN_BLK - half * 64;
@@ -716,6 +804,19 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         {
           uint32_t d[64], u[32];
           tmem_ld64(mP, d);
+          if (it.n == 1) {
+            float t[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 64; ++i) t[i & 1] += i < lim ? p[i] * __uint_as_float(d[i]) : 0.f;
+            row_x[half * ATTN_BLK + r] = t[0] + t[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_ready);
+            if (!wait.warp(x_ready, xn & 1)) break;
+            ++xn;
+            nd = seen ? -(row_x[r] + row_x[ATTN_BLK + r]) : 0.f;
+            if (half == 0) a.ndelta[pr] = nd;
+          }
+          const uint64_t nd2 = f2_pack(nd, nd);
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             float e0, e1;
@@ -736,30 +837,47 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         if (lane == 0) mbar_arrive(ds_ready);
       }
       if (!wait.ok) break;
-      // the next item's operands are on their way while this one's last product runs
-      const int wn = snake_item(first, step, ++k);
-      QItem nx = it;
-      nx.n = 0;
-      uint32_t u[64];
-      if (wn < items) {
-        nx = q_item(a, wn);
-        if (nx.n > 0) operand_row(nx, u);
+      // the next item's operands are read while this one's last product runs,
+      // and replace them in TMEM as soon as it is done
+      uint4 u[16];
+      if (nx.n > 0) {
+        lse = row_lse(nx);
+        operand_read(pos, u);
+        pos += 3 + 2 * nx.n;
       }
       if (it.n > 0) {
         if (!wait.warp(acc_full, done & 1)) break;
         ++done;
         tc_fence_after();
       }
+      if (!wait.ok) break;
       if (nx.n > 0) operand_store(u);
-      __nv_bfloat16* dst = a.dQ + ((static_cast<int64_t>(it.t.q0) + row) * a.n_q + it.head) * ATTN_D + half * 64;
-      const bool valid = row < it.t.lq;
+      // dQ: this warpgroup's 64 columns, through the box in whole lines
+      __nv_bfloat16* dst = a.dQ + ((static_cast<int64_t>(it.t.q0) + it.t.t0 + q_row) * a.n_q + it.head) * ATTN_D + half * 64;
       if (it.n > 0) {
-        store_row64(tDQ + lanes + half * 64, dst, a.scale, valid);
-        tc_fence_before();
-      } else if (valid) {
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < 2; ++q) {
+          float v[32];
+          tmem_ld32(tDQ + lanes + half * 64 + q * 32, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= a.scale;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            store_bf16x8(reinterpret_cast<__nv_bfloat16*>(box + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)), v + 8 * i);
+        }
+        tc_fence_before();
+        __syncwarp();
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int br = 4 * i + (lane >> 3);
+        if (it.t.t0 + q_row + br >= it.t.lq) continue;
+        const uint4 x = it.n > 0 ? *reinterpret_cast<const uint4*>(box + br * 128 + (((lane & 7) ^ (br & 7)) << 4))
+                                 : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(br) * a.n_q * ATTN_D + (lane & 7) * 8) = x;
+      }
+      __syncwarp();
       it = nx;
       w = wn;
     }
@@ -800,17 +918,15 @@ cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64
   e = attn_smem_attribute(reinterpret_cast<const void*>(attn_bwd_q_kernel), 4, Q_SMEM);
   if (e != cudaSuccess) return e;
   if (max_q_tiles > 0) {
-    e = launch(attn_bwd_rows_kernel, std::min<int64_t>(int64_t(8) * sms, max_q_tiles * a.n_q), 256, 0, s, a);
+    e = launch(attn_bwd_q_kernel, std::min<int64_t>(sms, max_q_tiles * a.n_q), BWD_THREADS, Q_SMEM, s, maps[0], maps[1],
+               maps[2], maps[3], maps[4], a);
     if (e != cudaSuccess) return e;
   }
-  if (max_k_tiles > 0) {
-    e = launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv), BWD_THREADS, KV_SMEM, s, maps[0],
-               maps[1], maps[2], maps[3], a);
-    if (e != cudaSuccess) return e;
-  }
-  if (max_q_tiles == 0) return cudaSuccess;
-  return launch(attn_bwd_q_kernel, std::min<int64_t>(sms, max_q_tiles * a.n_q), BWD_THREADS, Q_SMEM, s, maps[1],
-                maps[2], a);
+  if (max_k_tiles == 0) return cudaSuccess;
+  e = launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv * a.splits), BWD_THREADS, KV_SMEM, s, maps[0],
+             maps[1], maps[2], maps[3], a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return launch(attn_bwd_join_kernel, max_k_tiles * a.n_kv * 16, 256, 0, s, a);
 }
 
 }  // namespace coda
