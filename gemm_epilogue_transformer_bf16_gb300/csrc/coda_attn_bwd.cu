@@ -36,11 +36,10 @@ constexpr int BWD_THREADS = 384;
 constexpr uint32_t TILE_BYTES = ATTN_BLK * ATTN_D * 2;  // 32 KB
 constexpr uint32_t HALF_BYTES = TILE_BYTES / 2;
 constexpr int KV_STAGES = 5;  // key-tile kernel: ring of Q and dO tiles beside K and V
-constexpr int Q_STAGES = 6;   // query-tile kernel: ring of K and V tiles
+constexpr int Q_STAGES = 6;   // query-tile kernel: ring of K, V, dO and O tiles beside Q
 constexpr uint32_t ROW_BYTES = 2 * ATTN_BLK * 4;  // -lse2 and -D of a tile
 constexpr uint32_t KV_SMEM = (2 + KV_STAGES) * TILE_BYTES + 2 * ROW_BYTES + 512;
-constexpr uint32_t Q_BOX = 4096;  // 32 rows x 64 columns per softmax warp: rows on their way between memory and TMEM
-constexpr uint32_t Q_SMEM = Q_STAGES * TILE_BYTES + 8 * Q_BOX + 512 + 3 * ATTN_BLK * 4;
+constexpr uint32_t Q_SMEM = (1 + Q_STAGES) * TILE_BYTES + 512 + 3 * ATTN_BLK * 4;
 static_assert(KV_SMEM <= 232448 && Q_SMEM <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ int64_t padded_row(const AttnTile& t) {
@@ -495,12 +494,25 @@ __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const AttnBwdArgs a)
 
 // ------------------------------------------------------------------ dQ
 // Item: a tile of 128 queries of one head; it meets the key blocks it sees.
-// Q and dO go to TMEM (the A operands of S and dP), so each product reads
-// only its K or V block from shared memory.  They and O (for D) come through
-// the ring in front of the item's K and V blocks, so they are at hand when the
-// previous item ends:
-//   TMEM  S 128 | dP (dS over it) 128 | dQ 128 | Q 64 | dO 64
-//   UMMA  S' = Q K'^T | dQ += dS K | dP' = dO V'^T   (primes: the next block)
+//
+//   TMEM  S 128 | dP 128 | dQ 128 | dS 64 | dO 64 (the A operand of dP)
+//   UMMA  S = Q K^T | dP = dO V^T | dQ += dS K of the block before
+//
+// The three products of a block have places of their own, so the tensor core
+// always has work that does not wait for the arithmetic in front of it, and
+// the blocks of all items form one stream: the first scores of the next item
+// are under way while the last dQ product of this one runs, and dQ leaves
+// between the two arithmetic steps of the next item's first block.
+//
+//   warps 0-7   thread = query row, warpgroup = half of the 128 keys:
+//               E1 p = exp2(S c - lse2);  E2 dS = p (dP - D), bf16.
+//               Warpgroup 1 also moves the next dO to TMEM and forms D.
+//   warp 8      UMMA issuer      warp 9  TMA      warp 10  K rows behind the sequence
+//
+// Ring order of an item: dO, O, K0, V0, K1, V1, ...; Q has a buffer.  A block's
+// K stays until its dQ product, which runs behind the next block's dP: that
+// one's V lies three places on, within the ring.  The next item's first V lies
+// five places behind this item's last K, so there the dQ product runs first.
 struct QItem {
   AttnTile t;
   int head, n;
@@ -513,31 +525,36 @@ __device__ __forceinline__ QItem q_item(const AttnBwdArgs& a, int w) {
   it.n = key_blocks(it.t, min(it.t.t0 + ATTN_BLK, it.t.lq) - 1);
   return it;
 }
+__device__ __forceinline__ uint32_t ring_k(uint32_t pos, int j) { return pos + 2 + 2 * j; }
+__device__ __forceinline__ uint32_t ring_v(uint32_t pos, int j) { return pos + 3 + 2 * j; }
 
 __global__ void __launch_bounds__(BWD_THREADS, 1)
     attn_bwd_q_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                       const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mG,
                       const __grid_constant__ CUtensorMap mO, const AttnBwdArgs a) {
   extern __shared__ __align__(1024) uint8_t bwd_smem[];
-  uint8_t* ring = bwd_smem;
-  uint8_t* boxes = ring + Q_STAGES * TILE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(boxes + 8 * Q_BOX);
+  uint8_t* sQ = bwd_smem;
+  uint8_t* ring = sQ + TILE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + Q_STAGES * TILE_BYTES);
   uint64_t* empty = full + Q_STAGES;
   uint64_t* raw = empty + Q_STAGES;
-  uint64_t* qg_ready = raw + Q_STAGES;
-  uint64_t* s_full = qg_ready + 1;
+  uint64_t* q_full = raw + Q_STAGES;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* g_ready = q_empty + 1;   // dO is in TMEM
+  uint64_t* s_full = g_ready + 1;
   uint64_t* s_read = s_full + 1;
   uint64_t* dp_full = s_read + 1;
-  uint64_t* ds_ready = dp_full + 1;
-  uint64_t* acc_full = ds_ready + 1;
-  uint64_t* d_ready = acc_full + 1;
+  uint64_t* dp_read = dp_full + 1;
+  uint64_t* ds_ready = dp_read + 1;
+  uint64_t* dq_done = ds_ready + 1;  // the block's dQ product has read dS
+  uint64_t* d_ready = dq_done + 1;
   uint64_t* x_ready = d_ready + 1;
   uint64_t* drain = x_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((3 * Q_STAGES + 9) * 8 + 8 <= 512, "barrier area");
-  float* row_d = reinterpret_cast<float*>(boxes + 8 * Q_BOX + 512);  // D of the item's rows
-  float* row_x = row_d + ATTN_BLK;                                              // two half sums of p dP
+  static_assert((3 * Q_STAGES + 12) * 8 + 8 <= 512, "barrier area");
+  float* row_d = reinterpret_cast<float*>(ring + Q_STAGES * TILE_BYTES + 512);  // D of the item's rows
+  float* row_x = row_d + ATTN_BLK;                                   // two half sums of p dP
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -546,12 +563,15 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       mbar_init(&empty[s], 1);
       mbar_init(&raw[s], 1);
     }
-    mbar_init(qg_ready, 8);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(g_ready, 4);
     mbar_init(s_full, 1);
     mbar_init(s_read, 8);
     mbar_init(dp_full, 1);
+    mbar_init(dp_read, 8);
     mbar_init(ds_ready, 8);
-    mbar_init(acc_full, 1);
+    mbar_init(dq_done, 1);
     mbar_init(d_ready, 4);
     mbar_init(x_ready, 8);
     mbar_init(drain, 1);
@@ -573,7 +593,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tP = tmem + 128, tDQ = tmem + 256, tQ = tmem + 384, tG = tmem + 448;
+  const uint32_t tS = tmem, tP = tmem + 128, tDQ = tmem + 256, tDS = tmem + 384, tG = tmem + 448;
   griddep_wait();
   griddep_launch_dependents();
   const int items = *reinterpret_cast<const volatile int*>(a.counts) * a.n_q;
@@ -585,7 +605,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     if (warp == 9) {
       // ---------------------------------------------------------- producer
       const uint32_t el = elect_one();
-      uint32_t pos = 0;
+      uint32_t pos = 0, qn = 0;
       auto put = [&](const CUtensorMap& m, int col, int row, bool ragged) {
         const uint32_t s = pos % Q_STAGES;
         if (!wait(&empty[s], ((pos / Q_STAGES) & 1) ^ 1)) return;
@@ -596,11 +616,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       };
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const QItem it = q_item(a, w);
-        const int col = it.head / a.group * ATTN_D;
         if (it.n == 0) continue;
-        put(mQ, it.head * ATTN_D, it.t.q0 + it.t.t0, false);
-        if (wait.ok) put(mG, it.head * ATTN_D, it.t.q0 + it.t.t0, false);
-        if (wait.ok) put(mO, it.head * ATTN_D, it.t.q0 + it.t.t0, false);
+        const int col = it.head / a.group * ATTN_D, qcol = it.head * ATTN_D, qrow = it.t.q0 + it.t.t0;
+        put(mG, qcol, qrow, false);
+        if (wait.ok) put(mO, qcol, qrow, false);
+        if (!wait(q_empty, (qn & 1) ^ 1)) break;
+        ++qn;
+        mbar_arrive_expect_tx(q_full, TILE_BYTES, el);
+        load_pair(sQ, &mQ, q_full, qcol, qrow, el);
         for (int j = 0; j < it.n && wait.ok; ++j) {
           const int row = j * ATTN_BLK;
           put(mK, col, it.t.k0 + row, row + ATTN_BLK > it.t.lk);
@@ -614,9 +637,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const QItem it = q_item(a, w);
         if (it.n == 0) continue;
-        pos += 3 + 2 * it.n;
+        const uint32_t s = ring_k(pos, it.n - 1) % Q_STAGES;
+        pos += 2 + 2 * it.n;
         if (it.n * ATTN_BLK <= it.t.lk) continue;
-        const uint32_t s = (pos - 2) % Q_STAGES;
         if (!wait.warp(&raw[s], (seen >> s) & 1)) break;
         seen ^= 1u << s;
         zero_tile_rows(ring + s * TILE_BYTES, it.t.lk - (it.n - 1) * ATTN_BLK);
@@ -625,160 +648,162 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     } else if (warp == 8) {
       // ---------------------------------------------------------- UMMA issuer
       const uint32_t el = elect_one();
-      uint32_t pos = 0, iter = 0, itn = 0;
-      bool issued = false;
-      const uint32_t r_s = smem_u32(ring);
+      uint32_t pos = 0, iter = 0, itn = 0, k_before = 0;
+      bool acc = false;  // of the dQ product that is due
+      const uint32_t q_s = smem_u32(sQ), r_s = smem_u32(ring);
       auto stage = [&](uint32_t p) { return r_s + (p % Q_STAGES) * TILE_BYTES; };
       auto ready = [&](uint32_t p) {
         const bool ok = wait(&full[p % Q_STAGES], (p / Q_STAGES) & 1);
         tc_fence_after();
         return ok;
       };
+      auto before = [&](uint64_t* bar) {  // the previous block's arrival on `bar` (none for the first)
+        const bool ok = iter == 0 || wait(bar, (iter - 1) & 1);
+        tc_fence_after();
+        return ok;
+      };
+      auto product_dq = [&] {
+        constexpr uint32_t ID = idesc_bf16(128, 128, 0, 1);
+        const uint32_t b = stage(k_before);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          umma_bf16_ts(tDQ, tDS + i * 8, sdesc_sw128(b + i * 2048, HALF_BYTES, 1024), ID, acc || i > 0, el);
+        umma_commit(&empty[k_before % Q_STAGES], el);
+        umma_commit(dq_done, el);
+      };
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
         const QItem it = q_item(a, w);
         if (it.n == 0) continue;
-        if (!wait(qg_ready, itn & 1)) break;
-        tc_fence_after();
+        for (int j = 0; j < it.n; ++j) {
+          const uint32_t kp = ring_k(pos, j), vp = ring_v(pos, j);
+          if (!ready(kp) || (j == 0 && !wait(q_full, itn & 1)) || !before(s_read)) break;
+          mma_ss(tS, q_s, stage(kp), false, el);
+          umma_commit(s_full, el);
+          if (j + 1 == it.n) umma_commit(q_empty, el);
+          if (j == 0) {
+            if (!wait(g_ready, itn & 1)) break;
+            tc_fence_after();
+            if (el) {  // dO and O have left the ring
+              mbar_arrive(&empty[pos % Q_STAGES]);
+              mbar_arrive(&empty[(pos + 1) % Q_STAGES]);
+            }
+            __syncwarp();
+            if (iter > 0) {
+              if (!before(ds_ready)) break;
+              product_dq();
+            }
+          }
+          if (!ready(vp) || !before(dp_read)) break;
+          mma_ts(tP, tG, stage(vp), false, el);
+          umma_commit(dp_full, el);
+          umma_commit(&empty[vp % Q_STAGES], el);
+          if (j > 0) {
+            if (!before(ds_ready)) break;
+            product_dq();
+          }
+          k_before = kp;
+          acc = j > 0;
+          ++iter;
+        }
+        pos += 2 + 2 * it.n;
         ++itn;
-        if (el) {  // Q, dO and O have left the ring
-#pragma unroll
-          for (int i = 0; i < 3; ++i) mbar_arrive(&empty[(pos + i) % Q_STAGES]);
-        }
-        __syncwarp();
-        pos += 3;
-        if (!ready(pos)) break;
-        mma_ts(tS, tQ, stage(pos), false, el);
-        issued = true;
-        umma_commit(s_full, el);
-        if (!ready(pos + 1)) break;
-        mma_ts(tP, tG, stage(pos + 1), false, el);
-        umma_commit(dp_full, el);
-        umma_commit(&empty[(pos + 1) % Q_STAGES], el);
-        for (int i = 0; i < it.n; ++i, ++iter, pos += 2) {
-          if (!wait(s_read, iter & 1)) break;
-          tc_fence_after();
-          if (i + 1 < it.n) {
-            if (!ready(pos + 2)) break;
-            mma_ts(tS, tQ, stage(pos + 2), false, el);
-            umma_commit(s_full, el);
-          }
-          if (!wait(ds_ready, iter & 1)) break;
-          tc_fence_after();
-          mma_tn(tDQ, tP, stage(pos), i > 0, el);
-          umma_commit(&empty[pos % Q_STAGES], el);
-          if (i + 1 < it.n) {
-            if (!ready(pos + 3)) break;
-            mma_ts(tP, tG, stage(pos + 3), false, el);
-            umma_commit(dp_full, el);
-            umma_commit(&empty[(pos + 3) % Q_STAGES], el);
-          } else {
-            umma_commit(acc_full, el);
-          }
-        }
       }
-      if (!wait.ok && issued) {
+      if (wait.ok && iter > 0 && before(ds_ready)) product_dq();
+      if (!wait.ok) {
         umma_commit(drain, el);
         mbar_wait_drain(drain, 0, 200000000ull);
       }
     }
   } else {
-    // ------------------------------------------------------------ P, dS, and the Q and dO operands
+    // ------------------------------------------------------------ P, dS, dO and D
     reg_inc<216>();
     const int half = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t mS = tS + lanes + half * 64, mP = tP + lanes + half * 64;
+    const uint32_t mS = tS + lanes + half * 64, mP = tP + lanes + half * 64, mDS = tDS + lanes + half * 32;
     const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
-    uint32_t iter = 0, done = 0, dn = 0, xn = 0;
-    uint8_t* box = boxes + warp * Q_BOX;
-    const int q_row = (warp & 3) * 32;  // first row of the warp
-    // this thread's row of the item's Q (warpgroup 0) or dO (warpgroup 1) from
-    // ring position `at` on; D = dO . O of the row, for both warpgroups
-    auto operand_read = [&](uint32_t at, uint4 (&u)[16]) {
-      auto piece = [&](uint32_t p, int i) {
-        return *reinterpret_cast<const uint4*>(ring + (p % Q_STAGES) * TILE_BYTES + (i >> 3) * HALF_BYTES + r * 128 +
-                                               (((i & 7) ^ (r & 7)) << 4));
-      };
-      const uint32_t mine = at + half;
-      if (!wait.warp(&full[mine % Q_STAGES], (mine / Q_STAGES) & 1)) return;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) u[i] = piece(mine, i);
-      if (half == 0) return;
-      if (!wait.warp(&full[(at + 2) % Q_STAGES], ((at + 2) / Q_STAGES) & 1)) return;
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x[8], y[8];
-        bf16x8_to_f32(piece(at + 2, i), x);
-        bf16x8_to_f32(u[i], y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k & 3] = fmaf(x[k], y[k], d[k & 3]);
-      }
-      row_d[r] = (d[0] + d[1]) + (d[2] + d[3]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(d_ready);
-    };
-    auto operand_store = [&](const uint4 (&u)[16]) {
-      const uint32_t t = (half ? tG : tQ) + lanes;
-      uint32_t v[32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[4 * i] = u[8 * h + i].x;
-          v[4 * i + 1] = u[8 * h + i].y;
-          v[4 * i + 2] = u[8 * h + i].z;
-          v[4 * i + 3] = u[8 * h + i].w;
-        }
-        tmem_st32(t + 32 * h, v);
-      }
-      tmem_st_wait();
+    uint32_t iter = 0, itn = 0, xn = 0, pos = 0;
+
+    // dQ of a finished item, this warpgroup's 64 columns.  (Through boxes in
+    // shared memory the stores would cover whole lines; a sixth ring stage is
+    // worth more.)
+    auto leave = [&](const QItem& y) {
+      __nv_bfloat16* dst = a.dQ + ((static_cast<int64_t>(y.t.q0) + y.t.t0 + r) * a.n_q + y.head) * ATTN_D + half * 64;
+      store_row64(tDQ + lanes + half * 64, dst, a.scale, y.t.t0 + r < y.t.lq);
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qg_ready);
     };
-    auto row_lse = [&](const QItem& y) {  // lse of this thread's row, 0 where it has none
-      const int row = y.t.t0 + r;
-      return row < y.t.lq && row + 1 + y.t.lk - y.t.lq > 0
-                 ? __ldcg(a.lse + static_cast<int64_t>(y.head) * a.Tq + y.t.q0 + row) : 0.f;
-    };
-    uint32_t pos = 0;  // ring position behind the last item whose operands have been read
-    QItem it;
-    float lse = 0.f;
-    int k = 0, w = first;
-    if (w < items) {
-      it = q_item(a, w);
-      if (it.n > 0) {
-        uint4 u[16];
-        lse = row_lse(it);
-        operand_read(pos, u);
-        pos += 3 + 2 * it.n;
-        if (wait.ok) operand_store(u);
-      }
-    }
-    while (w < items && wait.ok) {
+
+    QItem was;  // the item whose dQ is still in TMEM
+    was.n = 0;
+    for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
+      const QItem it = q_item(a, w);
       const int row = it.t.t0 + r;
       const int vis = min(it.t.lk, row + 1 + it.t.lk - it.t.lq);
       const int all = it.t.t0 + 1 + it.t.lk - it.t.lq;  // keys every row sees
       // the row's -lse2 and -D (0 weight: behind the sequence, or no key)
       const int64_t pr = it.head * a.Tp + padded_row(it.t) + row;
       const bool seen = row < it.t.lq && vis > 0;
-      const float nl = seen ? -lse * 1.4426950408889634f : -INFINITY;
-      float nd = 0.f;
-      if (it.n > 0) {
-        if (!wait.warp(d_ready, dn & 1)) break;
-        ++dn;
-        nd = seen ? -row_d[r] : 0.f;
+      const float nl = seen ? -__ldcg(a.lse + static_cast<int64_t>(it.head) * a.Tq + it.t.q0 + row) * 1.4426950408889634f
+                            : -INFINITY;
+      if (it.n == 0) {
+        if (half == 0) {
+          a.nlse2[pr] = nl;
+          a.ndelta[pr] = 0.f;
+        }
+        if (row < it.t.lq) {
+          __nv_bfloat16* dst = a.dQ + ((static_cast<int64_t>(it.t.q0) + row) * a.n_q + it.head) * ATTN_D + half * 64;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + i * 8) = make_uint4(0, 0, 0, 0);
+        }
+        continue;
       }
+      if (half) {
+        // dO to TMEM (dP of the item before is complete: E2 has waited for
+        // it), and D = dO . O for both warpgroups
+        const uint32_t at = pos;
+        auto piece = [&](uint32_t p, int i) {
+          return *reinterpret_cast<const uint4*>(ring + (p % Q_STAGES) * TILE_BYTES + (i >> 3) * HALF_BYTES + r * 128 +
+                                                 (((i & 7) ^ (r & 7)) << 4));
+        };
+        if (!wait.warp(&full[at % Q_STAGES], (at / Q_STAGES) & 1)) break;
+        if (!wait.warp(&full[(at + 1) % Q_STAGES], ((at + 1) / Q_STAGES) & 1)) break;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 g = piece(at, 8 * h + i);
+            float x[8], y[8];
+            bf16x8_to_f32(piece(at + 1, 8 * h + i), x);
+            bf16x8_to_f32(g, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e & 3] = fmaf(x[e], y[e], d[e & 3]);
+            v[4 * i] = g.x;
+            v[4 * i + 1] = g.y;
+            v[4 * i + 2] = g.z;
+            v[4 * i + 3] = g.w;
+          }
+          tmem_st32(tG + lanes + 32 * h, v);
+        }
+        row_d[r] = (d[0] + d[1]) + (d[2] + d[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(g_ready);
+          mbar_arrive(d_ready);
+        }
+      }
+      pos += 2 + 2 * it.n;
+      if (!wait.warp(d_ready, itn & 1)) break;
+      ++itn;
+      float nd = seen ? -row_d[r] : 0.f;
       if (half == 0) {
         a.nlse2[pr] = nl;
         if (it.n != 1) a.ndelta[pr] = nd;
       }
       const uint64_t nl2 = f2_pack(nl, nl);
-      const int wn = snake_item(first, step, ++k);
-      QItem nx = it;
-      nx.n = 0;
-      if (wn < items) nx = q_item(a, wn);
       for (int j = 0; j < it.n; ++j, ++iter) {
         const bool diag = (j + 1) * ATTN_BLK > all;
         const int lim = vis - j * ATTN_BLK - half * 64;
@@ -799,11 +824,21 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             p[i + 1] = exp2_sfu(z1);
           }
         }
+        const bool flush = j == 0 && was.n > 0;
+        if (flush) {
+          if (!wait.warp(dq_done, (iter - 1) & 1)) break;
+          tc_fence_after();
+          leave(was);
+        }
         if (!wait.warp(dp_full, iter & 1)) break;
         tc_fence_after();
+        uint32_t u[32];
         {
-          uint32_t d[64], u[32];
+          uint32_t d[64];
           tmem_ld64(mP, d);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dp_read);
           if (it.n == 1) {
             float t[2] = {0.f, 0.f};
 #pragma unroll
@@ -829,57 +864,19 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             }
             u[i / 2] = pack_bf16x2(e0, e1);
           }
-          tmem_st32(mP, u);
         }
+        if (iter > 0 && !flush && !wait.warp(dq_done, (iter - 1) & 1)) break;  // dS may be replaced
+        tmem_st32(mDS, u);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_ready);
       }
-      if (!wait.ok) break;
-      // the next item's operands are read while this one's last product runs,
-      // and replace them in TMEM as soon as it is done
-      uint4 u[16];
-      if (nx.n > 0) {
-        lse = row_lse(nx);
-        operand_read(pos, u);
-        pos += 3 + 2 * nx.n;
-      }
-      if (it.n > 0) {
-        if (!wait.warp(acc_full, done & 1)) break;
-        ++done;
-        tc_fence_after();
-      }
-      if (!wait.ok) break;
-      if (nx.n > 0) operand_store(u);
-      // dQ: this warpgroup's 64 columns, through the box in whole lines
-      __nv_bfloat16* dst = a.dQ + ((static_cast<int64_t>(it.t.q0) + it.t.t0 + q_row) * a.n_q + it.head) * ATTN_D + half * 64;
-      if (it.n > 0) {
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float v[32];
-          tmem_ld32(tDQ + lanes + half * 64 + q * 32, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= a.scale;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            store_bf16x8(reinterpret_cast<__nv_bfloat16*>(box + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)), v + 8 * i);
-        }
-        tc_fence_before();
-        __syncwarp();
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int br = 4 * i + (lane >> 3);
-        if (it.t.t0 + q_row + br >= it.t.lq) continue;
-        const uint4 x = it.n > 0 ? *reinterpret_cast<const uint4*>(box + br * 128 + (((lane & 7) ^ (br & 7)) << 4))
-                                 : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(br) * a.n_q * ATTN_D + (lane & 7) * 8) = x;
-      }
-      __syncwarp();
-      it = nx;
-      w = wn;
+      was = it;
+    }
+    if (wait.ok && was.n > 0 && wait.warp(dq_done, (iter - 1) & 1)) {
+      tc_fence_after();
+      leave(was);
     }
   }
 
