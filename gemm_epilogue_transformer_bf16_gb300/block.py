@@ -39,13 +39,17 @@ weight-gradient GEMMs beside its dH -> dX chain); it is off by default:
 two persistent GEMMs started together split the SMs by whichever places its
 CTAs first, and in a loop of steps the backward ran 1 % slower that way than
 on one stream.  The gate/up and down GEMMs run alone.
+
+``AttentionBlock`` is the block with its attention core (coda_attention) in
+place of the given A, over packed sequences; ``ServingBlock`` runs the forward
+of prompts and of single new tokens over a 4-bit key/value cache.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (K_MAJOR, MN_MAJOR, EpilogueDesc, fold_gamma, gemm_epilogue, linear_cross_entropy,
-               linear_cross_entropy_bwd, linear_dswiglu_fp8, linear_fp8, linear_qknorm_rope, linear_qknorm_rope_bwd,
+from . import (K_MAJOR, MN_MAJOR, EpilogueDesc, attention, attention_bwd, attention_decode_nvfp4, fold_gamma,
+               gemm_epilogue, kv_append_nvfp4, kv_read_nvfp4, linear_cross_entropy, linear_cross_entropy_bwd, linear_dswiglu_fp8, linear_fp8, linear_qknorm_rope, linear_qknorm_rope_bwd,
                linear_qknorm_rope_bwd_fp8, linear_qknorm_rope_fp8, linear_residual, linear_residual_bwd, linear_swiglu, linear_swiglu_bwd,
                linear_swiglu_fp8, load, quantize_fp8_cols, quantize_fp8_rows, rms_rstd, rmsnorm_linear_dx_fp8,
                rmsnorm_scale, rope_table, workspace)
@@ -193,6 +197,118 @@ class Block:
     def step(self, x0, A, pos, dx2, dQ, dK, dV, mark=None):
         self.forward(x0, A, pos, mark)
         return self.backward(x0, A, pos, dx2, dQ, dK, dV, mark)
+
+
+class AttentionBlock(Block):
+    """The whole block over packed sequences: Block's projections and MLP with
+    causal attention between the QKV projection and the output projection, on
+    one stream.  ``cu_seqlens`` [n_seq + 1] int32 must cover every token (the
+    weight gradients sum over all of them).
+
+    Forward   Q, K, V -> A = attention(Q, K, V) -> x1 = x0 + A Wo^T -> MLP
+    Backward  MLP -> dA = dx1 Wo -> dQ, dK, dV = attention_bwd(dA) -> QKV"""
+
+    def __init__(self, shape, weights, n_seq, device="cuda"):
+        super().__init__(shape, weights, device=device, concurrent=False)
+        s, lib = self.s, load()
+        T, d = s.tokens, s.head_dim
+        bf = dict(dtype=torch.bfloat16, device=device)
+        self.att = {"O": torch.empty(T, s.n_q * d, **bf), "lse": torch.empty(s.n_q, T, dtype=torch.float32, device=device)}
+        self.att_grads = {"dQ": torch.empty(T, s.n_q * d, **bf), "dK": torch.empty(T, s.n_kv * d, **bf),
+                          "dV": torch.empty(T, s.n_kv * d, **bf)}
+        self.n_seq = n_seq
+        need = max(lib.coda_attention_workspace_size(T, T, n_seq, s.n_q, s.n_kv, d),
+                   lib.coda_attention_bwd_workspace_size(T, T, n_seq, s.n_q, s.n_kv, d))
+        if need > self.ws.numel():
+            self.ws = self.ws2 = workspace(need, device)
+
+    def forward(self, x0, pos, cu_seqlens):
+        s, w = self.s, self.w
+        if cu_seqlens.numel() != self.n_seq + 1:
+            raise ValueError(f"cu_seqlens: expected {self.n_seq + 1} offsets")
+        rmsnorm_scale(x0, w["gamma_attn"], s.eps, rstd=self.rstd0, U=self.U0)
+        linear_qknorm_rope(self.U0, w["Wqkv"], w["gamma_q"], w["gamma_k"], pos, self.cos_sin, s.n_q, s.n_kv,
+                           rstd=self.rstd0, eps=s.eps, head_dim=s.head_dim, out=self.fwd, ws=self.ws)
+        f = self.fwd
+        attention(f["Q"], f["K"], f["V"], cu_seqlens, s.n_q, s.n_kv, out=self.att, ws=self.ws)
+        linear_residual(self.att["O"], w["Wo"], x0, eps=s.eps, Y=self.x1, rstd_out=self.rstd1,
+                        gamma_next=w["gamma_mlp"], U_out=self.U1, ws=self.ws)
+        linear_swiglu(self.U1, w["Wg"], w["Wu"], rstd=self.rstd1, H=self.H, g=self.g, u=self.u, ws=self.ws)
+        linear_residual(self.H, w["Wd"], self.x1, Y=self.x2, ws=self.ws)
+        return {"Q": f["Q"], "K": f["K"], "V": f["V"], "A": self.att["O"], "x1": self.x1, "x2": self.x2}
+
+    def backward(self, x0, pos, cu_seqlens, dx2):
+        s, w, f = self.s, self.w, self.fwd
+        linear_swiglu_bwd(dx2, self.x1, w["Wg"], w["Wu"], w["Wd"], self.g, self.u, self.H, rstd=self.rstd1,
+                          gamma=w["gamma_mlp"], dX_resid=dx2, ws=self.ws, out=self.grads_mlp)
+        linear_residual_bwd(self.dx1, self.att["O"], w["Wo"], ws=self.ws, out=self.grads_o)
+        g = attention_bwd(self.grads_o["dX"], f["Q"], f["K"], f["V"], self.att["O"], self.att["lse"], cu_seqlens, s.n_q,
+                          s.n_kv, out=self.att_grads, ws=self.ws)
+        linear_qknorm_rope_bwd(g["dQ"], g["dK"], g["dV"], f["qk_save"], f["V"], w["gamma_q"], w["gamma_k"], pos,
+                               self.cos_sin, s.n_q, s.n_kv, x0, w["Wqkv"], rstd=self.rstd0, gamma_in=w["gamma_attn"],
+                               dX_resid=self.dx1, eps=s.eps, head_dim=s.head_dim, ws=self.ws, out=self.grads_qkv)
+        return {"dx0": self.grads_qkv["dX"], "dA": self.grads_o["dX"], **g, "dx1": self.dx1,
+                "dWqkv": self.grads_qkv["dW"], "dWo": self.grads_o["dW"], "dWg": self.grads_mlp["dWg"],
+                "dWu": self.grads_mlp["dWu"], "dWd": self.grads_mlp["dWd"],
+                "dgamma_attn": self.grads_qkv["dgamma_in"], "dgamma_mlp": self.grads_mlp["dgamma"],
+                "dgamma_q": self.grads_qkv["dgamma_q"], "dgamma_k": self.grads_qkv["dgamma_k"]}
+
+    def step(self, x0, pos, cu_seqlens, dx2):
+        self.forward(x0, pos, cu_seqlens)
+        return self.backward(x0, pos, cu_seqlens, dx2)
+
+
+class ServingBlock:
+    """Forward of the block for serving, with the keys and values of every
+    token in a 4-bit paged cache (kv_cache_nvfp4).  Sizes may differ from call
+    to call, so outputs are allocated per call.
+
+    prefill  whole prompts, or the next chunk of prompts whose earlier tokens
+             the cache holds (``key_slots``, ``cu_seqlens_k``)
+    decode   one new token per sequence
+    """
+
+    def __init__(self, shape, weights, cache, device="cuda"):
+        self.s, self.w, self.cache = shape, weights, cache
+        self.cos_sin = rope_table(shape.theta, shape.head_dim, shape.seq_len, device=device)
+
+    def _qkv(self, x, pos):
+        s, w = self.s, self.w
+        rstd, U = rmsnorm_scale(x, w["gamma_attn"], s.eps)
+        return linear_qknorm_rope(U, w["Wqkv"], w["gamma_q"], w["gamma_k"], pos, self.cos_sin, s.n_q, s.n_kv, rstd=rstd,
+                                  eps=s.eps, head_dim=s.head_dim, save=False)
+
+    def _rest(self, x, A):
+        s, w = self.s, self.w
+        U, rstd = torch.empty_like(x), torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        x1 = torch.empty_like(x)
+        linear_residual(A, w["Wo"], x, eps=s.eps, Y=x1, rstd_out=rstd, gamma_next=w["gamma_mlp"], U_out=U)
+        H, _, _ = linear_swiglu(U, w["Wg"], w["Wu"], rstd=rstd, save=False)
+        return linear_residual(H, w["Wd"], x1)
+
+    def prefill(self, x, pos, slots, cu_seqlens, key_slots=None, cu_seqlens_k=None):
+        """x [T, hidden]: the packed new tokens, their positions and cache
+        slots [T].  With key_slots [Tk] and cu_seqlens_k, every sequence's keys
+        are those cached rows, in order, its new tokens last; without, the new
+        tokens are whole prompts and attend to each other unquantised."""
+        s = self.s
+        f = self._qkv(x, pos)
+        kv_append_nvfp4(f["K"], f["V"], slots, self.cache)
+        K, V = f["K"], f["V"]
+        if key_slots is not None:
+            kv = kv_read_nvfp4(self.cache, key_slots)
+            K, V = kv["K"], kv["V"]
+        out = attention(f["Q"], K, V, cu_seqlens, s.n_q, s.n_kv, cu_seqlens_k=cu_seqlens_k)
+        return self._rest(x, out["O"])
+
+    def decode(self, x, pos, slots, block_table, seq_lens):
+        """x [batch, hidden]: one new token per sequence; seq_lens [batch]
+        counts it."""
+        s = self.s
+        f = self._qkv(x, pos)
+        kv_append_nvfp4(f["K"], f["V"], slots, self.cache)
+        out = attention_decode_nvfp4(f["Q"], self.cache, block_table, seq_lens, s.n_q)
+        return self._rest(x, out["O"])
 
 
 class BlockFP8:

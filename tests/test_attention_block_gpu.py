@@ -1,0 +1,179 @@
+"""The block with its attention core, and its serving form over the 4-bit
+cache, run together as they are used.  Each stage is compared with the fp64
+oracle on the stage's actual inputs (the bf16 tensors the previous stage
+stored), so the tolerances are those of the single operators."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import coda_oracle as O
+from parity import assert_bf16, to_np
+from test_attention_gpu import check_backward, check_forward, offsets
+from test_kvcache_gpu import check_decode
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+D = 128
+
+
+@pytest.fixture(scope="module")
+def coda():
+    import gemm_epilogue_transformer_bf16_gb300 as c
+    from gemm_epilogue_transformer_bf16_gb300 import _build
+    _build.build()
+    c.load()
+    return c
+
+
+def test_training_step(coda):
+    from gemm_epilogue_transformer_bf16_gb300.block import AttentionBlock
+    lens = [100, 1, 219]
+    shape = synth.BlockShape(tokens=320, hidden=256, n_q=4, n_kv=2, head_dim=D, inter=512, seq_len=256)
+    t = synth.make_block(shape, seed=5)
+    cu = offsets(lens)
+    t["pos"] = torch.cat([torch.arange(n) for n in lens]).to(torch.int32)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    blk = AttentionBlock(shape, d, n_seq=len(lens))
+    dcu = torch.from_numpy(cu).to(DEV)
+    f = blk.forward(d["x0"], d["pos"], dcu)
+    g = blk.backward(d["x0"], d["pos"], dcu, d["dx2"])
+    assert coda.get_status(blk.ws) == 0
+    cfg = dict(n_q=shape.n_q, n_kv=shape.n_kv, head_dim=D, theta=shape.theta, eps=shape.eps)
+    scale = D ** -0.5
+    qkv = {k: f[k].cpu() for k in ("Q", "K", "V")}
+    # attention on the Q, K, V the projection stored
+    ref = O.attention_fwd(*(to_np(qkv[k]) for k in ("Q", "K", "V")), cu, cu, shape.n_q, shape.n_kv, scale)
+    check_forward({"O": f["A"], "lse": blk.att["lse"]}, ref, qkv, cu, cu, shape.n_q, shape.n_kv, scale)
+    # its gradients on the dA the output projection's backward stored
+    qkv["dO"] = g["dA"].cpu()
+    refb = O.attention_bwd(to_np(g["dA"]), *(to_np(qkv[k]) for k in ("Q", "K", "V")), cu, cu, shape.n_q, shape.n_kv, scale)
+    check_backward({k: g[k] for k in ("dQ", "dK", "dV")}, refb, qkv, cu, cu, shape.n_q, shape.n_kv, scale)
+    # everything around it, on the A, dQ, dK, dV of the core
+    o = {k: v.double().numpy() for k, v in t.items()}
+    o.update(A=to_np(f["A"]), dQ=to_np(g["dQ"]), dK=to_np(g["dK"]), dV=to_np(g["dV"]))
+    rf, rb = O.block_fwd(o, **cfg), O.block_bwd(o, **cfg)
+    for k in ("Q", "K", "V", "x1", "x2"):
+        assert_bf16(f[k], rf[k], k)
+    for k in ("dx0", "dA", "dWqkv", "dWo", "dWg", "dWu", "dWd", "dgamma_attn", "dgamma_mlp"):
+        assert_bf16(g[k], rb[k], k)
+    with pytest.raises(ValueError, match="offsets"):
+        blk.forward(d["x0"], d["pos"], dcu[:-1])
+
+
+def test_training_step_twice_and_as_a_graph(coda):
+    from gemm_epilogue_transformer_bf16_gb300.block import AttentionBlock
+    lens = [130, 60, 66]
+    shape = synth.BlockShape(tokens=256, hidden=256, n_q=4, n_kv=2, head_dim=D, inter=256, seq_len=256)
+    t = synth.make_block(shape, seed=8)
+    t["pos"] = torch.cat([torch.arange(n) for n in lens]).to(torch.int32)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    dcu = torch.from_numpy(offsets(lens)).to(DEV)
+    blk = AttentionBlock(shape, d, n_seq=3)
+    want = {k: v.clone() for k, v in blk.step(d["x0"], d["pos"], dcu, d["dx2"]).items()}
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(cap):
+        again = blk.step(d["x0"], d["pos"], dcu, d["dx2"])
+    torch.cuda.synchronize()
+    for k in want:
+        assert torch.equal(want[k], again[k]), k
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=cap):
+        out = blk.step(d["x0"], d["pos"], dcu, d["dx2"])
+    for v in out.values():
+        v.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for k in want:
+        assert torch.equal(want[k], out[k]), k
+    assert coda.get_status(blk.ws) == 0
+
+
+def test_serving_prompts_chunks_and_single_tokens(coda):
+    """Two prompts are prefilled, one of them in two chunks, then both decode
+    three tokens: the attention output of every step against the oracle on the
+    rows the cache holds, and the block's output against the oracle on that."""
+    from gemm_epilogue_transformer_bf16_gb300 import block as B
+    page, n_q, n_kv = 16, 4, 2
+    shape = synth.BlockShape(tokens=64, hidden=256, n_q=n_q, n_kv=n_kv, head_dim=D, inter=512, seq_len=128)
+    t = synth.make_block(shape, seed=9)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    w = {k: v.double().numpy() for k, v in t.items()}
+    cache = coda.kv_cache_nvfp4(16, page, n_kv)
+    order = torch.randperm(16, generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    table = order.view(2, 8)                                   # sequence b: 8 pages, 128 tokens
+    blk = B.ServingBlock(shape, d, cache)
+    seen = {}
+
+    def keep(name):
+        real = getattr(B, name)
+
+        def call(*a, **k):
+            seen[name] = (a, real(*a, **k))
+            return seen[name][1]
+        return real, call
+    originals = {}
+    for name in ("attention", "attention_decode_nvfp4"):
+        originals[name], fake = keep(name)
+        setattr(B, name, fake)
+
+    def slot(b, j):
+        j = torch.as_tensor(j)
+        return table[b][j // page].long() * page + j % page
+
+    def x_of(n, seed):
+        return synth.randn_bf16((n, shape.hidden), 1.0, seed)
+
+    def rest(x, A):
+        # the output projection and the MLP on the attention output
+        x1 = x + A @ w["Wo"].T
+        return O.mlp_fwd(x1, w["Wg"], w["Wu"], w["Wd"], x1, w["gamma_mlp"], shape.eps)
+
+    def check_rest(y, x, A, name):
+        ref = rest(to_np(x), to_np(A))
+        assert_bf16(y, ref["y"], name)
+
+    try:
+        # both prompts' first part: 30 and 21 new tokens, whole so far
+        lens = [30, 21]
+        x = x_of(51, 30)
+        pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32)
+        slots = torch.cat([slot(b, torch.arange(n)) for b, n in enumerate(lens)]).to(torch.int32)
+        y = blk.prefill(x.to(DEV), pos.to(DEV), slots.to(DEV), torch.from_numpy(offsets(lens)).to(DEV))
+        (Q, K, V, *_), out = seen["attention"]
+        ref = O.attention_fwd(to_np(Q), to_np(K), to_np(V), offsets(lens), offsets(lens), n_q, n_kv, D ** -0.5)
+        check_forward(out, ref, {"Q": Q.cpu(), "K": K.cpu(), "V": V.cpu()}, offsets(lens), offsets(lens), n_q, n_kv, D ** -0.5)
+        check_rest(y, x, out["O"], "prefill")
+        # a second chunk of the first prompt: 17 new tokens behind the cached 30
+        x = x_of(17, 31)
+        keys = slot(0, torch.arange(47)).to(torch.int32)
+        y = blk.prefill(x.to(DEV), torch.arange(30, 47, dtype=torch.int32, device=DEV),
+                        slot(0, torch.arange(30, 47)).to(torch.int32).to(DEV),
+                        torch.tensor([0, 17], dtype=torch.int32, device=DEV), key_slots=keys.to(DEV),
+                        cu_seqlens_k=torch.tensor([0, 47], dtype=torch.int32, device=DEV))
+        (Q, K, V, *_), out = seen["attention"]
+        assert torch.equal(K, coda.kv_read_nvfp4(cache, keys.to(DEV))["K"])
+        cq, ck = offsets([17]), offsets([47])
+        ref = O.attention_fwd(to_np(Q), to_np(K), to_np(V), cq, ck, n_q, n_kv, D ** -0.5)
+        check_forward(out, ref, {"Q": Q.cpu(), "K": K.cpu(), "V": V.cpu()}, cq, ck, n_q, n_kv, D ** -0.5)
+        check_rest(y, x, out["O"], "second chunk")
+        lens = [47, 21]
+        for step in range(3):
+            x = x_of(2, 40 + step)
+            new = torch.tensor([slot(b, lens[b]) for b in range(2)], dtype=torch.int32)
+            pos = torch.tensor(lens, dtype=torch.int32)
+            lens = [n + 1 for n in lens]
+            y = blk.decode(x.to(DEV), pos.to(DEV), new.to(DEV), table.to(DEV),
+                           torch.tensor(lens, dtype=torch.int32, device=DEV))
+            (Q, *_), out = seen["attention_decode_nvfp4"]
+            rows = [coda.kv_read_nvfp4(cache, slot(b, torch.arange(n)).to(torch.int32).to(DEV), dtype=torch.float32)
+                    for b, n in enumerate(lens)]
+            at = [slot(b, torch.arange(n)) for b, n in enumerate(lens)]
+            scl = [to_np(cache["scale"])[a // page, 1, :, a % page] for a in at]
+            check_decode(out, to_np(Q), lens, [to_np(r["K"]) for r in rows], [to_np(r["V"]) for r in rows], scl, n_q, n_kv,
+                         D ** -0.5)
+            check_rest(y, x, out["O"], f"decode {step}")
+    finally:
+        for name, real in originals.items():
+            setattr(B, name, real)
