@@ -341,14 +341,13 @@ int coda_kv_append_nvfp4(const coda_bf16* K, int64_t ldk, const coda_bf16* V, in
   if (T < 0) return CODA_ERR_INVALID_ARG;
   coda::KvCache c{};
   CK(check_cache(c, codes, sf, scale, num_pages, page_size, n_kv, head_dim));
+  if (T >= (int64_t(1) << 30) / n_kv) return CODA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
   if (T == 0) return CODA_OK;
   if (!K || !V || !slots || ldk < int64_t(n_kv) * head_dim || ldv < int64_t(n_kv) * head_dim)
     return CODA_ERR_INVALID_ARG;
   if (!al16(K) || !al16(V) || !al4(slots) || ldk % 8 || ldv % 8) return CODA_ERR_ALIGNMENT;
   CK(check_ws(ws, ws_bytes, HEADER));
-  const int sms = coda::device_sms();
-  if (sms <= 0) return CODA_ERR_CUDA;
-  CU(coda::launch_kv_append(c, B(K), ldk, B(V), ldv, slots, T, static_cast<int*>(ws), sms,
+  CU(coda::launch_kv_append(c, B(K), ldk, B(V), ldv, slots, static_cast<int>(T * 2 * n_kv), static_cast<int*>(ws),
                             static_cast<cudaStream_t>(stream)));
   return CODA_OK;
 }
@@ -359,13 +358,12 @@ int coda_kv_read_nvfp4(const uint8_t* codes, const uint8_t* sf, const float* sca
   if (T < 0 || (dtype != CODA_BF16 && dtype != CODA_F32)) return CODA_ERR_INVALID_ARG;
   coda::KvCache c{};
   CK(check_cache(c, codes, sf, scale, num_pages, page_size, n_kv, head_dim));
+  if (T >= (int64_t(1) << 30) / n_kv) return CODA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
   if (T == 0) return CODA_OK;
   if (!K || !V || !slots) return CODA_ERR_INVALID_ARG;
   if (!al16(K) || !al16(V) || !al4(slots)) return CODA_ERR_ALIGNMENT;
   CK(check_ws(ws, ws_bytes, HEADER));
-  const int sms = coda::device_sms();
-  if (sms <= 0) return CODA_ERR_CUDA;
-  CU(coda::launch_kv_read(c, slots, T, K, V, dtype == CODA_F32, static_cast<int*>(ws), sms,
+  CU(coda::launch_kv_read(c, slots, static_cast<int>(T * 2 * n_kv), K, V, dtype == CODA_F32, static_cast<int*>(ws),
                           static_cast<cudaStream_t>(stream)));
   return CODA_OK;
 }

@@ -21,11 +21,12 @@ struct KvCache {
   int n_kv;
 };
 
+// rows: 2 * n_kv per token.
 cudaError_t launch_kv_append(const KvCache& c, const __nv_bfloat16* K, int64_t ldk, const __nv_bfloat16* V,
-                             int64_t ldv, const int32_t* slots, int64_t T, int* status, int sms, cudaStream_t s);
+                             int64_t ldv, const int32_t* slots, int rows, int* status, cudaStream_t s);
 // f32: outputs are fp32, else bf16; both [T, n_kv * 128].
-cudaError_t launch_kv_read(const KvCache& c, const int32_t* slots, int64_t T, void* K, void* V, bool f32, int* status,
-                           int sms, cudaStream_t s);
+cudaError_t launch_kv_read(const KvCache& c, const int32_t* slots, int rows, void* K, void* V, bool f32, int* status,
+                           cudaStream_t s);
 
 constexpr int DEC_MAX_CTAS = 3 * 160;  // partial results reserved for this many CTAs
 constexpr int DEC_HEADS = 16;          // query heads of one pass over a key/value head's rows
