@@ -26,7 +26,8 @@ static_assert(sizeof(AttnTile) == 32, "two 16-byte loads");
 
 // Work lists in the caller's workspace, written by attn_plan_kernel before
 // the kernels that walk them.  counts[0]: entries of the query list;
-// counts[1]: entries of the key list.
+// counts[1]: entries of the key list; counts[2]: parts that the query heads of
+// a group are cut into for the key list's items (see attn_plan_kernel).
 struct AttnPlan {
   int* counts;
   AttnTile* q_tiles;
@@ -42,6 +43,9 @@ struct AttnPlanArgs {
   int* prefix_q;     // [n_seq + 1] scratch
   int* prefix_k;
   AttnPlan plan;
+  int n_kv, group;   // key list: heads
+  int max_parts;     // key list: bound on entries * n_kv * parts (0: never cut)
+  int sms;
   int* status;
 };
 // Programmatic dependent launch of the attention kernels (CODA_PDL=0: off).
@@ -83,8 +87,8 @@ struct AttnBwdArgs {
   __nv_bfloat16* dV;
   int64_t Tq, Tk, Tp;
   int n_q, n_kv, group;
-  int splits;              // parts a group's heads are cut into for dK, dV (divides group)
-  float* part;             // splits > 1: [key tile, n_kv, splits, 2, 32, 128, 4] partial dV | dK
+  float* part;             // [key tile, n_kv, part, 2, 32, 128, 4] partial dV | dK when a group is cut; null: never
+  int max_parts;
   float scale_log2, scale;
   int* status;
   uint64_t timeout_ns;

@@ -92,7 +92,7 @@ struct PlanLayout {
 void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, int q_span, bool keys) {
   l.max_q_tiles = Tq / q_span + n_seq;
   l.max_k_tiles = keys ? Tk / coda::ATTN_BLK + n_seq : 0;
-  l.a.plan.counts = c.take<int>(2);
+  l.a.plan.counts = c.take<int>(3);
   l.a.prefix_q = c.take<int>(n_seq + 1);
   l.a.prefix_k = keys ? c.take<int>(n_seq + 1) : nullptr;
   l.a.plan.q_tiles = c.take<coda::AttnTile>(l.max_q_tiles);
@@ -103,33 +103,14 @@ void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, i
 // Padded rows of the backward's per-row values (see AttnBwdArgs).
 int64_t padded_rows(int64_t Tq, int64_t n_seq) { return (Tq / coda::ATTN_BLK + n_seq + 1) * coda::ATTN_BLK; }
 
-// Parts a group's heads are cut into for dK and dV (a divisor of the group).
-// An item of the key-tile kernel meets all query tiles of its part's heads, so
-// with few key tiles the longest item (whole group, whole sequence) runs on
-// while most SMs are idle; each part costs a write and a read of 128 KB.  The
-// choice minimises that kernel's estimated time for sequences of the mean
-// length: ITER us per block pair of the longest item or of an SM's share,
-// JOIN us for the joining kernel and PART us for each part.
-int bwd_splits(int64_t Tk, int64_t n_seq, int group, int n_kv) {
-  constexpr double SMS = 152, ITER = 1.1, JOIN = 3, PART = 0.06;
-  if (Tk == 0 || n_seq == 0) return 1;
-  const double blocks = std::ceil(std::ceil(double(Tk) / n_seq) / coda::ATTN_BLK);
-  const double items = blocks * n_seq * n_kv, pairs = items * group * (blocks + 1) / 2;
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= group; ++s) {
-    if (group % s) continue;
-    const double t = ITER * std::max(group / s * blocks, pairs / SMS) + (s > 1 ? JOIN + PART * items * s : 0);
-    if (s == 1 || t < least) {
-      best = s;
-      least = t;
-    }
-  }
-  return best;
+// Bound on the parts (of 128 KB) that the backward's key-tile items may be cut
+// into: 0 where the tiles alone already occupy the SMs more than once.
+int bwd_max_parts(int64_t Tk, int64_t n_seq, int n_q, int n_kv) {
+  constexpr int64_t PARTS = 512;
+  const int64_t least = Tk / coda::ATTN_BLK * n_kv, most = (Tk / coda::ATTN_BLK + n_seq) * n_kv * (n_q / n_kv);
+  return n_q == n_kv || least * 2 > PARTS ? 0 : static_cast<int>(std::min(PARTS, most));
 }
-int64_t bwd_part_floats(int64_t key_tiles, int splits, int n_kv) {
-  return splits == 1 ? 0 : key_tiles * n_kv * splits * 2 * coda::ATTN_BLK * coda::ATTN_D;
-}
+constexpr int64_t PART_FLOATS = 2 * coda::ATTN_BLK * coda::ATTN_D;
 
 bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
@@ -267,7 +248,7 @@ size_t coda_attention_bwd_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, 
   PlanLayout l{};
   lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true);
   c.take<float>(2 * n_q * padded_rows(Tq, n_seq));
-  c.take<float>(bwd_part_floats(l.max_k_tiles, bwd_splits(Tk, n_seq, n_q / n_kv, n_kv), n_kv));
+  c.take<float>(bwd_max_parts(Tk, n_seq, n_q, n_kv) * PART_FLOATS);
   return c.off;
 }
 
@@ -304,8 +285,12 @@ int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, con
   a.Tp = padded_rows(Tq, n_seq);
   a.nlse2 = c.take<float>(2 * n_q * a.Tp);
   a.ndelta = a.nlse2 + n_q * a.Tp;
-  a.splits = bwd_splits(Tk, n_seq, n_q / n_kv, n_kv);
-  a.part = c.take<float>(bwd_part_floats(l.max_k_tiles, a.splits, n_kv));
+  a.max_parts = bwd_max_parts(Tk, n_seq, n_q, n_kv);
+  a.part = c.take<float>(a.max_parts * PART_FLOATS);
+  l.a.n_kv = n_kv;
+  l.a.group = n_q / n_kv;
+  l.a.max_parts = a.max_parts;
+  l.a.sms = sms;
   a.counts = l.a.plan.counts;
   a.q_tiles = l.a.plan.q_tiles;
   a.k_tiles = l.a.plan.k_tiles;

@@ -16,7 +16,7 @@
 //
 // Few or short sequences give few key tiles, and one item of the key-tile
 // kernel holds all query heads of its group.  Then the group is cut into
-// parts (`splits`), whose fp32 partial dK and dV a third kernel adds in fixed
+// parts, whose fp32 partial dK and dV a third kernel adds in fixed
 // order.
 //
 // Roundings: P and dS to bf16 before their products; dQ, dK, dV to bf16 once.
@@ -136,13 +136,13 @@ struct KvItem {
   int kv, first, n;  // first query tile, query tiles
   int h0, nh;        // query heads
 };
-__device__ __forceinline__ KvItem kv_item(const AttnBwdArgs& a, int w) {
+__device__ __forceinline__ KvItem kv_item(const AttnBwdArgs& a, int w, int splits) {
   KvItem it;
-  const int per = a.n_kv * a.splits;
+  const int per = a.n_kv * splits;
   const int ti = w / per, rest = w - ti * per;
-  it.kv = rest / a.splits;
-  it.nh = a.group / a.splits;
-  it.h0 = it.kv * a.group + (rest - it.kv * a.splits) * it.nh;
+  it.kv = rest / splits;
+  it.nh = a.group / splits;
+  it.h0 = it.kv * a.group + (rest - it.kv * splits) * it.nh;
   it.t = load_tile(a.k_tiles + ti);
   it.first = max(0, it.t.t0 - (it.t.lk - it.t.lq)) / ATTN_BLK;
   it.n = max(0, (it.t.lq + ATTN_BLK - 1) / ATTN_BLK - it.first);
@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 384;
   griddep_wait();
   griddep_launch_dependents();
-  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv * a.splits;
+  const int splits = reinterpret_cast<const volatile int*>(a.counts)[2];
+  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv * splits;
   const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
   Waiter wait{abort_flag, a.status, a.timeout_ns};
 
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         ++pos;
       };
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
-        const KvItem it = kv_item(a, w);
+        const KvItem it = kv_item(a, w, splits);
         if (it.n == 0) continue;
         if (!wait(kv_empty, (kvn & 1) ^ 1)) break;
         ++kvn;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
       // ---------------------------------------------------------- rows behind the sequence
       uint32_t pos = 0, seen = 0;
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
-        const KvItem it = kv_item(a, w);
+        const KvItem it = kv_item(a, w, splits);
         const int last = (it.first + it.n - 1) * ATTN_BLK;
         for (int h = 0; h < it.nh && it.n > 0 && wait.ok; ++h) {
           pos += 2 * it.n;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         return ok;
       };
       for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
-        const KvItem it = kv_item(a, w);
+        const KvItem it = kv_item(a, w, splits);
         if (it.n == 0) continue;
         const int n = it.n * it.nh;
         if (!wait(kv_full, kvn & 1)) break;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
     uint32_t iter = 0, done = 0;
     for (int k = 0, w = first; w < items && wait.ok; w = snake_item(first, step, ++k)) {
-      const KvItem it = kv_item(a, w);
+      const KvItem it = kv_item(a, w, splits);
       const int off = it.t.lk - it.t.lq;
       for (int h = 0; h < it.nh && wait.ok; ++h) {
         for (int j = 0; j < it.n; ++j, ++iter) {
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         ++done;
         tc_fence_after();
       }
-      if (a.splits > 1) {
+      if (splits > 1) {
         // column by column of four, rows side by side
         float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(w) * 2 + half) * ATTN_BLK * ATTN_D) + r;
 #pragma unroll 1
@@ -465,31 +466,34 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 }
 
 // Adds the parts of a key tile's dV and dK: a thread takes one row and eight
-// columns, a block 256 of the 2 * 2048 such pieces of a (key tile, head), so
-// the loads of all parts are in flight at once.
+// columns, a block 256 of the 2 * 2048 such pieces of a (key tile, head) at a
+// time, so the loads of all parts are in flight at once.
 __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const AttnBwdArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int tiles = reinterpret_cast<const volatile int*>(a.counts)[1];
-  const int which = (blockIdx.x >> 3) & 1;  // 0: dV
-  const int64_t at = blockIdx.x >> 4;       // key tile, head
-  const int ti = static_cast<int>(at / a.n_kv), kv = static_cast<int>(at - static_cast<int64_t>(ti) * a.n_kv);
-  if (ti >= tiles) return;
-  const AttnTile t = load_tile(a.k_tiles + ti);
-  const int u = (blockIdx.x & 7) * 256 + static_cast<int>(threadIdx.x);
-  const int row = u & (ATTN_BLK - 1), c8 = u >> 7;
-  if (t.t0 + row >= t.lk) return;
-  const float4* src = reinterpret_cast<const float4*>(a.part + (at * a.splits * 2 + which) * ATTN_BLK * ATTN_D) +
-                      2 * c8 * ATTN_BLK + row;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int splits = reinterpret_cast<const volatile int*>(a.counts)[2];
+  if (splits == 1) return;  // nothing was cut
+  for (int w = blockIdx.x; w < tiles * a.n_kv * 16; w += gridDim.x) {
+    const int which = (w >> 3) & 1;  // 0: dV
+    const int64_t at = w >> 4;       // key tile, head
+    const int ti = static_cast<int>(at / a.n_kv), kv = static_cast<int>(at - static_cast<int64_t>(ti) * a.n_kv);
+    const AttnTile t = load_tile(a.k_tiles + ti);
+    const int u = (w & 7) * 256 + static_cast<int>(threadIdx.x);
+    const int row = u & (ATTN_BLK - 1), c8 = u >> 7;
+    if (t.t0 + row >= t.lk) continue;
+    const float4* src = reinterpret_cast<const float4*>(a.part + (at * splits * 2 + which) * ATTN_BLK * ATTN_D) +
+                        2 * c8 * ATTN_BLK + row;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int p = 0; p < a.splits; ++p) {
-    const float4* s = src + static_cast<int64_t>(p) * 2 * ATTN_BLK * ATTN_D / 4;
-    const float4 x = s[0], y = s[ATTN_BLK];
-    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    for (int p = 0; p < splits; ++p) {
+      const float4* s = src + static_cast<int64_t>(p) * 2 * ATTN_BLK * ATTN_D / 4;
+      const float4 x = s[0], y = s[ATTN_BLK];
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    store_bf16x8((which ? a.dK : a.dV) + ((static_cast<int64_t>(t.k0) + t.t0 + row) * a.n_kv + kv) * ATTN_D + c8 * 8, v);
   }
-  store_bf16x8((which ? a.dK : a.dV) + ((static_cast<int64_t>(t.k0) + t.t0 + row) * a.n_kv + kv) * ATTN_D + c8 * 8, v);
 }
 
 // ------------------------------------------------------------------ dQ
@@ -920,10 +924,10 @@ cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64
     if (e != cudaSuccess) return e;
   }
   if (max_k_tiles == 0) return cudaSuccess;
-  e = launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv * a.splits), BWD_THREADS, KV_SMEM, s, maps[0],
-             maps[1], maps[2], maps[3], a);
-  if (e != cudaSuccess || a.splits == 1) return e;
-  return launch(attn_bwd_join_kernel, max_k_tiles * a.n_kv * 16, 256, 0, s, a);
+  e = launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv * (a.max_parts ? a.group : 1)), BWD_THREADS,
+             KV_SMEM, s, maps[0], maps[1], maps[2], maps[3], a);
+  if (e != cudaSuccess || a.max_parts == 0) return e;
+  return launch(attn_bwd_join_kernel, std::min<int64_t>(max_k_tiles * a.n_kv * 16, 8 * sms), 256, 0, s, a);
 }
 
 }  // namespace coda

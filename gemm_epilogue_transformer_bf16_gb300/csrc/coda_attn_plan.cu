@@ -50,7 +50,7 @@ struct Side {
 };
 
 // Entry t of a list and its bin (longest first).
-__device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side& sd, int t, int shift, int& bin) {
+__device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side& sd, int t, int shift, int& bin, int& w) {
   int lo = 0, hi = a.n_seq;  // prefix[lo] <= t < prefix[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -64,7 +64,6 @@ __device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side
   e.t0 = (t - sd.prefix[lo]) * sd.span;
   e.seq = lo;
   e.pad1 = e.pad2 = 0;
-  int w;
   if (sd.keys) {
     const int first = max(0, e.t0 - (e.lk - e.lq)) / ATTN_BLK;  // first query block that sees the run
     w = max(0, (e.lq + ATTN_BLK - 1) / ATTN_BLK - first);
@@ -80,7 +79,8 @@ __device__ __forceinline__ void put_entry(AttnTile* out, const AttnTile& e) {
   o[1] = make_int4(e.t0, e.seq, 0, 0);
 }
 
-__device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int* warp_sums) {
+// weights (key list): each warp's largest and total weight of its entries.
+__device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int* warp_sums, float2* weights) {
   const int32_t* cu = sd.keys ? sd.cu_k : sd.cu_q;
   const int64_t other = (sd.keys ? a.Tq : a.Tk) / ATTN_BLK + 2;
   int shift = 0;  // weights beyond the bins share bins
@@ -101,15 +101,27 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
   // counts per bin -> first positions -> entries.  A thread's first entry
   // stays in registers between the two passes.
   const int t0 = static_cast<int>(threadIdx.x);
-  int bin0 = 0, bin;
+  int bin0 = 0, bin, w, top = 0;
+  float sum = 0.f;
   AttnTile e0;
   if (t0 < total) {
-    e0 = make_entry(a, sd, t0, shift, bin0);
+    e0 = make_entry(a, sd, t0, shift, bin0, top);
+    sum = static_cast<float>(top);
     atomicAdd(&hist[bin0], 1);
   }
   for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
-    make_entry(a, sd, t, shift, bin);
+    make_entry(a, sd, t, shift, bin, w);
+    top = max(top, w);
+    sum += static_cast<float>(w);
     atomicAdd(&hist[bin], 1);
+  }
+  if (sd.keys) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if ((threadIdx.x & 31) == 0) weights[threadIdx.x >> 5] = make_float2(static_cast<float>(top), sum);
   }
   __syncthreads();
   const int i = 2 * t0, c0 = hist[i], c1 = hist[i + 1];
@@ -119,7 +131,7 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
   __syncthreads();
   if (t0 < total) put_entry(sd.out + atomicAdd(&hist[bin0], 1), e0);
   for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
-    const AttnTile e = make_entry(a, sd, t, shift, bin);
+    const AttnTile e = make_entry(a, sd, t, shift, bin, w);
     put_entry(sd.out + atomicAdd(&hist[bin], 1), e);
   }
   if (threadIdx.x == 0) *sd.count = total;
@@ -132,6 +144,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
   __shared__ int32_t small_q[PLAN_SMALL + 1], small_k[PLAN_SMALL + 1];
   __shared__ int small_prefix[PLAN_SMALL + 1];
   __shared__ int bad;
+  __shared__ float2 weights[PLAN_THREADS / 32];
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
   griddep_wait();
@@ -158,16 +171,57 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
       atomicOr(a.status, CODA_DEV_SEQLEN_RANGE);
       a.plan.counts[0] = 0;
       a.plan.counts[1] = 0;
+      a.plan.counts[2] = 1;
     }
     return;
   }
   const int32_t* cq = small ? small_q : a.cu_q;
   const int32_t* ck = small ? small_k : a.cu_k;
   build_side(a, Side{cq, ck, a.q_span, small ? small_prefix : a.prefix_q, a.plan.q_tiles, a.plan.counts, false}, hist,
-             warp_sums);
-  if (a.plan.k_tiles)
-    build_side(a, Side{cq, ck, ATTN_BLK, small ? small_prefix : a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true},
-               hist, warp_sums);
+             warp_sums, weights);
+  if (!a.plan.k_tiles) return;
+  build_side(a, Side{cq, ck, ATTN_BLK, small ? small_prefix : a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true}, hist,
+             warp_sums, weights);
+  // Parts of a group (a divisor of it).  An item of the key list meets all
+  // query tiles of its part's heads, so with few key tiles the longest item
+  // (whole group, whole sequence) runs on while most SMs are idle; each part
+  // costs a write and a read of 128 KB.  The choice minimises the kernel's
+  // estimated time: ITER us per block pair of the longest item or of an SM's
+  // share, JOIN us for the joining kernel, PART us for each part (one sequence
+  // of 1024 tokens, 64 + 8 heads: 135 -> 82 us with four parts).  One warp
+  // looks at a divisor per lane.
+  if (threadIdx.x >= 32) return;
+  constexpr float ITER = 1.2f, JOIN = 3.f, PART = 0.06f;
+  const float heads = static_cast<float>(a.plan.counts[1]) * a.n_kv;  // items of whole groups
+  float longest = weights[threadIdx.x].x, pairs = weights[threadIdx.x].y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+  }
+  const float share = pairs * a.n_kv * a.group / a.sms;
+  int best = 1;
+  float least = ITER * fmaxf(static_cast<float>(a.group) * longest, share);
+  if (a.max_parts > 0) {
+    for (int s = 2 + static_cast<int>(threadIdx.x); s <= a.group; s += 32) {
+      if (heads * s > a.max_parts || a.group % s) continue;
+      const float t = ITER * fmaxf(static_cast<float>(a.group / s) * longest, share) + JOIN + PART * heads * s;
+      if (t < least) {
+        best = s;
+        least = t;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, least, o);
+      const int s = __shfl_xor_sync(0xffffffffu, best, o);
+      if (t < least || (t == least && s < best)) {
+        best = s;
+        least = t;
+      }
+    }
+  }
+  if (threadIdx.x == 0) a.plan.counts[2] = best;
 }
 
 }  // namespace
