@@ -202,6 +202,11 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Keeps the code of a rare, warp-uniform case behind a branch: without it the
+// compiler turns the masks of diagonal blocks into selects that every block
+// executes.
+__device__ __forceinline__ void keep_branch() { asm volatile("" ::: "memory"); }
+
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

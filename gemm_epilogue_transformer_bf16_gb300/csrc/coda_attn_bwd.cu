@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             }
           }
           if (diag) {
+            keep_branch();
 #pragma unroll
             for (int i = 0; i < 64; ++i) p[i] = i >= from ? p[i] : 0.f;
           }
@@ -844,6 +845,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(dp_read);
           if (it.n == 1) {
+            keep_branch();
             float t[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 64; ++i) t[i & 1] += i < lim ? p[i] * __uint_as_float(d[i]) : 0.f;
@@ -855,6 +857,15 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             nd = seen ? -(row_x[r] + row_x[ATTN_BLK + r]) : 0.f;
             if (half == 0) a.ndelta[pr] = nd;
           }
+          if (diag) {
+            // masked keys: weight 0 and a dP that cannot make it NaN
+            keep_branch();
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              p[i] = i < lim ? p[i] : 0.f;
+              d[i] = i < lim ? d[i] : 0u;
+            }
+          }
           const uint64_t nd2 = f2_pack(nd, nd);
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
@@ -862,10 +873,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             f2_unpack(f2_mul(f2_pack(p[i], p[i + 1]),
                              f2_add(f2_pack(__uint_as_float(d[i]), __uint_as_float(d[i + 1])), nd2)),
                       e0, e1);
-            if (diag) {
-              e0 = i < lim ? e0 : 0.f;
-              e1 = i + 1 < lim ? e1 : 0.f;
-            }
             u[i / 2] = pack_bf16x2(e0, e1);
           }
         }

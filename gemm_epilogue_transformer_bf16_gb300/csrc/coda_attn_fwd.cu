@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         uint32_t s[128];
         tmem_ld128(tS, s);
         if ((j + 1) * ATTN_BLK > all) {
+          keep_branch();
           const int lim = vis - j * ATTN_BLK;
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i] = i < lim ? s[i] : 0xFF800000u;
