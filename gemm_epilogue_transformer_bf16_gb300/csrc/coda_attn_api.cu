@@ -379,7 +379,7 @@ int coda_attention_decode_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* 
   // key positions and work units are 32-bit on the device
   const int64_t longest = max_pages * page_size;
   if (max_pages >= (int64_t(1) << 31) || longest >= (int64_t(1) << 31) - 256 ||
-      batch * ((longest + 127) / 128) * n_kv * a.splits >= (int64_t(1) << 31) - 65536)
+      batch * ((longest + 383) / 128) * n_kv * a.splits >= (int64_t(1) << 31) - 65536)
     return CODA_ERR_UNSUPPORTED;
   CK(check_ws(ws, ws_bytes, coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, head_dim)));
   const int sms = coda::device_sms();

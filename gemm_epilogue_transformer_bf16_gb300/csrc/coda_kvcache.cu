@@ -184,9 +184,10 @@ __global__ void __launch_bounds__(256)
 //
 // Work: every (sequence, key/value head) is cut into units of 128 keys; the
 // units of the whole batch form one line that the CTAs divide evenly, so a
-// batch of mixed lengths, or one long sequence, keeps every SM busy.  A CTA
-// whose stretch covers a whole (sequence, head) writes the output itself;
-// the others leave normalised partial outputs, merged by a second kernel.
+// batch of mixed lengths, or one long sequence, keeps every SM busy.  Each
+// (sequence, head) has DEC_END places more on that line than it has units,
+// for the work at its end.  A CTA whose stretch covers a whole (sequence,
+// head) writes the output itself; the others leave normalised partial outputs, merged by a second kernel.
 //
 // A fifth warp copies units into a shared-memory ring by bulk copies (one per
 // page and array), ahead of the four that compute and across the ends of
@@ -198,7 +199,8 @@ __global__ void __launch_bounds__(256)
 //     with one scale each: the k index of the product is a permutation of
 //     the head's elements, the same for Q.
 //   O^T [16 elements x 8 heads] += V'^T P'^T with the row scale of V in
-//     P' = exp2(z - m) * rs * f, where f (per head) keeps P' <= 2^8: P' is
+//     P' = exp2(z - m) * rs * f, where f (per head) sets the largest P' to 1
+//     and is renewed before one would pass 2^14 (f16 ends at 2^16): P' is
 //     rounded to f16 (2^-11), O accumulates in fp32.
 // The keys of a tile are read in the order 0 4 1 5 2 6 3 7: then the lanes'
 // shared-memory reads of both K and V are contiguous, and movmatrix turns
@@ -242,25 +244,38 @@ __device__ __forceinline__ int decode_len(const DecodeArgs& a, int b, bool tell)
   return n;
 }
 
-// A CTA's way along the line of units: stretches of one (sequence, virtual
-// head).  Every warp walks it for itself.
+// Measured with 64 + 8 heads, 0 against 1, 2 and 3 places: 128 sequences of 1 to
+// 8192 keys 153, 137, 132 and 131 us; 512 of 512 keys with 64 of 4096 167, 164,
+// 158 and 166 us; 128 of 4096 keys 132, 135, 134 and 134 us.
+constexpr int DEC_END = 2;
+
+// Places on the line of units that each head of a sequence of `len` keys takes.
+__device__ __forceinline__ int decode_places(int len) { return len > 0 ? (len + DEC_UNIT - 1) / DEC_UNIT + DEC_END : 0; }
+
+// A CTA's way along the line: stretches of one (sequence, virtual head).
+// Every warp walks it for itself.
 struct Stretch {
-  int b, before;        // sequence, units before it
-  int u;                // next unit of the line
+  int b, before;        // sequence, places before it
+  int u;                // next place of the line
   // current stretch
-  int first, nu, stop;  // its first unit, its units, where this CTA stops in it
+  int first, nu, stop;  // the place of its first unit, its units, where this CTA stops in it
   int vh, len;
-  __device__ __forceinline__ void next(const DecodeArgs& a, int vheads, int last) {
+  // false: no unit before `last`
+  __device__ __forceinline__ bool next(const DecodeArgs& a, int vheads, int last) {
+    if (u >= last) return false;
     len = decode_len(a, b, false);
-    nu = (len + DEC_UNIT - 1) / DEC_UNIT;
-    while (u >= before + nu * vheads) {
-      before += nu * vheads;
+    int places = decode_places(len);
+    while (u >= before + places * vheads) {
+      before += places * vheads;
       len = decode_len(a, ++b, false);
-      nu = (len + DEC_UNIT - 1) / DEC_UNIT;
+      places = decode_places(len);
     }
-    vh = (u - before) / nu;
-    first = before + vh * nu;
+    vh = (u - before) / places;
+    nu = places - DEC_END;
+    first = before + vh * places + DEC_END;  // the places in front stand for its end
+    u = max(u, first);
     stop = min(last, first + nu);
+    return u < last;
   }
 };
 
@@ -288,12 +303,12 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
   griddep_wait();
   griddep_launch_dependents();
 
-  // units before each sequence: a contiguous run of sequences per thread,
+  // places before each sequence: a contiguous run of sequences per thread,
   // scanned over the block
   const int chunk = (a.B + DEC_THREADS - 1) / DEC_THREADS;
   const int s0 = min(a.B, tid * chunk), s1 = min(a.B, s0 + chunk);
   int mine = 0;
-  for (int b = s0; b < s1; ++b) mine += (decode_len(a, b, blockIdx.x == 0) + DEC_UNIT - 1) / DEC_UNIT * vheads;
+  for (int b = s0; b < s1; ++b) mine += decode_places(decode_len(a, b, blockIdx.x == 0)) * vheads;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
   {
     int before = incl - mine;
     for (int b = s0; b < s1; ++b) {
-      const int n = (decode_len(a, b, false) + DEC_UNIT - 1) / DEC_UNIT * vheads;
+      const int n = decode_places(decode_len(a, b, false)) * vheads;
       if (blockIdx.x == 0) a.units[b] = before;
       if (first >= before && first < before + n) {
         sh_seq = b;
@@ -348,8 +363,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
     const uint32_t to_k = arr == 0 ? ST_K : arr == 1 ? ST_SFK : ST_RSK, to_v = arr == 0 ? ST_V : arr == 1 ? ST_SFV : ST_RSV;
     const uint8_t* src = arr == 0 ? kc.codes : arr == 1 ? kc.sf : reinterpret_cast<const uint8_t*>(kc.scale);
     const int64_t plane = static_cast<int64_t>(kc.n_kv) << kc.page_shift;
-    while (x.u < last && ok) {
-      x.next(a, vheads, last);
+    while (ok && x.next(a, vheads, last)) {
       const int kvh = x.vh / a.splits;
       const int32_t* table = a.table + static_cast<int64_t>(x.b) * a.max_pages;
       auto page_of = [&](int u) {  // of this lane's part of unit u; -1: nothing there
@@ -404,8 +418,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
   const uint8_t* v_at = dec_smem + ST_V + (warp * 32 + c) * 64 + g * 8;
   const uint8_t* sfv_at = dec_smem + ST_SFV + (warp * 32 + c) * 8 + g;
   const uint8_t* rsv_at = dec_smem + ST_RSV + (warp * 32 + pi) * 4;
-  while (x.u < last) {
-    x.next(a, vheads, last);
+  while (x.next(a, vheads, last)) {
     const int u0 = x.u;
     const int kvh = x.vh / a.splits;
     const int head0 = kvh * a.group + (x.vh - kvh * a.splits) * DEC_HEADS;
@@ -529,7 +542,7 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
             rv[2 * h + 1] = in1 ? rv[2 * h + 1] : 0.f;
           }
         }
-        // raise m when a weight passes 2^8 of it
+        // raise m only when a weight passes 2^8: l and f have room, and rows that rise slowly rarely come here
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -748,16 +761,16 @@ __global__ void __launch_bounds__(256) attn_decode_join_kernel(const DecodeArgs 
   const int64_t at = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (at >= static_cast<int64_t>(a.B) * a.n_q) return;
   const int b = static_cast<int>(at / a.n_q), head = static_cast<int>(at - static_cast<int64_t>(b) * a.n_q);
-  const int before = a.units[b], nu = (a.units[b + 1] - before) / vheads, per = a.units[a.B + 1];
+  const int before = a.units[b], places = (a.units[b + 1] - before) / vheads, per = a.units[a.B + 1];
   uint2* out = reinterpret_cast<uint2*>(a.O + at * 128 + lane * 4);
-  if (nu == 0) {
+  if (places == 0) {
     *out = make_uint2(0, 0);
     if (lane == 0) a.lse[at] = -INFINITY;
     return;
   }
   const int kvh = head / a.group, in = head - kvh * a.group;
   const int vh = kvh * a.splits + in / DEC_HEADS, h = in % DEC_HEADS;
-  const int u0 = before + vh * nu, u1 = u0 + nu - 1;
+  const int u0 = before + vh * places + DEC_END, u1 = before + (vh + 1) * places - 1;  // places of its units
   const int c0 = u0 / per, c1 = u1 / per;
   if (c0 == c1) return;  // the stretch's CTA wrote the output
   float W = -INFINITY;

@@ -42,7 +42,7 @@ struct DecodeArgs {
   float scale_log2;
   __nv_bfloat16* O;  // [B, n_q * 128]
   float* lse;        // [B, n_q]
-  int* units;        // [B + 2]: 128-key units before each sequence, their total, units per CTA
+  int* units;        // [B + 2]: places on the line of units before each sequence, their total, places per CTA
   float* part;       // [2 * DEC_MAX_CTAS, heads, 128] normalised partial outputs
   float* part_lse;   // [2 * DEC_MAX_CTAS, heads] log2 domain
   int part_heads;    // min(group, DEC_HEADS)

@@ -19,7 +19,8 @@
  *    take a caller-allocated workspace `ws` of at least the size returned by
  *    the matching *_workspace_size() query; its first 256 bytes hold the
  *    device status word (zero it once, e.g. with coda_reset_status, before
- *    first use).
+ *    first use).  Calls that may run at the same time (other streams, graphs
+ *    replayed side by side) need a workspace each.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *    default stream).  They return after enqueueing.  A GEMM may run part of
  *    its tiles on a second, library-created non-blocking stream (one per

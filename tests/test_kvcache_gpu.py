@@ -10,9 +10,9 @@ Tolerances of the attention, from the kernel's roundings:
           2^-24 of the score each:
             e = scale (128 2^-24 sum|q k| + 128 2^-25 max|q| max|k|) + 2^-22 |s|
   O       weights times row scales are rounded to f16: half a step is 2^-11
-          relative, or 2^-25 of at least the largest weighted row scale
-          (the kernel keeps that between 1 and 2^8 units), times values of at
-          most 2688; O is rounded to bf16 once (2^-8); a weight moves by
+          relative, or 2^-25 units where the largest weighted row scale is
+          at least one unit (the kernel keeps it between 1 and 2^14), times
+          values of at most 2688; O is rounded to bf16 once (2^-8); a weight moves by
           exp(+-2e); the sums over n keys add n 2^-24 each.
   lse     off by e, n 2^-24, and 2^-22 (|lse| + 16) for the fp32 logarithms
           and products.
@@ -180,6 +180,7 @@ CASES = {
     "flat": ([700, 90], 64, 8, 2, True, 0.0),
     "tiny_q": ([300], 64, 4, 1, False, 2.0 ** -40),
     "many": (list(range(1, 60)), 16, 8, 8, False, 1.0),
+    "more_than_threads": ([(7 * i) % 41 for i in range(400)], 16, 2, 1, True, 1.0),
 }
 
 
@@ -273,3 +274,44 @@ def test_binding_refuses_shapes(coda):
     with pytest.raises(coda.CodaError):                 # 5 query heads over 2 key/value heads
         coda.attention_decode_nvfp4(torch.zeros(3, 5 * D, dtype=torch.bfloat16, device=DEV), cache,
                                     torch.zeros(3, 2, dtype=torch.int32, device=DEV), slots, 5)
+
+
+def test_decode_in_a_graph_and_on_two_streams(coda):
+    """A captured append and decode reads the lengths and pages of its replay;
+    two streams with a workspace each give the bits of one; sequences may share
+    pages."""
+    lens, page, n_q, n_kv = [300, 41, 1000], 64, 8, 2
+    cache, table, *_ = fill(coda, lens, page, n_kv, True)
+    table[1, 0] = table[0, 0]                            # a shared first page
+    tab, n = table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    Q = synth.randn_bf16((3, n_q * D), 1.0, 5).to(DEV)
+    K, V = rows(1, n_kv, 21).to(DEV), rows(1, n_kv, 22).to(DEV)
+    slot = (tab[0, 4] * page + 44).reshape(1).to(torch.int32)      # sequence 0's token 300
+    size = coda.load().coda_attention_decode_nvfp4_workspace_size(3, n_q, n_kv, D)
+    ws = [coda.workspace(size) for _ in range(2)]
+    before = coda.attention_decode_nvfp4(Q, cache, tab, n, n_q, ws=ws[0])
+    out = {k: torch.zeros_like(v) for k, v in before.items()}
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=cap):
+        coda.kv_append_nvfp4(K, V, slot, cache, ws=ws[0])
+        coda.attention_decode_nvfp4(Q, cache, tab, n, n_q, out=out, ws=ws[0])
+    g.replay()                                           # the token is there, the lengths do not name it
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[k], before[k]) for k in out)
+    n[0] += 1
+    g.replay()
+    torch.cuda.synchronize()
+    after = coda.attention_decode_nvfp4(Q, cache, tab, n, n_q, ws=ws[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(out[k], after[k]) for k in out) and not torch.equal(after["O"][0], before["O"][0])
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[coda.attention_decode_nvfp4(Q, cache, tab, n, n_q, ws=w, stream=s) for w, s in zip(ws, side)]
+           for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for one in pair:
+            assert all(torch.equal(one[k], after[k]) for k in after)
+    assert coda.get_status(ws[0]) == 0 and coda.get_status(ws[1]) == 0
