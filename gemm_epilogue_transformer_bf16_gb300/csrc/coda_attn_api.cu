@@ -69,7 +69,7 @@ int check_shape(int64_t Tq, int64_t Tk, int64_t n_seq, int32_t n_q, int32_t n_kv
   // rows and work items are counted in 32 bits on the device
   constexpr int64_t LIM = int64_t(1) << 30;
   if (Tq >= LIM || Tk >= LIM || n_seq >= LIM / 4 || n_q >= 65536) return CODA_ERR_UNSUPPORTED;
-  if ((Tq / 32 + n_seq + 1) * n_q >= (int64_t(1) << 31)) return CODA_ERR_UNSUPPORTED;
+  if ((std::max(Tq / 32, Tk / coda::ATTN_BLK) + n_seq + 1) * n_q >= (int64_t(1) << 31)) return CODA_ERR_UNSUPPORTED;
   return CODA_OK;
 }
 

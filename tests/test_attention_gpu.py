@@ -98,6 +98,9 @@ CASES = {
     "prefix_short": ([1, 1, 2, 3], [129, 1, 64, 700], 16, 2, 0, 0),
     "rows_without_keys": ([300, 5, 9, 4], [100, 0, 9, 3], 4, 4, 0, 3),
     "long": ([2500], None, 4, 2, 0, 0),
+    # more sequences, and more runs of rows, than the list builder's block has threads
+    "many_sequences": ([(7 * i) % 5 for i in range(1500)], None, 2, 1, 1, 2),
+    "many_prefixes": ([(3 * i) % 4 for i in range(1100)], [(5 * i) % 7 for i in range(1100)], 1, 1, 0, 0),
 }
 
 

@@ -40,6 +40,18 @@ def test_forward_refusals(lib, change, code):
     assert fwd(lib, **change) == code
 
 
+@pytest.mark.parametrize("call", ["forward", "backward"])
+def test_key_tiles_are_counted_too(lib, call):
+    """Few queries over many keys: the key tiles times the heads must fit 32
+    bits as the query tiles do."""
+    Tq, Tk, n_q = 64, (1 << 30) - 1, 65535
+    if call == "forward":
+        assert fwd(lib, Tq=Tq, Tk=Tk, cu_k=2 * FAKE, n_q=n_q, n_kv=1, ldq=n_q * 128) == 3
+    else:
+        assert lib.coda_attention_bwd(FAKE, FAKE, n_q * 128, FAKE, 128, FAKE, 128, FAKE, FAKE, FAKE, 2 * FAKE, 2, n_q, 1,
+                                      128, 0.1, FAKE, FAKE, FAKE, Tq, Tk, FAKE, 1 << 60, None) == 3
+
+
 def test_workspace_grows_with_rows_and_sequences(lib):
     w = lib.coda_attention_workspace_size
     assert w(8192, 8192, 4, 64, 8, 128) < 65536
