@@ -20,18 +20,21 @@ constexpr int ATTN_BLK = 128;  // keys per block, rows per tile
 // tensors; t0 is the run's first row within the sequence.
 struct AttnTile {
   int q0, lq, k0, lk;
-  int t0, seq, pad1, pad2;
+  int t0, seq;
+  int slot, pad;  // key list: number of the part among all parts of cut tiles; -1: the whole group
 };
 static_assert(sizeof(AttnTile) == 32, "two 16-byte loads");
 
 // Work lists in the caller's workspace, written by attn_plan_kernel before
 // the kernels that walk them.  counts[0]: entries of the query list;
 // counts[1]: entries of the key list; counts[2]: parts that the query heads of
-// a group are cut into for the key list's items (see attn_plan_kernel).
+// a group are cut into where they are cut; counts[3]: key tiles cut, whose
+// first parts stand in `cuts` (see attn_plan_kernel).
 struct AttnPlan {
   int* counts;
   AttnTile* q_tiles;
   AttnTile* k_tiles;  // null: no key list
+  AttnTile* cuts;
 };
 
 struct AttnPlanArgs {
@@ -44,7 +47,8 @@ struct AttnPlanArgs {
   int* prefix_k;
   AttnPlan plan;
   int n_kv, group;   // key list: heads
-  int max_parts;     // key list: bound on entries * n_kv * parts (0: never cut)
+  int max_parts;     // key list: bound on the parts of all key tiles and heads (0: never cut)
+  uint32_t divisors;  // bit s - 1: a group may be cut into s parts (2 <= s <= 32)
   int sms;
   int* status;
 };
@@ -79,6 +83,7 @@ struct AttnBwdArgs {
   const int* counts;
   const AttnTile* q_tiles;
   const AttnTile* k_tiles;
+  const AttnTile* cuts;
   const float* lse;         // [n_q, Tq]
   float* nlse2;             // [n_q, Tp]: -lse * log2(e); -inf where the row has no weight
   float* ndelta;            // [n_q, Tp]: -rowsum(dO * O)
@@ -87,7 +92,7 @@ struct AttnBwdArgs {
   __nv_bfloat16* dV;
   int64_t Tq, Tk, Tp;
   int n_q, n_kv, group;
-  float* part;             // [key tile, n_kv, part, 2, 32, 128, 4] partial dV | dK when a group is cut; null: never
+  float* part;             // [cut tile, n_kv, part, 2, 32, 128, 4] partial dV | dK
   int max_parts;
   float scale_log2, scale;
   int* status;
@@ -237,7 +242,7 @@ __device__ __forceinline__ AttnTile load_tile(const AttnTile* p) {
   const int4 b = __ldcg(reinterpret_cast<const int4*>(p) + 1);
   AttnTile t;
   t.q0 = a.x; t.lq = a.y; t.k0 = a.z; t.lk = a.w;
-  t.t0 = b.x; t.seq = b.y; t.pad1 = t.pad2 = 0;
+  t.t0 = b.x; t.seq = b.y; t.slot = b.z; t.pad = 0;
   return t;
 }
 

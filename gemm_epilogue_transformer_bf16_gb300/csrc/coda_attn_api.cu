@@ -89,14 +89,16 @@ struct PlanLayout {
   int64_t max_q_tiles, max_k_tiles;
 };
 
-void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, int q_span, bool keys) {
+// parts: room in the key list for cut tiles (see bwd_max_parts).
+void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, int q_span, bool keys, int64_t parts) {
   l.max_q_tiles = Tq / q_span + n_seq;
   l.max_k_tiles = keys ? Tk / coda::ATTN_BLK + n_seq : 0;
-  l.a.plan.counts = c.take<int>(3);
+  l.a.plan.counts = c.take<int>(4);
   l.a.prefix_q = c.take<int>(n_seq + 1);
   l.a.prefix_k = keys ? c.take<int>(n_seq + 1) : nullptr;
   l.a.plan.q_tiles = c.take<coda::AttnTile>(l.max_q_tiles);
-  l.a.plan.k_tiles = keys ? c.take<coda::AttnTile>(l.max_k_tiles) : nullptr;
+  l.a.plan.k_tiles = keys ? c.take<coda::AttnTile>(l.max_k_tiles + parts) : nullptr;
+  l.a.plan.cuts = keys ? c.take<coda::AttnTile>(parts) : nullptr;
   l.a.q_span = q_span;
 }
 
@@ -176,7 +178,7 @@ size_t coda_attention_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, int3
   Cursor c{nullptr};
   PlanLayout l{};
   // the shortest entry a call can take, so the size depends on the shape alone
-  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK >> head_shift(Tq, n_seq, n_q / n_kv), false);
+  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK >> head_shift(Tq, n_seq, n_q / n_kv), false, 0);
   return c.off;
 }
 
@@ -205,7 +207,7 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
   const int span = coda::ATTN_BLK >> hs;
   Cursor c{static_cast<uint8_t*>(ws)};
   PlanLayout l{};
-  lay_plan(c, l, Tq, Tk, n_seq, pair_heads ? span : 2 * span, false);
+  lay_plan(c, l, Tq, Tk, n_seq, pair_heads ? span : 2 * span, false, 0);
   l.a.cu_q = cu_q;
   l.a.cu_k = cu_k;
   l.a.n_seq = static_cast<int>(n_seq);
@@ -246,7 +248,7 @@ size_t coda_attention_bwd_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, 
   if (check_shape(Tq, Tk, n_seq, n_q, n_kv, head_dim, 1.f) != CODA_OK) return HEADER;
   Cursor c{nullptr};
   PlanLayout l{};
-  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true);
+  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true, bwd_max_parts(Tk, n_seq, n_q, n_kv) / n_kv);
   c.take<float>(2 * n_q * padded_rows(Tq, n_seq));
   c.take<float>(bwd_max_parts(Tk, n_seq, n_q, n_kv) * PART_FLOATS);
   return c.off;
@@ -274,7 +276,7 @@ int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   Cursor c{static_cast<uint8_t*>(ws)};
   PlanLayout l{};
-  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true);
+  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK, true, bwd_max_parts(Tk, n_seq, n_q, n_kv) / n_kv);
   l.a.cu_q = cu_q;
   l.a.cu_k = cu_k;
   l.a.n_seq = static_cast<int>(n_seq);
@@ -290,10 +292,13 @@ int coda_attention_bwd(const coda_bf16* dO, const coda_bf16* Q, int64_t ldq, con
   l.a.n_kv = n_kv;
   l.a.group = n_q / n_kv;
   l.a.max_parts = a.max_parts;
+  for (int p = 2; p <= std::min(l.a.group, 32); ++p)
+    if (l.a.group % p == 0) l.a.divisors |= 1u << (p - 1);
   l.a.sms = sms;
   a.counts = l.a.plan.counts;
   a.q_tiles = l.a.plan.q_tiles;
   a.k_tiles = l.a.plan.k_tiles;
+  a.cuts = l.a.plan.cuts;
   a.lse = lse;
   a.dQ = B(dQ);
   a.dK = B(dK);

@@ -14,10 +14,10 @@
 // The query-tile kernel runs first: it has the rows of dO at hand, forms D, and
 // leaves -lse * log2(e) and -D per row and head for the key-tile kernel.
 //
-// Few or short sequences give few key tiles, and one item of the key-tile
-// kernel holds all query heads of its group.  Then the group is cut into
-// parts, whose fp32 partial dK and dV a third kernel adds in fixed
-// order.
+// One item of the key-tile kernel holds all query heads of its group, so few
+// sequences, or one long one among short ones, give it items longer than an
+// SM's share.  Such tiles' groups are cut into parts, whose fp32 partial dK and
+// dV a third kernel adds in fixed order.
 //
 // Roundings: P and dS to bf16 before their products; dQ, dK, dV to bf16 once.
 // D = dO . O inherits O's rounding to bf16, which weighs where a row sees few
@@ -135,15 +135,26 @@ struct KvItem {
   AttnTile t;
   int kv, first, n;  // first query tile, query tiles
   int h0, nh;        // query heads
+  int64_t part;      // place of the partial results; -1: the whole group
 };
+// The entries of a cut tile stand together, and so do the parts of a head: in
+// the order of the items and in memory.
 __device__ __forceinline__ KvItem kv_item(const AttnBwdArgs& a, int w, int splits) {
   KvItem it;
-  const int per = a.n_kv * splits;
-  const int ti = w / per, rest = w - ti * per;
-  it.kv = rest / splits;
-  it.nh = a.group / splits;
-  it.h0 = it.kv * a.group + (rest - it.kv * splits) * it.nh;
+  const int ti = w / a.n_kv;
   it.t = load_tile(a.k_tiles + ti);
+  it.kv = w - ti * a.n_kv;
+  it.nh = a.group;
+  it.h0 = it.kv * a.group;
+  it.part = -1;
+  if (it.t.slot >= 0) {
+    const int rank = it.t.slot / splits;
+    const int rest = w - (ti - (it.t.slot - rank * splits)) * a.n_kv;
+    it.kv = rest / splits;
+    it.nh = a.group / splits;
+    it.h0 = it.kv * a.group + (rest - it.kv * splits) * it.nh;
+    it.part = static_cast<int64_t>(rank) * a.n_kv * splits + rest;
+  }
   it.first = max(0, it.t.t0 - (it.t.lk - it.t.lq)) / ATTN_BLK;
   it.n = max(0, (it.t.lq + ATTN_BLK - 1) / ATTN_BLK - it.first);
   return it;
@@ -215,7 +226,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   griddep_wait();
   griddep_launch_dependents();
   const int splits = reinterpret_cast<const volatile int*>(a.counts)[2];
-  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv * splits;
+  const int items = reinterpret_cast<const volatile int*>(a.counts)[1] * a.n_kv;
   const int step = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
   Waiter wait{abort_flag, a.status, a.timeout_ns};
 
@@ -426,9 +437,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         ++done;
         tc_fence_after();
       }
-      if (splits > 1) {
+      if (it.part >= 0) {
         // column by column of four, rows side by side
-        float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(w) * 2 + half) * ATTN_BLK * ATTN_D) + r;
+        float4* dst = reinterpret_cast<float4*>(a.part + (it.part * 2 + half) * ATTN_BLK * ATTN_D) + r;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float v[32];
@@ -472,19 +483,19 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const AttnBwdArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int tiles = reinterpret_cast<const volatile int*>(a.counts)[1];
   const int splits = reinterpret_cast<const volatile int*>(a.counts)[2];
-  if (splits == 1) return;  // nothing was cut
-  for (int w = blockIdx.x; w < tiles * a.n_kv * 16; w += gridDim.x) {
+  const int cuts = reinterpret_cast<const volatile int*>(a.counts)[3];
+  for (int w = blockIdx.x; w < cuts * a.n_kv * 16; w += gridDim.x) {
     const int which = (w >> 3) & 1;  // 0: dV
-    const int64_t at = w >> 4;       // key tile, head
-    const int ti = static_cast<int>(at / a.n_kv), kv = static_cast<int>(at - static_cast<int64_t>(ti) * a.n_kv);
-    const AttnTile t = load_tile(a.k_tiles + ti);
+    const int at = w >> 4;           // key tile, head
+    const int ti = at / a.n_kv, kv = at - ti * a.n_kv;
+    const AttnTile t = load_tile(a.cuts + ti);
     const int u = (w & 7) * 256 + static_cast<int>(threadIdx.x);
     const int row = u & (ATTN_BLK - 1), c8 = u >> 7;
     if (t.t0 + row >= t.lk) continue;
-    const float4* src = reinterpret_cast<const float4*>(a.part + (at * splits * 2 + which) * ATTN_BLK * ATTN_D) +
-                        2 * c8 * ATTN_BLK + row;
+    const int64_t part = static_cast<int64_t>(at) * splits;  // t.slot is ti * splits
+    const float4* src =
+        reinterpret_cast<const float4*>(a.part + (part * 2 + which) * ATTN_BLK * ATTN_D) + 2 * c8 * ATTN_BLK + row;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int p = 0; p < splits; ++p) {

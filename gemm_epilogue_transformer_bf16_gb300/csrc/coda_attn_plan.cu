@@ -1,8 +1,9 @@
 // Work lists of the attention kernels.  The sequence lengths live on the
-// device, so one small block cuts the sequences into runs of rows and orders
+// device, so one small block per list cuts the sequences into runs of rows and orders
 // the runs by the number of 128-key blocks (or query blocks) they meet,
 // longest first: the persistent kernels deal the list out round robin, and
-// the long runs must not start last.
+// the long runs must not start last.  The backward's key tiles may be cut by
+// query heads as well, where whole groups would make too long an item.
 #include "coda_attn.cuh"
 #include "coda_internal.h"
 #include "coda_status.h"
@@ -49,8 +50,8 @@ struct Side {
   bool keys;            // the list of key runs
 };
 
-// Entry t of a list and its bin (longest first).
-__device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side& sd, int t, int shift, int& bin, int& w) {
+// Run t of a list and the blocks it meets.
+__device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side& sd, int t, int& w) {
   int lo = 0, hi = a.n_seq;  // prefix[lo] <= t < prefix[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -63,28 +64,89 @@ __device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side
   e.lk = sd.cu_k[lo + 1] - e.k0;
   e.t0 = (t - sd.prefix[lo]) * sd.span;
   e.seq = lo;
-  e.pad1 = e.pad2 = 0;
+  e.slot = -1;
+  e.pad = 0;
   if (sd.keys) {
     const int first = max(0, e.t0 - (e.lk - e.lq)) / ATTN_BLK;  // first query block that sees the run
     w = max(0, (e.lq + ATTN_BLK - 1) / ATTN_BLK - first);
   } else {
     w = key_blocks(e, min(e.t0 + sd.span, e.lq) - 1);
   }
-  bin = PLAN_BINS - 1 - min(w >> shift, PLAN_BINS - 1);
   return e;
 }
 __device__ __forceinline__ void put_entry(AttnTile* out, const AttnTile& e) {
   int4* o = reinterpret_cast<int4*>(out);
   o[0] = make_int4(e.q0, e.lq, e.k0, e.lk);
-  o[1] = make_int4(e.t0, e.seq, 0, 0);
+  o[1] = make_int4(e.t0, e.seq, e.slot, 0);
 }
 
-// weights (key list): each warp's largest and total weight of its entries.
+// Longest first.
+__device__ __forceinline__ int bin_of(int64_t w, int shift) {
+  return PLAN_BINS - 1 - static_cast<int>(min(w >> shift, static_cast<int64_t>(PLAN_BINS - 1)));
+}
+__device__ __forceinline__ int bin_shift(int64_t most) {  // weights beyond the bins share bins
+  int shift = 0;
+  while ((most >> shift) >= PLAN_BINS) ++shift;
+  return shift;
+}
+// Counts per bin -> first positions.
+__device__ void scan_bins(int* hist, int* warp_sums) {
+  __syncthreads();
+  const int i = 2 * static_cast<int>(threadIdx.x), c0 = hist[i], c1 = hist[i + 1];
+  const int incl = block_scan(c0 + c1, warp_sums);
+  hist[i] = incl - c0 - c1;
+  hist[i + 1] = incl - c1;
+  __syncthreads();
+}
+
+// How the groups of the key list are cut: tiles that meet more than `above`
+// query blocks into `parts`; `cuts` of them.
+struct Cut {
+  int parts, above, cuts;
+};
+
+// An item of the key list meets all query tiles of its heads, so the longest
+// one (whole group, whole sequence) may run on while most SMs are idle; each
+// part costs a write and a read of 128 KB.  For each number of parts (a divisor
+// of the group) either all tiles are cut, or those longer than NEAR of an SM's
+// share or of the longest tile's part.  The choice minimises the kernels'
+// estimated time: ITER us per block pair of the longest item or of a share,
+// JOIN us for the joining kernel, PART us for each part, and MIXED on the pairs
+// where only some are cut (items of many heads and few blocks hold more of the
+// dearer blocks on the diagonal than the estimate says).
+// Backward in us, all tiles cut alike where room allows -> this rule: 12 + 4
+// heads, sequences of 1911, 700, 480, 255, 128, 33, 1: 88 -> 77; 28 + 4 heads,
+// 2000 and 20 of 150: 246 -> 182; 16 + 2 heads, 4000 and 100 of 30: 462 -> 267;
+// one of 1024, 64 + 8 heads: 82 either way, 135 without a cut.
+// longest, pairs: largest and total weight of the runs; count(w): runs above w.
+template <class F>
+__device__ Cut choose_cut(const AttnPlanArgs& a, int total, float longest, float pairs, F count) {
+  constexpr float ITER = 1.2f, JOIN = 3.f, PART = 0.04f, NEAR = 0.7f, MIXED = 1.12f;
+  const float share = pairs * a.n_kv * a.group / a.sms;
+  Cut best{1, 0, 0};
+  float least = ITER * fmaxf(a.group * longest, share);
+  for (uint32_t left = a.divisors; left; left &= left - 1) {
+    const int s = __ffs(left);  // bit s - 1: a divisor
+    const float time = fmaxf(a.group / s * longest, share);
+    const int some = static_cast<int>(NEAR * time / a.group);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int above = k == 0 ? -1 : some;
+      const int n = k == 0 ? total : count(above);
+      if (n == 0 || static_cast<int64_t>(n) * a.n_kv * s > a.max_parts) continue;
+      const float t = ITER * time * (k == 0 ? 1.f : MIXED) + JOIN + PART * static_cast<float>(n * a.n_kv * s);
+      if (t < least) {
+        best = Cut{s, above, n};
+        least = t;
+      }
+    }
+  }
+  return best;
+}
+
 __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int* warp_sums, float2* weights) {
   const int32_t* cu = sd.keys ? sd.cu_k : sd.cu_q;
-  const int64_t other = (sd.keys ? a.Tq : a.Tk) / ATTN_BLK + 2;
-  int shift = 0;  // weights beyond the bins share bins
-  while ((other >> shift) >= PLAN_BINS) ++shift;
+  const int64_t most = (sd.keys ? a.Tq : a.Tk) / ATTN_BLK + 2;
   for (int i = threadIdx.x; i < PLAN_BINS; i += PLAN_THREADS) hist[i] = 0;
   // runs before each sequence
   int total = 0;
@@ -98,43 +160,89 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
     __syncthreads();
     total = warp_sums[32];
   }
-  // counts per bin -> first positions -> entries.  A thread's first entry
-  // stays in registers between the two passes.
+  // A thread's first run stays in registers between the passes.
   const int t0 = static_cast<int>(threadIdx.x);
-  int bin0 = 0, bin, w, top = 0;
-  float sum = 0.f;
+  int w0 = 0, w;
   AttnTile e0;
-  if (t0 < total) {
-    e0 = make_entry(a, sd, t0, shift, bin0, top);
-    sum = static_cast<float>(top);
-    atomicAdd(&hist[bin0], 1);
-  }
-  for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
-    make_entry(a, sd, t, shift, bin, w);
-    top = max(top, w);
-    sum += static_cast<float>(w);
-    atomicAdd(&hist[bin], 1);
-  }
-  if (sd.keys) {
+  if (t0 < total) e0 = make_entry(a, sd, t0, w0);
+
+  const bool may_cut = sd.keys && a.max_parts > 0;
+  Cut cut{1, 0, 0};
+  if (may_cut) {
+    int top = w0;
+    float pairs = static_cast<float>(w0);
+    for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
+      make_entry(a, sd, t, w);
+      top = max(top, w);
+      pairs += static_cast<float>(w);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+    if ((t0 & 31) == 0) weights[t0 >> 5] = make_float2(static_cast<float>(top), pairs);
+    __syncthreads();
+    float longest = weights[t0 & 31].x;
+    pairs = weights[t0 & 31].y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+      pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
     }
-    if ((threadIdx.x & 31) == 0) weights[threadIdx.x >> 5] = make_float2(static_cast<float>(top), sum);
+    // every thread chooses for itself, on the same numbers
+    cut = choose_cut(a, total, longest, pairs, [&](int above) {
+      int n = __syncthreads_count(w0 > above);
+      for (int t = PLAN_THREADS; t < total; t += PLAN_THREADS) {
+        int v = 0;
+        if (t + t0 < total) make_entry(a, sd, t + t0, v);
+        n += __syncthreads_count(v > above);
+      }
+      return n;
+    });
   }
+  const int parts = cut.parts, shift = bin_shift(most * (may_cut ? a.group : 1));
+  __shared__ int ranks;
+  if (t0 == 0) ranks = 0;
   __syncthreads();
-  const int i = 2 * t0, c0 = hist[i], c1 = hist[i + 1];
-  const int incl = block_scan(c0 + c1, warp_sums);
-  hist[i] = incl - c0 - c1;
-  hist[i + 1] = incl - c1;
-  __syncthreads();
-  if (t0 < total) put_entry(sd.out + atomicAdd(&hist[bin0], 1), e0);
+  const int heads = may_cut ? a.group : 1;
+  auto is_cut = [&](int weight) { return parts > 1 && weight > cut.above; };
+  auto bin = [&](int weight, bool c) { return bin_of(static_cast<int64_t>(weight) * (c ? heads / parts : heads), shift); };
+  // counts per bin -> first positions -> entries
+  auto count = [&](int weight) {
+    const bool c = is_cut(weight);
+    atomicAdd(&hist[bin(weight, c)], c ? parts : 1);
+  };
+  auto put = [&](AttnTile e, int weight) {
+    const bool c = is_cut(weight);
+    int at = atomicAdd(&hist[bin(weight, c)], c ? parts : 1);
+    if (!c) {
+      put_entry(sd.out + at, e);
+      return;
+    }
+    const int rank = atomicAdd(&ranks, 1);
+    for (int p = 0; p < parts; ++p, ++at) {
+      e.slot = rank * parts + p;
+      put_entry(sd.out + at, e);
+      if (p == 0) put_entry(a.plan.cuts + rank, e);
+    }
+  };
+  if (t0 < total) count(w0);
   for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
-    const AttnTile e = make_entry(a, sd, t, shift, bin, w);
-    put_entry(sd.out + atomicAdd(&hist[bin], 1), e);
+    make_entry(a, sd, t, w);
+    count(w);
   }
-  if (threadIdx.x == 0) *sd.count = total;
+  scan_bins(hist, warp_sums);
+  if (t0 < total) put(e0, w0);
+  for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
+    const AttnTile e = make_entry(a, sd, t, w);
+    put(e, w);
+  }
+  if (t0 == 0) {
+    *sd.count = total + cut.cuts * (parts - 1);
+    if (sd.keys) {
+      a.plan.counts[2] = parts;
+      a.plan.counts[3] = cut.cuts;
+    }
+  }
   __syncthreads();
 }
 
@@ -166,69 +274,30 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
     }
   }
   __syncthreads();
+  const bool keys = blockIdx.x != 0;
   if (bad) {
     if (threadIdx.x == 0) {
       atomicOr(a.status, CODA_DEV_SEQLEN_RANGE);
-      a.plan.counts[0] = 0;
-      a.plan.counts[1] = 0;
-      a.plan.counts[2] = 1;
+      a.plan.counts[keys] = 0;
+      if (keys) {
+        a.plan.counts[2] = 1;
+        a.plan.counts[3] = 0;
+      }
     }
     return;
   }
   const int32_t* cq = small ? small_q : a.cu_q;
   const int32_t* ck = small ? small_k : a.cu_k;
-  build_side(a, Side{cq, ck, a.q_span, small ? small_prefix : a.prefix_q, a.plan.q_tiles, a.plan.counts, false}, hist,
-             warp_sums, weights);
-  if (!a.plan.k_tiles) return;
-  build_side(a, Side{cq, ck, ATTN_BLK, small ? small_prefix : a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true}, hist,
-             warp_sums, weights);
-  // Parts of a group (a divisor of it).  An item of the key list meets all
-  // query tiles of its part's heads, so with few key tiles the longest item
-  // (whole group, whole sequence) runs on while most SMs are idle; each part
-  // costs a write and a read of 128 KB.  The choice minimises the kernel's
-  // estimated time: ITER us per block pair of the longest item or of an SM's
-  // share, JOIN us for the joining kernel, PART us for each part (one sequence
-  // of 1024 tokens, 64 + 8 heads: 135 -> 82 us with four parts).  One warp
-  // looks at a divisor per lane.
-  if (threadIdx.x >= 32) return;
-  constexpr float ITER = 1.2f, JOIN = 3.f, PART = 0.06f;
-  const float heads = static_cast<float>(a.plan.counts[1]) * a.n_kv;  // items of whole groups
-  float longest = weights[threadIdx.x].x, pairs = weights[threadIdx.x].y;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-    pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
-  }
-  const float share = pairs * a.n_kv * a.group / a.sms;
-  int best = 1;
-  float least = ITER * fmaxf(static_cast<float>(a.group) * longest, share);
-  if (a.max_parts > 0) {
-    for (int s = 2 + static_cast<int>(threadIdx.x); s <= a.group; s += 32) {
-      if (heads * s > a.max_parts || a.group % s) continue;
-      const float t = ITER * fmaxf(static_cast<float>(a.group / s) * longest, share) + JOIN + PART * heads * s;
-      if (t < least) {
-        best = s;
-        least = t;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const float t = __shfl_xor_sync(0xffffffffu, least, o);
-      const int s = __shfl_xor_sync(0xffffffffu, best, o);
-      if (t < least || (t == least && s < best)) {
-        best = s;
-        least = t;
-      }
-    }
-  }
-  if (threadIdx.x == 0) a.plan.counts[2] = best;
+  const Side sd = keys ? Side{cq, ck, ATTN_BLK, small ? small_prefix : a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true}
+                       : Side{cq, ck, a.q_span, small ? small_prefix : a.prefix_q, a.plan.q_tiles, a.plan.counts, false};
+  build_side(a, sd, hist, warp_sums, weights);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_plan(const AttnPlanArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1);
+  cfg.gridDim = dim3(a.plan.k_tiles ? 2 : 1);
   cfg.blockDim = dim3(PLAN_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

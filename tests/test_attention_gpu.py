@@ -230,6 +230,8 @@ def run_backward(coda, t, cq, ck, n_q, n_kv, same, fill=7.0):
 
 BWD_CASES = {k: CASES[k] for k in CASES if k != "long"}
 BWD_CASES["long"] = ([1100], None, 4, 2, 0, 0)
+BWD_CASES["some_groups_cut"] = ([1500, 40, 200], None, 12, 1, 0, 3)
+BWD_CASES["few_queries_cut"] = ([300, 1, 20], [290, 900, 20], 16, 2, 0, 0)
 BWD_CASES["queries_missing"] = ([0, 40], [200, 60], 4, 2, 0, 5)
 
 
