@@ -50,10 +50,11 @@ __device__ __forceinline__ float f16_hi(uint32_t v) { return __half2float(__usho
 // Eight lanes per row of 128, one 16-element block each; every arithmetic
 // step is one fp32 operation, the same steps as quantize_nvfp4_rows, so the
 // codes and scales agree with it bit for bit.  HBM-bound: 512 bytes in and
-// 152 out per token and head, 12.9 us for 8192 tokens and 8 heads (44 MB).
+// 152 out per token and head, 11.6 us for 8192 tokens and 8 heads (44 MB; 12.3
+// with the 36 registers that six blocks per SM leave).
 // One row per lane group, many blocks: with four rows per group in flight
 // instead it took 21.5 us (6.6 instead of 3.7 us for 61 tokens).
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 8)
     kv_append_kernel(const KvCache c, const __nv_bfloat16* __restrict__ K, int64_t ldk,
                      const __nv_bfloat16* __restrict__ V, int64_t ldv, const int32_t* __restrict__ slots, int rows,
                      int* status) {
@@ -115,63 +116,62 @@ __global__ void __launch_bounds__(256)
 }
 
 // -------------------------------------------------------------------- read
-// The rows back: (e2m1 * e4m3, exact) * scale, one fp32 rounding; then bf16
-// for the bf16 form.  A row is written by 32 lanes (fp32) or 16 (bf16), 16
-// bytes each, so a warp's store covers whole lines; bound by the writes (67 MB
-// in fp32 for 8192 tokens and 8 heads: 22 us, two to eight rows in flight alike).
+// The rows back: (e2m1 * e4m3, exact in f16) * scale, one fp32 rounding; then
+// bf16 for the bf16 form.  Sixteen lanes per row, eight elements each; in fp32
+// four of each half, so that every store of a warp covers whole lines.  Bound by
+// the writes and the start: 67 MB in fp32 for 8192 tokens and 8 heads, 15.8 us
+// (22.3 with 32 lanes per row and the products in fp32, where the instructions
+// were the limit; two and four rows per lane group in turn 15.8 and 16.4, and
+// 4.4 and 6.0 instead of 3.7 us for 61 tokens).
 template <bool F32>
 __global__ void __launch_bounds__(256)
     kv_read_kernel(const KvCache c, const int32_t* __restrict__ slots, int rows, void* __restrict__ K,
                    void* __restrict__ V, int* status) {
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int LANES = F32 ? 32 : 16, PER = 128 / LANES, RW = 32 / LANES, UN = 2;  // elements a lane, rows a step
-  const int lane = threadIdx.x & 31, sub = lane % LANES;
-  const int first = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (RW * UN) + lane / LANES;
-  uint32_t codes[UN], sfs[UN];
-  float sc[UN];
-#pragma unroll
-  for (int u = 0; u < UN; ++u) {
-    const int row = first + u * RW;
-    codes[u] = sfs[u] = 0;
-    sc[u] = 0.f;
-    if (row < rows) {
-      const int t = row / (2 * c.n_kv), rest = row - t * 2 * c.n_kv;
-      const int plane = rest >= c.n_kv, h = rest - plane * c.n_kv;
-      const int slot = slots[t];
-      if (slot >= 0) {
-        if ((slot >> c.page_shift) < c.num_pages) {
-          const int64_t r = cache_row(c, slot >> c.page_shift, plane, h, slot & ((1 << c.page_shift) - 1));
-          codes[u] = F32 ? *reinterpret_cast<const uint16_t*>(c.codes + r * 64 + sub * 2)
-                         : *reinterpret_cast<const uint32_t*>(c.codes + r * 64 + sub * 4);
-          sfs[u] = c.sf[r * 8 + sub * PER / 16];
-          sc[u] = c.scale[r];
-        } else if (rest == 0 && sub == 0) {
-          atomicOr(status, CODA_DEV_PAGE_RANGE);
-        }
+  const int sub = threadIdx.x & 15;
+  const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (row >= rows) return;
+  const int t = row / (2 * c.n_kv), rest = row - t * 2 * c.n_kv;
+  const int plane = rest >= c.n_kv, h = rest - plane * c.n_kv;
+  const int slot = slots[t];
+  uint32_t codes = 0, sfs = 0;
+  float sc = 0.f;
+  if (slot >= 0) {
+    if ((slot >> c.page_shift) < c.num_pages) {
+      const int64_t r = cache_row(c, slot >> c.page_shift, plane, h, slot & ((1 << c.page_shift) - 1));
+      const uint8_t* q = c.codes + r * 64;
+      const uint8_t* f = c.sf + r * 8;
+      if constexpr (F32) {
+        codes = *reinterpret_cast<const uint16_t*>(q + sub * 2) |
+                static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(q + 32 + sub * 2)) << 16;
+        sfs = f[sub >> 2] | static_cast<uint32_t>(f[4 + (sub >> 2)]) << 8;
+      } else {
+        codes = *reinterpret_cast<const uint32_t*>(q + sub * 4);
+        sfs = f[sub >> 1] * 0x101u;
       }
+      sc = c.scale[r];
+    } else if (rest == 0 && sub == 0) {
+      atomicOr(status, CODA_DEV_PAGE_RANGE);
     }
   }
+  const uint32_t sf = e4m3x2_f16(sfs);
+  uint32_t f[4];
+  e2m1x8_f16(codes, f);
+  float v[8];
 #pragma unroll
-  for (int u = 0; u < UN; ++u) {
-    const int row = first + u * RW;
-    if (row >= rows) continue;
-    const int t = row / (2 * c.n_kv), rest = row - t * 2 * c.n_kv;
-    const int plane = rest >= c.n_kv, h = rest - plane * c.n_kv;
-    const float sf = e4m3_f32(sfs[u]);
-    uint32_t f[4];
-    e2m1x8_f16(codes[u], f);
-    float v[PER];
-#pragma unroll
-    for (int i = 0; i < PER / 2; ++i) {
-      v[2 * i] = __fmul_rn(f16_lo(f[i]) * sf, sc[u]);
-      v[2 * i + 1] = __fmul_rn(f16_hi(f[i]) * sf, sc[u]);
-    }
-    const int64_t at = (static_cast<int64_t>(t) * c.n_kv + h) * 128 + sub * PER;
-    if constexpr (F32)
-      *reinterpret_cast<float4*>(static_cast<float*>(plane ? V : K) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      store_bf16x8(static_cast<__nv_bfloat16*>(plane ? V : K) + at, v);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = hmul2(f[i], __byte_perm(sf, sf, i < 2 ? 0x1010 : 0x3232));
+    v[2 * i] = __fmul_rn(f16_lo(x), sc);
+    v[2 * i + 1] = __fmul_rn(f16_hi(x), sc);
+  }
+  const int64_t at = (static_cast<int64_t>(t) * c.n_kv + h) * 128;
+  if constexpr (F32) {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(plane ? V : K) + at) + sub;
+    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+    dst[16] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    store_bf16x8(static_cast<__nv_bfloat16*>(plane ? V : K) + at + sub * 8, v);
   }
 }
 
@@ -821,7 +821,7 @@ cudaError_t launch_kv_append(const KvCache& c, const __nv_bfloat16* K, int64_t l
 
 cudaError_t launch_kv_read(const KvCache& c, const int32_t* slots, int rows, void* K, void* V, bool f32, int* status,
                            cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((rows - 1) / (f32 ? 16 : 32) + 1);
+  const unsigned grid = static_cast<unsigned>((rows - 1) / 16 + 1);
   return f32 ? launch(kv_read_kernel<true>, grid, 256, 0, s, c, slots, rows, K, V, status)
              : launch(kv_read_kernel<false>, grid, 256, 0, s, c, slots, rows, K, V, status);
 }
