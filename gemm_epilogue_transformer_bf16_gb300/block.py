@@ -202,8 +202,9 @@ class Block:
 class AttentionBlock(Block):
     """The whole block over packed sequences: Block's projections and MLP with
     causal attention between the QKV projection and the output projection, on
-    one stream.  ``cu_seqlens`` [n_seq + 1] int32 must cover every token (the
-    weight gradients sum over all of them).
+    one stream.  Rows outside the sequences of ``cu_seqlens`` [n_seq + 1] int32
+    (padding) have A = 0 and dQ = dK = dV = 0; like every other row they take
+    part in the weight gradients with their dx2.
 
     Forward   Q, K, V -> A = attention(Q, K, V) -> x1 = x0 + A Wo^T -> MLP
     Backward  MLP -> dA = dx1 Wo -> dQ, dK, dV = attention_bwd(dA) -> QKV"""
@@ -230,6 +231,7 @@ class AttentionBlock(Block):
         linear_qknorm_rope(self.U0, w["Wqkv"], w["gamma_q"], w["gamma_k"], pos, self.cos_sin, s.n_q, s.n_kv,
                            rstd=self.rstd0, eps=s.eps, head_dim=s.head_dim, out=self.fwd, ws=self.ws)
         f = self.fwd
+        self.att["O"].zero_()  # rows outside the sequences, which the attention leaves as they are
         attention(f["Q"], f["K"], f["V"], cu_seqlens, s.n_q, s.n_kv, out=self.att, ws=self.ws)
         linear_residual(self.att["O"], w["Wo"], x0, eps=s.eps, Y=self.x1, rstd_out=self.rstd1,
                         gamma_next=w["gamma_mlp"], U_out=self.U1, ws=self.ws)
@@ -242,6 +244,8 @@ class AttentionBlock(Block):
         linear_swiglu_bwd(dx2, self.x1, w["Wg"], w["Wu"], w["Wd"], self.g, self.u, self.H, rstd=self.rstd1,
                           gamma=w["gamma_mlp"], dX_resid=dx2, ws=self.ws, out=self.grads_mlp)
         linear_residual_bwd(self.dx1, self.att["O"], w["Wo"], ws=self.ws, out=self.grads_o)
+        for t in self.att_grads.values():
+            t.zero_()
         g = attention_bwd(self.grads_o["dX"], f["Q"], f["K"], f["V"], self.att["O"], self.att["lse"], cu_seqlens, s.n_q,
                           s.n_kv, out=self.att_grads, ws=self.ws)
         linear_qknorm_rope_bwd(g["dQ"], g["dK"], g["dV"], f["qk_save"], f["V"], w["gamma_q"], w["gamma_k"], pos,
@@ -266,11 +270,22 @@ class ServingBlock:
     prefill  whole prompts, or the next chunk of prompts whose earlier tokens
              the cache holds (``key_slots``, ``cu_seqlens_k``)
     decode   one new token per sequence
+
+    ``ws``, of at least ``workspace_size`` bytes, is the cache's and the
+    attention's workspace: its status word tells of slots, pages, lengths or
+    offsets out of range.  Without it each call makes its own.
     """
 
     def __init__(self, shape, weights, cache, device="cuda"):
         self.s, self.w, self.cache = shape, weights, cache
         self.cos_sin = rope_table(shape.theta, shape.head_dim, shape.seq_len, device=device)
+
+    def workspace_size(self, tokens, keys, sequences):
+        """For calls of up to ``tokens`` new tokens, ``keys`` rows of K and V
+        and ``sequences`` sequences."""
+        s, lib = self.s, load()
+        return max(lib.coda_attention_workspace_size(tokens, keys, sequences, s.n_q, s.n_kv, s.head_dim),
+                   lib.coda_attention_decode_nvfp4_workspace_size(sequences, s.n_q, s.n_kv, s.head_dim))
 
     def _qkv(self, x, pos):
         s, w = self.s, self.w
@@ -286,28 +301,33 @@ class ServingBlock:
         H, _, _ = linear_swiglu(U, w["Wg"], w["Wu"], rstd=rstd, save=False)
         return linear_residual(H, w["Wd"], x1)
 
-    def prefill(self, x, pos, slots, cu_seqlens, key_slots=None, cu_seqlens_k=None):
+    def prefill(self, x, pos, slots, cu_seqlens, key_slots=None, cu_seqlens_k=None, ws=None):
         """x [T, hidden]: the packed new tokens, their positions and cache
         slots [T].  With key_slots [Tk] and cu_seqlens_k, every sequence's keys
         are those cached rows, in order, its new tokens last; without, the new
-        tokens are whole prompts and attend to each other unquantised."""
+        tokens are whole prompts and attend to each other unquantised.  Padding
+        behind the last sequence: slots -1, and an output of the row without
+        attention."""
         s = self.s
         f = self._qkv(x, pos)
-        kv_append_nvfp4(f["K"], f["V"], slots, self.cache)
+        kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
         K, V = f["K"], f["V"]
         if key_slots is not None:
-            kv = kv_read_nvfp4(self.cache, key_slots)
+            kv = kv_read_nvfp4(self.cache, key_slots, ws=ws)
             K, V = kv["K"], kv["V"]
-        out = attention(f["Q"], K, V, cu_seqlens, s.n_q, s.n_kv, cu_seqlens_k=cu_seqlens_k)
+        T = x.shape[0]
+        out = {"O": torch.zeros(T, s.n_q * s.head_dim, dtype=torch.bfloat16, device=x.device),
+               "lse": torch.empty(s.n_q, T, dtype=torch.float32, device=x.device)}
+        attention(f["Q"], K, V, cu_seqlens, s.n_q, s.n_kv, cu_seqlens_k=cu_seqlens_k, out=out, ws=ws)
         return self._rest(x, out["O"])
 
-    def decode(self, x, pos, slots, block_table, seq_lens):
+    def decode(self, x, pos, slots, block_table, seq_lens, ws=None):
         """x [batch, hidden]: one new token per sequence; seq_lens [batch]
         counts it."""
         s = self.s
         f = self._qkv(x, pos)
-        kv_append_nvfp4(f["K"], f["V"], slots, self.cache)
-        out = attention_decode_nvfp4(f["Q"], self.cache, block_table, seq_lens, s.n_q)
+        kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
+        out = attention_decode_nvfp4(f["Q"], self.cache, block_table, seq_lens, s.n_q, ws=ws)
         return self._rest(x, out["O"])
 
 

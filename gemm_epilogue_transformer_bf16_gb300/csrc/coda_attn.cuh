@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "coda_internal.h"
 #include "coda_ptx.cuh"
 
 namespace coda {
@@ -56,6 +57,26 @@ struct AttnPlanArgs {
 bool attn_programmatic_launch();
 // Raises a kernel's dynamic shared-memory limit, once per device and kernel id.
 cudaError_t attn_smem_attribute(const void* kernel, int id, uint32_t bytes);
+
+// Launch with the programmatic attribute: the kernel's prologue may run while
+// the kernel before it ends (griddep_wait orders the rest).
+template <class... Exp, class... Act>
+cudaError_t attn_launch(void (*kern)(Exp...), int64_t grid, unsigned threads, uint32_t smem, cudaStream_t s,
+                        Act&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid < 1 ? 1 : grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = attn_programmatic_launch() ? 1 : 0;
+  note_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Exp>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 cudaError_t launch_attn_plan(const AttnPlanArgs& a, cudaStream_t s);
 

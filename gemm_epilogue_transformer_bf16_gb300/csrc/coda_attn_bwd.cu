@@ -131,6 +131,10 @@ __device__ __forceinline__ void store_row64(uint32_t taddr, __nv_bfloat16* dst, 
 //               dK and dP^T, and dS^T beside dV and S^T.
 //   warp 9      TMA: K and V, a ring of Q and dO tiles, the rows' -lse2 and -D.
 //   warp 10     zeroes Q and dO rows behind the sequence.
+//
+// Measured: 4 sequences of 2048 tokens, 64 + 8 heads (four products, 550 GFLOP)
+// 330 us, 1670 TFLOP/s, the tensor pipe active 76 %: bound by the products (620
+// to 700 clocks each for 128^3).
 struct KvItem {
   AttnTile t;
   int kv, first, n;  // first query tile, query tiles
@@ -529,6 +533,12 @@ __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const AttnBwdArgs a)
 // K stays until its dQ product, which runs behind the next block's dP: that
 // one's V lies three places on, within the ring.  The next item's first V lies
 // five places behind this item's last K, so there the dQ product runs first.
+//
+// Measured: 4 sequences of 2048 tokens, 64 + 8 heads (three products, 413 GFLOP)
+// 361 us, 1140 TFLOP/s, the tensor pipe active 50 %.  A block's arithmetic (2000
+// clocks in two warpgroups) is as long as its three products, and E1, E2 and the
+// products wait for one another in turn: a form of 370 us took 367 without the
+// exponentials, 357 without the loads, 321 without the products.
 struct QItem {
   AttnTile t;
   int head, n;
@@ -911,23 +921,6 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
   }
 }
 
-template <class... Exp, class... Act>
-cudaError_t launch(void (*kern)(Exp...), int64_t grid, unsigned threads, uint32_t smem, cudaStream_t s, Act&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, grid)));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = attn_programmatic_launch() ? 1 : 0;
-  note_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Exp>(args)...);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64_t max_q_tiles, int64_t max_k_tiles,
@@ -937,15 +930,15 @@ cudaError_t launch_attn_bwd(const AttnBwdArgs& a, const CUtensorMap* maps, int64
   e = attn_smem_attribute(reinterpret_cast<const void*>(attn_bwd_q_kernel), 4, Q_SMEM);
   if (e != cudaSuccess) return e;
   if (max_q_tiles > 0) {
-    e = launch(attn_bwd_q_kernel, std::min<int64_t>(sms, max_q_tiles * a.n_q), BWD_THREADS, Q_SMEM, s, maps[0], maps[1],
+    e = attn_launch(attn_bwd_q_kernel, std::min<int64_t>(sms, max_q_tiles * a.n_q), BWD_THREADS, Q_SMEM, s, maps[0], maps[1],
                maps[2], maps[3], maps[4], a);
     if (e != cudaSuccess) return e;
   }
   if (max_k_tiles == 0) return cudaSuccess;
-  e = launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv * (a.max_parts ? a.group : 1)), BWD_THREADS,
+  e = attn_launch(attn_bwd_kv_kernel, std::min<int64_t>(sms, max_k_tiles * a.n_kv * (a.max_parts ? a.group : 1)), BWD_THREADS,
              KV_SMEM, s, maps[0], maps[1], maps[2], maps[3], a);
   if (e != cudaSuccess || a.max_parts == 0) return e;
-  return launch(attn_bwd_join_kernel, std::min<int64_t>(max_k_tiles * a.n_kv * 16, 8 * sms), 256, 0, s, a);
+  return attn_launch(attn_bwd_join_kernel, std::min<int64_t>(max_k_tiles * a.n_kv * 16, 8 * sms), 256, 0, s, a);
 }
 
 }  // namespace coda

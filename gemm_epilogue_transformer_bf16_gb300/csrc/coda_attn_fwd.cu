@@ -29,6 +29,12 @@
 // previous block is complete by then, since S of this block was issued
 // behind it.
 //
+// Measured: 4 sequences of 2048 tokens, 64 + 8 heads (275 GFLOP over the visible
+// pairs) 211 us, 1300 TFLOP/s; one of 16384 tokens, 32 + 8 heads 1280 us, 1720.
+// The tensor pipe is active 58 % of the first: the two products of a 128 x 128
+// block take 1250 to 1400 clocks with N = 128 and one CTA (1024 at the pipe's
+// rate), and the masked half of the diagonal blocks is computed too.
+//
 // Roundings: P to bf16 before the second product (the sum l adds the fp32
 // weights), O to bf16 once at the end.
 #include <algorithm>
@@ -423,19 +429,8 @@ cudaError_t launch_attn_fwd(const AttnFwdArgs& a, const CUtensorMap* maps, int64
                             cudaStream_t s) {
   cudaError_t e = attn_smem_attribute(reinterpret_cast<const void*>(attn_fwd_kernel), 0, FWD_SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(sms, max_items))));
-  cfg.blockDim = dim3(FWD_THREADS);
-  cfg.dynamicSmemBytes = FWD_SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = attn_programmatic_launch() ? 1 : 0;
-  note_launch();
-  e = cudaLaunchKernelEx(&cfg, attn_fwd_kernel, maps[0], maps[1], maps[2], a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return attn_launch(attn_fwd_kernel, std::min<int64_t>(sms, max_items), FWD_THREADS, FWD_SMEM, s, maps[0], maps[1],
+                     maps[2], a);
 }
 
 }  // namespace coda

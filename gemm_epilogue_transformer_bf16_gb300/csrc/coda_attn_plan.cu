@@ -296,18 +296,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
 }  // namespace
 
 cudaError_t launch_attn_plan(const AttnPlanArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.plan.k_tiles ? 2 : 1);
-  cfg.blockDim = dim3(PLAN_THREADS);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = attn_programmatic_launch() ? 1 : 0;
-  note_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_plan_kernel, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return attn_launch(attn_plan_kernel, a.plan.k_tiles ? 2 : 1, PLAN_THREADS, 0, s, a);
 }
 
 }  // namespace coda

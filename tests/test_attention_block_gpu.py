@@ -2,6 +2,10 @@
 cache, run together as they are used.  Each stage is compared with the fp64
 oracle on the stage's actual inputs (the bf16 tensors the previous stage
 stored), so the tolerances are those of the single operators."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -177,3 +181,71 @@ def test_serving_prompts_chunks_and_single_tokens(coda):
     finally:
         for name, real in originals.items():
             setattr(B, name, real)
+
+
+def test_padded_training_batch_after_a_full_one(coda):
+    """Rows behind the last sequence take no part in the attention, whatever an
+    earlier step left there, and add to the weight gradients what their own dx2
+    gives."""
+    from gemm_epilogue_transformer_bf16_gb300.block import AttentionBlock
+    shape = synth.BlockShape(tokens=256, hidden=256, n_q=4, n_kv=2, head_dim=D, inter=256, seq_len=256)
+    t = synth.make_block(shape, seed=12)
+    t["pos"] = (torch.arange(256) % 128).to(torch.int32)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu = offsets([70, 100])
+    blk, fresh = AttentionBlock(shape, d, n_seq=2), AttentionBlock(shape, d, n_seq=2)
+    blk.step(d["x0"], d["pos"], torch.tensor([0, 128, 256], dtype=torch.int32, device=DEV), d["dx2"])
+    dcu = torch.from_numpy(cu).to(DEV)
+    f = blk.forward(d["x0"], d["pos"], dcu)
+    g = blk.backward(d["x0"], d["pos"], dcu, d["dx2"])
+    want = fresh.step(d["x0"], d["pos"], dcu, d["dx2"])
+    for k in want:
+        assert torch.equal(g[k], want[k]), k
+    assert torch.all(f["A"][170:] == 0) and all(torch.all(g[k][170:] == 0) for k in ("dQ", "dK", "dV"))
+    cfg = dict(n_q=4, n_kv=2, head_dim=D, theta=shape.theta, eps=shape.eps)
+    o = {k: v.double().numpy() for k, v in t.items()}
+    o.update(A=to_np(f["A"]), dQ=to_np(g["dQ"]), dK=to_np(g["dK"]), dV=to_np(g["dV"]))
+    rf, rb = O.block_fwd(o, **cfg), O.block_bwd(o, **cfg)
+    for k in ("x1", "x2"):
+        assert_bf16(f[k], rf[k], k)
+    for k in ("dx0", "dWqkv", "dWo", "dWg", "dWu", "dWd"):
+        assert_bf16(g[k], rb[k], k)
+    assert coda.get_status(blk.ws) == 0
+
+
+def test_serving_reports_errors_and_pads(coda):
+    from gemm_epilogue_transformer_bf16_gb300.block import ServingBlock
+    shape = synth.BlockShape(tokens=64, hidden=256, n_q=4, n_kv=2, head_dim=D, inter=512, seq_len=128)
+    d = {k: v.to(DEV) for k, v in synth.make_block(shape, seed=9).items()}
+    cache = coda.kv_cache_nvfp4(4, 16, 2)
+    blk = ServingBlock(shape, d, cache)
+    ws = coda.workspace(blk.workspace_size(20, 20, 2))
+
+    def i32(v):
+        return torch.tensor(v, dtype=torch.int32, device=DEV)
+    x, pos = synth.randn_bf16((20, shape.hidden), 1.0, 3).to(DEV), i32(list(range(17)) + [0] * 3)
+    cu = i32([0, 5, 17])
+    y = blk.prefill(x, pos, i32(list(range(17)) + [-1] * 3), cu, ws=ws)      # three rows of padding
+    again = blk.prefill(x, pos, i32(list(range(17)) + [-1] * 3), cu)
+    assert coda.get_status(ws) == 0 and torch.equal(y, again) and bool(torch.isfinite(y.float()).all())
+    blk.prefill(x, pos, i32(list(range(17)) + [64, -1, -1]), cu, ws=ws)
+    assert coda.get_status(ws) == 10                     # CODA_ERR_PAGE_RANGE
+    coda.reset_status(ws)
+    blk.prefill(x, pos, i32([-1] * 20), i32([0, 5, 21]), ws=ws)
+    assert coda.get_status(ws) == 9                      # CODA_ERR_SEQLEN_RANGE
+    coda.reset_status(ws)
+    one, p1, at, table = x[:2], i32([5, 12]), i32([-1, -1]), i32([[0], [0]])
+    blk.decode(one, p1, at, table, i32([5, 16]), ws=ws)
+    assert coda.get_status(ws) == 0
+    blk.decode(one, p1, at, table, i32([5, 17]), ws=ws)
+    assert coda.get_status(ws) == 9
+
+
+def test_without_programmatic_launch():
+    """The runs above with programmatic dependent launch off (the switch is
+    read once per process)."""
+    e = dict(os.environ, CODA_PDL="0")
+    here = os.path.abspath(__file__)
+    r = subprocess.run([sys.executable, "-m", "pytest", here, "-x", "-q", "-m", "gpu", "-k", "training or serving"],
+                       env=e, cwd=os.path.dirname(os.path.dirname(here)), capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-3000:] + r.stderr[-2000:]
