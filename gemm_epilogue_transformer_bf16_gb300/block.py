@@ -261,6 +261,9 @@ class AttentionBlock(Block):
         self.forward(x0, pos, cu_seqlens)
         return self.backward(x0, pos, cu_seqlens, dx2)
 
+    def launches(self):
+        raise NotImplementedError("the attention's kernels depend on the shape: count them with coda_launch_count")
+
 
 class ServingBlock:
     """Forward of the block for serving, with the keys and values of every
