@@ -738,7 +738,8 @@ int coda_linear_cross_entropy_bwd(const coda_bf16* X, const coda_bf16* W, const 
  * word and nothing is computed.  scale > 0 and finite.  P is rounded to bf16
  * before the P V product; sums, maxima and O are fp32 until O's rounding.  An
  * infinity or NaN reaches tokens of its own sequence only (and there also
- * earlier ones: a zero weight times an infinite value is NaN).
+ * earlier ones: a zero weight times an infinite value is NaN).  Here and in
+ * the calls below no output may overlap an input or another output.
  * head_dim 128; n_q a multiple of n_kv; Tq, Tk below 2^30 and
  * (max(Tq / 32, Tk / 128) + n_seq + 1) * n_q below 2^31.
  * ---------------------------------------------------------------------- */

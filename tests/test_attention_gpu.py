@@ -353,3 +353,65 @@ def test_on_another_stream(coda):
     got = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, stream=side)
     side.synchronize()
     assert torch.equal(got["O"], want["O"]) and torch.equal(got["lse"], want["lse"])
+
+
+def test_own_scale_both_ways(coda):
+    n_q, n_kv, scale = 4, 2, 0.3
+    t, cq, _, Tq, _ = make([140, 9], None, n_q, n_kv, seed=9)
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 82)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu = torch.from_numpy(cq).to(DEV)
+    f = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, scale=scale)
+    x = {k: to_np(v) for k, v in t.items()}
+    check_forward(f, O.attention_fwd(x["Q"], x["K"], x["V"], cq, cq, n_q, n_kv, scale), t, cq, cq, n_q, n_kv, scale)
+    g = coda.attention_bwd(d["dO"], d["Q"], d["K"], d["V"], f["O"], f["lse"], cu, n_q, n_kv, scale=scale)
+    r = O.attention_bwd(x["dO"], x["Q"], x["K"], x["V"], cq, cq, n_q, n_kv, scale)
+    check_backward(g, r, t, cq, cq, n_q, n_kv, scale)
+
+
+def test_no_queries_or_no_keys_at_all(coda):
+    n_q, n_kv = 4, 2
+
+    def bf(rows, heads, v=1.0):
+        return torch.full((rows, heads * D), v, dtype=torch.bfloat16, device=DEV)
+
+    def i32(v):
+        return torch.tensor(v, dtype=torch.int32, device=DEV)
+    # no keys: O = 0, lse = -inf, dQ = 0
+    kw = {"cu_seqlens_k": i32([0, 0, 0])}
+    f = coda.attention(bf(9, n_q), bf(0, n_kv), bf(0, n_kv), i32([0, 4, 9]), n_q, n_kv, **kw)
+    assert torch.all(f["O"] == 0) and bool(torch.isneginf(f["lse"]).all())
+    g = coda.attention_bwd(bf(9, n_q), bf(9, n_q), bf(0, n_kv), bf(0, n_kv), f["O"], f["lse"], i32([0, 4, 9]), n_q, n_kv, **kw)
+    assert torch.all(g["dQ"] == 0) and g["dK"].shape == (0, n_kv * D)
+    # no queries: dK = dV = 0
+    kw = {"cu_seqlens_k": i32([0, 200, 209])}
+    f = coda.attention(bf(0, n_q), bf(209, n_kv), bf(209, n_kv), i32([0, 0, 0]), n_q, n_kv, **kw)
+    assert f["O"].shape == (0, n_q * D)
+    g = coda.attention_bwd(bf(0, n_q), bf(0, n_q), bf(209, n_kv), bf(209, n_kv), f["O"], f["lse"], i32([0, 0, 0]), n_q, n_kv,
+                           out={"dQ": bf(0, n_q), "dK": bf(209, n_kv, 7.0), "dV": bf(209, n_kv, 7.0)}, **kw)
+    assert torch.all(g["dK"] == 0) and torch.all(g["dV"] == 0)
+    # no sequences: nothing is written
+    out = {"O": bf(5, n_q, 7.0), "lse": torch.full((n_q, 5), 7.0, device=DEV)}
+    coda.attention(bf(5, n_q), bf(5, n_kv), bf(5, n_kv), i32([0]), n_q, n_kv, out=out)
+    assert torch.all(out["O"] == 7) and torch.all(out["lse"] == 7)
+
+
+def test_two_streams_with_a_workspace_each(coda):
+    n_q, n_kv = 4, 2
+    t, cq, _, Tq, _ = make([300, 41, 200], None, n_q, n_kv, seed=8)
+    t["dO"] = synth.randn_bf16((Tq, n_q * D), 1.0, 83)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu = torch.from_numpy(cq).to(DEV)
+    f = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv)
+    want = coda.attention_bwd(d["dO"], d["Q"], d["K"], d["V"], f["O"], f["lse"], cu, n_q, n_kv)
+    torch.cuda.synchronize()
+    got = []
+    for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+        for _ in range(3):
+            h = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, stream=s)
+            got.append((h, coda.attention_bwd(d["dO"], d["Q"], d["K"], d["V"], h["O"], h["lse"], cu, n_q, n_kv, stream=s)))
+    torch.cuda.synchronize()
+    for h, g in got:
+        assert torch.equal(h["O"], f["O"]) and torch.equal(h["lse"], f["lse"])
+        for k in want:
+            assert torch.equal(g[k], want[k]), k

@@ -315,3 +315,67 @@ def test_decode_in_a_graph_and_on_two_streams(coda):
         for one in pair:
             assert all(torch.equal(one[k], after[k]) for k in after)
     assert coda.get_status(ws[0]) == 0 and coda.get_status(ws[1]) == 0
+
+
+def test_append_takes_the_quantiser_s_codes_of_any_number(coda):
+    """Infinities, NaN, the smallest and largest numbers and zeros of both
+    signs: the cached codes and row scales are quantize_nvfp4_rows' own."""
+    n_kv = 2
+    K = rows(8, n_kv, 3).float()
+    K[0, 3], K[1, 130], K[2, :] = float("inf"), float("nan"), float("-inf")
+    K[3, :] = torch.finfo(torch.bfloat16).max
+    K[4, :] = 1e-40
+    K[5, :] = -0.0
+    K[6, ::2] = 2.0 ** -133
+    K = K.to(torch.bfloat16).to(DEV)
+    cache = coda.kv_cache_nvfp4(1, 16, n_kv)
+    slots = torch.arange(8, dtype=torch.int32, device=DEV)
+    coda.kv_append_nvfp4(K, K, slots, cache)
+    codes, _, scale = coda.quantize_nvfp4_rows(K.view(8 * n_kv, D))
+    for plane in range(2):
+        got = cache["codes"][0, plane, :, :8].transpose(0, 1).reshape(8 * n_kv, 64)
+        assert torch.equal(got, codes)
+        sc = cache["scale"][0, plane, :, :8].transpose(0, 1).reshape(8 * n_kv)
+        assert torch.equal(sc.view(torch.int32), scale.view(torch.int32))
+    # a slot may be read twice
+    twice = coda.kv_read_nvfp4(cache, slots[[3, 3, 7]], dtype=torch.float32)
+    assert torch.equal(twice["K"][0], twice["K"][1]) and torch.equal(twice["K"][2], twice["V"][2])
+
+
+def test_decode_non_finite_numbers_stay_in_their_sequence(coda):
+    """NaN and infinities in one sequence's query, keys or values: the others
+    keep their bits, and the sequence's own result is NaN."""
+    lens, page, n_q, n_kv = [150, 700, 90], 32, 8, 2
+    Q = synth.randn_bf16((3, n_q * D), 1.0, 5)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cache, table, *_ = fill(coda, lens, page, n_kv, True)
+    clean = coda.attention_decode_nvfp4(Q.to(DEV), cache, table.to(DEV), n, n_q)
+    assert bool(torch.isfinite(clean["O"].float()).all())
+    bad_q = Q.clone()
+    bad_q[1, 5] = float("nan")
+    got = coda.attention_decode_nvfp4(bad_q.to(DEV), cache, table.to(DEV), n, n_q)
+    for k in got:
+        assert torch.equal(got[k][[0, 2]], clean[k][[0, 2]]), k
+    assert bool(torch.isnan(got["O"][1, :D].float()).all()) and bool(torch.isnan(got["lse"][1, 0]))
+    # the other heads: those of the same key/value head may renew their units elsewhere
+    assert torch.equal(got["O"][1, 4 * D:], clean["O"][1, 4 * D:])
+    assert bool(torch.isfinite(got["O"][1, D:].float()).all())
+    for plane, value in ((0, float("nan")), (0, float("inf")), (1, float("nan")), (1, float("inf"))):
+        hurt = {k: v.clone() for k, v in cache.items()}
+        hurt["scale"][int(table[1, 20]), plane, :, 7] = value           # key 647 of the second sequence
+        got = coda.attention_decode_nvfp4(Q.to(DEV), hurt, table.to(DEV), n, n_q)
+        for k in got:
+            assert torch.equal(got[k][[0, 2]], clean[k][[0, 2]]), (plane, value, k)
+        assert not bool(torch.isfinite(got["O"][1].float()).any()) or plane == 0
+
+
+def test_decode_without_pages_and_with_an_own_scale(coda):
+    n_q, n_kv = 4, 2
+    Q = synth.randn_bf16((2, n_q * D), 1.0, 5)
+    cache, table, kval, vval, vs = fill(coda, [40, 7], 16, n_kv, False)
+    none = coda.attention_decode_nvfp4(Q.to(DEV), cache, torch.zeros(2, 0, dtype=torch.int32, device=DEV),
+                                       torch.zeros(2, dtype=torch.int32, device=DEV), n_q)
+    assert torch.all(none["O"] == 0) and bool(torch.isneginf(none["lse"]).all())
+    out = coda.attention_decode_nvfp4(Q.to(DEV), cache, table.to(DEV),
+                                      torch.tensor([40, 7], dtype=torch.int32, device=DEV), n_q, scale=0.3)
+    check_decode(out, to_np(Q), [40, 7], kval, vval, vs, n_q, n_kv, 0.3)
