@@ -30,10 +30,12 @@
 // behind it.
 //
 // Measured: 4 sequences of 2048 tokens, 64 + 8 heads (275 GFLOP over the visible
-// pairs) 211 us, 1300 TFLOP/s; one of 16384 tokens, 32 + 8 heads 1280 us, 1720.
+// pairs) 209 us, 1320 TFLOP/s; one of 16384 tokens, 32 + 8 heads 1280 us, 1720.
 // The tensor pipe is active 58 % of the first: the two products of a 128 x 128
 // block take 1250 to 1400 clocks with N = 128 and one CTA (1024 at the pipe's
-// rate), and the masked half of the diagonal blocks is computed too.
+// rate), the masked half of the diagonal blocks is computed too, and O leaves in
+// front of the next tile (20 us of the 209; four warps of their own for it took
+// registers from the others: 226 to 270 us).
 //
 // Roundings: P to bf16 before the second product (the sum l adds the fp32
 // weights), O to bf16 once at the end.
@@ -60,8 +62,9 @@ struct FwdItem {
   int kv;
 };
 
-// Loading the next item's entry one item ahead was slower (prompt of 16384
-// tokens 1295 -> 1375 us): the registers it holds cost more than the latency.
+// The softmax warps load the next item's entry before O leaves, when no scores
+// are held (4 x 2048 tokens 214 -> 210 us); one whole item ahead the registers
+// cost more than the latency (16384 tokens 1295 -> 1375 us).
 __device__ __forceinline__ FwdItem fwd_item(const AttnFwdArgs& a, int w) {
   FwdItem it;
   const int hp = 1 << a.head_shift;
@@ -282,8 +285,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     const int tok = r >> a.head_shift, hd = r & ((1 << a.head_shift) - 1);
     const float c = a.scale_log2;
     uint32_t sn = 0, on = 0;
-    for (int k = 0, w = first; w < items && ok; w = snake_item(first, step, ++k)) {
-      const FwdItem it = fwd_item(a, w);
+    FwdItem it = first < items ? fwd_item(a, first) : FwdItem{};
+    for (int k = 0, w = first; w < items && ok;) {
       const int n = x ? it.n[1] : it.n[0];
       const int row0 = x ? it.row[1] : it.row[0];
       const int row = row0 + tok;
@@ -358,6 +361,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         l += s0 + s1;
       }
       if (!ok) break;
+      w = snake_item(first, step, ++k);
+      FwdItem nx = it;
+      if (w < items) nx = fwd_item(a, w);
       const bool valid = row < it.t.lq;
       const int head = (x ? it.head[1] : it.head[0]) + hd;
       const int64_t grow = static_cast<int64_t>(it.t.q0) + row;
@@ -411,6 +417,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         }
         a.lse[static_cast<int64_t>(head) * a.Tq + grow] = vis == 0 ? -INFINITY : m * a.scale + logf(l);
       }
+      it = nx;
     }
   }
 
