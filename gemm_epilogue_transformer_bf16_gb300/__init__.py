@@ -974,15 +974,21 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _own_scratch(need, dev):
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws[:256].zero_()  # the status word; the calls write the rest before they read it
+    return ws
+
+
 def _scratch(ws, need, dev, stream):
-    """Pointer and size of the caller's workspace, or of a zeroed one made on
-    the call's stream (returned too: it must outlive the launch)."""
+    """Pointer and size of the caller's workspace, or of one made on the call's
+    stream (returned too: it must outlive the launch)."""
     if ws is None:
         if stream is None:
-            ws = workspace(need, dev)
+            ws = _own_scratch(need, dev)
         else:
             with torch.cuda.stream(stream):
-                ws = workspace(need, dev)
+                ws = _own_scratch(need, dev)
     elif ws.get_device() != dev:
         _where(ws, dev, "ws")
     n = ws.numel()

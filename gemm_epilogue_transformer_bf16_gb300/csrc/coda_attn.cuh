@@ -22,15 +22,17 @@ constexpr int ATTN_BLK = 128;  // keys per block, rows per tile
 struct AttnTile {
   int q0, lq, k0, lk;
   int t0, seq;
-  int slot, pad;  // key list: number of the part among all parts of cut tiles; -1: the whole group
+  int slot;   // number of the part among all parts of cut runs; -1: a whole run
+  int block;  // query list: the part's first key block
 };
 static_assert(sizeof(AttnTile) == 32, "two 16-byte loads");
 
 // Work lists in the caller's workspace, written by attn_plan_kernel before
 // the kernels that walk them.  counts[0]: entries of the query list;
-// counts[1]: entries of the key list; counts[2]: parts that the query heads of
-// a group are cut into where they are cut; counts[3]: key tiles cut, whose
-// first parts stand in `cuts` (see attn_plan_kernel).
+// counts[1]: entries of the key list.  Runs may be cut (see attn_plan_kernel):
+// counts[2] is the number of parts that the query heads of a group are cut into
+// (key list), or the key blocks of a part (query list); counts[3] the number of
+// runs cut, whose first parts stand in `cuts`.  A call cuts one of its lists.
 struct AttnPlan {
   int* counts;
   AttnTile* q_tiles;
@@ -49,6 +51,8 @@ struct AttnPlanArgs {
   AttnPlan plan;
   int n_kv, group;   // key list: heads
   int max_parts;     // key list: bound on the parts of all key tiles and heads (0: never cut)
+  int max_q_parts;   // query list: bound on the parts of all runs (0: never cut)
+  int q_items;       // items per entry of the query list
   uint32_t divisors;  // bit s - 1: a group may be cut into s parts (2 <= s <= 32)
   int sms;
   int* status;
@@ -88,6 +92,9 @@ struct AttnFwdArgs {
   int64_t Tq;
   int n_q, group;    // query heads; query heads per key/value head
   int head_shift;    // log2 of the heads that share a 128-row tile
+  float* part;       // [part, item of the entry, 2, 32, 128, 4] partial O where the keys of a run are cut; null: never
+  float* part_lse;   // [part, item of the entry, 2, 128] their log2-sum-exp
+  const AttnTile* cuts;
   int pair_heads;    // 1: an item's two tiles are two head sets on the same tokens; 0: consecutive tokens
   float scale_log2;  // scale * log2(e)
   float scale;
@@ -263,7 +270,7 @@ __device__ __forceinline__ AttnTile load_tile(const AttnTile* p) {
   const int4 b = __ldcg(reinterpret_cast<const int4*>(p) + 1);
   AttnTile t;
   t.q0 = a.x; t.lq = a.y; t.k0 = a.z; t.lk = a.w;
-  t.t0 = b.x; t.seq = b.y; t.slot = b.z; t.pad = 0;
+  t.t0 = b.x; t.seq = b.y; t.slot = b.z; t.block = b.w;
   return t;
 }
 

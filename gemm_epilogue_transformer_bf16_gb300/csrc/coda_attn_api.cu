@@ -89,17 +89,41 @@ struct PlanLayout {
   int64_t max_q_tiles, max_k_tiles;
 };
 
-// parts: room in the key list for cut tiles (see bwd_max_parts).
+// parts: room for the parts of cut runs, in the key list if there is one (see
+// bwd_max_parts), else in the query list (fwd_max_parts).
 void lay_plan(Cursor& c, PlanLayout& l, int64_t Tq, int64_t Tk, int64_t n_seq, int q_span, bool keys, int64_t parts) {
   l.max_q_tiles = Tq / q_span + n_seq;
   l.max_k_tiles = keys ? Tk / coda::ATTN_BLK + n_seq : 0;
   l.a.plan.counts = c.take<int>(4);
   l.a.prefix_q = c.take<int>(n_seq + 1);
   l.a.prefix_k = keys ? c.take<int>(n_seq + 1) : nullptr;
-  l.a.plan.q_tiles = c.take<coda::AttnTile>(l.max_q_tiles);
+  l.a.plan.q_tiles = c.take<coda::AttnTile>(l.max_q_tiles + (keys ? 0 : parts));
   l.a.plan.k_tiles = keys ? c.take<coda::AttnTile>(l.max_k_tiles + parts) : nullptr;
-  l.a.plan.cuts = keys ? c.take<coda::AttnTile>(parts) : nullptr;
+  l.a.plan.cuts = c.take<coda::AttnTile>(parts);
   l.a.q_span = q_span;
+}
+
+constexpr int64_t PART_FLOATS = 2 * coda::ATTN_BLK * coda::ATTN_D;
+
+// Forward: how a shape is cut into items.
+struct FwdShape {
+  int head_shift, pair_heads, span, q_span, per;  // rows per tile, per list entry; items per entry
+};
+FwdShape fwd_shape(int64_t Tq, int64_t n_seq, int n_q, int group) {
+  FwdShape f;
+  f.head_shift = head_shift(Tq, n_seq, group);
+  f.pair_heads = (group >> f.head_shift) % 2 == 0 ? 1 : 0;
+  f.span = coda::ATTN_BLK >> f.head_shift;
+  f.q_span = f.pair_heads ? f.span : 2 * f.span;
+  f.per = n_q >> (f.head_shift + f.pair_heads);
+  return f;
+}
+// Bound on the parts (of 128 KB) that the forward's items may be cut into along
+// the keys: 0 where the items may occupy the SMs twice already, or where the
+// keys are too few to gain more than the second kernel costs.
+int fwd_max_parts(const FwdShape& f, int64_t Tq, int64_t Tk, int64_t n_seq) {
+  constexpr int64_t PARTS = 512, LEAST = 14 * coda::ATTN_BLK;
+  return Tk < LEAST || (Tq / f.q_span + n_seq) * f.per > 304 ? 0 : PARTS;
 }
 
 // Padded rows of the backward's per-row values (see AttnBwdArgs).
@@ -112,7 +136,6 @@ int bwd_max_parts(int64_t Tk, int64_t n_seq, int n_q, int n_kv) {
   const int64_t least = Tk / coda::ATTN_BLK * n_kv, most = (Tk / coda::ATTN_BLK + n_seq) * n_kv * (n_q / n_kv);
   return n_q == n_kv || least * 2 > PARTS ? 0 : static_cast<int>(std::min(PARTS, most));
 }
-constexpr int64_t PART_FLOATS = 2 * coda::ATTN_BLK * coda::ATTN_D;
 
 bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
@@ -177,8 +200,11 @@ size_t coda_attention_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, int3
   if (check_shape(Tq, Tk, n_seq, n_q, n_kv, head_dim, 1.f) != CODA_OK) return HEADER;
   Cursor c{nullptr};
   PlanLayout l{};
-  // the shortest entry a call can take, so the size depends on the shape alone
-  lay_plan(c, l, Tq, Tk, n_seq, coda::ATTN_BLK >> head_shift(Tq, n_seq, n_q / n_kv), false, 0);
+  const FwdShape f = fwd_shape(Tq, n_seq, n_q, n_q / n_kv);
+  const int parts = fwd_max_parts(f, Tq, Tk, n_seq);
+  lay_plan(c, l, Tq, Tk, n_seq, f.q_span, false, parts / f.per);
+  c.take<float>(parts * PART_FLOATS);
+  c.take<float>(parts * 2 * coda::ATTN_BLK);
   return c.off;
 }
 
@@ -201,13 +227,14 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
   const int sms = coda::device_sms();
   if (sms <= 0 || !coda::tensor_map_encoder()) return CODA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int group = n_q / n_kv;
-  const int hs = head_shift(Tq, n_seq, group);
-  const int pair_heads = (group >> hs) % 2 == 0 ? 1 : 0;
-  const int span = coda::ATTN_BLK >> hs;
+  const FwdShape f = fwd_shape(Tq, n_seq, n_q, n_q / n_kv);
+  const int parts = fwd_max_parts(f, Tq, Tk, n_seq);
   Cursor c{static_cast<uint8_t*>(ws)};
   PlanLayout l{};
-  lay_plan(c, l, Tq, Tk, n_seq, pair_heads ? span : 2 * span, false, 0);
+  lay_plan(c, l, Tq, Tk, n_seq, f.q_span, false, parts / f.per);
+  l.a.max_q_parts = parts;
+  l.a.q_items = f.per;
+  l.a.sms = sms;
   l.a.cu_q = cu_q;
   l.a.cu_k = cu_k;
   l.a.n_seq = static_cast<int>(n_seq);
@@ -217,7 +244,7 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
   CUtensorMap maps[3];
   const uint64_t dims[3] = {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(n_q), static_cast<uint64_t>(Tq)};
   const uint64_t st[2] = {static_cast<uint64_t>(head_dim) * 2, static_cast<uint64_t>(ldq) * 2};
-  const uint32_t box[3] = {64, 1u << hs, static_cast<uint32_t>(span)};
+  const uint32_t box[3] = {64, 1u << f.head_shift, static_cast<uint32_t>(f.span)};
   if (!coda::encode_bf16_map(&maps[0], Q, 3, dims, st, box)) return CODA_ERR_CUDA;
   if (Tk > 0) {
     if (!map_rows(&maps[1], K, Tk, wk, ldk) || !map_rows(&maps[2], V, Tk, wk, ldv)) return CODA_ERR_CUDA;
@@ -231,15 +258,18 @@ int coda_attention(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t 
   a.lse = lse;
   a.Tq = Tq;
   a.n_q = n_q;
-  a.group = group;
-  a.head_shift = hs;
-  a.pair_heads = pair_heads;
+  a.group = n_q / n_kv;
+  a.head_shift = f.head_shift;
+  a.pair_heads = f.pair_heads;
+  a.part = parts ? c.take<float>(parts * PART_FLOATS) : nullptr;
+  a.part_lse = parts ? c.take<float>(parts * 2 * coda::ATTN_BLK) : nullptr;
+  a.cuts = l.a.plan.cuts;
   a.scale = scale;
   a.scale_log2 = static_cast<float>(scale * LOG2E);
   a.status = static_cast<int*>(ws);
   a.timeout_ns = WAIT_LIMIT_NS;
   CU(coda::launch_attn_plan(l.a, s));
-  CU(coda::launch_attn_fwd(a, maps, l.max_q_tiles * (n_q >> (hs + pair_heads)), sms, s));
+  CU(coda::launch_attn_fwd(a, maps, l.max_q_tiles * f.per + parts, sms, s));
   return CODA_OK;
 }
 

@@ -37,6 +37,11 @@
 // front of the next tile (20 us of the 209; four warps of their own for it took
 // registers from the others: 226 to 270 us).
 //
+// Few rows over many keys leave most SMs without an item: then the keys of the
+// longer runs are cut into parts (attn_plan_kernel), which leave normalised
+// fp32 outputs and log-sum-exps that a second kernel joins in fixed order.
+// 16 rows over 100000 keys, 64 + 8 heads: 989 -> 84 us.
+//
 // Roundings: P to bf16 before the second product (the sum l adds the fp32
 // weights), O to bf16 once at the end.
 #include <algorithm>
@@ -80,6 +85,11 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnFwdArgs& a, int w) {
 #pragma unroll
   for (int x = 0; x < 2; ++x)
     it.n[x] = it.row[x] < it.t.lq ? key_blocks(it.t, min(it.row[x] + span, it.t.lq) - 1) : 0;
+  if (it.t.slot >= 0) {  // a part of the keys
+    const int len = __ldcg(a.counts + 2);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) it.n[x] = max(0, min(it.n[x] - it.t.block, len));
+  }
   return it;
 }
 
@@ -174,10 +184,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
           tma_load_3d(q, &mQ, &q_full[x], 0, it.head[x], it.t.q0 + it.row[x], el);
           tma_load_3d(q + HALF_BYTES, &mQ, &q_full[x], 64, it.head[x], it.t.q0 + it.row[x], el);
         }
-        if (x == 0 && n > 0) ok = put(mK, it.kv * ATTN_D, it.t.k0, false);
+        if (x == 0 && n > 0) ok = put(mK, it.kv * ATTN_D, it.t.k0 + it.t.block * ATTN_BLK, false);
       }
       for (int j = 0; j < n && ok; ++j) {
-        const int row = j * ATTN_BLK;
+        const int row = (it.t.block + j) * ATTN_BLK;
         ok = put(mV, it.kv * ATTN_D, it.t.k0 + row, row + ATTN_BLK > it.t.lk);
         if (ok && j + 1 < n) ok = put(mK, it.kv * ATTN_D, it.t.k0 + row + ATTN_BLK, false);
       }
@@ -194,13 +204,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     for (int k = 0, w = first; w < items && ok; w = snake_item(first, step, ++k)) {
       const FwdItem it = fwd_item(a, w);
       const int n = max(it.n[0], it.n[1]);
-      if (n > 0 && n * ATTN_BLK > it.t.lk) {
+      const int end = it.t.block + n;
+      if (n > 0 && end * ATTN_BLK > it.t.lk) {
         const uint32_t s = (pos + 2 * n - 1) % FWD_STAGES;  // the item's last V block
         ok = mbar_wait_bounded(&kv_raw[s], (seen >> s) & 1, abort_flag, a.status, a.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         seen ^= 1u << s;
-        zero_tile_rows(sKV + s * TILE_BYTES, it.t.lk - (n - 1) * ATTN_BLK);
+        zero_tile_rows(sKV + s * TILE_BYTES, it.t.lk - (end - 1) * ATTN_BLK);
         if (lane == 0) mbar_arrive(&kv_full[s]);
       }
       pos += 2 * n;
@@ -290,8 +301,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
       const int n = x ? it.n[1] : it.n[0];
       const int row0 = x ? it.row[1] : it.row[0];
       const int row = row0 + tok;
-      const int vis = max(0, min(it.t.lk, row + 1 + it.t.lk - it.t.lq));  // keys this row sees
-      const int all = row0 + 1 + it.t.lk - it.t.lq;                  // keys every row of the tile sees
+      // keys this row sees, keys every row of the tile sees, from the item's first on
+      const int vis = max(0, min(it.t.lk, row + 1 + it.t.lk - it.t.lq) - it.t.block * ATTN_BLK);
+      const int all = row0 + 1 + it.t.lk - it.t.lq - it.t.block * ATTN_BLK;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j) {
         ok = mbar_wait_bounded(&s_full[x], sn & 1, abort_flag, a.status, a.timeout_ns);
@@ -376,6 +388,30 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         tc_fence_after();
       }
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // NaN stays NaN
+      if (it.t.slot >= 0) {
+        // column by column of four, rows side by side
+        const int shift = a.head_shift + a.pair_heads;
+        const int64_t at = (static_cast<int64_t>(it.t.slot) * (a.n_q >> shift) + (it.head[0] >> shift)) * 2 + x;
+        if (n > 0) {
+          float4* dst = reinterpret_cast<float4*>(a.part + at * ATTN_BLK * ATTN_D) + r;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float o[32];
+            __syncwarp();
+            tmem_ld32(tO + q * 32, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (valid)
+                dst[(q * 8 + i) * ATTN_BLK] =
+                    make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+          }
+          tc_fence_before();
+        }
+        // -inf: no key of this part, and no output read
+        a.part_lse[at * ATTN_BLK + r] = n == 0 || vis == 0 ? -INFINITY : m * c + log2f(l);
+        it = nx;
+        continue;
+      }
       if (n > 0) {
         // through shared memory, so that a warp's store covers whole 128-byte
         // lines: rows of 64 columns, 16-byte piece p of row r at p ^ (r & 7)
@@ -430,14 +466,61 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
   }
 }
 
+// Joins the parts of a run's keys: O = sum_p 2^(lse_p - W) O_p / sum_p 2^(lse_p - W).
+// A thread takes one row and eight columns, a block 256 of the 2 * 2048 such
+// pieces of an item at a time.
+__global__ void __launch_bounds__(256) attn_fwd_join_kernel(const AttnFwdArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int cuts = __ldcg(a.counts + 3);
+  const int per = a.n_q >> (a.head_shift + a.pair_heads);
+  const int span = ATTN_BLK >> a.head_shift, hp = 1 << a.head_shift;
+  for (int w = blockIdx.x; w < cuts * per * 16; w += gridDim.x) {
+    const int x = (w >> 3) & 1, at = w >> 4;  // tile; run, item
+    const int ti = at / per, hi = at - ti * per;
+    const AttnTile t = load_tile(a.cuts + ti);
+    const int u = (w & 7) * 256 + static_cast<int>(threadIdx.x);
+    const int r = u & (ATTN_BLK - 1), c8 = u >> 7;
+    const int row = t.t0 + (a.pair_heads ? 0 : x * span) + (r >> a.head_shift);
+    if (row >= t.lq) continue;
+    const int head = (hi << (a.head_shift + a.pair_heads)) + (a.pair_heads ? x * hp : 0) + (r & (hp - 1));
+    const int parts = t.block;
+    const int64_t step = static_cast<int64_t>(per) * 2 * ATTN_BLK;  // rows from part to part
+    const int64_t first = ((static_cast<int64_t>(t.slot) * per + hi) * 2 + x) * ATTN_BLK;
+    float top = -INFINITY;
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_lse[first + p * step + r]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float lse = a.part_lse[first + p * step + r];
+      if (lse == -INFINITY) continue;  // nothing was left there
+      const float4* s = reinterpret_cast<const float4*>(a.part + (first + p * step) * ATTN_D) + 2 * c8 * ATTN_BLK + r;
+      const float4 lo = s[0], hi4 = s[ATTN_BLK];
+      const float wgt = exp2_sfu(lse - base);
+      sum += wgt;
+      v[0] += wgt * lo.x; v[1] += wgt * lo.y; v[2] += wgt * lo.z; v[3] += wgt * lo.w;
+      v[4] += wgt * hi4.x; v[5] += wgt * hi4.y; v[6] += wgt * hi4.z; v[7] += wgt * hi4.w;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    const int64_t grow = static_cast<int64_t>(t.q0) + row;
+    store_bf16x8(a.O + (grow * a.n_q + head) * ATTN_D + c8 * 8, v);
+    if (c8 == 0)
+      a.lse[static_cast<int64_t>(head) * a.Tq + grow] = sum == 0.f ? -INFINITY : top * 0.69314718056f + logf(sum);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_attn_fwd(const AttnFwdArgs& a, const CUtensorMap* maps, int64_t max_items, int sms,
                             cudaStream_t s) {
   cudaError_t e = attn_smem_attribute(reinterpret_cast<const void*>(attn_fwd_kernel), 0, FWD_SMEM);
   if (e != cudaSuccess) return e;
-  return attn_launch(attn_fwd_kernel, std::min<int64_t>(sms, max_items), FWD_THREADS, FWD_SMEM, s, maps[0], maps[1],
-                     maps[2], a);
+  e = attn_launch(attn_fwd_kernel, std::min<int64_t>(sms, max_items), FWD_THREADS, FWD_SMEM, s, maps[0], maps[1], maps[2], a);
+  if (e != cudaSuccess || !a.part) return e;
+  return attn_launch(attn_fwd_join_kernel, 4 * sms, 256, 0, s, a);
 }
 
 }  // namespace coda

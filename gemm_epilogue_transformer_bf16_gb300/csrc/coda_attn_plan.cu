@@ -65,7 +65,7 @@ __device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side
   e.t0 = (t - sd.prefix[lo]) * sd.span;
   e.seq = lo;
   e.slot = -1;
-  e.pad = 0;
+  e.block = 0;
   if (sd.keys) {
     const int first = max(0, e.t0 - (e.lk - e.lq)) / ATTN_BLK;  // first query block that sees the run
     w = max(0, (e.lq + ATTN_BLK - 1) / ATTN_BLK - first);
@@ -77,7 +77,7 @@ __device__ __forceinline__ AttnTile make_entry(const AttnPlanArgs& a, const Side
 __device__ __forceinline__ void put_entry(AttnTile* out, const AttnTile& e) {
   int4* o = reinterpret_cast<int4*>(out);
   o[0] = make_int4(e.q0, e.lq, e.k0, e.lk);
-  o[1] = make_int4(e.t0, e.seq, e.slot, 0);
+  o[1] = make_int4(e.t0, e.seq, e.slot, e.block);
 }
 
 // Longest first.
@@ -98,6 +98,8 @@ __device__ void scan_bins(int* hist, int* warp_sums) {
   hist[i + 1] = incl - c1;
   __syncthreads();
 }
+
+constexpr int LENS = 4;  // lengths of parts that are weighed (query list)
 
 // How the groups of the key list are cut: tiles that meet more than `above`
 // query blocks into `parts`; `cuts` of them.
@@ -144,6 +146,47 @@ __device__ Cut choose_cut(const AttnPlanArgs& a, int total, float longest, float
   return best;
 }
 
+// Few rows over many keys: the runs of a query list longer than `len` key blocks
+// are cut into parts of `len`, whose outputs a second kernel joins.  Of an SM's
+// share, its half, third and quarter, and no cut, the one with the least
+// estimated time: ITER us for each key block of the longest item, or, where
+// there are more items than SMs, of the share and half an item (they are dealt
+// whole); JOIN us for the parts' own work and PART us for each.  Forward in us,
+// whole runs -> parts: 16 rows over 100000 keys, 64 + 8 heads 989 -> 84; 128
+// over 32768 357 -> 102; one row over 65536, 8 + 1 heads 648 -> 53; 5000 tokens,
+// 2 + 1 heads 62 -> 28; 2000 tokens, 8 + 2 heads 31 -> 27.  Weighing it costs 4
+// us where nothing is cut (1024 rows over 9000, 32 + 8 heads 106 -> 110).
+// count(lens, parts, runs): for each length the parts of the longer runs, and
+// those runs' number.
+template <class F>
+__device__ int choose_len(const AttnPlanArgs& a, int total, float longest, float blocks, F count) {
+  constexpr float ITER = 1.4f, JOIN = 7.f, PART = 0.04f;
+  const float share = blocks * a.q_items / a.sms;
+  auto time = [&](float item, int entries) {
+    return ITER * (static_cast<int64_t>(entries) * a.q_items <= a.sms ? item : fmaxf(item, share + 0.5f * item));
+  };
+  float least = time(longest, total);
+  int best = 0;
+  if (least <= ITER * share + JOIN) return 0;
+  int lens[LENS], parts[LENS], runs[LENS];
+#pragma unroll
+  for (int k = 0; k < LENS; ++k) lens[k] = max(4, static_cast<int>(ceilf(share / static_cast<float>(k + 1))));
+  count(lens, parts, runs);
+#pragma unroll
+  for (int k = 0; k < LENS; ++k) {
+    if (parts[k] == 0 || static_cast<int64_t>(parts[k]) * a.q_items > a.max_q_parts) continue;
+    const float t = time(static_cast<float>(lens[k]), total - runs[k] + parts[k]) + JOIN +
+                    PART * static_cast<float>(parts[k] * a.q_items);
+    if (t < least) {
+      best = lens[k];
+      least = t;
+    }
+  }
+  return best;
+}
+
+// CUT: runs may be cut.
+template <bool CUT>
 __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int* warp_sums, float2* weights) {
   const int32_t* cu = sd.keys ? sd.cu_k : sd.cu_q;
   const int64_t most = (sd.keys ? a.Tq : a.Tk) / ATTN_BLK + 2;
@@ -166,8 +209,9 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
   AttnTile e0;
   if (t0 < total) e0 = make_entry(a, sd, t0, w0);
 
-  const bool may_cut = sd.keys && a.max_parts > 0;
+  const bool may_cut = CUT && (sd.keys ? a.max_parts : a.max_q_parts) > 0;
   Cut cut{1, 0, 0};
+  int len = 0;  // query list: key blocks of a part
   if (may_cut) {
     int top = w0;
     float pairs = static_cast<float>(w0);
@@ -189,41 +233,92 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
       pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
     }
     // every thread chooses for itself, on the same numbers
-    cut = choose_cut(a, total, longest, pairs, [&](int above) {
-      int n = __syncthreads_count(w0 > above);
-      for (int t = PLAN_THREADS; t < total; t += PLAN_THREADS) {
-        int v = 0;
-        if (t + t0 < total) make_entry(a, sd, t + t0, v);
-        n += __syncthreads_count(v > above);
-      }
-      return n;
-    });
+    if (sd.keys) {
+      cut = choose_cut(a, total, longest, pairs, [&](int above) {
+        int n = __syncthreads_count(w0 > above);
+        for (int t = PLAN_THREADS; t < total; t += PLAN_THREADS) {
+          int v = 0;
+          if (t + t0 < total) make_entry(a, sd, t + t0, v);
+          n += __syncthreads_count(v > above);
+        }
+        return n;
+      });
+    } else {
+      len = choose_len(a, total, longest, pairs, [&](const int(&lens)[LENS], int(&parts)[LENS], int(&runs)[LENS]) {
+#pragma unroll
+        for (int k = 0; k < LENS; ++k) {
+          runs[k] = w0 > lens[k];
+          parts[k] = runs[k] ? (w0 + lens[k] - 1) / lens[k] : 0;
+        }
+        for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
+          make_entry(a, sd, t, w);
+#pragma unroll
+          for (int k = 0; k < LENS; ++k) {
+            if (w <= lens[k]) continue;
+            ++runs[k];
+            parts[k] += (w + lens[k] - 1) / lens[k];
+          }
+        }
+        __shared__ int sums[PLAN_THREADS / 32][2 * LENS];
+#pragma unroll
+        for (int k = 0; k < LENS; ++k) {
+          parts[k] = __reduce_add_sync(0xffffffffu, parts[k]);
+          runs[k] = __reduce_add_sync(0xffffffffu, runs[k]);
+          if ((t0 & 31) == 0) {
+            sums[t0 >> 5][k] = parts[k];
+            sums[t0 >> 5][LENS + k] = runs[k];
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < LENS; ++k) {
+          parts[k] = __reduce_add_sync(0xffffffffu, sums[t0 & 31][k]);
+          runs[k] = __reduce_add_sync(0xffffffffu, sums[t0 & 31][LENS + k]);
+        }
+      });
+    }
   }
-  const int parts = cut.parts, shift = bin_shift(most * (may_cut ? a.group : 1));
-  __shared__ int ranks;
-  if (t0 == 0) ranks = 0;
+  const int heads = sd.keys && may_cut ? a.group : 1;
+  const int shift = bin_shift(most * heads);
+  __shared__ int ranks, runs_cut;  // parts of cut runs, cut runs
+  if (t0 == 0) ranks = runs_cut = 0;
   __syncthreads();
-  const int heads = may_cut ? a.group : 1;
-  auto is_cut = [&](int weight) { return parts > 1 && weight > cut.above; };
-  auto bin = [&](int weight, bool c) { return bin_of(static_cast<int64_t>(weight) * (c ? heads / parts : heads), shift); };
-  // counts per bin -> first positions -> entries
+  // parts of a run of this weight, and the weight of its part p
+  auto parts_of = [&](int weight) {
+    if (!CUT) return 1;
+    if (sd.keys) return weight > cut.above ? cut.parts : 1;
+    return len > 0 && weight > len ? (weight + len - 1) / len : 1;
+  };
+  auto bin = [&](int weight, int parts, int p) {
+    if (sd.keys) return bin_of(static_cast<int64_t>(weight) * (heads / parts), shift);
+    return bin_of(parts == 1 ? weight : min(len, weight - p * len), shift);
+  };
+  // counts per bin -> first positions -> entries.  The parts of a key tile
+  // stand together: they lie in one bin.
   auto count = [&](int weight) {
-    const bool c = is_cut(weight);
-    atomicAdd(&hist[bin(weight, c)], c ? parts : 1);
+    const int parts = parts_of(weight);
+    if (sd.keys) {
+      atomicAdd(&hist[bin(weight, parts, 0)], parts);
+    } else {
+      for (int p = 0; p < parts; ++p) atomicAdd(&hist[bin(weight, parts, p)], 1);
+    }
   };
   auto put = [&](AttnTile e, int weight) {
-    const bool c = is_cut(weight);
-    int at = atomicAdd(&hist[bin(weight, c)], c ? parts : 1);
-    if (!c) {
-      put_entry(sd.out + at, e);
+    const int parts = parts_of(weight);
+    if (parts == 1) {
+      put_entry(sd.out + atomicAdd(&hist[bin(weight, 1, 0)], 1), e);
       return;
     }
-    const int rank = atomicAdd(&ranks, 1);
-    for (int p = 0; p < parts; ++p, ++at) {
-      e.slot = rank * parts + p;
-      put_entry(sd.out + at, e);
-      if (p == 0) put_entry(a.plan.cuts + rank, e);
+    const int first = atomicAdd(&ranks, parts), rank = atomicAdd(&runs_cut, 1);
+    const int at = sd.keys ? atomicAdd(&hist[bin(weight, parts, 0)], parts) : 0;
+    for (int p = 0; p < parts; ++p) {
+      e.slot = first + p;
+      e.block = p * len;
+      put_entry(sd.out + (sd.keys ? at + p : atomicAdd(&hist[bin(weight, parts, p)], 1)), e);
     }
+    e.slot = first;
+    e.block = parts;
+    put_entry(a.plan.cuts + (sd.keys ? first / parts : rank), e);
   };
   if (t0 < total) count(w0);
   for (int t = t0 + PLAN_THREADS; t < total; t += PLAN_THREADS) {
@@ -236,16 +331,18 @@ __device__ void build_side(const AttnPlanArgs& a, const Side& sd, int* hist, int
     const AttnTile e = make_entry(a, sd, t, w);
     put(e, w);
   }
+  __syncthreads();
   if (t0 == 0) {
-    *sd.count = total + cut.cuts * (parts - 1);
-    if (sd.keys) {
-      a.plan.counts[2] = parts;
-      a.plan.counts[3] = cut.cuts;
+    *sd.count = total + ranks - runs_cut;
+    if (may_cut) {
+      a.plan.counts[2] = sd.keys ? cut.parts : len;
+      a.plan.counts[3] = runs_cut;
     }
   }
   __syncthreads();
 }
 
+template <bool CUT>
 __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanArgs a) {
   __shared__ int hist[PLAN_BINS];
   __shared__ int warp_sums[33];
@@ -279,8 +376,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
     if (threadIdx.x == 0) {
       atomicOr(a.status, CODA_DEV_SEQLEN_RANGE);
       a.plan.counts[keys] = 0;
-      if (keys) {
-        a.plan.counts[2] = 1;
+      if ((keys ? a.max_parts : a.max_q_parts) > 0) {
+        a.plan.counts[2] = keys;
         a.plan.counts[3] = 0;
       }
     }
@@ -290,13 +387,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) attn_plan_kernel(const AttnPlanA
   const int32_t* ck = small ? small_k : a.cu_k;
   const Side sd = keys ? Side{cq, ck, ATTN_BLK, small ? small_prefix : a.prefix_k, a.plan.k_tiles, a.plan.counts + 1, true}
                        : Side{cq, ck, a.q_span, small ? small_prefix : a.prefix_q, a.plan.q_tiles, a.plan.counts, false};
-  build_side(a, sd, hist, warp_sums, weights);
+  build_side<CUT>(a, sd, hist, warp_sums, weights);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_plan(const AttnPlanArgs& a, cudaStream_t s) {
-  return attn_launch(attn_plan_kernel, a.plan.k_tiles ? 2 : 1, PLAN_THREADS, 0, s, a);
+  const int lists = a.plan.k_tiles ? 2 : 1;
+  return a.max_parts > 0 || a.max_q_parts > 0 ? attn_launch(attn_plan_kernel<true>, lists, PLAN_THREADS, 0, s, a)
+                                              : attn_launch(attn_plan_kernel<false>, lists, PLAN_THREADS, 0, s, a);
 }
 
 }  // namespace coda

@@ -123,6 +123,70 @@ def test_forward(coda, name):
         out["lse"].cpu()[:, ~torch.from_numpy(inside)] == 7)
 
 
+# few rows over many keys: the keys are cut into parts that a second kernel joins
+SPLIT_CASES = {
+    # lq, lk, n_q, n_kv, rows in front, rows behind
+    "one_row": ([1], [9000], 8, 1, 0, 0),
+    "rows_of_all_heads": ([16, 3], [5001, 130], 16, 2, 2, 5),
+    "two_runs": ([130], [4097], 4, 2, 0, 0),
+    "no_pairs": ([300, 1], [3000, 2561], 3, 3, 0, 1),
+    "odd_group": ([40, 200, 0, 7], [6000, 100, 900, 1700], 7, 1, 1, 0),
+    "one_sequence": ([2600], None, 2, 1, 0, 3),
+    "rows_without_keys": ([600, 5], [300, 4000], 2, 2, 0, 0),
+}
+
+
+@pytest.mark.parametrize("name", SPLIT_CASES)
+def test_forward_over_parts_of_the_keys(coda, name):
+    lq, lk, n_q, n_kv, front, pad = SPLIT_CASES[name]
+    t, cq, ck, Tq, Tk = make(lq, lk, n_q, n_kv, front, pad, seed=len(name))
+    d = {k: v.to(DEV) for k, v in t.items()}
+    kw = {} if lk is None else {"cu_seqlens_k": torch.from_numpy(ck).to(DEV)}
+    ws = coda.workspace(coda.load().coda_attention_workspace_size(Tq, Tk, len(lq), n_q, n_kv, D))
+    ws[256:].fill_(0xFF)                                  # what an earlier call may have left: NaN
+    got = []
+    for _ in range(2):
+        out = {"O": torch.full((Tq, n_q * D), 7.0, dtype=torch.bfloat16, device=DEV),
+               "lse": torch.full((n_q, Tq), 7.0, device=DEV)}
+        got.append(coda.attention(d["Q"], d["K"], d["V"], torch.from_numpy(cq).to(DEV), n_q, n_kv, out=out, ws=ws, **kw))
+    assert coda.get_status(ws) == 0
+    assert all(torch.equal(got[0][k], got[1][k]) for k in out)
+    scale = D ** -0.5
+    ref = O.attention_fwd(to_np(t["Q"]), to_np(t["K"]), to_np(t["V"]), cq, ck, n_q, n_kv, scale)
+    inside = check_forward(out, ref, t, cq, ck, n_q, n_kv, scale)
+    assert torch.all(out["O"].cpu()[~torch.from_numpy(inside)] == 7) and torch.all(
+        out["lse"].cpu()[:, ~torch.from_numpy(inside)] == 7)
+
+
+def test_parts_of_the_keys_in_a_graph_with_other_lengths(coda):
+    """A captured call cuts by the lengths of its replay, not by the capture's."""
+    n_q, n_kv = 4, 1
+    t, _, _, Tq, Tk = make([8, 8], [6000, 6000], n_q, n_kv, seed=5)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    cu, ck = torch.tensor([0, 8, 16], dtype=torch.int32, device=DEV), torch.tensor([0, 40, 80], dtype=torch.int32, device=DEV)
+    ws = coda.workspace(coda.load().coda_attention_workspace_size(Tq, Tk, 2, n_q, n_kv, D))
+
+    def run(out=None):
+        return coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, cu_seqlens_k=ck, out=out, ws=ws)
+    out = run()
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=cap):
+        run(out)
+    for ends in ([0, 6000, 12000], [0, 9, 11009], [0, 0, 50], [0, 12000, 12000]):
+        ck.copy_(torch.tensor(ends, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        assert torch.equal(out["O"], want["O"]) and torch.equal(out["lse"], want["lse"])
+        ref = O.attention_fwd(to_np(t["Q"]), to_np(t["K"]), to_np(t["V"]), [0, 8, 16], ends, n_q, n_kv, D ** -0.5)
+        check_forward(out, ref, t, np.array([0, 8, 16]), np.array(ends), n_q, n_kv, D ** -0.5)
+    assert coda.get_status(ws) == 0
+
+
 def test_forward_columns_of_one_projection(coda):
     """Q, K, V as columns of one [T, (n_q + 2 n_kv) * 128] tensor give the same
     bits as separate tensors."""
