@@ -284,10 +284,15 @@ class ServingBlock:
         self.cos_sin = rope_table(shape.theta, shape.head_dim, shape.seq_len, device=device)
 
     def workspace_size(self, tokens, keys, sequences):
-        """For calls of up to ``tokens`` new tokens, ``keys`` rows of K and V
-        and ``sequences`` sequences."""
+        """For every call of up to ``tokens`` new tokens, ``keys`` rows of K and
+        V and ``sequences`` sequences.  Few tokens over many keys need room for
+        partial results that more tokens do not, so the shortest call counts
+        too; the work lists of the calls between are below 64 bytes for each
+        token and sequence."""
         s, lib = self.s, load()
+        lists = 64 * (tokens + sequences) + 65536
         return max(lib.coda_attention_workspace_size(tokens, keys, sequences, s.n_q, s.n_kv, s.head_dim),
+                   lib.coda_attention_workspace_size(1, keys, 1, s.n_q, s.n_kv, s.head_dim) + lists,
                    lib.coda_attention_decode_nvfp4_workspace_size(sequences, s.n_q, s.n_kv, s.head_dim))
 
     def _qkv(self, x, pos):

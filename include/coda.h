@@ -742,6 +742,8 @@ int coda_linear_cross_entropy_bwd(const coda_bf16* X, const coda_bf16* W, const 
  * the calls below no output may overlap an input or another output.
  * head_dim 128; n_q a multiple of n_kv; Tq, Tk below 2^30 and
  * (max(Tq / 32, Tk / 128) + n_seq + 1) * n_q below 2^31.
+ * The workspace sizes of both directions are those of the very shape: a
+ * shorter call may need more (room for partial results).
  * ---------------------------------------------------------------------- */
 size_t coda_attention_workspace_size(int64_t Tq, int64_t Tk, int64_t n_seq, int32_t n_q, int32_t n_kv,
                                      int32_t head_dim);

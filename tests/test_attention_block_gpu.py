@@ -241,6 +241,31 @@ def test_serving_reports_errors_and_pads(coda):
     assert coda.get_status(ws) == 9
 
 
+def test_serving_workspace_holds_for_shorter_calls(coda):
+    """workspace_size covers every call up to its counts: a few new tokens
+    behind a long cached prefix need more room than many."""
+    from gemm_epilogue_transformer_bf16_gb300.block import ServingBlock
+    n_q, n_kv, keys = 4, 2, 2100
+    shape = synth.BlockShape(tokens=64, hidden=256, n_q=n_q, n_kv=n_kv, head_dim=D, inter=512, seq_len=4096)
+    d = {k: v.to(DEV) for k, v in synth.make_block(shape, seed=9).items()}
+    cache = coda.kv_cache_nvfp4(2, 2048, n_kv)
+    kv = synth.randn_bf16((keys, n_kv * D), 1.0, 4).to(DEV)
+    slots = torch.arange(keys, dtype=torch.int32, device=DEV)
+    coda.kv_append_nvfp4(kv, kv, slots, cache)
+    blk = ServingBlock(shape, d, cache)
+    ws = coda.workspace(blk.workspace_size(20000, 20000, 40))
+    lib = coda.load()
+    for t, n in ((1, 1), (3, 2), (40, 40), (700, 3), (2100, 1), (20000, 40)):
+        assert lib.coda_attention_workspace_size(t, 20000, n, n_q, n_kv, D) <= ws.numel(), (t, n)
+    for new in (1, 5, 200):
+        x = synth.randn_bf16((new, shape.hidden), 1.0, 3).to(DEV)
+        at = slots[keys - new:]
+        y = blk.prefill(x, at, at, torch.tensor([0, new], dtype=torch.int32, device=DEV), key_slots=slots,
+                        cu_seqlens_k=torch.tensor([0, keys], dtype=torch.int32, device=DEV), ws=ws)
+        assert bool(torch.isfinite(y.float()).all())
+    assert coda.get_status(ws) == 0
+
+
 def test_without_programmatic_launch():
     """The runs above with programmatic dependent launch off (the switch is
     read once per process)."""

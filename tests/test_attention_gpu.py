@@ -158,6 +158,25 @@ def test_forward_over_parts_of_the_keys(coda, name):
         out["lse"].cpu()[:, ~torch.from_numpy(inside)] == 7)
 
 
+def test_non_finite_rows_and_parts_of_the_keys(coda):
+    """As in the calls that cut nothing: another sequence's numbers, and those
+    behind the last, change no bit; a NaN in one part reaches the joined rows."""
+    n_q, n_kv, pad = 4, 2, 30
+    t, cq, ck, Tq, Tk = make([9, 7], [3001, 2500], n_q, n_kv, 0, pad, seed=3)
+    cu, cuk = torch.from_numpy(cq).to(DEV), torch.from_numpy(ck).to(DEV)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    clean = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, cu_seqlens_k=cuk)
+    for k, c, bad in (("Q", cq, float("nan")), ("K", ck, float("inf")), ("V", ck, float("nan"))):
+        e = {n: v.clone() for n, v in d.items()}
+        e[k][int(c[1]):] = bad
+        got = coda.attention(e["Q"], e["K"], e["V"], cu, n_q, n_kv, cu_seqlens_k=cuk)
+        assert torch.equal(got["O"][:9], clean["O"][:9]) and torch.equal(got["lse"][:, :9], clean["lse"][:, :9]), k
+    e = d["V"].clone()
+    e[1500] = float("nan")
+    got = coda.attention(d["Q"], d["K"], e, cu, n_q, n_kv, cu_seqlens_k=cuk)
+    assert bool(torch.isnan(got["O"][:9].float()).all()) and torch.equal(got["O"][9:16], clean["O"][9:16])
+
+
 def test_parts_of_the_keys_in_a_graph_with_other_lengths(coda):
     """A captured call cuts by the lengths of its replay, not by the capture's."""
     n_q, n_kv = 4, 1
