@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(256)
 //     with one scale each: the k index of the product is a permutation of
 //     the head's elements, the same for Q.
 //   O^T [16 elements x 8 heads] += V'^T P'^T with the row scale of V in
-//     P' = exp2(z - m) * rs * f, where f (per head) sets the largest P' to 1
-//     and is renewed before one would pass 2^14 (f16 ends at 2^16): P' is
-//     rounded to f16 (2^-11), O accumulates in fp32.
+//     P' = exp2(z - m) * rs * f, where f (per head) sets the largest P' of a row
+//     that is not all zeros to 1 and is renewed before one would pass 2^14 (f16
+//     ends at 2^16): P' is rounded to f16 (2^-11, or 2^-25 of that largest one),
+//     O accumulates in fp32.
 // The keys of a tile are read in the order 0 4 1 5 2 6 3 7: then the lanes'
 // shared-memory reads of both K and V are contiguous, and movmatrix turns
 // the S^T fragment into the P operand.
@@ -595,6 +596,19 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
         // new units when P' would pass 2^14, or a head has none yet
         if (__any_sync(0xffffffffu, unset || big > 16384.f)) {
           unset = false;
+          // A row of zeros has the row scale 1 and adds nothing: it has no say
+          // in the units (a row scale that is not finite keeps its own)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 b = *reinterpret_cast<const uint2*>(dec_smem + ST_SFV + (warp * 32 + pi) * 8 + so + i * 64);
+            if (((b.x | b.y) & 0x7F7F7F7Fu) == 0) {
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                z[t][i >> 1][2 * (i & 1)] *= 0.f;
+                z[t][i >> 1][2 * (i & 1) + 1] *= 0.f;
+              }
+            }
+          }
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll

@@ -810,9 +810,11 @@ int coda_kv_read_nvfp4(const uint8_t* codes, const uint8_t* sf, const float* sca
  * [batch, n_q] fp32.  A length of 0 gives O = 0, lse = -inf.  A negative
  * length, or one beyond max_pages * page_size, sets CODA_ERR_SEQLEN_RANGE and
  * counts as 0; a page outside the cache sets CODA_ERR_PAGE_RANGE and its keys
- * are left out.  The weights are rounded to f16 before the second product,
- * Q is scaled per head by a power of two and held in f16; everything else is
- * fp32 until O's rounding.  softmax_scale > 0 and finite. */
+ * are left out.  The weights, times the values' row scales, are rounded to f16
+ * before the second product: by 2^-11 of themselves, or by 2^-25 of the largest
+ * of them over rows that are not all zeros where that is more.  Q is scaled per
+ * head by a power of two and held in f16; everything else is fp32 until O's
+ * rounding.  softmax_scale > 0 and finite. */
 size_t coda_attention_decode_nvfp4_workspace_size(int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
 int coda_attention_decode_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
                                 const float* scale, int64_t num_pages, int32_t page_size, const int32_t* block_table,

@@ -379,3 +379,43 @@ def test_decode_without_pages_and_with_an_own_scale(coda):
     out = coda.attention_decode_nvfp4(Q.to(DEV), cache, table.to(DEV),
                                       torch.tensor([40, 7], dtype=torch.int32, device=DEV), n_q, scale=0.3)
     check_decode(out, to_np(Q), [40, 7], kval, vval, vs, n_q, n_kv, 0.3)
+
+
+def shared_rows(coda, K, V, lens, page, n_kv):
+    """Sequences of `lens` tokens that all begin with the same rows K, V: as
+    fill(), with the row scales of value rows that hold only zeros taken as 0
+    (such a row adds nothing to O, so the bound has no use for its scale of 1)."""
+    n = K.shape[0]
+    pages = -(-n // page)
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(4)).to(torch.int32)
+    j = torch.arange(n)
+    cache = coda.kv_cache_nvfp4(pages, page, n_kv)
+    coda.kv_append_nvfp4(K.to(DEV), V.to(DEV), (order[j // page] * page + j % page).to(torch.int32).to(DEV), cache)
+    kval, (vval, vs) = oracle_rows(K, n_kv)[3], (oracle_rows(V, n_kv)[i] for i in (3, 2))
+    vs = np.where(np.abs(vval).reshape(n, n_kv, D).max(axis=2) > 0, vs, 0)
+    return cache, order.repeat(len(lens), 1), [kval[:m] for m in lens], [vval[:m] for m in lens], [vs[:m] for m in lens]
+
+
+def run_shared(coda, K, V, lens, page, Q, n_q, n_kv):
+    cache, table, kval, vval, vs = shared_rows(coda, K, V, lens, page, n_kv)
+    out = coda.attention_decode_nvfp4(Q.to(DEV), cache, table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), n_q)
+    check_decode(out, to_np(Q), lens, kval, vval, vs, n_q, n_kv, D ** -0.5)
+    return out
+
+
+@pytest.mark.parametrize("n_q, n_kv", [(8, 1), (16, 1), (4, 2)])
+@pytest.mark.parametrize("std", [1.0, 1e-3, 1e-5, 1e-20])
+def test_decode_value_rows_of_zeros(coda, std, n_q, n_kv):
+    """Value rows of zeros (row scale 1) among small values, in front, in
+    between, at the end, over whole units and with by far the largest weight:
+    within the bound that rows without them meet."""
+    base = synth.randn_bf16((1, D), 1.0, 31).float()
+    K = synth.randn_bf16((700, n_kv * D), 0.3, 32)
+    V = synth.randn_bf16((700, n_kv * D), std, 33)
+    V[[0, 1, 39, 100, 159, 699]] = 0
+    V[200:330] = 0
+    K[100] = base.repeat(1, n_kv)[0].to(torch.bfloat16)
+    lens = [1, 2, 40, 160, 331, 700] * 40
+    Q = (base.repeat(len(lens), n_q) + 0.2 * synth.randn_bf16((len(lens), n_q * D), 1.0, 34).float()).to(torch.bfloat16)
+    out = run_shared(coda, K, V, lens, 64, Q, n_q, n_kv)
+    assert torch.all(out["O"][::6] == 0) and torch.all(out["O"][1::6] == 0) and bool(torch.isfinite(out["lse"]).all())
