@@ -568,8 +568,20 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
               for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
               if ((fresh && y > -INFINITY) || y > 0.f) {
                 l[t][k] = fresh ? 0.f : l[t][k] * exp2_sfu(-y);
-                // O is in units of f * 2^m and keeps its value
-                f[t][k] = f[t][k] == 0.f ? 0.f : fminf(f[t][k] * exp2_sfu(y), 3e38f);
+                // O is in units of f * 2^m and keeps its value; where f ends (values
+                // below about 1e-32), O takes the rest of the step
+                float nf = f[t][k] == 0.f ? 0.f : f[t][k] * exp2_sfu(y);
+                if (nf > 3e38f) {
+                  const float root = exp2_sfu(-0.5f * y);  // 2^-y alone may be less than fp32 holds
+                  const float by = 3e38f * root / f[t][k] * root;
+                  nf = 3e38f;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    o[t][i][k] *= by;
+                    o[t][i][k + 2] *= by;
+                  }
+                }
+                f[t][k] = nf;
                 m[t][k] += y;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {

@@ -419,3 +419,18 @@ def test_decode_value_rows_of_zeros(coda, std, n_q, n_kv):
     Q = (base.repeat(len(lens), n_q) + 0.2 * synth.randn_bf16((len(lens), n_q * D), 1.0, 34).float()).to(torch.bfloat16)
     out = run_shared(coda, K, V, lens, 64, Q, n_q, n_kv)
     assert torch.all(out["O"][::6] == 0) and torch.all(out["O"][1::6] == 0) and bool(torch.isfinite(out["lse"]).all())
+
+
+@pytest.mark.parametrize("n_q, n_kv", [(8, 1), (16, 1)])
+@pytest.mark.parametrize("std", [1e-30, 1e-33, 1e-34, 1e-35])
+def test_decode_smallest_values_behind_rising_scores(coda, std, n_q, n_kv):
+    """Scores that rise late by 2^12 and more over values near the end of
+    fp32's range: keys in front keep their small weights."""
+    base = synth.randn_bf16((1, D), 1.0, 41).float()
+    rise = torch.zeros(420, 1)
+    rise[230:], rise[400:] = 0.73, 1.3                   # 2^12 and 2^21 at |base|^2 = 128
+    K = (rise * base + 0.02 * synth.randn_bf16((420, D), 1.0, 42).float()).to(torch.bfloat16)
+    V = synth.randn_bf16((420, D), std, 43)
+    lens = [420, 380, 256, 131] * 100
+    Q = (base.repeat(len(lens), n_q) + 0.1 * synth.randn_bf16((len(lens), n_q * D), 1.0, 44).float()).to(torch.bfloat16)
+    run_shared(coda, K, V, lens, 64, Q, n_q, n_kv)
