@@ -989,8 +989,12 @@ def _scratch(ws, need, dev, stream):
         else:
             with torch.cuda.stream(stream):
                 ws = _own_scratch(need, dev)
+    elif not isinstance(ws, torch.Tensor):
+        raise TypeError("ws: expected a torch.Tensor")
     elif ws.get_device() != dev:
         _where(ws, dev, "ws")
+    elif not ws.is_contiguous():  # numel() of an expanded tensor is not memory
+        raise ValueError("ws: must be contiguous")
     n = ws.numel()
     if n < need:
         raise ValueError(f"workspace too small: {n} < {need}")

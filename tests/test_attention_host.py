@@ -170,3 +170,23 @@ def test_oracle_backward_against_differences():
                 y[name][i] += s * 1e-6
                 f.append(np.sum(O.attention_fwd(y["Q"], y["K"], y["V"], cq, ck, n_q, n_kv, 0.4)["O"] * dO))
             assert abs((f[0] - f[1]) / 2e-6 - r["d" + name][i]) < 1e-7
+
+
+# --------------------------------------------------------------------------- workspaces
+
+@pytest.mark.parametrize("ws, error, match", [
+    (torch.zeros(1, dtype=torch.uint8).expand(4096), ValueError, "contiguous"),     # one byte, said to be 4096
+    (torch.zeros(8192, dtype=torch.uint8)[::2], ValueError, "contiguous"),
+    (bytearray(4096), TypeError, "Tensor"),
+    (torch.zeros(255, dtype=torch.uint8), ValueError, "too small"),
+])
+def test_workspace_must_be_memory_of_its_size(ws, error, match):
+    """What the attention and cache calls take for their workspace, before
+    anything is enqueued (device -1: the host, where the check alone runs)."""
+    with pytest.raises(error, match=match):
+        coda._scratch(ws, 256, -1, None)
+
+
+def test_workspace_of_the_size_is_taken():
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    assert coda._scratch(ws, 4096, -1, None) == (ws.data_ptr(), 4096, ws)
