@@ -908,6 +908,10 @@ def linear_cross_entropy_bwd(X, W, labels, lse, n_valid, dloss=1.0, ignore_index
 
 # These calls are short next to their checks, so each argument is looked at
 # once: _arg and _strided test type, device, dtype and layout together.
+#
+# Without `ws` a call makes its own workspace, and result["ws"] is it (kept as
+# long as the result): get_status(result["ws"]) tells of offsets, lengths, slots
+# and pages out of range.
 
 def _where(t, dev, name):
     at = t.get_device()
@@ -1001,6 +1005,21 @@ def _scratch(ws, need, dev, stream):
     return ws.data_ptr(), n, ws
 
 
+class _Outputs(dict):
+    """Outputs of a call that made its own workspace: result["ws"] is that
+    workspace, whose status word get_status reads.  It is not one of the items,
+    so values() are the outputs alone."""
+
+    def __init__(self, outputs, ws):
+        super().__init__(outputs)
+        self.ws = ws
+
+    def __missing__(self, key):
+        if key == "ws":
+            return self.ws
+        raise KeyError(key)
+
+
 def _on_stream(stream, dev):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
@@ -1034,7 +1053,8 @@ def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, hea
     cu_seqlens_k those of their keys when they are longer (a prompt continued
     from a cached prefix).  scale defaults to 1/sqrt(head_dim).  Returns O
     [Tq, n_q*128] and lse [n_q, Tq]; rows outside every sequence stay as they
-    are (undefined in tensors allocated here)."""
+    are (undefined in tensors allocated here).  Without `ws`, result["ws"] holds
+    the status word."""
     lib = load()
     dev = _device(Q, "Q")
     qkv, rest, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim, dev)
@@ -1043,9 +1063,9 @@ def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, hea
                "lse": _new((n_q, Tq), torch.float32, dev, stream)}
     O = _arg(out["O"], torch.bfloat16, (Tq, n_q * head_dim), dev, "O")
     lse = _arg(out["lse"], torch.float32, (n_q, Tq), dev, "lse")
-    w, nw, ws = _scratch(ws, lib.coda_attention_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
+    w, nw, made = _scratch(ws, lib.coda_attention_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
     _check("coda_attention", lib.coda_attention(*qkv, *rest, O, lse, Tq, Tk, w, nw, _on_stream(stream, dev)))
-    return out
+    return out if ws is not None else _Outputs(out, made)
 
 
 def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, head_dim=128, out=None,
@@ -1053,7 +1073,7 @@ def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None,
     """Gradients dQ [Tq, n_q*128], dK, dV [Tk, n_kv*128] of attention for the
     upstream gradient dO (coda_attention_bwd); O and lse as the forward wrote
     them.  Rows outside every sequence stay as they are (undefined in tensors
-    allocated here)."""
+    allocated here).  Without `ws`, result["ws"] holds the status word."""
     lib = load()
     dev = _device(Q, "Q")
     qkv, rest, Tq, Tk, n_seq = _attention_args(Q, K, V, cu_seqlens, cu_seqlens_k, n_q, n_kv, scale, head_dim, dev)
@@ -1063,10 +1083,10 @@ def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None,
         out = {"dQ": _new(sq, bf, dev, stream), "dK": _new(sk, bf, dev, stream), "dV": _new(sk, bf, dev, stream)}
     saved = (_arg(O, bf, sq, dev, "O"), _arg(lse, torch.float32, (n_q, Tq), dev, "lse"))
     grads = (_arg(out["dQ"], bf, sq, dev, "dQ"), _arg(out["dK"], bf, sk, dev, "dK"), _arg(out["dV"], bf, sk, dev, "dV"))
-    w, nw, ws = _scratch(ws, lib.coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
+    w, nw, made = _scratch(ws, lib.coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
     _check("coda_attention_bwd", lib.coda_attention_bwd(_arg(dO, bf, sq, dev, "dO"), *qkv, *saved, *rest, *grads, Tq, Tk,
                                                         w, nw, _on_stream(stream, dev)))
-    return out
+    return out if ws is not None else _Outputs(out, made)
 
 
 def kv_cache_nvfp4(num_pages, page_size, n_kv, head_dim=128, device="cuda"):
@@ -1093,7 +1113,8 @@ def _cache_args(cache, dev):
 def kv_append_nvfp4(K, V, slots, cache, ws=None, stream=None):
     """Quantise the rows of K, V [T, n_kv*128] (rows may be columns of a wider
     tensor) into their cache slots [T] int32 (coda_kv_append_nvfp4; a negative
-    slot skips its token, the slots of one call must differ)."""
+    slot skips its token, the slots of one call must differ).  Returns the cache;
+    without `ws`, result["ws"] holds the status word."""
     dev = _device(K, "K")
     c, n_kv, d = _cache_args(cache, dev)
     k, ldk, T = _strided(K, n_kv * d, dev, "K")
@@ -1101,16 +1122,16 @@ def kv_append_nvfp4(K, V, slots, cache, ws=None, stream=None):
     if Tv != T:
         raise ValueError(f"K has {T} rows, V {Tv}")
     at = _arg(slots, torch.int32, (T,), dev, "slots")
-    w, nw, ws = _scratch(ws, 256, dev, stream)
+    w, nw, made = _scratch(ws, 256, dev, stream)
     _check("coda_kv_append_nvfp4", load().coda_kv_append_nvfp4(k, ldk, v, ldv, at, T, *c, n_kv, d, w, nw,
                                                                _on_stream(stream, dev)))
-    return cache
+    return cache if ws is not None else _Outputs(cache, made)
 
 
 def kv_read_nvfp4(cache, slots, dtype=torch.bfloat16, out=None, ws=None, stream=None):
     """The rows of cache slots [T] int32 back as {"K", "V"} [T, n_kv*128] in
     torch.bfloat16 or torch.float32 (coda_kv_read_nvfp4; a negative slot gives
-    zeros)."""
+    zeros).  Without `ws`, result["ws"] holds the status word."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"kv_read_nvfp4: dtype must be torch.bfloat16 or torch.float32, not {dtype}")
     dev = _device(cache["scale"], "cache scale")
@@ -1120,18 +1141,19 @@ def kv_read_nvfp4(cache, slots, dtype=torch.bfloat16, out=None, ws=None, stream=
     shape = (T, n_kv * d)
     if out is None:
         out = {"K": _new(shape, dtype, dev, stream), "V": _new(shape, dtype, dev, stream)}
-    w, nw, ws = _scratch(ws, 256, dev, stream)
+    w, nw, made = _scratch(ws, 256, dev, stream)
     _check("coda_kv_read_nvfp4", load().coda_kv_read_nvfp4(
         *c, at, T, n_kv, d, _arg(out["K"], dtype, shape, dev, "K"), _arg(out["V"], dtype, shape, dev, "V"),
         F32 if dtype is torch.float32 else BF16, w, nw, _on_stream(stream, dev)))
-    return out
+    return out if ws is not None else _Outputs(out, made)
 
 
 def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out=None, ws=None, stream=None):
     """One query token per sequence, Q [batch, n_q*128], over the first
     seq_lens [batch] int32 cached tokens of the pages block_table
     [batch, max_pages] int32 names (coda_attention_decode_nvfp4).  Returns O
-    [batch, n_q*128] and lse [batch, n_q]."""
+    [batch, n_q*128] and lse [batch, n_q].  Without `ws`, result["ws"] holds the
+    status word."""
     lib = load()
     dev = _device(Q, "Q")
     c, n_kv, d = _cache_args(cache, dev)
@@ -1143,9 +1165,9 @@ def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out
     if out is None:
         out = {"O": _new((batch, n_q * d), torch.bfloat16, dev, stream),
                "lse": _new((batch, n_q), torch.float32, dev, stream)}
-    w, nw, ws = _scratch(ws, lib.coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, d), dev, stream)
+    w, nw, made = _scratch(ws, lib.coda_attention_decode_nvfp4_workspace_size(batch, n_q, n_kv, d), dev, stream)
     _check("coda_attention_decode_nvfp4", lib.coda_attention_decode_nvfp4(
         q, ldq, *c, table, block_table.shape[1], lens, batch, n_q, n_kv, d, d ** -0.5 if scale is None else float(scale),
         _arg(out["O"], torch.bfloat16, (batch, n_q * d), dev, "O"),
         _arg(out["lse"], torch.float32, (batch, n_q), dev, "lse"), w, nw, _on_stream(stream, dev)))
-    return out
+    return out if ws is not None else _Outputs(out, made)

@@ -498,3 +498,33 @@ def test_two_streams_with_a_workspace_each(coda):
         assert torch.equal(h["O"], f["O"]) and torch.equal(h["lse"], f["lse"])
         for k in want:
             assert torch.equal(g[k], want[k]), k
+
+
+def test_status_of_calls_that_make_their_own_workspace(coda):
+    """Without `ws` the status word is read through the result; the outputs are
+    the result's only items."""
+    n_q, n_kv = 4, 2
+    t, _, _, Tq, _ = make([64, 64], None, n_q, n_kv)
+    d = {k: v.to(DEV) for k, v in t.items()}
+    good, bad = (torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([0, 64, 128], [0, 64, 129]))
+    f = coda.attention(d["Q"], d["K"], d["V"], good, n_q, n_kv)
+    args = (d["Q"], d["Q"], d["K"], d["V"], f["O"], f["lse"])
+    g = coda.attention_bwd(*args, good, n_q, n_kv)
+    assert list(f) == ["O", "lse"] and list(g) == ["dQ", "dK", "dV"] and len(g.values()) == 3
+    assert coda.get_status(f["ws"]) == 0 and coda.get_status(g["ws"]) == 0
+    with pytest.raises(KeyError):
+        f["dQ"]
+    own = {k: torch.full_like(v, 7.0) for k, v in f.items()}
+    h = coda.attention(d["Q"], d["K"], d["V"], bad, n_q, n_kv, out=own)
+    assert coda.get_status(h["ws"]) == 9 and h["O"] is own["O"] and list(own) == ["O", "lse"]
+    assert coda.get_status(coda.attention_bwd(*args, bad, n_q, n_kv)["ws"]) == 9
+    cache = coda.kv_cache_nvfp4(2, 16, n_kv)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    for slot, code in ((31, 0), (32, 10)):
+        a = coda.kv_append_nvfp4(d["K"][:1], d["V"][:1], i32([slot]), cache)
+        r = coda.kv_read_nvfp4(a, i32([slot]))           # the returned cache is the cache
+        assert list(a) == list(cache) and all(a[k] is cache[k] for k in cache) and list(r) == ["K", "V"]
+        assert coda.get_status(a["ws"]) == code and coda.get_status(r["ws"]) == code
+    for page, n, code in ((1, 16, 0), (2, 16, 10), (1, 17, 9)):
+        o = coda.attention_decode_nvfp4(d["Q"][:1], cache, i32([[page]]), i32([n]), n_q)
+        assert coda.get_status(o["ws"]) == code and list(o) == ["O", "lse"]
