@@ -274,9 +274,9 @@ class ServingBlock:
              the cache holds (``key_slots``, ``cu_seqlens_k``)
     decode   one new token per sequence
 
-    ``ws``, of at least ``workspace_size`` bytes, is the cache's and the
-    attention's workspace: its status word tells of slots, pages, lengths or
-    offsets out of range.  Without it each call makes its own.
+    ``ws``, of at least ``workspace_size`` bytes, is the workspace of every call
+    within: its status word tells of positions, slots, pages, lengths or offsets
+    out of range.  Without it each of them makes its own, and nothing tells.
     """
 
     def __init__(self, shape, weights, cache, device="cuda"):
@@ -291,23 +291,29 @@ class ServingBlock:
         token and sequence."""
         s, lib = self.s, load()
         lists = 64 * (tokens + sequences) + 65536
+        rows = max(tokens, sequences)
         return max(lib.coda_attention_workspace_size(tokens, keys, sequences, s.n_q, s.n_kv, s.head_dim),
                    lib.coda_attention_workspace_size(1, keys, 1, s.n_q, s.n_kv, s.head_dim) + lists,
-                   lib.coda_attention_decode_nvfp4_workspace_size(sequences, s.n_q, s.n_kv, s.head_dim))
+                   lib.coda_attention_decode_nvfp4_workspace_size(sequences, s.n_q, s.n_kv, s.head_dim),
+                   lib.coda_linear_qknorm_rope_workspace_size(rows, s.hidden, s.n_q, s.n_kv, s.head_dim),
+                   lib.coda_linear_residual_workspace_size(rows, s.hidden, s.n_q * s.head_dim),
+                   lib.coda_linear_swiglu_workspace_size(rows, s.inter, s.hidden),
+                   lib.coda_linear_residual_workspace_size(rows, s.hidden, s.inter))
 
-    def _qkv(self, x, pos):
+    def _qkv(self, x, pos, ws):
         s, w = self.s, self.w
         rstd, U = rmsnorm_scale(x, w["gamma_attn"], s.eps)
         return linear_qknorm_rope(U, w["Wqkv"], w["gamma_q"], w["gamma_k"], pos, self.cos_sin, s.n_q, s.n_kv, rstd=rstd,
-                                  eps=s.eps, head_dim=s.head_dim, save=False)
+                                  eps=s.eps, head_dim=s.head_dim, save=False, ws=ws)
 
-    def _rest(self, x, A):
+    def _rest(self, x, A, ws):
         s, w = self.s, self.w
         U, rstd = torch.empty_like(x), torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
         x1 = torch.empty_like(x)
-        linear_residual(A, w["Wo"], x, eps=s.eps, Y=x1, rstd_out=rstd, gamma_next=w["gamma_mlp"], U_out=U)
-        H, _, _ = linear_swiglu(U, w["Wg"], w["Wu"], rstd=rstd, save=False)
-        return linear_residual(H, w["Wd"], x1)
+        linear_residual(A, w["Wo"], x, eps=s.eps, Y=x1, rstd_out=rstd, gamma_next=w["gamma_mlp"], U_out=U,
+                        ws=ws)
+        H, _, _ = linear_swiglu(U, w["Wg"], w["Wu"], rstd=rstd, save=False, ws=ws)
+        return linear_residual(H, w["Wd"], x1, ws=ws)
 
     def prefill(self, x, pos, slots, cu_seqlens, key_slots=None, cu_seqlens_k=None, ws=None):
         """x [T, hidden]: the packed new tokens, their positions and cache
@@ -317,7 +323,7 @@ class ServingBlock:
         behind the last sequence: slots -1, and an output of the row without
         attention."""
         s = self.s
-        f = self._qkv(x, pos)
+        f = self._qkv(x, pos, ws)
         kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
         K, V = f["K"], f["V"]
         if key_slots is not None:
@@ -327,16 +333,16 @@ class ServingBlock:
         out = {"O": torch.zeros(T, s.n_q * s.head_dim, dtype=torch.bfloat16, device=x.device),
                "lse": torch.empty(s.n_q, T, dtype=torch.float32, device=x.device)}
         attention(f["Q"], K, V, cu_seqlens, s.n_q, s.n_kv, cu_seqlens_k=cu_seqlens_k, out=out, ws=ws)
-        return self._rest(x, out["O"])
+        return self._rest(x, out["O"], ws)
 
     def decode(self, x, pos, slots, block_table, seq_lens, ws=None):
         """x [batch, hidden]: one new token per sequence; seq_lens [batch]
         counts it."""
         s = self.s
-        f = self._qkv(x, pos)
+        f = self._qkv(x, pos, ws)
         kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
         out = attention_decode_nvfp4(f["Q"], self.cache, block_table, seq_lens, s.n_q, ws=ws)
-        return self._rest(x, out["O"])
+        return self._rest(x, out["O"], ws)
 
 
 class BlockFP8:

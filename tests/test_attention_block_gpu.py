@@ -266,6 +266,33 @@ def test_serving_workspace_holds_for_shorter_calls(coda):
     assert coda.get_status(ws) == 0
 
 
+def test_serving_reports_positions(coda):
+    """A position behind the rotation table shows in the caller's workspace, in
+    both forms; the workspace serves the projections too."""
+    from gemm_epilogue_transformer_bf16_gb300.block import ServingBlock
+    shape = synth.BlockShape(tokens=64, hidden=256, n_q=4, n_kv=2, head_dim=D, inter=512, seq_len=128)
+    d = {k: v.to(DEV) for k, v in synth.make_block(shape, seed=9).items()}
+    blk = ServingBlock(shape, d, coda.kv_cache_nvfp4(4, 16, 2))
+
+    def i32(v):
+        return torch.tensor(v, dtype=torch.int32, device=DEV)
+    for rows in (1, 20):
+        ws = coda.workspace(blk.workspace_size(rows, rows, rows))
+        x, slots = synth.randn_bf16((rows, shape.hidden), 1.0, 3).to(DEV), i32(list(range(rows)))
+        one = i32([[0], [1]] * (rows // 2) or [[0]])
+        for last, code in ((127, 0), (128, 8), (-1, 8)):     # CODA_ERR_POSITION_RANGE
+            pos = i32(list(range(rows - 1)) + [last])
+            y = blk.prefill(x, pos, slots, i32([0, rows]), ws=ws)
+            assert coda.get_status(ws) == code
+            coda.reset_status(ws)
+            z = blk.decode(x, pos, slots, one, i32([1] * rows), ws=ws)
+            assert coda.get_status(ws) == code
+            coda.reset_status(ws)
+            if code == 0:                                    # the bits of calls that make their own
+                assert torch.equal(y, blk.prefill(x, pos, slots, i32([0, rows])))
+                assert torch.equal(z, blk.decode(x, pos, slots, one, i32([1] * rows)))
+
+
 def test_without_programmatic_launch():
     """The runs above with programmatic dependent launch off (the switch is
     read once per process)."""
