@@ -528,3 +528,64 @@ def test_status_of_calls_that_make_their_own_workspace(coda):
     for page, n, code in ((1, 16, 0), (2, 16, 10), (1, 17, 9)):
         o = coda.attention_decode_nvfp4(d["Q"][:1], cache, i32([[page]]), i32([n]), n_q)
         assert coda.get_status(o["ws"]) == code and list(o) == ["O", "lse"]
+
+
+@pytest.mark.parametrize("lq, lk, n_q, n_kv", [
+    ([150, 20], None, 4, 2),
+    ([1500, 40, 200], None, 12, 1),                      # some key tiles' groups are cut
+    ([300, 1, 20], [290, 900, 20], 16, 2),
+])
+def test_backward_columns_of_one_projection(coda, lq, lk, n_q, n_kv):
+    """Q, K, V as columns of one projection's output (K and V of another one
+    where the keys are longer), each with its own offset and row stride: the
+    bits of separate tensors."""
+    cq = offsets(lq)
+    ck = cq if lk is None else offsets(lk)
+    Tq, Tk = int(cq[-1]), int(ck[-1])
+    if lk is None:
+        wide = synth.randn_bf16((Tq, (n_q + 2 * n_kv + 1) * D), 1.0, 5).to(DEV)
+        Q, K, V, _ = wide.split([n_q * D, n_kv * D, n_kv * D, D], dim=1)
+        kw = {}
+    else:
+        _, Q = synth.randn_bf16((Tq, (1 + n_q) * D), 1.0, 5).to(DEV).split([D, n_q * D], dim=1)
+        V, _, K, _ = synth.randn_bf16((Tk, (2 * n_kv + 3) * D), 1.0, 6).to(DEV).split([n_kv * D, D, n_kv * D, 2 * D], dim=1)
+        kw = {"cu_seqlens_k": torch.from_numpy(ck).to(DEV)}
+    dO = synth.randn_bf16((Tq, n_q * D), 1.0, 7).to(DEV)
+    cu = torch.from_numpy(cq).to(DEV)
+    got = []
+    for q, k, v in ((Q, K, V), (Q.contiguous(), K.contiguous(), V.contiguous())):
+        f = coda.attention(q, k, v, cu, n_q, n_kv, **kw)
+        g = coda.attention_bwd(dO, q, k, v, f["O"], f["lse"], cu, n_q, n_kv, **kw)
+        assert coda.get_status(g["ws"]) == 0
+        got.append({**f, **g})
+    for k in got[0]:
+        assert torch.equal(got[0][k], got[1][k]), k
+
+
+@pytest.mark.parametrize("rows, n_q, backward", [(8300, 32, True), (30000, 32, True), (263000, 2, False)])
+def test_short_sequences_in_front_of_many_padding_rows(coda, rows, n_q, backward):
+    """The work lists' bins are as wide as the tensors' rows ask for, so here
+    runs of different lengths share bins; the rows behind hold NaN."""
+    lens, n_kv = [700, 1, 260, 0, 129, 40, 385], 1
+    t, cq, _, n, _ = make(lens, None, n_q, n_kv, seed=21)
+    t["dO"] = synth.randn_bf16((n, n_q * D), 1.0, 22)
+    d = {}
+    for k, v in t.items():
+        d[k] = torch.full((rows, v.shape[1]), float("nan"), dtype=torch.bfloat16, device=DEV)
+        d[k][:n] = v.to(DEV)
+    cu = torch.from_numpy(cq).to(DEV)
+    out = {"O": torch.full((rows, n_q * D), 7.0, dtype=torch.bfloat16, device=DEV),
+           "lse": torch.full((n_q, rows), 7.0, device=DEV)}
+    f = coda.attention(d["Q"], d["K"], d["V"], cu, n_q, n_kv, out=out)
+    assert coda.get_status(f["ws"]) == 0
+    x = {k: to_np(v) for k, v in t.items()}
+    ref = O.attention_fwd(x["Q"], x["K"], x["V"], cq, cq, n_q, n_kv, D ** -0.5)
+    check_forward({"O": out["O"][:n], "lse": out["lse"][:, :n]}, ref, t, cq, cq, n_q, n_kv, D ** -0.5)
+    assert torch.all(out["O"][n:] == 7) and torch.all(out["lse"][:, n:] == 7)
+    if backward:
+        grads = {"d" + k: torch.full_like(d[k], 7.0) for k in ("Q", "K", "V")}
+        g = coda.attention_bwd(d["dO"], d["Q"], d["K"], d["V"], out["O"], out["lse"], cu, n_q, n_kv, out=grads)
+        assert coda.get_status(g["ws"]) == 0
+        r = O.attention_bwd(x["dO"], x["Q"], x["K"], x["V"], cq, cq, n_q, n_kv, D ** -0.5)
+        check_backward({k: v[:n] for k, v in grads.items()}, r, t, cq, cq, n_q, n_kv, D ** -0.5)
+        assert all(torch.all(v[n:] == 7) for v in grads.values())
