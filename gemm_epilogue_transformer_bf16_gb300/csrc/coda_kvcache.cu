@@ -571,10 +571,9 @@ __global__ void __launch_bounds__(DEC_THREADS, NT == 1 ? 3 : 2) attn_decode_kern
                 // O is in units of f * 2^m and keeps its value; where f ends (values
                 // below about 1e-32), O takes the rest of the step
                 float nf = f[t][k] == 0.f ? 0.f : f[t][k] * exp2_sfu(y);
-                if (nf > 3e38f) {
-                  const float root = exp2_sfu(-0.5f * y);  // 2^-y alone may be less than fp32 holds
-                  const float by = 3e38f * root / f[t][k] * root;
-                  nf = 3e38f;
+                if (nf > 0x1p127f) {
+                  const float by = exp2_sfu(127.f - __log2f(f[t][k]) - y);
+                  nf = 0x1p127f;
 #pragma unroll
                   for (int i = 0; i < 8; ++i) {
                     o[t][i][k] *= by;
