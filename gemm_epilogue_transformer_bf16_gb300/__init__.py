@@ -1020,6 +1020,16 @@ class _Outputs(dict):
         raise KeyError(key)
 
 
+def _told(out, ws, made):
+    """What a call returns: `out`, with the workspace it made if it was given
+    none.  Outputs of an earlier call, passed in again, name this call's."""
+    if ws is None:
+        return _Outputs(out, made)
+    if type(out) is _Outputs:
+        out.ws = ws
+    return out
+
+
 def _on_stream(stream, dev):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
@@ -1065,7 +1075,7 @@ def attention(Q, K, V, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, hea
     lse = _arg(out["lse"], torch.float32, (n_q, Tq), dev, "lse")
     w, nw, made = _scratch(ws, lib.coda_attention_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
     _check("coda_attention", lib.coda_attention(*qkv, *rest, O, lse, Tq, Tk, w, nw, _on_stream(stream, dev)))
-    return out if ws is not None else _Outputs(out, made)
+    return _told(out, ws, made)
 
 
 def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None, scale=None, head_dim=128, out=None,
@@ -1086,7 +1096,7 @@ def attention_bwd(dO, Q, K, V, O, lse, cu_seqlens, n_q, n_kv, cu_seqlens_k=None,
     w, nw, made = _scratch(ws, lib.coda_attention_bwd_workspace_size(Tq, Tk, n_seq, n_q, n_kv, head_dim), dev, stream)
     _check("coda_attention_bwd", lib.coda_attention_bwd(_arg(dO, bf, sq, dev, "dO"), *qkv, *saved, *rest, *grads, Tq, Tk,
                                                         w, nw, _on_stream(stream, dev)))
-    return out if ws is not None else _Outputs(out, made)
+    return _told(out, ws, made)
 
 
 def kv_cache_nvfp4(num_pages, page_size, n_kv, head_dim=128, device="cuda"):
@@ -1125,7 +1135,7 @@ def kv_append_nvfp4(K, V, slots, cache, ws=None, stream=None):
     w, nw, made = _scratch(ws, 256, dev, stream)
     _check("coda_kv_append_nvfp4", load().coda_kv_append_nvfp4(k, ldk, v, ldv, at, T, *c, n_kv, d, w, nw,
                                                                _on_stream(stream, dev)))
-    return cache if ws is not None else _Outputs(cache, made)
+    return _told(cache, ws, made)
 
 
 def kv_read_nvfp4(cache, slots, dtype=torch.bfloat16, out=None, ws=None, stream=None):
@@ -1145,7 +1155,7 @@ def kv_read_nvfp4(cache, slots, dtype=torch.bfloat16, out=None, ws=None, stream=
     _check("coda_kv_read_nvfp4", load().coda_kv_read_nvfp4(
         *c, at, T, n_kv, d, _arg(out["K"], dtype, shape, dev, "K"), _arg(out["V"], dtype, shape, dev, "V"),
         F32 if dtype is torch.float32 else BF16, w, nw, _on_stream(stream, dev)))
-    return out if ws is not None else _Outputs(out, made)
+    return _told(out, ws, made)
 
 
 def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out=None, ws=None, stream=None):
@@ -1170,4 +1180,4 @@ def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out
         q, ldq, *c, table, block_table.shape[1], lens, batch, n_q, n_kv, d, d ** -0.5 if scale is None else float(scale),
         _arg(out["O"], torch.bfloat16, (batch, n_q * d), dev, "O"),
         _arg(out["lse"], torch.float32, (batch, n_q), dev, "lse"), w, nw, _on_stream(stream, dev)))
-    return out if ws is not None else _Outputs(out, made)
+    return _told(out, ws, made)

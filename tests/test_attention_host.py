@@ -190,3 +190,17 @@ def test_workspace_must_be_memory_of_its_size(ws, error, match):
 def test_workspace_of_the_size_is_taken():
     ws = torch.zeros(4096, dtype=torch.uint8)
     assert coda._scratch(ws, 4096, -1, None) == (ws.data_ptr(), 4096, ws)
+
+
+def test_results_name_the_workspace_of_their_call():
+    """result["ws"] beside the items: the workspace a call made, or the one it
+    was given when an earlier result is passed as its outputs."""
+    a, b = torch.zeros(256, dtype=torch.uint8), torch.ones(256, dtype=torch.uint8)
+    plain = {"O": 1, "lse": 2}
+    assert coda._told(plain, a, a) is plain and "ws" not in plain
+    made = coda._told(plain, None, a)
+    assert made == plain and list(made.values()) == [1, 2] and made["ws"] is a and made.get("ws") is None
+    assert coda._told(made, b, b) is made and made["ws"] is b
+    assert coda._told(made, None, a)["ws"] is a and made["ws"] is b
+    with pytest.raises(KeyError):
+        made["K"]
