@@ -119,8 +119,9 @@ FwdShape fwd_shape(int64_t Tq, int64_t n_seq, int n_q, int group) {
   return f;
 }
 // Bound on the parts (of 128 KB) that the forward's items may be cut into along
-// the keys: 0 where the items may occupy the SMs twice already, or where the
-// keys are too few to gain more than the second kernel costs.
+// the keys: 0 where the items may occupy the SMs twice already (304: two for each
+// of this chip's 152, as a number since sizes are asked for without a device
+// too), or where the keys are too few to gain more than the second kernel costs.
 int fwd_max_parts(const FwdShape& f, int64_t Tq, int64_t Tk, int64_t n_seq) {
   constexpr int64_t PARTS = 512, LEAST = 14 * coda::ATTN_BLK;
   return Tk < LEAST || (Tq / f.q_span + n_seq) * f.per > 304 ? 0 : PARTS;

@@ -9,7 +9,8 @@
 // walks query tiles (dQ, three products).  S and dO V^T are formed twice: 7
 // products where a single pass has 5, against fp32 sums of dQ over the key
 // tiles in global memory (64 KB per block pair and head, in an order that
-// changes from run to run).  Tensor bound.
+// changes from run to run).  The products bound the key-tile kernel, the waits
+// between arithmetic and products the query-tile kernel.
 //
 // The query-tile kernel runs first: it has the rows of dO at hand, forms D, and
 // leaves -lse * log2(e) and -D per row and head for the key-tile kernel.
@@ -535,10 +536,11 @@ __global__ void __launch_bounds__(256) attn_bwd_join_kernel(const AttnBwdArgs a)
 // five places behind this item's last K, so there the dQ product runs first.
 //
 // Measured: 4 sequences of 2048 tokens, 64 + 8 heads (three products, 413 GFLOP)
-// 361 us, 1140 TFLOP/s, the tensor pipe active 50 %.  A block's arithmetic (2000
-// clocks in two warpgroups) is as long as its three products, and E1, E2 and the
-// products wait for one another in turn: a form of 370 us took 367 without the
-// exponentials, 357 without the loads, 321 without the products.
+// 361 us, 1140 TFLOP/s, the tensor pipe active 50 %.  A block takes about 3000
+// clocks, more than its arithmetic (2000 in two warpgroups) or its three products
+// (2100): one 128-row tile is in flight, so E1, E2 and the products wait for one
+// another in turn.  A form of 370 us took 367 without the exponentials, 357
+// without the loads, 321 without the products.
 struct QItem {
   AttnTile t;
   int head, n;

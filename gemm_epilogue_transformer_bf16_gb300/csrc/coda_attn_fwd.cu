@@ -5,8 +5,9 @@
 //
 // in one pass over the keys with the running maximum m and sum l of each row
 // (the attention core between the QKV projection and the output projection
-// of the block).  Tensor bound: 4 * 128 multiply-adds per visible pair and
-// head against 512 bytes of K and V per key, shared by a 256-row item.
+// of the block).  Tensor bound: 2 * 128 multiply-adds (4 * 128 operations) per
+// visible pair and head against 512 bytes of K and V per key, shared by a
+// 256-row item.
 //
 // One persistent CTA per SM walks the work list.  An item is two 128-row
 // query tiles of one key/value head -- two sets of query heads on the same
@@ -31,11 +32,13 @@
 //
 // Measured: 4 sequences of 2048 tokens, 64 + 8 heads (275 GFLOP over the visible
 // pairs) 209 us, 1320 TFLOP/s; one of 16384 tokens, 32 + 8 heads 1280 us, 1720.
-// The tensor pipe is active 58 % of the first: the two products of a 128 x 128
-// block take 1250 to 1400 clocks with N = 128 and one CTA (1024 at the pipe's
-// rate), the masked half of the diagonal blocks is computed too, and O leaves in
-// front of the next tile (20 us of the 209; four warps of their own for it took
-// registers from the others: 226 to 270 us).
+// The long one is bound by the products: the two of a 128 x 128 block take 1250
+// to 1400 clocks with N = 128 and one CTA (1024 at the pipe's rate).  The first,
+// with the masked halves of its diagonal blocks, would take 169 us at that rate;
+// the other 40 are 3 us at the ends of each of an SM's 13.5 items, the first
+// softmax and O leaving without products beside them (O alone 20 us; four warps
+// of their own for it took registers from the others: 226 to 270 us).  The tensor
+// pipe is active 59 % of the first.
 //
 // Few rows over many keys leave most SMs without an item: then the keys of the
 // longer runs are cut into parts (attn_plan_kernel), which leave normalised

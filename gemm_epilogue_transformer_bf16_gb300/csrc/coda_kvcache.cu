@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(256, 8)
 // the writes and the start: 67 MB in fp32 for 8192 tokens and 8 heads, 15.8 us
 // (22.3 with 32 lanes per row and the products in fp32, where the instructions
 // were the limit; two and four rows per lane group in turn 15.8 and 16.4, and
-// 4.4 and 6.0 instead of 3.7 us for 61 tokens).
+// 4.4 and 6.0 instead of 3.7 us for 61 tokens).  In bf16, 34 MB: 12.4 us against
+// 14.4 in fp32, both back to back.
 template <bool F32>
 __global__ void __launch_bounds__(256)
     kv_read_kernel(const KvCache c, const int32_t* __restrict__ slots, int rows, void* __restrict__ K,
@@ -178,9 +179,9 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ decode
 // One query token per sequence over its cached keys and values:
 //   s_j = scale q . k_j,  O = sum_j exp(s_j - lse) v_j,
-// HBM-bound: 152 bytes per cached token and key/value head feed 4 * 128
-// multiply-adds per query head.  The cost beside the bytes is unpacking: 256
-// codes per token and head.
+// HBM-bound: 152 bytes per cached token and key/value head feed 2 * 128
+// multiply-adds (4 * 128 operations) per query head.  The cost beside the bytes
+// is unpacking: 256 codes per token and head.
 //
 // Work: every (sequence, key/value head) is cut into units of 128 keys; the
 // units of the whole batch form one line that the CTAs divide evenly, so a
@@ -209,9 +210,13 @@ __global__ void __launch_bounds__(256)
 //
 // Measured: 127 sequences of 1 to 8192 keys, 64 + 8 heads (616 MB) 132 us, 4.6
 // TB/s; four of 98304 to 131072 keys, 32 + 8 heads (560 MB) 115 us, 4.9 TB/s.
-// Without any arithmetic an earlier form's copies took 119 and 94 us: three CTAs of
-// three stages hold 175 KB of an SM's shared memory, and the unpacking (309
-// instructions per 16 keys and warp) fills 55 % of its issue slots beside them.
+// The first with 32 heads for each of 4 key/value heads (two passes of 16) 213 us,
+// with 16 heads 115 (cold).
+// Without any arithmetic an earlier form's copies and stretch ends took 119 and
+// 94 us, so these come first (with pages of 64 a unit is 12 bulk copies, eight of
+// them of 512 or 256 bytes; which of the two it is was not measured apart); the
+// unpacking (309 instructions per 16 keys and warp) fills 55 % of the issue slots
+// beside them.
 constexpr int DEC_WARPS = 4;  // computing warps
 constexpr int DEC_THREADS = (DEC_WARPS + 1) * 32;
 constexpr int DEC_STAGES = 3;

@@ -736,7 +736,9 @@ int coda_linear_cross_entropy_bwd(const coda_bf16* X, const coda_bf16* W, const 
  * [n_q, Tq] fp32.  Rows outside every sequence are neither read nor written.
  * Offsets that fall or leave [0, T] set CODA_ERR_SEQLEN_RANGE in the status
  * word and nothing is computed.  scale > 0 and finite.  P is rounded to bf16
- * before the P V product; sums, maxima and O are fp32 until O's rounding.  An
+ * before the P V product; sums, maxima and O are fp32 until O's rounding.  O is
+ * divided by the sum of the weights (up to 2^8 each) at the end: values beyond
+ * 2^120 / lk may overflow on the way.  An
  * infinity or NaN reaches tokens of its own sequence only (and there also
  * earlier ones: a zero weight times an infinite value is NaN).  Here and in
  * the calls below no output may overlap an input or another output.
@@ -814,7 +816,7 @@ int coda_kv_read_nvfp4(const uint8_t* codes, const uint8_t* sf, const float* sca
  * before the second product: by 2^-11 of themselves, or by 2^-25 of the largest
  * of them over rows that are not all zeros where that is more.  Q is scaled per
  * head by a power of two and held in f16; everything else is fp32 until O's
- * rounding.  softmax_scale > 0 and finite. */
+ * rounding, divided last as in coda_attention.  softmax_scale > 0 and finite. */
 size_t coda_attention_decode_nvfp4_workspace_size(int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
 int coda_attention_decode_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
                                 const float* scale, int64_t num_pages, int32_t page_size, const int32_t* block_table,
