@@ -32,6 +32,7 @@ __all__ = [
     "linear_cross_entropy_bwd_fp8", "linear_dswiglu_fp8", "rmsnorm_linear_dx_fp8",
     "linear_qknorm_rope_bwd_fp8", "launch_count", "attention", "attention_bwd",
     "kv_cache_nvfp4", "kv_append_nvfp4", "kv_read_nvfp4", "attention_decode_nvfp4",
+    "rope", "rope_bwd", "kv_append_rope_nvfp4", "attention_tree_nvfp4", "verify_drafts", "kv_accept_nvfp4",
     "MAP_NONE", "MAP_SWIGLU", "MAP_DSWIGLU", "MAP_QKNORM_ROPE", "MAP_CE_LSE",
     "MAP_CE_DLOGITS", "MAP_COLDOT", "MAP_SIGMOID", "MAP_DSIGMOID", "K_MAJOR", "MN_MAJOR",
 ]
@@ -133,6 +134,19 @@ _SIGS = {
     "coda_attention_decode_nvfp4_workspace_size": ([_I64, _I32, _I32, _I32], _SZ),
     "coda_attention_decode_nvfp4": ([_P, _I64, _P, _P, _P, _I64, _I32, _P, _I64, _P, _I64, _I32, _I32, _I32, _F, _P,
                                      _P, _P, _SZ, _P], ctypes.c_int),
+    "coda_rope_table_scaled": ([_F, _I32, _I32, ctypes.c_int, _F, _F, _F, _F, _F, _P, _P], ctypes.c_int),
+    "coda_rope": ([_P, _I64, _P, _P, _I32, _I32, ctypes.c_int, _P, _I64, _I64, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "coda_rope_bwd": ([_P, _I64, _P, _P, _I32, _I32, ctypes.c_int, _P, _I64, _I64, _I32, _I32, _P, _SZ, _P],
+                      ctypes.c_int),
+    "coda_kv_append_rope_nvfp4": ([_P, _I64] * 3 + [_P, _P, _P, _I32, _I32, ctypes.c_int, _P, _P, _I64, _P, _P, _P, _I64,
+                                                    _I32, _I32, _I32, _I32, _P, _SZ, _P], ctypes.c_int),
+    "coda_attention_tree_nvfp4_workspace_size": ([_I64, _I64, _I32, _I32, _I32], _SZ),
+    "coda_attention_tree_nvfp4": ([_P, _I64, _P, _P, _P, _I64, _I32, _P, _I64, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _F,
+                                   _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "coda_verify_drafts_workspace_size": ([_I64, _I64, _I64], _SZ),
+    "coda_verify_drafts": ([_P, _P, ctypes.c_int, _I64] + [_P] * 5 + [_I64] * 3 + [_P] * 4 + [_SZ, _P], ctypes.c_int),
+    "coda_kv_accept_nvfp4": ([_P, _P, _P, _I64, _I32, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I32, _I32, _P, _P, _SZ,
+                              _P], ctypes.c_int),
     "coda_noalloc_scratch_bytes": ([], _SZ),
     "coda_linear_cross_entropy_noalloc": ([_P, _P, _P, _I32, _P, _P, _P, _P, _I64, _I64, _I64, _P], ctypes.c_int),
     "coda_linear_cross_entropy_bwd_workspace_size": ([_I64, _I64, _I64], _SZ),
@@ -323,10 +337,36 @@ def rmsnorm_scale(X, gamma, eps, rstd=None, U=None, stream=None):
     return _lead(rstd, lead), _lead(U, lead)
 
 
-def rope_table(theta, head_dim, max_pos, device="cuda", out=None, stream=None):
+_ROPE_SCALING = {"linear": 1, "bands": 2, "ramp": 3}
+
+
+def rope_table(theta, head_dim, max_pos, device="cuda", out=None, stream=None, scaling=None):
+    """cos | sin [max_pos, head_dim/2, 2] (coda_rope_table).  `head_dim` is the
+    rotated part of a head where that is less than the head.  `scaling`, for
+    contexts longer than the original one (coda_rope_table_scaled), is a dict:
+    kind "linear" with factor; "bands" with factor, original, low, high; "ramp"
+    with factor, original and, unless 1 and 32, low and high; amplitude (default
+    1) multiplies cosines and sines."""
     out = torch.empty(max_pos, head_dim // 2, 2, dtype=torch.float32, device=device) if out is None else out
-    _check("coda_rope_table", load().coda_rope_table(float(theta), int(head_dim), int(max_pos),
-                                                     _f32(out, "cos_sin"), _stream(stream)))
+    if scaling is None:
+        _check("coda_rope_table", load().coda_rope_table(float(theta), int(head_dim), int(max_pos),
+                                                         _f32(out, "cos_sin"), _stream(stream)))
+        return out
+    given = dict(scaling)
+    kind = given.pop("kind", None)
+    if kind not in _ROPE_SCALING:
+        raise ValueError(f"RoPE scaling must be one of {sorted(_ROPE_SCALING)}, not {kind!r}")
+    want = {"factor": None, "amplitude": 1.0}
+    if kind != "linear":
+        want.update(original=None, low=1.0 if kind == "ramp" else None, high=32.0 if kind == "ramp" else None)
+    unknown = set(given) - set(want)
+    missing = {k for k, v in want.items() if v is None} - set(given)
+    if unknown or missing:
+        raise ValueError(f"RoPE scaling {kind!r}: " + (f"unknown {sorted(unknown)}" if unknown else f"missing {sorted(missing)}"))
+    v = {"original": 0.0, "low": 0.0, "high": 0.0, **want, **given}
+    _check("coda_rope_table_scaled", load().coda_rope_table_scaled(
+        float(theta), int(head_dim), int(max_pos), _ROPE_SCALING[kind], float(v["factor"]), float(v["original"]),
+        float(v["low"]), float(v["high"]), float(v["amplitude"]), _f32(out, "cos_sin"), _stream(stream)))
     return out
 
 
@@ -1180,4 +1220,174 @@ def attention_decode_nvfp4(Q, cache, block_table, seq_lens, n_q, scale=None, out
         q, ldq, *c, table, block_table.shape[1], lens, batch, n_q, n_kv, d, d ** -0.5 if scale is None else float(scale),
         _arg(out["O"], torch.bfloat16, (batch, n_q * d), dev, "O"),
         _arg(out["lse"], torch.float32, (batch, n_q), dev, "lse"), w, nw, _on_stream(stream, dev)))
+    return _told(out, ws, made)
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, drafted tokens
+# ---------------------------------------------------------------------------
+
+def _rope_args(pos, cos_sin, T, pairing, head_dim, dev):
+    at = _arg(pos, torch.int32, (T,), dev, "pos")
+    table = _arg(cos_sin, torch.float32, None, dev, "cos_sin")
+    if cos_sin.dim() != 3 or cos_sin.shape[2] != 2:
+        raise ValueError(f"cos_sin: expected [max_pos, rotary_dim/2, 2], got {tuple(cos_sin.shape)}")
+    return at, table, cos_sin.shape[0], 2 * cos_sin.shape[1], _pairing(pairing)
+
+
+def _rope(name, X, pos, cos_sin, n_heads, pairing, head_dim, out, key, ws, stream):
+    dev = _device(X, "X")
+    x, ldx, T = _strided(X, n_heads * head_dim, dev, "X")
+    args = _rope_args(pos, cos_sin, T, pairing, head_dim, dev)
+    out = out if out is not None else {key: _new((T, n_heads * head_dim), torch.bfloat16, dev, stream)}
+    y, ldy, Ty = _strided(out[key], n_heads * head_dim, dev, key)
+    if Ty != T:
+        raise ValueError(f"{key}: expected {T} rows, got {Ty}")
+    w, nw, made = _scratch(ws, 256, dev, stream)
+    _check(name, getattr(load(), name)(x, ldx, *args, y, ldy, T, n_heads, head_dim, w, nw, _on_stream(stream, dev)))
+    return _told(out, ws, made)
+
+
+def rope(X, pos, cos_sin, n_heads, pairing="interleaved", head_dim=128, out=None, ws=None, stream=None):
+    """Rotary positions (coda_rope): X [T, n_heads*128], whose rows may be columns
+    of a wider tensor, pos [T] int32, cos_sin [max_pos, rotary_dim/2, 2] from
+    rope_table; the first rotary_dim elements of every head are rotated.  Returns
+    Y [T, n_heads*128]; out={"Y": X} rotates in place.  Without `ws`,
+    result["ws"] holds the status word."""
+    return _rope("coda_rope", X, pos, cos_sin, n_heads, pairing, head_dim, out, "Y", ws, stream)
+
+
+def rope_bwd(dY, pos, cos_sin, n_heads, pairing="interleaved", head_dim=128, out=None, ws=None, stream=None):
+    """Gradient dX [T, n_heads*128] of rope for the upstream gradient dY
+    (coda_rope_bwd), with the same arguments."""
+    return _rope("coda_rope_bwd", dY, pos, cos_sin, n_heads, pairing, head_dim, out, "dX", ws, stream)
+
+
+def kv_append_rope_nvfp4(K, V, slots, cache, pos, cos_sin, Q=None, n_q=0, pairing="interleaved", keep_k=False, out=None,
+                         ws=None, stream=None):
+    """kv_append_nvfp4 with the rotation on the way (coda_kv_append_rope_nvfp4):
+    K is rotated by pos [T] int32 and cos_sin before it is quantised.  Returns
+    the rotated queries "Q" [T, n_q*128] of Q, if given, and with keep_k the
+    rotated keys "K" [T, n_kv*128].  Without `ws`, result["ws"] holds the status
+    word."""
+    dev = _device(K, "K")
+    c, n_kv, d = _cache_args(cache, dev)
+    k, ldk, T = _strided(K, n_kv * d, dev, "K")
+    v, ldv, Tv = _strided(V, n_kv * d, dev, "V")
+    if Tv != T:
+        raise ValueError(f"K has {T} rows, V {Tv}")
+    if (Q is None) != (n_q == 0):
+        raise ValueError("Q and n_q: give both or none")
+    q, ldq, Tq = _strided(Q, n_q * d, dev, "Q") if Q is not None else (None, 0, T)
+    if Tq != T:
+        raise ValueError(f"K has {T} rows, Q {Tq}")
+    at = _arg(slots, torch.int32, (T,), dev, "slots")
+    args = _rope_args(pos, cos_sin, T, pairing, d, dev)
+    if out is None:
+        out = {}
+        if Q is not None:
+            out["Q"] = _new((T, n_q * d), torch.bfloat16, dev, stream)
+        if keep_k:
+            out["K"] = _new((T, n_kv * d), torch.bfloat16, dev, stream)
+    to = (_arg(out["Q"], torch.bfloat16, (T, n_q * d), dev, "Q out") if Q is not None else None,
+          _arg(out["K"], torch.bfloat16, (T, n_kv * d), dev, "K out") if keep_k else None)
+    w, nw, made = _scratch(ws, 256, dev, stream)
+    _check("coda_kv_append_rope_nvfp4", load().coda_kv_append_rope_nvfp4(
+        q, ldq, k, ldk, v, ldv, at, *args, *to, T, *c, n_q, n_kv, d, w, nw, _on_stream(stream, dev)))
+    return _told(out, ws, made)
+
+
+def _table_arg(block_table, batch, dev):
+    table = _arg(block_table, torch.int32, None, dev, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table: expected [{batch}, max_pages], got {tuple(block_table.shape)}")
+    return table, block_table.shape[1]
+
+
+def _offsets(cu_seqlens, dev):
+    cu = _arg(cu_seqlens, torch.int32, None, dev, "cu_seqlens")
+    batch = cu_seqlens.numel() - 1
+    if batch < 0 or cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens: expected batch + 1 offsets")
+    return cu, batch
+
+
+def attention_tree_nvfp4(Q, cache, block_table, seq_lens, cu_seqlens, n_q, parents=None, scale=None, out=None, ws=None,
+                         stream=None):
+    """Attention of drafted tokens over the cache (coda_attention_tree_nvfp4): Q
+    [T, n_q*128], sequence b's tokens in rows cu_seqlens[b] .. cu_seqlens[b + 1],
+    which are also the last of its seq_lens[b] cached ones; each sees the tokens
+    before them, its ancestors by parents [T] int32 (numbers within the tree, -1:
+    none; without parents: a chain) and itself.  Returns O [T, n_q*128] and lse
+    [T, n_q]; rows outside every sequence stay as they are (undefined in tensors
+    allocated here).  Without `ws`, result["ws"] holds the status word."""
+    lib = load()
+    dev = _device(Q, "Q")
+    c, n_kv, d = _cache_args(cache, dev)
+    q, ldq, T = _strided(Q, n_q * d, dev, "Q")
+    cu, batch = _offsets(cu_seqlens, dev)
+    table, pages = _table_arg(block_table, batch, dev)
+    lens = _arg(seq_lens, torch.int32, (batch,), dev, "seq_lens")
+    up = _arg(parents, torch.int32, (T,), dev, "parents")
+    out = out if out is not None else {"O": _new((T, n_q * d), torch.bfloat16, dev, stream),
+                                       "lse": _new((T, n_q), torch.float32, dev, stream)}
+    w, nw, made = _scratch(ws, lib.coda_attention_tree_nvfp4_workspace_size(T, batch, n_q, n_kv, d), dev, stream)
+    _check("coda_attention_tree_nvfp4", lib.coda_attention_tree_nvfp4(
+        q, ldq, *c, table, pages, lens, cu, up, T, batch, n_q, n_kv, d, d ** -0.5 if scale is None else float(scale),
+        _arg(out["O"], torch.bfloat16, (T, n_q * d), dev, "O"), _arg(out["lse"], torch.float32, (T, n_q), dev, "lse"), w, nw,
+        _on_stream(stream, dev)))
+    return _told(out, ws, made)
+
+
+def verify_drafts(probs, tokens, cu_seqlens, u, u_next, width, parents=None, draft_probs=None, out=None, ws=None,
+                  stream=None):
+    """Verification of drafted tokens (coda_verify_drafts): probs [T, V] in
+    torch.float32 or torch.bfloat16, the target's probabilities after each node of
+    the trees (or chains: no parents) in rows cu_seqlens[b] .. cu_seqlens[b + 1];
+    tokens [T] int32; u [T] and u_next [batch] random numbers in [0, 1);
+    draft_probs [T, V] those that a node's children were drawn from, None where
+    they were not drawn.  Returns count [batch], nodes and tokens [batch, width]:
+    node 0 and the accepted ones, their tokens and the next, -1 behind.  Without
+    `ws`, result["ws"] holds the status word."""
+    lib = load()
+    dev = _device(probs, "probs")
+    if probs.dim() != 2 or probs.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"probs: expected [T, V] in torch.float32 or torch.bfloat16, got {tuple(probs.shape)} {probs.dtype}")
+    T, V = probs.shape
+    p = _arg(probs, probs.dtype, None, dev, "probs")
+    q = _arg(draft_probs, probs.dtype, (T, V), dev, "draft_probs")
+    cu, batch = _offsets(cu_seqlens, dev)
+    x = _arg(tokens, torch.int32, (T,), dev, "tokens")
+    up = _arg(parents, torch.int32, (T,), dev, "parents")
+    uu = (_arg(u, torch.float32, (T,), dev, "u"), _arg(u_next, torch.float32, (batch,), dev, "u_next"))
+    if out is None:
+        out = {k: _new(s, torch.int32, dev, stream)
+               for k, s in (("count", (batch,)), ("nodes", (batch, width)), ("tokens", (batch, width)))}
+    to = (_arg(out["count"], torch.int32, (batch,), dev, "count"), _arg(out["nodes"], torch.int32, (batch, width), dev, "nodes"),
+          _arg(out["tokens"], torch.int32, (batch, width), dev, "tokens out"))
+    w, nw, made = _scratch(ws, lib.coda_verify_drafts_workspace_size(T, batch, V), dev, stream)
+    _check("coda_verify_drafts", lib.coda_verify_drafts(p, q, F32 if probs.dtype is torch.float32 else BF16, V, x, cu, up, *uu,
+                                                        T, batch, width, *to, w, nw, _on_stream(stream, dev)))
+    return _told(out, ws, made)
+
+
+def kv_accept_nvfp4(cache, block_table, seq_lens, cu_seqlens, nodes, count, out=None, ws=None, stream=None):
+    """The cache rows of the accepted nodes move to the places behind the prefix
+    (coda_kv_accept_nvfp4): nodes [batch, width] and count [batch] int32 from
+    verify_drafts, the others as for attention_tree_nvfp4.  Returns the new
+    "seq_lens" [batch].  Without `ws`, result["ws"] holds the status word."""
+    dev = _device(cache["scale"], "cache scale")
+    c, n_kv, d = _cache_args(cache, dev)
+    cu, batch = _offsets(cu_seqlens, dev)
+    table, pages = _table_arg(block_table, batch, dev)
+    lens = _arg(seq_lens, torch.int32, (batch,), dev, "seq_lens")
+    path = _arg(nodes, torch.int32, None, dev, "nodes")
+    if nodes.dim() != 2 or nodes.shape[0] != batch:
+        raise ValueError(f"nodes: expected [{batch}, width], got {tuple(nodes.shape)}")
+    took = _arg(count, torch.int32, (batch,), dev, "count")
+    out = out if out is not None else {"seq_lens": _new((batch,), torch.int32, dev, stream)}
+    w, nw, made = _scratch(ws, 256, dev, stream)
+    _check("coda_kv_accept_nvfp4", load().coda_kv_accept_nvfp4(
+        *c, table, pages, lens, cu, path, nodes.shape[1], took, batch, n_kv, d,
+        _arg(out["seq_lens"], torch.int32, (batch,), dev, "new seq_lens"), w, nw, _on_stream(stream, dev)))
     return _told(out, ws, made)

@@ -7,10 +7,8 @@
 #include <cstring>
 #include <mutex>
 
-#include "coda.h"
-#include "coda_attn.cuh"
+#include "coda_attn_host.h"
 #include "coda_internal.h"
-#include "coda_kvcache.cuh"
 #include "coda_status.h"
 
 namespace coda {
@@ -41,37 +39,7 @@ cudaError_t attn_smem_attribute(const void* kernel, int id, uint32_t bytes) {
 
 namespace {
 
-constexpr size_t HEADER = 256;
 constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;  // 2 s per pipeline wait
-constexpr double LOG2E = 1.4426950408889634074;
-
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Lays out (base == nullptr: only sizes) consecutive 256-byte aligned arrays.
-struct Cursor {
-  uint8_t* base;
-  size_t off = HEADER;
-  template <class T>
-  T* take(int64_t count) {
-    T* p = base ? reinterpret_cast<T*>(base + off) : nullptr;
-    off = up256(off + static_cast<size_t>(count) * sizeof(T));
-    return p;
-  }
-};
-
-// Shapes both directions share.  CODA_OK, or the error to return.
-int check_shape(int64_t Tq, int64_t Tk, int64_t n_seq, int32_t n_q, int32_t n_kv, int32_t head_dim, float scale) {
-  if (Tq < 0 || Tk < 0 || n_seq < 0 || n_q <= 0 || n_kv <= 0) return CODA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return CODA_ERR_INVALID_ARG;
-  if (head_dim != coda::ATTN_D || n_q % n_kv != 0) return CODA_ERR_UNSUPPORTED;
-  // rows and work items are counted in 32 bits on the device
-  constexpr int64_t LIM = int64_t(1) << 30;
-  if (Tq >= LIM || Tk >= LIM || n_seq >= LIM / 4 || n_q >= 65536) return CODA_ERR_UNSUPPORTED;
-  if ((std::max(Tq / 32, Tk / coda::ATTN_BLK) + n_seq + 1) * n_q >= (int64_t(1) << 31)) return CODA_ERR_UNSUPPORTED;
-  return CODA_OK;
-}
 
 // Heads that share a 128-row tile (a power of two dividing the group).  With
 // one head a tile covers 128 tokens, so sequences of a few tokens would leave
@@ -145,38 +113,6 @@ bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t
   return coda::encode_bf16_map(m, p, 2, dims, st, box);
 }
 
-#define CK(x)                     \
-  do {                            \
-    int _r = (x);                 \
-    if (_r != CODA_OK) return _r; \
-  } while (0)
-#define CU(x) \
-  do { if ((x) != cudaSuccess) return CODA_ERR_CUDA; } while (0)
-
-// The cache's shape; CODA_OK or the error to return.
-int check_cache(coda::KvCache& c, const uint8_t* codes, const uint8_t* sf, const float* scale, int64_t num_pages,
-                int32_t page_size, int32_t n_kv, int32_t head_dim) {
-  if (num_pages < 0 || page_size <= 0 || n_kv <= 0) return CODA_ERR_INVALID_ARG;
-  if (head_dim != coda::ATTN_D || page_size < 16 || (page_size & (page_size - 1)) || n_kv >= 65536)
-    return CODA_ERR_UNSUPPORTED;
-  if (num_pages * page_size >= (int64_t(1) << 31)) return CODA_ERR_UNSUPPORTED;  // slots are 32-bit
-  if (num_pages > 0 && (!codes || !sf || !scale)) return CODA_ERR_INVALID_ARG;
-  if (!al16(codes) || !al16(sf) || !al16(scale)) return CODA_ERR_ALIGNMENT;
-  c.codes = const_cast<uint8_t*>(codes);
-  c.sf = const_cast<uint8_t*>(sf);
-  c.scale = const_cast<float*>(scale);
-  c.num_pages = static_cast<int>(num_pages);
-  c.page_shift = 0;
-  while ((1 << c.page_shift) < page_size) ++c.page_shift;
-  c.n_kv = n_kv;
-  return CODA_OK;
-}
-
-int check_ws(const void* ws, size_t have, size_t need) {
-  if (!ws || have < need) return CODA_ERR_WORKSPACE;
-  return al16(ws) ? CODA_OK : CODA_ERR_ALIGNMENT;
-}
-
 struct DecodeLayout {
   int* units;
   float* part;
@@ -188,9 +124,6 @@ void lay_decode(Cursor& c, DecodeLayout& l, int64_t batch, int group) {
   l.part = c.take<float>(int64_t(2) * coda::DEC_MAX_CTAS * heads * coda::ATTN_D);
   l.part_lse = c.take<float>(int64_t(2) * coda::DEC_MAX_CTAS * heads);
 }
-
-const __nv_bfloat16* B(const coda_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
-__nv_bfloat16* B(coda_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
 
 }  // namespace
 

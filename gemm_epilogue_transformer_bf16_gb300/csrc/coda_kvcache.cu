@@ -1,55 +1,17 @@
 // The 4-bit key/value cache (NVFP4 rows): append, read back, and attention of
 // one new token per sequence over it.
 #include <algorithm>
-#include <cuda_fp16.h>
-#include <cuda_fp4.h>
-#include <cuda_fp8.h>
 
 #include "coda_attn.cuh"
 #include "coda_internal.h"
-#include "coda_kvcache.cuh"
+#include "coda_kvrow.cuh"
 #include "coda_status.h"
 
 namespace coda {
 namespace {
 
-__device__ __forceinline__ int64_t cache_row(const KvCache& c, int page, int plane, int h, int off) {
-  return ((static_cast<int64_t>(page) * 2 + plane) * c.n_kv + h << c.page_shift) + off;
-}
-
-// The eight codes of a word as four f16 pairs (byte by byte, low nibble
-// first), exact: the conversion takes its byte from the register, without
-// shifts and masks.
-__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
-__device__ __forceinline__ float e4m3_f32(uint32_t b) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3);
-  return __half2float(__half(h));
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ float f16_lo(uint32_t v) { return __half2float(__ushort_as_half(v & 0xFFFFu)); }
-__device__ __forceinline__ float f16_hi(uint32_t v) { return __half2float(__ushort_as_half(v >> 16)); }
-
 // ------------------------------------------------------------------ append
-// Eight lanes per row of 128, one 16-element block each; every arithmetic
-// step is one fp32 operation, the same steps as quantize_nvfp4_rows, so the
-// codes and scales agree with it bit for bit.  HBM-bound: 512 bytes in and
+// Eight lanes per row of 128, one 16-element block each (quantise_row16).  HBM-bound: 512 bytes in and
 // 152 out per token and head, 11.6 us for 8192 tokens and 8 heads (44 MB; 12.3
 // with the 36 registers that six blocks per SM leave).
 // One row per lane group, many blocks: with four rows per group in flight
@@ -81,33 +43,9 @@ __global__ void __launch_bounds__(256, 8)
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.f;
   }
-  float bmax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) bmax = fmaxf(bmax, fabsf(x[i]));
-  float amax = bmax;
-#pragma unroll
-  for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float s = amax > 0.f ? __fdiv_rn(amax, 2688.0f) : 1.0f;
-  const float sf_f = fminf(__fdiv_rn(bmax, __fmul_rn(6.0f, s)), 448.0f);
-  const uint32_t sfb = __nv_cvt_float_to_fp8(sf_f, __NV_SATFINITE, __NV_E4M3);
-  const float denom = __fmul_rn(e4m3_f32(sfb), s);
-  uint32_t w[2] = {0, 0};
-  if (denom > 0.f) {
-    const float inv = fminf(__fdiv_rn(1.0f, denom), 3.40282347e38f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t c2 = __nv_cvt_float2_to_fp4x2(make_float2(__fmul_rn(x[2 * i], inv), __fmul_rn(x[2 * i + 1], inv)),
-                                                   __NV_E2M1, cudaRoundNearest);
-      w[i >> 2] |= (c2 & 0xFFu) << (8 * (i & 3));
-    }
-    // no negative zero: clear the sign of codes whose magnitude bits are 0
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t mag = w[i] & 0x77777777u;
-      const uint32_t any = (mag | (mag << 1) | (mag << 2)) & 0x44444444u;
-      w[i] &= 0x77777777u | (any << 1);
-    }
-  }
+  uint32_t w[2], sfb;
+  float s;
+  quantise_row16(x, w, sfb, s);
   if (at >= 0) {
     *reinterpret_cast<uint2*>(c.codes + at * 64 + sub * 8) = make_uint2(w[0], w[1]);
     c.sf[at * 8 + sub] = static_cast<uint8_t>(sfb);
@@ -173,6 +111,81 @@ __global__ void __launch_bounds__(256)
     dst[16] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
     store_bf16x8(static_cast<__nv_bfloat16*>(plane ? V : K) + at + sub * 8, v);
+  }
+}
+
+// ------------------------------------------------------------------ accept
+// The rows of a tree's accepted nodes move to the places behind the prefix, in
+// the order of the path: place d takes node path[d] >= d.  A warp per sequence,
+// plane and head, four lanes per row; eight rows are read, then written, and
+// the rows of later steps lie behind every place written so far.
+__global__ void __launch_bounds__(256) kv_accept_kernel(const AcceptArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const KvCache& c = a.c;
+  const int w = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int b = w / (2 * c.n_kv), rest = w - b * 2 * c.n_kv;
+  if (b >= a.B) return;
+  const int plane = rest >= c.n_kv, h = rest - plane * c.n_kv;
+  const bool tell = rest == 0 && lane == 0;
+  const int q0 = a.cu[b], q1 = a.cu[b + 1], len = a.seq_lens[b];
+  const int n = q1 - q0;
+  if (q0 < 0 || n < 0 || len < n || len > (static_cast<int64_t>(a.max_pages) << c.page_shift)) {
+    if (tell) {
+      atomicOr(a.status, CODA_DEV_SEQLEN_RANGE);
+      a.out_lens[b] = 0;
+    }
+    return;
+  }
+  int count = n > 0 ? a.count[b] : 0;
+  const int32_t* path = a.nodes + static_cast<int64_t>(b) * a.width;
+  bool bad = count < 0 || (n > 0 && (count >= n || count >= a.width));
+  // a path rises from node 0: then no row is overwritten before it is read
+  for (int d = lane; !bad && d <= count && n > 0; d += 32) {
+    const int at = path[d];
+    bad = at >= n || (d == 0 ? at != 0 : at <= path[d - 1]);
+  }
+  if (__any_sync(0xffffffffu, bad)) {
+    if (tell) {
+      atomicOr(a.status, CODA_DEV_TREE_RANGE);
+      a.out_lens[b] = len - n;
+    }
+    return;
+  }
+  if (tell) a.out_lens[b] = n > 0 ? len - n + count + 1 : len;
+  const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+  const int part = lane & 3;
+  auto row_of = [&](int node) {
+    const int k = len - n + node, page = table[k >> c.page_shift];
+    if (page < 0 || page >= c.num_pages) {
+      if (rest == 0 && part == 0) atomicOr(a.status, CODA_DEV_PAGE_RANGE);
+      return static_cast<int64_t>(-1);
+    }
+    return cache_row(c, page, plane, h, k & ((1 << c.page_shift) - 1));
+  };
+  for (int d0 = 1; d0 <= count; d0 += 8) {
+    const int d = d0 + (lane >> 2);
+    int64_t to = -1;
+    uint4 codes = make_uint4(0, 0, 0, 0);
+    uint16_t sf = 0;
+    float scale = 0.f;
+    if (d <= count) {
+      const int node = path[d];
+      const int64_t from = node != d ? row_of(node) : -1;
+      to = from >= 0 ? row_of(d) : -1;
+      if (to >= 0) {
+        codes = reinterpret_cast<const uint4*>(c.codes + from * 64)[part];
+        sf = reinterpret_cast<const uint16_t*>(c.sf + from * 8)[part];
+        if (part == 0) scale = c.scale[from];
+      }
+    }
+    __syncwarp();
+    if (to >= 0) {
+      reinterpret_cast<uint4*>(c.codes + to * 64)[part] = codes;
+      reinterpret_cast<uint16_t*>(c.sf + to * 8)[part] = sf;
+      if (part == 0) c.scale[to] = scale;
+    }
+    __syncwarp();
   }
 }
 
@@ -842,6 +855,10 @@ cudaError_t launch_kv_read(const KvCache& c, const int32_t* slots, int rows, voi
   const unsigned grid = static_cast<unsigned>((rows - 1) / 16 + 1);
   return f32 ? attn_launch(kv_read_kernel<true>, grid, 256, 0, s, c, slots, rows, K, V, status)
              : attn_launch(kv_read_kernel<false>, grid, 256, 0, s, c, slots, rows, K, V, status);
+}
+
+cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s) {
+  return attn_launch(kv_accept_kernel, (static_cast<int64_t>(a.B) * 2 * a.c.n_kv + 7) / 8, 256, 0, s, a);
 }
 
 cudaError_t launch_attn_decode(const DecodeArgs& a, int sms, cudaStream_t s) {

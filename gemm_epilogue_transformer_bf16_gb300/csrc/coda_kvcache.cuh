@@ -28,6 +28,17 @@ cudaError_t launch_kv_append(const KvCache& c, const __nv_bfloat16* K, int64_t l
 cudaError_t launch_kv_read(const KvCache& c, const int32_t* slots, int rows, void* K, void* V, bool f32, int* status,
                            cudaStream_t s);
 
+struct AcceptArgs {
+  KvCache c;
+  const int32_t* table;  // [B, max_pages]
+  int max_pages;
+  const int32_t *seq_lens, *cu, *nodes, *count;  // [B], [B + 1], [B, width], [B]
+  int B, width;
+  int32_t* out_lens;     // [B]
+  int* status;
+};
+cudaError_t launch_kv_accept(const AcceptArgs& a, cudaStream_t s);
+
 constexpr int DEC_MAX_CTAS = 3 * 160;  // partial results reserved for this many CTAs
 constexpr int DEC_HEADS = 16;          // query heads of one pass over a key/value head's rows
 

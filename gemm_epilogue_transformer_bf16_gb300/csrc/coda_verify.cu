@@ -1,0 +1,409 @@
+// Verification of drafted tokens against the target's probabilities, from given
+// random numbers.
+//
+// The walk begins at node 0 with w = p_0, Z = 1.  A child i of the node where it
+// stands, in order of their numbers, with token x:
+//   u_i q(x) Z < w(x): accepted, the walk goes on there with w = p_i, Z = 1;
+//   else               w <- max(w - Z q, 0), Z <- sum w
+// (q: the probabilities the node's children were drawn from; without them, drafts
+// that were not drawn, q is 1 at x and 0 elsewhere: w(x) <- 0, Z <- Z - w(x)).
+// Where no child is left the next token is the first x with
+//   sum_{y <= x} w(y) > u sum w,
+// so that the tokens together are distributed as the target's own.
+//
+// A decision at the edge of a step of a sum over 10^5 tokens must not depend on
+// the order of the sum: fp32 sums of a vocabulary are off by more than many
+// tokens' probability.  The weights are therefore integers in units of 2^-60
+// (the probabilities' own bits down to there, smaller ones are dropped), and
+// their sums are exact in any order.
+//
+// HBM-bound: one row of p and q per request (the walk before it reads two values
+// per node), and bound by latency when there are few.  A cluster of eight CTAs
+// per request: every CTA walks for itself on the nodes' values in shared memory,
+// sums over the vocabulary are split between the CTAs and meet by distributed
+// shared memory.
+#include <algorithm>
+#include <cuda_bf16.h>
+
+#include "coda_attn.cuh"
+#include "coda_internal.h"
+#include "coda_status.h"
+#include "coda_verify.cuh"
+
+namespace coda {
+namespace {
+
+constexpr int VF_CTAS = 8;
+constexpr int VF_THREADS = 512;
+constexpr int VF_WARPS = VF_THREADS / 32;
+typedef unsigned long long u64;
+
+__device__ __forceinline__ u64 ld_cluster_u64(const void* p, uint32_t rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(p, rank)) : "memory");
+  return v;
+}
+
+// A probability in units of 2^-60; NaN and negative values count as 0, values
+// above 1 as 1.
+__device__ __forceinline__ u64 fixed60(float p) {
+  return p > 0.f ? __float2ull_rz(fminf(p, 1.f) * 0x1p60f) : 0ull;
+}
+// Z q, both in units of 2^-60.
+__device__ __forceinline__ u64 scaled60(u64 Z, u64 q) { return __umul64hi(Z << 2, q << 2); }
+
+template <bool F32>
+__device__ __forceinline__ float value(const void* base, int64_t at) {
+  if constexpr (F32) return static_cast<const float*>(base)[at];
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  return v;
+}
+
+struct VerifyShared {
+  u64 Z[VERIFY_MAX_NODES];  // Z after each refusal at the node (Z[0] = 1)
+  u64 warp[VF_WARPS], fine[VF_WARPS];
+  u64 total;                // of this CTA, read by the others
+  float p[VERIFY_MAX_NODES], q[VERIFY_MAX_NODES], u[VERIFY_MAX_NODES];
+  int token[VERIFY_MAX_NODES], parent[VERIFY_MAX_NODES];
+  int gone[VERIFY_MAX_NODES];  // tokens refused at the node (drafts not drawn)
+};
+
+// Weights of the row where the walk stands.  A row is read in aligned pieces
+// of 16 bytes, numbered from the one that holds its first element: E elements,
+// the first `lead` elements of piece 0 belong to the row before.
+template <bool F32>
+struct Row {
+  static constexpr int E = F32 ? 4 : 8;
+  const void *p, *q;  // row starts; q null: drafts not drawn
+  int lead, V;
+  int refused;        // refusals that w has gone through
+  __device__ __forceinline__ int pieces() const { return (V + lead + E - 1) / E; }
+
+  // A piece as it lies in memory, zeros outside the row.
+  __device__ __forceinline__ uint4 load(const void* base, int piece) const {
+    const int e0 = piece * E - lead;
+    if (e0 >= 0 && e0 + E <= V)
+      return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + static_cast<int64_t>(e0) * (16 / E));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (e0 + i >= 0 && e0 + i < V) {
+        const uint32_t bits = __float_as_uint(value<F32>(base, e0 + i));
+        w[F32 ? i : i >> 1] |= F32 ? bits : (i & 1) ? bits : bits >> 16;
+      }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ float element(const uint4& v, int i) {
+    const uint32_t w = (F32 ? i : i >> 1) == 0 ? v.x : (F32 ? i : i >> 1) == 1 ? v.y : (F32 ? i : i >> 1) == 2 ? v.z : v.w;
+    return F32 ? __uint_as_float(w) : (i & 1) ? bf16_hi(w) : bf16_lo(w);
+  }
+  __device__ __forceinline__ u64 weight(float pv, float qv, const u64* Z) const {
+    u64 w = fixed60(pv);
+    if (q == nullptr) return w;
+    const u64 fq = fixed60(qv);
+    for (int k = 0; k < refused; ++k) {
+      const u64 d = k == 0 ? fq : scaled60(Z[k], fq);
+      w = w > d ? w - d : 0;
+    }
+    return w;
+  }
+  __device__ __forceinline__ bool need_q() const { return q != nullptr && refused > 0; }
+};
+
+// Sum of the weights in [piece, stop) by stride; tokens refused where nothing
+// was drawn are left out by the caller.
+template <bool F32>
+__device__ __forceinline__ u64 sum_pieces(const Row<F32>& r, int piece, int stride, int stop, const u64* Z) {
+  u64 s = 0;
+  constexpr int N = 4;  // pieces in flight
+  for (; piece < stop; piece += N * stride) {
+    uint4 vp[N], vq[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const bool in = piece + n * stride < stop;
+      vp[n] = in ? r.load(r.p, piece + n * stride) : make_uint4(0, 0, 0, 0);
+      vq[n] = in && r.need_q() ? r.load(r.q, piece + n * stride) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < Row<F32>::E; ++i) s += r.weight(r.element(vp[n], i), r.element(vq[n], i), Z);
+  }
+  return s;
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs a) {
+  __shared__ VerifyShared sh;
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int E = Row<F32>::E;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int b = static_cast<int>(blockIdx.x) / VF_CTAS;
+  const int t0 = a.cu[b], t1 = a.cu[b + 1];
+  const int n = t1 - t0;
+  int32_t* nodes = a.nodes + static_cast<int64_t>(b) * a.width;
+  int32_t* out = a.out + static_cast<int64_t>(b) * a.width;
+  const bool off = t0 < 0 || n < 0 || t1 > a.T;
+  if (off || n == 0 || n > VERIFY_MAX_NODES) {
+    if (rank == 0) {
+      if (tid == 0) {
+        a.count[b] = 0;
+        if (off) atomicOr(a.status, CODA_DEV_SEQLEN_RANGE);
+        else if (n > 0) atomicOr(a.status, CODA_DEV_TREE_RANGE);
+      }
+      for (int i = tid; i < a.width; i += VF_THREADS) nodes[i] = out[i] = -1;
+    }
+    return;  // the whole cluster
+  }
+  // what the walk looks at
+  for (int i = tid; i < n; i += VF_THREADS) {
+    int up = i - 1, x = a.tokens[t0 + i];
+    if (a.parents) up = a.parents[t0 + i];
+    bool bad = up < -1 || up >= i;
+    if (bad && rank == 0) atomicOr(a.status, CODA_DEV_TREE_RANGE);
+    if (bad) up = -1;
+    if (i > 0 && up >= 0 && (x < 0 || x >= a.V)) {
+      if (rank == 0) atomicOr(a.status, CODA_DEV_LABEL_RANGE);
+      up = -1;  // never a child
+    }
+    const int64_t at = static_cast<int64_t>(t0 + max(up, 0)) * a.V + x;
+    sh.parent[i] = up;
+    sh.token[i] = x;
+    sh.u[i] = a.u[t0 + i];
+    sh.p[i] = up >= 0 ? value<F32>(a.P, at) : 0.f;
+    sh.q[i] = up >= 0 && a.Q ? value<F32>(a.Q, at) : 1.f;
+  }
+  __syncthreads();
+
+  Row<F32> r;
+  auto stand = [&](int node) {
+    const int64_t at = static_cast<int64_t>(t0 + node) * a.V;
+    r.p = F32 ? static_cast<const void*>(static_cast<const float*>(a.P) + at)
+              : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.P) + at);
+    r.q = !a.Q ? nullptr
+               : F32 ? static_cast<const void*>(static_cast<const float*>(a.Q) + at)
+                     : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.Q) + at);
+    r.V = static_cast<int>(a.V);
+    r.lead = static_cast<int>(at % E);
+    r.refused = 0;
+  };
+  // this CTA's and this warp's pieces
+  int c0 = 0, c1 = 0, w0 = 0, w1 = 0;
+  auto share = [&]() {
+    const int all = r.pieces(), per = (all + VF_CTAS - 1) / VF_CTAS;
+    c0 = min(all, static_cast<int>(rank) * per);
+    c1 = min(all, c0 + per);
+    const int pw = (c1 - c0 + VF_WARPS - 1) / VF_WARPS;
+    w0 = min(c1, c0 + warp * pw);
+    w1 = min(c1, w0 + pw);
+  };
+  // Weights that the refused tokens of a draft not drawn still have in [w0, w1).
+  auto refused_in = [&](int gone, int from, int to) {
+    u64 s = 0;
+    if (r.q == nullptr)
+      for (int k = lane; k < gone; k += 32) {
+        const int x = sh.gone[k], at = (x + r.lead) / E;
+        bool again = false;
+        for (int j = 0; j < k; ++j) again |= sh.gone[j] == x;
+        if (!again && at >= from && at < to) s += fixed60(value<F32>(r.p, x));
+      }
+    return warp_sum(s);
+  };
+  // Sum over the vocabulary; sh.warp holds the warps' parts of this CTA, and
+  // `before` what the CTAs in front of it have.
+  auto total = [&](int gone, u64& before) {
+    share();
+    const u64 s = warp_sum(sum_pieces<F32>(r, w0 + lane, 32, w1, sh.Z)) - refused_in(gone, w0, w1);
+    if (lane == 0) sh.warp[warp] = s;
+    __syncthreads();
+    if (tid == 0) {
+      u64 c = 0;
+#pragma unroll
+      for (int i = 0; i < VF_WARPS; ++i) c += sh.warp[i];
+      sh.total = c;
+    }
+    cluster_sync();
+    u64 all = 0;
+    before = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < VF_CTAS; ++i) {
+      const u64 c = ld_cluster_u64(&sh.total, i);
+      if (i < rank) before += c;
+      all += c;
+    }
+    cluster_sync();  // read by all before it is written again, or its CTA ends
+    return all;
+  };
+
+  // Every thread walks, on the same values.
+  int here = 0, count = 0, gone = 0, known = 0;  // known: refusals whose Z is there
+  double Z = 1.0;
+  u64 before = 0;
+  stand(0);
+  if (rank == 0 && tid == 0) nodes[0] = 0;
+  if (tid == 0) sh.Z[0] = 1ull << 60;
+  __syncthreads();
+  for (int i = 1; i < n && count + 1 < a.width; ++i) {
+    if (sh.parent[i] != here) continue;
+    const int x = sh.token[i];
+    double wx = sh.p[i];
+    if (a.Q) {
+      if (r.refused > known) {  // a refusal before this child: its sum is wanted now
+        const u64 z = total(0, before);
+        if (tid == 0) sh.Z[r.refused] = z;
+        __syncthreads();
+        known = r.refused;
+        Z = static_cast<double>(z) * 0x1p-60;
+      }
+      if (r.refused > 0) wx = static_cast<double>(r.weight(sh.p[i], sh.q[i], sh.Z)) * 0x1p-60;
+    } else {
+      for (int k = 0; k < gone; ++k)
+        if (sh.gone[k] == x) wx = 0.0;
+    }
+    if (static_cast<double>(sh.u[i]) * (static_cast<double>(sh.q[i]) * Z) < wx) {
+      if (rank == 0 && tid == 0) {
+        out[count] = x;
+        nodes[count + 1] = i;
+      }
+      ++count;
+      here = i;
+      Z = 1.0;
+      gone = known = 0;
+      stand(i);
+    } else if (a.Q) {
+      ++r.refused;
+    } else {
+      Z -= wx;
+      __syncthreads();
+      if (tid == 0) sh.gone[gone] = x;
+      __syncthreads();
+      ++gone;
+    }
+  }
+
+  // The next token.  Nothing left (probabilities that do not sum to 1): the
+  // row's own probabilities; none there either: -1.
+  u64 all = total(gone, before);
+  if (all == 0 && (r.refused > 0 || gone > 0)) {
+    r.refused = 0;
+    gone = 0;
+    all = total(0, before);
+  }
+  const float un = a.u_next[b];
+  u64 tau = un > 0.f ? static_cast<u64>(fmin(static_cast<double>(un), 1.0) * static_cast<double>(all)) : 0;
+  if (tau >= all && all > 0) tau = all - 1;
+  if (rank == 0) {
+    if (tid == 0) {
+      a.count[b] = count;
+      if (all == 0) out[count] = -1;
+    }
+    for (int i = count + 1 + tid; i < a.width; i += VF_THREADS) nodes[i] = out[i] = -1;
+  }
+  u64 mine = 0;
+#pragma unroll
+  for (int i = 0; i < VF_WARPS; ++i) mine += sh.warp[i];
+  if (all == 0 || tau < before || tau - before >= mine) return;
+  // In this CTA.  The warp's share that holds it, cut into pieces of 32 ...
+  u64 left = tau - before;  // the token's weight passes this
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < VF_WARPS; ++i) {
+    const u64 s = sh.warp[i];
+    if (at == i && left >= s && i + 1 < VF_WARPS) {
+      left -= s;
+      ++at;
+    }
+  }
+  const int pw = (c1 - c0 + VF_WARPS - 1) / VF_WARPS;
+  const int s0 = min(c1, c0 + at * pw), s1 = min(c1, s0 + pw);
+  const int run = ((s1 - s0 + VF_WARPS - 1) / VF_WARPS + 31) & ~31;  // pieces per warp
+  const int f0 = min(s1, s0 + warp * run), f1 = min(s1, f0 + run);
+  const u64 s = warp_sum(sum_pieces<F32>(r, f0 + lane, 32, f1, sh.Z)) - refused_in(gone, f0, f1);
+  if (lane == 0) sh.fine[warp] = s;
+  __syncthreads();
+  at = 0;
+#pragma unroll
+  for (int i = 0; i < VF_WARPS; ++i) {
+    const u64 c = sh.fine[i];
+    if (at == i && left >= c && i + 1 < VF_WARPS) {
+      left -= c;
+      ++at;
+    }
+  }
+  if (warp != at) return;
+  // ... and the warp that holds it goes through them in order
+  for (int p0 = f0; p0 < f1; p0 += 32) {
+    const bool in = p0 + lane < f1;
+    const uint4 vp = in ? r.load(r.p, p0 + lane) : make_uint4(0, 0, 0, 0);
+    const uint4 vq = in && r.need_q() ? r.load(r.q, p0 + lane) : make_uint4(0, 0, 0, 0);
+    u64 w[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = r.weight(r.element(vp, i), r.element(vq, i), sh.Z);
+    const int e0 = (p0 + lane) * E - r.lead;
+    if (r.q == nullptr)
+      for (int k = 0; k < gone; ++k) {
+        const int o = sh.gone[k] - e0;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (o == i) w[i] = 0;
+      }
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) sum += w[i];
+    const u64 incl = warp_scan(sum, lane), excl = incl - sum;
+    const u64 step = __shfl_sync(0xffffffffu, incl, 31);
+    if (left < step) {
+      if (left >= excl && left < incl) {
+        u64 c = excl;
+        int x = -1;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          c += w[i];
+          if (x < 0 && c > left) x = e0 + i;
+        }
+        out[count] = x;
+      }
+      return;
+    }
+    left -= step;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, bool f32, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * VF_CTAS);
+  cfg.blockDim = dim3(VF_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = VF_CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = attn_programmatic_launch() ? 2 : 1;
+  note_launch();
+  const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a)
+                            : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace coda

@@ -71,7 +71,8 @@ typedef enum coda_status {
   CODA_ERR_LABEL_RANGE = 7,    /* device: label outside [0,V) and != ignore_index */
   CODA_ERR_POSITION_RANGE = 8, /* device: RoPE position outside [0, max_pos) */
   CODA_ERR_SEQLEN_RANGE = 9,   /* device: sequence offsets that fall or leave the tensor, a length beyond its page table */
-  CODA_ERR_PAGE_RANGE = 10     /* device: cache slot or page index outside the cache */
+  CODA_ERR_PAGE_RANGE = 10,    /* device: cache slot or page index outside the cache */
+  CODA_ERR_TREE_RANGE = 11     /* device: a parent, path or size that no tree of drafted tokens has */
 } coda_status;
 
 /* Operand storage order of a GEMM operand. */
@@ -823,6 +824,135 @@ int coda_attention_decode_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* 
                                 int64_t max_pages, const int32_t* seq_lens, int64_t batch, int32_t n_q, int32_t n_kv,
                                 int32_t head_dim, float softmax_scale, coda_bf16* O, float* lse, void* ws,
                                 size_t ws_bytes, coda_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions of whole tensors, for projections without a per-head norm
+ * (coda_linear_qknorm_rope rotates in the projection's epilogue).
+ *
+ * Per head of 128 elements, with (c, s) = cos_sin[pos, j], j < rotary_dim / 2:
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s
+ * on the pairs (2j, 2j + 1) or (j, j + rotary_dim / 2) of the head's first
+ * rotary_dim elements (a multiple of 16, up to 128); the others are copied.
+ * Each product and the sum are rounded to fp32, then bf16 once.
+ * ---------------------------------------------------------------------- */
+
+/* Table [max_pos, rotary_dim / 2, 2] fp32 whose frequencies f_j =
+ * theta^(-2j / rotary_dim) are scaled for contexts longer than the original:
+ *   f_j (g_j + (1 - g_j) / factor), cos and sin times amplitude, with
+ *   CODA_ROPE_PLAIN   g = 1 (coda_rope_table's angles; factor is not read)
+ *   CODA_ROPE_LINEAR  g = 0: positions divided by factor
+ *   CODA_ROPE_BANDS   g rises from 0 to 1 as the rotations over the original
+ *                     context, original f_j / 2 pi, go from low to high
+ *   CODA_ROPE_RAMP    g falls from 1 to 0 as j goes from the pair that makes
+ *                     high rotations (rounded down, at least 0) to the one that
+ *                     makes low (rounded up, at most rotary_dim - 1).
+ * low < high and original count for the last two.  Angles in fp64. */
+enum { CODA_ROPE_PLAIN = 0, CODA_ROPE_LINEAR = 1, CODA_ROPE_BANDS = 2, CODA_ROPE_RAMP = 3 };
+int coda_rope_table_scaled(float theta, int32_t rotary_dim, int32_t max_pos, int kind, float factor, float original,
+                           float low, float high, float amplitude, float* cos_sin, coda_stream stream);
+
+/* X, Y [T, n_heads*128] bf16 (row strides ldx, ldy; heads of one kind or the
+ * query and key columns of one projection output together); pos [T] int32 in
+ * [0, max_pos) (outside: CODA_ERR_POSITION_RANGE, and the nearest position
+ * counts).  Y may be X with the same stride (in place).  ws: 256 bytes. */
+int coda_rope(const coda_bf16* X, int64_t ldx, const int32_t* pos, const float* cos_sin, int32_t max_pos,
+              int32_t rotary_dim, int pairing, coda_bf16* Y, int64_t ldy, int64_t T, int32_t n_heads, int32_t head_dim,
+              void* ws, size_t ws_bytes, coda_stream stream);
+/* Its gradient, the transposed rotation: dx1 = dy1 c + dy2 s, dx2 = dy2 c - dy1 s. */
+int coda_rope_bwd(const coda_bf16* dY, int64_t lddy, const int32_t* pos, const float* cos_sin, int32_t max_pos,
+                  int32_t rotary_dim, int pairing, coda_bf16* dX, int64_t lddx, int64_t T, int32_t n_heads,
+                  int32_t head_dim, void* ws, size_t ws_bytes, coda_stream stream);
+
+/* ------------------------------------------------------------------------
+ * A step of speculative decoding over the 4-bit cache: the tokens drafted for
+ * every sequence are appended, attend to the cache together, are verified
+ * against the target's probabilities, and the accepted ones stay.
+ *
+ * The tokens of sequence b are rows [cu[b], cu[b + 1]) of packed tensors: node
+ * 0 is the last committed token (its keys are not yet in the cache), the others
+ * are drafted.  parents [T] int32 names each node's predecessor within the
+ * tree, an earlier node, or -1: the committed prefix.  parents NULL: chains
+ * (each token follows the one before it).
+ * ---------------------------------------------------------------------- */
+
+/* coda_kv_append_nvfp4 with the rotation of coda_rope on the way: K is rotated
+ * (in fp32) and quantised, V quantised, both to slots [T]; the n_q query heads
+ * are rotated into Q_out [T, n_q*128] (n_q 0: none, Q and Q_out may be NULL),
+ * the rotated keys go to K_out [T, n_kv*128] in bf16 too, if it is not NULL.
+ * Tokens with a negative slot are rotated but not appended.  Outputs must not
+ * overlap inputs.  Slots, pages and positions out of range as in the calls of
+ * the parts. */
+int coda_kv_append_rope_nvfp4(const coda_bf16* Q, int64_t ldq, const coda_bf16* K, int64_t ldk, const coda_bf16* V,
+                              int64_t ldv, const int32_t* slots, const int32_t* pos, const float* cos_sin,
+                              int32_t max_pos, int32_t rotary_dim, int pairing, coda_bf16* Q_out, coda_bf16* K_out,
+                              int64_t T, uint8_t* codes, uint8_t* sf, float* scale, int64_t num_pages, int32_t page_size,
+                              int32_t n_q, int32_t n_kv, int32_t head_dim, void* ws, size_t ws_bytes,
+                              coda_stream stream);
+
+/* Attention of the nodes over the cache.  seq_lens [batch] counts the cached
+ * tokens of sequence b, its n_b = cu[b + 1] - cu[b] nodes among them as the
+ * last, in their order; node i sees the first seq_lens[b] - n_b tokens, its
+ * ancestors and itself (a chain: causal attention of the last n_b tokens).
+ * Q [T, n_q*128] bf16 (row stride ldq), O [T, n_q*128] bf16, lse [T, n_q] fp32;
+ * block_table as in coda_attention_decode_nvfp4.  A parent that is no earlier
+ * node sets CODA_ERR_TREE_RANGE and counts as -1; a tree given by parents with
+ * more than 256 nodes sets it and gets O = 0, lse = -inf (chains have no such
+ * limit); so does a sequence whose offsets or length are out of range
+ * (CODA_ERR_SEQLEN_RANGE, as far as its rows exist).  A page outside the cache
+ * sets CODA_ERR_PAGE_RANGE and its keys are left out.  Rows outside every sequence stay as they
+ * are; a row of the cache that holds an infinity or NaN reaches only the nodes
+ * that see it.  Roundings as in coda_attention_decode_nvfp4. */
+size_t coda_attention_tree_nvfp4_workspace_size(int64_t T, int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
+int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
+                              const float* scale, int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                              int64_t max_pages, const int32_t* seq_lens, const int32_t* cu, const int32_t* parents,
+                              int64_t T, int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim, float softmax_scale,
+                              coda_bf16* O, float* lse, void* ws, size_t ws_bytes, coda_stream stream);
+
+/* Verification.  probs [T, V] (dtype CODA_F32 or CODA_BF16): the target's
+ * probabilities p_i after every node; draft_probs [T, V] or NULL: those that a
+ * node's children were drawn from, independently (row i for the children of
+ * node i); tokens [T] int32 (node 0's is not read); u [T] and u_next [batch]
+ * fp32 in [0, 1).  The walk begins at node 0 with w = p_0, Z = 1; a child i of
+ * the node it stands at, in order of their numbers, with token x:
+ *   u_i q(x) Z < w(x): accepted; the walk stands at i with w = p_i, Z = 1;
+ *   else               w <- max(w - Z q, 0), Z <- sum w
+ * (without draft_probs q is 1 at x and 0 elsewhere).  Where no child is left the
+ * next token is the first x with sum_{y <= x} w(y) > u_next sum w.  Given
+ * probabilities that sum to 1 and independent uniform u, the accepted and the
+ * next token are distributed as the target's own, with or without draft_probs.
+ * Weights are held in units of 2^-60 and their sums are exact; a probability
+ * that is negative or NaN counts as 0, one above 1 as 1.
+ *   count [batch]         accepted drafts a
+ *   nodes [batch, width]  node 0, then the accepted nodes; -1 behind
+ *   out   [batch, width]  the accepted tokens, then the next; -1 behind
+ * The walk ends at depth width - 1.  Where every weight is 0 the next token is
+ * taken from the row's own probabilities, and is -1 where those are 0 too.  A
+ * sequence without nodes gets count 0 and -1 throughout; a parent that is no
+ * earlier node, or a token outside [0, V), sets CODA_ERR_TREE_RANGE or
+ * CODA_ERR_LABEL_RANGE and is never accepted; offsets out of range
+ * (CODA_ERR_SEQLEN_RANGE) or more than 1024 nodes (CODA_ERR_TREE_RANGE) count
+ * as a sequence without nodes.  V below 2^30. */
+size_t coda_verify_drafts_workspace_size(int64_t T, int64_t batch, int64_t V);
+int coda_verify_drafts(const void* probs, const void* draft_probs, int dtype, int64_t V, const int32_t* tokens,
+                       const int32_t* cu, const int32_t* parents, const float* u, const float* u_next, int64_t T,
+                       int64_t batch, int64_t width, int32_t* count, int32_t* nodes, int32_t* out_tokens, void* ws,
+                       size_t ws_bytes, coda_stream stream);
+
+/* What the verification accepted stays: the cache rows of node nodes[b, d]
+ * move to place d behind the committed prefix, d = 1 .. count[b], all heads and
+ * both planes; new_lens [batch] = seq_lens - n_b + count + 1 (seq_lens for a
+ * sequence without nodes), not seq_lens itself.  nodes and count as
+ * coda_verify_drafts writes them: a path that does not rise from node 0, or
+ * leaves the tree, sets CODA_ERR_TREE_RANGE, moves nothing and drops all nodes
+ * (new length seq_lens - n_b); lengths and offsets out of range set
+ * CODA_ERR_SEQLEN_RANGE and give length 0; rows on pages outside the cache are
+ * left out (CODA_ERR_PAGE_RANGE). */
+int coda_kv_accept_nvfp4(uint8_t* codes, uint8_t* sf, float* scale, int64_t num_pages, int32_t page_size,
+                         const int32_t* block_table, int64_t max_pages, const int32_t* seq_lens, const int32_t* cu,
+                         const int32_t* nodes, int64_t width, const int32_t* count, int64_t batch,
+                         int32_t n_kv, int32_t head_dim, int32_t* new_lens, void* ws, size_t ws_bytes,
+                         coda_stream stream);
 
 #ifdef __cplusplus
 }

@@ -831,3 +831,102 @@ def attention_bwd(dO, Q, K, V, cu_q, cu_k, n_q, n_kv, scale):
             out["dV"][k0:k1, kc] += p.T @ do
             out["EV"][k0:k1, kc] += p.T @ np.abs(do)
     return out
+
+
+# ---------------------------------------------------------------------------
+# rotary positions from a table, drafted tokens
+# ---------------------------------------------------------------------------
+
+def rope_scaled_frequencies(theta, rotary, kind=None, factor=1.0, original=0.0, low=1.0, high=32.0):
+    """Frequencies theta^(-2j/rotary), blended with those of `factor` times
+    longer positions: all of them ("linear"), by the rotations they make over
+    the original context ("bands"), by their number ("ramp")."""
+    j = np.arange(rotary // 2, dtype=np.float64)
+    f = theta ** (-2.0 * j / rotary)
+    if kind is None:
+        return f
+    turns = original * f / (2.0 * np.pi)
+    if kind == "linear":
+        g = np.zeros_like(f)
+    elif kind == "bands":
+        g = np.clip((turns - low) / (high - low), 0.0, 1.0)
+    elif kind == "ramp":
+        # the pair that makes `r` turns: original theta^(-2j/rotary) = 2 pi r
+        pair = lambda r: rotary * np.log(original / (2.0 * np.pi * r)) / (2.0 * np.log(theta))
+        a, b = max(0.0, np.floor(pair(high))), min(rotary - 1.0, np.ceil(pair(low)))
+        g = 1.0 - np.clip((j - a) / (b - a if b != a else 0.001), 0.0, 1.0)
+    else:
+        raise ValueError(kind)
+    return f * g + f / factor * (1.0 - g)
+
+
+def rope_part(x, cos, sin, pairing="interleaved"):
+    """x [t, head, d]: the first 2 * cos.shape[1] elements of every head turned
+    by the angles whose cosines and sines are given per token, the rest kept."""
+    r = 2 * cos.shape[1]
+    y = x.copy()
+    first, second = (np.s_[..., 0:r:2], np.s_[..., 1:r:2]) if pairing == "interleaved" else \
+        (np.s_[..., 0:r // 2], np.s_[..., r // 2:r])
+    z = (x[first] + 1j * x[second]) * (cos + 1j * sin)[:, None, :]
+    y[first], y[second] = z.real, z.imag
+    return y
+
+
+def tree_sees(parents):
+    """[n, n] bool: node i sees its ancestors and itself."""
+    m = np.zeros((len(parents), len(parents)), dtype=bool)
+    for i in range(len(parents)):
+        j = i
+        while j >= 0:
+            m[i, j] = True
+            j = parents[j]
+    return m
+
+
+def tree_attention_fwd(q, k, v, sees, n_q, n_kv, scale):
+    """One sequence: nodes q [n, n_q*d] over keys k, v [len, n_kv*d] (the last n
+    are the nodes' own), node i seeing all before them and those of sees[i].
+    O [n, n_q*d], lse [n, n_q], and A = sum_j p_ij |v_j|, B = max_j p_ij, S =
+    max |s| per node and head (for error bounds)."""
+    n, keys = q.shape[0], k.shape[0]
+    d = q.shape[1] // n_q
+    full = np.ones((n, keys), dtype=bool)
+    full[:, keys - n:] = sees
+    out = {"O": np.zeros(q.shape), "A": np.zeros(q.shape), "lse": np.full((n, n_q), -np.inf), "S": np.zeros((n, n_q)),
+           "P": np.zeros((n, n_q, keys))}
+    for h in range(n_q):
+        c, kc = slice(h * d, (h + 1) * d), slice((h // (n_q // n_kv)) * d, (h // (n_q // n_kv) + 1) * d)
+        s = scale * (q[:, c] @ k[:, kc].T)
+        out["S"][:, h] = np.where(full, np.abs(s), 0.0).max(axis=1, initial=0.0)
+        s = np.where(full, s, -np.inf)
+        out["lse"][:, h] = _lse(s)
+        p = np.exp(s - out["lse"][:, h:h + 1])
+        out["O"][:, c], out["A"][:, c], out["P"][:, h] = p @ v[:, kc], p @ np.abs(v[:, kc]), p
+    return out
+
+
+def verify_drafts(p, tokens, parents, u, u_next, q=None, width=None):
+    """One tree: p, q [n, V] float64, tokens, parents, u [n].  (accepted nodes
+    with node 0, their tokens and the next one.)"""
+    width = width or len(tokens)
+    here, path, text = 0, [0], []
+    w, Z = p[0].copy(), 1.0
+    for i in range(1, len(tokens)):
+        if parents[i] != here or len(path) >= width:
+            continue
+        x = tokens[i]
+        if u[i] * ((1.0 if q is None else q[here][x]) * Z) < w[x]:
+            here, w, Z = i, p[i].copy(), 1.0
+            path.append(i)
+            text.append(x)
+        elif q is None:
+            Z -= w[x]
+            w[x] = 0.0
+        else:
+            w = np.maximum(w - Z * q[here], 0.0)
+            Z = w.sum()
+    if w.sum() == 0:
+        w = p[here].copy()
+    c = np.cumsum(w)
+    text.append(int(np.searchsorted(c, u_next * c[-1], side="right")) if c[-1] > 0 else -1)
+    return path, text
