@@ -5,6 +5,8 @@
 namespace coda {
 
 constexpr int TREE_MAX_NODES = 256;  // of a tree given by parents
+constexpr int TREE_ROWS = 128;       // query rows (nodes times heads of a group) of a tile
+constexpr int TREE_MAX_CTAS = 160;   // partial results reserved for this many CTAs
 
 struct TreeArgs {
   KvCache c;
@@ -19,6 +21,11 @@ struct TreeArgs {
   float scale_log2;
   __nv_bfloat16* O;        // [T, n_q * 128]
   float* lse;              // [T, n_q]
+  int64_t* places;         // [B + 2]: places on the line of work before each sequence, their total, places per CTA
+  uint32_t* seen;          // [TREE_MAX_CTAS, TREE_ROWS, TREE_MAX_NODES / 32] what each row of a CTA's tile sees of its tree
+  float* part;             // [2 * TREE_MAX_CTAS, part_rows, 128] normalised partial outputs
+  float* part_lse;         // [2 * TREE_MAX_CTAS, part_rows] log2 domain
+  int part_rows;
   int* status;
 };
 cudaError_t launch_attn_tree(const TreeArgs& a, int sms, cudaStream_t s);

@@ -34,6 +34,15 @@ int rope(const coda_bf16* X, int64_t ldx, const int32_t* pos, const float* cs, i
   return CODA_OK;
 }
 
+// A row for each node and head of a group, up to a tile's.
+void lay_tree(Cursor& c, coda::TreeArgs& a, int64_t T, int64_t batch, int group) {
+  a.part_rows = static_cast<int>(std::min<int64_t>(coda::TREE_ROWS, T * group));
+  a.places = c.take<int64_t>(batch + 2);
+  a.seen = c.take<uint32_t>(int64_t(coda::TREE_MAX_CTAS) * coda::TREE_ROWS * (coda::TREE_MAX_NODES / 32));
+  a.part = c.take<float>(int64_t(2) * coda::TREE_MAX_CTAS * a.part_rows * coda::ATTN_D);
+  a.part_lse = c.take<float>(int64_t(2) * coda::TREE_MAX_CTAS * a.part_rows);
+}
+
 }  // namespace
 
 extern "C" {
@@ -130,7 +139,11 @@ int coda_kv_accept_nvfp4(uint8_t* codes, uint8_t* sf, float* scale, int64_t num_
 }
 
 size_t coda_attention_tree_nvfp4_workspace_size(int64_t T, int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim) {
-  return HEADER;
+  if (check_shape(T, T, batch, n_q, n_kv, head_dim, 1.f) != CODA_OK) return HEADER;
+  Cursor c{nullptr};
+  coda::TreeArgs a{};
+  lay_tree(c, a, T, batch, n_q / n_kv);
+  return c.off;
 }
 
 int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
@@ -151,6 +164,8 @@ int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* co
   CK(check_ws(ws, ws_bytes, coda_attention_tree_nvfp4_workspace_size(T, batch, n_q, n_kv, head_dim)));
   const int sms = coda::device_sms();
   if (sms <= 0) return CODA_ERR_CUDA;
+  Cursor cur{static_cast<uint8_t*>(ws)};
+  lay_tree(cur, a, T, batch, n_q / n_kv);
   a.Q = B(Q);
   a.ldq = ldq;
   a.table = block_table;

@@ -204,7 +204,15 @@ def test_infinities_reach_only_the_nodes_that_see_them(coda, n_q, n, sick):
         got = call()
         finite = torch.isfinite(got["O"].float()).all(dim=1).cpu()
         assert torch.equal(finite, ~sees), what
-        assert torch.equal(got["O"][~sees], want["O"][~sees]) and torch.equal(got["lse"][~sees], want["lse"][~sees])
+        # A hidden value meets a weight of exactly 0, so nothing is added; but a
+        # step of the product sums 16 keys in fp32 aligned to the largest operands,
+        # and 2^-14 (f16's smallest exponent, which a zero has) times 2688 may be the
+        # largest, so the other keys' terms may lose bits below 2^-25 of 2688 units
+        # in a step: within the bound's term for the rounding of small weights.
+        hidden = (~sees).to(DEV).unsqueeze(1)
+        rest = {k: torch.where(hidden, got[k], want[k]) for k in ("O", "lse")}
+        check_tree(rest, to_np(Q), [keys], [n], [tree], kval, vval, vs, n_q, n_kv, D ** -0.5)
+        assert torch.equal(rest["lse"], want["lse"])
 
 
 def test_bad_trees_lengths_and_pages_set_status(coda):
