@@ -42,20 +42,25 @@
 namespace coda {
 namespace {
 
-constexpr int TR_GROUPS = 4;                          // warpgroups that unpack and weigh
-constexpr int TR_THREADS = TR_GROUPS * 128 + 64;      // and two warps: copies, products
+constexpr int TR_THREADS = 512;
+constexpr int TR_UNPACK = 8, TR_COPY_WARP = 12, TR_MMA_WARP = 13;  // warps: 0-7 weights, 8-11 unpacking
 constexpr int TR_UNIT = 128;
 constexpr int TR_STAGES = 3;
-// a stage of the cache's rows as they lie in memory
-constexpr int RW_K = 0, RW_V = 8192, RW_SFK = 16384, RW_SFV = 17408, RW_RSK = 18432, RW_RSV = 18944;
+// A stage holds a unit's rows of the cache part by part (a page, or 128 keys of
+// one), each part as the copies leave it: keys, then values.  16-byte pieces of
+// the codes are exchanged by the 64-byte swizzle.
+constexpr int RW_CODES = 0, RW_SF = 16384, RW_RS = 18432;
 constexpr int TR_RAW = 19456;
+// Row of a key's codes (and of its value's, 1 << shift rows on) in a stage;
+// likewise of its block scales and row scales.
+__device__ __forceinline__ int raw_row(int key, int shift) { return ((key >> shift) << (shift + 1)) + (key & ((1 << shift) - 1)); }
 constexpr uint32_t TILE = 32768, HALF_TILE = 16384;  // 128 x 128 f16, as two halves of 64 columns
 constexpr uint32_t OFF_Q = 0, OFF_P = TILE, OFF_V = 3 * TILE, OFF_RAW = 5 * TILE;
 constexpr uint32_t OFF_ROW = OFF_RAW + TR_STAGES * TR_RAW;  // [2][64] pairs of rows, by item: factors, -r
 constexpr uint32_t OFF_KEY = OFF_ROW + 2048;                // [4][128] row scale of the key, log2 of the value's
-constexpr uint32_t OFF_RED = OFF_KEY + 4096;                // [4][4][32] exchange of a warpgroup
+constexpr uint32_t OFF_RED = OFF_KEY + 4096;                // [2][4][64] exchange of a warpgroup
 constexpr uint32_t OFF_BAR = OFF_RED + 2048;
-constexpr uint32_t TR_SMEM = 1024 + OFF_BAR + 256;
+constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
 constexpr float TR_RAISE = 10.f;
@@ -86,15 +91,6 @@ __device__ __forceinline__ bool group_any(int id, bool p) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : CODA_R8(r, 0), CODA_R8(r, 8)
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
@@ -103,23 +99,34 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
-__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[32]) {
-  float v[32];
-  tmem_ld32(taddr, v);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : CODA_R8(r, 0), CODA_R8(r, 8)
+      : "r"(taddr)
+      : "memory");
+}
+// The first n (a multiple of 16) of 64 columns, or more of them.
+__device__ __forceinline__ void tmem_columns(uint32_t taddr, int n, uint32_t (&r)[64]) {
+  if (n > 32)
+    tmem_ld64(taddr, r);
+  else if (n > 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+        "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : CODA_R32(r, 0)
+        : "r"(taddr)
+        : "memory");
+  else
+    tmem_ld16(taddr, r);
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), CODA_W8(r, 0)
                : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      CODA_W8(r, 0), CODA_W8(r, 8)
-      : "memory");
 }
 
 // A sequence's work.
@@ -162,10 +169,11 @@ __device__ __forceinline__ int unit_at(int64_t place, int64_t base, int cost, in
 struct TreeWalk {
   int b, item;            // sequence, next item of it
   int64_t base;           // place of that item
+  int64_t first, last;    // the CTA's places
   TreeSeq s;
   // current
   int kvh, tile, rows, u0, u1;
-  __device__ __forceinline__ bool next(const TreeArgs& a, int64_t first, int64_t last) {
+  __device__ __forceinline__ bool next(const TreeArgs& a) {
     while (base < last) {
       if (s.n == 0 || item == a.c.n_kv * s.tiles) {
         if (++b >= a.B) return false;
@@ -210,105 +218,297 @@ __device__ __forceinline__ float warp_columns(float (&v)[N], int lane) {
   return v[0];
 }
 
+extern __shared__ __align__(128) uint8_t tree_smem[];
+// Aligned, and known to the compiler as shared memory.
+__device__ __forceinline__ uint8_t* tree_shared() { return tree_smem + (-smem_u32(tree_smem) & 1023u); }
+
+// What a CTA does of an item; the copying warp walks the line and leaves it in
+// shared memory, ahead of the item's first unit.
+struct TreeItem {
+  int q0, n, len, kvh;
+  int row0, rows;      // of the tile, among the sequence's rows
+  int u0, u1, units;
+};
+constexpr int TR_ITEMS = 8;  // the copies are at most five units ahead
+
+// Where the copies are on the line.
+struct TreeCopies {
+  TreeWalk w;
+  int u;               // next unit of the walk's item
+  uint32_t it, items;  // units and items so far
+  int done;            // the end has been told
+};
+
 struct TreeBars {
+  TreeItem item[TR_ITEMS];
+  TreeCopies copies;
   uint64_t raw_full[TR_STAGES], raw_empty[TR_STAGES];
+  uint64_t key_full[4];  // the keys' scales
   uint64_t k_full[2], v_full[2], s_full[2], s_empty[2], p_full[2], o_done[2];
   uint64_t q_full, o_empty, drain;
+  uint64_t item_full[TR_ITEMS];
   uint32_t keys_in[TR_STAGES];  // bit i: keys 16 i .. 16 i + 15 of the stage are there; TR_NO_MORE: no unit, nor behind it
   int left[TR_STAGES];          // keys of the sequence from the stage's first on
+  int64_t scan[TR_THREADS / 32], before;  // of the places, and the sequence that the CTA begins with
+  int seq;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(TreeBars) <= 256, "barrier area");
+static_assert(sizeof(TreeBars) <= 1152, "barrier area");
 
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeBars* s, int* status, uint32_t sleep_ns = 0) {
   return mbar_wait_bounded(bar, parity, &s->abort, status, TR_WAIT_NS, sleep_ns);
 }
 
-// What a warp of the unpacking has in hand between the keys of a unit and its
-// values.
-struct Unpack {
-  uint32_t it;      // number of the unit
-  bool more;        // there is one
-  uint32_t on;      // its groups of 16 keys
-  int left;
-  uint32_t rs_zero;  // row scale that rows of zeros take
-};
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int v, int w,
+                                            uint32_t p) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %8, 0;\n\t"
+      "@P cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(v), "r"(w), "r"(p)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int v,
+                                            uint32_t p) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\tsetp.ne.b32 P, %7, 0;\n\t"
+      "@P cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(v), "r"(p)
+      : "memory");
+}
 
-// K' of unit x.it: thread (wg, key) takes elements 32 wg .. 32 wg + 31 of its
-// key's row, to TMEM.  Its place was read by the scores of two units ago, which
-// every warp has seen.
-__device__ __forceinline__ bool unpack_keys(const TreeArgs& a, uint8_t* smem, TreeBars* bar, uint32_t tmem, int wg, int warp4,
-                                            int lane, Unpack& x) {
-  const uint32_t st = x.it % TR_STAGES, buf = x.it & 1;
-  if (!__all_sync(0xffffffffu, tree_wait(&bar->raw_full[st], (x.it / TR_STAGES) & 1, bar, a.status))) return false;
-  x.on = bar->keys_in[st];
-  x.left = bar->left[st];
-  x.more = x.on != TR_NO_MORE;
-  if (!x.more) return true;
+// Copies of the next unit of the line into its stage, by one warp: three per
+// part, keys and values together.  Lane i holds the page of part i, read a unit
+// ahead (`page`).
+__device__ __forceinline__ bool copy_unit(const TreeArgs& a, const CUtensorMap* codes, const CUtensorMap* sf,
+                                          const CUtensorMap* scale, uint8_t* smem, TreeBars* bar, int lane, uint32_t el,
+                                          int& page) {
+  TreeCopies& c = bar->copies;
+  const KvCache& kc = a.c;
+  const int shift = min(kc.page_shift, 7);  // keys of a part
+  const uint32_t st = c.it % TR_STAGES;
+  bool ok = tree_wait(&bar->raw_empty[st], ((c.it / TR_STAGES) & 1) ^ 1, bar, a.status);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  auto page_of = [&](int u) {  // of this lane's part of unit u; -1: nothing there
+    const int k = u * TR_UNIT + (lane << shift);
+    return u < c.w.u1 && (lane << shift) < TR_UNIT && k < c.w.s.len
+               ? a.table[static_cast<int64_t>(c.w.b) * a.max_pages + (k >> kc.page_shift)]
+               : -1;
+  };
+  if (c.u == c.w.u1) {  // the next item
+    int more = 0;
+    if (lane == 0) {
+      TreeWalk w = c.w;
+      more = w.next(a);
+      c.w = w;
+      c.u = w.u0;
+      TreeItem& to = bar->item[c.items % TR_ITEMS];
+      to.rows = 0;
+      if (more) {
+        to.q0 = w.s.q0;
+        to.n = w.s.n;
+        to.len = w.s.len;
+        to.kvh = w.kvh;
+        to.row0 = w.tile * TREE_ROWS;
+        to.rows = w.rows;
+        to.u0 = w.u0;
+        to.u1 = w.u1;
+        to.units = w.s.units;
+      } else {
+        c.done = 1;
+        bar->keys_in[st] = TR_NO_MORE;
+        mbar_arrive(&bar->raw_full[st]);
+      }
+      mbar_arrive(&bar->item_full[c.items++ % TR_ITEMS]);
+    }
+    __syncwarp();
+    if (!__shfl_sync(0xffffffffu, more, 0)) return true;
+    page = page_of(c.u);
+  }
+  const int u = c.u, len = c.w.s.len;
+  const int k = u * TR_UNIT + (lane << shift);
+  const bool named = (lane << shift) < TR_UNIT && k < len;
+  const bool in = named && page >= 0 && page < kc.num_pages;
+  if (named && !in) atomicOr(a.status, CODA_DEV_PAGE_RANGE);
+  const uint32_t parts = __ballot_sync(0xffffffffu, in);
+  const int groups = 1 << (shift - 4);  // of 16 keys in a part
+  const uint32_t mask = __reduce_or_sync(0xffffffffu, in ? ((1u << groups) - 1) << (lane * groups) : 0);
+  if (lane == 0) {
+    bar->keys_in[st] = mask;
+    bar->left[st] = len - u * TR_UNIT;
+    if (parts == 0) mbar_arrive(&bar->raw_full[st]);
+  }
+  mbar_arrive_expect_tx(&bar->raw_full[st], __popc(parts) * (152u << shift), lane == 0 && parts != 0);
+  __syncwarp();
+  uint8_t* to = smem + OFF_RAW + st * TR_RAW;
+  const int row = (u * TR_UNIT) & ((1 << kc.page_shift) - 1);  // of the page, where it holds more than a unit
+  for (uint32_t left = parts; left; left &= left - 1) {
+    const int p = __ffs(left) - 1;
+    const int pg = __shfl_sync(0xffffffffu, page, p);
+    tma_load_5d(to + RW_CODES + (p << (shift + 7)), codes, &bar->raw_full[st], 0, row, c.w.kvh, 0, pg, el);
+    tma_load_4d(to + RW_SF + (p << (shift + 4)), sf, &bar->raw_full[st], row * 2, c.w.kvh, 0, pg, el);
+    tma_load_4d(to + RW_RS + (p << (shift + 3)), scale, &bar->raw_full[st], row, c.w.kvh, 0, pg, el);
+  }
+  page = page_of(u + 1);
+  __syncwarp();
+  if (lane == 0) {
+    c.u = u + 1;
+    ++c.it;
+  }
+  __syncwarp();
+  return true;
+}
+
+// The scores of unit i, once every warp has unpacked its keys.
+__device__ __forceinline__ bool issue_scores(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, int n,
+                                             uint32_t el) {
+  const uint32_t buf = i & 1, ph = (i >> 1) & 1;
+  const bool ok = tree_wait(&bar->k_full[buf], ph, bar, status) && tree_wait(&bar->s_empty[buf], ph ^ 1, bar, status);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  tc_fence_after();
+  const uint32_t q = smem_u32(smem + OFF_Q), id = idesc_f16(128, n, 0, 0);
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+    umma_bf16_ts(tmem + COL_S + buf * 128, tmem + COL_K + buf * 64 + x * 8,
+                 sdesc_sw128(q + (x >> 2) * HALF_TILE + (x & 3) * 32, 16, 1024), id, x > 0, el);
+  umma_commit(&bar->s_full[buf], el);
+  return true;
+}
+// O^T += V'^T P'^T of unit i; first: of an item, whose predecessor's O has left.
+__device__ __forceinline__ bool issue_outputs(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, int n,
+                                              bool first, uint32_t item, uint32_t el) {
+  const uint32_t buf = i & 1, ph = (i >> 1) & 1;
+  const bool ok = tree_wait(&bar->p_full[buf], ph, bar, status) && tree_wait(&bar->v_full[buf], ph, bar, status) &&
+                  (!first || tree_wait(&bar->o_empty, (item & 1) ^ 1, bar, status));
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  tc_fence_after();
+  const uint32_t v = smem_u32(smem + OFF_V + buf * TILE), p = smem_u32(smem + OFF_P + buf * TILE);
+  const uint32_t id = idesc_f16(128, n, 1, 1);
+#pragma unroll
+  for (int x = 0; x < 8; ++x)  // 16 keys a step
+    umma_bf16(tmem + COL_O, sdesc_sw128(v + x * 2048, HALF_TILE, 1024), sdesc_sw128(p + x * 2048, HALF_TILE, 1024), id,
+              !first || x > 0, el);
+  umma_commit(&bar->o_done[buf], el);
+  return true;
+}
+// After a wait that ran out: let what was issued land before the CTA's memory
+// is used again.
+__device__ __forceinline__ void tree_drain(TreeBars* bar, int warp, int lane) {
+  if (warp == TR_MMA_WARP) {
+    umma_commit(&bar->drain, lane == 0);
+    mbar_wait_drain(&bar->drain, 0, 200000000ull);
+  } else if (warp == TR_COPY_WARP) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+}
+
+// Unit `it` unpacked by four warps, a warp's 32 keys each.  K': a thread per
+// key, to the lane of TMEM that is its row.  False: a wait ran out, or no unit
+// (`more`) is left.
+__device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane, uint32_t it,
+                                       int shift, uint32_t& rs_zero, bool& more) {
+  const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
+  bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1, bar, status);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  const uint32_t on = bar->keys_in[st];
+  const int left = bar->left[st];
+  more = on != TR_NO_MORE;
+  if (!more) return false;
+  ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
+  if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
-  const int key = warp4 * 32 + lane;
-  const bool in = ((x.on >> (key >> 4)) & 1u) && key < x.left;
-  const uint32_t two =
-      e4m3x2_f16(in ? *reinterpret_cast<const uint16_t*>(raw + RW_SFK + key * 8 + wg * 2) : 0);
-  const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
-  const uint4 v = *reinterpret_cast<const uint4*>(raw + RW_K + key * 64 + wg * 16);
-  uint32_t o[16];
+  const int key = g * 32 + lane, krow = raw_row(key, shift);
+  const bool in = ((on >> (key >> 4)) & 1u) && key < left;
+  uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + krow * 8);
+  if (!in) sfk = make_uint2(0, 0);
+  uint4 kc[4];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t f[4];
-    e2m1x8_f16(w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w, f);
+  for (int q = 0; q < 4; ++q) kc[q] = *reinterpret_cast<const uint4*>(raw + RW_CODES + krow * 64 + ((q ^ ((krow >> 1) & 3)) << 4));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[w * 4 + i] = hmul2(f[i], w < 2 ? s0 : s1);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t o[32];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint4 v = kc[h * 2 + q];
+      const uint32_t two = e4m3x2_f16(((h ? sfk.y : sfk.x) >> (16 * q)) & 0xFFFFu);
+      const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t f[4];
+        e2m1x8_f16(w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[q * 16 + w * 4 + i] = hmul2(f[i], w < 2 ? s0 : s1);
+      }
+    }
+    tmem_st32(tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64 + h * 32, o);
   }
-  tmem_st16(tmem + (static_cast<uint32_t>(warp4 * 32) << 16) + COL_K + buf * 64 + wg * 16, o);
-  if (wg == 0) {  // the key's scales
-    const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SFV + key * 8);
-    const float rsk = *reinterpret_cast<const float*>(raw + RW_RSK + key * 4);
-    const float rsv = *reinterpret_cast<const float*>(raw + RW_RSV + key * 4);
+  bool tiny;
+  {  // the key's scales
+    const int vrow = krow + (1 << shift);
+    const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + vrow * 8);
+    const float rsk = *reinterpret_cast<const float*>(raw + RW_RS + krow * 4);
+    const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + vrow * 4);
     const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
     const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
     const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
-    if (least < 0x7F7FFFFFu) x.rs_zero = least;
-    const float rs = zeros ? __uint_as_float(x.rs_zero) : rsv;
+    if (least < 0x7F7FFFFFu) rs_zero = least;
+    const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
+    tiny = __any_sync(0xffffffffu, in && rs < 0x1p-100f);
     float2 meta;
     meta.x = in ? rsk : 0.f;
-    // below 2^-100 the sum l would pass fp32's end: unpack_values takes the rest
+    // below 2^-100 the sum l would pass fp32's end: V' takes the rest
     meta.y = !in ? -INFINITY : sick ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
-    *reinterpret_cast<float2*>(smem + OFF_KEY + (x.it & 3) * 1024 + key * 8) = meta;
+    *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + key * 8) = meta;
   }
   tmem_st_wait();
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) mbar_arrive(&bar->k_full[buf]);
-  return true;
-}
+  if (lane == 0) {
+    mbar_arrive(&bar->key_full[it & 3]);
+    mbar_arrive(&bar->k_full[buf]);
+  }
 
-// V' of the unit: a warp takes eight keys, a lane sixteen elements of two of
-// them.  A block scale that is NaN leaves zeros (the key's weights are NaN).
-__device__ __forceinline__ bool unpack_values(const TreeArgs& a, uint8_t* smem, TreeBars* bar, int wwarp, int lane, Unpack& x) {
-  const uint32_t st = x.it % TR_STAGES, buf = x.it & 1;
-  if (!__all_sync(0xffffffffu, tree_wait(&bar->o_done[buf], ((x.it >> 1) & 1) ^ 1, bar, a.status))) return false;
-  const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
+  // V': a lane sixteen elements of eight keys.  A block scale that is NaN
+  // leaves zeros (the key's weights are NaN).
+  ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
+  if (!__all_sync(0xffffffffu, ok)) return false;
   uint8_t* to = smem + OFF_V + buf * TILE;
+  const int piece = lane & 7, k0 = g * 32 + (lane >> 3);  // elements 16 piece .. of keys k0, k0 + 4, ...
+  uint2 c[8];
+  uint32_t sv[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int k = wwarp * 8 + i * 4 + (lane >> 3), piece = lane & 7;  // key, elements 16 piece ..
-    const uint2 c = *reinterpret_cast<const uint2*>(raw + RW_V + k * 64 + piece * 8);
-    uint32_t sf = raw[RW_SFV + k * 8 + piece];
-    const bool in = ((x.on >> (k >> 4)) & 1u) && k < x.left;  // else whatever the stage held before
-    const float rv = in ? *reinterpret_cast<const float*>(raw + RW_RSV + k * 4) : 1.f;
-    if (!in || (sf & 0x7Fu) == 0x7Fu) sf = 0;
-    uint32_t s = e4m3x2_f16(sf * 0x101u);
-    if (__any_sync(0xffffffffu, rv < 0x1p-100f)) {
-      keep_branch();
-      const float by = rv < 0x1p-100f ? rv * 0x1p100f : 1.f;
-      s = pack_f16(f16_lo(s) * by, f16_hi(s) * by);
+  for (int i = 0; i < 8; ++i) {
+    const int k = k0 + 4 * i, vrow = raw_row(k, shift) + (1 << shift);
+    c[i] = *reinterpret_cast<const uint2*>(raw + RW_CODES + vrow * 64 + ((((piece >> 1) ^ (vrow >> 1)) & 3) << 4) + (piece & 1) * 8);
+    sv[i] = raw[RW_SF + vrow * 8 + piece];
+    // outside the sequence is whatever the stage held before
+    if (!(((on >> (k >> 4)) & 1u) && k < left) || (sv[i] & 0x7Fu) == 0x7Fu) sv[i] = 0;
+    sv[i] = e4m3x2_f16(sv[i] * 0x101u);
+  }
+  if (tiny) {
+    keep_branch();
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int k = k0 + 4 * i;
+      const float rv = *reinterpret_cast<const float*>(raw + RW_RS + (raw_row(k, shift) + (1 << shift)) * 4);
+      const float by = k < left && rv < 0x1p-100f ? rv * 0x1p100f : 1.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (x == i) sv[x] = pack_f16(f16_lo(sv[x]) * by, f16_hi(sv[x]) * by);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = k0 + 4 * i;
+    const uint32_t s = sv[i];
     uint32_t f[4], h[4];
-    e2m1x8_f16(c.x, f);
-    e2m1x8_f16(c.y, h);
+    e2m1x8_f16(c[i].x, f);
+    e2m1x8_f16(c[i].y, h);
     uint8_t* row = to + (piece >> 2) * HALF_TILE + k * 128;
     const int p = 2 * (piece & 3);
     *reinterpret_cast<uint4*>(row + ((p ^ (k & 7)) << 4)) =
@@ -322,34 +522,37 @@ __device__ __forceinline__ bool unpack_values(const TreeArgs& a, uint8_t* smem, 
     mbar_arrive(&bar->v_full[buf]);
     mbar_arrive(&bar->raw_empty[st]);
   }
-  ++x.it;
   return true;
 }
 
-// A warpgroup's part of one stretch: the weights of columns wg * NC .. of the
-// tile, and between them its share of unpacking the next unit.  `it` counts the
-// CTA's units.  False: a wait ran out.
-template <int NC>
-__device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& w, uint8_t* smem, TreeBars* bar, uint32_t tmem,
-                                             int wg, uint32_t& it, uint32_t item, Unpack& x) {
+// Columns of a tile that each of the two warpgroups takes: whole chunks of 16.
+__device__ __forceinline__ int tree_columns(int rows) { return (rows + 31) / 32 * 16; }
+
+// A warpgroup's part of one stretch: the weights of nc columns of the tile, in
+// chunks of 16.  `it` counts the CTA's units.  False: a wait ran out.
+__device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t item,
+                                             uint32_t& it) {
+  int* const status = a.status;
+  const int wg = threadIdx.x >> 7;
   const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const int id = 1 + wg;                 // named barrier
-  const int row0 = w.tile * TREE_ROWS;   // of the tile, among the sequence's rows
-  const int col0 = wg * NC;
-  float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 128;  // [4][32]
+  const TreeItem& w = bar->item[item % TR_ITEMS];
+  const int row0 = w.row0;
+  const int nc = tree_columns(w.rows), col0 = wg * nc;
+  constexpr int NC = TREE_ROWS / 2;  // the most there may be
+  float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 256;  // [4][64]
   float* rowtab = reinterpret_cast<float*>(smem + OFF_ROW + (item & 1) * 1024);  // per pair of columns: f, f, -r, -r
-  const int64_t q0 = w.s.q0;
   bool ok = true;
 
   // ---- Q: rows scaled by a power of two to a maximum in [1, 2), f16; rows
   // behind the tile's are zeros.  Sixteen lanes per row.
-  for (int i = tid >> 4; i < NC; i += 8) {
+  for (int i = tid >> 4; i < nc; i += 8) {
     const int c = col0 + i, row = row0 + c, piece = tid & 15;
     float y[8];
     const bool there = c < w.rows;
     if (there) {
       const int node = row / a.group, head = w.kvh * a.group + row - node * a.group;
-      load_bf16x8(a.Q + (q0 + node) * a.ldq + head * 128 + piece * 8, y);
+      load_bf16x8(a.Q + (static_cast<int64_t>(w.q0) + node) * a.ldq + head * 128 + piece * 8, y);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[k] = 0.f;
@@ -379,27 +582,23 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
   if (lane == 0) mbar_arrive(&bar->q_full);
 
   // ---- what each row sees of its tree
-  const int prefix = w.s.len - w.s.n;  // keys that every row sees
-  uint32_t* seen = a.seen + (static_cast<int64_t>(blockIdx.x) * TREE_ROWS + col0) * (TREE_MAX_NODES / 32);
-  if (a.parents && min(w.u1 * TR_UNIT, w.s.len) > prefix) {
-    int16_t* up = reinterpret_cast<int16_t*>(red);  // 256 of them fit
-    for (int i = tid; i < w.s.n; i += 128) {
-      const int p = a.parents[q0 + i];
+  const int prefix = w.len - w.n;  // keys that every row sees
+  // For each node the rows that see it, a bit each: a thread of the last
+  // units has one key.
+  uint32_t* seen = a.seen + (static_cast<int64_t>(blockIdx.x) * 2 + wg) * TREE_MAX_NODES * 2;
+  const bool tree = a.parents != nullptr;
+  if (tree && min(w.u1 * TR_UNIT, w.len) > prefix) {
+    int16_t* up = reinterpret_cast<int16_t*>(red);
+    for (int i = tid; i < w.n; i += 128) {
+      const int p = a.parents[w.q0 + i];
       const bool bad = p < -1 || p >= i;
       if (bad) atomicOr(a.status, CODA_DEV_TREE_RANGE);
       up[i] = static_cast<int16_t>(bad ? -1 : p);
+      reinterpret_cast<uint2*>(seen)[i] = make_uint2(0, 0);
     }
     group_any(id, false);
-    if (tid < NC && col0 + tid < w.rows) {
-      uint32_t m[TREE_MAX_NODES / 32];
-#pragma unroll
-      for (int k = 0; k < TREE_MAX_NODES / 32; ++k) m[k] = 0;
-      for (int j = (row0 + col0 + tid) / a.group; j >= 0; j = up[j])
-#pragma unroll
-        for (int k = 0; k < TREE_MAX_NODES / 32; ++k) m[k] |= (j >> 5) == k ? 1u << (j & 31) : 0u;
-#pragma unroll
-      for (int k = 0; k < TREE_MAX_NODES / 32; ++k) seen[tid * (TREE_MAX_NODES / 32) + k] = m[k];
-    }
+    if (tid < nc && col0 + tid < w.rows)
+      for (int j = (row0 + col0 + tid) / a.group; j >= 0; j = up[j]) atomicOr(seen + 2 * j + (tid >> 5), 1u << (tid & 31));
   }
   group_any(id, false);
 
@@ -410,64 +609,79 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
   bool unset = true;        // some column has no reference
   bool mine_unset = true;   // column col0 + tid (tid < NC)
   const float4* tab4 = reinterpret_cast<const float4*>(rowtab) + (col0 >> 1);
-  uint8_t* pbase = smem + OFF_P + ((col0 >> 6) * HALF_TILE) + tid * 128;
-  const int chunk0 = (col0 & 63) >> 3;
+  uint8_t* pbase = smem + OFF_P + tid * 128;
 
-  for (int u = w.u0; u < w.u1; ++u, ++it) {
+  const int u0 = w.u0, u1 = w.u1, nodes = w.n, group = a.group;
+  for (int u = u0; u < u1; ++u, ++it) {
     const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-    ok = ok && (!x.more || unpack_keys(a, smem, bar, tmem, wg, warp, lane, x));
-    ok = ok && tree_wait(&bar->k_full[buf], ph, bar, a.status) && tree_wait(&bar->s_full[buf], ph, bar, a.status);
+    // (the unpacking is at most three units ahead: no phase of four is missed)
+    ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1, bar, status) && tree_wait(&bar->s_full[buf], ph, bar, status);
     ok = __all_sync(0xffffffffu, ok);
-    float t[NC];
-    float mx = -INFINITY;
-    float inv = 0.f;
-    if (ok) {
-      tc_fence_after();
-      const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
-      uint32_t s[NC];
-      tmem_ldn(tmem + lanes + COL_S + buf * 128 + col0, s);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->s_empty[buf]);
-      inv = fabsf(key.y) < 1e30f ? exp2_sfu(-key.y) : 0.f;  // finite: it meets zero weights too
-      const uint64_t rk = f2_pack(key.x, key.x), lr = f2_pack(key.y, key.y);
-#pragma unroll
-      for (int c = 0; c < NC; c += 2) {
-        const float4 f = tab4[c >> 1];
-        const uint64_t z = f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), rk);
-        f2_unpack(f2_fma(z, f2_pack(f.x, f.y), f2_add(lr, f2_pack(f.z, f.w))), t[c], t[c + 1]);
+    // rows that see this key, where it is a node (or none of the sequence)
+    const int d = u * TR_UNIT + tid - prefix;
+    uint64_t sees = ~0ull;
+    if ((u + 1) * TR_UNIT > prefix && d >= 0) {
+      keep_branch();
+      if (d >= nodes) {
+        sees = 0;
+      } else if (tree) {
+        const uint2 m = __ldcg(reinterpret_cast<const uint2*>(seen) + d);
+        sees = static_cast<uint64_t>(m.y) << 32 | m.x;
+      } else {
+        const int64_t from = static_cast<int64_t>(d) * group - row0 - col0;  // rows from the node's own on
+        sees = from <= 0 ? ~0ull : from >= 64 ? 0 : ~0ull << from;
       }
-      const int d = u * TR_UNIT + tid - prefix;  // this key's node, if it is one
-      if ((u + 1) * TR_UNIT > prefix) {
-        keep_branch();
-        if (a.parents) {
-          const uint32_t* at = seen + (max(d, 0) >> 5);
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (d >= 0 && (d >= w.s.n || !((__ldcg(at + c * (TREE_MAX_NODES / 32)) >> (d & 31)) & 1u))) t[c] = -INFINITY;
-        } else {
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-            if (d >= 0 && (d >= w.s.n || d * a.group > row0 + col0 + c)) t[c] = -INFINITY;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < NC; c += 2) mx = fmaxf(mx, fmaxf(t[c], t[c + 1]));
     }
-    if (group_any(id, !ok || unset || mx > TR_RAISE)) {
-      // a reference rises, or is not there yet
-      if (group_any(id, !ok)) return false;
-      float v[NC];
+    const bool hidden = __any_sync(0xffffffffu, sees != ~0ull);
+    uint32_t t[NC];  // scores, then exponents (fp32 bits)
+    float inv = 0.f;
+#pragma unroll 1
+    for (bool raised = false;; raised = true) {
+      float mx = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
+        inv = fabsf(key.y) < 1e30f ? exp2_sfu(-key.y) : 0.f;  // finite: it meets zero weights too
+        const uint64_t rk = f2_pack(key.x, key.x), lr = f2_pack(key.y, key.y);
+        tmem_columns(tmem + lanes + COL_S + buf * 128 + col0, nc, t);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) v[i] = t[i];
-      const float most = warp_columns<NC, false>(v, lane);
-      if (lane < NC) red[warp * 32 + lane] = most;
+        for (int q = 0; q < NC; q += 16)
+          if (q < nc) {
+#pragma unroll
+            for (int c = q; c < q + 16; c += 2) {
+              const float4 f = tab4[c >> 1];
+              const uint64_t z = f2_mul(f2_pack(__uint_as_float(t[c]), __uint_as_float(t[c + 1])), rk);
+              float x, y;
+              f2_unpack(f2_fma(z, f2_pack(f.x, f.y), f2_add(lr, f2_pack(f.z, f.w))), x, y);
+              t[c] = __float_as_uint(x);
+              t[c + 1] = __float_as_uint(y);
+            }
+            if (hidden) {
+              keep_branch();
+#pragma unroll
+              for (int c = q; c < q + 16; ++c) t[c] = (sees >> c) & 1 ? t[c] : 0xFF800000u;
+            }
+#pragma unroll
+            for (int c = q; c < q + 16; c += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(t[c]), __uint_as_float(t[c + 1])));
+          }
+      }
+      if (raised || !group_any(id, !ok || unset || mx > TR_RAISE)) break;
+      // A reference rises, or is not there yet: then the scores are taken again.
+      if (group_any(id, !ok)) return false;
+#pragma unroll
+      for (int c0 = 0; c0 < NC; c0 += 8)
+        if (c0 < nc) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(t[c0 + i]);
+          const float most = warp_columns<8, false>(v, lane);
+          if (lane < 8) red[warp * 64 + c0 + lane] = most;
+        }
       group_any(id, false);
-      float step = 0.f, shrink = 1.f;
-      if (tid < NC) {
-        const float m = fmaxf(fmaxf(red[tid], red[32 + tid]), fmaxf(red[64 + tid], red[96 + tid]));
+      float shrink = 1.f;
+      if (tid < nc) {
+        const float m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
         if (m > (mine_unset ? -INFINITY : TR_RAISE)) {  // whatever the other rows do
-          step = m;
           shrink = mine_unset ? 1.f : exp2_sfu(-m);
           mine_unset = false;
           const int c = col0 + tid;
@@ -475,26 +689,23 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
         }
       }
       group_any(id, false);  // the maxima are read
-      if (tid < NC) {
-        red[tid] = step;
-        red[32 + tid] = shrink;
-      }
-      unset = group_any(id, tid < NC && mine_unset);
-      const bool before = u > w.u0;  // O holds something
+      if (tid < nc) red[tid] = shrink;
+      unset = group_any(id, tid < nc && mine_unset);
+      const bool before = u > u0;  // O holds something
       if (before) {
         const uint32_t p = it - 1;
-        ok = tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, a.status);
+        ok = tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
 #pragma unroll
       for (int c0 = 0; c0 < NC; c0 += 8) {
+        if (c0 >= nc) break;
         float by[8];
         bool any = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          t[c0 + i] -= red[c0 + i];
-          by[i] = red[32 + c0 + i];
+          by[i] = red[c0 + i];
           l[c0 + i] *= by[i];
           any |= by[i] != 1.f;
         }
@@ -506,55 +717,66 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
           tmem_st8(tmem + lanes + COL_O + col0 + c0, o);
           tmem_st_wait();
         }
+        keep_branch();
       }
       tc_fence_before();
       group_any(id, false);  // red is read
     }
-    // ---- P', into the place that the product of two units ago has read
-    ok = ok && tree_wait(&bar->o_done[buf], ph ^ 1, bar, a.status);
-    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar->s_empty[buf]);
+    // ---- P', into the place that the product of two units ago has read: it was
+    // issued before these scores, so it is done
     if (ok) {
       const uint64_t in2 = f2_pack(inv, inv);
       uint8_t* at = pbase + buf * TILE;
 #pragma unroll
       for (int c = 0; c < NC; c += 8) {
+        if (c >= nc) break;
         uint32_t p[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float x = exp2_sfu(t[c + 2 * k]), y = exp2_sfu(t[c + 2 * k + 1]);
+          const float x = exp2_sfu(__uint_as_float(t[c + 2 * k])), y = exp2_sfu(__uint_as_float(t[c + 2 * k + 1]));
           f2_unpack(f2_fma(f2_pack(x, y), in2, f2_pack(l[c + 2 * k], l[c + 2 * k + 1])), l[c + 2 * k], l[c + 2 * k + 1]);
           p[k] = pack_f16(x, y);
         }
-        *reinterpret_cast<uint4*>(at + (((chunk0 + (c >> 3)) ^ (tid & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+        const int to = (col0 + c) >> 3;  // piece of eight rows
+        *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->p_full[buf]);
-      if (x.more) ok = unpack_values(a, smem, bar, wg * 4 + warp, lane, x);
     }
   }
 
   // ---- the end: l over the keys, O out of TMEM
   {
     const uint32_t p = it - 1;
-    ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, a.status);
+    ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
     ok = __all_sync(0xffffffffu, ok);
-    const float sum = warp_columns<NC, true>(l, lane);
-    if (lane < NC) red[warp * 32 + lane] = sum;
+#pragma unroll
+    for (int c0 = 0; c0 < NC; c0 += 16) {
+      if (c0 >= nc) break;
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = l[c0 + i];
+      const float sum = warp_columns<16, true>(v, lane);
+      if (lane < 16) red[warp * 64 + c0 + lane] = sum;
+    }
     if (group_any(id, !ok)) return false;
-    const bool alone = w.u0 == 0 && w.u1 == w.s.units;
+    const bool alone = w.u0 == 0 && w.u1 == w.units;
     const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.u0 > 0 ? 0 : 1);
     float total = 0.f;
-    if (tid < NC) total = (red[tid] + red[32 + tid]) + (red[64 + tid] + red[96 + tid]);
+    if (tid < nc) total = (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]);
     group_any(id, false);
-    if (tid < NC) {
+    if (tid < nc) {
       red[tid] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);  // NaN stays NaN
       const int c = col0 + tid;
       if (c < w.rows) {
         const float r = -rowtab[(c >> 1) * 4 + (c & 1) + 2];
         const int row = row0 + c, node = row / a.group, head = w.kvh * a.group + row - node * a.group;
         if (alone)
-          a.lse[(q0 + node) * a.n_q + head] = total == 0.f ? -INFINITY : r * 0.69314718056f + logf(total);
+          a.lse[(static_cast<int64_t>(w.q0) + node) * a.n_q + head] = total == 0.f ? -INFINITY : r * 0.69314718056f + logf(total);
         else
           a.part_lse[slot * a.part_rows + c] = total == 0.f ? -INFINITY : r + log2f(total);
       }
@@ -563,7 +785,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
     tc_fence_after();
     const int d = warp * 32 + lane;  // element
 #pragma unroll 1
-    for (int c0 = 0; c0 < NC && col0 + c0 < w.rows; c0 += 8) {
+    for (int c0 = 0; c0 < nc && col0 + c0 < w.rows; c0 += 8) {
       uint32_t o[8];
       tmem_ldn(tmem + lanes + COL_O + col0 + c0, o);
       if (alone) {
@@ -572,7 +794,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
           const int c = col0 + c0 + i, row = row0 + c;
           if (c < w.rows) {
             const int node = row / a.group, head = w.kvh * a.group + row - node * a.group;
-            a.O[((q0 + node) * a.n_q + head) * 128 + d] = __float2bfloat16(__uint_as_float(o[i]) * red[c0 + i]);
+            a.O[((static_cast<int64_t>(w.q0) + node) * a.n_q + head) * 128 + d] = __float2bfloat16(__uint_as_float(o[i]) * red[c0 + i]);
           }
         }
       } else {
@@ -591,35 +813,36 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, const TreeWalk& 
   return true;
 }
 
-__global__ void __launch_bounds__(TR_THREADS, 1) attn_tree_kernel(const TreeArgs a) {
-  extern __shared__ uint8_t tree_smem[];
-  __shared__ int64_t sh_warp[TR_THREADS / 32], sh_before;
-  __shared__ int sh_seq;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tree_smem) + 1023) & ~uintptr_t(1023));
+__global__ void __launch_bounds__(TR_THREADS, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap sf,
+                     const __grid_constant__ CUtensorMap scale, const TreeArgs a) {
+  uint8_t* smem = tree_shared();
   TreeBars* bar = reinterpret_cast<TreeBars*>(smem + OFF_BAR);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < TR_STAGES; ++s) {
       mbar_init(&bar->raw_full[s], 1);
-      mbar_init(&bar->raw_empty[s], TR_GROUPS * 4);
+      mbar_init(&bar->raw_empty[s], 4);
     }
+    for (int s = 0; s < 4; ++s) mbar_init(&bar->key_full[s], 4);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar->k_full[s], TR_GROUPS * 4);
-      mbar_init(&bar->v_full[s], TR_GROUPS * 4);
+      mbar_init(&bar->k_full[s], 4);
+      mbar_init(&bar->v_full[s], 4);
       mbar_init(&bar->s_full[s], 1);
-      mbar_init(&bar->s_empty[s], TR_GROUPS * 4);
-      mbar_init(&bar->p_full[s], TR_GROUPS * 4);
+      mbar_init(&bar->s_empty[s], 8);
+      mbar_init(&bar->p_full[s], 8);
       mbar_init(&bar->o_done[s], 1);
     }
-    mbar_init(&bar->q_full, TR_GROUPS * 4);
-    mbar_init(&bar->o_empty, TR_GROUPS * 4);
+    mbar_init(&bar->q_full, 8);
+    mbar_init(&bar->o_empty, 8);
+    for (int i = 0; i < TR_ITEMS; ++i) mbar_init(&bar->item_full[i], 1);
     mbar_init(&bar->drain, 1);
     bar->abort = 0;
-    sh_seq = a.B;
-    sh_before = 0;
+    bar->seq = a.B;
+    bar->before = 0;
     fence_mbar_init();
   }
-  if (warp == TR_GROUPS * 4 + 1) {
+  if (warp == TR_MMA_WARP) {
     tmem_alloc<false>(&bar->tmem, 512);
     tmem_relinquish<false>();
   }
@@ -638,7 +861,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1) attn_tree_kernel(const TreeArgs
     const int64_t n = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += n;
   }
-  if (lane == 31) sh_warp[warp] = incl;
+  if (lane == 31) bar->scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -646,8 +869,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1) attn_tree_kernel(const TreeArgs
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < TR_THREADS / 32; ++w) {
-    if (w < warp) incl += sh_warp[w];
-    total += sh_warp[w];
+    if (w < warp) incl += bar->scan[w];
+    total += bar->scan[w];
   }
   // no CTA between two others of an item is left without a unit
   const int64_t per = max(static_cast<int64_t>(TR_COST_MANY), (total + gridDim.x - 1) / gridDim.x);
@@ -658,8 +881,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1) attn_tree_kernel(const TreeArgs
       const int64_t n = tree_seq(a, b, false).place_kv * a.c.n_kv;
       if (blockIdx.x == 0) a.places[b] = before;
       if (first >= before && first < before + n) {
-        sh_seq = b;
-        sh_before = before;
+        bar->seq = b;
+        bar->before = before;
       }
       before += n;
     }
@@ -670,158 +893,75 @@ __global__ void __launch_bounds__(TR_THREADS, 1) attn_tree_kernel(const TreeArgs
   }
   __syncthreads();
 
-  TreeWalk w;
-  w.b = sh_seq;
-  w.base = sh_before;
-  w.item = 0;
   bool ok = true;
   if (first < last) {
-    w.s = tree_seq(a, w.b, false);
-    // to the item that holds `first`
-    const int64_t d = first - w.base, kv = d / w.s.place_kv;
-    const int64_t tile = (d - kv * w.s.place_kv) / (static_cast<int64_t>(w.s.units) * TR_COST_MANY + TR_END);
-    const int64_t tl = min(tile, static_cast<int64_t>(w.s.tiles - 1));
-    w.item = static_cast<int>(kv * w.s.tiles + tl);
-    w.base += kv * w.s.place_kv + tl * (static_cast<int64_t>(w.s.units) * TR_COST_MANY + TR_END);
-
-    if (warp < TR_GROUPS * 4) {
-      const int wg = warp >> 2;
-      uint32_t it = 0, item = 0;
-      Unpack x;
-      x.it = 0;
-      x.more = true;
-      x.rs_zero = __float_as_uint(0x1p-12f);
-      ok = unpack_keys(a, smem, bar, tmem, wg, warp & 3, lane, x);
-      if (ok && x.more) ok = unpack_values(a, smem, bar, warp, lane, x);
-      for (; ok && w.next(a, first, last); ++item) {
-        if (w.rows <= 32)
-          ok = tree_softmax<8>(a, w, smem, bar, tmem, wg, it, item, x);
-        else if (w.rows <= 64)
-          ok = tree_softmax<16>(a, w, smem, bar, tmem, wg, it, item, x);
-        else
-          ok = tree_softmax<32>(a, w, smem, bar, tmem, wg, it, item, x);
+    if (tid == TR_COPY_WARP * 32) {
+      // to the item that holds `first`
+      TreeCopies c;
+      TreeWalk& w = c.w;
+      w.b = bar->seq;
+      w.base = bar->before;
+      w.first = first;
+      w.last = last;
+      w.s = tree_seq(a, w.b, false);
+      const int64_t many = static_cast<int64_t>(w.s.units) * TR_COST_MANY + TR_END;
+      const int64_t d = first - w.base, kv = d / w.s.place_kv;
+      const int64_t tile = min((d - kv * w.s.place_kv) / many, static_cast<int64_t>(w.s.tiles - 1));
+      w.item = static_cast<int>(kv * w.s.tiles + tile);
+      w.base += kv * w.s.place_kv + tile * many;
+      w.u0 = w.u1 = 0;
+      c.u = 0;
+      c.it = c.items = 0;
+      c.done = 0;
+      bar->copies = c;
+    }
+    __syncwarp();
+    // Registers: 512 threads x 128 at launch = 256 x 192 + 128 x 72 + 128 x 56
+    if (warp < TR_UNPACK) {
+      reg_inc<192>();
+      uint32_t it = 0;
+      for (uint32_t item = 0; ok; ++item) {
+        ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
+        ok = !group_any(1 + (warp >> 2), !ok);
+        if (!ok || bar->item[item % TR_ITEMS].rows == 0) break;
+        ok = tree_softmax(a, smem, bar, tmem, item, it);
       }
+    } else if (warp < TR_COPY_WARP) {
+      reg_dec<72>();
+      uint32_t rs_zero = __float_as_uint(0x1p-12f);  // row scale that rows of zeros take
+      bool more = true;
+      for (uint32_t it = 0; ok && more; ++it) ok = unpack(a.status, smem, bar, tmem, warp - TR_UNPACK, lane, it, min(a.c.page_shift, 7), rs_zero, more) || !more;
     } else {
-      if (warp == TR_GROUPS * 4) {
-        // ------------------------------------------------------------ copies
-        // Lane i of each group of eight takes part i of a unit (a page, or 128
-        // keys of one): group 0 the codes, 1 the block scales, 2 the row scales,
-        // keys and values each.
-        const KvCache& kc = a.c;
-        const int part = lane & 7, arr = lane >> 3;
-        const int part_shift = min(kc.page_shift, 7);
-        const uint32_t row_bytes = arr == 0 ? 64 : arr == 1 ? 8 : 4;
-        const uint32_t to_k = arr == 0 ? RW_K : arr == 1 ? RW_SFK : RW_RSK, to_v = arr == 0 ? RW_V : arr == 1 ? RW_SFV : RW_RSV;
-        const uint8_t* src = arr == 0 ? kc.codes : arr == 1 ? kc.sf : reinterpret_cast<const uint8_t*>(kc.scale);
-        const int64_t plane = static_cast<int64_t>(kc.n_kv) << kc.page_shift;
-        uint32_t it = 0;
-        while (ok && w.next(a, first, last)) {
-          const int32_t* table = a.table + static_cast<int64_t>(w.b) * a.max_pages;
-          auto page_of = [&](int u) {  // of this lane's part of unit u; -1: nothing there
-            const int k = u * TR_UNIT + (part << part_shift);
-            return u < w.u1 && (part << part_shift) < TR_UNIT && k < w.s.len ? table[k >> kc.page_shift] : -1;
-          };
-          int page = page_of(w.u0);
-          for (int u = w.u0; u < w.u1; ++u, ++it) {
-            const int nextp = page_of(u + 1);
-            const int k = u * TR_UNIT + (part << part_shift);
-            const bool named = (part << part_shift) < TR_UNIT && k < w.s.len;
-            const bool in = named && page >= 0 && page < kc.num_pages;
-            if (named && !in && arr == 0) atomicOr(a.status, CODA_DEV_PAGE_RANGE);
-            // whole groups of 16 keys: rows behind the length exist within the page
-            const int n = in ? min(1 << part_shift, (w.s.len - k + 15) & ~15) : 0;
-            const uint32_t bytes = arr < 3 ? n * row_bytes : 0;
-            const uint32_t st = it % TR_STAGES;
-            ok = tree_wait(&bar->raw_empty[st], ((it / TR_STAGES) & 1) ^ 1, bar, a.status, 100);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t sum = __reduce_add_sync(0xffffffffu, 2 * bytes);
-            const uint32_t mask =
-                __reduce_or_sync(0xffffffffu, arr == 0 && n ? ((1u << (n / 16)) - 1) << (part << part_shift >> 4) : 0);
-            if (lane == 0) {
-              bar->keys_in[st] = mask;
-              bar->left[st] = w.s.len - u * TR_UNIT;
-              if (sum == 0) mbar_arrive(&bar->raw_full[st]);
-            }
-            mbar_arrive_expect_tx(&bar->raw_full[st], sum, lane == 0 && sum != 0);
-            __syncwarp();
-            if (bytes) {
-              const int64_t row = cache_row(kc, page, 0, w.kvh, k & ((1 << kc.page_shift) - 1));
-              uint8_t* to = smem + OFF_RAW + st * TR_RAW + (part << part_shift) * row_bytes;
-              bulk_load(to + to_k, src + row * row_bytes, bytes, &bar->raw_full[st], 1);
-              bulk_load(to + to_v, src + (row + plane) * row_bytes, bytes, &bar->raw_full[st], 1);
-            }
-            page = nextp;
-          }
-        }
-        if (ok) {  // nothing more
-          const uint32_t st = it % TR_STAGES;
-          ok = tree_wait(&bar->raw_empty[st], ((it / TR_STAGES) & 1) ^ 1, bar, a.status, 100);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok && lane == 0) {
-            bar->keys_in[st] = TR_NO_MORE;
-            mbar_arrive(&bar->raw_full[st]);
-          }
-        }
-        if (!ok) {
-          // let every copy already issued land before the CTA's memory is reused
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < 2000000ull) {
-          }
-        }
-      } else {
-        // ------------------------------------------------------------ products
+      reg_dec<56>();
+      if (warp == TR_COPY_WARP) {
+        int page = -1;  // of the lane's part of the next unit
         const uint32_t el = elect_one();
-        uint32_t it = 0, items = 0;
-        bool issued = false;
-        const uint32_t q = smem_u32(smem + OFF_Q);
-        auto wait = [&](uint64_t* b, uint32_t parity) {
-          ok = ok && tree_wait(b, parity, bar, a.status);
+        while (ok && !bar->copies.done) ok = copy_unit(a, &codes, &sf, &scale, smem, bar, lane, el, page);
+      } else if (warp == TR_MMA_WARP) {
+        const uint32_t el = elect_one();
+        uint32_t it = 0;
+        for (uint32_t item = 0; ok; ++item) {
+          ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
           ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
-          return ok;
-        };
-        while (ok && w.next(a, first, last)) {
-          const int n = w.u1 - w.u0;
-          const uint32_t id_s = idesc_f16(128, w.rows <= 32 ? 32 : w.rows <= 64 ? 64 : 128, 0, 0);
-          const uint32_t id_o = idesc_f16(128, w.rows <= 64 ? 64 : 128, 1, 1);
-          auto scores = [&](uint32_t i) {
-            const uint32_t buf = i & 1, ph = (i >> 1) & 1;
-            if (!wait(&bar->k_full[buf], ph) || !wait(&bar->s_empty[buf], ph ^ 1)) return;
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              umma_bf16_ts(tmem + COL_S + buf * 128, tmem + COL_K + buf * 64 + x * 8,
-                           sdesc_sw128(q + (x >> 2) * HALF_TILE + (x & 3) * 32, 16, 1024), id_s, x > 0, el);
-            umma_commit(&bar->s_full[buf], el);
-            issued = true;
-          };
-          if (!wait(&bar->q_full, items & 1)) break;
-          scores(it);
+          const TreeItem& w = bar->item[item % TR_ITEMS];
+          const int rows = w.rows, n = w.u1 - w.u0;
+          if (!ok || rows == 0) break;
+          const int ns = 2 * tree_columns(rows), no = (ns + 63) & ~63;
+          ok = tree_wait(&bar->q_full, item & 1, bar, a.status);
+          ok = __all_sync(0xffffffffu, ok) && issue_scores(a.status, smem, bar, tmem, it, ns, el);
           for (int j = 0; j < n && ok; ++j, ++it) {
-            if (j + 1 < n) scores(it + 1);
-            if (!ok || (j == 0 && !wait(&bar->o_empty, (items & 1) ^ 1))) break;
-            const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-            if (!wait(&bar->v_full[buf], ph) || !wait(&bar->p_full[buf], ph)) break;
-            const uint32_t v = smem_u32(smem + OFF_V + buf * TILE), p = smem_u32(smem + OFF_P + buf * TILE);
-#pragma unroll
-            for (int x = 0; x < 8; ++x)  // 16 keys a step
-              umma_bf16(tmem + COL_O, sdesc_sw128(v + x * 2048, HALF_TILE, 1024), sdesc_sw128(p + x * 2048, HALF_TILE, 1024),
-                        id_o, (j | x) > 0, el);
-            umma_commit(&bar->o_done[buf], el);
+            if (j + 1 < n) ok = issue_scores(a.status, smem, bar, tmem, it + 1, ns, el);
+            ok = ok && issue_outputs(a.status, smem, bar, tmem, it, no, j == 0, item, el);
           }
-          ++items;
-        }
-        if (!ok && issued) {
-          umma_commit(&bar->drain, el);
-          mbar_wait_drain(&bar->drain, 0, 200000000ull);
         }
       }
     }
+    if (!ok) tree_drain(bar, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == TR_GROUPS * 4 + 1) {
+  if (warp == TR_MMA_WARP) {
     __syncwarp();
     tmem_dealloc<false>(tmem, 512);
   }
@@ -879,10 +1019,28 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeArgs a) {
 
 }  // namespace
 
-cudaError_t launch_attn_tree(const TreeArgs& a, int sms, cudaStream_t s) {
+bool cache_maps(CUtensorMap* m, const KvCache& c) {
+  const uint64_t page = uint64_t(1) << c.page_shift, kv = c.n_kv, pages = c.num_pages;
+  const uint32_t part = static_cast<uint32_t>(std::min<uint64_t>(page, TR_UNIT));
+  {
+    const uint64_t dims[5] = {64, page, kv, 2, pages}, st[4] = {64, page * 64, kv * page * 64, 2 * kv * page * 64};
+    const uint32_t box[5] = {64, part, 1, 2, 1};
+    if (!encode_cache_map(&m[0], c.codes, 1, 5, dims, st, box, true)) return false;
+  }
+  for (int i = 1; i < 3; ++i) {  // words of a page's rows: two of block scales each, one row scale
+    const uint64_t row = page * (i == 1 ? 2 : 1);
+    const uint64_t dims[4] = {row, kv, 2, pages}, st[3] = {row * 4, kv * row * 4, 2 * kv * row * 4};
+    const uint32_t box[4] = {part * (i == 1 ? 2 : 1), 1, 2, 1};
+    if (!encode_cache_map(&m[i], i == 1 ? static_cast<const void*>(c.sf) : c.scale, 4, 4, dims, st, box, false)) return false;
+  }
+  return true;
+}
+
+cudaError_t launch_attn_tree(const TreeArgs& a, const CUtensorMap* maps, int sms, cudaStream_t s) {
   cudaError_t e = attn_smem_attribute(reinterpret_cast<const void*>(attn_tree_kernel), 7, TR_SMEM);
   if (e != cudaSuccess) return e;
-  e = attn_launch(attn_tree_kernel, std::min(sms, TREE_MAX_CTAS), TR_THREADS, TR_SMEM, s, a);
+  e = attn_launch(attn_tree_kernel, std::min(sms, TREE_MAX_CTAS), TR_THREADS, TR_SMEM, s, maps[0], maps[1], maps[2],
+                  a);
   if (e != cudaSuccess) return e;
   return attn_launch(attn_tree_join_kernel, (static_cast<int64_t>(a.T) * a.n_q + 7) / 8, 256, 0, s, a);
 }

@@ -1,5 +1,7 @@
 // Attention of drafted trees over the 4-bit cache: arguments and launcher.
 #pragma once
+#include <cuda.h>
+
 #include "coda_kvcache.cuh"
 
 namespace coda {
@@ -22,12 +24,17 @@ struct TreeArgs {
   __nv_bfloat16* O;        // [T, n_q * 128]
   float* lse;              // [T, n_q]
   int64_t* places;         // [B + 2]: places on the line of work before each sequence, their total, places per CTA
-  uint32_t* seen;          // [TREE_MAX_CTAS, TREE_ROWS, TREE_MAX_NODES / 32] what each row of a CTA's tile sees of its tree
+  uint32_t* seen;          // [TREE_MAX_CTAS, 2, TREE_MAX_NODES, 2] rows of a CTA's tile that see a node, by warpgroup: 64 bits
   float* part;             // [2 * TREE_MAX_CTAS, part_rows, 128] normalised partial outputs
   float* part_lse;         // [2 * TREE_MAX_CTAS, part_rows] log2 domain
   int part_rows;
   int* status;
 };
-cudaError_t launch_attn_tree(const TreeArgs& a, int sms, cudaStream_t s);
+// maps: codes, block scales, row scales (see cache_maps).
+cudaError_t launch_attn_tree(const TreeArgs& a, const CUtensorMap* maps, int sms, cudaStream_t s);
+
+// The cache's arrays as tensors whose boxes are one head's rows of a page, at
+// most 128 of them, keys and values together.
+bool cache_maps(CUtensorMap* maps, const KvCache& c);
 
 }  // namespace coda

@@ -38,7 +38,7 @@ int rope(const coda_bf16* X, int64_t ldx, const int32_t* pos, const float* cs, i
 void lay_tree(Cursor& c, coda::TreeArgs& a, int64_t T, int64_t batch, int group) {
   a.part_rows = static_cast<int>(std::min<int64_t>(coda::TREE_ROWS, T * group));
   a.places = c.take<int64_t>(batch + 2);
-  a.seen = c.take<uint32_t>(int64_t(coda::TREE_MAX_CTAS) * coda::TREE_ROWS * (coda::TREE_MAX_NODES / 32));
+  a.seen = c.take<uint32_t>(int64_t(coda::TREE_MAX_CTAS) * coda::TREE_MAX_NODES * (coda::TREE_ROWS / 32));
   a.part = c.take<float>(int64_t(2) * coda::TREE_MAX_CTAS * a.part_rows * coda::ATTN_D);
   a.part_lse = c.take<float>(int64_t(2) * coda::TREE_MAX_CTAS * a.part_rows);
 }
@@ -163,7 +163,9 @@ int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* co
   if (max_pages >= (int64_t(1) << 31) || max_pages * page_size >= (int64_t(1) << 31) - 256) return CODA_ERR_UNSUPPORTED;
   CK(check_ws(ws, ws_bytes, coda_attention_tree_nvfp4_workspace_size(T, batch, n_q, n_kv, head_dim)));
   const int sms = coda::device_sms();
-  if (sms <= 0) return CODA_ERR_CUDA;
+  if (sms <= 0 || !coda::tensor_map_encoder()) return CODA_ERR_CUDA;
+  CUtensorMap maps[3] = {};
+  if (num_pages > 0 && !coda::cache_maps(maps, a.c)) return CODA_ERR_CUDA;  // without pages nothing is ever loaded
   Cursor cur{static_cast<uint8_t*>(ws)};
   lay_tree(cur, a, T, batch, n_q / n_kv);
   a.Q = B(Q);
@@ -181,7 +183,7 @@ int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* co
   a.O = B(O);
   a.lse = lse;
   a.status = static_cast<int*>(ws);
-  CU(coda::launch_attn_tree(a, sms, static_cast<cudaStream_t>(stream)));
+  CU(coda::launch_attn_tree(a, maps, sms, static_cast<cudaStream_t>(stream)));
   return CODA_OK;
 }
 

@@ -25,6 +25,11 @@ bool tensor_map_encoder();
 bool encode_bf16_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* strides,
                      const uint32_t* box);
 
+// A tensor map of bytes (words 1) or 32-bit words (words 4) with up to five
+// dimensions, innermost first; strides in bytes; 64-byte swizzle or none.
+bool encode_cache_map(CUtensorMap* m, const void* ptr, int words, int rank, const uint64_t* dims, const uint64_t* strides,
+                      const uint32_t* box, bool swizzle64);
+
 // Tensor maps in the order A0, B0, A1, B1.  `cg` is the cluster size: 1
 // (single CTAs), 2 (a cta_group::2 pair) or 4 (two pairs sharing B by TMA
 // multicast); the launcher sizes the persistent grid.
