@@ -56,14 +56,17 @@ constexpr int TR_RAW = 19456;
 __device__ __forceinline__ int raw_row(int key, int shift) { return ((key >> shift) << (shift + 1)) + (key & ((1 << shift) - 1)); }
 constexpr uint32_t TILE = 32768, HALF_TILE = 16384;  // 128 x 128 f16, as two halves of 64 columns
 constexpr uint32_t OFF_Q = 0, OFF_P = TILE, OFF_V = 3 * TILE, OFF_RAW = 5 * TILE;
-constexpr uint32_t OFF_ROW = OFF_RAW + TR_STAGES * TR_RAW;  // [2][64] pairs of rows, by item: factors, -r
-constexpr uint32_t OFF_KEY = OFF_ROW + 2048;                // [4][128] row scale of the key, log2 of the value's
+constexpr uint32_t OFF_ROW = OFF_RAW + TR_STAGES * TR_RAW;  // [2][128] minus the rows' references, by item
+constexpr uint32_t OFF_KEY = OFF_ROW + 1024;                // [4][128] row scale of the key, log2 of the value's
 constexpr uint32_t OFF_RED = OFF_KEY + 4096;                // [2][4][64] exchange of a warpgroup
 constexpr uint32_t OFF_BAR = OFF_RED + 2048;
 constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
-constexpr float TR_RAISE = 10.f;
+constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
+constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 constexpr uint32_t TR_NO_MORE = 1u << 31;
 constexpr uint64_t TR_WAIT_NS = 2000000000ull;
 
@@ -99,30 +102,20 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : CODA_R8(r, 0), CODA_R8(r, 8)
+      : CODA_R32(r, 0)
       : "r"(taddr)
       : "memory");
 }
-// The first n (a multiple of 16) of 64 columns, or more of them.
-__device__ __forceinline__ void tmem_columns(uint32_t taddr, int n, uint32_t (&r)[64]) {
-  if (n > 32)
-    tmem_ld64(taddr, r);
-  else if (n > 16)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
-        "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : CODA_R32(r, 0)
-        : "r"(taddr)
-        : "memory");
-  else
-    tmem_ld16(taddr, r);
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), CODA_W8(r, 0)
@@ -361,36 +354,40 @@ __device__ __forceinline__ bool copy_unit(const TreeArgs& a, const CUtensorMap* 
   return true;
 }
 
-// The scores of unit i, once every warp has unpacked its keys.
-__device__ __forceinline__ bool issue_scores(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, int n,
+// The scores of unit i, once its keys are unpacked.  The places are constants
+// (BUF is i's parity), so that descriptors stay in uniform registers: with
+// computed ones eight products took twice the time to issue that they run.
+template <int BUF>
+__device__ __forceinline__ bool issue_scores(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
                                              uint32_t el) {
-  const uint32_t buf = i & 1, ph = (i >> 1) & 1;
-  const bool ok = tree_wait(&bar->k_full[buf], ph, bar, status) && tree_wait(&bar->s_empty[buf], ph ^ 1, bar, status);
+  const uint32_t ph = (i >> 1) & 1;
+  const bool ok = tree_wait(&bar->k_full[BUF], ph, bar, status) && tree_wait(&bar->s_empty[BUF], ph ^ 1, bar, status);
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
-  const uint32_t q = smem_u32(smem + OFF_Q), id = idesc_f16(128, n, 0, 0);
+  const uint32_t q = smem_u32(smem + OFF_Q);
 #pragma unroll
   for (int x = 0; x < 8; ++x)
-    umma_bf16_ts(tmem + COL_S + buf * 128, tmem + COL_K + buf * 64 + x * 8,
+    umma_bf16_ts(tmem + COL_S + BUF * 128, tmem + COL_K + BUF * 64 + x * 8,
                  sdesc_sw128(q + (x >> 2) * HALF_TILE + (x & 3) * 32, 16, 1024), id, x > 0, el);
-  umma_commit(&bar->s_full[buf], el);
+  umma_commit(&bar->s_full[BUF], el);
   return true;
 }
 // O^T += V'^T P'^T of unit i; first: of an item, whose predecessor's O has left.
-__device__ __forceinline__ bool issue_outputs(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, int n,
+template <int BUF>
+__device__ __forceinline__ bool issue_outputs(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
                                               bool first, uint32_t item, uint32_t el) {
-  const uint32_t buf = i & 1, ph = (i >> 1) & 1;
-  const bool ok = tree_wait(&bar->p_full[buf], ph, bar, status) && tree_wait(&bar->v_full[buf], ph, bar, status) &&
+  const uint32_t ph = (i >> 1) & 1;
+  const bool ok = tree_wait(&bar->p_full[BUF], ph, bar, status) && tree_wait(&bar->v_full[BUF], ph, bar, status) &&
                   (!first || tree_wait(&bar->o_empty, (item & 1) ^ 1, bar, status));
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
-  const uint32_t v = smem_u32(smem + OFF_V + buf * TILE), p = smem_u32(smem + OFF_P + buf * TILE);
-  const uint32_t id = idesc_f16(128, n, 1, 1);
+  const uint32_t v = smem_u32(smem + OFF_V + BUF * TILE), p = smem_u32(smem + OFF_P + BUF * TILE);
+  const uint32_t more = !first;
 #pragma unroll
   for (int x = 0; x < 8; ++x)  // 16 keys a step
     umma_bf16(tmem + COL_O, sdesc_sw128(v + x * 2048, HALF_TILE, 1024), sdesc_sw128(p + x * 2048, HALF_TILE, 1024), id,
-              !first || x > 0, el);
-  umma_commit(&bar->o_done[buf], el);
+              x > 0 ? 1u : more, el);
+  umma_commit(&bar->o_done[BUF], el);
   return true;
 }
 // After a wait that ran out: let what was issued land before the CTA's memory
@@ -406,36 +403,79 @@ __device__ __forceinline__ void tree_drain(TreeBars* bar, int warp, int lane) {
   }
 }
 
+// Places of a lane in a stage: its key's row, and the values of keys k0 + 4 i
+// (k0 = lane / 8 of the warp's 32), of which it takes elements 16 (lane % 8) ...
+struct UnpackLane {
+  uint32_t krow;      // row of the key
+  uint32_t v[2][2];   // codes of the values, for i < 4 and i >= 4, even and odd i
+  uint32_t sf[2];     // their block scales
+  uint32_t to[2];     // where V' goes, even and odd i: the first half of the lanes
+  __device__ __forceinline__ UnpackLane(int g, int lane, int shift) {
+    krow = raw_row(g * 32 + lane, shift);
+    const int piece = lane & 7, k0 = lane >> 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = raw_row(g * 32 + 16 * h + k0, shift) + (1 << shift);
+      sf[h] = RW_SF + row * 8 + piece;
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        v[h][o] = RW_CODES + row * 64 + ((((piece >> 1) ^ (row >> 1) ^ (2 * o)) & 3) << 4) + (piece & 1) * 8;
+    }
+    // pieces 2 p and 2 p + 1 of the row, exchanged for the upper elements so that
+    // eight lanes write to different banks
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      to[o] = (piece >> 2) * HALF_TILE + (g * 32 + k0) * 128 + (((2 * (piece & 3) + (piece >> 2)) ^ (k0 + 4 * o)) << 4);
+  }
+};
+
 // Unit `it` unpacked by four warps, a warp's 32 keys each.  K': a thread per
 // key, to the lane of TMEM that is its row.  False: a wait ran out, or no unit
 // (`more`) is left.
 __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane, uint32_t it,
-                                       int shift, uint32_t& rs_zero, bool& more) {
+                                       int shift, const UnpackLane& x, uint32_t& rs_zero, bool& more) {
   const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
   bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1, bar, status);
   if (!__all_sync(0xffffffffu, ok)) return false;
   const uint32_t on = bar->keys_in[st];
-  const int left = bar->left[st];
+  const int left = bar->left[st] - 32 * g;  // keys of the sequence from the warp's first on
   more = on != TR_NO_MORE;
   if (!more) return false;
+  const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
+  const bool in = ((on >> (2 * g + (lane >> 4))) & 1u) && lane < left;  // else whatever the stage held before
+  const uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + x.krow * 8);
+  const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + (x.krow + (1 << shift)) * 8);
+  const float rsk = *reinterpret_cast<const float*>(raw + RW_RS + x.krow * 4);
+  const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (x.krow + (1 << shift)) * 4);
+  uint4 kc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    kc[q] = *reinterpret_cast<const uint4*>(raw + RW_CODES + x.krow * 64 + ((q ^ ((x.krow >> 1) & 3)) << 4));
+  // the key's scales
+  bool odd;  // some key's value needs a second look
+  {
+    const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+    const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
+    const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
+    if (least < 0x7F7FFFFFu) rs_zero = least;
+    const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
+    odd = __any_sync(0xffffffffu, !in || sick || rs < 0x1p-100f);
+    float2 meta;
+    meta.x = in ? rsk : 0.f;
+    // below 2^-100 the sum l would pass fp32's end: V' takes the rest
+    meta.y = !in ? -INFINITY : sick ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
+    *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
+  }
   ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
-  const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
-  const int key = g * 32 + lane, krow = raw_row(key, shift);
-  const bool in = ((on >> (key >> 4)) & 1u) && key < left;
-  uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + krow * 8);
-  if (!in) sfk = make_uint2(0, 0);
-  uint4 kc[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) kc[q] = *reinterpret_cast<const uint4*>(raw + RW_CODES + krow * 64 + ((q ^ ((krow >> 1) & 3)) << 4));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t o[32];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const uint4 v = kc[h * 2 + q];
-      const uint32_t two = e4m3x2_f16(((h ? sfk.y : sfk.x) >> (16 * q)) & 0xFFFFu);
+      const uint32_t two = in ? e4m3x2_f16(((h ? sfk.y : sfk.x) >> (16 * q)) & 0xFFFFu) : 0;
       const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -447,23 +487,13 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
     }
     tmem_st32(tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64 + h * 32, o);
   }
-  bool tiny;
-  {  // the key's scales
-    const int vrow = krow + (1 << shift);
-    const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + vrow * 8);
-    const float rsk = *reinterpret_cast<const float*>(raw + RW_RS + krow * 4);
-    const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + vrow * 4);
-    const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
-    const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
-    const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
-    if (least < 0x7F7FFFFFu) rs_zero = least;
-    const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
-    tiny = __any_sync(0xffffffffu, in && rs < 0x1p-100f);
-    float2 meta;
-    meta.x = in ? rsk : 0.f;
-    // below 2^-100 the sum l would pass fp32's end: V' takes the rest
-    meta.y = !in ? -INFINITY : sick ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
-    *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + key * 8) = meta;
+  // the values' codes and scales, while the store goes on
+  uint2 c[8];
+  uint32_t sv[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    c[i] = *reinterpret_cast<const uint2*>(raw + x.v[i >> 2][i & 1] + (i & 3) * 256);
+    sv[i] = e4m3x2_f16(raw[x.sf[i >> 2] + (i & 3) * 32] * 0x101u);
   }
   tmem_st_wait();
   tc_fence_before();
@@ -472,48 +502,35 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
     mbar_arrive(&bar->key_full[it & 3]);
     mbar_arrive(&bar->k_full[buf]);
   }
-
-  // V': a lane sixteen elements of eight keys.  A block scale that is NaN
-  // leaves zeros (the key's weights are NaN).
+  if (odd) {  // zeros outside the sequence and for NaN (the key's weights are NaN), or a small row scale
+    keep_branch();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = 4 * i + (lane >> 3);
+      const bool kin = ((on >> (2 * g + (i >> 2))) & 1u) && k < left;
+      const uint32_t row = raw_row(g * 32 + k, shift) + (1 << shift);
+      const float rv = *reinterpret_cast<const float*>(raw + RW_RS + row * 4);
+      if (!kin || (sv[i] & 0x7FFFu) > 0x7C00u)
+        sv[i] = 0;
+      else if (rv < 0x1p-100f)
+        sv[i] = pack_f16(f16_lo(sv[i]) * (rv * 0x1p100f), f16_hi(sv[i]) * (rv * 0x1p100f));
+      keep_branch();
+    }
+  }
+  // V'
   ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
   if (!__all_sync(0xffffffffu, ok)) return false;
   uint8_t* to = smem + OFF_V + buf * TILE;
-  const int piece = lane & 7, k0 = g * 32 + (lane >> 3);  // elements 16 piece .. of keys k0, k0 + 4, ...
-  uint2 c[8];
-  uint32_t sv[8];
+  const bool upper = lane & 4;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int k = k0 + 4 * i, vrow = raw_row(k, shift) + (1 << shift);
-    c[i] = *reinterpret_cast<const uint2*>(raw + RW_CODES + vrow * 64 + ((((piece >> 1) ^ (vrow >> 1)) & 3) << 4) + (piece & 1) * 8);
-    sv[i] = raw[RW_SF + vrow * 8 + piece];
-    // outside the sequence is whatever the stage held before
-    if (!(((on >> (k >> 4)) & 1u) && k < left) || (sv[i] & 0x7Fu) == 0x7Fu) sv[i] = 0;
-    sv[i] = e4m3x2_f16(sv[i] * 0x101u);
-  }
-  if (tiny) {
-    keep_branch();
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const int k = k0 + 4 * i;
-      const float rv = *reinterpret_cast<const float*>(raw + RW_RS + (raw_row(k, shift) + (1 << shift)) * 4);
-      const float by = k < left && rv < 0x1p-100f ? rv * 0x1p100f : 1.f;
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x == i) sv[x] = pack_f16(f16_lo(sv[x]) * by, f16_hi(sv[x]) * by);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int k = k0 + 4 * i;
     const uint32_t s = sv[i];
     uint32_t f[4], h[4];
-    e2m1x8_f16(c[i].x, f);
-    e2m1x8_f16(c[i].y, h);
-    uint8_t* row = to + (piece >> 2) * HALF_TILE + k * 128;
-    const int p = 2 * (piece & 3);
-    *reinterpret_cast<uint4*>(row + ((p ^ (k & 7)) << 4)) =
-        make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
-    *reinterpret_cast<uint4*>(row + (((p + 1) ^ (k & 7)) << 4)) =
+    e2m1x8_f16(upper ? c[i].y : c[i].x, f);
+    e2m1x8_f16(upper ? c[i].x : c[i].y, h);
+    uint8_t* at = to + x.to[i & 1] + i * 512;
+    *reinterpret_cast<uint4*>(at) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
+    *reinterpret_cast<uint4*>(to + (x.to[i & 1] ^ 16) + i * 512) =
         make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
   }
   fence_async_smem();
@@ -540,43 +557,58 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   const int row0 = w.row0;
   const int nc = tree_columns(w.rows), col0 = wg * nc;
   constexpr int NC = TREE_ROWS / 2;  // the most there may be
-  float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 256;  // [4][64]
-  float* rowtab = reinterpret_cast<float*>(smem + OFF_ROW + (item & 1) * 1024);  // per pair of columns: f, f, -r, -r
+  float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 256;                           // [4][64]
+  float* nref = reinterpret_cast<float*>(smem + OFF_ROW) + (item & 1) * TREE_ROWS + col0;  // -r per column
   bool ok = true;
 
-  // ---- Q: rows scaled by a power of two to a maximum in [1, 2), f16; rows
-  // behind the tile's are zeros.  Sixteen lanes per row.
-  for (int i = tid >> 4; i < nc; i += 8) {
-    const int c = col0 + i, row = row0 + c, piece = tid & 15;
-    float y[8];
-    const bool there = c < w.rows;
-    if (there) {
-      const int node = row / a.group, head = w.kvh * a.group + row - node * a.group;
-      load_bf16x8(a.Q + (static_cast<int64_t>(w.q0) + node) * a.ldq + head * 128 + piece * 8, y);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = 0.f;
-    }
+  // ---- Q in f16: the warpgroup's rows scaled by one power of two, to a maximum
+  // in [2^14, 2^15) (an element below 2^-39 of it is rounded by 2^-39: scores are
+  // exponents, their absolute error counts); rows behind the tile's are zeros.
+  // Sixteen lanes per row.
+  float factor;  // of the scores
+  {
+    uint4 v[NC / 8];
+    const int piece = tid & 15;
     float mx = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(y[k]) <= 3.4e38f ? fabsf(y[k]) : 0.f);
+    for (int i = 0; i < NC / 8; ++i) {
+      const int c = col0 + 8 * i + (tid >> 4), row = row0 + c;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (8 * i < nc && c < w.rows) {
+        const int node = row / a.group, head = w.kvh * a.group + row - node * a.group;
+        v[i] = *reinterpret_cast<const uint4*>(a.Q + (static_cast<int64_t>(w.q0) + node) * a.ldq + head * 128 + piece * 8);
+      }
+    }
 #pragma unroll
-    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
-    e = mx == 0.f ? 0 : max(-126, min(126, e));
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    uint4 v;
-    v.x = pack_f16(y[0] * down, y[1] * down);
-    v.y = pack_f16(y[2] * down, y[3] * down);
-    v.z = pack_f16(y[4] * down, y[5] * down);
-    v.w = pack_f16(y[6] * down, y[7] * down);
-    *reinterpret_cast<uint4*>(smem + OFF_Q + (piece >> 3) * HALF_TILE + c * 128 + (((piece & 7) ^ (c & 7)) << 4)) = v;
-    if (piece == 0) {
-      float* at = rowtab + (c >> 1) * 4 + (c & 1);
-      at[0] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
-      at[2] = 0.f;  // no reference yet
+    for (int i = 0; i < NC / 8; ++i) {
+      float y[8];
+      bf16x8_to_f32(v[i], y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(y[k]) <= 3.4e38f ? fabsf(y[k]) : 0.f);
+    }
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    if (lane == 0) red[warp] = mx;
+    group_any(id, false);
+    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    // 2^-e scales the maximum to [2^14, 2^15), as two factors within fp32's range
+    const int e = mx == 0.f ? 0 : max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -126) - 14;
+    const int e0 = max(-126, min(126, e)), e1 = e - e0;
+    const float down0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
+    const float down1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+    factor = a.scale_log2 / down0 / down1;
+#pragma unroll
+    for (int i = 0; i < NC / 8; ++i) {
+      if (8 * i >= nc) break;
+      const int c = col0 + 8 * i + (tid >> 4);
+      float y[8];
+      bf16x8_to_f32(v[i], y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = y[k] * down0 * down1;
+      *reinterpret_cast<uint4*>(smem + OFF_Q + (piece >> 3) * HALF_TILE + c * 128 + (((piece & 7) ^ (c & 7)) << 4)) =
+          make_uint4(pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7]));
     }
   }
+  if (tid < nc) nref[tid] = 0.f;  // no reference yet
   fence_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(&bar->q_full);
@@ -587,6 +619,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   // units has one key.
   uint32_t* seen = a.seen + (static_cast<int64_t>(blockIdx.x) * 2 + wg) * TREE_MAX_NODES * 2;
   const bool tree = a.parents != nullptr;
+  group_any(id, false);  // red is read
   if (tree && min(w.u1 * TR_UNIT, w.len) > prefix) {
     int16_t* up = reinterpret_cast<int16_t*>(red);
     for (int i = tid; i < w.n; i += 128) {
@@ -599,24 +632,19 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     group_any(id, false);
     if (tid < nc && col0 + tid < w.rows)
       for (int j = (row0 + col0 + tid) / a.group; j >= 0; j = up[j]) atomicOr(seen + 2 * j + (tid >> 5), 1u << (tid & 31));
+    group_any(id, false);
   }
-  group_any(id, false);
 
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   float l[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) l[c] = 0.f;
   bool unset = true;        // some column has no reference
-  bool mine_unset = true;   // column col0 + tid (tid < NC)
-  const float4* tab4 = reinterpret_cast<const float4*>(rowtab) + (col0 >> 1);
-  uint8_t* pbase = smem + OFF_P + tid * 128;
-
+  bool mine_unset = true;   // column tid (tid < nc)
   const int u0 = w.u0, u1 = w.u1, nodes = w.n, group = a.group;
+
   for (int u = u0; u < u1; ++u, ++it) {
     const uint32_t buf = it & 1, ph = (it >> 1) & 1;
-    // (the unpacking is at most three units ahead: no phase of four is missed)
-    ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1, bar, status) && tree_wait(&bar->s_full[buf], ph, bar, status);
-    ok = __all_sync(0xffffffffu, ok);
     // rows that see this key, where it is a node (or none of the sequence)
     const int d = u * TR_UNIT + tid - prefix;
     uint64_t sees = ~0ull;
@@ -633,183 +661,217 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       }
     }
     const bool hidden = __any_sync(0xffffffffu, sees != ~0ull);
-    uint32_t t[NC];  // scores, then exponents (fp32 bits)
-    float inv = 0.f;
-#pragma unroll 1
-    for (bool raised = false;; raised = true) {
-      float mx = -INFINITY;
-      if (ok) {
-        tc_fence_after();
-        const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
-        inv = fabsf(key.y) < 1e30f ? exp2_sfu(-key.y) : 0.f;  // finite: it meets zero weights too
-        const uint64_t rk = f2_pack(key.x, key.x), lr = f2_pack(key.y, key.y);
-        tmem_columns(tmem + lanes + COL_S + buf * 128 + col0, nc, t);
-#pragma unroll
-        for (int q = 0; q < NC; q += 16)
-          if (q < nc) {
-#pragma unroll
-            for (int c = q; c < q + 16; c += 2) {
-              const float4 f = tab4[c >> 1];
-              const uint64_t z = f2_mul(f2_pack(__uint_as_float(t[c]), __uint_as_float(t[c + 1])), rk);
-              float x, y;
-              f2_unpack(f2_fma(z, f2_pack(f.x, f.y), f2_add(lr, f2_pack(f.z, f.w))), x, y);
-              t[c] = __float_as_uint(x);
-              t[c + 1] = __float_as_uint(y);
-            }
-            if (hidden) {
-              keep_branch();
-#pragma unroll
-              for (int c = q; c < q + 16; ++c) t[c] = (sees >> c) & 1 ? t[c] : 0xFF800000u;
-            }
-#pragma unroll
-            for (int c = q; c < q + 16; c += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(t[c]), __uint_as_float(t[c + 1])));
-          }
-      }
-      if (raised || !group_any(id, !ok || unset || mx > TR_RAISE)) break;
-      // A reference rises, or is not there yet: then the scores are taken again.
+    // (the unpacking is at most three units ahead: no phase of four is missed)
+    ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1, bar, status) && tree_wait(&bar->s_full[buf], ph, bar, status);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
+    const float inv = fabsf(key.y) < 1e30f ? exp2_sfu(-key.y) : 0.f;  // finite: it meets zero weights too
+    const float rk = key.x * factor;
+    const uint32_t tS = tmem + lanes + COL_S + buf * 128 + col0, tO = tmem + lanes + COL_O + col0;
+
+    if (unset) {
+      // A reference is missing (an item's first unit): the largest exponents
+      // of this unit's keys, row by row.
       if (group_any(id, !ok)) return false;
+#pragma unroll 1
+      for (int q = 0; q < nc; q += 8) {
+        uint32_t s[8];
+        tmem_ldn(tS + q, s);
+        float v[8];
 #pragma unroll
-      for (int c0 = 0; c0 < NC; c0 += 8)
-        if (c0 < nc) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(t[c0 + i]);
-          const float most = warp_columns<8, false>(v, lane);
-          if (lane < 8) red[warp * 64 + c0 + lane] = most;
-        }
+        for (int c = 0; c < 8; ++c) v[c] = (sees >> (q + c)) & 1 ? fmaf(__uint_as_float(s[c]), rk, key.y + nref[q + c]) : -INFINITY;
+        const float most = warp_columns<8, false>(v, lane);
+        if (lane < 8) red[warp * 64 + q + lane] = most;
+      }
       group_any(id, false);
-      float shrink = 1.f;
+      if (tid < nc && mine_unset) {
+        const float m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
+        if (m > -INFINITY) {
+          mine_unset = false;
+          nref[tid] = -m;
+        }
+      }
+      unset = group_any(id, tid < nc && mine_unset);
+    }
+
+    // ---- P', into the place that the product of two units ago has read: it was
+    // issued before these scores, so it is done
+    uint8_t* at = smem + OFF_P + buf * TILE + tid * 128;
+    uint32_t top = 0;  // the largest weight, as f16 pairs
+    const uint64_t rk2 = f2_pack(rk, rk), lr2 = f2_pack(key.y, key.y), in2 = f2_pack(inv, inv);
+    auto weights = [&](auto add) {
+      top = 0;
+#pragma unroll
+      for (int q = 0; q < NC; q += 32) {
+        if (q >= nc) break;
+        uint32_t s[32];
+        tmem_ld32u(tS + q, s);
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+          if (q + c >= nc) break;
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 8; k += 4) {
+            const float4 n = *reinterpret_cast<const float4*>(nref + q + c + k);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c + k]), __uint_as_float(s[c + k + 1])), rk2, f2_add(lr2, f2_pack(n.x, n.y))),
+                      x[k], x[k + 1]);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c + k + 2]), __uint_as_float(s[c + k + 3])), rk2,
+                             f2_add(lr2, f2_pack(n.z, n.w))),
+                      x[k + 2], x[k + 3]);
+          }
+          if (hidden) {
+            keep_branch();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = (sees >> (q + c + k)) & 1 ? x[k] : -INFINITY;
+          }
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            x[k] = exp2_sfu(x[k]);
+            x[k + 1] = exp2_sfu(x[k + 1]);
+            if (add.value)
+              f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), in2, f2_pack(l[q + c + k], l[q + c + k + 1])), l[q + c + k],
+                        l[q + c + k + 1]);
+            p[k >> 1] = pack_f16(x[k], x[k + 1]);
+          }
+          top = hmax2(hmax2(top, hmax2(p[0], p[1])), hmax2(p[2], p[3]));
+          const int to = (col0 + q + c) >> 3;  // piece of eight rows
+          *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+    };
+    weights(Yes{});
+    // (as numbers: f16 of one sign are ordered as their bits)
+    const bool high = max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16;
+    if (group_any(id, !ok || high)) {
+      // Some weight passed its bound: that row's reference rises, and the weights
+      // are taken again.  l holds them in fp32, which reaches 2^127: where a
+      // reference rises by 2^100 or more, what l held before is nothing.
+      if (group_any(id, !ok)) return false;
+#pragma unroll 1
+      for (int q = 0; q < nc; q += 8) {
+        uint32_t s[8];
+        tmem_ldn(tS + q, s);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = (sees >> (q + c)) & 1 ? fmaf(__uint_as_float(s[c]), rk, key.y + nref[q + c]) : -INFINITY;
+        const float most = warp_columns<8, false>(v, lane);
+        if (lane < 8) red[warp * 64 + q + lane] = most;
+      }
+      group_any(id, false);
+      float rise = 0.f;
       if (tid < nc) {
         const float m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
-        if (m > (mine_unset ? -INFINITY : TR_RAISE)) {  // whatever the other rows do
-          shrink = mine_unset ? 1.f : exp2_sfu(-m);
-          mine_unset = false;
-          const int c = col0 + tid;
-          rowtab[(c >> 1) * 4 + (c & 1) + 2] -= m;
-        }
+        if (m > TR_RAISE) rise = m;  // whatever the other rows do
       }
-      group_any(id, false);  // the maxima are read
-      if (tid < nc) red[tid] = shrink;
-      unset = group_any(id, tid < nc && mine_unset);
-      const bool before = u > u0;  // O holds something
-      if (before) {
+      group_any(id, false);
+      if (tid < nc) {
+        red[tid] = exp2_sfu(-rise);
+        red[64 + tid] = rise;
+        nref[tid] -= rise;
+      }
+      if (u > u0) {  // O holds something
         const uint32_t p = it - 1;
         ok = tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
+      group_any(id, false);
+      // l: rows that rise by less keep this unit's weights; the others begin anew
+      // and get them below, one chunk of rows at a time
 #pragma unroll
-      for (int c0 = 0; c0 < NC; c0 += 8) {
-        if (c0 >= nc) break;
-        float by[8];
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          by[i] = red[c0 + i];
-          l[c0 + i] *= by[i];
-          any |= by[i] != 1.f;
-        }
-        if (before && any && ok) {
-          uint32_t o[8];
-          tmem_ldn(tmem + lanes + COL_O + col0 + c0, o);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by[i]);
-          tmem_st8(tmem + lanes + COL_O + col0 + c0, o);
-          tmem_st_wait();
-        }
-        keep_branch();
+      for (int c = 0; c < NC; ++c) {
+        if (c < nc) l[c] = red[64 + c] >= 100.f ? 0.f : l[c] * red[c];
       }
-      tc_fence_before();
+      if (u > u0 && ok) {
+#pragma unroll 1
+        for (int q = 0; q < nc; q += 8) {
+          uint32_t o[8];
+          tmem_ldn(tO + q, o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * red[q + i]);
+          tmem_st8(tO + q, o);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      weights(No{});
+#pragma unroll
+      for (int q = 0; q < NC; q += 8) {
+        if (q >= nc) break;
+        uint32_t s[8];
+        tmem_ldn(tS + q, s);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (red[64 + q + c] >= 100.f)
+            l[q + c] = (sees >> (q + c)) & 1 ? exp2_sfu(fmaf(__uint_as_float(s[c]), rk, key.y + nref[q + c])) * inv : 0.f;
+      }
       group_any(id, false);  // red is read
     }
     tc_fence_before();
+    fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar->s_empty[buf]);
-    // ---- P', into the place that the product of two units ago has read: it was
-    // issued before these scores, so it is done
-    if (ok) {
-      const uint64_t in2 = f2_pack(inv, inv);
-      uint8_t* at = pbase + buf * TILE;
-#pragma unroll
-      for (int c = 0; c < NC; c += 8) {
-        if (c >= nc) break;
-        uint32_t p[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = exp2_sfu(__uint_as_float(t[c + 2 * k])), y = exp2_sfu(__uint_as_float(t[c + 2 * k + 1]));
-          f2_unpack(f2_fma(f2_pack(x, y), in2, f2_pack(l[c + 2 * k], l[c + 2 * k + 1])), l[c + 2 * k], l[c + 2 * k + 1]);
-          p[k] = pack_f16(x, y);
-        }
-        const int to = (col0 + c) >> 3;  // piece of eight rows
-        *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->p_full[buf]);
+    if (lane == 0) {
+      mbar_arrive(&bar->s_empty[buf]);
+      mbar_arrive(&bar->p_full[buf]);
     }
   }
 
   // ---- the end: l over the keys, O out of TMEM
-  {
-    const uint32_t p = it - 1;
-    ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
-    ok = __all_sync(0xffffffffu, ok);
+  const uint32_t p = it - 1;
+  ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
+  ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
-    for (int c0 = 0; c0 < NC; c0 += 16) {
-      if (c0 >= nc) break;
-      float v[16];
+  for (int c0 = 0; c0 < NC; c0 += 16) {
+    if (c0 >= nc) break;
+    float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = l[c0 + i];
-      const float sum = warp_columns<16, true>(v, lane);
-      if (lane < 16) red[warp * 64 + c0 + lane] = sum;
-    }
-    if (group_any(id, !ok)) return false;
-    const bool alone = w.u0 == 0 && w.u1 == w.units;
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.u0 > 0 ? 0 : 1);
-    float total = 0.f;
-    if (tid < nc) total = (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]);
-    group_any(id, false);
-    if (tid < nc) {
-      red[tid] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);  // NaN stays NaN
-      const int c = col0 + tid;
-      if (c < w.rows) {
-        const float r = -rowtab[(c >> 1) * 4 + (c & 1) + 2];
-        const int row = row0 + c, node = row / a.group, head = w.kvh * a.group + row - node * a.group;
-        if (alone)
-          a.lse[(static_cast<int64_t>(w.q0) + node) * a.n_q + head] = total == 0.f ? -INFINITY : r * 0.69314718056f + logf(total);
-        else
-          a.part_lse[slot * a.part_rows + c] = total == 0.f ? -INFINITY : r + log2f(total);
-      }
-    }
-    group_any(id, false);
-    tc_fence_after();
-    const int d = warp * 32 + lane;  // element
-#pragma unroll 1
-    for (int c0 = 0; c0 < nc && col0 + c0 < w.rows; c0 += 8) {
-      uint32_t o[8];
-      tmem_ldn(tmem + lanes + COL_O + col0 + c0, o);
-      if (alone) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col0 + c0 + i, row = row0 + c;
-          if (c < w.rows) {
-            const int node = row / a.group, head = w.kvh * a.group + row - node * a.group;
-            a.O[((static_cast<int64_t>(w.q0) + node) * a.n_q + head) * 128 + d] = __float2bfloat16(__uint_as_float(o[i]) * red[c0 + i]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col0 + c0 + i;
-          if (c < w.rows) a.part[(slot * a.part_rows + c) * 128 + d] = __uint_as_float(o[i]) * red[c0 + i];
-        }
-      }
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bar->o_empty);
-    group_any(id, false);  // red is read
+    for (int i = 0; i < 16; ++i) v[i] = l[c0 + i];
+    const float sum = warp_columns<16, true>(v, lane);
+    if (lane < 16) red[warp * 64 + c0 + lane] = sum;
   }
+  if (group_any(id, !ok)) return false;
+  const bool alone = u0 == 0 && u1 == w.units;
+  const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u0 > 0 ? 0 : 1);
+  float total = 0.f;
+  if (tid < nc) total = (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]);
+  group_any(id, false);
+  if (tid < nc) {
+    red[tid] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);  // NaN stays NaN
+    const int c = col0 + tid;
+    if (c < w.rows) {
+      const float r = -nref[tid];
+      const int row = row0 + c, node = row / group, head = w.kvh * group + row - node * group;
+      if (alone)
+        a.lse[(static_cast<int64_t>(w.q0) + node) * a.n_q + head] = total == 0.f ? -INFINITY : r * 0.69314718056f + logf(total);
+      else
+        a.part_lse[slot * a.part_rows + c] = total == 0.f ? -INFINITY : r + log2f(total);
+    }
+  }
+  group_any(id, false);
+  tc_fence_after();
+#pragma unroll 1
+  for (int c0 = 0; c0 < nc && col0 + c0 < w.rows; c0 += 8) {
+    uint32_t o[8];
+    tmem_ldn(tmem + lanes + COL_O + col0 + c0, o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = col0 + c0 + i, row = row0 + c;
+      if (c >= w.rows) break;
+      const float x = __uint_as_float(o[i]) * red[c0 + i];
+      if (alone) {
+        const int node = row / group, head = w.kvh * group + row - node * group;
+        a.O[((static_cast<int64_t>(w.q0) + node) * a.n_q + head) * 128 + tid] = __float2bfloat16(x);
+      } else {
+        a.part[(slot * a.part_rows + c) * 128 + tid] = x;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar->o_empty);
+  group_any(id, false);  // red is read
   return true;
 }
 
@@ -916,9 +978,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       bar->copies = c;
     }
     __syncwarp();
-    // Registers: 512 threads x 128 at launch = 256 x 192 + 128 x 72 + 128 x 56
+    // Registers: 512 threads x 128 at launch = 256 x 184 + 128 x 88 + 128 x 56
     if (warp < TR_UNPACK) {
-      reg_inc<192>();
+      reg_inc<184>();
       uint32_t it = 0;
       for (uint32_t item = 0; ok; ++item) {
         ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
@@ -927,10 +989,13 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         ok = tree_softmax(a, smem, bar, tmem, item, it);
       }
     } else if (warp < TR_COPY_WARP) {
-      reg_dec<72>();
+      reg_dec<88>();
       uint32_t rs_zero = __float_as_uint(0x1p-12f);  // row scale that rows of zeros take
       bool more = true;
-      for (uint32_t it = 0; ok && more; ++it) ok = unpack(a.status, smem, bar, tmem, warp - TR_UNPACK, lane, it, min(a.c.page_shift, 7), rs_zero, more) || !more;
+      const int shift = min(a.c.page_shift, 7);
+      const UnpackLane x(warp - TR_UNPACK, lane, shift);
+      for (uint32_t it = 0; ok && more; ++it)
+        ok = unpack(a.status, smem, bar, tmem, warp - TR_UNPACK, lane, it, shift, x, rs_zero, more) || !more;
     } else {
       reg_dec<56>();
       if (warp == TR_COPY_WARP) {
@@ -946,12 +1011,21 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           const TreeItem& w = bar->item[item % TR_ITEMS];
           const int rows = w.rows, n = w.u1 - w.u0;
           if (!ok || rows == 0) break;
-          const int ns = 2 * tree_columns(rows), no = (ns + 63) & ~63;
+          const int ns = 2 * tree_columns(rows);
+          const uint32_t id_s = idesc_f16(128, ns, 0, 0), id_o = idesc_f16(128, (ns + 63) & ~63, 1, 1);
+          auto scores = [&](uint32_t i) {
+            return i & 1 ? issue_scores<1>(a.status, smem, bar, tmem, i, id_s, el)
+                         : issue_scores<0>(a.status, smem, bar, tmem, i, id_s, el);
+          };
+          auto outputs = [&](uint32_t i, bool head) {
+            return i & 1 ? issue_outputs<1>(a.status, smem, bar, tmem, i, id_o, head, item, el)
+                         : issue_outputs<0>(a.status, smem, bar, tmem, i, id_o, head, item, el);
+          };
           ok = tree_wait(&bar->q_full, item & 1, bar, a.status);
-          ok = __all_sync(0xffffffffu, ok) && issue_scores(a.status, smem, bar, tmem, it, ns, el);
+          ok = __all_sync(0xffffffffu, ok) && scores(it);
           for (int j = 0; j < n && ok; ++j, ++it) {
-            if (j + 1 < n) ok = issue_scores(a.status, smem, bar, tmem, it + 1, ns, el);
-            ok = ok && issue_outputs(a.status, smem, bar, tmem, it, no, j == 0, item, el);
+            if (j + 1 < n) ok = scores(it + 1);
+            ok = ok && outputs(it, j == 0);
           }
         }
       }
