@@ -65,8 +65,6 @@ static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
 constexpr uint32_t TR_NO_MORE = 1u << 31;
 constexpr uint64_t TR_WAIT_NS = 2000000000ull;
 
@@ -102,13 +100,12 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
-      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : CODA_R32(r, 0)
+      : CODA_R8(r, 0), CODA_R8(r, 8)
       : "r"(taddr)
       : "memory");
 }
@@ -452,18 +449,24 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
   for (int q = 0; q < 4; ++q)
     kc[q] = *reinterpret_cast<const uint4*>(raw + RW_CODES + x.krow * 64 + ((q ^ ((x.krow >> 1) & 3)) << 4));
   // the key's scales
-  bool odd;  // some key's value needs a second look
+  bool odd, tiny;  // some key's value needs a second look
+  float less;      // what a row scale is below 2^-100
   {
     const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
     const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
     const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
     if (least < 0x7F7FFFFFu) rs_zero = least;
     const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
-    odd = __any_sync(0xffffffffu, !in || sick || rs < 0x1p-100f);
+    odd = __any_sync(0xffffffffu, !in || sick);
+    less = in && rs < 0x1p-100f ? rs * 0x1p100f : 1.f;
+    tiny = __any_sync(0xffffffffu, less != 1.f);
+    // a key that is not finite somewhere: NaN, and finite codes, so that rows that
+    // do not see it stay clear of it
+    const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
     float2 meta;
-    meta.x = in ? rsk : 0.f;
+    meta.x = !in ? 0.f : poison ? 1.f : rsk;
     // below 2^-100 the sum l would pass fp32's end: V' takes the rest
-    meta.y = !in ? -INFINITY : sick ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
+    meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
     *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
   }
   ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
@@ -487,6 +490,18 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
     }
     tmem_st32(tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64 + h * 32, o);
   }
+  if (odd) {
+    // zeros outside the sequence, and for a scale that is NaN (the key's weights
+    // are NaN then): in the stage, where the lane reads them below
+    keep_branch();
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int k = 4 * i + (lane >> 3);
+      uint8_t* sf = smem + OFF_RAW + st * TR_RAW + x.sf[0] + (i & 3) * 32;
+      if (i >= 4) sf += x.sf[1] - x.sf[0];
+      if (!(((on >> (2 * g + (i >> 2))) & 1u) && k < left) || (*sf & 0x7Fu) == 0x7Fu) *sf = 0;
+    }
+  }
   // the values' codes and scales, while the store goes on
   uint2 c[8];
   uint32_t sv[8];
@@ -502,19 +517,12 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
     mbar_arrive(&bar->key_full[it & 3]);
     mbar_arrive(&bar->k_full[buf]);
   }
-  if (odd) {  // zeros outside the sequence and for NaN (the key's weights are NaN), or a small row scale
+  if (tiny) {
     keep_branch();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int k = 4 * i + (lane >> 3);
-      const bool kin = ((on >> (2 * g + (i >> 2))) & 1u) && k < left;
-      const uint32_t row = raw_row(g * 32 + k, shift) + (1 << shift);
-      const float rv = *reinterpret_cast<const float*>(raw + RW_RS + row * 4);
-      if (!kin || (sv[i] & 0x7FFFu) > 0x7C00u)
-        sv[i] = 0;
-      else if (rv < 0x1p-100f)
-        sv[i] = pack_f16(f16_lo(sv[i]) * (rv * 0x1p100f), f16_hi(sv[i]) * (rv * 0x1p100f));
-      keep_branch();
+      const float by = __shfl_sync(0xffffffffu, less, 4 * i + (lane >> 3));
+      sv[i] = pack_f16(f16_lo(sv[i]) * by, f16_hi(sv[i]) * by);
     }
   }
   // V'
@@ -595,7 +603,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     const int e0 = max(-126, min(126, e)), e1 = e - e0;
     const float down0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
     const float down1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
-    factor = a.scale_log2 / down0 / down1;
+    factor = fmaxf(a.scale_log2 / down0 / down1, 1.2e-38f);
 #pragma unroll
     for (int i = 0; i < NC / 8; ++i) {
       if (8 * i >= nc) break;
@@ -640,7 +648,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
 #pragma unroll
   for (int c = 0; c < NC; ++c) l[c] = 0.f;
   bool unset = true;        // some column has no reference
-  bool mine_unset = true;   // column tid (tid < nc)
+  bool mine_unset = tid < nc;  // column tid
   const int u0 = w.u0, u1 = w.u1, nodes = w.n, group = a.group;
 
   for (int u = u0; u < u1; ++u, ++it) {
@@ -660,115 +668,112 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         sees = from <= 0 ? ~0ull : from >= 64 ? 0 : ~0ull << from;
       }
     }
-    const bool hidden = __any_sync(0xffffffffu, sees != ~0ull);
     // (the unpacking is at most three units ahead: no phase of four is missed)
     ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1, bar, status) && tree_wait(&bar->s_full[buf], ph, bar, status);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
-    const float inv = fabsf(key.y) < 1e30f ? exp2_sfu(-key.y) : 0.f;  // finite: it meets zero weights too
-    const float rk = key.x * factor;
+    const bool there = key.y != -INFINITY, poison = key.y != key.y;
+    const float lr = poison ? 0.f : key.y;
+    const float inv = there ? exp2_sfu(-lr) : 0.f;  // finite: it meets zero weights too
+    const float rk = there ? fmaxf(key.x * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
     const uint32_t tS = tmem + lanes + COL_S + buf * 128 + col0, tO = tmem + lanes + COL_O + col0;
-
-    if (unset) {
-      // A reference is missing (an item's first unit): the largest exponents
-      // of this unit's keys, row by row.
-      if (group_any(id, !ok)) return false;
+    if (__any_sync(0xffffffffu, sees != ~0ull || poison)) {  // scores that do not count become -inf where they lie
+      keep_branch();
+#pragma unroll 1
+      for (int q = 0; q < nc; q += 8) {
+        uint32_t s[8];
+        tmem_ldn(tS + q, s);
+        const uint32_t m = static_cast<uint32_t>(sees >> q);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s[c] = !((m >> c) & 1) ? there ? 0xFF800000u : 0u : poison ? 0x7FC00000u : s[c];
+        tmem_st8(tS + q, s);
+      }
+      tmem_st_wait();
+    }
+    // The largest exponent of each row over this unit's keys, to column tid.
+    auto row_max = [&]() {
 #pragma unroll 1
       for (int q = 0; q < nc; q += 8) {
         uint32_t s[8];
         tmem_ldn(tS + q, s);
         float v[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = (sees >> (q + c)) & 1 ? fmaf(__uint_as_float(s[c]), rk, key.y + nref[q + c]) : -INFINITY;
+        for (int c = 0; c < 8; ++c) v[c] = fmaf(__uint_as_float(s[c]), rk, lr + nref[q + c]);
         const float most = warp_columns<8, false>(v, lane);
         if (lane < 8) red[warp * 64 + q + lane] = most;
       }
       group_any(id, false);
-      if (tid < nc && mine_unset) {
-        const float m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
-        if (m > -INFINITY) {
-          mine_unset = false;
-          nref[tid] = -m;
-        }
+      float m = -INFINITY;
+      if (tid < nc) m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
+      group_any(id, false);
+      return m;
+    };
+    if (unset) {  // a reference is missing (an item's first unit)
+      keep_branch();
+      if (group_any(id, !ok)) return false;
+      const float m = row_max();
+      if (mine_unset && m > -INFINITY) {
+        mine_unset = false;
+        nref[tid] = -m;
       }
-      unset = group_any(id, tid < nc && mine_unset);
+      unset = group_any(id, mine_unset);
     }
 
     // ---- P', into the place that the product of two units ago has read: it was
-    // issued before these scores, so it is done
+    // issued before these scores, so it is done.  Where some weight passes its
+    // bound the round is taken back, the reference of that row rises, and a third
+    // one follows.
     uint8_t* at = smem + OFF_P + buf * TILE + tid * 128;
-    uint32_t top = 0;  // the largest weight, as f16 pairs
-    const uint64_t rk2 = f2_pack(rk, rk), lr2 = f2_pack(key.y, key.y), in2 = f2_pack(inv, inv);
-    auto weights = [&](auto add) {
-      top = 0;
-#pragma unroll
-      for (int q = 0; q < NC; q += 32) {
-        if (q >= nc) break;
-        uint32_t s[32];
-        tmem_ld32u(tS + q, s);
-#pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-          if (q + c >= nc) break;
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 8; k += 4) {
-            const float4 n = *reinterpret_cast<const float4*>(nref + q + c + k);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c + k]), __uint_as_float(s[c + k + 1])), rk2, f2_add(lr2, f2_pack(n.x, n.y))),
-                      x[k], x[k + 1]);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[c + k + 2]), __uint_as_float(s[c + k + 3])), rk2,
-                             f2_add(lr2, f2_pack(n.z, n.w))),
-                      x[k + 2], x[k + 3]);
-          }
-          if (hidden) {
-            keep_branch();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = (sees >> (q + c + k)) & 1 ? x[k] : -INFINITY;
-          }
-          uint32_t p[4];
-#pragma unroll
-          for (int k = 0; k < 8; k += 2) {
-            x[k] = exp2_sfu(x[k]);
-            x[k + 1] = exp2_sfu(x[k + 1]);
-            if (add.value)
-              f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), in2, f2_pack(l[q + c + k], l[q + c + k + 1])), l[q + c + k],
-                        l[q + c + k + 1]);
-            p[k >> 1] = pack_f16(x[k], x[k + 1]);
-          }
-          top = hmax2(hmax2(top, hmax2(p[0], p[1])), hmax2(p[2], p[3]));
-          const int to = (col0 + q + c) >> 3;  // piece of eight rows
-          *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-        }
-      }
-    };
-    weights(Yes{});
-    // (as numbers: f16 of one sign are ordered as their bits)
-    const bool high = max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16;
-    if (group_any(id, !ok || high)) {
-      // Some weight passed its bound: that row's reference rises, and the weights
-      // are taken again.  l holds them in fp32, which reaches 2^127: where a
-      // reference rises by 2^100 or more, what l held before is nothing.
-      if (group_any(id, !ok)) return false;
+    const uint64_t rk2 = f2_pack(rk, rk), lr2 = f2_pack(lr, lr);
+    float add = inv;
 #pragma unroll 1
-      for (int q = 0; q < nc; q += 8) {
-        uint32_t s[8];
-        tmem_ldn(tS + q, s);
-        float v[8];
+    for (int round = 0;; ++round) {
+      asm volatile("" : "+r"(round));  // one copy of the code: what misses the instruction cache costs most here
+      const uint64_t in2 = f2_pack(add, add);
+      uint32_t top = 0;  // the largest weight, as f16 pairs
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = (sees >> (q + c)) & 1 ? fmaf(__uint_as_float(s[c]), rk, key.y + nref[q + c]) : -INFINITY;
-        const float most = warp_columns<8, false>(v, lane);
-        if (lane < 8) red[warp * 64 + q + lane] = most;
+      for (int q = 0; q < NC; q += 16) {
+        if (q >= nc) break;
+        uint32_t s[16];
+        tmem_ldn(tS + q, s);
+        uint32_t p[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+          const float4 n = *reinterpret_cast<const float4*>(nref + q + k);
+          float x[4];
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), rk2, f2_add(lr2, f2_pack(n.x, n.y))), x[0],
+                    x[1]);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), rk2, f2_add(lr2, f2_pack(n.z, n.w))),
+                    x[2], x[3]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) x[h] = exp2_sfu(x[h]);
+          f2_unpack(f2_fma(f2_pack(x[0], x[1]), in2, f2_pack(l[q + k], l[q + k + 1])), l[q + k], l[q + k + 1]);
+          f2_unpack(f2_fma(f2_pack(x[2], x[3]), in2, f2_pack(l[q + k + 2], l[q + k + 3])), l[q + k + 2], l[q + k + 3]);
+          p[k / 2] = pack_f16(x[0], x[1]);
+          p[k / 2 + 1] = pack_f16(x[2], x[3]);
+        }
+        top = hmax2(top, hmax2(hmax2(hmax2(p[0], p[1]), hmax2(p[2], p[3])), hmax2(hmax2(p[4], p[5]), hmax2(p[6], p[7]))));
+        const int to = (col0 + q) >> 3;  // piece of eight rows, even
+        uint8_t* row = at + (to >> 3) * HALF_TILE;
+        *reinterpret_cast<uint4*>(row + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<uint4*>(row + ((((to + 1) ^ tid) & 7) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
       }
-      group_any(id, false);
-      float rise = 0.f;
-      if (tid < nc) {
-        const float m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
-        if (m > TR_RAISE) rise = m;  // whatever the other rows do
+      if (round == 2) break;
+      // (as numbers: f16 of one sign are ordered as their bits)
+      if (round == 0 && !group_any(id, !ok || max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16)) break;
+      keep_branch();
+      if (round == 0) {
+        if (group_any(id, !ok)) return false;
+        add = -inv;
+        continue;
       }
-      group_any(id, false);
+      // l is what it was, to a rounding of what this unit adds; where that passed
+      // fp32 the old l is nothing beside it.
+      const float m = row_max();
+      const float rise = m > TR_RAISE ? m : 0.f;  // whatever the other rows do
       if (tid < nc) {
         red[tid] = exp2_sfu(-rise);
-        red[64 + tid] = rise;
         nref[tid] -= rise;
       }
       if (u > u0) {  // O holds something
@@ -778,12 +783,9 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         tc_fence_after();
       }
       group_any(id, false);
-      // l: rows that rise by less keep this unit's weights; the others begin anew
-      // and get them below, one chunk of rows at a time
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        if (c < nc) l[c] = red[64 + c] >= 100.f ? 0.f : l[c] * red[c];
-      }
+      for (int c = 0; c < NC; ++c)
+        if (c < nc) l[c] = red[c] < 0x1p-100f ? 0.f : l[c] * red[c];
       if (u > u0 && ok) {
 #pragma unroll 1
         for (int q = 0; q < nc; q += 8) {
@@ -794,20 +796,9 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
           tmem_st8(tO + q, o);
         }
         tmem_st_wait();
-        tc_fence_before();
-      }
-      weights(No{});
-#pragma unroll
-      for (int q = 0; q < NC; q += 8) {
-        if (q >= nc) break;
-        uint32_t s[8];
-        tmem_ldn(tS + q, s);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (red[64 + q + c] >= 100.f)
-            l[q + c] = (sees >> (q + c)) & 1 ? exp2_sfu(fmaf(__uint_as_float(s[c]), rk, key.y + nref[q + c])) * inv : 0.f;
       }
       group_any(id, false);  // red is read
+      add = inv;
     }
     tc_fence_before();
     fence_async_smem();
@@ -822,31 +813,38 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   const uint32_t p = it - 1;
   ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
   ok = __all_sync(0xffffffffu, ok);
-#pragma unroll
-  for (int c0 = 0; c0 < NC; c0 += 16) {
-    if (c0 >= nc) break;
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = l[c0 + i];
-    const float sum = warp_columns<16, true>(v, lane);
-    if (lane < 16) red[warp * 64 + c0 + lane] = sum;
-  }
   if (group_any(id, !ok)) return false;
+  // The sums meet in shared memory (a place of P': no product reads it until every
+  // warp has its next rows): thread t's, 16 bytes at piece c / 4 ^ (t & 15).
+  float* box = reinterpret_cast<float*>(smem + OFF_P + wg * TILE);
+#pragma unroll
+  for (int c = 0; c < NC; c += 4)
+    if (c < nc)
+      *reinterpret_cast<float4*>(box + tid * 64 + (((c >> 2) ^ (tid & 15)) << 2)) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
+  group_any(id, false);
+  {
+    const int c = tid & 63;
+    float sum = 0.f;
+    if (c < nc)
+#pragma unroll 8
+      for (int t = tid & 64; t < (tid & 64) + 64; ++t) sum += box[t * 64 + (((c >> 2) ^ (t & 15)) << 2) + (c & 3)];
+    red[tid] = sum;
+  }
+  group_any(id, false);
   const bool alone = u0 == 0 && u1 == w.units;
   const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u0 > 0 ? 0 : 1);
-  float total = 0.f;
-  if (tid < nc) total = (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]);
-  group_any(id, false);
+  int64_t* to = reinterpret_cast<int64_t*>(red + 128);  // where each row goes
   if (tid < nc) {
+    const float total = red[tid] + red[64 + tid];
+    const int c = col0 + tid, row = row0 + c, node = row / group, head = w.kvh * group + row - node * group;
     red[tid] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);  // NaN stays NaN
-    const int c = col0 + tid;
+    to[tid] = alone ? (static_cast<int64_t>(w.q0) + node) * a.n_q + head : slot * a.part_rows + c;
     if (c < w.rows) {
       const float r = -nref[tid];
-      const int row = row0 + c, node = row / group, head = w.kvh * group + row - node * group;
       if (alone)
-        a.lse[(static_cast<int64_t>(w.q0) + node) * a.n_q + head] = total == 0.f ? -INFINITY : r * 0.69314718056f + logf(total);
+        a.lse[to[tid]] = total == 0.f ? -INFINITY : r * 0.69314718056f + logf(total);
       else
-        a.part_lse[slot * a.part_rows + c] = total == 0.f ? -INFINITY : r + log2f(total);
+        a.part_lse[to[tid]] = total == 0.f ? -INFINITY : r + log2f(total);
     }
   }
   group_any(id, false);
@@ -857,15 +855,12 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     tmem_ldn(tmem + lanes + COL_O + col0 + c0, o);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = col0 + c0 + i, row = row0 + c;
-      if (c >= w.rows) break;
+      if (col0 + c0 + i >= w.rows) break;
       const float x = __uint_as_float(o[i]) * red[c0 + i];
-      if (alone) {
-        const int node = row / group, head = w.kvh * group + row - node * group;
-        a.O[((static_cast<int64_t>(w.q0) + node) * a.n_q + head) * 128 + tid] = __float2bfloat16(x);
-      } else {
-        a.part[(slot * a.part_rows + c) * 128 + tid] = x;
-      }
+      if (alone)
+        a.O[to[c0 + i] * 128 + tid] = __float2bfloat16(x);
+      else
+        a.part[to[c0 + i] * 128 + tid] = x;
     }
   }
   tc_fence_before();
@@ -916,6 +911,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   const int chunk = (a.B + TR_THREADS - 1) / TR_THREADS;
   const int b0 = min(a.B, tid * chunk), b1 = min(a.B, b0 + chunk);
   int64_t mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += tree_seq(a, b, blockIdx.x == 0).place_kv * a.c.n_kv;
   int64_t incl = mine;
 #pragma unroll
@@ -939,6 +935,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   const int64_t first = blockIdx.x * per, last = min(total, first + per);
   {
     int64_t before = incl - mine;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int64_t n = tree_seq(a, b, false).place_kv * a.c.n_kv;
       if (blockIdx.x == 0) a.places[b] = before;
