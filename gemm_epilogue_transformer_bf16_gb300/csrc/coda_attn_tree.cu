@@ -114,6 +114,13 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      CODA_W8(r, 0), CODA_W8(r, 8)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), CODA_W8(r, 0)
                : "memory");
@@ -246,8 +253,9 @@ struct TreeBars {
 };
 static_assert(sizeof(TreeBars) <= 1152, "barrier area");
 
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeBars* s, int* status, uint32_t sleep_ns = 0) {
-  return mbar_wait_bounded(bar, parity, &s->abort, status, TR_WAIT_NS, sleep_ns);
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeBars* s, int* status) {
+  if (__builtin_expect(mbar_try_wait(smem_u32(bar), parity), 1)) return true;
+  return mbar_wait_bounded(bar, parity, &s->abort, status, TR_WAIT_NS);
 }
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int v, int w,
@@ -444,10 +452,6 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
   const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + (x.krow + (1 << shift)) * 8);
   const float rsk = *reinterpret_cast<const float*>(raw + RW_RS + x.krow * 4);
   const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (x.krow + (1 << shift)) * 4);
-  uint4 kc[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    kc[q] = *reinterpret_cast<const uint4*>(raw + RW_CODES + x.krow * 64 + ((q ^ ((x.krow >> 1) & 3)) << 4));
   // the key's scales
   bool odd, tiny;  // some key's value needs a second look
   float less;      // what a row scale is below 2^-100
@@ -472,23 +476,29 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
   ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t o[32];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint4 v = kc[h * 2 + q];
-      const uint32_t two = in ? e4m3x2_f16(((h ? sfk.y : sfk.x) >> (16 * q)) & 0xFFFFu) : 0;
+  // (Rolled: four warps of different roles share a scheduler, and their
+  // straight-line code does not fit its instruction cache together.)
+  {
+    const uint8_t* kc = raw + RW_CODES + x.krow * 64;
+    uint64_t sf8 = in ? static_cast<uint64_t>(sfk.y) << 32 | sfk.x : 0;
+    const uint32_t to = tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64;
+    uint4 v = *reinterpret_cast<const uint4*>(kc + (((x.krow >> 1) & 3) << 4));
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q, sf8 >>= 16) {
+      const uint4 now = v;
+      v = *reinterpret_cast<const uint4*>(kc + (((q + 1) ^ (x.krow >> 1)) & 3) * 16);
+      const uint32_t two = e4m3x2_f16(static_cast<uint32_t>(sf8) & 0xFFFFu);
       const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+      uint32_t o[16];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t f[4];
-        e2m1x8_f16(w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w, f);
+        e2m1x8_f16(w == 0 ? now.x : w == 1 ? now.y : w == 2 ? now.z : now.w, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[q * 16 + w * 4 + i] = hmul2(f[i], w < 2 ? s0 : s1);
+        for (int i = 0; i < 4; ++i) o[w * 4 + i] = hmul2(f[i], w < 2 ? s0 : s1);
       }
+      tmem_st16(to + q * 16, o);
     }
-    tmem_st32(tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64 + h * 32, o);
   }
   if (odd) {
     // zeros outside the sequence, and for a scale that is NaN (the key's weights
@@ -502,14 +512,6 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
       if (!(((on >> (2 * g + (i >> 2))) & 1u) && k < left) || (*sf & 0x7Fu) == 0x7Fu) *sf = 0;
     }
   }
-  // the values' codes and scales, while the store goes on
-  uint2 c[8];
-  uint32_t sv[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = *reinterpret_cast<const uint2*>(raw + x.v[i >> 2][i & 1] + (i & 3) * 256);
-    sv[i] = e4m3x2_f16(raw[x.sf[i >> 2] + (i & 3) * 32] * 0x101u);
-  }
   tmem_st_wait();
   tc_fence_before();
   __syncwarp();
@@ -517,29 +519,36 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
     mbar_arrive(&bar->key_full[it & 3]);
     mbar_arrive(&bar->k_full[buf]);
   }
-  if (tiny) {
-    keep_branch();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float by = __shfl_sync(0xffffffffu, less, 4 * i + (lane >> 3));
-      sv[i] = pack_f16(f16_lo(sv[i]) * by, f16_hi(sv[i]) * by);
-    }
-  }
   // V'
   ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
   if (!__all_sync(0xffffffffu, ok)) return false;
   uint8_t* to = smem + OFF_V + buf * TILE;
   const bool upper = lane & 4;
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint2 c[4];
+    uint32_t sv[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t s = sv[i];
-    uint32_t f[4], h[4];
-    e2m1x8_f16(upper ? c[i].y : c[i].x, f);
-    e2m1x8_f16(upper ? c[i].x : c[i].y, h);
-    uint8_t* at = to + x.to[i & 1] + i * 512;
-    *reinterpret_cast<uint4*>(at) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
-    *reinterpret_cast<uint4*>(to + (x.to[i & 1] ^ 16) + i * 512) =
-        make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+    for (int i = 0; i < 4; ++i) {
+      c[i] = *reinterpret_cast<const uint2*>(raw + (h ? x.v[1][i & 1] : x.v[0][i & 1]) + i * 256);
+      sv[i] = raw[(h ? x.sf[1] : x.sf[0]) + i * 32];
+    }
+    if (tiny) keep_branch();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t s = e4m3x2_f16(sv[i] * 0x101u);
+      if (tiny) {
+        const float by = __shfl_sync(0xffffffffu, less, 16 * h + 4 * i + (lane >> 3));
+        s = pack_f16(f16_lo(s) * by, f16_hi(s) * by);
+      }
+      uint32_t f[4], e[4];
+      e2m1x8_f16(upper ? c[i].y : c[i].x, f);
+      e2m1x8_f16(upper ? c[i].x : c[i].y, e);
+      uint8_t* at = to + h * 2048 + i * 512;
+      *reinterpret_cast<uint4*>(at + x.to[i & 1]) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
+      *reinterpret_cast<uint4*>(at + (x.to[i & 1] ^ 16)) =
+          make_uint4(hmul2(e[0], s), hmul2(e[1], s), hmul2(e[2], s), hmul2(e[3], s));
+    }
   }
   fence_async_smem();
   __syncwarp();
