@@ -42,8 +42,9 @@
 namespace coda {
 namespace {
 
-constexpr int TR_THREADS = 512;
-constexpr int TR_UNPACK = 8, TR_COPY_WARP = 12, TR_MMA_WARP = 13;  // warps: 0-7 weights, 8-11 unpacking
+constexpr int TR_THREADS = 896;
+constexpr int TR_GROUPS = 4;  // warpgroups of weights: warps 0-15
+constexpr int TR_KEYS = 16, TR_VALUES = 20, TR_COPY_WARP = 24, TR_MMA_WARP = 25;  // first warps of the other roles
 constexpr int TR_UNIT = 128;
 constexpr int TR_STAGES = 3;
 // A stage holds a unit's rows of the cache part by part (a page, or 128 keys of
@@ -58,8 +59,8 @@ constexpr uint32_t TILE = 32768, HALF_TILE = 16384;  // 128 x 128 f16, as two ha
 constexpr uint32_t OFF_Q = 0, OFF_P = TILE, OFF_V = 3 * TILE, OFF_RAW = 5 * TILE;
 constexpr uint32_t OFF_ROW = OFF_RAW + TR_STAGES * TR_RAW;  // [2][128] minus the rows' references, by item
 constexpr uint32_t OFF_KEY = OFF_ROW + 1024;                // [4][128] row scale of the key, log2 of the value's
-constexpr uint32_t OFF_RED = OFF_KEY + 4096;                // [2][4][64] exchange of a warpgroup
-constexpr uint32_t OFF_BAR = OFF_RED + 2048;
+constexpr uint32_t OFF_RED = OFF_KEY + 4096;                // [4][192] exchange of a warpgroup
+constexpr uint32_t OFF_BAR = OFF_RED + 3072;
 constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
@@ -408,146 +409,148 @@ __device__ __forceinline__ void tree_drain(TreeBars* bar, int warp, int lane) {
   }
 }
 
-// Places of a lane in a stage: its key's row, and the values of keys k0 + 4 i
-// (k0 = lane / 8 of the warp's 32), of which it takes elements 16 (lane % 8) ...
-struct UnpackLane {
-  uint32_t krow;      // row of the key
-  uint32_t v[2][2];   // codes of the values, for i < 4 and i >= 4, even and odd i
-  uint32_t sf[2];     // their block scales
-  uint32_t to[2];     // where V' goes, even and odd i: the first half of the lanes
-  __device__ __forceinline__ UnpackLane(int g, int lane, int shift) {
-    krow = raw_row(g * 32 + lane, shift);
-    const int piece = lane & 7, k0 = lane >> 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = raw_row(g * 32 + 16 * h + k0, shift) + (1 << shift);
-      sf[h] = RW_SF + row * 8 + piece;
-#pragma unroll
-      for (int o = 0; o < 2; ++o)
-        v[h][o] = RW_CODES + row * 64 + ((((piece >> 1) ^ (row >> 1) ^ (2 * o)) & 3) << 4) + (piece & 1) * 8;
-    }
-    // pieces 2 p and 2 p + 1 of the row, exchanged for the upper elements so that
-    // eight lanes write to different banks
-#pragma unroll
-    for (int o = 0; o < 2; ++o)
-      to[o] = (piece >> 2) * HALF_TILE + (g * 32 + k0) * 128 + (((2 * (piece & 3) + (piece >> 2)) ^ (k0 + 4 * o)) << 4);
-  }
+// Unit `it` of the stage ring, or none: its groups of 16 keys, and the keys of the
+// sequence from the warp's first (32 g) on.
+struct UnitIn {
+  uint32_t on;
+  int left;
 };
-
-// Unit `it` unpacked by four warps, a warp's 32 keys each.  K': a thread per
-// key, to the lane of TMEM that is its row.  False: a wait ran out, or no unit
-// (`more`) is left.
-__device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane, uint32_t it,
-                                       int shift, const UnpackLane& x, uint32_t& rs_zero, bool& more) {
-  const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
-  bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1, bar, status);
+__device__ __forceinline__ bool unit_in(int* status, TreeBars* bar, uint32_t it, int g, UnitIn& x, bool& more) {
+  const uint32_t st = it % TR_STAGES;
+  const bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1, bar, status);
   if (!__all_sync(0xffffffffu, ok)) return false;
-  const uint32_t on = bar->keys_in[st];
-  const int left = bar->left[st] - 32 * g;  // keys of the sequence from the warp's first on
-  more = on != TR_NO_MORE;
-  if (!more) return false;
+  x.on = bar->keys_in[st];
+  x.left = bar->left[st] - 32 * g;
+  more = x.on != TR_NO_MORE;
+  return more;
+}
+
+// K' of unit `it` by four warps, a thread per key, to the lane of TMEM that is
+// its row, and the key's scales.  False: a wait ran out, or no unit (`more`) is
+// left.  (Rolled, as below: warps of all roles share a scheduler, and their
+// straight-line code does not fit its instruction cache together.)
+__device__ __forceinline__ bool unpack_keys(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane,
+                                            uint32_t it, int shift, int krow, uint32_t& rs_zero, bool& more) {
+  const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
+  UnitIn x;
+  if (!unit_in(status, bar, it, g, x, more)) return false;
   const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
-  const bool in = ((on >> (2 * g + (lane >> 4))) & 1u) && lane < left;  // else whatever the stage held before
-  const uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + x.krow * 8);
-  const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + (x.krow + (1 << shift)) * 8);
-  const float rsk = *reinterpret_cast<const float*>(raw + RW_RS + x.krow * 4);
-  const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (x.krow + (1 << shift)) * 4);
-  // the key's scales
-  bool odd, tiny;  // some key's value needs a second look
-  float less;      // what a row scale is below 2^-100
-  {
-    const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
-    const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
-    const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
-    if (least < 0x7F7FFFFFu) rs_zero = least;
-    const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
-    odd = __any_sync(0xffffffffu, !in || sick);
-    less = in && rs < 0x1p-100f ? rs * 0x1p100f : 1.f;
-    tiny = __any_sync(0xffffffffu, less != 1.f);
-    // a key that is not finite somewhere: NaN, and finite codes, so that rows that
-    // do not see it stay clear of it
-    const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
-    float2 meta;
-    meta.x = !in ? 0.f : poison ? 1.f : rsk;
-    // below 2^-100 the sum l would pass fp32's end: V' takes the rest
-    meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
-    *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
-  }
-  ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
+  const bool in = ((x.on >> (2 * g + (lane >> 4))) & 1u) && lane < x.left;  // else whatever the stage held before
+  const uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + krow * 8);
+  const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + (krow + (1 << shift)) * 8);
+  const float rsk = *reinterpret_cast<const float*>(raw + RW_RS + krow * 4);
+  const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (krow + (1 << shift)) * 4);
+  const uint8_t* kc = raw + RW_CODES + krow * 64;
+  uint4 v = *reinterpret_cast<const uint4*>(kc + (((krow >> 1) & 3) << 4));
+  bool ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
-  // (Rolled: four warps of different roles share a scheduler, and their
-  // straight-line code does not fit its instruction cache together.)
-  {
-    const uint8_t* kc = raw + RW_CODES + x.krow * 64;
-    uint64_t sf8 = in ? static_cast<uint64_t>(sfk.y) << 32 | sfk.x : 0;
-    const uint32_t to = tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64;
-    uint4 v = *reinterpret_cast<const uint4*>(kc + (((x.krow >> 1) & 3) << 4));
+  uint64_t sf8 = in ? static_cast<uint64_t>(sfk.y) << 32 | sfk.x : 0;
+  const uint32_t to = tmem + (static_cast<uint32_t>(g * 32) << 16) + COL_K + buf * 64;
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q, sf8 >>= 16) {
-      const uint4 now = v;
-      v = *reinterpret_cast<const uint4*>(kc + (((q + 1) ^ (x.krow >> 1)) & 3) * 16);
-      const uint32_t two = e4m3x2_f16(static_cast<uint32_t>(sf8) & 0xFFFFu);
-      const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
-      uint32_t o[16];
+  for (int q = 0; q < 4; ++q, sf8 >>= 16) {
+    const uint4 now = v;
+    v = *reinterpret_cast<const uint4*>(kc + (((q + 1) ^ (krow >> 1)) & 3) * 16);
+    const uint32_t two = e4m3x2_f16(static_cast<uint32_t>(sf8) & 0xFFFFu);
+    const uint32_t s0 = __byte_perm(two, two, 0x1010), s1 = __byte_perm(two, two, 0x3232);
+    uint32_t o[16];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t f[4];
-        e2m1x8_f16(w == 0 ? now.x : w == 1 ? now.y : w == 2 ? now.z : now.w, f);
+    for (int w = 0; w < 4; ++w) {
+      uint32_t f[4];
+      e2m1x8_f16(w == 0 ? now.x : w == 1 ? now.y : w == 2 ? now.z : now.w, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[w * 4 + i] = hmul2(f[i], w < 2 ? s0 : s1);
-      }
-      tmem_st16(to + q * 16, o);
+      for (int i = 0; i < 4; ++i) o[w * 4 + i] = hmul2(f[i], w < 2 ? s0 : s1);
     }
+    tmem_st16(to + q * 16, o);
   }
-  if (odd) {
-    // zeros outside the sequence, and for a scale that is NaN (the key's weights
-    // are NaN then): in the stage, where the lane reads them below
-    keep_branch();
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const int k = 4 * i + (lane >> 3);
-      uint8_t* sf = smem + OFF_RAW + st * TR_RAW + x.sf[0] + (i & 3) * 32;
-      if (i >= 4) sf += x.sf[1] - x.sf[0];
-      if (!(((on >> (2 * g + (i >> 2))) & 1u) && k < left) || (*sf & 0x7Fu) == 0x7Fu) *sf = 0;
-    }
-  }
+  const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+  const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
+  const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
+  if (least < 0x7F7FFFFFu) rs_zero = least;
+  const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
+  // a key that is not finite somewhere: NaN, and finite codes, so that rows that
+  // do not see it stay clear of it
+  const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
+  float2 meta;
+  meta.x = !in ? 0.f : poison ? 1.f : rsk;
+  // below 2^-100 the sum l would pass fp32's end: V' takes the rest
+  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
+  *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
   tmem_st_wait();
   tc_fence_before();
   __syncwarp();
   if (lane == 0) {
     mbar_arrive(&bar->key_full[it & 3]);
     mbar_arrive(&bar->k_full[buf]);
+    mbar_arrive(&bar->raw_empty[st]);
   }
-  // V'
-  ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
+  return true;
+}
+
+// V' of unit `it` by four warps: a lane takes sixteen elements of keys k0 + 4 i
+// (k0 = lane / 8 of the warp's 32).
+struct ValueLane {
+  uint32_t v[2];    // codes of the values: first 16 keys, the others
+  uint32_t sf[2];   // their block scales
+  uint32_t to;      // where V' goes
+  // Even and odd i differ in one bit of the swizzled places.  Pieces 2 p and
+  // 2 p + 1 of a row are exchanged for the upper elements, so that eight lanes
+  // write to different banks.
+  __device__ __forceinline__ ValueLane(int g, int lane, int shift) {
+    const int piece = lane & 7, k0 = lane >> 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = raw_row(g * 32 + 16 * h + k0, shift) + (1 << shift);
+      sf[h] = RW_SF + row * 8 + piece;
+      v[h] = RW_CODES + row * 64 + ((((piece >> 1) ^ (row >> 1)) & 3) << 4) + (piece & 1) * 8;
+    }
+    to = (piece >> 2) * HALF_TILE + (g * 32 + k0) * 128 + (((2 * (piece & 3) + (piece >> 2)) ^ k0) << 4);
+  }
+};
+__device__ __forceinline__ bool unpack_values(int* status, uint8_t* smem, TreeBars* bar, int g, int lane, uint32_t it, int shift,
+                                              const ValueLane& x, bool& more) {
+  const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
+  UnitIn u;
+  if (!unit_in(status, bar, it, g, u, more)) return false;
+  uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
+  // a row scale below 2^-100 (unpack_keys): what it is of that
+  const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (raw_row(g * 32 + lane, shift) + (1 << shift)) * 4);
+  const bool in = ((u.on >> (2 * g + (lane >> 4))) & 1u) && lane < u.left;
+  const float less = in && rsv < 0x1p-100f ? rsv * 0x1p100f : 1.f;
+  const bool tiny = __any_sync(0xffffffffu, less != 1.f), whole = __all_sync(0xffffffffu, in);
+  const bool ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
   if (!__all_sync(0xffffffffu, ok)) return false;
-  uint8_t* to = smem + OFF_V + buf * TILE;
   const bool upper = lane & 4;
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    uint2 c[4];
-    uint32_t sv[4];
+  for (int h = 0; h < 4; ++h) {
+    uint2 c[2];
+    uint32_t sv[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = *reinterpret_cast<const uint2*>(raw + (h ? x.v[1][i & 1] : x.v[0][i & 1]) + i * 256);
-      sv[i] = raw[(h ? x.sf[1] : x.sf[0]) + i * 32];
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t at = (h & 1) * 512 + i * 256;
+      c[i] = *reinterpret_cast<const uint2*>(raw + ((h < 2 ? x.v[0] : x.v[1]) ^ (i * 32)) + at);
+      sv[i] = raw[(h < 2 ? x.sf[0] : x.sf[1]) + (at >> 3)];
     }
-    if (tiny) keep_branch();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t s = e4m3x2_f16(sv[i] * 0x101u);
+    for (int i = 0; i < 2; ++i) {
+      // zeros outside the sequence, and for a scale that is NaN (the key's weights
+      // are NaN then)
+      const int k = 8 * h + 4 * i + (lane >> 3);
+      const bool kin = whole || (((u.on >> (2 * g + (h >> 1))) & 1u) && k < u.left);
+      uint32_t s = e4m3x2_f16(kin && (sv[i] & 0x7Fu) != 0x7Fu ? sv[i] * 0x101u : 0u);
       if (tiny) {
-        const float by = __shfl_sync(0xffffffffu, less, 16 * h + 4 * i + (lane >> 3));
+        keep_branch();
+        const float by = __shfl_sync(0xffffffffu, less, k);
         s = pack_f16(f16_lo(s) * by, f16_hi(s) * by);
       }
       uint32_t f[4], e[4];
       e2m1x8_f16(upper ? c[i].y : c[i].x, f);
       e2m1x8_f16(upper ? c[i].x : c[i].y, e);
-      uint8_t* at = to + h * 2048 + i * 512;
-      *reinterpret_cast<uint4*>(at + x.to[i & 1]) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
-      *reinterpret_cast<uint4*>(at + (x.to[i & 1] ^ 16)) =
-          make_uint4(hmul2(e[0], s), hmul2(e[1], s), hmul2(e[2], s), hmul2(e[3], s));
+      const int turn = i * 64;  // of the swizzle
+      uint8_t* a0 = smem + OFF_V + buf * TILE + (x.to ^ turn) + h * 1024 + i * 512;
+      uint8_t* a1 = smem + OFF_V + buf * TILE + (x.to ^ turn ^ 16) + h * 1024 + i * 512;
+      *reinterpret_cast<uint4*>(a0) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
+      *reinterpret_cast<uint4*>(a1) = make_uint4(hmul2(e[0], s), hmul2(e[1], s), hmul2(e[2], s), hmul2(e[3], s));
     }
   }
   fence_async_smem();
@@ -559,11 +562,11 @@ __device__ __forceinline__ bool unpack(int* status, uint8_t* smem, TreeBars* bar
   return true;
 }
 
-// Columns of a tile that each of the two warpgroups takes: whole chunks of 16.
-__device__ __forceinline__ int tree_columns(int rows) { return (rows + 31) / 32 * 16; }
+// Columns of a tile that each of the four warpgroups takes: whole chunks of 8.
+__device__ __forceinline__ int tree_columns(int rows) { return (rows + 31) / 32 * 8; }
 
 // A warpgroup's part of one stretch: the weights of nc columns of the tile, in
-// chunks of 16.  `it` counts the CTA's units.  False: a wait ran out.
+// chunks of 8.  `it` counts the CTA's units.  False: a wait ran out.
 __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t item,
                                              uint32_t& it) {
   int* const status = a.status;
@@ -573,8 +576,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   const TreeItem& w = bar->item[item % TR_ITEMS];
   const int row0 = w.row0;
   const int nc = tree_columns(w.rows), col0 = wg * nc;
-  constexpr int NC = TREE_ROWS / 2;  // the most there may be
-  float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 256;                           // [4][64]
+  constexpr int NC = TREE_ROWS / TR_GROUPS;  // the most there may be
+  float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 192;                           // [4][32] and more
   float* nref = reinterpret_cast<float*>(smem + OFF_ROW) + (item & 1) * TREE_ROWS + col0;  // -r per column
   bool ok = true;
 
@@ -634,7 +637,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   const int prefix = w.len - w.n;  // keys that every row sees
   // For each node the rows that see it, a bit each: a thread of the last
   // units has one key.
-  uint32_t* seen = a.seen + (static_cast<int64_t>(blockIdx.x) * 2 + wg) * TREE_MAX_NODES * 2;
+  uint32_t* seen = a.seen + (static_cast<int64_t>(blockIdx.x) * TR_GROUPS + wg) * TREE_MAX_NODES;
   const bool tree = a.parents != nullptr;
   group_any(id, false);  // red is read
   if (tree && min(w.u1 * TR_UNIT, w.len) > prefix) {
@@ -644,11 +647,11 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       const bool bad = p < -1 || p >= i;
       if (bad) atomicOr(a.status, CODA_DEV_TREE_RANGE);
       up[i] = static_cast<int16_t>(bad ? -1 : p);
-      reinterpret_cast<uint2*>(seen)[i] = make_uint2(0, 0);
+      seen[i] = 0;
     }
     group_any(id, false);
     if (tid < nc && col0 + tid < w.rows)
-      for (int j = (row0 + col0 + tid) / a.group; j >= 0; j = up[j]) atomicOr(seen + 2 * j + (tid >> 5), 1u << (tid & 31));
+      for (int j = (row0 + col0 + tid) / a.group; j >= 0; j = up[j]) atomicOr(seen + j, 1u << tid);
     group_any(id, false);
   }
 
@@ -664,17 +667,16 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     const uint32_t buf = it & 1, ph = (it >> 1) & 1;
     // rows that see this key, where it is a node (or none of the sequence)
     const int d = u * TR_UNIT + tid - prefix;
-    uint64_t sees = ~0ull;
+    uint32_t sees = ~0u;
     if ((u + 1) * TR_UNIT > prefix && d >= 0) {
       keep_branch();
       if (d >= nodes) {
         sees = 0;
       } else if (tree) {
-        const uint2 m = __ldcg(reinterpret_cast<const uint2*>(seen) + d);
-        sees = static_cast<uint64_t>(m.y) << 32 | m.x;
+        sees = __ldcg(seen + d);
       } else {
         const int64_t from = static_cast<int64_t>(d) * group - row0 - col0;  // rows from the node's own on
-        sees = from <= 0 ? ~0ull : from >= 64 ? 0 : ~0ull << from;
+        sees = from <= 0 ? ~0u : from >= 32 ? 0 : ~0u << from;
       }
     }
     // (the unpacking is at most three units ahead: no phase of four is missed)
@@ -687,13 +689,13 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     const float inv = there ? exp2_sfu(-lr) : 0.f;  // finite: it meets zero weights too
     const float rk = there ? fmaxf(key.x * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
     const uint32_t tS = tmem + lanes + COL_S + buf * 128 + col0, tO = tmem + lanes + COL_O + col0;
-    if (__any_sync(0xffffffffu, sees != ~0ull || poison)) {  // scores that do not count become -inf where they lie
+    if (__any_sync(0xffffffffu, sees != ~0u || poison)) {  // scores that do not count become -inf where they lie
       keep_branch();
 #pragma unroll 1
       for (int q = 0; q < nc; q += 8) {
         uint32_t s[8];
         tmem_ldn(tS + q, s);
-        const uint32_t m = static_cast<uint32_t>(sees >> q);
+        const uint32_t m = sees >> q;
 #pragma unroll
         for (int c = 0; c < 8; ++c) s[c] = !((m >> c) & 1) ? there ? 0xFF800000u : 0u : poison ? 0x7FC00000u : s[c];
         tmem_st8(tS + q, s);
@@ -710,11 +712,11 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] = fmaf(__uint_as_float(s[c]), rk, lr + nref[q + c]);
         const float most = warp_columns<8, false>(v, lane);
-        if (lane < 8) red[warp * 64 + q + lane] = most;
+        if (lane < 8) red[warp * 32 + q + lane] = most;
       }
       group_any(id, false);
       float m = -INFINITY;
-      if (tid < nc) m = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
+      if (tid < nc) m = fmaxf(fmaxf(red[tid], red[32 + tid]), fmaxf(red[64 + tid], red[96 + tid]));
       group_any(id, false);
       return m;
     };
@@ -742,13 +744,13 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       const uint64_t in2 = f2_pack(add, add);
       uint32_t top = 0;  // the largest weight, as f16 pairs
 #pragma unroll
-      for (int q = 0; q < NC; q += 16) {
+      for (int q = 0; q < NC; q += 8) {
         if (q >= nc) break;
-        uint32_t s[16];
+        uint32_t s[8];
         tmem_ldn(tS + q, s);
-        uint32_t p[8];
+        uint32_t p[4];
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) {
+        for (int k = 0; k < 8; k += 4) {
           const float4 n = *reinterpret_cast<const float4*>(nref + q + k);
           float x[4];
           f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), rk2, f2_add(lr2, f2_pack(n.x, n.y))), x[0],
@@ -762,11 +764,9 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
           p[k / 2] = pack_f16(x[0], x[1]);
           p[k / 2 + 1] = pack_f16(x[2], x[3]);
         }
-        top = hmax2(top, hmax2(hmax2(hmax2(p[0], p[1]), hmax2(p[2], p[3])), hmax2(hmax2(p[4], p[5]), hmax2(p[6], p[7]))));
-        const int to = (col0 + q) >> 3;  // piece of eight rows, even
-        uint8_t* row = at + (to >> 3) * HALF_TILE;
-        *reinterpret_cast<uint4*>(row + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-        *reinterpret_cast<uint4*>(row + ((((to + 1) ^ tid) & 7) << 4)) = make_uint4(p[4], p[5], p[6], p[7]);
+        top = hmax2(top, hmax2(hmax2(p[0], p[1]), hmax2(p[2], p[3])));
+        const int to = (col0 + q) >> 3;  // piece of eight rows
+        *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
       }
       if (round == 2) break;
       // (as numbers: f16 of one sign are ordered as their bits)
@@ -824,19 +824,18 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   ok = __all_sync(0xffffffffu, ok);
   if (group_any(id, !ok)) return false;
   // The sums meet in shared memory (a place of P': no product reads it until every
-  // warp has its next rows): thread t's, 16 bytes at piece c / 4 ^ (t & 15).
-  float* box = reinterpret_cast<float*>(smem + OFF_P + wg * TILE);
+  // warp has its next rows): thread t's, 16 bytes at piece c / 4 ^ (t & 7).
+  float* box = reinterpret_cast<float*>(smem + OFF_P + wg * HALF_TILE);
 #pragma unroll
   for (int c = 0; c < NC; c += 4)
     if (c < nc)
-      *reinterpret_cast<float4*>(box + tid * 64 + (((c >> 2) ^ (tid & 15)) << 2)) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
+      *reinterpret_cast<float4*>(box + tid * 32 + (((c >> 2) ^ (tid & 7)) << 2)) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
   group_any(id, false);
   {
-    const int c = tid & 63;
     float sum = 0.f;
-    if (c < nc)
+    if (lane < nc)
 #pragma unroll 8
-      for (int t = tid & 64; t < (tid & 64) + 64; ++t) sum += box[t * 64 + (((c >> 2) ^ (t & 15)) << 2) + (c & 3)];
+      for (int t = warp * 32; t < warp * 32 + 32; ++t) sum += box[t * 32 + (((lane >> 2) ^ (t & 7)) << 2) + (lane & 3)];
     red[tid] = sum;
   }
   group_any(id, false);
@@ -844,7 +843,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u0 > 0 ? 0 : 1);
   int64_t* to = reinterpret_cast<int64_t*>(red + 128);  // where each row goes
   if (tid < nc) {
-    const float total = red[tid] + red[64 + tid];
+    const float total = (red[tid] + red[32 + tid]) + (red[64 + tid] + red[96 + tid]);
     const int c = col0 + tid, row = row0 + c, node = row / group, head = w.kvh * group + row - node * group;
     red[tid] = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);  // NaN stays NaN
     to[tid] = alone ? (static_cast<int64_t>(w.q0) + node) * a.n_q + head : slot * a.part_rows + c;
@@ -888,19 +887,19 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < TR_STAGES; ++s) {
       mbar_init(&bar->raw_full[s], 1);
-      mbar_init(&bar->raw_empty[s], 4);
+      mbar_init(&bar->raw_empty[s], 8);
     }
     for (int s = 0; s < 4; ++s) mbar_init(&bar->key_full[s], 4);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->k_full[s], 4);
       mbar_init(&bar->v_full[s], 4);
       mbar_init(&bar->s_full[s], 1);
-      mbar_init(&bar->s_empty[s], 8);
-      mbar_init(&bar->p_full[s], 8);
+      mbar_init(&bar->s_empty[s], TR_GROUPS * 4);
+      mbar_init(&bar->p_full[s], TR_GROUPS * 4);
       mbar_init(&bar->o_done[s], 1);
     }
-    mbar_init(&bar->q_full, 8);
-    mbar_init(&bar->o_empty, 8);
+    mbar_init(&bar->q_full, TR_GROUPS * 4);
+    mbar_init(&bar->o_empty, TR_GROUPS * 4);
     for (int i = 0; i < TR_ITEMS; ++i) mbar_init(&bar->item_full[i], 1);
     mbar_init(&bar->drain, 1);
     bar->abort = 0;
@@ -984,9 +983,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       bar->copies = c;
     }
     __syncwarp();
-    // Registers: 512 threads x 128 at launch = 256 x 184 + 128 x 88 + 128 x 56
-    if (warp < TR_UNPACK) {
-      reg_inc<184>();
+    // Registers: 896 threads x 72 at launch = 512 x 88 + 128 x 56 + 128 x 48 + 128 x 48
+    if (warp < TR_KEYS) {
+      reg_inc<88>();
       uint32_t it = 0;
       for (uint32_t item = 0; ok; ++item) {
         ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
@@ -994,16 +993,21 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         if (!ok || bar->item[item % TR_ITEMS].rows == 0) break;
         ok = tree_softmax(a, smem, bar, tmem, item, it);
       }
-    } else if (warp < TR_COPY_WARP) {
-      reg_dec<88>();
+    } else if (warp < TR_VALUES) {
+      reg_dec<56>();
       uint32_t rs_zero = __float_as_uint(0x1p-12f);  // row scale that rows of zeros take
       bool more = true;
-      const int shift = min(a.c.page_shift, 7);
-      const UnpackLane x(warp - TR_UNPACK, lane, shift);
+      const int shift = min(a.c.page_shift, 7), krow = raw_row((warp - TR_KEYS) * 32 + lane, shift);
       for (uint32_t it = 0; ok && more; ++it)
-        ok = unpack(a.status, smem, bar, tmem, warp - TR_UNPACK, lane, it, shift, x, rs_zero, more) || !more;
+        ok = unpack_keys(a.status, smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, rs_zero, more) || !more;
+    } else if (warp < TR_COPY_WARP) {
+      reg_dec<48>();
+      bool more = true;
+      const int shift = min(a.c.page_shift, 7);
+      const ValueLane x(warp - TR_VALUES, lane, shift);
+      for (uint32_t it = 0; ok && more; ++it) ok = unpack_values(a.status, smem, bar, warp - TR_VALUES, lane, it, shift, x, more) || !more;
     } else {
-      reg_dec<56>();
+      reg_dec<48>();
       if (warp == TR_COPY_WARP) {
         int page = -1;  // of the lane's part of the next unit
         const uint32_t el = elect_one();
@@ -1017,7 +1021,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           const TreeItem& w = bar->item[item % TR_ITEMS];
           const int rows = w.rows, n = w.u1 - w.u0;
           if (!ok || rows == 0) break;
-          const int ns = 2 * tree_columns(rows);
+          const int ns = TR_GROUPS * tree_columns(rows);
           const uint32_t id_s = idesc_f16(128, ns, 0, 0), id_o = idesc_f16(128, (ns + 63) & ~63, 1, 1);
           auto scores = [&](uint32_t i) {
             return i & 1 ? issue_scores<1>(a.status, smem, bar, tmem, i, id_s, el)

@@ -24,7 +24,7 @@ struct TreeArgs {
   __nv_bfloat16* O;        // [T, n_q * 128]
   float* lse;              // [T, n_q]
   int64_t* places;         // [B + 2]: places on the line of work before each sequence, their total, places per CTA
-  uint32_t* seen;          // [TREE_MAX_CTAS, 2, TREE_MAX_NODES, 2] rows of a CTA's tile that see a node, by warpgroup: 64 bits
+  uint32_t* seen;          // [TREE_MAX_CTAS, TREE_ROWS / 32, TREE_MAX_NODES] rows of a CTA's tile that see a node, by warpgroup
   float* part;             // [2 * TREE_MAX_CTAS, part_rows, 128] normalised partial outputs
   float* part_lse;         // [2 * TREE_MAX_CTAS, part_rows] log2 domain
   int part_rows;
