@@ -204,7 +204,7 @@ int coda_verify_drafts(const void* probs, const void* draft_probs, int dtype, in
     return CODA_ERR_ALIGNMENT;
   CK(check_ws(ws, ws_bytes, coda_verify_drafts_workspace_size(T, batch, V)));
   coda::VerifyArgs a{probs, draft_probs, tokens, cu, parents, u, u_next, count, nodes, out_tokens, V,
-                     static_cast<int>(T), static_cast<int>(batch), static_cast<int>(width), static_cast<int*>(ws)};
+                     static_cast<int>(T), static_cast<int>(batch), static_cast<int>(width), 0, static_cast<int*>(ws)};
   CU(coda::launch_verify(a, dtype == CODA_F32, static_cast<cudaStream_t>(stream)));
   return CODA_OK;
 }

@@ -18,10 +18,14 @@
 // their sums are exact in any order.
 //
 // HBM-bound: one row of p and q per request (the walk before it reads two values
-// per node), and bound by latency when there are few.  A cluster of eight CTAs
-// per request: every CTA walks for itself on the nodes' values in shared memory,
-// sums over the vocabulary are split between the CTAs and meet by distributed
-// shared memory.
+// per node), and bound by latency when there are few.  A cluster of up to eight
+// CTAs per request: in every CTA one warp walks on the nodes' values in shared
+// memory (the same walk in all of them), sums over the vocabulary are split
+// between the CTAs and meet by distributed shared memory.  128 requests of 5
+// drawn tokens over 128256 probabilities in fp32 (131 MB at most, 19 us): 32 us
+// in a graph; 8 requests 11 us; 48 trees of 1 to 40 nodes over 50257
+// probabilities in bf16 20 us.  With eight CTAs to every request, each thread
+// walking and sums by conversions to 64 bits it was 128, 33 and 61 us.
 #include <algorithm>
 #include <cuda_bf16.h>
 
@@ -33,7 +37,7 @@
 namespace coda {
 namespace {
 
-constexpr int VF_CTAS = 8;
+constexpr int VF_CTAS = 8;  // of a cluster, at most
 constexpr int VF_THREADS = 512;
 constexpr int VF_WARPS = VF_THREADS / 32;
 typedef unsigned long long u64;
@@ -72,13 +76,51 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
   return v;
 }
 
+// Sums of probabilities in units of 2^-60, with no conversion (F2I of 64 bits
+// runs at an eighth of the rate of an addition): the bits of a probability above
+// 2^-22, the next 22 and the 16 after them are each read off an addition, rounded
+// to zero, to a number whose last place is that unit.  Sums of the three in 32
+// bits hold for 512 values.
+struct Sum60 {
+  int hi = 0, mid = 0, lo = 0;
+  static __device__ __forceinline__ void cut(float p, int& a, int& b, int& c) {
+    const float t = __fadd_rz(p, 2.f), r = p - (t - 2.f);              // exact
+    const float t2 = __fadd_rz(r, 0x1p-21f), r2 = r - (t2 - 0x1p-21f);  // exact
+    a = __float_as_int(t);
+    b = __float_as_int(t2);
+    c = __float_as_int(__fadd_rz(r2, 0x1p-37f));
+  }
+  // p in [0, 1]
+  __device__ __forceinline__ void add(float p) {
+    int a, b, c;
+    cut(p, a, b, c);
+    hi += a - 0x40000000;   // the bits of 2
+    mid += b - 0x35000000;  // 2^-21
+    lo += c - 0x2d000000;   // 2^-37
+  }
+  // max(p - q, 0), each cut to its units
+  __device__ __forceinline__ void add_above(float p, float q) {
+    int a, b, c, d, e, f;
+    cut(p, a, b, c);
+    cut(fminf(p, q), d, e, f);
+    hi += a - d;
+    mid += b - e;
+    lo += c - f;
+  }
+  __device__ __forceinline__ u64 value() const {
+    return (static_cast<u64>(static_cast<int64_t>(hi)) << 38) + (static_cast<u64>(static_cast<int64_t>(mid)) << 16) +
+           static_cast<u64>(static_cast<int64_t>(lo));
+  }
+};
+
 struct VerifyShared {
   u64 Z[VERIFY_MAX_NODES];  // Z after each refusal at the node (Z[0] = 1)
   u64 warp[VF_WARPS], fine[VF_WARPS];
   u64 total;                // of this CTA, read by the others
+  int here, count, ngone, refused, more;  // where the walk stands; more: it wants a sum
   float p[VERIFY_MAX_NODES], q[VERIFY_MAX_NODES], u[VERIFY_MAX_NODES];
   int token[VERIFY_MAX_NODES], parent[VERIFY_MAX_NODES];
-  int gone[VERIFY_MAX_NODES];  // tokens refused at the node (drafts not drawn)
+  int gone[VERIFY_MAX_NODES];  // tokens refused at the node, each once (drafts not drawn)
 };
 
 // Weights of the row where the walk stands.  A row is read in aligned pieces
@@ -123,24 +165,49 @@ struct Row {
   __device__ __forceinline__ bool need_q() const { return q != nullptr && refused > 0; }
 };
 
-// Sum of the weights in [piece, stop) by stride; tokens refused where nothing
-// was drawn are left out by the caller.
+// Sum of this lane's share of the weights of pieces [piece, stop); tokens
+// refused where nothing was drawn are left out by the caller.  (One copy of the
+// code for all of a kernel's sums: the registers of a second one are spilled.)
 template <bool F32>
-__device__ __forceinline__ u64 sum_pieces(const Row<F32>& r, int piece, int stride, int stop, const u64* Z) {
+__device__ __noinline__ u64 sum_pieces(const Row<F32> r, int piece, int stop, const u64* Z) {
   u64 s = 0;
   constexpr int N = 4;  // pieces in flight
-  for (; piece < stop; piece += N * stride) {
-    uint4 vp[N], vq[N];
+  if (!r.need_q()) {
+    for (; piece < stop; piece += N * 32) {
+      uint4 vp[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const bool in = piece + n * stride < stop;
-      vp[n] = in ? r.load(r.p, piece + n * stride) : make_uint4(0, 0, 0, 0);
-      vq[n] = in && r.need_q() ? r.load(r.q, piece + n * stride) : make_uint4(0, 0, 0, 0);
+      for (int n = 0; n < N; ++n)
+        vp[n] = piece + n * 32 < stop ? r.load(r.p, piece + n * 32) : make_uint4(0, 0, 0, 0);
+      Sum60 c;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < Row<F32>::E; ++i) c.add(__saturatef(r.element(vp[n], i)));  // NaN: 0
+      s += c.value();
     }
+  } else if (r.refused == 1) {
+    for (; piece < stop; piece += N * 32) {
+      uint4 vp[N], vq[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+      for (int n = 0; n < N; ++n) {
+        const bool in = piece + n * 32 < stop;
+        vp[n] = in ? r.load(r.p, piece + n * 32) : make_uint4(0, 0, 0, 0);
+        vq[n] = in ? r.load(r.q, piece + n * 32) : make_uint4(0, 0, 0, 0);
+      }
+      Sum60 c;
 #pragma unroll
-      for (int i = 0; i < Row<F32>::E; ++i) s += r.weight(r.element(vp[n], i), r.element(vq[n], i), Z);
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < Row<F32>::E; ++i)
+          c.add_above(__saturatef(r.element(vp[n], i)), __saturatef(r.element(vq[n], i)));
+      s += c.value();
+    }
+  } else {
+    for (; piece < stop; piece += 32) {
+      const uint4 vp = r.load(r.p, piece), vq = r.load(r.q, piece);
+#pragma unroll 1
+      for (int i = 0; i < Row<F32>::E; ++i) s += r.weight(r.element(vp, i), r.element(vq, i), Z);
+    }
   }
   return s;
 }
@@ -153,7 +220,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   constexpr int E = Row<F32>::E;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
-  const int b = static_cast<int>(blockIdx.x) / VF_CTAS;
+  const int ctas = a.ctas, b = static_cast<int>(blockIdx.x) / ctas;
   const int t0 = a.cu[b], t1 = a.cu[b + 1];
   const int n = t1 - t0;
   int32_t* nodes = a.nodes + static_cast<int64_t>(b) * a.width;
@@ -205,7 +272,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   // this CTA's and this warp's pieces
   int c0 = 0, c1 = 0, w0 = 0, w1 = 0;
   auto share = [&]() {
-    const int all = r.pieces(), per = (all + VF_CTAS - 1) / VF_CTAS;
+    const int all = r.pieces(), per = (all + ctas - 1) / ctas;
     c0 = min(all, static_cast<int>(rank) * per);
     c1 = min(all, c0 + per);
     const int pw = (c1 - c0 + VF_WARPS - 1) / VF_WARPS;
@@ -218,9 +285,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
     if (r.q == nullptr)
       for (int k = lane; k < gone; k += 32) {
         const int x = sh.gone[k], at = (x + r.lead) / E;
-        bool again = false;
-        for (int j = 0; j < k; ++j) again |= sh.gone[j] == x;
-        if (!again && at >= from && at < to) s += fixed60(value<F32>(r.p, x));
+        if (at >= from && at < to) s += fixed60(value<F32>(r.p, x));
       }
     return warp_sum(s);
   };
@@ -228,72 +293,105 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   // `before` what the CTAs in front of it have.
   auto total = [&](int gone, u64& before) {
     share();
-    const u64 s = warp_sum(sum_pieces<F32>(r, w0 + lane, 32, w1, sh.Z)) - refused_in(gone, w0, w1);
+    const u64 s = warp_sum(sum_pieces<F32>(r, w0 + lane, w1, sh.Z)) - refused_in(gone, w0, w1);
     if (lane == 0) sh.warp[warp] = s;
     __syncthreads();
-    if (tid == 0) {
-      u64 c = 0;
-#pragma unroll
-      for (int i = 0; i < VF_WARPS; ++i) c += sh.warp[i];
-      sh.total = c;
-    }
-    cluster_sync();
-    u64 all = 0;
+    u64 c = 0;
     before = 0;
 #pragma unroll
-    for (uint32_t i = 0; i < VF_CTAS; ++i) {
-      const u64 c = ld_cluster_u64(&sh.total, i);
-      if (i < rank) before += c;
-      all += c;
-    }
+    for (int i = 0; i < VF_WARPS; ++i) c += sh.warp[i];
+    if (ctas == 1) return c;
+    if (tid == 0) sh.total = c;
+    cluster_sync();
+    u64 all = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < VF_CTAS; ++i)
+      if (i < ctas) {
+        c = ld_cluster_u64(&sh.total, i);
+        if (i < rank) before += c;
+        all += c;
+      }
     cluster_sync();  // read by all before it is written again, or its CTA ends
     return all;
   };
 
-  // Every thread walks, on the same values.
-  int here = 0, count = 0, gone = 0, known = 0;  // known: refusals whose Z is there
+  // Warp 0 walks (the comparisons are in 64 bits, of which an SM does few), up
+  // to a child whose decision needs a sum over the vocabulary, or to the end.
+  int here = 0, count = 0, gone = 0, refused = 0, next = 1;
+  bool summed = true;  // Z is that of the refusals so far
   double Z = 1.0;
   u64 before = 0;
-  stand(0);
   if (rank == 0 && tid == 0) nodes[0] = 0;
   if (tid == 0) sh.Z[0] = 1ull << 60;
-  __syncthreads();
-  for (int i = 1; i < n && count + 1 < a.width; ++i) {
-    if (sh.parent[i] != here) continue;
-    const int x = sh.token[i];
-    double wx = sh.p[i];
-    if (a.Q) {
-      if (r.refused > known) {  // a refusal before this child: its sum is wanted now
-        const u64 z = total(0, before);
-        if (tid == 0) sh.Z[r.refused] = z;
-        __syncthreads();
-        known = r.refused;
-        Z = static_cast<double>(z) * 0x1p-60;
+  for (;;) {
+    if (warp == 0) {
+      bool more = false;
+      while (count + 1 < a.width && next < n) {
+        const int seen = next & ~31;
+        const uint32_t kids = __ballot_sync(0xffffffffu, seen + lane < n && sh.parent[seen + lane] == here) &
+                              (0xffffffffu << (next & 31));
+        if (kids == 0) {
+          next = seen + 32;
+          continue;
+        }
+        const int i = seen + __ffs(kids) - 1;
+        if (!summed) {
+          next = i;
+          more = true;
+          break;
+        }
+        next = i + 1;
+        const int x = sh.token[i];
+        double wx = sh.p[i];
+        bool again = false;  // refused here before: nothing is left of it
+        if (a.Q) {
+          r.q = a.Q;  // (only whether there is one)
+          r.refused = refused;
+          if (refused > 0) wx = static_cast<double>(r.weight(sh.p[i], sh.q[i], sh.Z)) * 0x1p-60;
+        } else {
+          again = false;
+          for (int k = lane; k < gone; k += 32) again |= sh.gone[k] == x;
+          again = __any_sync(0xffffffffu, again);
+          if (again) wx = 0.0;
+        }
+        if (static_cast<double>(sh.u[i]) * (static_cast<double>(sh.q[i]) * Z) < wx) {
+          if (rank == 0 && lane == 0) {
+            out[count] = x;
+            nodes[count + 1] = i;
+          }
+          ++count;
+          here = i;
+          Z = 1.0;
+          gone = refused = 0;
+        } else if (a.Q) {
+          ++refused;
+          summed = false;
+        } else if (!again) {
+          Z -= wx;
+          if (lane == 0) sh.gone[gone] = x;
+          __syncwarp();
+          ++gone;
+        }
       }
-      if (r.refused > 0) wx = static_cast<double>(r.weight(sh.p[i], sh.q[i], sh.Z)) * 0x1p-60;
-    } else {
-      for (int k = 0; k < gone; ++k)
-        if (sh.gone[k] == x) wx = 0.0;
-    }
-    if (static_cast<double>(sh.u[i]) * (static_cast<double>(sh.q[i]) * Z) < wx) {
-      if (rank == 0 && tid == 0) {
-        out[count] = x;
-        nodes[count + 1] = i;
+      if (lane == 0) {
+        sh.here = here;
+        sh.count = count;
+        sh.ngone = gone;
+        sh.refused = refused;
+        sh.more = more;
       }
-      ++count;
-      here = i;
-      Z = 1.0;
-      gone = known = 0;
-      stand(i);
-    } else if (a.Q) {
-      ++r.refused;
-    } else {
-      Z -= wx;
-      __syncthreads();
-      if (tid == 0) sh.gone[gone] = x;
-      __syncthreads();
-      ++gone;
     }
+    __syncthreads();
+    stand(sh.here);
+    r.refused = sh.refused;
+    count = sh.count;
+    gone = sh.ngone;
+    if (!sh.more) break;
+    const u64 z = total(0, before);
+    if (tid == 0) sh.Z[r.refused] = z;
+    __syncthreads();
+    summed = true;
+    Z = static_cast<double>(z) * 0x1p-60;
   }
 
   // The next token.  Nothing left (probabilities that do not sum to 1): the
@@ -302,6 +400,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   if (all == 0 && (r.refused > 0 || gone > 0)) {
     r.refused = 0;
     gone = 0;
+    __syncthreads();  // the warps' parts have been read
     all = total(0, before);
   }
   const float un = a.u_next[b];
@@ -333,7 +432,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   const int s0 = min(c1, c0 + at * pw), s1 = min(c1, s0 + pw);
   const int run = ((s1 - s0 + VF_WARPS - 1) / VF_WARPS + 31) & ~31;  // pieces per warp
   const int f0 = min(s1, s0 + warp * run), f1 = min(s1, f0 + run);
-  const u64 s = warp_sum(sum_pieces<F32>(r, f0 + lane, 32, f1, sh.Z)) - refused_in(gone, f0, f1);
+  const u64 s = warp_sum(sum_pieces<F32>(r, f0 + lane, f1, sh.Z)) - refused_in(gone, f0, f1);
   if (lane == 0) sh.fine[warp] = s;
   __syncthreads();
   at = 0;
@@ -386,14 +485,19 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs& a, bool f32, cudaStream_t s) {
+cudaError_t launch_verify(VerifyArgs a, bool f32, cudaStream_t s) {
+  // As many CTAs to a request as are resident at once, two to an SM; a second
+  // wave would walk its trees while the memory has nothing to do.
+  const int64_t slots = 2 * static_cast<int64_t>(device_sms());
+  a.ctas = VF_CTAS;
+  while (a.ctas > 1 && static_cast<int64_t>(a.B) * a.ctas > slots) a.ctas >>= 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * VF_CTAS);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.ctas);
   cfg.blockDim = dim3(VF_THREADS);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = VF_CTAS;
+  attr[0].val.clusterDim.x = a.ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;

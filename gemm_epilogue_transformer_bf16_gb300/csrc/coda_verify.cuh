@@ -20,8 +20,9 @@ struct VerifyArgs {
   int32_t* out;             // [B, width]
   int64_t V;
   int T, B, width;
+  int ctas;                 // of a request, set at the launch
   int* status;
 };
-cudaError_t launch_verify(const VerifyArgs& a, bool f32, cudaStream_t s);
+cudaError_t launch_verify(VerifyArgs a, bool f32, cudaStream_t s);
 
 }  // namespace coda
