@@ -2,7 +2,7 @@
 // sees the committed prefix, its ancestors and itself,
 //   s_ij = scale q_i . k_j,  O_i = sum_j exp(s_ij - lse_i) v_j.
 //
-// Bounds: 152 bytes per cached token and key/value head feed 2 * 128
+// Floor: 152 bytes per cached token and key/value head feed 2 * 128
 // multiply-adds for each row, a row being a node and a query head of the
 // group.  Up to about 80 rows the bytes take longer at this chip's rates, then the
 // products.
@@ -21,16 +21,38 @@
 //   O^T [128 elements x rows] += V'^T P'^T V' in shared memory, elements
 //                                          contiguous; P' too, rows contiguous
 // so that few rows make a narrow product instead of an empty one, and a
-// softmax thread has one key: its scales are two registers, sums over keys stay
-// in the thread until the end, and no maximum is exchanged unless a weight passes
-// its bound.
+// thread of the weights has one key: its scales are two registers, sums over
+// keys stay in the thread until the end, and no maximum is exchanged unless a
+// weight passes its bound.  (K' from shared memory would take the whole of its
+// bandwidth with 128 rows; from TMEM the product runs at its own rate.)
 //
 // A weight carries its value's row scale rs:
 //   P' = 2^t,  t = scale log2(e) rs_k (q . k') + log2 rs_v - r,  l = sum P' / rs_v
-// with a reference r per row, raised when some t passes 10 (f16 holds 2^15),
+// with a reference r per row that rises when some t passes 10 (f16 holds 2^15),
 // so P' is rounded by 2^-11 of itself or 2^-25 of the largest weighted row
 // scale.  Rows of zeros take the smallest row scale of their neighbours: their
-// own says nothing.  l, r and O are fp32.
+// own says nothing.  l, r and O are fp32.  Weights are computed and summed in one
+// pass over the scores; where one turns out to pass the bound the pass is taken
+// back (the sums with a minus), the reference rises and a second pass follows.
+//
+// Roles: four warpgroups of weights with a quarter of the tile's rows each (their
+// sums fit the 72 registers that 28 warps leave), four warps each for K' and V',
+// one that copies by tensor maps, one that issues the products, two idle.
+// Stages of the cache, scores, K', V' and P' are double or triple, so that all
+// roles work on different units.
+//
+// What bounds it: instructions.  A unit of 128 keys takes 2600 to 3600 clocks (at
+// 32 to 128 rows) for 850 of copies and 130 to 510 of products: the roles' code
+// takes turns in the four schedulers and in their instruction caches (two
+// instructions a clock and SM).  What counted most on the way were fewer and
+// shorter code paths: rolled unpacking 268 -> 218 us for 8 trees of 64 nodes
+// over 16384 keys, one copy of the weights' code 299 -> 268, no spilled
+// register 580 -> 321; 32 warps with eight for V' and scores loaded ahead
+// gained 8 % at two long documents and lost 4 to 8 % elsewhere.  Now, in a
+// graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 187 us (floor 45), 24
+// trees of 1 to 64 nodes over 60 to 6000 keys 206 us (44), a chain of 6 over 777
+// keys 20.6 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys 210 us (71), trees
+// of 16 and 11 nodes over 131055 and 100001 keys 169 us (42).
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -69,8 +91,12 @@ constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
 constexpr uint64_t TR_WAIT_NS = 2000000000ull;
 
-// Places of a unit, by the rows of its tile, and of a stretch's ends.
-constexpr int TR_COST_FEW = 4, TR_COST_MANY = 6, TR_END = 12;
+// Places of a unit, by the rows of its tile, and of a stretch's ends, whose
+// loads, sums and stores take as long as four to seven units.  Measured, for 24 ragged trees
+// / 64 chains / 8 trees of 64 nodes: 4, 6, 12 245 / 190 / 211 us; 4, 6, 20 237 / 188
+// / 211; 4, 6, 32 244 / 197 / 212; 5, 6, 18 222 / 185 / 211; 5, 6, 24 206 / 187 /
+// 210; 6, 6, 24 208 / 187 / 215.
+constexpr int TR_COST_FEW = 5, TR_COST_MANY = 6, TR_END = 24;
 
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |

@@ -23,7 +23,7 @@
 // memory (the same walk in all of them), sums over the vocabulary are split
 // between the CTAs and meet by distributed shared memory.  128 requests of 5
 // drawn tokens over 128256 probabilities in fp32 (131 MB at most, 19 us): 32 us
-// in a graph; 8 requests 11 us; 48 trees of 1 to 40 nodes over 50257
+// in a graph; one request of 7 11 us; 48 trees of 1 to 40 nodes over 50257
 // probabilities in bf16 20 us.  With eight CTAs to every request, each thread
 // walking and sums by conversions to 64 bits it was 128, 33 and 61 us.
 #include <algorithm>
