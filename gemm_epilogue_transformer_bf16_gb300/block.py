@@ -42,16 +42,17 @@ on one stream.  The gate/up and down GEMMs run alone.
 
 ``AttentionBlock`` is the block with its attention core (coda_attention) in
 place of the given A, over packed sequences; ``ServingBlock`` runs the forward
-of prompts and of single new tokens over a 4-bit key/value cache.
+of prompts, of single new tokens and of trees of drafted ones over a 4-bit
+key/value cache.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (K_MAJOR, MN_MAJOR, EpilogueDesc, attention, attention_bwd, attention_decode_nvfp4, fold_gamma,
-               gemm_epilogue, kv_append_nvfp4, kv_read_nvfp4, linear_cross_entropy, linear_cross_entropy_bwd, linear_dswiglu_fp8, linear_fp8, linear_qknorm_rope, linear_qknorm_rope_bwd,
+from . import (K_MAJOR, MN_MAJOR, EpilogueDesc, attention, attention_bwd, attention_decode_nvfp4, attention_tree_nvfp4,
+               fold_gamma, gemm_epilogue, kv_accept_nvfp4, kv_append_nvfp4, kv_append_rope_nvfp4, kv_read_nvfp4, linear_cross_entropy, linear_cross_entropy_bwd, linear_dswiglu_fp8, linear_fp8, linear_qknorm_rope, linear_qknorm_rope_bwd,
                linear_qknorm_rope_bwd_fp8, linear_qknorm_rope_fp8, linear_residual, linear_residual_bwd, linear_swiglu, linear_swiglu_bwd,
-               linear_swiglu_fp8, load, quantize_fp8_cols, quantize_fp8_rows, rms_rstd, rmsnorm_linear_dx_fp8,
+               linear_swiglu_fp8, load, quantize_fp8_cols, quantize_fp8_rows, rms_rstd, rmsnorm_linear, rmsnorm_linear_dx_fp8,
                rmsnorm_scale, rope_table, workspace)
 
 
@@ -273,15 +274,31 @@ class ServingBlock:
     prefill  whole prompts, or the next chunk of prompts whose earlier tokens
              the cache holds (``key_slots``, ``cu_seqlens_k``)
     decode   one new token per sequence
+    tree     drafted tokens, a tree or chain per sequence
+    accept   the cache rows of the drafts that were accepted move to the places
+             behind the prefix
+
+    Weights without ``gamma_q`` and ``gamma_k`` are of a block without QK-norm:
+    its projection is the plain one, and the append to the cache rotates Q and K
+    on its way (``pairing``, and ``rotary_dim`` elements of each head).
+    ``scaling`` is rope_table's, for contexts longer than those trained on.
 
     ``ws``, of at least ``workspace_size`` bytes, is the workspace of every call
-    within: its status word tells of positions, slots, pages, lengths or offsets
-    out of range.  Without it each of them makes its own, and nothing tells.
+    within: its status word tells of positions, slots, pages, lengths, offsets or
+    parents out of range.  Without it each of them makes its own, and nothing
+    tells.
     """
 
-    def __init__(self, shape, weights, cache, device="cuda"):
-        self.s, self.w, self.cache = shape, weights, cache
-        self.cos_sin = rope_table(shape.theta, shape.head_dim, shape.seq_len, device=device)
+    def __init__(self, shape, weights, cache, device="cuda", pairing="interleaved", rotary_dim=None, scaling=None):
+        self.s, self.w, self.cache, self.pairing = shape, weights, cache, pairing
+        self.qk_norm = "gamma_q" in weights
+        if self.qk_norm != ("gamma_k" in weights):
+            raise ValueError("weights: gamma_q and gamma_k, or neither")
+        if self.qk_norm and rotary_dim not in (None, shape.head_dim):
+            raise ValueError("rotary_dim: the projection with QK-norm rotates whole heads")
+        self.cos_sin = rope_table(shape.theta, rotary_dim or shape.head_dim, shape.seq_len, device=device, scaling=scaling)
+        if not self.qk_norm:
+            self.Wqkv_f = fold_gamma(weights["Wqkv"], weights["gamma_attn"])
 
     def workspace_size(self, tokens, keys, sequences):
         """For every call of up to ``tokens`` new tokens, ``keys`` rows of K and
@@ -295,16 +312,28 @@ class ServingBlock:
         return max(lib.coda_attention_workspace_size(tokens, keys, sequences, s.n_q, s.n_kv, s.head_dim),
                    lib.coda_attention_workspace_size(1, keys, 1, s.n_q, s.n_kv, s.head_dim) + lists,
                    lib.coda_attention_decode_nvfp4_workspace_size(sequences, s.n_q, s.n_kv, s.head_dim),
+                   lib.coda_attention_tree_nvfp4_workspace_size(rows, sequences, s.n_q, s.n_kv, s.head_dim),
+                   lib.coda_rmsnorm_linear_workspace_size(rows, (s.n_q + 2 * s.n_kv) * s.head_dim, s.hidden),
                    lib.coda_linear_qknorm_rope_workspace_size(rows, s.hidden, s.n_q, s.n_kv, s.head_dim),
                    lib.coda_linear_residual_workspace_size(rows, s.hidden, s.n_q * s.head_dim),
                    lib.coda_linear_swiglu_workspace_size(rows, s.inter, s.hidden),
                    lib.coda_linear_residual_workspace_size(rows, s.hidden, s.inter))
 
-    def _qkv(self, x, pos, ws):
+    def _qkv(self, x, pos, slots, ws, keep_k=False):
+        """The new tokens' Q, K (with keep_k) and V, their keys and values in the
+        cache."""
         s, w = self.s, self.w
-        rstd, U = rmsnorm_scale(x, w["gamma_attn"], s.eps)
-        return linear_qknorm_rope(U, w["Wqkv"], w["gamma_q"], w["gamma_k"], pos, self.cos_sin, s.n_q, s.n_kv, rstd=rstd,
-                                  eps=s.eps, head_dim=s.head_dim, save=False, ws=ws)
+        if self.qk_norm:
+            rstd, U = rmsnorm_scale(x, w["gamma_attn"], s.eps)
+            f = linear_qknorm_rope(U, w["Wqkv"], w["gamma_q"], w["gamma_k"], pos, self.cos_sin, s.n_q, s.n_kv, rstd=rstd,
+                                   eps=s.eps, head_dim=s.head_dim, save=False, ws=ws, pairing=self.pairing)
+            kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
+            return f
+        Y, _ = rmsnorm_linear(x, self.Wqkv_f, rstd_in=rms_rstd(x, s.eps), ws=ws)
+        Q, K, V = Y.split([s.n_q * s.head_dim, s.n_kv * s.head_dim, s.n_kv * s.head_dim], dim=1)
+        f = kv_append_rope_nvfp4(K, V, slots, self.cache, pos, self.cos_sin, Q=Q, n_q=s.n_q, pairing=self.pairing,
+                                 keep_k=keep_k, ws=ws)
+        return {"Q": f["Q"], "K": f["K"] if keep_k else None, "V": V}
 
     def _rest(self, x, A, ws):
         s, w = self.s, self.w
@@ -323,8 +352,7 @@ class ServingBlock:
         behind the last sequence: slots -1, and an output of the row without
         attention."""
         s = self.s
-        f = self._qkv(x, pos, ws)
-        kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
+        f = self._qkv(x, pos, slots, ws, keep_k=key_slots is None)
         K, V = f["K"], f["V"]
         if key_slots is not None:
             kv = kv_read_nvfp4(self.cache, key_slots, ws=ws)
@@ -339,10 +367,26 @@ class ServingBlock:
         """x [batch, hidden]: one new token per sequence; seq_lens [batch]
         counts it."""
         s = self.s
-        f = self._qkv(x, pos, ws)
-        kv_append_nvfp4(f["K"], f["V"], slots, self.cache, ws=ws)
+        f = self._qkv(x, pos, slots, ws)
         out = attention_decode_nvfp4(f["Q"], self.cache, block_table, seq_lens, s.n_q, ws=ws)
         return self._rest(x, out["O"], ws)
+
+    def tree(self, x, pos, slots, cu_seqlens, block_table, seq_lens, parents=None, ws=None):
+        """x [T, hidden]: the packed drafted tokens, a tree (parents [T] within
+        it, -1: none) or chain per sequence; seq_lens [batch] counts them.  A
+        node's position is its depth behind the prefix, its slot the place of its
+        number there.  Padding as in prefill."""
+        s = self.s
+        f = self._qkv(x, pos, slots, ws)
+        out = {"O": torch.zeros(x.shape[0], s.n_q * s.head_dim, dtype=torch.bfloat16, device=x.device),
+               "lse": torch.empty(x.shape[0], s.n_q, dtype=torch.float32, device=x.device)}
+        attention_tree_nvfp4(f["Q"], self.cache, block_table, seq_lens, cu_seqlens, s.n_q, parents=parents, out=out, ws=ws)
+        return self._rest(x, out["O"], ws)
+
+    def accept(self, block_table, seq_lens, cu_seqlens, nodes, count, ws=None):
+        """The accepted nodes (verify_drafts) take the places behind the prefix:
+        the sequences' new lengths."""
+        return kv_accept_nvfp4(self.cache, block_table, seq_lens, cu_seqlens, nodes, count, ws=ws)["seq_lens"]
 
 
 class BlockFP8:
