@@ -86,6 +86,7 @@ constexpr uint32_t OFF_BAR = OFF_RED + 3072;
 constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
+constexpr int TR_HALF_ROWS = 32;
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
@@ -108,6 +109,9 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 // Barrier of a warpgroup that tells whether any thread's predicate holds.
 __device__ __forceinline__ bool group_any(int id, bool p) {
   uint32_t r;
@@ -544,34 +548,40 @@ __device__ __forceinline__ bool unpack_values(int* status, uint8_t* smem, TreeBa
   const bool in = ((u.on >> (2 * g + (lane >> 4))) & 1u) && lane < u.left;
   const float less = in && rsv < 0x1p-100f ? rsv * 0x1p100f : 1.f;
   const bool tiny = __any_sync(0xffffffffu, less != 1.f), whole = __all_sync(0xffffffffu, in);
-  const bool ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
-  if (!__all_sync(0xffffffffu, ok)) return false;
-  const bool upper = lane & 4;
-#pragma unroll 1
-  for (int h = 0; h < 4; ++h) {
-    uint2 c[2];
-    uint32_t sv[2];
+  uint2 c[2];
+  uint32_t sv[2];
+  auto load = [&](int h) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t at = (h & 1) * 512 + i * 256;
       c[i] = *reinterpret_cast<const uint2*>(raw + ((h < 2 ? x.v[0] : x.v[1]) ^ (i * 32)) + at);
       sv[i] = raw[(h < 2 ? x.sf[0] : x.sf[1]) + (at >> 3)];
     }
+  };
+  load(0);
+  const bool ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  const bool upper = lane & 4;
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    const uint2 now[2] = {c[0], c[1]};
+    const uint32_t snow[2] = {sv[0], sv[1]};
+    load((h + 1) & 3);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // zeros outside the sequence, and for a scale that is NaN (the key's weights
       // are NaN then)
       const int k = 8 * h + 4 * i + (lane >> 3);
       const bool kin = whole || (((u.on >> (2 * g + (h >> 1))) & 1u) && k < u.left);
-      uint32_t s = e4m3x2_f16(kin && (sv[i] & 0x7Fu) != 0x7Fu ? sv[i] * 0x101u : 0u);
+      uint32_t s = e4m3x2_f16(kin && (snow[i] & 0x7Fu) != 0x7Fu ? snow[i] * 0x101u : 0u);
       if (tiny) {
         keep_branch();
         const float by = __shfl_sync(0xffffffffu, less, k);
         s = pack_f16(f16_lo(s) * by, f16_hi(s) * by);
       }
       uint32_t f[4], e[4];
-      e2m1x8_f16(upper ? c[i].y : c[i].x, f);
-      e2m1x8_f16(upper ? c[i].x : c[i].y, e);
+      e2m1x8_f16(upper ? now[i].y : now[i].x, f);
+      e2m1x8_f16(upper ? now[i].x : now[i].y, e);
       const int turn = i * 64;  // of the swizzle
       uint8_t* a0 = smem + OFF_V + buf * TILE + (x.to ^ turn) + h * 1024 + i * 512;
       uint8_t* a1 = smem + OFF_V + buf * TILE + (x.to ^ turn ^ 16) + h * 1024 + i * 512;
@@ -588,8 +598,13 @@ __device__ __forceinline__ bool unpack_values(int* status, uint8_t* smem, TreeBa
   return true;
 }
 
-// Columns of a tile that each of the four warpgroups takes: whole chunks of 8.
-__device__ __forceinline__ int tree_columns(int rows) { return (rows + 31) / 32 * 8; }
+// Warpgroups that share a tile's rows, and the columns that each takes: whole
+// chunks of 8.
+__device__ __forceinline__ int tree_groups(int rows) { return rows <= TR_HALF_ROWS ? 2 : TR_GROUPS; }
+__device__ __forceinline__ int tree_columns(int rows) {
+  const int per = 8 * tree_groups(rows);
+  return (rows + per - 1) / per * 8;
+}
 
 // A warpgroup's part of one stretch: the weights of nc columns of the tile, in
 // chunks of 8.  `it` counts the CTA's units.  False: a wait ran out.
@@ -602,6 +617,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   const TreeItem& w = bar->item[item % TR_ITEMS];
   const int row0 = w.row0;
   const int nc = tree_columns(w.rows), col0 = wg * nc;
+  const uint32_t arrive = TR_GROUPS / tree_groups(w.rows);  // for the warps without rows too
   constexpr int NC = TREE_ROWS / TR_GROUPS;  // the most there may be
   float* red = reinterpret_cast<float*>(smem + OFF_RED) + wg * 192;                           // [4][32] and more
   float* nref = reinterpret_cast<float*>(smem + OFF_ROW) + (item & 1) * TREE_ROWS + col0;  // -r per column
@@ -657,7 +673,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   if (tid < nc) nref[tid] = 0.f;  // no reference yet
   fence_async_smem();
   __syncwarp();
-  if (lane == 0) mbar_arrive(&bar->q_full);
+  if (lane == 0) mbar_arrive_n(&bar->q_full, arrive);
 
   // ---- what each row sees of its tree
   const int prefix = w.len - w.n;  // keys that every row sees
@@ -839,8 +855,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&bar->s_empty[buf]);
-      mbar_arrive(&bar->p_full[buf]);
+      mbar_arrive_n(&bar->s_empty[buf], arrive);
+      mbar_arrive_n(&bar->p_full[buf], arrive);
     }
   }
 
@@ -1013,10 +1029,24 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     if (warp < TR_KEYS) {
       reg_inc<88>();
       uint32_t it = 0;
+      bool behind = false;
       for (uint32_t item = 0; ok; ++item) {
         ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
         ok = !group_any(1 + (warp >> 2), !ok);
-        if (!ok || bar->item[item % TR_ITEMS].rows == 0) break;
+        const TreeItem& w = bar->item[item % TR_ITEMS];
+        if (!ok || w.rows == 0) break;
+        const bool idle = warp >= 4 * tree_groups(w.rows);  // few rows: the other warpgroups have them
+        // The item before is done: its products have read Q, and a warpgroup that
+        // has no rows is at most one item away from the others.
+        if (item > 0 && (idle || behind)) ok = tree_wait(&bar->o_empty, (item - 1) & 1, bar, a.status);
+        ok = !group_any(1 + (warp >> 2), !ok);
+        if (!ok) break;
+        behind = idle;
+        if (idle) {
+          it += w.u1 - w.u0;
+          if (lane == 0) mbar_arrive(&bar->o_empty);
+          continue;
+        }
         ok = tree_softmax(a, smem, bar, tmem, item, it);
       }
     } else if (warp < TR_VALUES) {
@@ -1047,7 +1077,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           const TreeItem& w = bar->item[item % TR_ITEMS];
           const int rows = w.rows, n = w.u1 - w.u0;
           if (!ok || rows == 0) break;
-          const int ns = TR_GROUPS * tree_columns(rows);
+          const int ns = tree_groups(rows) * tree_columns(rows);
           const uint32_t id_s = idesc_f16(128, ns, 0, 0), id_o = idesc_f16(128, (ns + 63) & ~63, 1, 1);
           auto scores = [&](uint32_t i) {
             return i & 1 ? issue_scores<1>(a.status, smem, bar, tmem, i, id_s, el)
