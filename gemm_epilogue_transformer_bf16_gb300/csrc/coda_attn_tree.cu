@@ -86,7 +86,7 @@ constexpr uint32_t OFF_BAR = OFF_RED + 3072;
 constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
-constexpr int TR_HALF_ROWS = 32;
+constexpr int TR_HALF_ROWS = 64;
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
