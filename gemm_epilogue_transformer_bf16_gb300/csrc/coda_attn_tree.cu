@@ -90,7 +90,6 @@ constexpr int TR_HALF_ROWS = 64;
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
-constexpr uint64_t TR_WAIT_NS = 2000000000ull;
 
 // Places of a unit, by the rows of its tile, and of a stretch's ends, whose
 // loads, sums and stores take as long as four to seven units.  Measured, for 24 ragged trees
@@ -280,13 +279,31 @@ struct TreeBars {
   int64_t scan[TR_THREADS / 32], before;  // of the places, and the sequence that the CTA begins with
   int seq;
   uint32_t tmem;
-  int abort;
 };
 static_assert(sizeof(TreeBars) <= 1152, "barrier area");
 
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, TreeBars* s, int* status) {
-  if (__builtin_expect(mbar_try_wait(smem_u32(bar), parity), 1)) return true;
-  return mbar_wait_bounded(bar, parity, &s->abort, status, TR_WAIT_NS);
+// A wait that gives up after 2^19 tries, for each of which the hardware may
+// suspend the warp for 4 us (2 s in all).  As short as can be: roles wait in every unit, and
+// the code competes for the instruction caches (a clock in it and a flag that
+// others gave up cost 3 % of the whole kernel).
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "again_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+      "@p bra done_%=;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.ge.u32 p, n, 524288;\n\t"
+      "@!p bra again_%=;\n\t"
+      "setp.ne.u32 p, n, n;\n\t"
+      "done_%=:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y, int z, int v, int w,
@@ -318,7 +335,7 @@ __device__ __forceinline__ bool copy_unit(const TreeArgs& a, const CUtensorMap* 
   const KvCache& kc = a.c;
   const int shift = min(kc.page_shift, 7);  // keys of a part
   const uint32_t st = c.it % TR_STAGES;
-  bool ok = tree_wait(&bar->raw_empty[st], ((c.it / TR_STAGES) & 1) ^ 1, bar, a.status);
+  bool ok = tree_wait(&bar->raw_empty[st], ((c.it / TR_STAGES) & 1) ^ 1);
   if (!__all_sync(0xffffffffu, ok)) return false;
   auto page_of = [&](int u) {  // of this lane's part of unit u; -1: nothing there
     const int k = u * TR_UNIT + (lane << shift);
@@ -394,10 +411,10 @@ __device__ __forceinline__ bool copy_unit(const TreeArgs& a, const CUtensorMap* 
 // (BUF is i's parity), so that descriptors stay in uniform registers: with
 // computed ones eight products took twice the time to issue that they run.
 template <int BUF>
-__device__ __forceinline__ bool issue_scores(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
+__device__ __forceinline__ bool issue_scores(uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
                                              uint32_t el) {
   const uint32_t ph = (i >> 1) & 1;
-  const bool ok = tree_wait(&bar->k_full[BUF], ph, bar, status) && tree_wait(&bar->s_empty[BUF], ph ^ 1, bar, status);
+  const bool ok = tree_wait(&bar->k_full[BUF], ph) && tree_wait(&bar->s_empty[BUF], ph ^ 1);
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   const uint32_t q = smem_u32(smem + OFF_Q);
@@ -410,11 +427,11 @@ __device__ __forceinline__ bool issue_scores(int* status, uint8_t* smem, TreeBar
 }
 // O^T += V'^T P'^T of unit i; first: of an item, whose predecessor's O has left.
 template <int BUF>
-__device__ __forceinline__ bool issue_outputs(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
+__device__ __forceinline__ bool issue_outputs(uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
                                               bool first, uint32_t item, uint32_t el) {
   const uint32_t ph = (i >> 1) & 1;
-  const bool ok = tree_wait(&bar->p_full[BUF], ph, bar, status) && tree_wait(&bar->v_full[BUF], ph, bar, status) &&
-                  (!first || tree_wait(&bar->o_empty, (item & 1) ^ 1, bar, status));
+  const bool ok = tree_wait(&bar->p_full[BUF], ph) && tree_wait(&bar->v_full[BUF], ph) &&
+                  (!first || tree_wait(&bar->o_empty, (item & 1) ^ 1));
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   const uint32_t v = smem_u32(smem + OFF_V + BUF * TILE), p = smem_u32(smem + OFF_P + BUF * TILE);
@@ -445,9 +462,9 @@ struct UnitIn {
   uint32_t on;
   int left;
 };
-__device__ __forceinline__ bool unit_in(int* status, TreeBars* bar, uint32_t it, int g, UnitIn& x, bool& more) {
+__device__ __forceinline__ bool unit_in(TreeBars* bar, uint32_t it, int g, UnitIn& x, bool& more) {
   const uint32_t st = it % TR_STAGES;
-  const bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1, bar, status);
+  const bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1);
   if (!__all_sync(0xffffffffu, ok)) return false;
   x.on = bar->keys_in[st];
   x.left = bar->left[st] - 32 * g;
@@ -459,11 +476,11 @@ __device__ __forceinline__ bool unit_in(int* status, TreeBars* bar, uint32_t it,
 // its row, and the key's scales.  False: a wait ran out, or no unit (`more`) is
 // left.  (Rolled, as below: warps of all roles share a scheduler, and their
 // straight-line code does not fit its instruction cache together.)
-__device__ __forceinline__ bool unpack_keys(int* status, uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane,
+__device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane,
                                             uint32_t it, int shift, int krow, uint32_t& rs_zero, bool& more) {
   const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
   UnitIn x;
-  if (!unit_in(status, bar, it, g, x, more)) return false;
+  if (!unit_in(bar, it, g, x, more)) return false;
   const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
   const bool in = ((x.on >> (2 * g + (lane >> 4))) & 1u) && lane < x.left;  // else whatever the stage held before
   const uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + krow * 8);
@@ -472,7 +489,7 @@ __device__ __forceinline__ bool unpack_keys(int* status, uint8_t* smem, TreeBars
   const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (krow + (1 << shift)) * 4);
   const uint8_t* kc = raw + RW_CODES + krow * 64;
   uint4 v = *reinterpret_cast<const uint4*>(kc + (((krow >> 1) & 3) << 4));
-  bool ok = tree_wait(&bar->s_full[buf], ph ^ 1, bar, status);  // the scores of two units ago have read K'
+  bool ok = tree_wait(&bar->s_full[buf], ph ^ 1);  // the scores of two units ago have read K'
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   uint64_t sf8 = in ? static_cast<uint64_t>(sfk.y) << 32 | sfk.x : 0;
@@ -517,76 +534,79 @@ __device__ __forceinline__ bool unpack_keys(int* status, uint8_t* smem, TreeBars
   return true;
 }
 
-// V' of unit `it` by four warps: a lane takes sixteen elements of keys k0 + 4 i
-// (k0 = lane / 8 of the warp's 32).
+// V' of unit `it` by four warps: a lane takes sixteen elements (piece p of eight)
+// of keys k0 + 4 j of the warp's 32.  Eight lanes write four pieces of two
+// neighbouring keys, which the swizzle sends to different banks.
 struct ValueLane {
   uint32_t v[2];    // codes of the values: first 16 keys, the others
   uint32_t sf[2];   // their block scales
-  uint32_t to;      // where V' goes
-  // Even and odd i differ in one bit of the swizzled places.  Pieces 2 p and
-  // 2 p + 1 of a row are exchanged for the upper elements, so that eight lanes
-  // write to different banks.
+  uint32_t to;      // where V' goes; even and odd j differ in one bit of the swizzled places
+  int k0, row;      // and the row of key `lane`
   __device__ __forceinline__ ValueLane(int g, int lane, int shift) {
-    const int piece = lane & 7, k0 = lane >> 3;
+    const int piece = ((lane >> 1) & 4) | (lane & 3);
+    k0 = ((lane >> 2) & 1) | ((lane >> 3) & 2);
+    row = raw_row(g * 32 + lane, shift) + (1 << shift);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = raw_row(g * 32 + 16 * h + k0, shift) + (1 << shift);
-      sf[h] = RW_SF + row * 8 + piece;
-      v[h] = RW_CODES + row * 64 + ((((piece >> 1) ^ (row >> 1)) & 3) << 4) + (piece & 1) * 8;
+      const int r = raw_row(g * 32 + 16 * h + k0, shift) + (1 << shift);
+      sf[h] = RW_SF + r * 8 + piece;
+      v[h] = RW_CODES + r * 64 + ((((piece >> 1) ^ (r >> 1)) & 3) << 4) + (piece & 1) * 8;
     }
-    to = (piece >> 2) * HALF_TILE + (g * 32 + k0) * 128 + (((2 * (piece & 3) + (piece >> 2)) ^ k0) << 4);
+    to = (piece >> 2) * HALF_TILE + (g * 32 + k0) * 128 + (((2 * (piece & 3)) ^ k0) << 4);
   }
 };
-__device__ __forceinline__ bool unpack_values(int* status, uint8_t* smem, TreeBars* bar, int g, int lane, uint32_t it, int shift,
+__device__ __forceinline__ void value_out(uint8_t* a0, uint8_t* a1, uint2 c, uint32_t s) {
+  uint32_t f[4], e[4];
+  e2m1x8_f16(c.x, f);
+  e2m1x8_f16(c.y, e);
+  *reinterpret_cast<uint4*>(a0) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
+  *reinterpret_cast<uint4*>(a1) = make_uint4(hmul2(e[0], s), hmul2(e[1], s), hmul2(e[2], s), hmul2(e[3], s));
+}
+__device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int g, int lane, uint32_t it, int shift,
                                               const ValueLane& x, bool& more) {
   const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
   UnitIn u;
-  if (!unit_in(status, bar, it, g, u, more)) return false;
+  if (!unit_in(bar, it, g, u, more)) return false;
   uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
   // a row scale below 2^-100 (unpack_keys): what it is of that
-  const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (raw_row(g * 32 + lane, shift) + (1 << shift)) * 4);
+  const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + x.row * 4);
+  const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + x.row * 8);
   const bool in = ((u.on >> (2 * g + (lane >> 4))) & 1u) && lane < u.left;
   const float less = in && rsv < 0x1p-100f ? rsv * 0x1p100f : 1.f;
-  const bool tiny = __any_sync(0xffffffffu, less != 1.f), whole = __all_sync(0xffffffffu, in);
-  uint2 c[2];
-  uint32_t sv[2];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t at = (h & 1) * 512 + i * 256;
-      c[i] = *reinterpret_cast<const uint2*>(raw + ((h < 2 ? x.v[0] : x.v[1]) ^ (i * 32)) + at);
-      sv[i] = raw[(h < 2 ? x.sf[0] : x.sf[1]) + (at >> 3)];
-    }
-  };
-  load(0);
-  const bool ok = tree_wait(&bar->o_done[buf], ph ^ 1, bar, status);
+  const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
+  const bool odd = __any_sync(0xffffffffu, !in || less != 1.f || sick);
+  const bool ok = tree_wait(&bar->o_done[buf], ph ^ 1);
   if (!__all_sync(0xffffffffu, ok)) return false;
-  const bool upper = lane & 4;
+  uint8_t* out = smem + OFF_V + buf * TILE;
 #pragma unroll 1
-  for (int h = 0; h < 4; ++h) {
-    const uint2 now[2] = {c[0], c[1]};
-    const uint32_t snow[2] = {sv[0], sv[1]};
-    load((h + 1) & 3);
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t v = h ? x.v[1] : x.v[0], sf = h ? x.sf[1] : x.sf[0];
+    uint2 c[4];
+    uint32_t s[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      c[j] = *reinterpret_cast<const uint2*>(raw + (v ^ ((j & 1) * 32)) + j * 256);
+      s[j] = raw[sf + j * 32] * 0x101u;
+    }
+    if (odd) {
+      keep_branch();
       // zeros outside the sequence, and for a scale that is NaN (the key's weights
       // are NaN then)
-      const int k = 8 * h + 4 * i + (lane >> 3);
-      const bool kin = whole || (((u.on >> (2 * g + (h >> 1))) & 1u) && k < u.left);
-      uint32_t s = e4m3x2_f16(kin && (snow[i] & 0x7Fu) != 0x7Fu ? snow[i] * 0x101u : 0u);
-      if (tiny) {
-        keep_branch();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = 16 * h + 4 * j + x.k0;
         const float by = __shfl_sync(0xffffffffu, less, k);
-        s = pack_f16(f16_lo(s) * by, f16_hi(s) * by);
+        const uint32_t t = e4m3x2_f16((s[j] & 0x7Fu) != 0x7Fu ? s[j] : 0u);
+        s[j] = ((u.on >> (2 * g + h)) & 1u) && k < u.left ? pack_f16(f16_lo(t) * by, f16_hi(t) * by) : 0u;
       }
-      uint32_t f[4], e[4];
-      e2m1x8_f16(upper ? now[i].y : now[i].x, f);
-      e2m1x8_f16(upper ? now[i].x : now[i].y, e);
-      const int turn = i * 64;  // of the swizzle
-      uint8_t* a0 = smem + OFF_V + buf * TILE + (x.to ^ turn) + h * 1024 + i * 512;
-      uint8_t* a1 = smem + OFF_V + buf * TILE + (x.to ^ turn ^ 16) + h * 1024 + i * 512;
-      *reinterpret_cast<uint4*>(a0) = make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
-      *reinterpret_cast<uint4*>(a1) = make_uint4(hmul2(e[0], s), hmul2(e[1], s), hmul2(e[2], s), hmul2(e[3], s));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = e4m3x2_f16(s[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t turn = (j & 1) * 64, by = h * 2048 + j * 512;  // of the swizzle
+      value_out(out + (x.to ^ turn) + by, out + (x.to ^ turn ^ 16) + by, c[j], s[j]);
     }
   }
   fence_async_smem();
@@ -610,7 +630,6 @@ __device__ __forceinline__ int tree_columns(int rows) {
 // chunks of 8.  `it` counts the CTA's units.  False: a wait ran out.
 __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t item,
                                              uint32_t& it) {
-  int* const status = a.status;
   const int wg = threadIdx.x >> 7;
   const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const int id = 1 + wg;                 // named barrier
@@ -722,7 +741,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       }
     }
     // (the unpacking is at most three units ahead: no phase of four is missed)
-    ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1, bar, status) && tree_wait(&bar->s_full[buf], ph, bar, status);
+    ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1) && tree_wait(&bar->s_full[buf], ph);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
@@ -762,17 +781,6 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       group_any(id, false);
       return m;
     };
-    if (unset) {  // a reference is missing (an item's first unit)
-      keep_branch();
-      if (group_any(id, !ok)) return false;
-      const float m = row_max();
-      if (mine_unset && m > -INFINITY) {
-        mine_unset = false;
-        nref[tid] = -m;
-      }
-      unset = group_any(id, mine_unset);
-    }
-
     // ---- P', into the place that the product of two units ago has read: it was
     // issued before these scores, so it is done.  Where some weight passes its
     // bound the round is taken back, the reference of that row rises, and a third
@@ -780,11 +788,14 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     uint8_t* at = smem + OFF_P + buf * TILE + tid * 128;
     const uint64_t rk2 = f2_pack(rk, rk), lr2 = f2_pack(lr, lr);
     float add = inv;
+    // Round 0 (an item's first unit, a reference is missing): it is set.  1: the
+    // weights.  2: they are taken back, the reference rises.  3: again.
 #pragma unroll 1
-    for (int round = 0;; ++round) {
+    for (int round = unset ? 0 : 1;; ++round) {
       asm volatile("" : "+r"(round));  // one copy of the code: what misses the instruction cache costs most here
-      const uint64_t in2 = f2_pack(add, add);
       uint32_t top = 0;  // the largest weight, as f16 pairs
+      if (round != 0) {
+      const uint64_t in2 = f2_pack(add, add);
 #pragma unroll
       for (int q = 0; q < NC; q += 8) {
         if (q >= nc) break;
@@ -810,26 +821,28 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         const int to = (col0 + q) >> 3;  // piece of eight rows
         *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
       }
-      if (round == 2) break;
+      }
+      if (round == 3) break;
       // (as numbers: f16 of one sign are ordered as their bits)
-      if (round == 0 && !group_any(id, !ok || max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16)) break;
+      if (round == 1 && !group_any(id, !ok || max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16)) break;
       keep_branch();
-      if (round == 0) {
-        if (group_any(id, !ok)) return false;
+      if (round < 2 && group_any(id, !ok)) return false;
+      if (round == 1) {
         add = -inv;
         continue;
       }
       // l is what it was, to a rounding of what this unit adds; where that passed
       // fp32 the old l is nothing beside it.
       const float m = row_max();
-      const float rise = m > TR_RAISE ? m : 0.f;  // whatever the other rows do
+      const bool first = mine_unset && m > -INFINITY;
+      const float rise = first || (!mine_unset && m > TR_RAISE) ? m : 0.f;  // whatever the other rows do
       if (tid < nc) {
-        red[tid] = exp2_sfu(-rise);
+        red[tid] = first ? 1.f : exp2_sfu(-rise);
         nref[tid] -= rise;
       }
       if (u > u0) {  // O holds something
         const uint32_t p = it - 1;
-        ok = tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
+        ok = tree_wait(&bar->o_done[p & 1], (p >> 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       }
@@ -848,8 +861,10 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         }
         tmem_st_wait();
       }
-      group_any(id, false);  // red is read
+      if (first) mine_unset = false;
+      unset = group_any(id, mine_unset);  // (red is read)
       add = inv;
+      if (round == 0) continue;
     }
     tc_fence_before();
     fence_async_smem();
@@ -862,7 +877,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
 
   // ---- the end: l over the keys, O out of TMEM
   const uint32_t p = it - 1;
-  ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1, bar, status);
+  ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1);
   ok = __all_sync(0xffffffffu, ok);
   if (group_any(id, !ok)) return false;
   // The sums meet in shared memory (a place of P': no product reads it until every
@@ -944,7 +959,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     mbar_init(&bar->o_empty, TR_GROUPS * 4);
     for (int i = 0; i < TR_ITEMS; ++i) mbar_init(&bar->item_full[i], 1);
     mbar_init(&bar->drain, 1);
-    bar->abort = 0;
     bar->seq = a.B;
     bar->before = 0;
     fence_mbar_init();
@@ -1031,14 +1045,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       uint32_t it = 0;
       bool behind = false;
       for (uint32_t item = 0; ok; ++item) {
-        ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
+        ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1);
         ok = !group_any(1 + (warp >> 2), !ok);
         const TreeItem& w = bar->item[item % TR_ITEMS];
         if (!ok || w.rows == 0) break;
         const bool idle = warp >= 4 * tree_groups(w.rows);  // few rows: the other warpgroups have them
         // The item before is done: its products have read Q, and a warpgroup that
         // has no rows is at most one item away from the others.
-        if (item > 0 && (idle || behind)) ok = tree_wait(&bar->o_empty, (item - 1) & 1, bar, a.status);
+        if (item > 0 && (idle || behind)) ok = tree_wait(&bar->o_empty, (item - 1) & 1);
         ok = !group_any(1 + (warp >> 2), !ok);
         if (!ok) break;
         behind = idle;
@@ -1055,13 +1069,13 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       bool more = true;
       const int shift = min(a.c.page_shift, 7), krow = raw_row((warp - TR_KEYS) * 32 + lane, shift);
       for (uint32_t it = 0; ok && more; ++it)
-        ok = unpack_keys(a.status, smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, rs_zero, more) || !more;
+        ok = unpack_keys(smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, rs_zero, more) || !more;
     } else if (warp < TR_COPY_WARP) {
       reg_dec<48>();
       bool more = true;
       const int shift = min(a.c.page_shift, 7);
       const ValueLane x(warp - TR_VALUES, lane, shift);
-      for (uint32_t it = 0; ok && more; ++it) ok = unpack_values(a.status, smem, bar, warp - TR_VALUES, lane, it, shift, x, more) || !more;
+      for (uint32_t it = 0; ok && more; ++it) ok = unpack_values(smem, bar, warp - TR_VALUES, lane, it, shift, x, more) || !more;
     } else {
       reg_dec<48>();
       if (warp == TR_COPY_WARP) {
@@ -1072,7 +1086,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         const uint32_t el = elect_one();
         uint32_t it = 0;
         for (uint32_t item = 0; ok; ++item) {
-          ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1, bar, a.status);
+          ok = tree_wait(&bar->item_full[item % TR_ITEMS], (item / TR_ITEMS) & 1);
           ok = __all_sync(0xffffffffu, ok);
           const TreeItem& w = bar->item[item % TR_ITEMS];
           const int rows = w.rows, n = w.u1 - w.u0;
@@ -1080,14 +1094,14 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
           const int ns = tree_groups(rows) * tree_columns(rows);
           const uint32_t id_s = idesc_f16(128, ns, 0, 0), id_o = idesc_f16(128, (ns + 63) & ~63, 1, 1);
           auto scores = [&](uint32_t i) {
-            return i & 1 ? issue_scores<1>(a.status, smem, bar, tmem, i, id_s, el)
-                         : issue_scores<0>(a.status, smem, bar, tmem, i, id_s, el);
+            return i & 1 ? issue_scores<1>(smem, bar, tmem, i, id_s, el)
+                         : issue_scores<0>(smem, bar, tmem, i, id_s, el);
           };
           auto outputs = [&](uint32_t i, bool head) {
-            return i & 1 ? issue_outputs<1>(a.status, smem, bar, tmem, i, id_o, head, item, el)
-                         : issue_outputs<0>(a.status, smem, bar, tmem, i, id_o, head, item, el);
+            return i & 1 ? issue_outputs<1>(smem, bar, tmem, i, id_o, head, item, el)
+                         : issue_outputs<0>(smem, bar, tmem, i, id_o, head, item, el);
           };
-          ok = tree_wait(&bar->q_full, item & 1, bar, a.status);
+          ok = tree_wait(&bar->q_full, item & 1);
           ok = __all_sync(0xffffffffu, ok) && scores(it);
           for (int j = 0; j < n && ok; ++j, ++it) {
             if (j + 1 < n) ok = scores(it + 1);
@@ -1096,7 +1110,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         }
       }
     }
-    if (!ok) tree_drain(bar, warp, lane);
+    if (!ok) {
+      if (lane == 0) atomicOr(a.status, CODA_DEV_TIMEOUT);
+      tree_drain(bar, warp, lane);
+    }
   }
   tc_fence_before();
   __syncthreads();
