@@ -36,23 +36,28 @@
 // back (the sums with a minus), the reference rises and a second pass follows.
 //
 // Roles: four warpgroups of weights with a quarter of the tile's rows each (their
-// sums fit the 72 registers that 28 warps leave), four warps each for K' and V',
-// one that copies by tensor maps, one that issues the products, two idle.
-// Stages of the cache, scores, K', V' and P' are double or triple, so that all
-// roles work on different units.
+// sums fit the 72 registers that 28 warps leave), two of them with half each for
+// up to 64 rows; four warps each for K' and V', one that copies by tensor maps,
+// one that issues the products, two idle.  Stages of the cache, scores, K', V'
+// and P' are double or triple, so that all roles work on different units.
 //
-// What bounds it: instructions.  A unit of 128 keys takes 2600 to 3600 clocks (at
-// 32 to 128 rows) for 850 of copies and 130 to 510 of products: the roles' code
-// takes turns in the four schedulers and in their instruction caches (two
-// instructions a clock and SM).  What counted most on the way were fewer and
-// shorter code paths: rolled unpacking 268 -> 218 us for 8 trees of 64 nodes
-// over 16384 keys, one copy of the weights' code 299 -> 268, no spilled
-// register 580 -> 321; 32 warps with eight for V' and scores loaded ahead
-// gained 8 % at two long documents and lost 4 to 8 % elsewhere.  Now, in a
-// graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 187 us (floor 45), 24
-// trees of 1 to 64 nodes over 60 to 6000 keys 206 us (44), a chain of 6 over 777
-// keys 20.6 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys 210 us (71), trees
-// of 16 and 11 nodes over 131055 and 100001 keys 169 us (42).
+// What bounds it: instructions, and fetching them.  A unit of 128 keys takes 1900
+// to 3100 clocks (at 32 to 128 rows) for 850 of copies and 130 to 510 of
+// products; the roles' loops take turns in the four schedulers (2.7 instructions a
+// clock and SM) and evict each other from the instruction caches.  So code that is
+// run in every unit counts, and how often:
+//   waits without a clock and a flag in their loops   192 -> 150 us (64 chains)
+//   one copy of what sets and raises a reference      150 -> 140
+//   unpacking rolled, its waits' loads ahead          268 -> 218 (8 trees)
+//   one copy of the weights' code                     299 -> 268
+//   no register spilled                               580 -> 321
+// Two teams of warpgroups for alternate units (126 for 139 us at two long
+// documents) and 32 warps with eight for V' cost more elsewhere than they gained.
+//
+// Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 139 us
+// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 191 us (44), a chain
+// of 6 over 777 keys 20.6 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
+// 188 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 138 us (42).
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -86,16 +91,16 @@ constexpr uint32_t OFF_BAR = OFF_RED + 3072;
 constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
-constexpr int TR_HALF_ROWS = 64;
+constexpr int TR_HALF_ROWS = 64;               // up to here two warpgroups: 64 chains 140 us for 152, long documents 138 for 140
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
 
 // Places of a unit, by the rows of its tile, and of a stretch's ends, whose
-// loads, sums and stores take as long as four to seven units.  Measured, for 24 ragged trees
-// / 64 chains / 8 trees of 64 nodes: 4, 6, 12 245 / 190 / 211 us; 4, 6, 20 237 / 188
-// / 211; 4, 6, 32 244 / 197 / 212; 5, 6, 18 222 / 185 / 211; 5, 6, 24 206 / 187 /
-// 210; 6, 6, 24 208 / 187 / 215.
+// loads, sums and stores take as long as four to seven units.  Measured, for 24
+// ragged trees / 64 chains / 8 trees of 64 nodes: 4, 6, 18 215 / 141 / 190 us; 4, 6,
+// 24 200 / 139 / 189; 4, 6, 30 199 / 142 / 189; 5, 6, 24 191 / 139 / 188; 5, 8, 30 207 /
+// 139 / 190.
 constexpr int TR_COST_FEW = 5, TR_COST_MANY = 6, TR_END = 24;
 
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
@@ -282,10 +287,8 @@ struct TreeBars {
 };
 static_assert(sizeof(TreeBars) <= 1152, "barrier area");
 
-// A wait that gives up after 2^19 tries, for each of which the hardware may
-// suspend the warp for 4 us (2 s in all).  As short as can be: roles wait in every unit, and
-// the code competes for the instruction caches (a clock in it and a flag that
-// others gave up cost 3 % of the whole kernel).
+// A wait that gives up after 2^19 tries, for each of which the hardware suspends
+// the warp for up to 4 us.  As short as can be: every role waits in every unit.
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -579,12 +582,13 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
   if (!__all_sync(0xffffffffu, ok)) return false;
   uint8_t* out = smem + OFF_V + buf * TILE;
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t v = h ? x.v[1] : x.v[0], sf = h ? x.sf[1] : x.sf[0];
-    uint2 c[4];
-    uint32_t s[4];
+  for (int h2 = 0; h2 < 4; ++h2) {
+    const int h = h2 >> 1;
+    const uint32_t v = (h ? x.v[1] : x.v[0]) + (h2 & 1) * 512, sf = (h ? x.sf[1] : x.sf[0]) + (h2 & 1) * 64;
+    uint2 c[2];
+    uint32_t s[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       c[j] = *reinterpret_cast<const uint2*>(raw + (v ^ ((j & 1) * 32)) + j * 256);
       s[j] = raw[sf + j * 32] * 0x101u;
     }
@@ -593,19 +597,19 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
       // zeros outside the sequence, and for a scale that is NaN (the key's weights
       // are NaN then)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = 16 * h + 4 * j + x.k0;
+      for (int j = 0; j < 2; ++j) {
+        const int k = 8 * h2 + 4 * j + x.k0;
         const float by = __shfl_sync(0xffffffffu, less, k);
         const uint32_t t = e4m3x2_f16((s[j] & 0x7Fu) != 0x7Fu ? s[j] : 0u);
         s[j] = ((u.on >> (2 * g + h)) & 1u) && k < u.left ? pack_f16(f16_lo(t) * by, f16_hi(t) * by) : 0u;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = e4m3x2_f16(s[j]);
+      for (int j = 0; j < 2; ++j) s[j] = e4m3x2_f16(s[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t turn = (j & 1) * 64, by = h * 2048 + j * 512;  // of the swizzle
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t turn = j * 64, by = h2 * 1024 + j * 512;  // of the swizzle
       value_out(out + (x.to ^ turn) + by, out + (x.to ^ turn ^ 16) + by, c[j], s[j]);
     }
   }
