@@ -55,9 +55,9 @@
 // documents) and 32 warps with eight for V' cost more elsewhere than they gained.
 //
 // Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 139 us
-// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 191 us (44), a chain
-// of 6 over 777 keys 20.6 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
-// 188 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 138 us (42).
+// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 192 us (44), a chain
+// of 6 over 777 keys 19 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
+// 190 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 134 us (42).
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -1150,19 +1150,29 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeArgs a) {
   const int64_t u0 = a.places[b] + kvh * s.place_kv + tile * (static_cast<int64_t>(s.units) * TR_COST_MANY + TR_END) + TR_END;
   const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + static_cast<int64_t>(s.units - 1) * cost) / per);
   if (c0 == c1) return;  // that CTA wrote the output
+  // The weights a lane each, then the parts in order with four loads in flight:
+  // two long documents (up to 76 parts a row) 138 -> 134 us, a chain of 6 over 777
+  // keys 21 -> 19, 8 trees of 64 nodes 189 -> 190.
+  auto part_of = [&](int x) { return (2ll * x + (x == c0 ? 1 : 0)) * a.part_rows + c; };
   float W = -INFINITY;
-  for (int x = c0; x <= c1; ++x) W = fmaxf(W, a.part_lse[(2ll * x + (x == c0 ? 1 : 0)) * a.part_rows + c]);
+  for (int x = c0 + lane; x <= c1; x += 32) W = fmaxf(W, a.part_lse[part_of(x)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) W = fmaxf(W, __shfl_xor_sync(0xffffffffu, W, o));
   const float W0 = W == -INFINITY ? 0.f : W;
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  for (int x = c0; x <= c1; ++x) {
-    const int64_t p = (2ll * x + (x == c0 ? 1 : 0)) * a.part_rows + c;
-    const float wgt = exp2_sfu(a.part_lse[p] - W0);
-    const float4 v = *reinterpret_cast<const float4*>(a.part + p * 128 + lane * 4);
-    sum += wgt;
-    acc[0] += wgt * v.x;
-    acc[1] += wgt * v.y;
-    acc[2] += wgt * v.z;
-    acc[3] += wgt * v.w;
+  for (int x0 = c0; x0 <= c1; x0 += 32) {
+    const int n = min(32, c1 - x0 + 1);
+    const float mine = lane < n ? exp2_sfu(a.part_lse[part_of(x0 + lane)] - W0) : 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wgt = __shfl_sync(0xffffffffu, mine, i);
+      const float4 v = *reinterpret_cast<const float4*>(a.part + part_of(x0 + i) * 128 + lane * 4);
+      sum += wgt;
+      acc[0] += wgt * v.x;
+      acc[1] += wgt * v.y;
+      acc[2] += wgt * v.z;
+      acc[3] += wgt * v.w;
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *out = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
