@@ -279,8 +279,9 @@ class ServingBlock:
              behind the prefix
 
     Weights without ``gamma_q`` and ``gamma_k`` are of a block without QK-norm:
-    its projection is the plain one, and the append to the cache rotates Q and K
-    on its way (``pairing``, and ``rotary_dim`` elements of each head).
+    its projection is the plain one (``gamma_attn`` folded into the weights when
+    the block is made), and the append to the cache rotates Q and K on its way
+    (``pairing``, and ``rotary_dim`` elements of each head).
     ``scaling`` is rope_table's, for contexts longer than those trained on.
 
     ``ws``, of at least ``workspace_size`` bytes, is the workspace of every call
