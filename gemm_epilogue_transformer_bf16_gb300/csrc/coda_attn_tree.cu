@@ -54,10 +54,10 @@
 // Two teams of warpgroups for alternate units (126 for 139 us at two long
 // documents) and 32 warps with eight for V' cost more elsewhere than they gained.
 //
-// Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 139 us
-// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 192 us (44), a chain
+// Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 138 us
+// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 191 us (44), a chain
 // of 6 over 777 keys 19 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
-// 190 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 134 us (42).
+// 187 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 133 us (42).
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -267,7 +267,7 @@ struct TreeBars {
   TreeCopies copies;
   uint64_t raw_full[TR_STAGES], raw_empty[TR_STAGES];
   uint64_t key_full[4];  // the keys' scales
-  uint64_t k_full[2], v_full[2], s_full[2], s_empty[2], p_full[2], o_done[2];
+  uint64_t k_full[2], v_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t q_full, o_empty, drain;
   uint64_t item_full[TR_ITEMS];
   uint32_t keys_in[TR_STAGES];  // bit i: keys 16 i .. 16 i + 15 of the stage are there; TR_NO_MORE: no unit, nor behind it
@@ -401,14 +401,16 @@ __device__ __forceinline__ bool copy_unit(const TreeArgs& a, const CUtensorMap* 
   return true;
 }
 
-// The scores of unit i, once its keys are unpacked.  The places are constants
+// The scores of unit i, once its keys are unpacked (those of two units ago have
+// been read: the outputs of that unit, issued before, have waited for its weights).
+// The places are constants
 // (BUF is i's parity), so that descriptors stay in uniform registers: with
 // computed ones eight products took twice the time to issue that they run.
 template <int BUF>
 __device__ __forceinline__ bool issue_scores(uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
                                              uint32_t el) {
   const uint32_t ph = (i >> 1) & 1;
-  const bool ok = tree_wait(&bar->k_full[BUF], ph) && tree_wait(&bar->s_empty[BUF], ph ^ 1);
+  const bool ok = tree_wait(&bar->k_full[BUF], ph);
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   const uint32_t q = smem_u32(smem + OFF_Q);
@@ -864,10 +866,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     tc_fence_before();
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive_n(&bar->s_empty[buf], arrive);
-      mbar_arrive_n(&bar->p_full[buf], arrive);
-    }
+    if (lane == 0) mbar_arrive_n(&bar->p_full[buf], arrive);
   }
 
   // ---- the end: l over the keys, O out of TMEM
@@ -946,7 +945,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       mbar_init(&bar->k_full[s], 4);
       mbar_init(&bar->v_full[s], 4);
       mbar_init(&bar->s_full[s], 1);
-      mbar_init(&bar->s_empty[s], TR_GROUPS * 4);
       mbar_init(&bar->p_full[s], TR_GROUPS * 4);
       mbar_init(&bar->o_done[s], 1);
     }
