@@ -967,7 +967,7 @@ def _device(t, name):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.get_device() < 0:
         _where(t, -1, name)
-    return torch.cuda.current_device()
+    return torch._C._cuda_getDevice()  # (a tensor lives on a GPU: the runtime is up)
 
 
 def _arg(t, dtype, shape, dev, name):
@@ -1349,7 +1349,6 @@ def verify_drafts(probs, tokens, cu_seqlens, u, u_next, width, parents=None, dra
     they were not drawn.  Returns count [batch], nodes and tokens [batch, width]:
     node 0 and the accepted ones, their tokens and the next, -1 behind.  Without
     `ws`, result["ws"] holds the status word."""
-    lib = load()
     dev = _device(probs, "probs")
     if probs.dim() != 2 or probs.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"probs: expected [T, V] in torch.float32 or torch.bfloat16, got {tuple(probs.shape)} {probs.dtype}")
@@ -1365,8 +1364,8 @@ def verify_drafts(probs, tokens, cu_seqlens, u, u_next, width, parents=None, dra
                for k, s in (("count", (batch,)), ("nodes", (batch, width)), ("tokens", (batch, width)))}
     to = (_arg(out["count"], torch.int32, (batch,), dev, "count"), _arg(out["nodes"], torch.int32, (batch, width), dev, "nodes"),
           _arg(out["tokens"], torch.int32, (batch, width), dev, "tokens out"))
-    w, nw, made = _scratch(ws, lib.coda_verify_drafts_workspace_size(T, batch, V), dev, stream)
-    _check("coda_verify_drafts", lib.coda_verify_drafts(p, q, F32 if probs.dtype is torch.float32 else BF16, V, x, cu, up, *uu,
+    w, nw, made = _scratch(ws, 256, dev, stream)
+    _check("coda_verify_drafts", load().coda_verify_drafts(p, q, F32 if probs.dtype is torch.float32 else BF16, V, x, cu, up, *uu,
                                                         T, batch, width, *to, w, nw, _on_stream(stream, dev)))
     return _told(out, ws, made)
 
