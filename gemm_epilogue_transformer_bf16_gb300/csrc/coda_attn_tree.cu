@@ -266,7 +266,6 @@ struct TreeBars {
   TreeItem item[TR_ITEMS];
   TreeCopies copies;
   uint64_t raw_full[TR_STAGES], raw_empty[TR_STAGES];
-  uint64_t key_full[4];  // the keys' scales
   uint64_t k_full[2], v_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t q_full, o_empty, drain;
   uint64_t item_full[TR_ITEMS];
@@ -419,6 +418,7 @@ __device__ __forceinline__ bool issue_scores(uint8_t* smem, TreeBars* bar, uint3
     umma_bf16_ts(tmem + COL_S + BUF * 128, tmem + COL_K + BUF * 64 + x * 8,
                  sdesc_sw128(q + (x >> 2) * HALF_TILE + (x & 3) * 32, 16, 1024), id, x > 0, el);
   umma_commit(&bar->s_full[BUF], el);
+  if (el) mbar_arrive(&bar->s_full[BUF]);
   return true;
 }
 // O^T += V'^T P'^T of unit i; first: of an item, whose predecessor's O has left.
@@ -523,7 +523,6 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   tc_fence_before();
   __syncwarp();
   if (lane == 0) {
-    mbar_arrive(&bar->key_full[it & 3]);
     mbar_arrive(&bar->k_full[buf]);
     mbar_arrive(&bar->raw_empty[st]);
   }
@@ -737,8 +736,9 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         sees = from <= 0 ? ~0u : from >= 32 ? 0 : ~0u << from;
       }
     }
-    // (the unpacking is at most three units ahead: no phase of four is missed)
-    ok = ok && tree_wait(&bar->key_full[it & 3], (it >> 2) & 1) && tree_wait(&bar->s_full[buf], ph);
+    // the scores, and through the warp that issued them the keys' scales (the
+    // unpacking is at most three units ahead: none of four places is lost)
+    ok = ok && tree_wait(&bar->s_full[buf], ph);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
@@ -940,11 +940,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       mbar_init(&bar->raw_full[s], 1);
       mbar_init(&bar->raw_empty[s], 8);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(&bar->key_full[s], 4);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->k_full[s], 4);
       mbar_init(&bar->v_full[s], 4);
-      mbar_init(&bar->s_full[s], 1);
+      mbar_init(&bar->s_full[s], 2);  // the products, and who issued them having seen the keys' scales
       mbar_init(&bar->p_full[s], TR_GROUPS * 4);
       mbar_init(&bar->o_done[s], 1);
     }
