@@ -266,7 +266,7 @@ struct TreeBars {
   TreeItem item[TR_ITEMS];
   TreeCopies copies;
   uint64_t raw_full[TR_STAGES], raw_empty[TR_STAGES];
-  uint64_t k_full[2], v_full[2], s_full[2], p_full[2], o_done[2];
+  uint64_t k_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t q_full, o_empty, drain;
   uint64_t item_full[TR_ITEMS];
   uint32_t keys_in[TR_STAGES];  // bit i: keys 16 i .. 16 i + 15 of the stage are there; TR_NO_MORE: no unit, nor behind it
@@ -426,8 +426,7 @@ template <int BUF>
 __device__ __forceinline__ bool issue_outputs(uint8_t* smem, TreeBars* bar, uint32_t tmem, uint32_t i, uint32_t id,
                                               bool first, uint32_t item, uint32_t el) {
   const uint32_t ph = (i >> 1) & 1;
-  const bool ok = tree_wait(&bar->p_full[BUF], ph) && tree_wait(&bar->v_full[BUF], ph) &&
-                  (!first || tree_wait(&bar->o_empty, (item & 1) ^ 1));
+  const bool ok = tree_wait(&bar->p_full[BUF], ph) && (!first || tree_wait(&bar->o_empty, (item & 1) ^ 1));
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   const uint32_t v = smem_u32(smem + OFF_V + BUF * TILE), p = smem_u32(smem + OFF_P + BUF * TILE);
@@ -608,7 +607,7 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
   fence_async_smem();
   __syncwarp();
   if (lane == 0) {
-    mbar_arrive(&bar->v_full[buf]);
+    mbar_arrive(&bar->p_full[buf]);
     mbar_arrive(&bar->raw_empty[st]);
   }
   return true;
@@ -618,8 +617,8 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
 // chunks of 8.
 __device__ __forceinline__ int tree_groups(int rows) { return rows <= TR_HALF_ROWS ? 2 : TR_GROUPS; }
 __device__ __forceinline__ int tree_columns(int rows) {
-  const int per = 8 * tree_groups(rows);
-  return (rows + per - 1) / per * 8;
+  const int per = 16 * tree_groups(rows);
+  return (rows + per - 1) / per * 16;
 }
 
 // A warpgroup's part of one stretch: the weights of nc columns of the tile, in
@@ -795,7 +794,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       const uint64_t in2 = f2_pack(add, add);
 #pragma unroll
       for (int q = 0; q < NC; q += 8) {
-        if (q >= nc) break;
+        if (q == 16 && nc == 16) break;
         uint32_t s[8];
         tmem_ldn(tS + q, s);
         uint32_t p[4];
@@ -942,9 +941,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar->k_full[s], 4);
-      mbar_init(&bar->v_full[s], 4);
       mbar_init(&bar->s_full[s], 2);  // the products, and who issued them having seen the keys' scales
-      mbar_init(&bar->p_full[s], TR_GROUPS * 4);
+      mbar_init(&bar->p_full[s], TR_GROUPS * 4 + 4);  // weights and values
       mbar_init(&bar->o_done[s], 1);
     }
     mbar_init(&bar->q_full, TR_GROUPS * 4);
