@@ -460,22 +460,21 @@ struct UnitIn {
 __device__ __forceinline__ bool unit_in(TreeBars* bar, uint32_t it, int g, UnitIn& x, bool& more) {
   const uint32_t st = it % TR_STAGES;
   const bool ok = tree_wait(&bar->raw_full[st], (it / TR_STAGES) & 1);
-  if (!__all_sync(0xffffffffu, ok)) return false;
   x.on = bar->keys_in[st];
   x.left = bar->left[st] - 32 * g;
-  more = x.on != TR_NO_MORE;
-  return more;
+  more = __all_sync(0xffffffffu, ok && x.on != TR_NO_MORE);
+  return ok;
 }
 
 // K' of unit `it` by four warps, a thread per key, to the lane of TMEM that is
-// its row, and the key's scales.  False: a wait ran out, or no unit (`more`) is
+// its row, and the key's scales.  False: a wait ran out; without `more`, no unit was
 // left.  (Rolled, as below: warps of all roles share a scheduler, and their
 // straight-line code does not fit its instruction cache together.)
 __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane,
                                             uint32_t it, int shift, int krow, uint32_t& rs_zero, bool& more) {
   const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
   UnitIn x;
-  if (!unit_in(bar, it, g, x, more)) return false;
+  const bool here = unit_in(bar, it, g, x, more);
   const uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
   const bool in = ((x.on >> (2 * g + (lane >> 4))) & 1u) && lane < x.left;  // else whatever the stage held before
   const uint2 sfk = *reinterpret_cast<const uint2*>(raw + RW_SF + krow * 8);
@@ -484,7 +483,8 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + (krow + (1 << shift)) * 4);
   const uint8_t* kc = raw + RW_CODES + krow * 64;
   uint4 v = *reinterpret_cast<const uint4*>(kc + (((krow >> 1) & 3) << 4));
-  bool ok = tree_wait(&bar->s_full[buf], ph ^ 1);  // the scores of two units ago have read K'
+  if (!more) return here;
+  const bool ok = tree_wait(&bar->s_full[buf], ph ^ 1);  // the scores of two units ago have read K'
   if (!__all_sync(0xffffffffu, ok)) return false;
   tc_fence_after();
   uint64_t sf8 = in ? static_cast<uint64_t>(sfk.y) << 32 | sfk.x : 0;
@@ -560,7 +560,7 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
                                               const ValueLane& x, bool& more) {
   const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
   UnitIn u;
-  if (!unit_in(bar, it, g, u, more)) return false;
+  const bool here = unit_in(bar, it, g, u, more);
   uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
   // a row scale below 2^-100 (unpack_keys): what it is of that
   const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + x.row * 4);
@@ -569,6 +569,7 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
   const float less = in && rsv < 0x1p-100f ? rsv * 0x1p100f : 1.f;
   const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
   const bool odd = __any_sync(0xffffffffu, !in || less != 1.f || sick);
+  if (!more) return here;
   const bool ok = tree_wait(&bar->o_done[buf], ph ^ 1);
   if (!__all_sync(0xffffffffu, ok)) return false;
   uint8_t* out = smem + OFF_V + buf * TILE;
@@ -724,7 +725,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     // rows that see this key, where it is a node (or none of the sequence)
     const int d = u * TR_UNIT + tid - prefix;
     uint32_t sees = ~0u;
-    if ((u + 1) * TR_UNIT > prefix && d >= 0) {
+    if (d >= 0) {
       keep_branch();
       if (d >= nodes) {
         sees = 0;
@@ -1059,13 +1060,13 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       bool more = true;
       const int shift = min(a.c.page_shift, 7), krow = raw_row((warp - TR_KEYS) * 32 + lane, shift);
       for (uint32_t it = 0; ok && more; ++it)
-        ok = unpack_keys(smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, rs_zero, more) || !more;
+        ok = unpack_keys(smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, rs_zero, more);
     } else if (warp < TR_COPY_WARP) {
       reg_dec<48>();
       bool more = true;
       const int shift = min(a.c.page_shift, 7);
       const ValueLane x(warp - TR_VALUES, lane, shift);
-      for (uint32_t it = 0; ok && more; ++it) ok = unpack_values(smem, bar, warp - TR_VALUES, lane, it, shift, x, more) || !more;
+      for (uint32_t it = 0; ok && more; ++it) ok = unpack_values(smem, bar, warp - TR_VALUES, lane, it, shift, x, more);
     } else {
       reg_dec<48>();
       if (warp == TR_COPY_WARP) {
