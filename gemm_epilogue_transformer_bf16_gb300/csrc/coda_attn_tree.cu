@@ -42,22 +42,26 @@
 // and P' are double or triple, so that all roles work on different units.
 //
 // What bounds it: instructions, and fetching them.  A unit of 128 keys takes 1900
-// to 3100 clocks (at 32 to 128 rows) for 850 of copies and 130 to 510 of
+// to 2900 clocks (at 32 to 128 rows) for 850 of copies and 130 to 510 of
 // products; the roles' loops take turns in the four schedulers (2.7 instructions a
 // clock and SM) and evict each other from the instruction caches.  So code that is
 // run in every unit counts, and how often:
 //   waits without a clock and a flag in their loops   192 -> 150 us (64 chains)
 //   one copy of what sets and raises a reference      150 -> 140
+//   columns in sixteens (a branch for four)           184 -> 178 (8 trees)
+//   one barrier for scores and scales, one for scores
+//   read and weights written                          190 -> 184
 //   unpacking rolled, its waits' loads ahead          268 -> 218 (8 trees)
 //   one copy of the weights' code                     299 -> 268
 //   no register spilled                               580 -> 321
 // Two teams of warpgroups for alternate units (126 for 139 us at two long
-// documents) and 32 warps with eight for V' cost more elsewhere than they gained.
+// documents) and 32 warps with eight for V' cost more elsewhere than they gained;
+// the next item's Q in front of an item's end gained nothing.
 //
-// Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 138 us
-// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 191 us (44), a chain
+// Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 136 us
+// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 185 us (44), a chain
 // of 6 over 777 keys 19 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
-// 187 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 133 us (42).
+// 177 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 125 us (42).
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -87,7 +91,7 @@ constexpr uint32_t OFF_Q = 0, OFF_P = TILE, OFF_V = 3 * TILE, OFF_RAW = 5 * TILE
 constexpr uint32_t OFF_ROW = OFF_RAW + TR_STAGES * TR_RAW;  // [2][128] minus the rows' references, by item
 constexpr uint32_t OFF_KEY = OFF_ROW + 1024;                // [4][128] row scale of the key, log2 of the value's
 constexpr uint32_t OFF_RED = OFF_KEY + 4096;                // [4][192] exchange of a warpgroup
-constexpr uint32_t OFF_BAR = OFF_RED + 3072;
+constexpr uint32_t OFF_BAR = OFF_RED + TR_GROUPS * 192 * 4;
 constexpr uint32_t TR_SMEM = 896 + OFF_BAR + 1152;
 static_assert(TR_SMEM <= 232448, "shared memory per CTA");
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_K = 384;  // TMEM columns: S twice, O, K' twice (64 each)
@@ -614,8 +618,8 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
   return true;
 }
 
-// Warpgroups that share a tile's rows, and the columns that each takes: whole
-// chunks of 8.
+// Warpgroups that share a tile's rows, and the columns that each takes, in
+// sixteens: 16 or 32.
 __device__ __forceinline__ int tree_groups(int rows) { return rows <= TR_HALF_ROWS ? 2 : TR_GROUPS; }
 __device__ __forceinline__ int tree_columns(int rows) {
   const int per = 16 * tree_groups(rows);
@@ -792,32 +796,32 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       asm volatile("" : "+r"(round));  // one copy of the code: what misses the instruction cache costs most here
       uint32_t top = 0;  // the largest weight, as f16 pairs
       if (round != 0) {
-      const uint64_t in2 = f2_pack(add, add);
+        const uint64_t in2 = f2_pack(add, add);
 #pragma unroll
-      for (int q = 0; q < NC; q += 8) {
-        if (q == 16 && nc == 16) break;
-        uint32_t s[8];
-        tmem_ldn(tS + q, s);
-        uint32_t p[4];
+        for (int q = 0; q < NC; q += 8) {
+          if (q == 16 && nc == 16) break;
+          uint32_t s[8];
+          tmem_ldn(tS + q, s);
+          uint32_t p[4];
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-          const float4 n = *reinterpret_cast<const float4*>(nref + q + k);
-          float x[4];
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), rk2, f2_add(lr2, f2_pack(n.x, n.y))), x[0],
-                    x[1]);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), rk2, f2_add(lr2, f2_pack(n.z, n.w))),
-                    x[2], x[3]);
+          for (int k = 0; k < 8; k += 4) {
+            const float4 n = *reinterpret_cast<const float4*>(nref + q + k);
+            float x[4];
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), rk2, f2_add(lr2, f2_pack(n.x, n.y))), x[0],
+                      x[1]);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), rk2, f2_add(lr2, f2_pack(n.z, n.w))),
+                      x[2], x[3]);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) x[h] = exp2_sfu(x[h]);
-          f2_unpack(f2_fma(f2_pack(x[0], x[1]), in2, f2_pack(l[q + k], l[q + k + 1])), l[q + k], l[q + k + 1]);
-          f2_unpack(f2_fma(f2_pack(x[2], x[3]), in2, f2_pack(l[q + k + 2], l[q + k + 3])), l[q + k + 2], l[q + k + 3]);
-          p[k / 2] = pack_f16(x[0], x[1]);
-          p[k / 2 + 1] = pack_f16(x[2], x[3]);
+            for (int h = 0; h < 4; ++h) x[h] = exp2_sfu(x[h]);
+            f2_unpack(f2_fma(f2_pack(x[0], x[1]), in2, f2_pack(l[q + k], l[q + k + 1])), l[q + k], l[q + k + 1]);
+            f2_unpack(f2_fma(f2_pack(x[2], x[3]), in2, f2_pack(l[q + k + 2], l[q + k + 3])), l[q + k + 2], l[q + k + 3]);
+            p[k / 2] = pack_f16(x[0], x[1]);
+            p[k / 2 + 1] = pack_f16(x[2], x[3]);
+          }
+          top = hmax2(top, hmax2(hmax2(p[0], p[1]), hmax2(p[2], p[3])));
+          const int to = (col0 + q) >> 3;  // piece of eight rows
+          *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
         }
-        top = hmax2(top, hmax2(hmax2(p[0], p[1]), hmax2(p[2], p[3])));
-        const int to = (col0 + q) >> 3;  // piece of eight rows
-        *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
-      }
       }
       if (round == 3) break;
       // (as numbers: f16 of one sign are ordered as their bits)
