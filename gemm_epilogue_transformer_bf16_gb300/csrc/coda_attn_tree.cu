@@ -43,7 +43,7 @@
 //
 // What bounds it: instructions, and fetching them.  A unit of 128 keys takes 1900
 // to 2900 clocks (at 32 to 128 rows) for 850 of copies and 130 to 510 of
-// products; the roles' loops take turns in the four schedulers (2.7 instructions a
+// products; the roles' loops take turns in the four schedulers (2.95 instructions a
 // clock and SM) and evict each other from the instruction caches.  So code that is
 // run in every unit counts, and how often:
 //   waits without a clock and a flag in their loops   192 -> 150 us (64 chains)
