@@ -692,7 +692,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   if (tid < nc) nref[tid] = 0.f;  // no reference yet
   fence_async_smem();
   __syncwarp();
-  if (lane == 0) mbar_arrive_n(&bar->q_full, arrive);
+  if (lane == 0) mbar_arrive(&bar->q_full);  // (and that the item before is read: its end's place is P' now)
 
   // ---- what each row sees of its tree
   const int prefix = w.len - w.n;  // keys that every row sees
@@ -878,8 +878,9 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   ok = ok && tree_wait(&bar->o_done[p & 1], (p >> 1) & 1);
   ok = __all_sync(0xffffffffu, ok);
   if (group_any(id, !ok)) return false;
-  // The sums meet in shared memory (a place of P': no product reads it until every
-  // warp has its next rows): thread t's, 16 bytes at piece c / 4 ^ (t & 7).
+  // The sums meet in shared memory (a place of P': no score of the next item is
+  // issued, so no weight written, before all sixteen warps have arrived there, with
+  // rows or without): thread t's, 16 bytes at piece c / 4 ^ (t & 7).
   float* box = reinterpret_cast<float*>(smem + OFF_P + wg * HALF_TILE);
 #pragma unroll
   for (int c = 0; c < NC; c += 4)
@@ -1045,15 +1046,19 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         const TreeItem& w = bar->item[item % TR_ITEMS];
         if (!ok || w.rows == 0) break;
         const bool idle = warp >= 4 * tree_groups(w.rows);  // few rows: the other warpgroups have them
-        // The item before is done: its products have read Q, and a warpgroup that
-        // has no rows is at most one item away from the others.
+        // The item before is done: its products have read Q, every warpgroup has
+        // read what its end left in P', and one that has no rows is at most one item
+        // away from the others.
         if (item > 0 && (idle || behind)) ok = tree_wait(&bar->o_empty, (item - 1) & 1);
         ok = !group_any(1 + (warp >> 2), !ok);
         if (!ok) break;
         behind = idle;
         if (idle) {
           it += w.u1 - w.u0;
-          if (lane == 0) mbar_arrive(&bar->o_empty);
+          if (lane == 0) {
+            mbar_arrive(&bar->q_full);
+            mbar_arrive(&bar->o_empty);
+          }
           continue;
         }
         ok = tree_softmax(a, smem, bar, tmem, item, it);
