@@ -144,6 +144,12 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
   asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -519,8 +525,9 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
   float2 meta;
   meta.x = !in ? 0.f : poison ? 1.f : rsk;
-  // below 2^-100 the sum l would pass fp32's end: V' takes the rest
-  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : rs < 0x1p-100f ? -100.f : log2f(rs);
+  // below 2^-90 the sum l would pass fp32's end (2^10 / 2^-90 for a key, up to 2^26
+  // of them): V' takes the rest
+  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : rs < 0x1p-90f ? -90.f : log2f(rs);
   *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
   tmem_st_wait();
   tc_fence_before();
@@ -566,11 +573,11 @@ __device__ __forceinline__ bool unpack_values(uint8_t* smem, TreeBars* bar, int 
   UnitIn u;
   const bool here = unit_in(bar, it, g, u, more);
   uint8_t* raw = smem + OFF_RAW + st * TR_RAW;
-  // a row scale below 2^-100 (unpack_keys): what it is of that
+  // a row scale below 2^-90 (unpack_keys): what it is of that
   const float rsv = *reinterpret_cast<const float*>(raw + RW_RS + x.row * 4);
   const uint2 sfv = *reinterpret_cast<const uint2*>(raw + RW_SF + x.row * 8);
   const bool in = ((u.on >> (2 * g + (lane >> 4))) & 1u) && lane < u.left;
-  const float less = in && rsv < 0x1p-100f ? rsv * 0x1p100f : 1.f;
+  const float less = in && rsv < 0x1p-90f ? rsv * 0x1p90f : 1.f;
   const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
   const bool odd = __any_sync(0xffffffffu, !in || less != 1.f || sick);
   if (!more) return here;
@@ -830,15 +837,21 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       if (round < 2 && group_any(id, !ok)) return false;
       if (round == 1) {
         add = -inv;
+        // A sum that passed fp32 cannot be taken back: it is marked.
+#pragma unroll
+        for (int c = 0; c < NC; ++c) l[c] = l[c] == INFINITY ? -INFINITY : l[c];
         continue;
       }
-      // l is what it was, to a rounding of what this unit adds; where that passed
-      // fp32 the old l is nothing beside it.
+      // l is what it was, to a rounding of what this unit adds.  Where that passed
+      // fp32, 2^t / rs_v >= 2^128, the old l is dropped: a unit left it 2^10 / 2^-90 at
+      // most, 2^-28 of what this one leaves once r has risen by t or more.  Elsewhere
+      // it falls by 2^-rise in two steps: values much smaller than the ones that raise
+      // r make it so large that one step would leave nothing.  NaN stays NaN.
       const float m = row_max();
       const bool first = mine_unset && m > -INFINITY;
       const float rise = first || (!mine_unset && m > TR_RAISE) ? m : 0.f;  // whatever the other rows do
       if (tid < nc) {
-        red[tid] = first ? 1.f : exp2_sfu(-rise);
+        red[tid] = first ? 1.f : exp2_sfu(-0.5f * rise);
         nref[tid] -= rise;
       }
       if (u > u0) {  // O holds something
@@ -850,14 +863,14 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       group_any(id, false);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        if (c < nc) l[c] = red[c] < 0x1p-100f ? 0.f : l[c] * red[c];
+        if (c < nc) l[c] = max_nan(l[c], 0.f) * red[c] * red[c];
       if (u > u0 && ok) {
 #pragma unroll 1
         for (int q = 0; q < nc; q += 8) {
           uint32_t o[8];
           tmem_ldn(tO + q, o);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * red[q + i]);
+          for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * red[q + i] * red[q + i]);
           tmem_st8(tO + q, o);
         }
         tmem_st_wait();

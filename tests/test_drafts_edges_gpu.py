@@ -9,7 +9,7 @@ import synth
 from oracle import coda_oracle as O
 from parity import to_np
 from test_drafts_gpu import D, DEV, check_tree, grow, i32, offsets
-from test_kvcache_gpu import fill
+from test_kvcache_gpu import fill, oracle_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,82 @@ def test_many_rows_then_few_unit_by_unit(coda):
         assert all(torch.equal(out[k], first[k]) for k in first)
     assert coda.get_status(ws) == 0
     check_tree(first, to_np(Q), lens, nodes, trees, kval, vval, vs, n_q, n_kv, D ** -0.5)
+
+
+def attend(coda, K, V, Q, lens, n, n_q, n_kv=1, page=64, seed=1):
+    """Chains of n nodes behind rows K, V [sum(lens), n_kv * D], checked; K, V, Q as
+    floats.  A row of zeros has no size."""
+    K, V, Q = (x.to(torch.bfloat16) for x in (K, V, Q))
+    need = [-(-x // page) for x in lens]
+    cache = coda.kv_cache_nvfp4(sum(need), page, n_kv)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    slots, at = [], 0
+    for b, x in enumerate(lens):
+        table[b, :need[b]] = order[at:at + need[b]]
+        j = torch.arange(x)
+        slots.append(table[b][j // page] * page + j.to(torch.int32) % page)
+        at += need[b]
+    ws = coda.workspace(coda.load().coda_attention_tree_nvfp4_workspace_size(n * len(lens), len(lens), n_q, n_kv, D))
+    coda.kv_append_nvfp4(K.to(DEV), V.to(DEV), torch.cat(slots).to(DEV), cache, ws=ws)
+    out = coda.attention_tree_nvfp4(Q.to(DEV), cache, table.to(DEV), i32(lens), offsets([n] * len(lens)), n_q, ws=ws)
+    assert coda.get_status(ws) == 0
+    (_, _, _, kv), (_, _, sc, vv) = oracle_rows(K, n_kv), oracle_rows(V, n_kv)
+    sc = np.where(np.abs(vv).reshape(*sc.shape, D).max(axis=2) == 0, 2.0 ** -100, sc)
+    cut = np.cumsum([0] + lens)
+    part = lambda x: [x[a:b] for a, b in zip(cut, cut[1:])]
+    check_tree(out, to_np(Q), lens, [n] * len(lens), [[i - 1 for i in range(n)]] * len(lens), part(kv), part(vv), part(sc), n_q,
+               n_kv, D ** -0.5)
+
+
+def sizes(batch, keys):
+    """Sequences of about that length, one of them long enough to be cut."""
+    return [keys + i % 7 for i in range(batch)] + ([40 * keys] if batch > 1 else [])
+
+
+# sequences (a CTA has whole ones of many, and parts of one), exponents of the values
+# before the last keys and in them, by how much their scores (base 2) lie above
+JUMPS = [(-50, -50, 80), (0, -30, 125), (0, -30, 100), (-90, -90, 30), (-60, -60, 60), (-100, 15, 0), (-90, 20, -20), (30, -80, 95),
+         (0, 0, 140), (0, 0, 300)]
+
+
+@pytest.mark.parametrize("batch", [1, 330])
+@pytest.mark.parametrize("before, behind, jump", JUMPS, ids=str)
+def test_scores_that_jump_at_values_of_other_sizes(coda, batch, before, behind, jump):
+    """The first weights against a reference are far too large, and what they add is
+    taken back: the sums before them count as far as they did."""
+    n_q, n = 4, 3
+    lens = sizes(batch, 390)
+    K, V = synth.randn_bf16((sum(lens), D), 0.5, 1).float(), synth.randn_bf16((sum(lens), D), 1.0, 2).float()
+    Q = synth.randn_bf16((n * len(lens), n_q * D), 0.1, 3).float()
+    Q.view(-1, n_q, D)[..., :64] = 1.0
+    at = 0
+    for x in lens:
+        late = torch.arange(x) >= 0.7 * x
+        late &= torch.arange(x) % 5 < 2
+        V[at:at + x] *= torch.where(late, 2.0 ** behind, 2.0 ** before).unsqueeze(1)
+        K[at:at + x, :64] = torch.where(late, jump * 0.6931 / (64 * D ** -0.5), 0.0).unsqueeze(1)
+        at += x
+    attend(coda, K, V, Q, lens, n, n_q)
+
+
+def test_a_key_that_is_not_finite_stays_in_sums_that_pass_fp32(coda):
+    n_q, n, page, keys, batch = 4, 3, 64, 390, 330
+    lens = [keys] * batch
+    cache, table, *_ = fill(coda, lens, page, 1, False)
+    K, V = synth.randn_bf16((keys, D), 0.5, 1).float(), synth.randn_bf16((keys, D), 2.0 ** -60, 2)
+    K[:, :64] = 0
+    K[300:, :64] = 60 * 0.6931 / (64 * D ** -0.5)
+    K = K.to(torch.bfloat16).to(DEV)
+    j = torch.arange(keys)
+    for b in range(batch):
+        slots = table[b][j // page] * page + j.to(torch.int32) % page
+        coda.kv_append_nvfp4(K, V.to(DEV), slots.to(DEV), cache)
+        if b % 2:
+            cache["scale"].view(-1, 2, page)[int(slots[5]) // page, b // 2 % 2, int(slots[5]) % page] = float("nan")
+    Q = synth.randn_bf16((n * batch, n_q * D), 0.1, 3).float()
+    Q.view(-1, n_q, D)[..., :64] = 1.0
+    out = coda.attention_tree_nvfp4(Q.to(torch.bfloat16).to(DEV), cache, table.to(DEV), i32(lens), offsets([n] * batch), n_q)
+    sick = (torch.arange(batch) % 2 == 1).repeat_interleave(n).to(DEV)
+    assert torch.isnan(out["lse"][sick]).all() and torch.isnan(out["O"][sick].float()).all()
+    assert torch.isfinite(out["lse"][~sick]).all() and torch.isfinite(out["O"][~sick].float()).all()
