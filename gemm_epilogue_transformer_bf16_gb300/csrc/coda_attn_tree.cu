@@ -34,6 +34,9 @@
 // own says nothing.  l, r and O are fp32.  Weights are computed and summed in one
 // pass over the scores; where one turns out to pass the bound the pass is taken
 // back (the sums with a minus), the reference rises and a second pass follows.
+// A 2^t below fp32's least may count in l where its value is much smaller than
+// others: units with row scales outside 2^-50 to 2^30 are treated as those whose
+// bound is passed, and what was lost is added in a third pass.
 //
 // Roles: four warpgroups of weights with a quarter of the tile's rows each (their
 // sums fit the 72 registers that 28 warps leave), two of them with half each for
@@ -99,6 +102,11 @@ constexpr int TR_HALF_ROWS = 64;               // up to here two warpgroups: 64 
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
+// Row scales of values between 2^-50 and 2^30 differ so little that a weight below
+// fp32's least, 2^-126, is at most 2^-46 of its row's sum; the sign of a key's scale
+// tells of others (TR_ODD), with which what is lost is looked for.
+constexpr float TR_LOW = -50.f, TR_HIGH = 30.f;
+constexpr uint32_t TR_ODD = 0x80000000u;
 
 // Places of a unit, by the rows of its tile, and of a stretch's ends, whose
 // loads, sums and stores take as long as four to seven units.  Measured, for 24
@@ -524,10 +532,12 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   // do not see it stay clear of it
   const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
   float2 meta;
-  meta.x = !in ? 0.f : poison ? 1.f : rsk;
+  const float log_rs = rs < 0x1p-90f ? -90.f : log2f(rs);
+  const bool odd = log_rs < TR_LOW || log_rs > TR_HIGH;
+  meta.x = !in ? 0.f : poison ? 1.f : odd ? -rsk : rsk;
   // below 2^-90 the sum l would pass fp32's end (2^10 / 2^-90 for a key, up to 2^26
   // of them): V' takes the rest
-  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : rs < 0x1p-90f ? -90.f : log2f(rs);
+  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : log_rs;
   *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
   tmem_st_wait();
   tc_fence_before();
@@ -729,6 +739,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   for (int c = 0; c < NC; ++c) l[c] = 0.f;
   bool unset = true;        // some column has no reference
   bool mine_unset = tid < nc;  // column tid
+  uint32_t high = 0;        // TR_ODD: a key of this thread had a row scale beyond 2^30
   const int u0 = w.u0, u1 = w.u1, nodes = w.n, group = a.group;
 
   for (int u = u0; u < u1; ++u, ++it) {
@@ -756,7 +767,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     const bool there = key.y != -INFINITY, poison = key.y != key.y;
     const float lr = poison ? 0.f : key.y;
     const float inv = there ? exp2_sfu(-lr) : 0.f;  // finite: it meets zero weights too
-    const float rk = there ? fmaxf(key.x * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
+    const float rk = there ? fmaxf(fabsf(key.x) * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
     const uint32_t tS = tmem + lanes + COL_S + buf * 128 + col0, tO = tmem + lanes + COL_O + col0;
     if (__any_sync(0xffffffffu, sees != ~0u || poison)) {  // scores that do not count become -inf where they lie
       keep_branch();
@@ -771,6 +782,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       }
       tmem_st_wait();
     }
+    const uint32_t odd = high | (__float_as_uint(key.x) & TR_ODD);
+    bool lost = false;  // some weights may be below 2^-126 and count in the sum all the same
     // The largest exponent of each row over this unit's keys, to column tid.
     auto row_max = [&]() {
 #pragma unroll 1
@@ -783,7 +796,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         const float most = warp_columns<8, false>(v, lane);
         if (lane < 8) red[warp * 32 + q + lane] = most;
       }
-      group_any(id, false);
+      lost = group_any(id, odd != 0);
       float m = -INFINITY;
       if (tid < nc) m = fmaxf(fmaxf(red[tid], red[32 + tid]), fmaxf(red[64 + tid], red[96 + tid]));
       group_any(id, false);
@@ -830,9 +843,31 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
           *reinterpret_cast<uint4*>(at + (to >> 3) * HALF_TILE + (((to ^ tid) & 7) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
         }
       }
-      if (round == 3) break;
+      if (round == 3) {
+        if (!lost) break;
+        keep_branch();
+        // 2^t / rs_v = 2^(s - r), where 2^t was nothing.  (Rolled, l turning by eight
+        // columns: little code, and nothing spilled.)
+        const float below = there ? exp2_sfu(-126.f - lr) : 0.f;
+#pragma unroll 1
+        for (int q = 0; q < NC; q += 8) {
+          uint32_t s[8];
+          tmem_ldn(tS + q, s);
+          float next[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float y = exp2_sfu(fmaf(__uint_as_float(s[k]), rk, nref[q + k]));
+            next[k] = l[k] + (y < below ? y : 0.f);
+          }
+#pragma unroll
+          for (int k = 0; k < NC - 8; ++k) l[k] = l[k + 8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) l[NC - 8 + k] = next[k];
+        }
+        break;
+      }
       // (as numbers: f16 of one sign are ordered as their bits)
-      if (round == 1 && !group_any(id, !ok || max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16)) break;
+      if (round == 1 && !group_any(id, !ok || max(top & 0xFFFFu, (top | odd) >> 16) > TR_RAISE_F16)) break;
       keep_branch();
       if (round < 2 && group_any(id, !ok)) return false;
       if (round == 1) {
@@ -847,6 +882,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       // most, 2^-28 of what this one leaves once r has risen by t or more.  Elsewhere
       // it falls by 2^-rise in two steps: values much smaller than the ones that raise
       // r make it so large that one step would leave nothing.  NaN stays NaN.
+      if (there && lr > TR_HIGH) high = TR_ODD;  // the reference may be that of its value from now on
       const float m = row_max();
       const bool first = mine_unset && m > -INFINITY;
       const float rise = first || (!mine_unset && m > TR_RAISE) ? m : 0.f;  // whatever the other rows do
@@ -878,7 +914,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       if (first) mine_unset = false;
       unset = group_any(id, mine_unset);  // (red is read)
       add = inv;
-      if (round == 0) continue;
+      if (round == 0) round = 2;  // nothing passes its bound now
     }
     tc_fence_before();
     fence_async_smem();

@@ -120,3 +120,18 @@ def test_a_key_that_is_not_finite_stays_in_sums_that_pass_fp32(coda):
     sick = (torch.arange(batch) % 2 == 1).repeat_interleave(n).to(DEV)
     assert torch.isnan(out["lse"][sick]).all() and torch.isnan(out["O"][sick].float()).all()
     assert torch.isfinite(out["lse"][~sick]).all() and torch.isfinite(out["O"][~sick].float()).all()
+
+
+@pytest.mark.parametrize("std", [0.1, 3.0])
+@pytest.mark.parametrize("batch", [1, 330])
+def test_values_of_all_sizes_in_one_sequence(coda, batch, std):
+    """Row by row from 2^-80 to 2^60, and zeros: the smallest count in the sum as far
+    as their scores say."""
+    n_q, n = 4, 3
+    lens = sizes(batch, 390)
+    r = np.random.default_rng(5)
+    K, V = synth.randn_bf16((sum(lens), D), 1.0, 1).float(), synth.randn_bf16((sum(lens), D), 1.0, 2).float()
+    Q = synth.randn_bf16((n * len(lens), n_q * D), std, 3).float()
+    V *= torch.exp2(torch.from_numpy(r.integers(-80, 61, size=(sum(lens), 1))).float())
+    V[::11] = 0
+    attend(coda, K, V, Q, lens, n, n_q)
