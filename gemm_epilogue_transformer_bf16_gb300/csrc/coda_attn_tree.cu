@@ -30,8 +30,8 @@
 //   P' = 2^t,  t = scale log2(e) rs_k (q . k') + log2 rs_v - r,  l = sum P' / rs_v
 // with a reference r per row that rises when some t passes 10 (f16 holds 2^15),
 // so P' is rounded by 2^-11 of itself or 2^-25 of the largest weighted row
-// scale.  Rows of zeros take the smallest row scale of their neighbours: their
-// own says nothing.  l, r and O are fp32.  Weights are computed and summed in one
+// scale.  Rows of zeros take one of 2^-50 or less: their own says nothing.
+// l, r and O are fp32.  Weights are computed and summed in one
 // pass over the scores; where one turns out to pass the bound the pass is taken
 // back (the sums with a minus), the reference rises and a second pass follows.
 // A 2^t below fp32's least may count in l where its value is much smaller than
@@ -104,8 +104,10 @@ constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
 // Row scales of values between 2^-50 and 2^30 differ so little that a weight below
 // fp32's least, 2^-126, is at most 2^-46 of its row's sum; the sign of a key's scale
-// tells of others (TR_ODD), with which what is lost is looked for.
-constexpr float TR_LOW = -50.f, TR_HIGH = 30.f;
+// tells of others (TR_ODD), with which what is lost is looked for.  A row of zeros
+// takes a smaller one than they (its own says nothing); where it passes its bound
+// all the same, or a reference is set, the smallest there is.
+constexpr float TR_LOW = -50.f, TR_HIGH = 30.f, TR_LEAST = -90.f, TR_ZEROS = -50.5f;
 constexpr uint32_t TR_ODD = 0x80000000u;
 
 // Places of a unit, by the rows of its tile, and of a stretch's ends, whose
@@ -489,7 +491,7 @@ __device__ __forceinline__ bool unit_in(TreeBars* bar, uint32_t it, int g, UnitI
 // left.  (Rolled, as below: warps of all roles share a scheduler, and their
 // straight-line code does not fit its instruction cache together.)
 __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32_t tmem, int g, int lane,
-                                            uint32_t it, int shift, int krow, uint32_t& rs_zero, bool& more) {
+                                            uint32_t it, int shift, int krow, bool& more) {
   const uint32_t st = it % TR_STAGES, buf = it & 1, ph = (it >> 1) & 1;
   UnitIn x;
   const bool here = unit_in(bar, it, g, x, more);
@@ -525,15 +527,12 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   }
   const bool sick = (((sfv.x & 0x7F7F7F7Fu) + 0x01010101u) | ((sfv.y & 0x7F7F7F7Fu) + 0x01010101u)) & 0x80808080u;
   const bool zeros = ((sfv.x | sfv.y) & 0x7F7F7F7Fu) == 0;
-  const uint32_t least = __reduce_min_sync(0xffffffffu, in && !zeros && !sick ? __float_as_uint(rsv) : 0x7F7FFFFFu);
-  if (least < 0x7F7FFFFFu) rs_zero = least;
-  const float rs = zeros ? __uint_as_float(rs_zero) : rsv;
   // a key that is not finite somewhere: NaN, and finite codes, so that rows that
   // do not see it stay clear of it
   const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
   float2 meta;
-  const float log_rs = rs < 0x1p-90f ? -90.f : log2f(rs);
-  const bool odd = log_rs < TR_LOW || log_rs > TR_HIGH;
+  const float log_rs = zeros ? TR_ZEROS : rsv < 0x1p-90f ? TR_LEAST : log2f(rsv);
+  const bool odd = !zeros && (log_rs < TR_LOW || log_rs > TR_HIGH);
   meta.x = !in ? 0.f : poison ? 1.f : odd ? -rsk : rsk;
   // below 2^-90 the sum l would pass fp32's end (2^10 / 2^-90 for a key, up to 2^26
   // of them): V' takes the rest
@@ -765,8 +764,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     tc_fence_after();
     const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
     const bool there = key.y != -INFINITY, poison = key.y != key.y;
-    const float lr = poison ? 0.f : key.y;
-    const float inv = there ? exp2_sfu(-lr) : 0.f;  // finite: it meets zero weights too
+    float lr = poison ? 0.f : key.y;
+    float inv = there ? exp2_sfu(-lr) : 0.f;  // finite: it meets zero weights too
     const float rk = there ? fmaxf(fabsf(key.x) * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
     const uint32_t tS = tmem + lanes + COL_S + buf * 128 + col0, tO = tmem + lanes + COL_O + col0;
     if (__any_sync(0xffffffffu, sees != ~0u || poison)) {  // scores that do not count become -inf where they lie
@@ -796,7 +795,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         const float most = warp_columns<8, false>(v, lane);
         if (lane < 8) red[warp * 32 + q + lane] = most;
       }
-      lost = group_any(id, odd != 0);
+      lost = group_any(id, odd != 0 || lr == TR_LEAST);
       float m = -INFINITY;
       if (tid < nc) m = fmaxf(fmaxf(red[tid], red[32 + tid]), fmaxf(red[64 + tid], red[96 + tid]));
       group_any(id, false);
@@ -807,7 +806,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     // bound the round is taken back, the reference of that row rises, and a third
     // one follows.
     uint8_t* at = smem + OFF_P + buf * TILE + tid * 128;
-    const uint64_t rk2 = f2_pack(rk, rk), lr2 = f2_pack(lr, lr);
+    const uint64_t rk2 = f2_pack(rk, rk);
     float add = inv;
     // Round 0 (an item's first unit, a reference is missing): it is set.  1: the
     // weights.  2: they are taken back, the reference rises.  3: again.
@@ -816,7 +815,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       asm volatile("" : "+r"(round));  // one copy of the code: what misses the instruction cache costs most here
       uint32_t top = 0;  // the largest weight, as f16 pairs
       if (round != 0) {
-        const uint64_t in2 = f2_pack(add, add);
+        const uint64_t in2 = f2_pack(add, add), lr2 = f2_pack(lr, lr);
 #pragma unroll
         for (int q = 0; q < NC; q += 8) {
           if (q == 16 && nc == 16) break;
@@ -883,6 +882,11 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       // it falls by 2^-rise in two steps: values much smaller than the ones that raise
       // r make it so large that one step would leave nothing.  NaN stays NaN.
       if (there && lr > TR_HIGH) high = TR_ODD;  // the reference may be that of its value from now on
+      const bool zeros = lr == TR_ZEROS && !(__float_as_uint(key.x) & TR_ODD);
+      if (zeros) {
+        lr = TR_LEAST;
+        inv = 0x1p90f;
+      }
       const float m = row_max();
       const bool first = mine_unset && m > -INFINITY;
       const float rise = first || (!mine_unset && m > TR_RAISE) ? m : 0.f;  // whatever the other rows do
@@ -1114,11 +1118,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       }
     } else if (warp < TR_VALUES) {
       reg_dec<56>();
-      uint32_t rs_zero = __float_as_uint(0x1p-12f);  // row scale that rows of zeros take
       bool more = true;
       const int shift = min(a.c.page_shift, 7), krow = raw_row((warp - TR_KEYS) * 32 + lane, shift);
       for (uint32_t it = 0; ok && more; ++it)
-        ok = unpack_keys(smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, rs_zero, more);
+        ok = unpack_keys(smem, bar, tmem, warp - TR_KEYS, lane, it, shift, krow, more);
     } else if (warp < TR_COPY_WARP) {
       reg_dec<48>();
       bool more = true;

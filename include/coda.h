@@ -904,7 +904,8 @@ int coda_kv_append_rope_nvfp4(const coda_bf16* Q, int64_t ldq, const coda_bf16* 
  * that see it.  Roundings as in coda_attention_decode_nvfp4, but that one power
  * of two scales the queries of up to 32 rows (a node and a query head of a group
  * each) to a maximum in [2^14, 2^15): an element below 2^-39 of that maximum is
- * rounded by 2^-39 of it.  The keys are divided over the SMs by the whole
+ * rounded by 2^-39 of it, and that value rows of zeros count as rows of scale
+ * 2^-90, and so do smaller ones.  The keys are divided over the SMs by the whole
  * batch's lengths, which the last bits depend on. */
 size_t coda_attention_tree_nvfp4_workspace_size(int64_t T, int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
 int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,

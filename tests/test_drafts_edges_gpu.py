@@ -122,6 +122,28 @@ def test_a_key_that_is_not_finite_stays_in_sums_that_pass_fp32(coda):
     assert torch.isfinite(out["lse"][~sick]).all() and torch.isfinite(out["O"][~sick].float()).all()
 
 
+@pytest.mark.parametrize("first, lift", [(32, 1.0), (129, 1.0), (256, 1.0), (32, 20.0)])
+@pytest.mark.parametrize("batch", [1, 330])
+@pytest.mark.parametrize("sizes_of", [(-60,), (20, -60), (-60, 40), (0,)], ids=str)
+def test_rows_of_zeros_have_no_say_in_the_units(coda, sizes_of, batch, first, lift):
+    """Every sequence begins with value rows of zeros, has one in seven among the
+    others and a few with the largest scores (by up to 60); sequences of small values
+    follow those of large ones in a CTA."""
+    n_q, n = 4, 3
+    lens = sizes(batch, 390)
+    K, V = synth.randn_bf16((sum(lens), D), 1.0, 1).float(), synth.randn_bf16((sum(lens), D), 1.0, 2).float()
+    Q = synth.randn_bf16((n * len(lens), n_q * D), 0.1, 3).float()
+    Q.view(-1, n_q, D)[..., :64] = 0.5
+    at = 0
+    for b, x in enumerate(lens):
+        V[at:at + x] *= 2.0 ** sizes_of[b % len(sizes_of)]
+        V[at:at + first] = 0
+        V[at:at + x:7] = 0
+        K[at:at + x:21, :64] += lift
+        at += x
+    attend(coda, K, V, Q, lens, n, n_q)
+
+
 @pytest.mark.parametrize("std", [0.1, 3.0])
 @pytest.mark.parametrize("batch", [1, 330])
 def test_values_of_all_sizes_in_one_sequence(coda, batch, std):
