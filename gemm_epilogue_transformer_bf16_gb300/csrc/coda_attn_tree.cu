@@ -1219,16 +1219,17 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeArgs a) {
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
   for (int x0 = c0; x0 <= c1; x0 += 32) {
     const int n = min(32, c1 - x0 + 1);
-    const float mine = lane < n ? exp2_sfu(a.part_lse[part_of(x0 + lane)] - W0) : 0.f;
+    // halves of the exponent: a large value counts at a probability below 2^-126 too
+    const float mine = lane < n ? exp2_sfu(0.5f * (a.part_lse[part_of(x0 + lane)] - W0)) : 0.f;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float wgt = __shfl_sync(0xffffffffu, mine, i);
       const float4 v = *reinterpret_cast<const float4*>(a.part + part_of(x0 + i) * 128 + lane * 4);
-      sum += wgt;
-      acc[0] += wgt * v.x;
-      acc[1] += wgt * v.y;
-      acc[2] += wgt * v.z;
-      acc[3] += wgt * v.w;
+      sum += wgt * wgt;
+      acc[0] += wgt * v.x * wgt;
+      acc[1] += wgt * v.y * wgt;
+      acc[2] += wgt * v.z * wgt;
+      acc[3] += wgt * v.w * wgt;
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
