@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
     sh.parent[i] = up;
     sh.token[i] = x;
     sh.u[i] = a.u[t0 + i];
-    sh.p[i] = up >= 0 ? value<F32>(a.P, at) : 0.f;
-    sh.q[i] = up >= 0 && a.Q ? value<F32>(a.Q, at) : 1.f;
+    // negative or NaN: 0, above 1: 1, as in the sums
+    sh.p[i] = up >= 0 ? __saturatef(value<F32>(a.P, at)) : 0.f;
+    sh.q[i] = up >= 0 && a.Q ? __saturatef(value<F32>(a.Q, at)) : 1.f;
   }
   __syncthreads();
 

@@ -8,7 +8,7 @@ import torch
 import synth
 from oracle import coda_oracle as O
 from parity import to_np
-from test_drafts_gpu import D, DEV, check_tree, grow, i32, offsets
+from test_drafts_gpu import D, DEV, check_tree, drafts, grow, i32, offsets, oracle_verify, run_verify
 from test_kvcache_gpu import fill, oracle_rows
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +157,31 @@ def test_values_of_all_sizes_in_one_sequence(coda, batch, std):
     V *= torch.exp2(torch.from_numpy(r.integers(-80, 61, size=(sum(lens), 1))).float())
     V[::11] = 0
     attend(coda, K, V, Q, lens, n, n_q)
+
+
+# --------------------------------------------------------------------------- verification
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("drawn", [True, False], ids=["drawn", "chosen"])
+def test_values_that_are_no_probabilities(coda, drawn, dtype):
+    """Negative ones and NaN count as 0, those above 1 as 1, in the walk as in the
+    sums; most of them at drafted tokens."""
+    bad = torch.tensor([float("nan"), -0.25, -2.0, float("-inf"), 0.0, 1.5, float("inf")], dtype=dtype)
+    clean = lambda x: x if x is None else x.float().nan_to_num(0.0, float("inf"), float("-inf")).clamp(0, 1)
+    nodes, V = [9, 1, 14, 6] * 6, 23
+    for seed in range(12):
+        r = np.random.default_rng(seed)
+        P, Q, trees, tokens, u, un = drafts(nodes, V, drawn, dtype, seed, peaked=1.0)
+        at = 0
+        for t in trees:
+            for i, up in enumerate(t):
+                for X in (P, Q):
+                    if up >= 0 and X is not None and r.random() < 0.3:
+                        X[at + up, tokens[at + i]] = bad[r.integers(5)]
+                if r.random() < 0.1:
+                    P[at + i, r.integers(V)] = bad[r.integers(7)]
+                if Q is not None and r.random() < 0.1:
+                    Q[at + i, r.integers(V)] = bad[r.integers(7)]
+            at += len(t)
+        got = run_verify(coda, P, Q, trees, tokens, u, un, 8)
+        assert got == oracle_verify(clean(P), clean(Q), trees, tokens, u, un, 8)
