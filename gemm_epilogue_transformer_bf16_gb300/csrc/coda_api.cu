@@ -616,6 +616,7 @@ const char* coda_status_string(int st) {
     case CODA_ERR_SEQLEN_RANGE: return "CODA_ERR_SEQLEN_RANGE";
     case CODA_ERR_PAGE_RANGE: return "CODA_ERR_PAGE_RANGE";
     case CODA_ERR_TREE_RANGE: return "CODA_ERR_TREE_RANGE";
+    case CODA_ERR_PROBABILITY_RANGE: return "CODA_ERR_PROBABILITY_RANGE";
     default: return "CODA_ERR_UNKNOWN";
   }
 }
@@ -631,6 +632,7 @@ int coda_get_status(const void* ws, coda_stream stream) {
   if (word & CODA_DEV_SEQLEN_RANGE) return CODA_ERR_SEQLEN_RANGE;
   if (word & CODA_DEV_PAGE_RANGE) return CODA_ERR_PAGE_RANGE;
   if (word & CODA_DEV_TREE_RANGE) return CODA_ERR_TREE_RANGE;
+  if (word & CODA_DEV_PROB_RANGE) return CODA_ERR_PROBABILITY_RANGE;
   return CODA_OK;
 }
 

@@ -9,3 +9,4 @@
 #define CODA_DEV_SEQLEN_RANGE 0x8    // sequence offsets that fall or leave the tensor, or a length beyond its page table
 #define CODA_DEV_PAGE_RANGE 0x10     // a cache slot or page index outside the cache
 #define CODA_DEV_TREE_RANGE 0x20     // a tree's parent, path or size that names no tree
+#define CODA_DEV_PROB_RANGE 0x40     // probabilities of a row that sum to 16 or more

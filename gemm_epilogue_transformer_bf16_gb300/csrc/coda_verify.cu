@@ -42,9 +42,9 @@ constexpr int VF_THREADS = 512;
 constexpr int VF_WARPS = VF_THREADS / 32;
 typedef unsigned long long u64;
 
-__device__ __forceinline__ u64 ld_cluster_u64(const void* p, uint32_t rank) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(p, rank)) : "memory");
+__device__ __forceinline__ ulonglong2 ld_cluster_2u64(const void* p, uint32_t rank) {
+  ulonglong2 v;
+  asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(mapa_shared(p, rank)) : "memory");
   return v;
 }
 
@@ -54,7 +54,7 @@ __device__ __forceinline__ u64 fixed60(float p) {
   return p > 0.f ? __float2ull_rz(fminf(p, 1.f) * 0x1p60f) : 0ull;
 }
 // Z q, both in units of 2^-60.
-__device__ __forceinline__ u64 scaled60(u64 Z, u64 q) { return __umul64hi(Z << 2, q << 2); }
+__device__ __forceinline__ u64 scaled60(u64 Z, u64 q) { return __umul64hi(Z, q) << 4 | Z * q >> 60; }
 
 template <bool F32>
 __device__ __forceinline__ float value(const void* base, int64_t at) {
@@ -80,7 +80,7 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {
 // runs at an eighth of the rate of an addition): the bits of a probability above
 // 2^-22, the next 22 and the 16 after them are each read off an addition, rounded
 // to zero, to a number whose last place is that unit.  Sums of the three in 32
-// bits hold for 512 values.
+// bits hold for 511 values.
 struct Sum60 {
   int hi = 0, mid = 0, lo = 0;
   static __device__ __forceinline__ void cut(float p, int& a, int& b, int& c) {
@@ -107,16 +107,22 @@ struct Sum60 {
     mid += b - e;
     lo += c - f;
   }
-  __device__ __forceinline__ u64 value() const {
-    return (static_cast<u64>(static_cast<int64_t>(hi)) << 38) + (static_cast<u64>(static_cast<int64_t>(mid)) << 16) +
-           static_cast<u64>(static_cast<int64_t>(lo));
-  }
 };
+
+// A thread's sum in units of 2^-60, modulo 16, and the whole of it in units of 2^-22,
+// 16 at most: sums of the latter over all threads are too low by less than 2^-10,
+// which tells whether those of the former have passed 16.
+struct Sum {
+  u64 fine;
+  uint32_t coarse;
+};
+constexpr uint32_t COARSE_16 = 16u << 22, COARSE_LOW = 1u << 12;
 
 struct VerifyShared {
   u64 Z[VERIFY_MAX_NODES];  // Z after each refusal at the node (Z[0] = 1)
-  u64 warp[VF_WARPS], fine[VF_WARPS];
-  u64 total;                // of this CTA, read by the others
+  ulonglong2 warp[VF_WARPS];  // fine and coarse sums
+  ulonglong2 total;           // of this CTA, read by the others
+  u64 fine[VF_WARPS];
   int here, count, ngone, refused, more;  // where the walk stands; more: it wants a sum
   float p[VERIFY_MAX_NODES], q[VERIFY_MAX_NODES], u[VERIFY_MAX_NODES];
   int token[VERIFY_MAX_NODES], parent[VERIFY_MAX_NODES];
@@ -169,8 +175,8 @@ struct Row {
 // refused where nothing was drawn are left out by the caller.  (One copy of the
 // code for all of a kernel's sums: the registers of a second one are spilled.)
 template <bool F32>
-__device__ __noinline__ u64 sum_pieces(const Row<F32> r, int piece, int stop, const u64* Z) {
-  u64 s = 0;
+__device__ __noinline__ Sum sum_pieces(const Row<F32> r, int piece, int stop, const u64* Z) {
+  int64_t hi = 0, lo = 0;  // in units of 2^-22 and 2^-60
   constexpr int N = 4;  // pieces in flight
   if (!r.need_q()) {
     for (; piece < stop; piece += N * 32) {
@@ -183,7 +189,8 @@ __device__ __noinline__ u64 sum_pieces(const Row<F32> r, int piece, int stop, co
       for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int i = 0; i < Row<F32>::E; ++i) c.add(__saturatef(r.element(vp[n], i)));  // NaN: 0
-      s += c.value();
+      hi += c.hi;
+      lo += (static_cast<int64_t>(c.mid) << 16) + c.lo;
     }
   } else if (r.refused == 1) {
     for (; piece < stop; piece += N * 32) {
@@ -200,16 +207,22 @@ __device__ __noinline__ u64 sum_pieces(const Row<F32> r, int piece, int stop, co
 #pragma unroll
         for (int i = 0; i < Row<F32>::E; ++i)
           c.add_above(__saturatef(r.element(vp[n], i)), __saturatef(r.element(vq[n], i)));
-      s += c.value();
+      hi += c.hi;
+      lo += (static_cast<int64_t>(c.mid) << 16) + c.lo;
     }
   } else {
     for (; piece < stop; piece += 32) {
       const uint4 vp = r.load(r.p, piece), vq = r.load(r.q, piece);
 #pragma unroll 1
-      for (int i = 0; i < Row<F32>::E; ++i) s += r.weight(r.element(vp, i), r.element(vq, i), Z);
+      for (int i = 0; i < Row<F32>::E; ++i) {
+        const u64 w = r.weight(r.element(vp, i), r.element(vq, i), Z);
+        hi += static_cast<int64_t>(w >> 38);
+        lo += static_cast<int64_t>(w & ((u64(1) << 38) - 1));
+      }
     }
   }
-  return s;
+  return {(static_cast<u64>(hi) << 38) + static_cast<u64>(lo),
+          static_cast<uint32_t>(min(hi + (lo >> 38), static_cast<int64_t>(COARSE_16)))};
 }
 
 template <bool F32>
@@ -291,28 +304,42 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
     return warp_sum(s);
   };
   // Sum over the vocabulary; sh.warp holds the warps' parts of this CTA, and
-  // `before` what the CTAs in front of it have.
+  // `before` what the CTAs in front of it have.  A row of 16 or more is `excess`.
+  bool excess = false;
   auto total = [&](int gone, u64& before) {
     share();
-    const u64 s = warp_sum(sum_pieces<F32>(r, w0 + lane, w1, sh.Z)) - refused_in(gone, w0, w1);
-    if (lane == 0) sh.warp[warp] = s;
+    const Sum part = sum_pieces<F32>(r, w0 + lane, w1, sh.Z);
+    const u64 s = warp_sum(part.fine) - refused_in(gone, w0, w1);
+    const uint32_t high = __reduce_add_sync(0xffffffffu, part.coarse);
+    if (lane == 0) sh.warp[warp] = make_ulonglong2(s, min(high, COARSE_16));
     __syncthreads();
-    u64 c = 0;
+    u64 c = 0, all = 0;
+    uint32_t coarse = 0;
     before = 0;
 #pragma unroll
-    for (int i = 0; i < VF_WARPS; ++i) c += sh.warp[i];
-    if (ctas == 1) return c;
-    if (tid == 0) sh.total = c;
-    cluster_sync();
-    u64 all = 0;
+    for (int i = 0; i < VF_WARPS; ++i) {
+      const ulonglong2 v = sh.warp[i];
+      c += v.x;
+      coarse += static_cast<uint32_t>(v.y);
+    }
+    all = c;
+    if (ctas > 1) {
+      if (tid == 0) sh.total = make_ulonglong2(c, min(coarse, COARSE_16));
+      cluster_sync();
+      all = 0;
+      coarse = 0;
 #pragma unroll
-    for (uint32_t i = 0; i < VF_CTAS; ++i)
-      if (i < ctas) {
-        c = ld_cluster_u64(&sh.total, i);
-        if (i < rank) before += c;
-        all += c;
-      }
-    cluster_sync();  // read by all before it is written again, or its CTA ends
+      for (uint32_t i = 0; i < VF_CTAS; ++i)
+        if (i < ctas) {
+          const ulonglong2 v = ld_cluster_2u64(&sh.total, i);
+          if (i < rank) before += v.x;
+          all += v.x;
+          coarse += static_cast<uint32_t>(v.y);
+        }
+      cluster_sync();  // read by all before it is written again, or its CTA ends
+    }
+    excess = coarse >= COARSE_16 ||
+             (coarse >= COARSE_16 - COARSE_LOW && all >> 63 == 0);
     return all;
   };
 
@@ -389,6 +416,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
     gone = sh.ngone;
     if (!sh.more) break;
     const u64 z = total(0, before);
+    if (excess) break;
     if (tid == 0) sh.Z[r.refused] = z;
     __syncthreads();
     summed = true;
@@ -397,12 +425,16 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
 
   // The next token.  Nothing left (probabilities that do not sum to 1): the
   // row's own probabilities; none there either: -1.
-  u64 all = total(gone, before);
-  if (all == 0 && (r.refused > 0 || gone > 0)) {
+  u64 all = excess ? 0 : total(gone, before);
+  if (all == 0 && !excess && (r.refused > 0 || gone > 0)) {
     r.refused = 0;
     gone = 0;
     __syncthreads();  // the warps' parts have been read
     all = total(0, before);
+  }
+  if (excess) {
+    all = 0;
+    if (rank == 0 && tid == 0) atomicOr(a.status, CODA_DEV_PROB_RANGE);
   }
   const float un = a.u_next[b];
   u64 tau = un > 0.f ? static_cast<u64>(fmin(static_cast<double>(un), 1.0) * static_cast<double>(all)) : 0;
@@ -416,14 +448,14 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   }
   u64 mine = 0;
 #pragma unroll
-  for (int i = 0; i < VF_WARPS; ++i) mine += sh.warp[i];
+  for (int i = 0; i < VF_WARPS; ++i) mine += sh.warp[i].x;
   if (all == 0 || tau < before || tau - before >= mine) return;
   // In this CTA.  The warp's share that holds it, cut into pieces of 32 ...
   u64 left = tau - before;  // the token's weight passes this
   int at = 0;
 #pragma unroll
   for (int i = 0; i < VF_WARPS; ++i) {
-    const u64 s = sh.warp[i];
+    const u64 s = sh.warp[i].x;
     if (at == i && left >= s && i + 1 < VF_WARPS) {
       left -= s;
       ++at;
@@ -433,7 +465,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
   const int s0 = min(c1, c0 + at * pw), s1 = min(c1, s0 + pw);
   const int run = ((s1 - s0 + VF_WARPS - 1) / VF_WARPS + 31) & ~31;  // pieces per warp
   const int f0 = min(s1, s0 + warp * run), f1 = min(s1, f0 + run);
-  const u64 s = warp_sum(sum_pieces<F32>(r, f0 + lane, f1, sh.Z)) - refused_in(gone, f0, f1);
+  const u64 s = warp_sum(sum_pieces<F32>(r, f0 + lane, f1, sh.Z).fine) - refused_in(gone, f0, f1);
   if (lane == 0) sh.fine[warp] = s;
   __syncthreads();
   at = 0;

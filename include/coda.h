@@ -72,7 +72,8 @@ typedef enum coda_status {
   CODA_ERR_POSITION_RANGE = 8, /* device: RoPE position outside [0, max_pos) */
   CODA_ERR_SEQLEN_RANGE = 9,   /* device: sequence offsets that fall or leave the tensor, a length beyond its page table */
   CODA_ERR_PAGE_RANGE = 10,    /* device: cache slot or page index outside the cache */
-  CODA_ERR_TREE_RANGE = 11     /* device: a parent, path or size that no tree of drafted tokens has */
+  CODA_ERR_TREE_RANGE = 11,    /* device: a parent, path or size that no tree of drafted tokens has */
+  CODA_ERR_PROBABILITY_RANGE = 12 /* device: probabilities of a row that sum to 16 or more */
 } coda_status;
 
 /* Operand storage order of a GEMM operand. */
@@ -926,8 +927,11 @@ int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* co
  * next token is the first x with sum_{y <= x} w(y) > u_next sum w.  Given
  * probabilities that sum to 1 and independent uniform u, the accepted and the
  * next token are distributed as the target's own, with or without draft_probs.
- * Weights are held in units of 2^-60 and their sums are exact; a probability
- * that is negative or NaN counts as 0, one above 1 as 1.
+ * Weights are held in units of 2^-60 and their sums are exact; a probability of
+ * either that is negative or NaN counts as 0, one above 1 as 1.  Where the weights
+ * of a row sum to 16 or more (without draft_probs those of refused tokens among
+ * them, to 2^-10) the walk ends without a next token (-1) and sets
+ * CODA_ERR_PROBABILITY_RANGE.
  *   count [batch]         accepted drafts a
  *   nodes [batch, width]  node 0, then the accepted nodes; -1 behind
  *   out   [batch, width]  the accepted tokens, then the next; -1 behind

@@ -185,3 +185,55 @@ def test_values_that_are_no_probabilities(coda, drawn, dtype):
             at += len(t)
         got = run_verify(coda, P, Q, trees, tokens, u, un, 8)
         assert got == oracle_verify(clean(P), clean(Q), trees, tokens, u, un, 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("drawn", [True, False], ids=["drawn", "chosen"])
+@pytest.mark.parametrize("copies", [1, 200])
+def test_rows_that_sum_to_more_than_one(coda, copies, drawn, dtype):
+    """Up to 16 they count as they are; from there on the sequence ends, with a status
+    and without a next token, and the others are as without it."""
+    r = np.random.default_rng(4)
+    V = 5000
+    for many, level in ((15, 1.0), (150, 0.1), (60, 0.25), (20, 0.75), (5000, 2.0 ** -9)):
+        P = torch.zeros(4, V)
+        for row in P:
+            row[torch.from_numpy(r.permutation(V)[:many])] = level
+        Q = torch.full((4, V), 1.0 / V) if drawn else None
+        P, Q = P.repeat(copies, 1).to(dtype), Q.repeat(copies, 1).to(dtype) if drawn else None
+        zero = [int(torch.nonzero(row == 0)[0]) if (row == 0).any() else 0 for row in P]
+        tokens = np.array([0, zero[0], zero[0], zero[0]] * copies)            # refused, where there is anything to refuse
+        trees = [[-1, 0, 0, 0]] * copies
+        u, un = np.full(4 * copies, 0.9999, np.float32), r.random(copies).astype(np.float32)
+        assert run_verify(coda, P, Q, trees, tokens, u, un, 3) == oracle_verify(P, Q, trees, tokens, u, un, 3), (many, level)
+    for many, level in ((16, 1.0), (17, 1.0), (32, 1.0), (31, 1.0), (5000, 1.0), (33, 0.5), (4096, 2.0 ** -8)):
+        P = torch.full((4, V), 0.0)
+        P[:, :many] = level
+        P[:, -1] = 2.0 ** -30                                                 # never drafted
+        good = torch.softmax(torch.randn(4, V, generator=torch.Generator().manual_seed(1)) * 3, 1)
+        P = torch.cat([good, P, good]).repeat(copies, 1).to(dtype)
+        Q = torch.full((12 * copies, V), 1.0 / V).to(dtype) if drawn else None
+        trees = [[-1, 0, 0, 0]] * 3 * copies
+        tokens = np.array([0, V - 1, V - 2, V - 1] * 3 * copies)
+        u, un = np.full(12 * copies, 0.9999, np.float32), r.random(3 * copies).astype(np.float32)
+        ws = coda.workspace(256)
+        count, path, out = run_verify(coda, P, Q, trees, tokens, u, un, 3, ws=ws)
+        # (with drawn drafts the weights count, from which the refused child's q is gone)
+        over = float((P[4].double() - (Q[4].double() if drawn else 0)).clamp(min=0).sum()) >= 16
+        assert coda.get_status(ws) == (12 if over else 0)                     # CODA_ERR_PROBABILITY_RANGE
+        want = oracle_verify(P, Q, trees, tokens, u, un, 3)
+        for b in range(3 * copies):
+            if over and b % 3 == 1:
+                end = count[b]
+                assert path[b] == want[1][b][:end + 1] + [-1] * (2 - end) and out[b] == want[2][b][:end] + [-1] * (3 - end)
+            else:
+                assert (count[b], path[b], out[b]) == tuple(x[b] for x in want), (many, level, b)
+
+
+@pytest.mark.parametrize("drawn", [True, False], ids=["drawn", "chosen"])
+def test_refusals_in_rows_that_sum_to_several(coda, drawn):
+    for seed in range(10):
+        P, Q, trees, tokens, u, un = drafts([9, 30, 5, 17] * 5, 97, drawn, torch.float32, seed, peaked=1.0)
+        P = (P * (4.0 + seed)).clamp(max=1.0)
+        u = (1 - 0.3 * u).astype(np.float32)
+        assert run_verify(coda, P, Q, trees, tokens, u, un, 6) == oracle_verify(P, Q, trees, tokens, u, un, 6)
