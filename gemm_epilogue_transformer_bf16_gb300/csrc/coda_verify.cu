@@ -437,7 +437,12 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
     if (rank == 0 && tid == 0) atomicOr(a.status, CODA_DEV_PROB_RANGE);
   }
   const float un = a.u_next[b];
-  u64 tau = un > 0.f ? static_cast<u64>(fmin(static_cast<double>(un), 1.0) * static_cast<double>(all)) : 0;
+  u64 tau = 0;  // floor(un all): a sum in whole units that passes it passes un all
+  if (un > 0.f) {
+    const uint32_t bits = __float_as_uint(un), e = bits >> 23;
+    const u64 m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);  // un = m 2^(e - 150)
+    tau = e > 126 ? all : e < 63 ? 0 : __umul64hi(all, m << 40) >> (126 - e);  // of all < 2^64
+  }
   if (tau >= all && all > 0) tau = all - 1;
   if (rank == 0) {
     if (tid == 0) {

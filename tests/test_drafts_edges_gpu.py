@@ -237,3 +237,27 @@ def test_refusals_in_rows_that_sum_to_several(coda, drawn):
         P = (P * (4.0 + seed)).clamp(max=1.0)
         u = (1 - 0.3 * u).astype(np.float32)
         assert run_verify(coda, P, Q, trees, tokens, u, un, 6) == oracle_verify(P, Q, trees, tokens, u, un, 6)
+
+
+def test_the_next_token_at_an_exact_border(coda):
+    """Weights of 2^-60 units about the border of u times a sum of more than 53 bits."""
+    u = lambda n: n * 2.0 ** -60
+    rows = [  # weights in units, u_next, the first x whose sum passes u_next times the sum
+        ([2 ** 59, 2, 2 ** 59, 6], 0.5, 2),              # 2^59 + 4: not passed by 2^59 + 2
+        ([2 ** 59, 4, 1, 2 ** 59, 3], 0.5, 2),           # 2^59 + 4: equal is not above
+        ([2 ** 58, 1, 1, 2 ** 59, 2 ** 58, 6], 0.25, 3), # 2^58 + 2: equal again
+        ([2 ** 58, 1, 2, 2 ** 59, 2 ** 58, 5], 0.25, 2),
+        ([2 ** 59, 2 ** 58, 3, 1, 2 ** 58, 0], 0.75, 3), # 3 * 2^58 + 3: only its sum with 1 is above
+        ([5, 1, 1, 1], 0.625, 1), ([5, 1, 1, 1], 0.5, 0), ([1, 2 ** 60], 2.0 ** -60, 1), ([1, 2 ** 60 - 2 ** 36], 2.0 ** -60, 0),
+        ([1, 1], 2.0 ** -140, 0), ([0, 3], 0.0, 1)]
+    for w, un, x in rows:
+        total, c, first = sum(w), 0, None
+        for i, n in enumerate(w):                        # in whole numbers
+            c += n
+            if first is None and c * 2 ** 140 > int(un * 2 ** 140) * total:
+                first = i
+        assert first == x
+        P = torch.tensor([[u(n) for n in w]], dtype=torch.float64).float()
+        assert [int(p * 2.0 ** 60) for p in P.double().tolist()[0]] == w
+        got = run_verify(coda, P, None, [[-1]], np.array([0]), np.zeros(1, np.float32), np.array([un], np.float32), 1)
+        assert got == ([0], [[0]], [[x]]), (w, un, got)
