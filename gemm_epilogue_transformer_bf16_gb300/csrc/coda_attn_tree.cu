@@ -9,7 +9,7 @@
 //
 // Work: the rows of a sequence and key/value head are cut into tiles of up to
 // 128, and the keys of a tile into units of 128.  The units of the whole batch
-// form one line, each as many places as it costs, that the CTAs (one per SM)
+// form one line, with places for the ends of every tile, that the CTAs (one per SM)
 // divide evenly.  A CTA whose stretch covers all keys of a tile writes the
 // output; the others leave normalised partial outputs that a second kernel
 // joins.
@@ -110,12 +110,12 @@ constexpr uint32_t TR_NO_MORE = 1u << 31;
 constexpr float TR_LOW = -50.f, TR_HIGH = 30.f, TR_LEAST = -90.f, TR_ZEROS = -50.5f;
 constexpr uint32_t TR_ODD = 0x80000000u;
 
-// Places of a unit, by the rows of its tile, and of a stretch's ends, whose
-// loads, sums and stores take as long as four to seven units.  Measured, for 24
-// ragged trees / 64 chains / 8 trees of 64 nodes: 4, 6, 18 215 / 141 / 190 us; 4, 6,
-// 24 200 / 139 / 189; 4, 6, 30 199 / 142 / 189; 5, 6, 24 191 / 139 / 188; 5, 8, 30 207 /
-// 139 / 190.
-constexpr int TR_COST_FEW = 5, TR_COST_MANY = 6, TR_END = 24;
+// Places of a stretch's ends on the line, a unit having one: their loads, sums and
+// stores take as long as four to seven units.  Geometric mean over 80 batches drawn
+// at random (1 to 64 sequences of up to 131072 keys, 1 to 64 nodes, all groups):
+// 3 22.6 us, 4 22.5, 5 22.5, 6 22.4, 7 22.5; with a unit of more than 64 rows a fifth
+// dearer (5, 6, ends 24) 23.0.
+constexpr int TR_END = 5;
 
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
@@ -176,10 +176,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 struct TreeSeq {
   int q0, n, len;     // first token, nodes, cached tokens; n = 0: no work
   int units, tiles;
-  int64_t place_kv;   // places per key/value head
+  int64_t place_kv;   // places per key/value head: of each tile, its ends' and units'
   __device__ __forceinline__ int rows(int tile, int group) const { return min(TREE_ROWS, n * group - tile * TREE_ROWS); }
 };
-__device__ __forceinline__ int tree_cost(int rows) { return rows <= 64 ? TR_COST_FEW : TR_COST_MANY; }
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool tell) {
   TreeSeq s;
   s.q0 = a.cu[b];
@@ -195,16 +194,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int b, bool tell)
   }
   s.units = (s.len + TR_UNIT - 1) / TR_UNIT;
   s.tiles = (s.n * a.group + TREE_ROWS - 1) / TREE_ROWS;
-  s.place_kv = 0;
-  if (s.n > 0)
-    s.place_kv = static_cast<int64_t>(s.tiles - 1) * (static_cast<int64_t>(s.units) * TR_COST_MANY + TR_END) +
-                 static_cast<int64_t>(s.units) * tree_cost(s.rows(s.tiles - 1, a.group)) + TR_END;
+  s.place_kv = s.n > 0 ? static_cast<int64_t>(s.tiles) * (s.units + TR_END) : 0;
   return s;
 }
-// First unit that starts at `place` or behind it, of an item at `base`.
-__device__ __forceinline__ int unit_at(int64_t place, int64_t base, int cost, int units) {
-  const int64_t d = place - base - TR_END;
-  return d <= 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(units), (d + cost - 1) / cost));
+// First unit at `place` or behind it, of an item at `base`.
+__device__ __forceinline__ int unit_at(int64_t place, int64_t base, int units) {
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(units), place - base - TR_END)));
 }
 
 // A CTA's way along the line: items (sequence, key/value head, tile) with the
@@ -227,10 +222,9 @@ struct TreeWalk {
       kvh = item / s.tiles;
       tile = item - kvh * s.tiles;
       rows = s.rows(tile, a.group);
-      const int cost = tree_cost(rows);
-      u0 = unit_at(first, base, cost, s.units);
-      u1 = unit_at(last, base, cost, s.units);
-      base += static_cast<int64_t>(s.units) * cost + TR_END;
+      u0 = unit_at(first, base, s.units);
+      u1 = unit_at(last, base, s.units);
+      base += s.units + TR_END;
       ++item;
       if (u0 < u1) return true;
     }
@@ -1043,8 +1037,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     if (w < warp) incl += bar->scan[w];
     total += bar->scan[w];
   }
-  // no CTA between two others of an item is left without a unit
-  const int64_t per = max(static_cast<int64_t>(TR_COST_MANY), (total + gridDim.x - 1) / gridDim.x);
+  const int64_t per = max(static_cast<int64_t>(1), (total + gridDim.x - 1) / gridDim.x);
   const int64_t first = blockIdx.x * per, last = min(total, first + per);
   {
     int64_t before = incl - mine;
@@ -1076,11 +1069,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
       w.first = first;
       w.last = last;
       w.s = tree_seq(a, w.b, false);
-      const int64_t many = static_cast<int64_t>(w.s.units) * TR_COST_MANY + TR_END;
-      const int64_t d = first - w.base, kv = d / w.s.place_kv;
-      const int64_t tile = min((d - kv * w.s.place_kv) / many, static_cast<int64_t>(w.s.tiles - 1));
-      w.item = static_cast<int>(kv * w.s.tiles + tile);
-      w.base += kv * w.s.place_kv + tile * many;
+      const int64_t each = w.s.units + TR_END, item = (first - w.base) / each;
+      w.item = static_cast<int>(item);
+      w.base += item * each;
       w.u0 = w.u1 = 0;
       c.u = 0;
       c.it = c.items = 0;
@@ -1202,10 +1193,9 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeArgs a) {
   }
   const int kvh = head / a.group, row = (t - s.q0) * a.group + head - kvh * a.group;
   const int tile = row / TREE_ROWS, c = row - tile * TREE_ROWS;
-  const int cost = tree_cost(s.rows(tile, a.group));
   const int64_t per = a.places[a.B + 1];
-  const int64_t u0 = a.places[b] + kvh * s.place_kv + tile * (static_cast<int64_t>(s.units) * TR_COST_MANY + TR_END) + TR_END;
-  const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + static_cast<int64_t>(s.units - 1) * cost) / per);
+  const int64_t u0 = a.places[b] + kvh * s.place_kv + tile * static_cast<int64_t>(s.units + TR_END) + TR_END;
+  const int c0 = static_cast<int>(u0 / per), c1 = static_cast<int>((u0 + s.units - 1) / per);
   if (c0 == c1) return;  // that CTA wrote the output
   // The weights a lane each, then the parts in order with four loads in flight:
   // two long documents (up to 76 parts a row) 138 -> 134 us, a chain of 6 over 777
