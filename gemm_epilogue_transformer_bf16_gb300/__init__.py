@@ -967,7 +967,7 @@ def _device(t, name):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.get_device() < 0:
         _where(t, -1, name)
-    return torch._C._cuda_getDevice()  # (a tensor lives on a GPU: the runtime is up)
+    return torch.cuda.current_device()
 
 
 def _arg(t, dtype, shape, dev, name):
