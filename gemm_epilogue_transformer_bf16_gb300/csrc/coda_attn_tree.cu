@@ -30,13 +30,14 @@
 //   P' = 2^t,  t = scale log2(e) rs_k (q . k') + log2 rs_v - r,  l = sum P' / rs_v
 // with a reference r per row that rises when some t passes 10 (f16 holds 2^15),
 // so P' is rounded by 2^-11 of itself or 2^-25 of the largest weighted row
-// scale.  Rows of zeros take one of 2^-50 or less: their own says nothing.
-// l, r and O are fp32.  Weights are computed and summed in one
+// scale.  l, r and O are fp32.  Weights are computed and summed in one
 // pass over the scores; where one turns out to pass the bound the pass is taken
 // back (the sums with a minus), the reference rises and a second pass follows.
-// A 2^t below fp32's least may count in l where its value is much smaller than
-// others: units with row scales outside 2^-50 to 2^30 are treated as those whose
-// bound is passed, and what was lost is added in a third pass.
+// A 2^t below fp32's least, 2^-126, may count in l where its value is much smaller
+// than others.  With row scales of 2^-90 to 1 it is 2^-36 of l at most; from a key
+// with a larger one on (values beyond 2688) units are treated as those that pass
+// the bound, and what was lost is added in a third pass.  (l itself is 2^-117 or
+// more: values beyond 1e33 leave its smaller terms no room.)
 //
 // Roles: four warpgroups of weights with a quarter of the tile's rows each (their
 // sums fit the 72 registers that 28 warps leave), two of them with half each for
@@ -102,13 +103,9 @@ constexpr int TR_HALF_ROWS = 64;               // up to here two warpgroups: 64 
 constexpr float TR_RAISE = 10.f;               // a weight may pass 2^10 ...
 constexpr uint32_t TR_RAISE_F16 = 0x6400;      // ... 1024 in f16
 constexpr uint32_t TR_NO_MORE = 1u << 31;
-// Row scales of values between 2^-50 and 2^30 differ so little that a weight below
-// fp32's least, 2^-126, is at most 2^-46 of its row's sum; the sign of a key's scale
-// tells of others (TR_ODD), with which what is lost is looked for.  A row of zeros
-// takes a smaller one than they (its own says nothing); where it passes its bound
-// all the same, or a reference is set, the smallest there is.
-constexpr float TR_LOW = -50.f, TR_HIGH = 30.f, TR_LEAST = -90.f, TR_ZEROS = -50.5f;
-constexpr uint32_t TR_ODD = 0x80000000u;
+// The least row scale of a weight, in log2: smaller ones take it (V' the rest), and
+// rows of zeros, whose own says nothing.
+constexpr float TR_LEAST = -90.f;
 
 // Places of a stretch's ends on the line, a unit having one: their loads, sums and
 // stores take as long as four to seven units.  Geometric mean over 80 batches drawn
@@ -525,12 +522,10 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   // do not see it stay clear of it
   const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
   float2 meta;
-  const float log_rs = zeros ? TR_ZEROS : rsv < 0x1p-90f ? TR_LEAST : log2f(rsv);
-  const bool odd = !zeros && (log_rs < TR_LOW || log_rs > TR_HIGH);
-  meta.x = !in ? 0.f : poison ? 1.f : odd ? -rsk : rsk;
+  meta.x = !in ? 0.f : poison ? 1.f : rsk;
   // below 2^-90 the sum l would pass fp32's end (2^10 / 2^-90 for a key, up to 2^26
   // of them): V' takes the rest
-  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : log_rs;
+  meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : zeros || rsv < 0x1p-90f ? TR_LEAST : log2f(rsv);
   *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
   tmem_st_wait();
   tc_fence_before();
@@ -732,7 +727,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
   for (int c = 0; c < NC; ++c) l[c] = 0.f;
   bool unset = true;        // some column has no reference
   bool mine_unset = tid < nc;  // column tid
-  uint32_t high = 0;        // TR_ODD: a key of this thread had a row scale beyond 2^30
+  bool large = false;       // a key of this thread had a row scale above 1
   const int u0 = w.u0, u1 = w.u1, nodes = w.n, group = a.group;
 
   for (int u = u0; u < u1; ++u, ++it) {
@@ -757,13 +752,26 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
     const float2 key = *reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024 + tid * 8);
-    const bool there = key.y != -INFINITY, poison = key.y != key.y;
-    float lr = poison ? 0.f : key.y;
+    const bool there = key.y != -INFINITY;
+    float lr = key.y;
     float inv = there ? exp2_sfu(-lr) : 0.f;  // finite: it meets zero weights too
-    const float rk = there ? fmaxf(fabsf(key.x) * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
+    const float rk = there ? fmaxf(key.x * factor, 1.2e-38f) : 0.f;  // not 0, so that -inf below stays what it is
     const uint32_t tS = tmem + lanes + COL_S + buf * 128 + col0, tO = tmem + lanes + COL_O + col0;
-    if (__any_sync(0xffffffffu, sees != ~0u || poison)) {  // scores that do not count become -inf where they lie
+    bool odd = false;
+    if (__any_sync(0xffffffffu, sees != ~0u || !(lr <= 0.f))) {  // scores that do not count become -inf where they lie
       keep_branch();
+      const bool poison = lr != lr;
+      if (poison) {
+        lr = 0.f;
+        inv = 1.f;
+      } else if (lr > 0.f) {
+        // A key whose row scale is above 1 is left out of the first weights, which
+        // are taken back: 2^t might be infinite although 2^t / rs_v, without which it
+        // cannot be, is no more than l.
+        odd = true;
+        lr = -INFINITY;
+        inv = 0.f;
+      }
 #pragma unroll 1
       for (int q = 0; q < nc; q += 8) {
         uint32_t s[8];
@@ -775,7 +783,6 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       }
       tmem_st_wait();
     }
-    const uint32_t odd = high | (__float_as_uint(key.x) & TR_ODD);
     bool lost = false;  // some weights may be below 2^-126 and count in the sum all the same
     // The largest exponent of each row over this unit's keys, to column tid.
     auto row_max = [&]() {
@@ -789,7 +796,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         const float most = warp_columns<8, false>(v, lane);
         if (lane < 8) red[warp * 32 + q + lane] = most;
       }
-      lost = group_any(id, odd != 0 || lr == TR_LEAST);
+      lost = group_any(id, odd || large);
       float m = -INFINITY;
       if (tid < nc) m = fmaxf(fmaxf(red[tid], red[32 + tid]), fmaxf(red[64 + tid], red[96 + tid]));
       group_any(id, false);
@@ -841,7 +848,6 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         keep_branch();
         // 2^t / rs_v = 2^(s - r), where 2^t was nothing.  (Rolled, l turning by eight
         // columns: little code, and nothing spilled.)
-        const float below = there ? exp2_sfu(-126.f - lr) : 0.f;
 #pragma unroll 1
         for (int q = 0; q < NC; q += 8) {
           uint32_t s[8];
@@ -849,8 +855,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
           float next[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float y = exp2_sfu(fmaf(__uint_as_float(s[k]), rk, nref[q + k]));
-            next[k] = l[k] + (y < below ? y : 0.f);
+            const float n = nref[q + k], z = __uint_as_float(s[k]);  // the weight to the bit as above
+            next[k] = l[k] + (there && exp2_sfu(fmaf(z, rk, lr + n)) == 0.f ? exp2_sfu(fmaf(z, rk, n)) : 0.f);
           }
 #pragma unroll
           for (int k = 0; k < NC - 8; ++k) l[k] = l[k + 8];
@@ -860,7 +866,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
         break;
       }
       // (as numbers: f16 of one sign are ordered as their bits)
-      if (round == 1 && !group_any(id, !ok || max(top & 0xFFFFu, (top | odd) >> 16) > TR_RAISE_F16)) break;
+      if (round == 1 && !group_any(id, !ok || odd || large || max(top & 0xFFFFu, top >> 16) > TR_RAISE_F16)) break;
       keep_branch();
       if (round < 2 && group_any(id, !ok)) return false;
       if (round == 1) {
@@ -875,11 +881,11 @@ __device__ __forceinline__ bool tree_softmax(const TreeArgs& a, uint8_t* smem, T
       // most, 2^-28 of what this one leaves once r has risen by t or more.  Elsewhere
       // it falls by 2^-rise in two steps: values much smaller than the ones that raise
       // r make it so large that one step would leave nothing.  NaN stays NaN.
-      if (there && lr > TR_HIGH) high = TR_ODD;  // the reference may be that of its value from now on
-      const bool zeros = lr == TR_ZEROS && !(__float_as_uint(key.x) & TR_ODD);
-      if (zeros) {
-        lr = TR_LEAST;
-        inv = 0x1p90f;
+      const float size = reinterpret_cast<const float2*>(smem + OFF_KEY + (it & 3) * 1024)[tid].y;
+      if (size > 0.f) {
+        large = true;  // the reference may be its value's from now on
+        lr = size;
+        inv = exp2_sfu(-lr);
       }
       const float m = row_max();
       const bool first = mine_unset && m > -INFINITY;

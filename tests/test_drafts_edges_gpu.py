@@ -159,6 +159,52 @@ def test_values_of_all_sizes_in_one_sequence(coda, batch, std):
     attend(coda, K, V, Q, lens, n, n_q)
 
 
+@pytest.mark.parametrize("batch", [1, 330])
+@pytest.mark.parametrize("before, behind, jump", [(-100, 60, 0), (-100, 40, 5), (-90, 55, -10), (None, 60, 0), (-110, 100, 0),
+                                                   (-40, 90, 3)], ids=str)
+def test_large_values_behind_small_ones(coda, batch, before, behind, jump):
+    """Scores of one size, values 2^100 times as large from some key on (None: zeros
+    before them): a weight is infinite against the first reference though its share
+    is no larger than the others'."""
+    n_q, n = 4, 3
+    lens = sizes(batch, 390)
+    K, V = synth.randn_bf16((sum(lens), D), 0.5, 1).float(), synth.randn_bf16((sum(lens), D), 1.0, 2).float()
+    Q = synth.randn_bf16((n * len(lens), n_q * D), 0.1, 3).float()
+    Q.view(-1, n_q, D)[..., :64] = 1.0
+    at = 0
+    for x in lens:
+        late = (torch.arange(x) >= 0.4 * x) & (torch.arange(x) % 3 < 2)
+        V[at:at + x] *= torch.where(late, 2.0 ** behind, 0.0 if before is None else 2.0 ** before).unsqueeze(1)
+        K[at:at + x, :64] = torch.where(late, jump * 0.6931 / (64 * D ** -0.5), 0.0).unsqueeze(1)
+        at += x
+    attend(coda, K, V, Q, lens, n, n_q)
+
+
+@pytest.mark.parametrize("batch", [1, 330])
+def test_weights_at_fp32_s_least(coda, batch):
+    """Values of 2688 * 2^36 among rows of zeros, which count as rows of scale 2^-90:
+    with scores that hardly differ every weight of theirs lies at 2^-126, just above
+    or just below, and each is counted once."""
+    n_q, n = 4, 3
+    lens = sizes(batch, 390)
+    K, V = synth.randn_bf16((sum(lens), D), 1.0, 1).float(), torch.zeros(sum(lens), D)
+    V[::37] = 2688.0 * 2.0 ** 36 * torch.sign(synth.randn_bf16((len(V[::37]), D), 1.0, 2).float())
+    attend(coda, K, V, synth.randn_bf16((n * len(lens), n_q * D), 2.0 ** -10, 3).float(), lens, n, n_q)
+
+
+@pytest.mark.parametrize("group, n, batch, top", [(13, 30, 60, 170), (4, 2, 9, 1300), (8, 3, 200, 300), (2, 30, 60, 700)])
+def test_values_about_fp32_s_range_apart(coda, group, n, batch, top):
+    """Weights on either side of fp32's least, each counted once."""
+    r = np.random.default_rng(group)
+    lens = [int(x) for x in r.integers(n, top, size=batch)]
+    T = sum(lens)
+    K, V = synth.randn_bf16((T, D), 1.0, 1).float(), synth.randn_bf16((T, D), 1.0, 2).float()
+    Q = synth.randn_bf16((n * batch, group * D), 1.0, 3).float()
+    V *= torch.exp2(torch.from_numpy(r.integers(-80, 61, size=(T, 1))).float())
+    V[torch.from_numpy(r.random(T) < 0.5)] = 0
+    attend(coda, K, V, Q, lens, n, group, page=32)
+
+
 # --------------------------------------------------------------------------- verification
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
