@@ -47,9 +47,12 @@
 //
 // What bounds it: instructions, and fetching them.  A unit of 128 keys takes 1900
 // to 2900 clocks (at 32 to 128 rows) for 850 of copies and 130 to 510 of
-// products; the roles' loops take turns in the four schedulers (2.95 instructions a
-// clock and SM) and evict each other from the instruction caches.  So code that is
-// run in every unit counts, and how often:
+// products, and 5500 to 8600 warp instructions (2.95 a clock and SM at 128 rows).
+// Weights, four per score, and unpacking, two per element, are 2600 to 4100 of them;
+// the others (waits, barriers, votes, addresses of 26 warps) have not been taken
+// apart.  The roles' loops take turns in the four schedulers and evict each other
+// from the instruction caches.  So code that is run in every unit counts, and how
+// often:
 //   waits without a clock and a flag in their loops   192 -> 150 us (64 chains)
 //   one copy of what sets and raises a reference      150 -> 140
 //   columns in sixteens (a branch for four)           184 -> 178 (8 trees)
@@ -63,9 +66,9 @@
 // the next item's Q in front of an item's end gained nothing.
 //
 // Now, in a graph: 64 + 8 heads, 64 chains of 4 over up to 8192 keys 136 us
-// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 185 us (44), a chain
-// of 6 over 777 keys 19 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
-// 177 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 125 us (42).
+// (floor 45), 24 trees of 1 to 64 nodes over 60 to 6000 keys 191 us (44), a chain
+// of 6 over 777 keys 18 us; 32 + 8 heads, 8 trees of 64 nodes over 16384 keys
+// 180 us (71), trees of 16 and 11 nodes over 131055 and 100001 keys 128 us (42).
 #include <algorithm>
 
 #include "coda_attn.cuh"
@@ -288,8 +291,9 @@ struct TreeBars {
 };
 static_assert(sizeof(TreeBars) <= 1152, "barrier area");
 
-// A wait that gives up after 2^19 tries, for each of which the hardware suspends
-// the warp for up to 4 us.  As short as can be: every role waits in every unit.
+// A wait that gives up after 2^19 tries, for each of which the hardware may suspend
+// the warp for about 2 us: a second in all.  As short as can be: every role waits
+// in every unit.
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -523,8 +527,8 @@ __device__ __forceinline__ bool unpack_keys(uint8_t* smem, TreeBars* bar, uint32
   const bool poison = sick || !(fabsf(rsk) <= 3.4e38f) || !(fabsf(rsv) <= 3.4e38f);
   float2 meta;
   meta.x = !in ? 0.f : poison ? 1.f : rsk;
-  // below 2^-90 the sum l would pass fp32's end (2^10 / 2^-90 for a key, up to 2^26
-  // of them): V' takes the rest
+  // below 2^-90 the sum l would pass fp32's end (2^10 / 2^-90 for a key, room for
+  // 2^26 of them): V' takes the rest
   meta.y = !in ? -INFINITY : poison ? __uint_as_float(0x7FC00000u) : zeros || rsv < 0x1p-90f ? TR_LEAST : log2f(rsv);
   *reinterpret_cast<float2*>(smem + OFF_KEY + (it & 3) * 1024 + (g * 32 + lane) * 8) = meta;
   tmem_st_wait();

@@ -24,7 +24,7 @@
 // between the CTAs and meet by distributed shared memory.  128 requests of 5
 // drawn tokens over 128256 probabilities in fp32 (131 MB at most, 19 us): 32 us
 // in a graph; one request of 7 11 us; 48 trees of 1 to 40 nodes over 50257
-// probabilities in bf16 20 us.  With eight CTAs to every request, each thread
+// probabilities in bf16 19 us.  With eight CTAs to every request, each thread
 // walking and sums by conversions to 64 bits it was 128, 33 and 61 us.
 #include <algorithm>
 #include <cuda_bf16.h>
@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(VF_THREADS, 2) verify_kernel(const VerifyArgs 
 
 cudaError_t launch_verify(VerifyArgs a, bool f32, cudaStream_t s) {
   // As many CTAs to a request as are resident at once, two to an SM; a second
-  // wave would walk its trees while the memory has nothing to do.
+  // wave would walk its trees while the memory has nothing to do.  (Shares are not
+  // even then: 128 requests have two each, so that of 152 SMs 104 have two of 256
+  // and the others one.)
   const int64_t slots = 2 * static_cast<int64_t>(device_sms());
   a.ctas = VF_CTAS;
   while (a.ctas > 1 && static_cast<int64_t>(a.B) * a.ctas > slots) a.ctas >>= 1;

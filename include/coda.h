@@ -902,12 +902,14 @@ int coda_kv_append_rope_nvfp4(const coda_bf16* Q, int64_t ldq, const coda_bf16* 
  * (CODA_ERR_SEQLEN_RANGE, as far as its rows exist).  A page outside the cache
  * sets CODA_ERR_PAGE_RANGE and its keys are left out.  Rows outside every sequence stay as they
  * are; a row of the cache that holds an infinity or NaN reaches only the nodes
- * that see it.  Roundings as in coda_attention_decode_nvfp4, but that one power
- * of two scales the queries of up to 32 rows (a node and a query head of a group
- * each) to a maximum in [2^14, 2^15): an element below 2^-39 of that maximum is
- * rounded by 2^-39 of it, and that value rows of zeros count as rows of scale
- * 2^-90, and so do smaller ones.  The keys are divided over the SMs by the whole
- * batch's lengths, which the last bits depend on. */
+ * that see it.  Roundings as in coda_attention_decode_nvfp4 (exponentials are off by
+ * 2^-22 of themselves in both), with two differences.  One power of two scales the
+ * queries of up to 32 rows (a node and a query head of a group each) to a maximum
+ * in [2^14, 2^15): an element below 2^-39 of that maximum is rounded by 2^-39 of it,
+ * so nodes that only pad a tree must not hold queries 2^20 times larger than the
+ * others'.  And of the weights times row scales that the rounding to f16 refers to,
+ * rows of zeros count with a scale of 2^-90, and so do smaller ones.  The keys are
+ * divided over the SMs by the whole batch's lengths, which the last bits depend on. */
 size_t coda_attention_tree_nvfp4_workspace_size(int64_t T, int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
 int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
                               const float* scale, int64_t num_pages, int32_t page_size, const int32_t* block_table,
@@ -927,8 +929,10 @@ int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* co
  * next token is the first x with sum_{y <= x} w(y) > u_next sum w.  Given
  * probabilities that sum to 1 and independent uniform u, the accepted and the
  * next token are distributed as the target's own, with or without draft_probs.
- * Weights are held in units of 2^-60 and their sums are exact; a probability of
- * either that is negative or NaN counts as 0, one above 1 as 1.  Where the weights
+ * Weights are held in units of 2^-60 (less is 0), their sums are exact, and so is
+ * the choice of the next token among them; a decision about a child compares two
+ * products in fp64.  A probability of either kind that is negative or NaN counts as
+ * 0, one above 1 as 1.  Where the weights
  * of a row sum to 16 or more (without draft_probs those of refused tokens among
  * them, to 2^-10) the walk ends without a next token (-1) and sets
  * CODA_ERR_PROBABILITY_RANGE.
