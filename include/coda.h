@@ -908,7 +908,8 @@ int coda_kv_append_rope_nvfp4(const coda_bf16* Q, int64_t ldq, const coda_bf16* 
  * in [2^14, 2^15): an element below 2^-39 of that maximum is rounded by 2^-39 of it,
  * so nodes that only pad a tree must not hold queries 2^20 times larger than the
  * others'.  And of the weights times row scales that the rounding to f16 refers to,
- * rows of zeros count with a scale of 2^-90, and so do smaller ones.  The keys are
+ * rows of zeros count with a scale of 2^-90, and so do smaller ones, whose values
+ * are rounded to f16 (2^-11) on top.  The keys are
  * divided over the SMs by the whole batch's lengths, which the last bits depend on. */
 size_t coda_attention_tree_nvfp4_workspace_size(int64_t T, int64_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
 int coda_attention_tree_nvfp4(const coda_bf16* Q, int64_t ldq, const uint8_t* codes, const uint8_t* sf,
